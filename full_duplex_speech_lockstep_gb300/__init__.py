@@ -41,7 +41,9 @@ EXPORTS = ["pp_weight_shape", "pp_workspace_bytes", "pp_create", "pp_destroy",
            "pp_ring_attention_noalloc", "pp_rvq_dequantize", "pp_driver_create",
            "pp_driver_destroy", "pp_driver_open", "pp_driver_close", "pp_driver_phase",
            "pp_driver_prepare", "pp_driver_absorb", "pp_driver_tick", "pp_session_sampling",
-           "pp_sample", "pp_test_faults"]
+           "pp_sample", "pp_test_faults", "pp_paged_append",
+           "pp_paged_attention_scratch_bytes", "pp_paged_attention", "pp_paged_mass",
+           "pp_paged_evict"]
 
 # enum pp_kernel_kind
 KERNEL_KINDS = ["begin", "norm", "qkv", "rope_ring", "attn", "oproj", "gateup", "down",
@@ -80,6 +82,17 @@ class pp_sampling(ctypes.Structure):
 
 
 SAMPLE_HISTORY = 256   # the longest repetition-penalty window
+
+
+PP_F32, PP_BF16, PP_F16 = 0, 1, 2
+
+
+class pp_paged_kv(ctypes.Structure):
+    """One cache of pages with its block table (device pointers)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("mass", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("page_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ["n_pages", "page_size", "n_kv_heads", "head_dim", "type",
+                                      "n_seqs", "table_ld"]]
 
 
 class pp_weights(ctypes.Structure):
@@ -157,6 +170,19 @@ def lib():
         L.pp_sample.argtypes = [P, I64, I, I, F, I, F, F, P, I, P, P, P, P, P]
         L.pp_sample.restype = I
         L.pp_driver_tick.restype = I
+        KV = ctypes.POINTER(pp_paged_kv)
+        L.pp_paged_append.argtypes = [KV, P, I64, P, I64, P, I64, I, P, P, F, F, I, I, P, P, P, I,
+                                      I, P, P, P]
+        L.pp_paged_append.restype = I
+        L.pp_paged_attention_scratch_bytes.argtypes = [KV, I, I, I]
+        L.pp_paged_attention_scratch_bytes.restype = ctypes.c_size_t
+        L.pp_paged_attention.argtypes = [KV, P, I64, P, P, I, I, I, F, I, P, P, P, P,
+                                         ctypes.c_size_t, P]
+        L.pp_paged_attention.restype = I
+        L.pp_paged_mass.argtypes = [KV, P, I64, P, P, P, I, I, I, F, I, F, P, P]
+        L.pp_paged_mass.restype = I
+        L.pp_paged_evict.argtypes = [KV, P, I, I, KV, P, P, P, P]
+        L.pp_paged_evict.restype = I
         _lib = L
     return _lib
 
@@ -408,6 +434,44 @@ def sampling(text_temperature=0.0, text_top_k=0, text_top_p=1.0, repetition_pena
                        int(seed) & (2**64 - 1))
 
 
+def pp_paged_append(kv, q, q_stride, k, k_stride, v, v_stride, in_type, q_alpha, k_alpha, eps,
+                    rope_base, rot_dim, halves, positions, cu, kv_len, T, n_heads, q_out, status,
+                    stream):
+    """Norm and rotation of new queries and keys; keys and values into the paged cache."""
+    return _check("pp_paged_append", lib().pp_paged_append(
+        ctypes.byref(kv), q, q_stride, k, k_stride, v, v_stride, in_type, q_alpha, k_alpha, eps,
+        rope_base, rot_dim, halves, positions, cu, kv_len, T, n_heads, q_out, status, stream))
+
+
+def pp_paged_attention_scratch_bytes(kv, n_heads, max_q, window):
+    n = lib().pp_paged_attention_scratch_bytes(ctypes.byref(kv), n_heads, max_q, window)
+    if n == 0:
+        raise PPError("pp_paged_attention_scratch_bytes", PP_EINVAL)
+    return n
+
+
+def pp_paged_attention(kv, q, q_stride, cu, kv_len, T, max_q, n_heads, scale, window, out, lse,
+                       status, scratch, scratch_bytes, stream):
+    """Attention of new rows over the paged cache."""
+    return _check("pp_paged_attention", lib().pp_paged_attention(
+        ctypes.byref(kv), q, q_stride, cu, kv_len, T, max_q, n_heads, scale, window, out, lse,
+        status, scratch, scratch_bytes, stream))
+
+
+def pp_paged_mass(kv, q, q_stride, lse, cu, kv_len, T, max_q, n_heads, scale, window, decay, status,
+                  stream):
+    """The attention weight that new rows give to each entry, added to the cache's mass."""
+    return _check("pp_paged_mass", lib().pp_paged_mass(
+        ctypes.byref(kv), q, q_stride, lse, cu, kv_len, T, max_q, n_heads, scale, window, decay,
+        status, stream))
+
+
+def pp_paged_evict(kv, kv_len, budget, recent, to, to_len, kept, status, stream):
+    """The newest and heaviest entries of the paged cache into another's pages."""
+    return _check("pp_paged_evict", lib().pp_paged_evict(
+        ctypes.byref(kv), kv_len, budget, recent, ctypes.byref(to), to_len, kept, status, stream))
+
+
 # ---- convenience wrapper over torch device memory ---------------------------------------
 
 class Engine:
@@ -507,3 +571,171 @@ class Engine:
         pp_step_host(self.h, ptr(prev_column), ptr(user_codes), ptr(force_mask), ptr(forced),
                      ptr(column), ptr(logits), self._stream())
         return column
+
+
+class PagedKV:
+    """One layer's paged cache over torch-owned device memory.
+
+    ``k`` and ``v`` are [pages, kv_heads, page_size, head_dim] in bf16 or fp16, ``table``
+    [sequences, table width] int32 page numbers, ``mass`` (optional) f32 [pages, kv_heads,
+    page_size].  ``cu`` is int32 [sequences + 1] row offsets and ``kv_len`` int32 [sequences]
+    entry counts, the new entries included.  Every call runs on the cache's device, on its
+    current stream.  Tensors that do not fit raise ValueError; what the library refuses
+    raises PPError."""
+
+    def __init__(self, k, v, table, mass=None, status=None):
+        import torch
+        self.torch = torch
+        self.types = {torch.float32: PP_F32, torch.bfloat16: PP_BF16, torch.float16: PP_F16}
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise ValueError("k and v must be [pages, heads, rows, dims] of one layout and type")
+        if k.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("the cache holds bf16 or fp16, not %s" % k.dtype)
+        n_pages, heads, rows, dim = k.shape
+        if k.stride()[1:] != (rows * dim, dim, 1):
+            raise ValueError("each page of k and v must be contiguous")
+        self.device = k.device
+        self.k, self.v, self.table, self.mass = k, v, table, mass
+        self._fits("v", v, v.dtype)
+        self._fits("table", table, torch.int32, (None, None))
+        if mass is not None:
+            self._fits("mass", mass, torch.float32, (n_pages, heads, rows))
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device) if status is None \
+            else self._fits("status", status, torch.int32)
+        self.heads, self.dim = heads, dim
+        stride = k.stride(0) if n_pages > 1 else heads * rows * dim
+        self.c = pp_paged_kv(k.data_ptr(), v.data_ptr(), self._ptr(mass), table.data_ptr(),
+                             stride, n_pages, rows, heads, dim, self.types[k.dtype],
+                             table.shape[0], table.shape[1])
+
+    @staticmethod
+    def _ptr(t):
+        return None if t is None else t.data_ptr()
+
+    def _fits(self, name, t, dtype, shape=None):
+        """t, if it is a tensor of this device, type and shape (None: any extent), contiguous
+        when a shape is asked for."""
+        if not t.is_cuda or t.device != self.device:
+            raise ValueError("%s must be on %s, not %s" % (name, self.device, t.device))
+        if t.dtype != dtype:
+            raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
+        if shape is not None and (t.dim() != len(shape) or not t.is_contiguous() or any(
+                n is not None and n != m for n, m in zip(shape, t.shape))):
+            raise ValueError("%s: shape %s, expected contiguous %s" % (name, tuple(t.shape), shape))
+        return t
+
+    def _rows(self, name, t, dtype, T=None, heads=None):
+        """Row stride of a [rows, heads, dims] tensor whose rows are contiguous."""
+        self._fits(name, t, dtype)
+        if t.dim() != 3 or t.shape[2] != self.dim or (T is not None and t.shape[0] != T) or (
+                heads is not None and t.shape[1] != heads):
+            raise ValueError("%s: shape %s, expected (%s, %s, %d)" % (
+                name, tuple(t.shape), T or "rows", heads or "heads", self.dim))
+        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.dim)):
+            raise ValueError("%s: the heads of a row must be contiguous" % name)
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * self.dim
+
+    def _batch(self, cu, kv_len):
+        n = self.table.shape[0]
+        self._fits("cu", cu, self.torch.int32, (n + 1,))
+        self._fits("kv_len", kv_len, self.torch.int32, (n,))
+
+    def _stream(self):
+        return self.torch.cuda.current_stream(self.device).cuda_stream
+
+    def read_status(self):
+        """Wait for the current stream, then read and clear the status word."""
+        bits = int(self.status.item())
+        self.status.zero_()
+        return bits
+
+    def append(self, q, k, v, cu, kv_len, positions=None, q_alpha=None, k_alpha=None, eps=1e-5,
+               rope_base=10000.0, rot_dim=None, halves=False, out=None):
+        """New queries normed and rotated ([rows, heads, dims], returned in the cache's type);
+        new keys, the same way, and values become cache entries."""
+        torch, f32 = self.torch, self.torch.float32
+        if q.dtype not in self.types:
+            raise ValueError("q must be f32 or the cache's type, not %s" % q.dtype)
+        qs = self._rows("q", q, q.dtype)
+        T, H = q.shape[:2]
+        ks = self._rows("k", k, q.dtype, T, self.heads)
+        vs = self._rows("v", v, q.dtype, T, self.heads)
+        self._batch(cu, kv_len)
+        for name, t in (("q_alpha", q_alpha), ("k_alpha", k_alpha)):
+            if t is not None:
+                self._fits(name, t, f32, (self.dim,))
+        if positions is not None:
+            self._fits("positions", positions, torch.int32, (T,))
+        if out is None:
+            out = torch.empty((T, H, self.dim), dtype=self.k.dtype, device=self.device)
+        else:
+            self._fits("out", out, self.k.dtype, (T, H, self.dim))
+        with torch.cuda.device(self.device):
+            pp_paged_append(self.c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                            self.types[q.dtype], self._ptr(q_alpha), self._ptr(k_alpha), eps,
+                            rope_base, self.dim if rot_dim is None else rot_dim, int(halves),
+                            self._ptr(positions), cu.data_ptr(), kv_len.data_ptr(), T, H,
+                            out.data_ptr(), self.status.data_ptr(), self._stream())
+        return out
+
+    def attention(self, q, cu, kv_len, max_q=None, scale=None, window=0, with_lse=False,
+                  out=None):
+        """Attention of the new rows over the cache: out, or (out, lse) on request.  max_q is
+        the longest chunk as far as the host knows (default: all rows)."""
+        torch = self.torch
+        qs = self._rows("q", q, self.k.dtype)
+        T, H = q.shape[:2]
+        self._batch(cu, kv_len)
+        if out is None:
+            out = torch.empty((T, H, self.dim), dtype=q.dtype, device=self.device)
+        else:
+            self._fits("out", out, q.dtype, (T, H, self.dim))
+        lse = torch.empty((T, H), dtype=torch.float32, device=self.device) if with_lse else None
+        max_q = max(1, T if max_q is None else min(max_q, T) if max_q > 0 else max_q)
+        nbytes = pp_paged_attention_scratch_bytes(self.c, H, max_q, window)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(self.device):
+            pp_paged_attention(self.c, q.data_ptr(), qs, cu.data_ptr(), kv_len.data_ptr(), T,
+                               max_q, H, self.dim ** -0.5 if scale is None else scale, window,
+                               out.data_ptr(), self._ptr(lse), self.status.data_ptr(),
+                               scratch.data_ptr(), nbytes, self._stream())
+        return (out, lse) if with_lse else out
+
+    def attention_mass(self, q, lse, cu, kv_len, max_q=None, scale=None, window=0, decay=1.0,
+                       mass=None):
+        """Add the attention weight of the new rows to the cache's mass (or to ``mass``, of the
+        same layout)."""
+        torch = self.torch
+        qs = self._rows("q", q, self.k.dtype)
+        T, H = q.shape[:2]
+        self._fits("lse", lse, torch.float32, (T, H))
+        self._batch(cu, kv_len)
+        c = self.c
+        if mass is not None:
+            self._fits("mass", mass, torch.float32, tuple(self.k.shape[:3]))
+            c = pp_paged_kv.from_buffer_copy(self.c)
+            c.mass = mass.data_ptr()
+        elif self.mass is None:
+            raise ValueError("this cache keeps no mass")
+        max_q = max(1, T if max_q is None else min(max_q, T) if max_q > 0 else max_q)
+        with torch.cuda.device(self.device):
+            pp_paged_mass(c, q.data_ptr(), qs, lse.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), T,
+                          max_q, H, self.dim ** -0.5 if scale is None else scale, window, decay,
+                          self.status.data_ptr(), self._stream())
+
+    def evict(self, kv_len, budget, recent, to):
+        """Keep the newest `recent` and the heaviest other entries, `budget` in all, in the
+        PagedKV `to`; returns (lengths there, the entries kept)."""
+        torch = self.torch
+        if self.mass is None:
+            raise ValueError("this cache keeps no mass")
+        if to.device != self.device:
+            raise ValueError("both caches must be on one device")
+        n = self.table.shape[0]
+        self._fits("kv_len", kv_len, torch.int32, (n,))
+        to_len = torch.empty(n, dtype=torch.int32, device=self.device)
+        kept = torch.empty((n, self.heads, max(budget, 0)), dtype=torch.int32, device=self.device)
+        with torch.cuda.device(self.device):
+            pp_paged_evict(self.c, kv_len.data_ptr(), budget, recent, to.c, to_len.data_ptr(),
+                           kept.data_ptr(), self.status.data_ptr(), self._stream())
+        return to_len, kept

@@ -190,6 +190,13 @@ cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
+// The driver's tensor-map encoder (looked up once; null if it cannot be found).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 // ---- launchers (stream-ordered; return cudaGetLastError) ----------------------------
 // op (may be null): also write the layer-0 operand hi/lo(alpha * x) and the sum of x^2
 cudaError_t launch_begin(const Dims& D, const Buffers& b, const float* alpha, uint16_t* op,

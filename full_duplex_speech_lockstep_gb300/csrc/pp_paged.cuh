@@ -1,0 +1,283 @@
+// pp_paged.cuh - the paged cache as its kernels see it: sequences, rows, key tiles, page
+// lookups, and the tile loads, matrix fragments and masks that they share.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "pp_async.cuh"
+#include "pp_internal.cuh"
+
+namespace pp {
+namespace paged {
+
+constexpr int kTile = 128;       // cache entries of one key tile
+constexpr int kMaxSeqs = 2048;   // sequences of one call (their prefix sums sit in shared memory)
+constexpr int kMaxGroup = 64;    // query heads to a key head
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// One call's cache and batch.  Lengths come from the device and are clamped to what the
+// host has checked, so no length or offset can carry an access out of the arrays.
+struct Args {
+  const int32_t* table;
+  const int32_t* len;      // cache entries of each sequence
+  const int32_t* cu;       // first row of each sequence, and the end of the last
+  int64_t page_stride;     // elements
+  int n_pages, lps;        // pages of the pool; log2(page size)
+  int Hk, G, D;            // key heads, query heads to each, head dim
+  int n_seqs, table_ld, T;
+  int window;              // 0: none
+  float c;                 // scale * log2(e): scores in powers of two
+  uint32_t* status;
+};
+
+struct Seq {
+  int row0, n, len;        // first row, new tokens, cache entries (new ones included)
+};
+
+// Lengths and tables are read with plain loads: an earlier kernel of the same stream may
+// have written them while this one was already on its SM (programmatic launch), which the
+// non-coherent path does not allow.
+__device__ __forceinline__ int seq_len(const Args& a, int b) {
+  return min(max(a.len[b], 0), a.table_ld << a.lps);
+}
+
+__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+  Seq s;
+  s.row0 = min(max(a.cu[b], 0), a.T);
+  s.n = min(max(a.cu[b + 1], s.row0), a.T) - s.row0;
+  s.len = seq_len(a, b);
+  return s;
+}
+
+// Page of entries [j, j + 1) of sequence b, or -1 when the table holds no page of the pool.
+__device__ __forceinline__ int page_of(const Args& a, int b, int j) {
+  const int p = a.table[(int64_t)b * a.table_ld + (j >> a.lps)];
+  return (unsigned)p < (unsigned)a.n_pages ? p : -1;
+}
+
+__device__ __forceinline__ void raise(const Args& a, uint32_t bits) {
+  if (a.status) atomicOr(a.status, bits);
+}
+
+// Prefix sums of count(b) over the sequences into pre[0..n], by one CTA; ends with a
+// barrier.
+template <typename F>
+__device__ __forceinline__ void prefix_units(int* pre, int n, F count) {
+  for (int b = threadIdx.x; b < n; b += blockDim.x) pre[b + 1] = count(b);
+  if (threadIdx.x == 0) pre[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int base = 0;
+    for (int b0 = 0; b0 < n; b0 += 32) {
+      const int b = b0 + threadIdx.x;
+      int x = b < n ? pre[b + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((int)threadIdx.x >= o) x += y;
+      }
+      if (b < n) pre[b + 1] = base + x;
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// The sequence whose units hold u: pre[b] <= u < pre[b + 1].
+__device__ __forceinline__ int find_seq(const int* pre, int n, int u) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ---- shared-memory tiles -----------------------------------------------------------------
+// A tile of R rows of D 16-bit values is D/64 boxes of R rows x 128 bytes, each in the
+// 128-byte swizzle: 16-byte chunk c of row r sits at chunk c ^ (r & 7).
+
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int box_bytes, int row, int chunk) {
+  return base + (chunk >> 3) * box_bytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// Load one key tile (entries [j0, j0 + 128) of head h) by one warp: a lane for each
+// (page, 64-dim box).  Entries at or past `end` and pages outside the pool arrive as zeros;
+// returns, in every lane, a mask of the tile's pages outside the pool.
+__device__ __forceinline__ uint32_t load_key_tile(const Args& a, const CUtensorMap* map,
+                                                  uint32_t dst, uint32_t bar, int b, int h, int j0,
+                                                  int end, int lane) {
+  const int per = min(1 << a.lps, kTile);          // rows of one box
+  const int pages = kTile / per, boxes = a.D >> 6;
+  const int pg = lane % pages, bx = lane / pages;  // lane < pages * boxes <= 16 loads
+  const int j = j0 + pg * per;
+  int page = a.n_pages;                            // past the last page: zeros
+  bool bad = false;
+  if (bx < boxes && j < end) {
+    const int p = page_of(a, b, j);
+    bad = p < 0;
+    if (!bad) page = p;
+  }
+  if (lane == 0) mbar_expect_tx(bar, (uint32_t)(kTile * a.D * 2));
+  __syncwarp();
+  if (bx < boxes)
+    tma_load_4d(dst + bx * (kTile * 128) + pg * per * 128, map, bx * 64, j & ((1 << a.lps) - 1), h,
+                page, bar);
+  return __ballot_sync(0xffffffffu, bad && bx == 0) & 0xffu;
+}
+
+// ---- matrix fragments ----------------------------------------------------------------------
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t r[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t r[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// The two 16-bit types: their product, their packed rounding, their non-finite values, and
+// the power of two that softmax weights carry so that small ones stay normal numbers
+// (fp16 has no exponents below 2^-14; bf16 has fp32's).
+template <typename T>
+struct Num;
+template <>
+struct Num<__nv_bfloat16> {
+  static constexpr float kShift = 0.f;
+  static constexpr uint32_t kExp = 0x7f80u, kOne = 0x3f80u;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  static __device__ __forceinline__ float to_float(uint32_t h) { return __uint_as_float(h << 16); }
+  static __device__ __forceinline__ void mma(float d[4], const uint32_t a[4], uint32_t b0,
+                                             uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+template <>
+struct Num<__half> {
+  static constexpr float kShift = 7.f;
+  static constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  static __device__ __forceinline__ float to_float(uint32_t h) {
+    return __half2float(__ushort_as_half((unsigned short)h));
+  }
+  static __device__ __forceinline__ void mma(float d[4], const uint32_t a[4], uint32_t b0,
+                                             uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- launches ------------------------------------------------------------------------------
+// Programmatic dependent launch: every kernel of this family waits for its predecessor
+// (griddepcontrol.wait) before it reads anything, so it may be scheduled early.
+template <typename... KArgs, typename... Args_>
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                   Args_... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+struct Maps {
+  CUtensorMap k, v, q;
+};
+
+// Rows of one unit: whole tokens with all G heads of a key head, up to 16 * wr rows.
+struct RowTile {
+  int wr;          // 16-row fragments: 1, 2 or 4
+  int tp;          // tokens
+};
+inline RowTile row_tile(int G, int max_q) {
+  const int64_t rows = (int64_t)max_q * G;
+  RowTile r;
+  r.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  r.tp = 16 * r.wr / G;
+  if (max_q < r.tp) r.tp = max_q;
+  return r;
+}
+
+// Split of the rows and keys of one attention call (k_paged_attn.cu).
+struct AttnPlan : RowTile {
+  int ns_cap;      // splits of the longest sequence that the table can hold
+  size_t rec_bytes, ml_bytes;
+};
+AttnPlan attn_plan(const Args& a, int max_q);
+
+struct AttnOut {
+  void* out;
+  float* lse;      // may be null
+  float* part;     // split partials: [row][split][D] and [row][split] (reference, sum)
+  float2* part_ml;
+};
+
+cudaError_t launch_paged_attn(const Args& a, int type, const AttnPlan& plan, const Maps& maps,
+                              const AttnOut& o, cudaStream_t s);
+cudaError_t launch_paged_mass(const Args& a, int type, const RowTile& r, const Maps& maps,
+                              const float* lse, float* mass, float decay, cudaStream_t s);
+
+struct AppendArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const float *q_alpha, *k_alpha;
+  float eps;
+  int rot, halves;
+  const int32_t* positions;
+  void *q_out, *k_pages, *v_pages;
+  float* mass;
+};
+struct Turns {
+  uint64_t f[64];   // turns of each pair per position, as a fraction of 2^64
+};
+cudaError_t launch_paged_append(const Args& a, const AppendArgs& x, const Turns& turns, int in_type,
+                                int type, cudaStream_t s);
+
+struct EvictArgs {
+  const void *k, *v;
+  const float* mass;
+  void *to_k, *to_v;
+  float* to_mass;
+  const int32_t* to_table;
+  int64_t to_page_stride;
+  int to_n_pages, to_lps, to_table_ld;
+  int budget, recent;
+  int32_t *to_len, *kept;
+};
+cudaError_t launch_paged_evict(const Args& a, const EvictArgs& x, cudaStream_t s);
+
+}  // namespace paged
+}  // namespace pp

@@ -494,6 +494,133 @@ int pp_rvq_dequantize(const int32_t* codes, int code_stride, int n_frames, int n
                       const float* codebooks, int card, int dim, float* out, uint32_t* status,
                       void* stream);
 
+/* ---- the paged cache: chunks of new tokens beside the ring's single ones --------------
+ * The ring of an engine holds one window per slot and takes one token per tick.  The four
+ * calls below work on a cache of pages instead, shared by sequences of any length, and
+ * take any number of new tokens at once: a prompt is one call where the tick takes one
+ * step per token (vllm-omni recipe, "Architecture"; mhpq, "Persona Voice 注入": prefill is
+ * forced tokens), a tick is a chunk of one token per sequence, and entries leave by the
+ * attention that they received instead of by age.  The pages of the method have no
+ * counterpart to them.  One layer's calls, in order:
+ *   pp_paged_append      norm and rotation of the new queries and keys; keys and values
+ *                        into the cache
+ *   pp_paged_attention   the new queries over the cache, new entries included
+ *   pp_paged_mass        (optional) what each entry received is added to its weight
+ *   pp_paged_evict       (now and then) the lightest entries leave
+ *
+ * Entry j of sequence b is row j % page_size of page table[b][j / page_size]; kv_len[b]
+ * entries exist.  All device arrays are the caller's.  A page number outside [0, n_pages)
+ * that a call needs is never followed: nothing is stored there, its entries take no part,
+ * and PP_S_INDEX is OR-ed into the status word.  Table entries past a sequence's last page
+ * are not looked at.  kv_len is clamped to [0, table_ld * page_size].
+ *
+ * New rows are packed: sequence b has rows cu[b] .. cu[b+1] - 1 of the T rows, its newest
+ * tokens, in order; a sequence may have none.  Values of cu are clamped to [0, T]; rows of
+ * no sequence (before cu[0], from cu[n_seqs] on) are neither read as queries nor written.
+ * Row i of a sequence of n new rows sits at entry p = kv_len - n + i: kv_len counts the
+ * new entries.  It sees the entries j <= p, with window > 0 only those with j > p - window
+ * (entries are counted by index, so after an eviction a window counts what is left).
+ *
+ * Every call is asynchronous on `stream`, belongs to the current device, allocates nothing
+ * and may be captured into a graph; lengths, tables and row offsets are read when the
+ * graph runs.  status (a device word) may be NULL.  A sequence's results depend on its
+ * own rows, entries and lengths and on the call's head counts and max_q, bit for bit,
+ * never on the other sequences. */
+#define PP_F32 0
+#define PP_BF16 1
+#define PP_F16 2
+
+typedef struct {
+  void* k;                 /* [n_pages] pages of [n_kv_heads][page_size][head_dim], 16-byte
+                              aligned, page_stride elements apart */
+  void* v;                 /* the same layout and stride */
+  float* mass;             /* [n_pages][n_kv_heads][page_size]: the attention weight that each
+                              entry has received; NULL where a call does not need it */
+  const int32_t* table;    /* [n_seqs][table_ld] */
+  int64_t page_stride;     /* elements, >= n_kv_heads * page_size * head_dim, multiple of 8 */
+  int32_t n_pages;
+  int32_t page_size;       /* 16, 32, 64, 128 or 256 */
+  int32_t n_kv_heads;      /* 1..1024 */
+  int32_t head_dim;        /* 64 or 128 */
+  int32_t type;            /* PP_BF16 or PP_F16 */
+  int32_t n_seqs;          /* 1..2048 */
+  int32_t table_ld;        /* table_ld * page_size <= 2^28 */
+} pp_paged_kv;
+
+/* Norm and rotation of the new queries and keys for each head, and the new cache entries:
+ *   y = x / sqrt(mean(x^2) + eps) * alpha   over the head's dims (no norm where the alpha is
+ *                                           NULL);
+ *   pair i < rot_dim/2 turned by positions[t] * rope_base^(-2i/rot_dim): dims (2i, 2i+1), or
+ *   with halves != 0 dims (i, i + rot_dim/2); dims from rot_dim on stay;
+ *   q_out = y of the queries; K entry = y of the keys; V entry = the values; the mass of the
+ *   new entries (where kv->mass is given) = 0.
+ * In fp32, rounded once; the angle keeps its precision at any int32 position.
+ *   q, k, v    [T] rows of n_heads (n_kv_heads) x head_dim values, rows q_stride (k_stride,
+ *              v_stride) elements apart (multiples of 8), 16-byte aligned: views of one joint
+ *              projection will do.  in_type: PP_F32 or the cache's type
+ *   q_alpha, k_alpha  f32 [head_dim], 16-byte aligned, or NULL
+ *   positions  int32 [T], or NULL: the token's entry index p
+ *   q_out      [T][n_heads][head_dim] in the cache's type, 16-byte aligned; may be q itself when
+ *              q has that type and layout
+ * rot_dim is even, 0..head_dim; rope_base >= 1; n_heads a multiple of n_kv_heads, at most 64
+ * query heads to a key head.  A row whose entry index is negative (kv_len < n) stores no key.
+ * T == 0 does nothing.  Errors: PP_EINVAL, PP_E_CUDA. */
+int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, const void* k,
+                    int64_t k_stride, const void* v, int64_t v_stride, int in_type,
+                    const float* q_alpha, const float* k_alpha, float eps, float rope_base,
+                    int rot_dim, int halves, const int32_t* positions, const int32_t* cu,
+                    const int32_t* kv_len, int T, int n_heads, void* q_out, uint32_t* status,
+                    void* stream);
+
+/* Attention of the new rows over the cache:
+ *   out[t][h] = sum_j exp(s_j - lse) V_j,  s_j = scale q[t][h] . K_j,  lse = log sum_j exp(s_j)
+ * over the entries j that the row sees, of key head h / (n_heads / n_kv_heads).  A row that
+ * sees none gives zeros and an lse of -infinity.  What a row does not see never reaches it,
+ * whatever is stored there (NaN and infinities included).  Scores, sums and outputs are
+ * accumulated in fp32; softmax weights enter the second product in the cache's type.
+ *   q        [T] rows of [n_heads][head_dim] in the cache's type, q_stride elements apart
+ *            (a multiple of 8), 16-byte aligned
+ *   max_q    the largest number of new rows of any sequence, as far as the host knows; sets
+ *            tile sizes and scratch only: longer chunks are computed all the same
+ *   out      [T][n_heads][head_dim] in the cache's type, 16-byte aligned
+ *   lse      f32 [T][n_heads], or NULL
+ *   scratch  at least pp_paged_attention_scratch_bytes(...) bytes, 256-byte aligned; its
+ *            contents need no set-up; calls that may overlap need their own
+ * scale > 0; window >= 0 (0: none); max_q >= 1.  T == 0 does nothing.  Errors: PP_EINVAL,
+ * PP_E_NOSPACE, PP_E_CUDA.  pp_paged_attention_scratch_bytes returns 0 for bad arguments. */
+size_t pp_paged_attention_scratch_bytes(const pp_paged_kv* kv, int n_heads, int max_q, int window);
+int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, const int32_t* cu,
+                       const int32_t* kv_len, int T, int max_q, int n_heads, float scale,
+                       int window, void* out, float* lse, uint32_t* status, void* scratch,
+                       size_t scratch_bytes, void* stream);
+
+/* The attention weight that the new rows give to each entry, added to kv->mass:
+ *   mass_j = decay * mass_j + sum over rows t and query heads h of j's key head that see j of
+ *            exp(scale q[t][h] . K_j - lse[t][h])
+ * for every entry j < kv_len, seen or not.  decay in [0, 1]: 1 accumulates, 0 starts afresh
+ * (old contents are then not read).  q, lse, scale and window as in (and from)
+ * pp_paged_attention; a caller may pass fewer rows than it attended with, the last ones of
+ * each sequence.  Rows with an lse of -infinity give nothing.  The sum over rows runs in a
+ * fixed order.  Errors: PP_EINVAL, PP_E_CUDA. */
+int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const float* lse,
+                  const int32_t* cu, const int32_t* kv_len, int T, int max_q, int n_heads,
+                  float scale, int window, float decay, uint32_t* status, void* stream);
+
+/* Keep at most `budget` entries of each sequence and key head: the `recent` newest, and of the
+ * older ones those of the largest mass (the lower index first among equals; NaN counts as
+ * the lowest).  They go, in their order and with their mass, to entries 0.. of the same
+ * sequence of `to`: other pages, of the same pool or another, of any page size.  No page may
+ * be both read and written.  Keys stay rotated as they are: give later positions to
+ * pp_paged_append.
+ *   to_len  int32 [n_seqs]: min(kv_len, budget)
+ *   kept    int32 [n_seqs][n_kv_heads][budget]: the entries that stayed, ascending, then -1
+ * kv->mass is required, to->mass is written if given.  0 <= recent <= budget, budget >= 1.
+ * Errors: PP_EINVAL (`to` of other sequences, heads, head dim or type), PP_E_RANGE (to's table
+ * is too narrow for the budget), PP_E_CUDA. */
+int pp_paged_evict(const pp_paged_kv* kv, const int32_t* kv_len, int budget, int recent,
+                   const pp_paged_kv* to, int32_t* to_len, int32_t* kept, uint32_t* status,
+                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif
