@@ -174,7 +174,7 @@ def lib():
         L.pp_paged_append.argtypes = [KV, P, I64, P, I64, P, I64, I, P, P, F, F, I, I, P, P, P, I,
                                       I, P, P, P]
         L.pp_paged_append.restype = I
-        L.pp_paged_attention_scratch_bytes.argtypes = [KV, I, I, I]
+        L.pp_paged_attention_scratch_bytes.argtypes = [KV, I, I, I, I]
         L.pp_paged_attention_scratch_bytes.restype = ctypes.c_size_t
         L.pp_paged_attention.argtypes = [KV, P, I64, P, P, I, I, I, F, I, P, P, P, P,
                                          ctypes.c_size_t, P]
@@ -443,8 +443,8 @@ def pp_paged_append(kv, q, q_stride, k, k_stride, v, v_stride, in_type, q_alpha,
         rope_base, rot_dim, halves, positions, cu, kv_len, T, n_heads, q_out, status, stream))
 
 
-def pp_paged_attention_scratch_bytes(kv, n_heads, max_q, window):
-    n = lib().pp_paged_attention_scratch_bytes(ctypes.byref(kv), n_heads, max_q, window)
+def pp_paged_attention_scratch_bytes(kv, n_heads, T, max_q, window):
+    n = lib().pp_paged_attention_scratch_bytes(ctypes.byref(kv), n_heads, T, max_q, window)
     if n == 0:
         raise PPError("pp_paged_attention_scratch_bytes", PP_EINVAL)
     return n
@@ -692,7 +692,7 @@ class PagedKV:
             self._fits("out", out, q.dtype, (T, H, self.dim))
         lse = torch.empty((T, H), dtype=torch.float32, device=self.device) if with_lse else None
         max_q = max(1, T if max_q is None else min(max_q, T) if max_q > 0 else max_q)
-        nbytes = pp_paged_attention_scratch_bytes(self.c, H, max_q, window)
+        nbytes = pp_paged_attention_scratch_bytes(self.c, H, T, max_q, window)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         with torch.cuda.device(self.device):
             pp_paged_attention(self.c, q.data_ptr(), qs, cu.data_ptr(), kv_len.data_ptr(), T,

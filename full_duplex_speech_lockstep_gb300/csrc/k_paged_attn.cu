@@ -185,14 +185,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (*abort_flag) break;
         const uint32_t bad =
             load_key_tile(a, &mapK, smem_u32(smem + ks * C::kTileBytes),
-                          smem_u32(&ctl->kfull[ks]), x.b, x.h, t * kTile, x.end, lane);
+                          smem_u32(&ctl->kfull[ks]), x.b, x.h, t * kTile, x.end, lane, nullptr);
         seen_bad |= bad;
         ++nk;
         if (nv >= C::VS) wait(&ctl->vempty[vs], (nv / C::VS - 1) & 1);
         if (*abort_flag) break;
-        if (lane == 0) ctl->bad[vs] = bad;   // released by the V tile's barrier
         load_key_tile(a, &mapV, smem_u32(smem + C::kVOff + vs * C::kTileBytes),
-                      smem_u32(&ctl->vfull[vs]), x.b, x.h, t * kTile, x.end, lane);
+                      smem_u32(&ctl->vfull[vs]), x.b, x.h, t * kTile, x.end, lane, &ctl->bad[vs]);
         ++nv;
       }
     }
@@ -266,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->kempty[ks]));
       ++nk;
-      // which pages of the tile do not exist comes with its V tile
+      // which parts of the tile have no page comes with its V tile
       const int vs = nv % C::VS;
       const uint32_t vbuf = smem_u32(smem + C::kVOff + vs * C::kTileBytes);
       wait(&ctl->vfull[vs], (nv / C::VS) & 1);
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (a.window && j0 <= first + x.nt - 1 - a.window);
       auto sees = [&](int p, int j) {
         return j <= p && (!a.window || j > p - a.window) &&
-               !((bad >> ((j - j0) >> min(a.lps, 7))) & 1u);
+               !((bad >> ((j - j0) >> 4)) & 1u);
       };
 #pragma unroll
       for (int i = 0; i < 2 * WR; ++i) {
@@ -473,58 +472,9 @@ __global__ void __launch_bounds__(128)
   if (s.n > tp || tk >= s.n) return;
   const int ns = n_splits(max_tiles(a, s.len, tp), WR);
   if (ns == 1) return;
-  const int64_t rec = (((int64_t)b * tp + tk) * H + hd) * ns_cap;
-  float2 ml[4];                        // ns <= 128: four records to a lane
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int k = i * 32 + lane;
-    ml[i] = k < ns ? __ldcg(o.part_ml + rec + k) : make_float2(-INFINITY, 0.f);
-    top = fmaxf(top, ml[i].x);
-  }
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-  const float ref = top == -INFINITY ? 0.f : top;
-  float f[4], sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = exp2f(ml[i].x - ref);
-    sum += f[i] * ml[i].y;
-  }
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-  constexpr int DL = D / 32;
-  float acc[DL] = {};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int cnt = min(32, ns - i * 32);
-    for (int k = 0; k < cnt; ++k) {
-      const float w = __shfl_sync(0xffffffffu, f[i], k);
-      const float* src = o.part + (rec + i * 32 + k) * D + lane * DL;
-      if (w == 0.f) continue;          // a split without keys that this row sees
-#pragma unroll
-      for (int e = 0; e < DL; e += 2) {
-        const float2 y = __ldcg(reinterpret_cast<const float2*>(src + e));
-        acc[e] = fmaf(w, y.x, acc[e]);
-        acc[e + 1] = fmaf(w, y.y, acc[e + 1]);
-      }
-    }
-  }
   const int64_t row = (int64_t)(s.row0 + tk) * H + hd;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int e = 0; e < DL; e += 2)
-    *reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(o.out) + row * D + lane * DL + e) =
-        Num<T>::pack(acc[e] * inv, acc[e + 1] * inv);
-  if (o.lse && lane == 0) o.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 1;
-  return n;
+  join_row<T, D>(o.part, o.part_ml, (((int64_t)b * tp + tk) * H + hd) * ns_cap, ns,
+                 reinterpret_cast<T*>(o.out) + row * D, o.lse ? o.lse + row : nullptr, lane);
 }
 
 template <typename T, int D, int WR>

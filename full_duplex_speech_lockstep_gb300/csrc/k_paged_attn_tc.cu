@@ -1,0 +1,641 @@
+// k_paged_attn_tc.cu - attention of long chunks over the paged cache, on the 5th-generation
+// tensor cores.  Rows, masks and results as in k_paged_attn.cu.
+//
+// A unit is (sequence, pair of row tiles, key head, split of the keys); a row tile is 128 rows,
+// floor(128 / G) tokens with all G heads of the key head.  The two tiles of a pair take turns:
+// while the tensor cores multiply for one, the other's softmax runs.
+//
+//   S_t = Q_t K^T   M = 128 rows, N = 128 keys, operands in shared memory, S in tensor memory
+//   P_t = 2^(S c - m), in the cache's type over S's own tensor-memory columns
+//   O_t += P_t V    A = P from tensor memory, B = V as it lies (keys x dims, dims contiguous)
+//
+// Tensor memory: S0, S1 (128 columns each), O0, O1 (D columns each).
+//   warp 0       producer: queries of the pair, then K and V tiles in turn, by TMA
+//   warp 1       one thread issues every MMA.  Order for each tile of keys: O0 += P0 V,
+//                S0 = Q0 K', O1 += P1 V, S1 = Q1 K' (K' the next keys).  MMAs run in issue
+//                order, so S_t may overwrite P_t right after the product that reads it.
+//   warps 4-7, 8-11  softmax of tile 0, 1: one thread to a row.  A row's reference m follows
+//                its maximum only when it would fall behind by more than 2^8, so the sums of
+//                O in tensor memory are rarely rescaled; p stays below 2^8 (2^15 in fp16),
+//                and m cancels in the end.
+//
+// Where some row does not see some key of a tile, non-finite values of V are taken out of
+// shared memory before the product (zero times infinity would be NaN) and added to the rows
+// that do see the key at the end.
+#include <type_traits>
+
+#include "pp_paged.cuh"
+#include "pp_tcgen05.cuh"
+
+namespace pp {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRowsT = 128;          // rows of a row tile
+constexpr float kLag = 8.f;          // a row's maximum may exceed its reference by this (log2)
+// registers a thread: launched with 168; the softmax warps take what the others give up
+// (80 + 2 x 208 = 496 <= 3 x 168 for each three threads)
+constexpr int kRegsFew = 80, kRegsMany = 208;
+
+template <int D>
+struct Cfg {
+  static constexpr int kSlots = D == 128 ? 4 : 8;   // K and V tiles
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kQBytes = kRowsT * D * 2;    // one row tile
+  static constexpr int kQOff = kSlots * kTileBytes;
+  static constexpr int kCtlOff = kQOff + 2 * kQBytes;
+};
+
+struct Ctl {
+  uint64_t full[8], empty[8];
+  uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], done;
+  uint64_t clean[2][2];   // [group][edge tile & 1]: the group's half of V is clean
+  uint32_t bad[8];
+  uint32_t tmem;
+  // 1 + the unit in which a softmax group took a non-finite value out of V.  A group is at
+  // most one unit ahead of the other, so two entries each are enough.
+  int wild[2][2];
+  int abort;
+};
+
+struct Unit {
+  int b, h, split, ns;
+  int row0, n, len;
+  int t0, nt;            // first token of the pair, its tokens (up to 2 tp)
+  int tile0, tile1;      // key tiles
+  int end, low;          // entries that some row of the pair sees: [low, end)
+};
+
+__device__ __forceinline__ int seq_splits(const Args& a, const Seq& s, int tp, int ns) {
+  const int all = (s.len + kTile - 1) / kTile;
+  const int most = a.window ? min(all, (int)(((int64_t)a.window + 2 * tp - 2) / kTile) + 2) : all;
+  return max(1, min(ns, most / 8));    // a split has at least eight tiles of keys
+}
+
+__device__ __forceinline__ int seq_units(const Args& a, int b, int tp, int ns) {
+  const Seq s = seq_of(a, b);
+  if (s.n == 0) return 0;
+  return a.Hk * ((s.n + 2 * tp - 1) / (2 * tp)) * seq_splits(a, s, tp, ns);
+}
+
+__device__ __forceinline__ Unit unit_of(const Args& a, const int* pre, int u, int tp, int ns) {
+  Unit x;
+  x.b = find_seq(pre, a.n_seqs, u);
+  const Seq s = seq_of(a, x.b);
+  u -= pre[x.b];
+  const int pairs = (s.n + 2 * tp - 1) / (2 * tp);
+  x.ns = seq_splits(a, s, tp, ns);
+  // the last pairs, whose rows see most, come first; heads vary fastest
+  const int per = a.Hk * x.ns;
+  const int p = pairs - 1 - u / per;
+  u %= per;
+  x.h = u / x.ns;
+  x.split = u - x.h * x.ns;
+  x.t0 = p * 2 * tp;
+  x.nt = min(2 * tp, s.n - x.t0);
+  x.row0 = s.row0;
+  x.n = s.n;
+  x.len = s.len;
+  const int first = s.len - s.n + x.t0;
+  x.end = max(first + x.nt, 0);
+  x.low = a.window ? min(max(first - a.window + 1, 0), x.end) : 0;
+  const int ta = x.low / kTile, tb = (x.end + kTile - 1) / kTile;
+  const int st = (tb - ta + x.ns - 1) / x.ns;
+  x.tile0 = min(ta + x.split * st, tb);
+  x.tile1 = min(x.tile0 + st, tb);
+  return x;
+}
+
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// 32 columns of this thread's tensor-memory lane
+__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+
+// Zeroes the non-finite halves of w; true if there were any.
+template <typename N>
+__device__ __forceinline__ bool finite_only(uint32_t& w) {
+  uint32_t keep = 0xffffffffu;
+  if ((w & N::kExp) == N::kExp) keep &= 0xffff0000u;
+  if (((w >> 16) & N::kExp) == N::kExp) keep &= 0xffffu;
+  w &= keep;
+  return keep != 0xffffffffu;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_paged_attn_tc(const Args a, const int tp, const int ns_cap, const AttnOut o,
+                    const __grid_constant__ CUtensorMap mapK,
+                    const __grid_constant__ CUtensorMap mapV,
+                    const __grid_constant__ CUtensorMap mapQ, const void* v_pages) {
+  using C = Cfg<D>;
+  using N = Num<T>;
+  constexpr int kSlots = C::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::kCtlOff);
+  int* pre = reinterpret_cast<int*>(ctl + 1);
+  volatile int* abort_flag = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&ctl->full[i]), 1);
+      mbar_init(smem_u32(&ctl->empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ctl->qfull), 1);
+    mbar_init(smem_u32(&ctl->qempty), 1);
+    mbar_init(smem_u32(&ctl->done), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&ctl->sfull[t]), 1);
+      mbar_init(smem_u32(&ctl->pfull[t]), 4);
+      mbar_init(smem_u32(&ctl->ofull[t]), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&ctl->clean[t][i]), 4);
+        ctl->wild[t][i] = 0;
+      }
+    }
+    ctl->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&ctl->tmem)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  pdl_wait_and_trigger();
+  pdl_trigger();
+  prefix_units(pre, a.n_seqs, [&](int b) { return seq_units(a, b, tp, ns_cap); });
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = ctl->tmem;
+  const int units = pre[a.n_seqs];
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (*abort_flag) return;
+    if (!mbar_wait(smem_u32(bar), parity)) {
+      *abort_flag = 1;
+      raise(a, PP_S_TIMEOUT);
+    }
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp == 0) {
+      // ---- producer -----------------------------------------------------------------------
+      uint32_t nq = 0, nl = 0, seen_bad = 0;
+      for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
+        const Unit x = unit_of(a, pre, u, tp, ns_cap);
+        if (x.tile0 == x.tile1) continue;
+        const int tiles = x.nt > tp ? 2 : 1;
+        if (nq > 0) wait(&ctl->qempty, (nq - 1) & 1);
+        if (*abort_flag) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&ctl->qfull);
+          mbar_expect_tx(bar, (uint32_t)(tiles * tp * a.G * D * 2));
+          for (int t = 0; t < tiles; ++t)
+            for (int bx = 0; bx < D / 64; ++bx)
+              tma_load_4d(smem_u32(smem + C::kQOff + t * C::kQBytes + bx * kRowsT * 128), &mapQ,
+                          bx * 64, x.h * a.G, x.row0 + x.t0 + t * tp, 0, bar);
+        }
+        ++nq;
+        for (int i = 0; i < 2 * (x.tile1 - x.tile0); ++i) {
+          const int slot = nl % kSlots;
+          if (nl >= kSlots) wait(&ctl->empty[slot], (nl / kSlots - 1) & 1);
+          if (*abort_flag) break;
+          const int t = x.tile0 + (i >> 1);
+          const uint32_t bad =
+              load_key_tile(a, (i & 1) ? &mapV : &mapK, smem_u32(smem + slot * C::kTileBytes),
+                            smem_u32(&ctl->full[slot]), x.b, x.h, t * kTile, x.end, lane,
+                            &ctl->bad[slot]);
+          seen_bad |= bad;
+          ++nl;
+        }
+      }
+      if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
+      // every copy lands before the CTA may exit (bounded waits)
+      if (lane == 0) {
+        if (nq > 0) mbar_wait(smem_u32(&ctl->qfull), (nq - 1) & 1);
+        for (uint32_t i = nl > kSlots ? nl - kSlots : 0; i < nl; ++i)
+          mbar_wait(smem_u32(&ctl->full[i % kSlots]), (i / kSlots) & 1);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---- MMA issuer ---------------------------------------------------------------------
+      if (lane == 0) {
+        constexpr uint32_t id = (1u << 4) | N::kMmaTypes | ((uint32_t)(kRowsT >> 4) << 24);
+        constexpr uint32_t id_s = id | ((uint32_t)(kTile >> 3) << 17);
+        constexpr uint32_t id_o = id | ((uint32_t)(D >> 3) << 17) | (1u << 16);   // B = V by keys
+        uint32_t nq = 0, nl = 0, np[2] = {0, 0};
+        auto scores = [&](int t, uint32_t slot) {
+          const uint32_t qb = smem_u32(smem + C::kQOff + t * C::kQBytes);
+          const uint32_t kb = smem_u32(smem + slot * C::kTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+            umma_bf16(tmem + t * kTile, smem_desc(qb + off), smem_desc(kb + off), id_s, kk > 0);
+          }
+          umma_commit(smem_u32(&ctl->sfull[t]));
+        };
+        for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
+          const Unit x = unit_of(a, pre, u, tp, ns_cap);
+          const int nt = x.tile1 - x.tile0;
+          if (nt == 0) continue;
+          const int tiles = x.nt > tp ? 2 : 1;
+          wait(&ctl->qfull, nq & 1);
+          ++nq;
+          wait(&ctl->full[nl % kSlots], (nl / kSlots) & 1);
+          if (*abort_flag) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          for (int t = 0; t < tiles; ++t) scores(t, nl % kSlots);
+          umma_commit(smem_u32(&ctl->empty[nl % kSlots]));
+          if (nt == 1) umma_commit(smem_u32(&ctl->qempty));
+          ++nl;
+          for (int j = 0; j < nt; ++j) {
+            const uint32_t sv = nl % kSlots, sk = (nl + 1) % kSlots;
+            const bool more = j + 1 < nt;
+            wait(&ctl->full[sv], (nl / kSlots) & 1);
+            for (int t = 0; t < tiles; ++t) {
+              wait(&ctl->pfull[t], np[t] & 1);
+              ++np[t];
+              if (*abort_flag) break;
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              const uint32_t vb = smem_u32(smem + sv * C::kTileBytes);
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                umma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + kk * 8,
+                        smem_desc_mn(vb + kk * 2048, kTile * 128), id_o, j > 0 || kk > 0);
+              if (more) {
+                if (t == 0) {
+                  wait(&ctl->full[sk], ((nl + 1) / kSlots) & 1);
+                  if (*abort_flag) break;
+                  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                }
+                scores(t, sk);
+              } else {
+                umma_commit(smem_u32(&ctl->ofull[t]));
+              }
+            }
+            if (*abort_flag) break;
+            umma_commit(smem_u32(&ctl->empty[sv]));
+            if (more) {
+              umma_commit(smem_u32(&ctl->empty[sk]));
+              if (j + 2 == nt) umma_commit(smem_u32(&ctl->qempty));
+              nl += 2;
+            } else {
+              nl += 1;
+            }
+          }
+        }
+        // every MMA is done before tensor memory is given back (bounded wait)
+        umma_commit(smem_u32(&ctl->done));
+        mbar_wait(smem_u32(&ctl->done), 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+    // ---- softmax: thread r of the group owns row r of its tile -------------------------------
+    const int t = (warp - 4) >> 2;
+    const int r = threadIdx.x - 128 - t * 128;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_at = lane_base + t * kTile, o_at = lane_base + 2 * kTile + t * D;
+    const uint64_t c2 = pair(a.c, a.c);
+    uint32_t ns_ = 0, no = 0, nl = 0, ne = 0, nu = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++nu) {
+      const Unit x = unit_of(a, pre, u, tp, ns_cap);
+      const int nt = x.tile1 - x.tile0;
+      const int tiles = x.nt > tp ? 2 : 1;
+      if (t >= tiles) {        // a pair of one tile: nothing to do here but count
+        nl += 2 * nt;
+        continue;
+      }
+      const int first = x.len - x.n + x.t0;
+      const int tokens = min(tp, x.nt - t * tp);
+      const int tk = min(r / a.G, tokens - 1);
+      const int pos = first + t * tp + tk;
+      const bool live = r < tokens * a.G;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nt; ++j) {
+        const int j0 = (x.tile0 + j) * kTile;
+        // does some row of the pair not see some key?
+        const int last = first + x.nt - 1;
+        const uint32_t vslot = (nl + 2 * j + 1) % kSlots;
+        wait(&ctl->full[vslot], ((nl + 2 * j + 1) / kSlots) & 1);
+        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&ctl->bad[vslot]);
+        const bool edge = bad || j0 + kTile - 1 > first || (a.window && j0 <= last - a.window);
+        if (edge) {
+          // take non-finite values out of V (this group's rows of the tile)
+          const int share = kTile / tiles;
+          uint8_t* vt = smem + vslot * C::kTileBytes;
+          bool found = false;
+          for (int i = r; i < share * (D / 8); i += 128) {
+            const int row = t * share + i / (D / 8), ch = i % (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(
+                vt + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            uint4 w = *at;
+            const bool hit = finite_only<N>(w.x) | finite_only<N>(w.y) | finite_only<N>(w.z) |
+                             finite_only<N>(w.w);
+            if (hit) {
+              *at = w;
+              found = found || (j0 + row >= x.low && j0 + row < x.end);
+            }
+          }
+          if (found) ctl->wild[t][nu & 1] = u + 1;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (tiles == 2) {    // both halves, before either product
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->clean[t][ne & 1]));
+            wait(&ctl->clean[t ^ 1][ne & 1], (ne >> 1) & 1);
+            ++ne;
+          }
+        }
+        wait(&ctl->sfull[t], ns_ & 1);
+        ++ns_;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        auto weights = [&](auto masked) {
+          uint32_t s[kTile];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_at + i * 32, s + i * 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) asm volatile("" : "+r"(s[i]));
+          if constexpr (decltype(masked)::value) {
+            // keys (pos - window, pos], as places in this tile
+            const int hi = pos - j0, lo = a.window ? hi - a.window : -1;
+#pragma unroll
+            for (int i = 0; i < kTile; ++i)
+              if (i > hi || i <= lo) s[i] = 0xff800000u;
+            if (bad) {
+  #pragma unroll
+              for (int i = 0; i < kTile; ++i)
+                if ((bad >> (i >> 4)) & 1u) s[i] = 0xff800000u;
+            }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kTile; i += 2)
+            mx = max3(mx, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          const float want = mx * a.c - N::kShift;
+          if (j == 0) {
+            m = mx == -INFINITY ? -INFINITY : want;
+          } else if (__any_sync(0xffffffffu, want > m + kLag)) {
+            // O = O 2^(old - new), row by row; the product that O holds is done, since S was
+            // issued after it
+            const float mn = want > m + kLag ? want : m;
+            const float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
+            l *= f;
+            m = mn;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              uint32_t w[8];
+              tmem_ld8(o_at + i * 8, w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(after_wait(w[e]) * f);
+              tmem_st8(o_at + i * 8, w);
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          const uint64_t r2 = pair(-ref, -ref);
+          uint64_t sum2 = pair(l, 0.f);
+          uint32_t p[kTile / 2];
+#pragma unroll
+          for (int i = 0; i < kTile; i += 2) {
+            const uint64_t z = fma2((uint64_t)s[i] | ((uint64_t)s[i + 1] << 32), c2, r2);
+            const float p0 = exp2_approx(lo_of(z)), p1 = exp2_approx(hi_of(z));
+            sum2 = add2(sum2, pair(p0, p1));
+            p[i >> 1] = N::pack(p0, p1);
+          }
+          l = lo_of(sum2) + hi_of(sum2);
+          tmem_st32(s_at, p);
+          tmem_st32(s_at + 32, p + 32);
+        };
+        if (edge)
+          weights(std::true_type());
+        else
+          weights(std::false_type());
+        tmem_wait_st();
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->pfull[t]));
+      }
+      nl += 2 * nt;
+
+      // ---- the rows' results, or the split's partials --------------------------------------
+      const int H = a.Hk * a.G;
+      const int token = x.t0 + t * tp + tk, hd = x.h * a.G + r - tk * a.G;
+      const int64_t row = (int64_t)(x.row0 + token) * H + hd;
+      const int64_t rec = row * ns_cap + x.split;
+      const bool whole = x.ns == 1;
+      bool wild = false;
+      if (nt > 0) {
+        wait(&ctl->ofull[t], no & 1);
+        ++no;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        wild = *reinterpret_cast<volatile int*>(&ctl->wild[0][nu & 1]) == u + 1 ||
+               *reinterpret_cast<volatile int*>(&ctl->wild[1][nu & 1]) == u + 1;
+      }
+      const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t w[32];
+        if (nt > 0) {
+          tmem_ld32(o_at + i * 32, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(w[e]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = 0;
+        }
+        if (wild && live) {
+          // rare: add the non-finite values that this row sees in the tiles that were cleaned
+          // (their weights are positive)
+          for (int j0 = x.tile0 * kTile; j0 < min(x.tile1 * kTile, x.end); j0 += kTile) {
+            const int j1 = min(j0 + kTile, x.end);
+            bool cleaned = j0 + kTile - 1 > first ||
+                           (a.window && j0 <= first + x.nt - 1 - a.window);
+            for (int j = j0; j < j1; j += 1 << a.lps) cleaned |= page_of(a, x.b, j) < 0;
+            if (!cleaned) continue;
+            for (int j = j0; j < j1; ++j) {
+              const int pg = page_of(a, x.b, j);
+              if (j > pos || (a.window && j <= pos - a.window) || pg < 0) continue;
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(v_pages) + pg * a.page_stride +
+                                  (((int64_t)x.h << a.lps) + (j & ((1 << a.lps) - 1))) * D + i * 32;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((v[e] & N::kExp) == N::kExp)
+                  w[e] = __float_as_uint(__uint_as_float(w[e]) + N::to_float(v[e]));
+            }
+          }
+        }
+        if (live) {
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(o.out) + row * D + i * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                y[k] = N::pack(__uint_as_float(w[e * 8 + k * 2]) * f,
+                               __uint_as_float(w[e * 8 + k * 2 + 1]) * f);
+              dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else if (nt > 0) {
+            uint4* dst = reinterpret_cast<uint4*>(o.part + rec * D + i * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_uint4(w[e * 4], w[e * 4 + 1], w[e * 4 + 2], w[e * 4 + 3]);
+          }
+        }
+      }
+      if (live) {
+        if (!whole)
+          o.part_ml[rec] = make_float2(m, l);
+        else if (o.lse)
+          o.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+      // the next unit's products into O come after this group's next P
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+// Join the splits of each row: one warp to a (row, head).
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+    k_paged_join_rows(const Args a, const int tp, const int ns_cap, const AttnOut o) {
+  pdl_wait_and_trigger();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, H = a.Hk * a.G;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int64_t row = id / H;
+  if (row >= a.T) return;
+  int lo = 0, hi = a.n_seqs;           // the last sequence that starts at or before the row
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= row) lo = mid; else hi = mid;
+  }
+  const Seq s = seq_of(a, lo);
+  if (row < s.row0 || row >= s.row0 + s.n) return;
+  const int ns = seq_splits(a, s, tp, ns_cap);
+  if (ns == 1) return;
+  join_row<T, D>(o.part, o.part_ml, id * ns_cap, ns, reinterpret_cast<T*>(o.out) + id * D,
+                 o.lse ? o.lse + id : nullptr, lane);
+}
+
+template <typename T, int D>
+cudaError_t run(const Args& a, const LongPlan& p, const Maps& maps, const AttnOut& o,
+                const void* v_pages, cudaStream_t s) {
+  const size_t smem = Cfg<D>::kCtlOff + sizeof(Ctl) + (size_t)(a.n_seqs + 1) * sizeof(int) + 1024;
+  cudaError_t err = cudaFuncSetAttribute(k_paged_attn_tc<T, D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  const int64_t most = ((int64_t)a.T / (2 * p.tp) + a.n_seqs) * a.Hk * p.ns;
+  const int nsm = sm_count();
+  err = launch(k_paged_attn_tc<T, D>, dim3((unsigned)(most < nsm ? most : nsm)), kThreads, smem, s,
+               a, p.tp, p.ns, o, maps.k, maps.v, maps.q, v_pages);
+  if (err != cudaSuccess || p.ns == 1) return err;
+  const int64_t rows = (int64_t)a.T * a.Hk * a.G;
+  return launch(k_paged_join_rows<T, D>, dim3((unsigned)((rows + 3) / 4)), 128, 0, s, a, p.tp, p.ns,
+                o);
+}
+
+}  // namespace
+
+LongPlan long_plan(const Args& a, int T, int max_q) {
+  LongPlan p{};
+  p.tp = kRowsT / a.G;
+  // sequences as long as max_q, and the units they make without a split; fewer than two for
+  // each of the 152 SMs: split the keys
+  const int64_t q = max_q < T ? max_q : (T < 1 ? 1 : T);
+  int64_t seqs = (T + q - 1) / q;
+  if (seqs > a.n_seqs) seqs = a.n_seqs;
+  const int64_t units = seqs * a.Hk * ((q + 2 * p.tp - 1) / (2 * p.tp));
+  int64_t ns = units < 1 ? 1 : (2 * 152 + units - 1) / units;
+  const int64_t tiles = (((int64_t)a.table_ld << a.lps) + kTile - 1) / kTile;
+  if (ns > tiles / 8) ns = tiles / 8;
+  p.ns = (int)(ns < 1 ? 1 : ns > 16 ? 16 : ns);
+  const size_t recs = (size_t)T * a.Hk * a.G * p.ns;
+  p.rec_bytes = p.ns == 1 ? 0 : (recs * a.D * sizeof(float) + 255) & ~(size_t)255;
+  p.ml_bytes = p.ns == 1 ? 0 : (recs * sizeof(float2) + 255) & ~(size_t)255;
+  return p;
+}
+
+cudaError_t launch_paged_attn_tc(const Args& a, int type, const LongPlan& plan, const Maps& maps,
+                                 const AttnOut& o, const void* v_pages, cudaStream_t s) {
+  if (type == PP_BF16)
+    return a.D == 128 ? run<__nv_bfloat16, 128>(a, plan, maps, o, v_pages, s)
+                      : run<__nv_bfloat16, 64>(a, plan, maps, o, v_pages, s);
+  return a.D == 128 ? run<__half, 128>(a, plan, maps, o, v_pages, s)
+                    : run<__half, 64>(a, plan, maps, o, v_pages, s);
+}
+
+}  // namespace paged
+}  // namespace pp

@@ -28,7 +28,6 @@ struct Cfg {
 
 struct Ctl {
   uint64_t kfull[kKS], kempty[kKS], qfull[kQS], qempty[kQS];
-  uint32_t bad[kKS];
   int abort;
 };
 
@@ -106,7 +105,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nk >= kKS) wait(&ctl->kempty[ks], (nk / kKS - 1) & 1);
       if (*abort_flag) break;
       const uint32_t bad = load_key_tile(a, &mapK, smem_u32(smem + ks * C::kTileBytes),
-                                         smem_u32(&ctl->kfull[ks]), x.b, x.h, x.j0, x.len, lane);
+                                         smem_u32(&ctl->kfull[ks]), x.b, x.h, x.j0, x.len, lane,
+                                         nullptr);
       seen_bad |= bad;
       ++nk;
       for (int t = x.t0; t < x.t1; t += tp) {
@@ -229,10 +229,7 @@ cudaError_t run(const Args& a, const Maps& maps, int tp, const float* lse, float
   cudaError_t err = cudaFuncSetAttribute(k_paged_mass<T, D, WR>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  int dev = 0, nsm = 1;
-  if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
-  if ((err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return err;
+  const int nsm = sm_count();
   const int64_t tiles = (((int64_t)a.table_ld << a.lps) + kTile - 1) / kTile;
   const int64_t most = (int64_t)a.n_seqs * a.Hk * tiles;
   return launch(k_paged_mass<T, D, WR>, dim3((unsigned)(most < nsm ? most : nsm)), kThreads, smem,

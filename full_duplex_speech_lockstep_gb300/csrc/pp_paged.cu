@@ -93,6 +93,8 @@ bool query_map(CUtensorMap* m, const Args& a, int type, const void* q, int64_t s
   return encode(m, type, q, dim, stride, box);
 }
 
+bool is_long(const Args& a, int max_q) { return (int64_t)max_q * a.G > kShortRows; }
+
 int rc(cudaError_t err) { return err == cudaSuccess ? PP_OK : PP_E_CUDA; }
 
 }  // namespace
@@ -147,13 +149,18 @@ int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, cons
   return rc(launch_paged_append(a, x, turns, in_type, kv->type, (cudaStream_t)stream));
 }
 
-size_t pp_paged_attention_scratch_bytes(const pp_paged_kv* kv, int n_heads, int max_q, int window) {
-  if (!cache_ok(kv) || n_heads < 1 || n_heads % kv->n_kv_heads != 0 ||
-      n_heads / kv->n_kv_heads > kMaxGroup || !scores_ok(1.f, window, max_q))
+size_t pp_paged_attention_scratch_bytes(const pp_paged_kv* kv, int n_heads, int T, int max_q,
+                                        int window) {
+  const int32_t any = 0;
+  if (!cache_ok(kv) || !rows_ok(kv, &any, &any, T, n_heads) || !scores_ok(1.f, window, max_q))
     return 0;
   Args a = base_args(kv, nullptr, nullptr);
   a.G = n_heads / kv->n_kv_heads;
   a.window = effective_window(kv, window);
+  if (is_long(a, max_q)) {
+    const LongPlan p = long_plan(a, T, max_q);
+    return p.rec_bytes + p.ml_bytes + 256;
+  }
   const AttnPlan p = attn_plan(a, max_q);
   return p.rec_bytes + p.ml_bytes + 256;
 }
@@ -171,7 +178,7 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
     return PP_EINVAL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(scratch, 256))
     return PP_EINVAL;
-  if (scratch_bytes < pp_paged_attention_scratch_bytes(kv, n_heads, max_q, window))
+  if (scratch_bytes < pp_paged_attention_scratch_bytes(kv, n_heads, T, max_q, window))
     return PP_E_NOSPACE;
   Args a = base_args(kv, kv_len, status);
   a.cu = cu;
@@ -179,17 +186,21 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
   a.G = n_heads / kv->n_kv_heads;
   a.window = effective_window(kv, window);
   a.c = scale * kLog2e;
+  const bool tall = is_long(a, max_q);
   const AttnPlan plan = attn_plan(a, max_q);
+  const LongPlan tall_plan = long_plan(a, T, max_q);
   Maps maps;
   if (!page_map(&maps.k, kv, kv->k) || !page_map(&maps.v, kv, kv->v) ||
-      !query_map(&maps.q, a, kv->type, q, q_stride, plan.tp))
+      !query_map(&maps.q, a, kv->type, q, q_stride, tall ? tall_plan.tp : plan.tp))
     return PP_EINVAL;
   AttnOut o{};
   o.out = out;
   o.lse = lse;
   o.part = reinterpret_cast<float*>(scratch);
-  o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) + plan.rec_bytes);
-  return rc(launch_paged_attn(a, kv->type, plan, maps, o, (cudaStream_t)stream));
+  o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) +
+                                        (tall ? tall_plan.rec_bytes : plan.rec_bytes));
+  return rc(tall ? launch_paged_attn_tc(a, kv->type, tall_plan, maps, o, kv->v, (cudaStream_t)stream)
+                 : launch_paged_attn(a, kv->type, plan, maps, o, (cudaStream_t)stream));
 }
 
 int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const float* lse,

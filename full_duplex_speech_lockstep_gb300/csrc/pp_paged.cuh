@@ -104,11 +104,13 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int box_bytes, int 
 }
 
 // Load one key tile (entries [j0, j0 + 128) of head h) by one warp: a lane for each
-// (page, 64-dim box).  Entries at or past `end` and pages outside the pool arrive as zeros;
-// returns, in every lane, a mask of the tile's pages outside the pool.
+// (page, 64-dim box).  Entries at or past `end` and pages outside the pool arrive as zeros.
+// A mask of the tile's 16-key groups in pages outside the pool is returned in every lane and,
+// with `bad_out`, stored before the copy's barrier is armed: whoever has waited for the tile may
+// read it.
 __device__ __forceinline__ uint32_t load_key_tile(const Args& a, const CUtensorMap* map,
                                                   uint32_t dst, uint32_t bar, int b, int h, int j0,
-                                                  int end, int lane) {
+                                                  int end, int lane, uint32_t* bad_out) {
   const int per = min(1 << a.lps, kTile);          // rows of one box
   const int pages = kTile / per, boxes = a.D >> 6;
   const int pg = lane % pages, bx = lane / pages;  // lane < pages * boxes <= 16 loads
@@ -120,12 +122,21 @@ __device__ __forceinline__ uint32_t load_key_tile(const Args& a, const CUtensorM
     bad = p < 0;
     if (!bad) page = p;
   }
-  if (lane == 0) mbar_expect_tx(bar, (uint32_t)(kTile * a.D * 2));
+  uint32_t mask = __ballot_sync(0xffffffffu, bad && bx == 0);
+  if (mask) {                                      // rare: from pages to groups
+    uint32_t groups = 0;
+    for (int g = 0; g < 8; ++g) groups |= ((mask >> (g * 16 / per)) & 1u) << g;
+    mask = groups;
+  }
+  if (lane == 0) {
+    if (bad_out) *reinterpret_cast<volatile uint32_t*>(bad_out) = mask;
+    mbar_expect_tx(bar, (uint32_t)(kTile * a.D * 2));
+  }
   __syncwarp();
   if (bx < boxes)
     tma_load_4d(dst + bx * (kTile * 128) + pg * per * 128, map, bx * 64, j & ((1 << a.lps) - 1), h,
                 page, bar);
-  return __ballot_sync(0xffffffffu, bad && bx == 0) & 0xffu;
+  return mask;
 }
 
 // ---- matrix fragments ----------------------------------------------------------------------
@@ -151,6 +162,7 @@ template <>
 struct Num<__nv_bfloat16> {
   static constexpr float kShift = 0.f;
   static constexpr uint32_t kExp = 0x7f80u, kOne = 0x3f80u;
+  static constexpr uint32_t kMmaTypes = (1u << 7) | (1u << 10);   // A and B in an MMA descriptor
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -170,6 +182,7 @@ template <>
 struct Num<__half> {
   static constexpr float kShift = 7.f;
   static constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;
+  static constexpr uint32_t kMmaTypes = 0u;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -192,6 +205,62 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Split partials of one row joined by one warp, in split order: rec is the row's first record
+// and ns <= 128 their count.
+template <typename T, int D>
+__device__ __forceinline__ void join_row(const float* part, const float2* part_ml, int64_t rec,
+                                         int ns, T* out, float* lse, int lane) {
+  float2 ml[4];                        // four records to a lane
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = i * 32 + lane;
+    ml[i] = k < ns ? __ldcg(part_ml + rec + k) : make_float2(-INFINITY, 0.f);
+    top = fmaxf(top, ml[i].x);
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float f[4], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = exp2f(ml[i].x - ref);
+    sum += f[i] * ml[i].y;
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+  constexpr int DL = D / 32;
+  float acc[DL] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int cnt = min(32, ns - i * 32);
+    for (int k = 0; k < cnt; ++k) {
+      const float w = __shfl_sync(0xffffffffu, f[i], k);
+      const float* src = part + (rec + i * 32 + k) * D + lane * DL;
+      if (w == 0.f) continue;          // a split without keys that this row sees
+#pragma unroll
+      for (int e = 0; e < DL; e += 2) {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(src + e));
+        acc[e] = fmaf(w, y.x, acc[e]);
+        acc[e + 1] = fmaf(w, y.y, acc[e + 1]);
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < DL; e += 2)
+    *reinterpret_cast<uint32_t*>(out + lane * DL + e) = Num<T>::pack(acc[e] * inv, acc[e + 1] * inv);
+  if (lse && lane == 0) *lse = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 1;
+  return n;
 }
 
 // ---- launches ------------------------------------------------------------------------------
@@ -238,6 +307,16 @@ struct AttnPlan : RowTile {
 };
 AttnPlan attn_plan(const Args& a, int max_q);
 
+// Chunks of more than kShortRows rows (tokens x heads of a key head) run on the 5th-generation
+// tensor cores (k_paged_attn_tc.cu): row tiles of 128 rows, taken in pairs.
+constexpr int kShortRows = 64;
+struct LongPlan {
+  int tp;          // tokens of a row tile
+  int ns;          // splits of a sequence's keys, at most
+  size_t rec_bytes, ml_bytes;
+};
+LongPlan long_plan(const Args& a, int T, int max_q);
+
 struct AttnOut {
   void* out;
   float* lse;      // may be null
@@ -247,6 +326,8 @@ struct AttnOut {
 
 cudaError_t launch_paged_attn(const Args& a, int type, const AttnPlan& plan, const Maps& maps,
                               const AttnOut& o, cudaStream_t s);
+cudaError_t launch_paged_attn_tc(const Args& a, int type, const LongPlan& plan, const Maps& maps,
+                                 const AttnOut& o, const void* v_pages, cudaStream_t s);
 cudaError_t launch_paged_mass(const Args& a, int type, const RowTile& r, const Maps& maps,
                               const float* lse, float* mass, float decay, cudaStream_t s);
 

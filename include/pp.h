@@ -523,9 +523,10 @@ int pp_rvq_dequantize(const int32_t* codes, int code_stride, int n_frames, int n
  *
  * Every call is asynchronous on `stream`, belongs to the current device, allocates nothing
  * and may be captured into a graph; lengths, tables and row offsets are read when the
- * graph runs.  status (a device word) may be NULL.  A sequence's results depend on its
- * own rows, entries and lengths and on the call's head counts and max_q, bit for bit,
- * never on the other sequences. */
+ * graph runs.  status (a device word) may be NULL; PP_S_TIMEOUT is OR-ed into it when a
+ * bounded wait inside a kernel gave up (the results are then incomplete).  A sequence's results depend on its
+ * own rows, entries and lengths and on the call's head counts, n_seqs, T and max_q, bit for
+ * bit, never on what the other sequences hold. */
 #define PP_F32 0
 #define PP_BF16 1
 #define PP_F16 2
@@ -588,7 +589,8 @@ int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, cons
  *            contents need no set-up; calls that may overlap need their own
  * scale > 0; window >= 0 (0: none); max_q >= 1.  T == 0 does nothing.  Errors: PP_EINVAL,
  * PP_E_NOSPACE, PP_E_CUDA.  pp_paged_attention_scratch_bytes returns 0 for bad arguments. */
-size_t pp_paged_attention_scratch_bytes(const pp_paged_kv* kv, int n_heads, int max_q, int window);
+size_t pp_paged_attention_scratch_bytes(const pp_paged_kv* kv, int n_heads, int T, int max_q,
+                                        int window);
 int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, const int32_t* cu,
                        const int32_t* kv_len, int T, int max_q, int n_heads, float scale,
                        int window, void* out, float* lse, uint32_t* status, void* scratch,

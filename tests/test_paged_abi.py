@@ -60,7 +60,7 @@ def test_every_call_refuses_a_bad_cache(bad):
     assert evict(kv, cache()) == pp.PP_EINVAL
     assert evict(cache(), kv) == pp.PP_EINVAL
     with pytest.raises(pp.PPError):
-        pp.pp_paged_attention_scratch_bytes(kv, 4, 1, 0)
+        pp.pp_paged_attention_scratch_bytes(kv, 4, 3, 1, 0)
 
 
 def test_null_cache():
@@ -91,19 +91,20 @@ def test_attention_refuses(bad):
 
 
 def test_attention_refuses_small_scratch():
-    n = pp.pp_paged_attention_scratch_bytes(cache(), 4, 5, 0)
+    n = pp.pp_paged_attention_scratch_bytes(cache(), 4, 5, 5, 0)
     assert attention(cache(), nbytes=n - 1) == pp.PP_E_NOSPACE
 
 
-def test_scratch_does_not_depend_on_rows_and_grows_with_the_table():
-    one = pp.pp_paged_attention_scratch_bytes(cache(table_ld=400), 4, 1, 0)
-    assert pp.pp_paged_attention_scratch_bytes(cache(table_ld=4000), 4, 1, 0) > one
-    assert pp.pp_paged_attention_scratch_bytes(cache(table_ld=400), 4, 1, 200) < one
+def test_scratch_grows_with_the_table():
+    one = pp.pp_paged_attention_scratch_bytes(cache(table_ld=400), 4, 9, 1, 0)
+    assert pp.pp_paged_attention_scratch_bytes(cache(table_ld=4000), 4, 9, 1, 0) > one
+    assert pp.pp_paged_attention_scratch_bytes(cache(table_ld=400), 4, 9, 1, 200) < one
     for bad in [dict(n_heads=5), dict(n_heads=0), dict(max_q=0), dict(window=-1)]:
         a = dict(n_heads=4, max_q=1, window=0)
         a.update(bad)
         with pytest.raises(pp.PPError):
-            pp.pp_paged_attention_scratch_bytes(cache(), a["n_heads"], a["max_q"], a["window"])
+            pp.pp_paged_attention_scratch_bytes(cache(), a["n_heads"], 9, a["max_q"],
+                                                a["window"])
 
 
 @pytest.mark.parametrize("bad", [
