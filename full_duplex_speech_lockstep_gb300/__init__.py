@@ -591,57 +591,74 @@ class PagedKV:
             raise ValueError("k and v must be [pages, heads, rows, dims] of one layout and type")
         if k.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("the cache holds bf16 or fp16, not %s" % k.dtype)
+        if not k.is_cuda or v.device != k.device:
+            raise ValueError("k and v must be on one CUDA device")
         n_pages, heads, rows, dim = k.shape
-        if k.stride()[1:] != (rows * dim, dim, 1):
+        if n_pages and not k[0].is_contiguous():
             raise ValueError("each page of k and v must be contiguous")
-        self.device = k.device
+        if table.dim() != 2:
+            raise ValueError("table must be [sequences, width]")
+        self.device, self.index, self.dtype = k.device, k.get_device(), k.dtype
         self.k, self.v, self.table, self.mass = k, v, table, mass
-        self._fits("v", v, v.dtype)
-        self._fits("table", table, torch.int32, (None, None))
+        self.heads, self.dim, self.n = heads, dim, table.shape[0]
+        self._fits("table", table, torch.int32, table.shape)
+        self.mass_shape = (n_pages, heads, rows)
         if mass is not None:
-            self._fits("mass", mass, torch.float32, (n_pages, heads, rows))
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device) if status is None \
-            else self._fits("status", status, torch.int32)
-        self.heads, self.dim = heads, dim
+            self._fits("mass", mass, torch.float32, self.mass_shape)
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._fits("status", status, torch.int32, (1,))
+        self.status = status
+        # stands in for a scratch that a call asks for but does not use (the smallest size)
+        self.unused = torch.empty(256, dtype=torch.uint8, device=self.device)
         stride = k.stride(0) if n_pages > 1 else heads * rows * dim
         self.c = pp_paged_kv(k.data_ptr(), v.data_ptr(), self._ptr(mass), table.data_ptr(),
                              stride, n_pages, rows, heads, dim, self.types[k.dtype],
                              table.shape[0], table.shape[1])
+        # the current stream's handle without building a stream object, where torch offers it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
 
     @staticmethod
     def _ptr(t):
         return None if t is None else t.data_ptr()
 
-    def _fits(self, name, t, dtype, shape=None):
-        """t, if it is a tensor of this device, type and shape (None: any extent), contiguous
-        when a shape is asked for."""
-        if not t.is_cuda or t.device != self.device:
-            raise ValueError("%s must be on %s, not %s" % (name, self.device, t.device))
-        if t.dtype != dtype:
-            raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
-        if shape is not None and (t.dim() != len(shape) or not t.is_contiguous() or any(
-                n is not None and n != m for n, m in zip(shape, t.shape))):
-            raise ValueError("%s: shape %s, expected contiguous %s" % (name, tuple(t.shape), shape))
+    def _fits(self, name, t, dtype, shape):
+        """Raise unless t is a contiguous tensor of this cache's device, of this type and shape."""
+        if (t.get_device() != self.index or t.dtype is not dtype or t.shape != shape
+                or not t.is_contiguous()):
+            raise ValueError("%s: %s %s on %s, expected contiguous %s %s on %s" % (
+                name, t.dtype, tuple(t.shape), t.device, dtype, tuple(shape), self.device))
         return t
 
-    def _rows(self, name, t, dtype, T=None, heads=None):
-        """Row stride of a [rows, heads, dims] tensor whose rows are contiguous."""
-        self._fits(name, t, dtype)
-        if t.dim() != 3 or t.shape[2] != self.dim or (T is not None and t.shape[0] != T) or (
-                heads is not None and t.shape[1] != heads):
-            raise ValueError("%s: shape %s, expected (%s, %s, %d)" % (
-                name, tuple(t.shape), T or "rows", heads or "heads", self.dim))
-        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.dim)):
-            raise ValueError("%s: the heads of a row must be contiguous" % name)
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * self.dim
+    def _rows(self, name, t, dtype):
+        """(rows, heads, row stride) of a [rows, heads, dims] tensor whose rows are contiguous."""
+        if t.get_device() != self.index or t.dtype is not dtype or t.dim() != 3:
+            raise ValueError("%s: %s %s on %s, expected [rows, heads, %d] in %s on %s" % (
+                name, t.dtype, tuple(t.shape), t.device, self.dim, dtype, self.device))
+        T, H, D = t.shape
+        row, head, one = t.stride()
+        if D != self.dim or (T and H and (one != 1 or (H > 1 and head != D))):
+            raise ValueError("%s: shape %s, strides %s: the heads of a row must be contiguous, of "
+                             "%d values" % (name, tuple(t.shape), t.stride(), self.dim))
+        return T, H, row if T > 1 else H * D
 
     def _batch(self, cu, kv_len):
-        n = self.table.shape[0]
-        self._fits("cu", cu, self.torch.int32, (n + 1,))
-        self._fits("kv_len", kv_len, self.torch.int32, (n,))
+        self._fits("cu", cu, self.torch.int32, (self.n + 1,))
+        self._fits("kv_len", kv_len, self.torch.int32, (self.n,))
 
-    def _stream(self):
-        return self.torch.cuda.current_stream(self.device).cuda_stream
+    def _call(self, fn, *args):
+        """One library call on the cache's device and that device's current stream."""
+        torch = self.torch
+        if torch.cuda.current_device() == self.index:
+            return fn(*args, self.raw_stream(self.index))
+        with torch.cuda.device(self.index):
+            return fn(*args, self.raw_stream(self.index))
+
+    @staticmethod
+    def _longest(max_q, T):
+        # the library's hint is at least 1; more than all rows no chunk can be
+        return max(1, T if max_q is None else min(max_q, T))
 
     def read_status(self):
         """Wait for the current stream, then read and clear the status word."""
@@ -653,29 +670,29 @@ class PagedKV:
                rope_base=10000.0, rot_dim=None, halves=False, out=None):
         """New queries normed and rotated ([rows, heads, dims], returned in the cache's type);
         new keys, the same way, and values become cache entries."""
-        torch, f32 = self.torch, self.torch.float32
-        if q.dtype not in self.types:
-            raise ValueError("q must be f32 or the cache's type, not %s" % q.dtype)
-        qs = self._rows("q", q, q.dtype)
-        T, H = q.shape[:2]
-        ks = self._rows("k", k, q.dtype, T, self.heads)
-        vs = self._rows("v", v, q.dtype, T, self.heads)
+        torch, dtype = self.torch, q.dtype
+        if dtype not in self.types:
+            raise ValueError("q must be f32 or the cache's type, not %s" % dtype)
+        T, H, qs = self._rows("q", q, dtype)
+        kT, kH, ks = self._rows("k", k, dtype)
+        vT, vH, vs = self._rows("v", v, dtype)
+        if kT != T or vT != T or kH != self.heads or vH != self.heads:
+            raise ValueError("k and v must have %d rows of %d heads" % (T, self.heads))
         self._batch(cu, kv_len)
-        for name, t in (("q_alpha", q_alpha), ("k_alpha", k_alpha)):
-            if t is not None:
-                self._fits(name, t, f32, (self.dim,))
+        if q_alpha is not None:
+            self._fits("q_alpha", q_alpha, torch.float32, (self.dim,))
+        if k_alpha is not None:
+            self._fits("k_alpha", k_alpha, torch.float32, (self.dim,))
         if positions is not None:
             self._fits("positions", positions, torch.int32, (T,))
         if out is None:
-            out = torch.empty((T, H, self.dim), dtype=self.k.dtype, device=self.device)
+            out = torch.empty((T, H, self.dim), dtype=self.dtype, device=self.device)
         else:
-            self._fits("out", out, self.k.dtype, (T, H, self.dim))
-        with torch.cuda.device(self.device):
-            pp_paged_append(self.c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                            self.types[q.dtype], self._ptr(q_alpha), self._ptr(k_alpha), eps,
-                            rope_base, self.dim if rot_dim is None else rot_dim, int(halves),
-                            self._ptr(positions), cu.data_ptr(), kv_len.data_ptr(), T, H,
-                            out.data_ptr(), self.status.data_ptr(), self._stream())
+            self._fits("out", out, self.dtype, (T, H, self.dim))
+        self._call(pp_paged_append, self.c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                   self.types[dtype], self._ptr(q_alpha), self._ptr(k_alpha), eps, rope_base,
+                   self.dim if rot_dim is None else rot_dim, int(halves), self._ptr(positions),
+                   cu.data_ptr(), kv_len.data_ptr(), T, H, out.data_ptr(), self.status.data_ptr())
         return out
 
     def attention(self, q, cu, kv_len, max_q=None, scale=None, window=0, with_lse=False,
@@ -683,45 +700,41 @@ class PagedKV:
         """Attention of the new rows over the cache: out, or (out, lse) on request.  max_q is
         the longest chunk as far as the host knows (default: all rows)."""
         torch = self.torch
-        qs = self._rows("q", q, self.k.dtype)
-        T, H = q.shape[:2]
+        T, H, qs = self._rows("q", q, self.dtype)
         self._batch(cu, kv_len)
         if out is None:
-            out = torch.empty((T, H, self.dim), dtype=q.dtype, device=self.device)
+            out = torch.empty((T, H, self.dim), dtype=self.dtype, device=self.device)
         else:
-            self._fits("out", out, q.dtype, (T, H, self.dim))
+            self._fits("out", out, self.dtype, (T, H, self.dim))
         lse = torch.empty((T, H), dtype=torch.float32, device=self.device) if with_lse else None
-        max_q = max(1, T if max_q is None else min(max_q, T) if max_q > 0 else max_q)
+        max_q = self._longest(max_q, T)
         nbytes = pp_paged_attention_scratch_bytes(self.c, H, T, max_q, window)
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        with torch.cuda.device(self.device):
-            pp_paged_attention(self.c, q.data_ptr(), qs, cu.data_ptr(), kv_len.data_ptr(), T,
-                               max_q, H, self.dim ** -0.5 if scale is None else scale, window,
-                               out.data_ptr(), self._ptr(lse), self.status.data_ptr(),
-                               scratch.data_ptr(), nbytes, self._stream())
+        scratch = self.unused if nbytes <= 256 else \
+            torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self._call(pp_paged_attention, self.c, q.data_ptr(), qs, cu.data_ptr(), kv_len.data_ptr(),
+                   T, max_q, H, self.dim ** -0.5 if scale is None else scale, window,
+                   out.data_ptr(), self._ptr(lse), self.status.data_ptr(), scratch.data_ptr(),
+                   nbytes)
         return (out, lse) if with_lse else out
 
     def attention_mass(self, q, lse, cu, kv_len, max_q=None, scale=None, window=0, decay=1.0,
                        mass=None):
         """Add the attention weight of the new rows to the cache's mass (or to ``mass``, of the
         same layout)."""
-        torch = self.torch
-        qs = self._rows("q", q, self.k.dtype)
-        T, H = q.shape[:2]
-        self._fits("lse", lse, torch.float32, (T, H))
+        T, H, qs = self._rows("q", q, self.dtype)
+        self._fits("lse", lse, self.torch.float32, (T, H))
         self._batch(cu, kv_len)
         c = self.c
         if mass is not None:
-            self._fits("mass", mass, torch.float32, tuple(self.k.shape[:3]))
-            c = pp_paged_kv.from_buffer_copy(self.c)
+            self._fits("mass", mass, self.torch.float32, self.mass_shape)
+            c = pp_paged_kv.from_buffer_copy(c)
             c.mass = mass.data_ptr()
         elif self.mass is None:
             raise ValueError("this cache keeps no mass")
-        max_q = max(1, T if max_q is None else min(max_q, T) if max_q > 0 else max_q)
-        with torch.cuda.device(self.device):
-            pp_paged_mass(c, q.data_ptr(), qs, lse.data_ptr(), cu.data_ptr(), kv_len.data_ptr(), T,
-                          max_q, H, self.dim ** -0.5 if scale is None else scale, window, decay,
-                          self.status.data_ptr(), self._stream())
+        self._call(pp_paged_mass, c, q.data_ptr(), qs, lse.data_ptr(), cu.data_ptr(),
+                   kv_len.data_ptr(), T, self._longest(max_q, T), H,
+                   self.dim ** -0.5 if scale is None else scale, window, decay,
+                   self.status.data_ptr())
 
     def evict(self, kv_len, budget, recent, to):
         """Keep the newest `recent` and the heaviest other entries, `budget` in all, in the
@@ -729,13 +742,12 @@ class PagedKV:
         torch = self.torch
         if self.mass is None:
             raise ValueError("this cache keeps no mass")
-        if to.device != self.device:
+        if to.index != self.index:
             raise ValueError("both caches must be on one device")
-        n = self.table.shape[0]
-        self._fits("kv_len", kv_len, torch.int32, (n,))
-        to_len = torch.empty(n, dtype=torch.int32, device=self.device)
-        kept = torch.empty((n, self.heads, max(budget, 0)), dtype=torch.int32, device=self.device)
-        with torch.cuda.device(self.device):
-            pp_paged_evict(self.c, kv_len.data_ptr(), budget, recent, to.c, to_len.data_ptr(),
-                           kept.data_ptr(), self.status.data_ptr(), self._stream())
+        self._fits("kv_len", kv_len, torch.int32, (self.n,))
+        to_len = torch.empty(self.n, dtype=torch.int32, device=self.device)
+        kept = torch.empty((self.n, self.heads, max(budget, 0)), dtype=torch.int32,
+                           device=self.device)
+        self._call(pp_paged_evict, self.c, kv_len.data_ptr(), budget, recent, to.c,
+                   to_len.data_ptr(), kept.data_ptr(), self.status.data_ptr())
         return to_len, kept

@@ -154,23 +154,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
-__device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
-
 // Zeroes the non-finite halves of w; true if there were any.
 template <typename N>
 __device__ __forceinline__ bool finite_only(uint32_t& w) {
@@ -359,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x - 128 - t * 128;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lane_base + t * kTile, o_at = lane_base + 2 * kTile + t * D;
-    const uint64_t c2 = pair(a.c, a.c);
+    const uint64_t c2 = f32x2(a.c, a.c);
     uint32_t ns_ = 0, no = 0, nl = 0, ne = 0, nu = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++nu) {
       const Unit x = unit_of(a, pre, u, tp, ns_cap);
@@ -456,14 +439,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          const uint64_t r2 = pair(-ref, -ref);
-          uint64_t sum2 = pair(l, 0.f);
+          const uint64_t r2 = f32x2(-ref, -ref);
+          uint64_t sum2 = f32x2(l, 0.f);
           uint32_t p[kTile / 2];
 #pragma unroll
           for (int i = 0; i < kTile; i += 2) {
             const uint64_t z = fma2((uint64_t)s[i] | ((uint64_t)s[i + 1] << 32), c2, r2);
             const float p0 = exp2_approx(lo_of(z)), p1 = exp2_approx(hi_of(z));
-            sum2 = add2(sum2, pair(p0, p1));
+            sum2 = add2(sum2, f32x2(p0, p1));
             p[i >> 1] = N::pack(p0, p1);
           }
           l = lo_of(sum2) + hi_of(sum2);

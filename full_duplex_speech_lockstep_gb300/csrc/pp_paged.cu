@@ -220,15 +220,15 @@ int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const 
   if (T > 0 && (!q || !lse || q_stride < n_heads * D || (q_stride & 7) ||
                 q_stride >= (int64_t)1 << 38 || !aligned(q, 16) || !aligned(lse, 4)))
     return PP_EINVAL;
-  const RowTile r = row_tile(a.G, max_q);
+  const int tp = mass_tokens(a.G, max_q);
   Maps maps;
   // without a row the query map is never used: any valid one will do
   Args qa = a;
   if (T == 0) qa.T = 1;
   if (!page_map(&maps.k, kv, kv->k) ||
-      !query_map(&maps.q, qa, kv->type, T ? q : kv->k, T ? q_stride : n_heads * D, r.tp))
+      !query_map(&maps.q, qa, kv->type, T ? q : kv->k, T ? q_stride : n_heads * D, tp))
     return PP_EINVAL;
-  return rc(launch_paged_mass(a, kv->type, r, maps, lse, kv->mass, decay, (cudaStream_t)stream));
+  return rc(launch_paged_mass(a, kv->type, maps, lse, kv->mass, decay, tp, (cudaStream_t)stream));
 }
 
 int pp_paged_evict(const pp_paged_kv* kv, const int32_t* kv_len, int budget, int recent,

@@ -207,6 +207,23 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+
 // Split partials of one row joined by one warp, in split order: rec is the row's first record
 // and ns <= 128 their count.
 template <typename T, int D>
@@ -328,8 +345,10 @@ cudaError_t launch_paged_attn(const Args& a, int type, const AttnPlan& plan, con
                               const AttnOut& o, cudaStream_t s);
 cudaError_t launch_paged_attn_tc(const Args& a, int type, const LongPlan& plan, const Maps& maps,
                                  const AttnOut& o, const void* v_pages, cudaStream_t s);
-cudaError_t launch_paged_mass(const Args& a, int type, const RowTile& r, const Maps& maps,
-                              const float* lse, float* mass, float decay, cudaStream_t s);
+// Tokens of one step of rows (k_paged_mass.cu).
+int mass_tokens(int G, int max_q);
+cudaError_t launch_paged_mass(const Args& a, int type, const Maps& maps, const float* lse,
+                              float* mass, float decay, int tp, cudaStream_t s);
 
 struct AppendArgs {
   const void *q, *k, *v;
