@@ -152,13 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   prefix_units(pre, a.n_seqs, [&](int b) { return seq_units<WR>(a, b, tp); });
   const int units = pre[a.n_seqs];
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (*abort_flag) return;
-    if (!mbar_wait(smem_u32(bar), parity)) {
-      *abort_flag = 1;
-      raise(a, PP_S_TIMEOUT);
-    }
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
 
   if (warp == kWarps) {
     // ---- producer -------------------------------------------------------------------------

@@ -213,13 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = ctl->tmem;
   const int units = pre[a.n_seqs];
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (*abort_flag) return;
-    if (!mbar_wait(smem_u32(bar), parity)) {
-      *abort_flag = 1;
-      raise(a, PP_S_TIMEOUT);
-    }
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));

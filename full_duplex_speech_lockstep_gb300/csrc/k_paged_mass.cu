@@ -6,14 +6,18 @@
 // 128 rows:
 //   S' = K Q^T   M = 128 keys, N = the step's rows, on the 5th-generation tensor cores
 // so that a thread owns a key (a tensor-memory lane) and adds up its weights in row order:
-// no sum crosses threads but one (two groups take alternate columns), nothing is added
+// no sum crosses threads but one (two groups take alternate steps), nothing is added
 // atomically, and the bits are the same in every run.
 //
+// A CTA takes a run of consecutive units of about the same number of steps as the others,
+// and each of its roles walks the run by itself:
 //   warp 0        producer: the key tile, then the steps' rows, by TMA
 //   warp 1        one thread issues the MMAs, up to four steps ahead of the sums
-//   warps 2-3     what the sums need from memory, ahead of them: each row's lse (with the
-//                 rows that do not count set to infinity), each key's old mass and page
-//   warps 4-7, 8-11   the sums: columns 0-15, 32-47, ... and 16-31, 48-63, ...
+//   warp 2        each key's old mass and page, four units at a time (their loads overlap)
+//   warp 3        each row's lse, four steps at a time; rows that do not count: infinity
+//   warps 4-7, 8-11   the sums, the two groups in turn to a step
+#include <type_traits>
+
 #include "pp_paged.cuh"
 #include "pp_tcgen05.cuh"
 
@@ -34,37 +38,75 @@ struct Ctl {
   uint64_t done;
   uint32_t tmem;
   int abort;
-  float ref[kAux][kTile];            // lse * log2(e) of a step's rows
-  float old[kAux][kTile];            // decayed mass of a unit's keys
+  alignas(16) float ref[kAux][kTile];   // lse * log2(e) of a step's rows
+  alignas(16) float old[kAux][kTile];   // decayed mass of a unit's keys
   int page[kAux][8];                 // pages of its 16-key groups, -1 for none
-  float half[2][kTile];              // the second group's sums
+  float half[2][kTile];              // sums from one group to the other
 };
 
-struct Unit {
-  int b, h, j0;
-  int row0, n, len;
-  int t0, t1;        // tokens that see some key of the tile
-};
-
-__device__ __forceinline__ Unit unit_of(const Args& a, const int* pre, int u) {
-  Unit x;
-  x.b = find_seq(pre, a.n_seqs, u);
-  const Seq s = seq_of(a, x.b);
-  u -= pre[x.b];
-  const int tiles = (s.len + kTile - 1) / kTile;
-  x.h = u / tiles;
-  x.j0 = (u - x.h * tiles) * kTile;
-  x.row0 = s.row0;
-  x.n = s.n;
-  x.len = s.len;
-  const int first = s.len - s.n;
-  x.t0 = max(0, x.j0 - first);
-  x.t1 = s.n;
-  if (a.window)
-    x.t1 = (int)min((int64_t)s.n, (int64_t)min(x.j0 + kTile, s.len) - 1 + a.window - first);
-  if (x.t1 < x.t0) x.t1 = x.t0;
-  return x;
+// Steps of rows of a unit, at most: what it costs.
+__device__ __forceinline__ int unit_cost(const Seq& s, int tp) {
+  return max(1, (s.n + tp - 1) / tp);
 }
+
+// A walk over this CTA's units, in order.
+struct Walk {
+  const Args& a;
+  const int64_t* pre;
+  const int tp;
+  int64_t at, end;      // cost before this unit, cost where the run ends
+  int b, h, tile;
+  int tiles, cost;      // of the sequence
+  Seq s;
+  int j0, t0, t1;       // the unit's first key; the tokens that see some key of it
+
+  __device__ __forceinline__ Walk(const Args& a_, const int64_t* pre_, int tp_)
+      : a(a_), pre(pre_), tp(tp_) {
+    const int64_t total = pre[a.n_seqs];
+    at = total * blockIdx.x / gridDim.x;
+    end = total * (blockIdx.x + 1) / gridDim.x;
+    if (at >= end) return;
+    b = find_seq(pre, a.n_seqs, at);
+    sequence();
+    const int64_t i = (at - pre[b] + cost - 1) / cost;   // the first unit that starts in the run
+    h = (int)(i / tiles);
+    tile = (int)(i - (int64_t)h * tiles);
+    at = pre[b] + i * cost;
+    if (h == a.Hk) next_sequence();
+    unit();
+  }
+  __device__ __forceinline__ bool done() const { return at >= end; }
+  __device__ __forceinline__ void sequence() {
+    s = seq_of(a, b);
+    tiles = (s.len + kTile - 1) / kTile;
+    cost = unit_cost(s, tp);
+  }
+  __device__ __forceinline__ void next_sequence() {
+    h = tile = 0;
+    do {
+      ++b;
+    } while (b < a.n_seqs && pre[b + 1] == pre[b]);
+    if (b < a.n_seqs) sequence();
+  }
+  __device__ __forceinline__ void next() {
+    at += cost;
+    if (++tile == tiles) {
+      tile = 0;
+      if (++h == a.Hk) next_sequence();
+    }
+    unit();
+  }
+  __device__ __forceinline__ void unit() {
+    if (done()) return;
+    j0 = tile * kTile;
+    const int first = s.len - s.n;
+    t0 = max(0, j0 - first);
+    t1 = s.n;
+    if (a.window)
+      t1 = (int)min((int64_t)s.n, (int64_t)min(j0 + kTile, s.len) - 1 + a.window - first);
+    if (t1 < t0) t1 = t0;
+  }
+};
 
 // 16 columns of this thread's tensor-memory lane
 __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t r[16]) {
@@ -75,6 +117,42 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t r[16]) {
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(t));
+}
+
+// Sum of 2^(s c - ref) over the columns [0, cols) of a lane, those outside [lo, hi) left out
+// (`masked`).  Columns from cols to the next multiple of 16 have an infinite ref.
+template <typename M>
+__device__ __forceinline__ float weigh(uint32_t at, const float* ref, uint64_t c2, int cols, int lo,
+                                       int hi, M) {
+  uint64_t part[2] = {0, 0};   // two sums of two
+  for (int c0 = 0; c0 < cols; c0 += 16) {
+    uint32_t s[16];
+    tmem_ld16(at + c0, s);
+    float4 z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = reinterpret_cast<const float4*>(ref + c0)[i];
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(after_wait(s[i]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t e0 = fma2((uint64_t)s[4 * i] | ((uint64_t)s[4 * i + 1] << 32), c2,
+                               f32x2(-z[i].x, -z[i].y));
+      const uint64_t e1 = fma2((uint64_t)s[4 * i + 2] | ((uint64_t)s[4 * i + 3] << 32), c2,
+                               f32x2(-z[i].z, -z[i].w));
+      float p[4] = {exp2_approx(lo_of(e0)), exp2_approx(hi_of(e0)), exp2_approx(lo_of(e1)),
+                    exp2_approx(hi_of(e1))};
+      if constexpr (M::value) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (c0 + 4 * i + k < lo || c0 + 4 * i + k >= hi) p[k] = 0.f;
+      }
+      part[0] = add2(part[0], f32x2(p[0], p[1]));
+      part[1] = add2(part[1], f32x2(p[2], p[3]));
+    }
+  }
+  const uint64_t both = add2(part[0], part[1]);
+  return lo_of(both) + hi_of(both);
 }
 
 template <typename T, int D>
@@ -89,10 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int q_bytes = N_ * D * 2;                       // a stage of rows
   uint8_t* q_smem = smem + KS * kTileBytes;
   Ctl* ctl = reinterpret_cast<Ctl*>(q_smem + kQStages * q_bytes);
-  int* pre = reinterpret_cast<int*>(ctl + 1);
+  int64_t* pre = reinterpret_cast<int64_t*>(ctl + 1);
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = N_ > 16 ? 2 : 1;                   // groups that sum
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) {
       mbar_init(smem_u32(&ctl->kfull[i]), 1);
@@ -104,12 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(smem_u32(&ctl->sfull[i]), 1);
-      mbar_init(smem_u32(&ctl->sfree[i]), 4 * groups);
+      mbar_init(smem_u32(&ctl->sfree[i]), 4);
     }
     for (int i = 0; i < kAux; ++i) {
-      mbar_init(smem_u32(&ctl->lfull[i]), 2);
-      mbar_init(smem_u32(&ctl->lempty[i]), 4 * groups);
-      mbar_init(smem_u32(&ctl->ufull[i]), 2);
+      mbar_init(smem_u32(&ctl->lfull[i]), 1);
+      mbar_init(smem_u32(&ctl->lempty[i]), 4);
+      mbar_init(smem_u32(&ctl->ufull[i]), 1);
       mbar_init(smem_u32(&ctl->uempty[i]), 4);
     }
     mbar_init(smem_u32(&ctl->done), 1);
@@ -125,31 +202,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   pdl_wait_and_trigger();
   pdl_trigger();
-  prefix_units(pre, a.n_seqs, [&](int b) { return a.Hk * ((seq_len(a, b) + kTile - 1) / kTile); });
+  // (a sequence without new rows only decays, and not even that at 1)
+  prefix_units(pre, a.n_seqs, [&](int b) -> int64_t {
+    const Seq s = seq_of(a, b);
+    if (s.n == 0 && decay == 1.f) return 0;
+    return (int64_t)a.Hk * ((s.len + kTile - 1) / kTile) * unit_cost(s, tp);
+  });
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = ctl->tmem;
-  const int units = pre[a.n_seqs];
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (*abort_flag) return;
-    if (!mbar_wait(smem_u32(bar), parity)) {
-      *abort_flag = 1;
-      raise(a, PP_S_TIMEOUT);
-    }
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
   // A unit that no row sees has nothing to add; without decay it is left out.
-  auto skip = [&](const Unit& x) { return x.t0 == x.t1 && decay == 1.f; };
+  auto skip = [&](const Walk& x) { return x.t0 == x.t1 && decay == 1.f; };
 
   if (warp == 0) {
     // ---- producer -------------------------------------------------------------------------
     uint32_t nk = 0, nq = 0, seen_bad = 0;
-    for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
-      const Unit x = unit_of(a, pre, u);
+    for (Walk x(a, pre, tp); !x.done() && !*abort_flag; x.next()) {
       if (x.t0 == x.t1) continue;
       const int ks = nk % KS;
       if (nk >= KS) wait(&ctl->kempty[ks], (nk / KS - 1) & 1);
       if (*abort_flag) break;
       seen_bad |= load_key_tile(a, &mapK, smem_u32(smem + ks * kTileBytes),
-                                smem_u32(&ctl->kfull[ks]), x.b, x.h, x.j0, x.len, lane, nullptr);
+                                smem_u32(&ctl->kfull[ks]), x.b, x.h, x.j0, x.s.len, lane, nullptr);
       ++nk;
       for (int t = x.t0; t < x.t1; t += tp) {
         const int qs = nq % kQStages;
@@ -160,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_expect_tx(bar, (uint32_t)(tp * a.G * D * 2));
           for (int bx = 0; bx < D / 64; ++bx)
             tma_load_4d(smem_u32(q_smem + qs * q_bytes + bx * N_ * 128), &mapQ, bx * 64, x.h * a.G,
-                        x.row0 + t, 0, bar);
+                        x.s.row0 + t, 0, bar);
         }
         ++nq;
       }
@@ -179,8 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id = (1u << 4) | Num<T>::kMmaTypes | ((uint32_t)(kTile >> 4) << 24) |
                           ((uint32_t)(N_ >> 3) << 17);
       uint32_t nk = 0, nq = 0;
-      for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
-        const Unit x = unit_of(a, pre, u);
+      for (Walk x(a, pre, tp); !x.done() && !*abort_flag; x.next()) {
         if (x.t0 == x.t1) continue;
         const int ks = nk % KS;
         wait(&ctl->kfull[ks], (nk / KS) & 1);
@@ -209,72 +282,108 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(smem_u32(&ctl->done), 0);
     }
     __syncwarp();
-  } else if (warp < 4) {
-    // ---- memory warps: two values to a thread ---------------------------------------------
-    const int i = threadIdx.x - 64;
-    const int H = a.Hk * a.G;
-    uint32_t nl = 0, nu = 0;
-    for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
-      const Unit x = unit_of(a, pre, u);
-      if (skip(x)) continue;
-      const int us = nu % kAux;
-      if (nu >= kAux) wait(&ctl->uempty[us], (nu / kAux - 1) & 1);
-      if (*abort_flag) break;
-      if (i < 8) {
-        const int j = x.j0 + i * 16;
-        ctl->page[us][i] = j < x.len ? page_of(a, x.b, j) : -1;
+  } else if (warp == 2) {
+    // ---- old mass and pages: four keys to a lane, four units at a time
+    uint32_t nu = 0;
+    for (Walk x(a, pre, tp); !x.done() && !*abort_flag;) {
+      float old[4][4];
+      int page[4], n = 0;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        while (!x.done() && skip(x)) x.next();
+        if (!x.done()) {
+          const int j = x.j0 + lane * 4;               // one page: 4 divides the page size
+          const int p = j < x.s.len ? page_of(a, x.b, j) : -1;
+          page[y] = p;
+          const float* src =
+              mass + ((((int64_t)p * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1)));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            old[y][k] = p >= 0 && j + k < x.s.len && decay != 0.f ? src[k] * decay : 0.f;
+          n = y + 1;
+          x.next();
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int j = x.j0 + i + k * 64;
-        float old = 0.f;
-        if (decay != 0.f && j < x.len) {
-          const int p = page_of(a, x.b, j);
-          if (p >= 0)
-            old = decay *
-                  mass[(((int64_t)p * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1))];
-        }
-        ctl->old[us][i + k * 64] = old;
+      for (int y = 0; y < 4; ++y) {
+        if (y >= n) break;
+        const int us = nu % kAux;
+        if (nu >= kAux) wait(&ctl->uempty[us], (nu / kAux - 1) & 1);
+        if (*abort_flag) break;
+        *reinterpret_cast<float4*>(&ctl->old[us][lane * 4]) =
+            make_float4(old[y][0], old[y][1], old[y][2], old[y][3]);
+        if ((lane & 3) == 0) ctl->page[us][lane >> 2] = page[y];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->ufull[us]));
+        ++nu;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->ufull[us]));
-      ++nu;
-      for (int t = x.t0; t < x.t1; t += tp) {
+    }
+  } else if (warp == 3) {
+    // ---- lse: four rows to a lane, four steps at a time
+    const int H = a.Hk * a.G;
+    int tk[4], gh[4];                                   // a lane's rows: token and head of a step
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      tk[k] = (lane + k * 32) / a.G;
+      gh[k] = lane + k * 32 - tk[k] * a.G;
+    }
+    uint32_t nl = 0;
+    Walk x(a, pre, tp);
+    int t = x.done() ? 0 : x.t0;
+    while (!x.done() && !*abort_flag) {
+      float z[4][4];
+      int n = 0;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        while (!x.done() && t >= x.t1) {
+          x.next();
+          if (!x.done()) t = x.t0;
+        }
+        if (!x.done()) {
+          const int nt = min(tp, x.t1 - t);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // rows that are not there, or that saw nothing, give nothing
+            float v = -INFINITY;
+            if (tk[k] < nt) v = lse[(int64_t)(x.s.row0 + t + tk[k]) * H + x.h * a.G + gh[k]];
+            z[y][k] = v == -INFINITY ? INFINITY : v * kLog2e;
+          }
+          n = y + 1;
+          t += tp;
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if (y >= n) break;
         const int ls = nl % kAux;
-        const int rows = min(tp, x.t1 - t) * a.G;
         if (nl >= kAux) wait(&ctl->lempty[ls], (nl / kAux - 1) & 1);
         if (*abort_flag) break;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = i + k * 64, tk = r / a.G;
-          // rows that are not there, or that saw nothing, give nothing
-          float z = r < rows
-                        ? lse[(int64_t)(x.row0 + t + tk) * H + x.h * a.G + (r - tk * a.G)] * kLog2e
-                        : INFINITY;
-          ctl->ref[ls][r] = z == -INFINITY ? INFINITY : z;
-        }
+        for (int k = 0; k < 4; ++k) ctl->ref[ls][lane + k * 32] = z[y][k];
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->lfull[ls]));
         ++nl;
       }
     }
-  } else if (warp < 4 + 4 * groups) {
-    // ---- sums: a thread to a key --------------------------------------------------------------
+  } else {
+    // ---- sums: a thread to a key, the two groups in turn to a step --------------------------
     const int g = (warp - 4) >> 2, key = threadIdx.x - 128 - g * 128;
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint64_t c2 = f32x2(a.c, a.c);
-    uint32_t nl = 0, nu = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const Unit x = unit_of(a, pre, u);
+    uint32_t nl = 0, nu = 0, nm = 0;
+    for (Walk x(a, pre, tp); !x.done(); x.next()) {
       if (skip(x)) continue;
-      const int first = x.len - x.n, j = x.j0 + key;
+      const int first = x.s.len - x.s.n, j = x.j0 + key;
+      const int steps = (x.t1 - x.t0 + tp - 1) / tp;
       float sum = 0.f;
-      for (int t = x.t0; t < x.t1; t += tp) {
+      int t = x.t0;
+      for (int i = 0; i < steps; ++i, ++nl, t += tp) {
+        if ((nl & 1) != g) continue;
         const int bb = nl % kBufs, ls = nl % kAux;
-        const int nt = min(tp, x.t1 - t);
+        const int nt = min(tp, x.t1 - t), cols = nt * a.G;
         // the rows of the step that see this key: columns [lo, hi)
-        int lo = 0, hi = nt * a.G;
-        const bool edge = hi < N_ || x.j0 + kTile - 1 > first + t ||
+        int lo = 0, hi = cols;
+        const bool edge = (cols & 15) || x.j0 + kTile - 1 > first + t ||
                           (a.window && x.j0 <= first + t + nt - 1 - a.window);
         if (edge) {
           lo = max(0, j - first - t) * a.G;
@@ -283,50 +392,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&ctl->lfull[ls], (nl / kAux) & 1);
         wait(&ctl->sfull[bb], (nl / kBufs) & 1);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int c0 = g * 16; c0 < N_; c0 += 16 * groups) {
-          uint32_t s[16];
-          tmem_ld16(at + bb * kTile + c0, s);
-          tmem_wait_ld();
-          const float4* rp = reinterpret_cast<const float4*>(&ctl->ref[ls][c0]);
-          uint64_t part = 0;   // (0, 0)
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 z = rp[i / 4];
-            const uint64_t e0 = fma2(f32x2(after_wait(s[i]), after_wait(s[i + 1])), c2,
-                                     f32x2(-z.x, -z.y));
-            const uint64_t e1 = fma2(f32x2(after_wait(s[i + 2]), after_wait(s[i + 3])), c2,
-                                     f32x2(-z.z, -z.w));
-            float p[4] = {exp2_approx(lo_of(e0)), exp2_approx(hi_of(e0)), exp2_approx(lo_of(e1)),
-                          exp2_approx(hi_of(e1))};
-            if (edge) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (c0 + i + k < lo || c0 + i + k >= hi) p[k] = 0.f;
-            }
-            part = add2(part, add2(f32x2(p[0], p[1]), f32x2(p[2], p[3])));
-          }
-          sum += lo_of(part) + hi_of(part);
-        }
+        if (edge)
+          sum += weigh(at + bb * kTile, ctl->ref[ls], c2, cols, lo, hi, std::true_type());
+        else
+          sum += weigh(at + bb * kTile, ctl->ref[ls], c2, cols, lo, hi, std::false_type());
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&ctl->sfree[bb]));
           mbar_arrive(smem_u32(&ctl->lempty[ls]));
         }
-        ++nl;
       }
-      if (groups == 2) {
-        // the second group's sums come through shared memory, two units deep
-        if (g == 1) ctl->half[nu & 1][key] = sum;
+      // the group of the unit's last step writes; the other one's sum comes through shared
+      // memory, two units deep
+      const int writer = steps > 0 ? (nl - 1) & 1 : nu & 1;
+      if (steps > 1) {
+        if (g != writer) ctl->half[nm & 1][key] = sum;
         named_sync(1, 256);
-        if (g == 0) sum += ctl->half[nu & 1][key];
+        if (g == writer) sum += ctl->half[nm & 1][key];
+        ++nm;
       }
-      if (g == 0) {
+      if (g == writer) {
         const int us = nu % kAux;
         wait(&ctl->ufull[us], (nu / kAux) & 1);
         const int p = ctl->page[us][key >> 4];
         sum += ctl->old[us][key];
-        if (p >= 0 && j < x.len)
+        if (p >= 0 && j < x.s.len)
           mass[(((int64_t)p * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1))] = sum;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
@@ -348,7 +439,7 @@ cudaError_t run(const Args& a, const Maps& maps, int tp, const float* lse, float
   const int n = (tp * a.G + 15) / 16 * 16;
   const int q_bytes = n * D * 2, tile = kTile * D * 2;
   // key tiles fill what the rows and the control block leave of 227 KB
-  const int fixed = (int)(sizeof(Ctl) + (a.n_seqs + 1) * sizeof(int)) + 1024 + kQStages * q_bytes;
+  const int fixed = (int)(sizeof(Ctl) + (a.n_seqs + 1) * sizeof(int64_t)) + 1024 + kQStages * q_bytes;
   int ks = (227 * 1024 - fixed) / tile;
   if (ks > kMaxStages) ks = kMaxStages;
   const size_t smem = (size_t)fixed + (size_t)ks * tile;

@@ -61,21 +61,35 @@ __device__ __forceinline__ void raise(const Args& a, uint32_t bits) {
   if (a.status) atomicOr(a.status, bits);
 }
 
+// Bounded wait for a barrier's phase.  A phase that has completed costs one test; only a wait
+// that goes on looks at the CTA's abort flag, and one that runs out sets it and reports.
+__device__ __forceinline__ void wait_phase(const Args& a, uint64_t* bar, uint32_t parity,
+                                           volatile int* abort_flag) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait(at, parity)) return;
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (*abort_flag) return;
+    if (mbar_try_wait(at, parity)) return;
+  }
+  *abort_flag = 1;
+  raise(a, PP_S_TIMEOUT);
+}
+
 // Prefix sums of count(b) over the sequences into pre[0..n], by one CTA; ends with a
 // barrier.
-template <typename F>
-__device__ __forceinline__ void prefix_units(int* pre, int n, F count) {
+template <typename I, typename F>
+__device__ __forceinline__ void prefix_units(I* pre, int n, F count) {
   for (int b = threadIdx.x; b < n; b += blockDim.x) pre[b + 1] = count(b);
   if (threadIdx.x == 0) pre[0] = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
-    int base = 0;
+    I base = 0;
     for (int b0 = 0; b0 < n; b0 += 32) {
       const int b = b0 + threadIdx.x;
-      int x = b < n ? pre[b + 1] : 0;
+      I x = b < n ? pre[b + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const I y = __shfl_up_sync(0xffffffffu, x, o);
         if ((int)threadIdx.x >= o) x += y;
       }
       if (b < n) pre[b + 1] = base + x;
@@ -86,7 +100,8 @@ __device__ __forceinline__ void prefix_units(int* pre, int n, F count) {
 }
 
 // The sequence whose units hold u: pre[b] <= u < pre[b + 1].
-__device__ __forceinline__ int find_seq(const int* pre, int n, int u) {
+template <typename I>
+__device__ __forceinline__ int find_seq(const I* pre, int n, I u) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
