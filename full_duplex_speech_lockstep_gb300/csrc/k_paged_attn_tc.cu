@@ -107,13 +107,21 @@ __device__ __forceinline__ Unit unit_of(const Args& a, const int* pre, int u, in
   return x;
 }
 
-// D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
+// One MMA.  Descriptors come as lower words: the issuing thread is alone on its scheduler slot
+// and every instruction between two MMAs counts.  `acc` false: D = A B, else D += A B.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                        bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %4};\n"
+      " mov.b64 b, {%2, %4};\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"((uint32_t)acc));
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                        bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"((uint32_t)acc));
 }
 
 // 32 columns of this thread's tensor-memory lane
@@ -262,14 +270,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id = (1u << 4) | N::kMmaTypes | ((uint32_t)(kRowsT >> 4) << 24);
         constexpr uint32_t id_s = id | ((uint32_t)(kTile >> 3) << 17);
         constexpr uint32_t id_o = id | ((uint32_t)(D >> 3) << 17) | (1u << 16);   // B = V by keys
+        // lower descriptor words: the tiles' addresses in units of 16 bytes (below 2^14), and
+        // for V the distance of its 64-dim boxes
+        const uint32_t t_lo = smem_u32(smem) >> 4, q_lo = smem_u32(smem + C::kQOff) >> 4;
+        const uint32_t v_lo = t_lo | ((uint32_t)(kTile * 128 >> 4) << 16);
         uint32_t nq = 0, nl = 0, np[2] = {0, 0};
         auto scores = [&](int t, uint32_t slot) {
-          const uint32_t qb = smem_u32(smem + C::kQOff + t * C::kQBytes);
-          const uint32_t kb = smem_u32(smem + slot * C::kTileBytes);
+          const uint32_t q = q_lo + t * (C::kQBytes >> 4), k = t_lo + slot * (C::kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-            umma_bf16(tmem + t * kTile, smem_desc(qb + off), smem_desc(kb + off), id_s, kk > 0);
+            const uint32_t off = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+            umma_ss(tmem + t * kTile, q + off, k + off, id_s, kk > 0);
           }
           umma_commit(smem_u32(&ctl->sfull[t]));
         };
@@ -296,11 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++np[t];
               if (*abort_flag) break;
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-              const uint32_t vb = smem_u32(smem + sv * C::kTileBytes);
+              const uint32_t v = v_lo + sv * (C::kTileBytes >> 4);
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + kk * 8,
-                        smem_desc_mn(vb + kk * 2048, kTile * 128), id_o, j > 0 || kk > 0);
+                umma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + kk * 8, v + kk * (2048 >> 4),
+                        id_o, j > 0 || kk > 0);
               if (more) {
                 if (t == 0) {
                   wait(&ctl->full[sk], ((nl + 1) / kSlots) & 1);

@@ -57,6 +57,10 @@ __device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t r[2]) {
                : "r"(taddr));
 }
 
+// The constant upper words of the two kinds of descriptors here, for code that steps through a
+// tile by adding to the lower word (an address in units of 16 bytes).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
 // Shared-memory matrix descriptor, MN-major tile with the 128-byte swizzle: 8 k-rows of
 // 128 bytes (64 bf16 along M/N) per 1024-byte atom; atoms follow each other along K
 // every 1024 bytes (stride offset) and along M/N every `lbo` bytes (leading offset).
