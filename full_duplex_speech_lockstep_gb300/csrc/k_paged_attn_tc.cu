@@ -12,8 +12,10 @@
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D columns each).
 //   warp 0       producer: queries of the pair, then K and V tiles in turn, by TMA
 //   warp 1       one thread issues every MMA.  Order for each tile of keys: O0 += P0 V,
-//                S0 = Q0 K', O1 += P1 V, S1 = Q1 K' (K' the next keys).  MMAs run in issue
-//                order, so S_t may overwrite P_t right after the product that reads it.
+//                S0 = Q0 K', O1 += P1 V, S1 = Q1 K' (K' the next keys).  A thread's MMAs run in
+//                issue order, so S_t may overwrite P_t right after the product that reads it.
+//                (An issuer for each tile measured 689 us against 605: the two softmaxes then
+//                fall into step, and neither hides behind the other's MMAs.)
 //   warps 4-7, 8-11  softmax of tile 0, 1: one thread to a row.  A row's reference m follows
 //                its maximum only when it would fall behind by more than 2^8, so the sums of
 //                O in tensor memory are rarely rescaled; p stays below 2^8 (2^15 in fp16),
@@ -53,9 +55,9 @@ struct Ctl {
   uint64_t clean[2][2];   // [group][edge tile & 1]: the group's half of V is clean
   uint32_t bad[8];
   uint32_t tmem;
-  // 1 + the unit in which a softmax group took a non-finite value out of V.  A group is at
-  // most one unit ahead of the other, so two entries each are enough.
-  int wild[2][2];
+  // 1 + the unit in which a softmax group took a non-finite value out of V.  The single query
+  // buffer keeps a group at most two units ahead of the other: four entries are enough.
+  int wild[2][4];
   int abort;
 };
 
@@ -200,10 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->sfull[t]), 1);
       mbar_init(smem_u32(&ctl->pfull[t]), 4);
       mbar_init(smem_u32(&ctl->ofull[t]), 1);
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_u32(&ctl->clean[t][i]), 4);
-        ctl->wild[t][i] = 0;
-      }
+      for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl->clean[t][i]), 4);
+      for (int i = 0; i < 4; ++i) ctl->wild[t][i] = 0;
     }
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -266,6 +266,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ---- MMA issuer ---------------------------------------------------------------------
+      // The tensor pipe takes little ahead of time, so a wait between two MMAs leaves it idle, a
+      // completed one too (about 100 clocks).  So the next barrier is tested while two MMAs are
+      // still to be issued, and V is waited for by the softmax threads, before they hand over P.
+      // (Handing P over in two halves, for an earlier start, cost more in waits than it gave:
+      // 644 us against 605.)
       if (lane == 0) {
         constexpr uint32_t id = (1u << 4) | N::kMmaTypes | ((uint32_t)(kRowsT >> 4) << 24);
         constexpr uint32_t id_s = id | ((uint32_t)(kTile >> 3) << 17);
@@ -275,14 +280,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_lo = smem_u32(smem) >> 4, q_lo = smem_u32(smem + C::kQOff) >> 4;
         const uint32_t v_lo = t_lo | ((uint32_t)(kTile * 128 >> 4) << 16);
         uint32_t nq = 0, nl = 0, np[2] = {0, 0};
-        auto scores = [&](int t, uint32_t slot) {
+        constexpr int kS = D / 16, kP = kTile / 16;   // MMAs of one S, of one P V
+        auto scores = [&](int t, uint32_t slot, int from, int to) {
           const uint32_t q = q_lo + t * (C::kQBytes >> 4), k = t_lo + slot * (C::kTileBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
+          for (int kk = 0; kk < kS; ++kk) {
+            if (kk < from || kk >= to) continue;
             const uint32_t off = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
             umma_ss(tmem + t * kTile, q + off, k + off, id_s, kk > 0);
           }
-          umma_commit(smem_u32(&ctl->sfull[t]));
+        };
+        auto values = [&](int t, uint32_t slot, int from, int to, bool acc) {
+          const uint32_t v = v_lo + slot * (C::kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kP; ++kk) {
+            if (kk < from || kk >= to) continue;
+            umma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + kk * 8, v + kk * (2048 >> 4), id_o,
+                    acc || kk > 0);
+          }
         };
         for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
           const Unit x = unit_of(a, pre, u, tp, ns_cap);
@@ -294,32 +309,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&ctl->full[nl % kSlots], (nl / kSlots) & 1);
           if (*abort_flag) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          for (int t = 0; t < tiles; ++t) scores(t, nl % kSlots);
+          for (int t = 0; t < tiles; ++t) {
+            scores(t, nl % kSlots, 0, kS);
+            umma_commit(smem_u32(&ctl->sfull[t]));
+          }
           umma_commit(smem_u32(&ctl->empty[nl % kSlots]));
           if (nt == 1) umma_commit(smem_u32(&ctl->qempty));
           ++nl;
+          bool ready = false;                          // the next P has been seen
           for (int j = 0; j < nt; ++j) {
-            const uint32_t sv = nl % kSlots, sk = (nl + 1) % kSlots;
+            const uint32_t sv = nl % kSlots, sk = (nl + 1) % kSlots, kp = ((nl + 1) / kSlots) & 1;
             const bool more = j + 1 < nt;
-            wait(&ctl->full[sv], (nl / kSlots) & 1);
+#pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
-              wait(&ctl->pfull[t], np[t] & 1);
+              if (!ready) wait(&ctl->pfull[t], np[t] & 1);
               ++np[t];
-              if (*abort_flag) break;
+              const int next = t + 1 < tiles ? t + 1 : 0;
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-              const uint32_t v = v_lo + sv * (C::kTileBytes >> 4);
-#pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + kk * 8, v + kk * (2048 >> 4),
-                        id_o, j > 0 || kk > 0);
               if (more) {
-                if (t == 0) {
-                  wait(&ctl->full[sk], ((nl + 1) / kSlots) & 1);
-                  if (*abort_flag) break;
-                  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                }
-                scores(t, sk);
+                values(t, sv, 0, kP - 2, j > 0);
+                const bool k_in = t > 0 || mbar_test(smem_u32(&ctl->full[sk]), kp);
+                values(t, sv, kP - 2, kP, true);
+                if (!k_in) wait(&ctl->full[sk], kp);
+                scores(t, sk, 0, kS - 2);
+                ready = mbar_test(smem_u32(&ctl->pfull[next]), np[next] & 1);
+                scores(t, sk, kS - 2, kS);
+                umma_commit(smem_u32(&ctl->sfull[t]));
               } else {
+                values(t, sv, 0, kP - 2, j > 0);
+                ready = next != 0 && mbar_test(smem_u32(&ctl->pfull[next]), np[next] & 1);
+                values(t, sv, kP - 2, kP, true);
                 umma_commit(smem_u32(&ctl->ofull[t]));
               }
             }
@@ -388,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               found = found || (j0 + row >= x.low && j0 + row < x.end);
             }
           }
-          if (found) ctl->wild[t][nu & 1] = u + 1;
+          if (found) ctl->wild[t][nu & 3] = u + 1;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (tiles == 2) {    // both halves, before either product
             __syncwarp();
@@ -419,10 +438,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((bad >> (i >> 4)) & 1u) s[i] = 0xff800000u;
             }
           }
-          float mx = -INFINITY;
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < kTile; i += 2)
-            mx = max3(mx, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+            m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], __uint_as_float(s[i]),
+                                    __uint_as_float(s[i + 1]));
+          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
           const float want = mx * a.c - N::kShift;
           if (j == 0) {
             m = mx == -INFINITY ? -INFINITY : want;
@@ -445,27 +466,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float ref = m == -INFINITY ? 0.f : m;
           const uint64_t r2 = f32x2(-ref, -ref);
-          uint64_t sum2 = f32x2(l, 0.f);
+          uint64_t sum2[2] = {f32x2(l, 0.f), 0};
           uint32_t p[kTile / 2];
 #pragma unroll
           for (int i = 0; i < kTile; i += 2) {
             const uint64_t z = fma2((uint64_t)s[i] | ((uint64_t)s[i + 1] << 32), c2, r2);
             const float p0 = exp2_approx(lo_of(z)), p1 = exp2_approx(hi_of(z));
-            sum2 = add2(sum2, f32x2(p0, p1));
+            sum2[(i >> 1) & 1] = add2(sum2[(i >> 1) & 1], f32x2(p0, p1));
             p[i >> 1] = N::pack(p0, p1);
           }
-          l = lo_of(sum2) + hi_of(sum2);
           tmem_st32(s_at, p);
           tmem_st32(s_at + 32, p + 32);
+          tmem_wait_st();
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->pfull[t]));
+          const uint64_t both = add2(sum2[0], sum2[1]);
+          l = lo_of(both) + hi_of(both);
         };
         if (edge)
           weights(std::true_type());
         else
           weights(std::false_type());
-        tmem_wait_st();
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->pfull[t]));
       }
       nl += 2 * nt;
 
@@ -480,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&ctl->ofull[t], no & 1);
         ++no;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        wild = *reinterpret_cast<volatile int*>(&ctl->wild[0][nu & 1]) == u + 1 ||
-               *reinterpret_cast<volatile int*>(&ctl->wild[1][nu & 1]) == u + 1;
+        wild = *reinterpret_cast<volatile int*>(&ctl->wild[0][nu & 3]) == u + 1 ||
+               *reinterpret_cast<volatile int*>(&ctl->wild[1][nu & 3]) == u + 1;
       }
       const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll
