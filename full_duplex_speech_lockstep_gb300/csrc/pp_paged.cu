@@ -186,21 +186,22 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
   a.G = n_heads / kv->n_kv_heads;
   a.window = effective_window(kv, window);
   a.c = scale * kLog2e;
-  const bool tall = is_long(a, max_q);
-  const AttnPlan plan = attn_plan(a, max_q);
-  const LongPlan tall_plan = long_plan(a, T, max_q);
-  Maps maps;
-  if (!page_map(&maps.k, kv, kv->k) || !page_map(&maps.v, kv, kv->v) ||
-      !query_map(&maps.q, a, kv->type, q, q_stride, tall ? tall_plan.tp : plan.tp))
-    return PP_EINVAL;
   AttnOut o{};
   o.out = out;
   o.lse = lse;
   o.part = reinterpret_cast<float*>(scratch);
-  o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) +
-                                        (tall ? tall_plan.rec_bytes : plan.rec_bytes));
-  return rc(tall ? launch_paged_attn_tc(a, kv->type, tall_plan, maps, o, kv->v, (cudaStream_t)stream)
-                 : launch_paged_attn(a, kv->type, plan, maps, o, (cudaStream_t)stream));
+  Maps maps;
+  if (!page_map(&maps.k, kv, kv->k) || !page_map(&maps.v, kv, kv->v)) return PP_EINVAL;
+  if (is_long(a, max_q)) {
+    const LongPlan p = long_plan(a, T, max_q);
+    if (!query_map(&maps.q, a, kv->type, q, q_stride, p.tp)) return PP_EINVAL;
+    o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) + p.rec_bytes);
+    return rc(launch_paged_attn_tc(a, kv->type, p, maps, o, kv->v, (cudaStream_t)stream));
+  }
+  const AttnPlan p = attn_plan(a, max_q);
+  if (!query_map(&maps.q, a, kv->type, q, q_stride, p.tp)) return PP_EINVAL;
+  o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) + p.rec_bytes);
+  return rc(launch_paged_attn(a, kv->type, p, maps, o, (cudaStream_t)stream));
 }
 
 int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const float* lse,

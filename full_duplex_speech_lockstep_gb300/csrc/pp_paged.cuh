@@ -318,22 +318,11 @@ struct Maps {
   CUtensorMap k, v, q;
 };
 
-// Rows of one unit: whole tokens with all G heads of a key head, up to 16 * wr rows.
-struct RowTile {
-  int wr;          // 16-row fragments: 1, 2 or 4
-  int tp;          // tokens
-};
-inline RowTile row_tile(int G, int max_q) {
-  const int64_t rows = (int64_t)max_q * G;
-  RowTile r;
-  r.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  r.tp = 16 * r.wr / G;
-  if (max_q < r.tp) r.tp = max_q;
-  return r;
-}
-
-// Split of the rows and keys of one attention call (k_paged_attn.cu).
-struct AttnPlan : RowTile {
+// Split of the rows and keys of a call of short chunks (k_paged_attn.cu).
+struct AttnPlan {
+  int wr;          // 16-row fragments of a row tile: 1 or 2
+  int tp;          // tokens of a row tile
+  int share;       // SMs for each (sequence, key head), at least 1
   int ns_cap;      // splits of the longest sequence that the table can hold
   size_t rec_bytes, ml_bytes;
 };
@@ -341,7 +330,7 @@ AttnPlan attn_plan(const Args& a, int max_q);
 
 // Chunks of more than kShortRows rows (tokens x heads of a key head) run on the 5th-generation
 // tensor cores (k_paged_attn_tc.cu): row tiles of 128 rows, taken in pairs.
-constexpr int kShortRows = 64;
+constexpr int kShortRows = 32;
 struct LongPlan {
   int tp;          // tokens of a row tile
   int ns;          // splits of a sequence's keys, at most

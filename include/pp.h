@@ -524,9 +524,10 @@ int pp_rvq_dequantize(const int32_t* codes, int code_stride, int n_frames, int n
  * Every call is asynchronous on `stream`, belongs to the current device, allocates nothing
  * and may be captured into a graph; lengths, tables and row offsets are read when the
  * graph runs.  status (a device word) may be NULL; PP_S_TIMEOUT is OR-ed into it when a
- * bounded wait inside a kernel gave up (the results are then incomplete).  A sequence's results depend on its
- * own rows, entries and lengths and on the call's head counts, n_seqs, T and max_q, bit for
- * bit, never on what the other sequences hold. */
+ * bounded wait inside a kernel gave up (the results are then incomplete).  A sequence's results depend,
+ * bit for bit, on its own rows, entries and lengths and on the call's head counts and max_q,
+ * not on the rest of the batch; with max_q rows of more than 32 query heads x tokens to a
+ * key head, n_seqs and T (never what the other sequences hold) may set how its keys are split. */
 #define PP_F32 0
 #define PP_BF16 1
 #define PP_F16 2
