@@ -26,8 +26,8 @@
 //
 // Keys that some row of a tile may not see need care in the second product, where a
 // weight of zero times a stored infinity would be NaN: on such tiles every non-finite
-// value of V is taken out of the product and its infinities and NaNs are added to just
-// the rows that see the key.
+// value of V is taken out of the product and, at the unit's end, added to the rows that see
+// the key.
 #include "pp_paged.cuh"
 
 namespace pp {
@@ -60,6 +60,7 @@ struct Cfg {
 struct Ctl {
   uint64_t kfull[6], kempty[6], vfull[6], vempty[6], qfull[kQBufs], qempty[kQBufs];
   uint32_t bad[6];
+  int wild;              // 1 + place of the unit in which a non-finite V was taken out
   int abort;
 };
 
@@ -169,7 +170,7 @@ template <typename T, int D, int WR>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_attn(const Args a, const int tp, const int share, const int ns_cap, const AttnOut o,
                  const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                 const __grid_constant__ CUtensorMap mapQ) {
+                 const __grid_constant__ CUtensorMap mapQ, const void* v_pages) {
   using C = Cfg<D, WR>;
   using N = Num<T>;
   constexpr int R = C::R;
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->qfull[i]), 1);
       mbar_init(smem_u32(&ctl->qempty[i]), kWarps);
     }
+    ctl->wild = 0;
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -206,13 +208,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   });
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
 
+  Walk x(a, pre, tp, share);            // every role walks by itself from the same start
+
   if (threadIdx.x < 128) {
     // ---- producer -------------------------------------------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (threadIdx.x >= 32) return;
     uint32_t nq = 0, nk = 0, nv = 0;
     uint32_t seen_bad = 0;
-    for (Walk x(a, pre, tp, share); !x.done() && !*abort_flag; x.next()) {
+#pragma unroll 1
+    for (; !x.done() && !*abort_flag; x.next()) {
       if (x.tile0 == x.tile1) continue;
       const int qb = nq % kQBufs;
       if (nq >= kQBufs) wait(&ctl->qempty[qb], (nq / kQBufs - 1) & 1);
@@ -226,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(dst + bx * (R * 128), &mapQ, bx * 64, x.h * a.G, x.s.row0 + x.t0, 0, bar);
       }
       ++nq;
+#pragma unroll 1
       for (int t = x.tile0; t < x.tile1; ++t) {
         const int ks = nk % C::KS, vs = nv % C::VS;
         if (nk >= C::KS) wait(&ctl->kempty[ks], (nk / C::KS - 1) & 1);
@@ -244,12 +250,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
     // every copy lands before the CTA may exit (bounded waits)
     if (lane == 0) {
+#pragma unroll 1
       for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; i < nq; ++i)
-        mbar_wait(smem_u32(&ctl->qfull[i % kQBufs]), (i / kQBufs) & 1);
+        drain_phase(&ctl->qfull[i % kQBufs], (i / kQBufs) & 1);
+#pragma unroll 1
       for (uint32_t i = nk > C::KS ? nk - C::KS : 0; i < nk; ++i)
-        mbar_wait(smem_u32(&ctl->kfull[i % C::KS]), (i / C::KS) & 1);
+        drain_phase(&ctl->kfull[i % C::KS], (i / C::KS) & 1);
+#pragma unroll 1
       for (uint32_t i = nv > C::VS ? nv - C::VS : 0; i < nv; ++i)
-        mbar_wait(smem_u32(&ctl->vfull[i % C::VS]), (i / C::VS) & 1);
+        drain_phase(&ctl->vfull[i % C::VS], (i / C::VS) & 1);
     }
     return;
   }
@@ -268,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     grp[i] = i * 8 + fr - tok[i] * a.G;
   }
   uint32_t nq = 0, nk = 0, nv = 0;
-  for (Walk x(a, pre, tp, share); !x.done(); x.next()) {
+#pragma unroll 1
+  for (; !x.done(); x.next()) {
     const int rows = x.nt * a.G;
     float m[2 * WR], l[2 * WR], acc[WR][D / 8][4];
 #pragma unroll
@@ -292,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kk = 0; kk < D / 16; ++kk)
         ldsm4(tile_addr(qbuf, R * 128, (lm & 1) * 8 + lr, kk * 2 + (lm >> 1)), aq[kk]);
     }
+#pragma unroll 1
     for (int t = x.tile0; t < x.tile1; ++t) {
       const int j0 = t * kTile;
       // ---- S = Q K^T: this warp's 16 keys, every row
@@ -353,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return j <= p && (!a.window || j > p - a.window) && !((bad >> ((j - j0) >> 4)) & 1u);
       };
       const int j1 = j0 + warp * 16;
+      const int low = a.window ? max(x.first - a.window + 1, 0) : 0;
       uint32_t ap[WR][4];                       // P as the second product's operand
       float grow[2 * WR];
       bool grown = false;
@@ -373,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         top = fmaf(top, a.c, -N::kShift);
         // the reference follows the maximum only when it falls behind by kLag (or is none yet)
         const float mn = top > m[i] + kLag || m[i] == -INFINITY ? fmaxf(m[i], top) : m[i];
-        grow[i] = mn == m[i] ? 1.f : exp2f(m[i] - mn);
+        grow[i] = mn == m[i] ? 1.f : exp2_approx(m[i] - mn);
         grown = grown || mn != m[i];
         m[i] = mn;
         const float ref = mn == -INFINITY ? 0.f : -mn;
@@ -399,22 +411,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int y = 0; y < D / 32; ++y)
           ldsm4_t(tile_addr(vbuf, kTile * 128, warp * 16 + (lm & 1) * 8 + lr,
                             half * (D / 16) + y * 2 + (lm >> 1)), bv[y]);
-        uint32_t lost[D / 32][4];
-        uint32_t wild = 0;   // non-finite halves of V
         if (edge) {
+          bool seen = false;     // of an entry that some row sees
 #pragma unroll
           for (int y = 0; y < D / 32; ++y)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t w = bv[y][e];
-              uint32_t mask = 0;
-              if ((w & N::kExp) == N::kExp) mask |= 0xffffu;
-              if (((w >> 16) & N::kExp) == N::kExp) mask |= 0xffff0000u;
-              lost[y][e] = w & mask;
-              bv[y][e] = w & ~mask;
-              wild |= mask;
+              const int j = j1 + (e & 1) * 8 + fc;
+              uint32_t& w = bv[y][e];
+              if ((w & N::kExp) == N::kExp) {
+                w &= 0xffff0000u;
+                seen = seen || (j >= low && j < x.stop);
+              }
+              if (((w >> 16) & N::kExp) == N::kExp) {
+                w &= 0xffffu;
+                seen = seen || (j + 1 >= low && j + 1 < x.stop);
+              }
             }
-          wild = __ballot_sync(0xffffffffu, wild != 0);
+          if (seen) ctl->wild = x.at + 1;
         }
 #pragma unroll
         for (int y = 0; y < D / 32; ++y)
@@ -423,44 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             N::mma(acc[i][half * (D / 16) + y * 2], ap[i], bv[y][0], bv[y][1]);
             N::mma(acc[i][half * (D / 16) + y * 2 + 1], ap[i], bv[y][2], bv[y][3]);
           }
-        if (wild) {
-          // rare: count, per row and dim, the +inf, -inf and NaN entries that the row sees
-#pragma unroll
-          for (int i = 0; i < WR; ++i) {
-            uint32_t av[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = j1 + (e >> 1) * 8 + fc;
-              av[e] = (sees(i * 2 + (e & 1), j) ? N::kOne : 0u) |
-                      (sees(i * 2 + (e & 1), j + 1) ? N::kOne << 16 : 0u);
-            }
-#pragma unroll
-            for (int y = 0; y < D / 32; ++y)
-#pragma unroll
-              for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int kind = 0; kind < 3; ++kind) {
-                  uint32_t ind[2];
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    auto is = [&](uint32_t hw) -> uint32_t {
-                      if ((hw & N::kExp) != N::kExp) return 0u;
-                      const int k2 = (hw & 0x7fffu) != N::kExp ? 2 : (int)(hw >> 15);
-                      return k2 == kind ? N::kOne : 0u;
-                    };
-                    const uint32_t w = lost[y][n * 2 + e];
-                    ind[e] = is(w & 0xffffu) | (is(w >> 16) << 16);
-                  }
-                  float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-                  N::mma(cnt, av, ind[0], ind[1]);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (cnt[e] > 0.f)
-                      acc[i][half * (D / 16) + y * 2 + n][e] +=
-                          kind == 0 ? INFINITY : kind == 1 ? -INFINITY : NAN;
-                }
-          }
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->vempty[vs]));
@@ -480,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((lane & 3) == 0) ml[warp * R + i * 8 + fr] = make_float2(m[i], l[i]);
     }
     named_sync(1, kWarps * 32);
+    const bool wild = *reinterpret_cast<volatile int*>(&ctl->wild) == x.at + 1;
 #pragma unroll
     for (int i = 0; i < 2 * WR; ++i) {
       if (i * 8 >= rows) break;
@@ -487,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * R + i * 8 + fr].x);
       // (a warp without a reference has nothing, or NaN: either passes unscaled)
-      scale_rows<WR, D>(acc, i, m[i] == -INFINITY ? 1.f : exp2f(m[i] - top));
+      scale_rows<WR, D>(acc, i, m[i] == -INFINITY ? 1.f : exp2_approx(m[i] - top));
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int r0 = i * 8 + half * kJoinRows;
@@ -509,25 +486,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             ol[w] = ml[w * R + r];
             M = fmaxf(M, ol[w].x);
           }
-          float2 sum = make_float2(0.f, 0.f);
+          float sum[2] = {0.f, 0.f};
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            L += (ol[w].x == -INFINITY ? 1.f : exp2f(ol[w].x - M)) * ol[w].y;
+            L += (ol[w].x == -INFINITY ? 1.f : exp2_approx(ol[w].x - M)) * ol[w].y;
             const float2 y =
                 *reinterpret_cast<const float2*>(join + (w * kJoinRows + jr) * D + (d ^ (jr << 3)));
-            sum.x += y.x;
-            sum.y += y.y;
+            sum[0] += y.x;
+            sum[1] += y.y;
           }
           const int tk = r / a.G, hd = x.h * a.G + r - tk * a.G;
+          if (wild)
+            add_lost<N, 2>(a, v_pages, x.b, x.h, x.tile0, x.tile1, x.stop, x.first,
+                           x.first + x.nt - 1, x.first + tk, d, sum);
           if (x.ns == 1) {
             const int64_t row = (int64_t)(x.s.row0 + x.t0 + tk) * (a.Hk * a.G) + hd;
             const float inv = L == 0.f ? 0.f : 1.f / L;
             *reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(o.out) + row * D + d) =
-                N::pack(sum.x * inv, sum.y * inv);
+                N::pack(sum[0] * inv, sum[1] * inv);
             if (o.lse && d == 0) o.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
           } else {
             const int64_t rec = (((int64_t)x.b * tp + tk) * (a.Hk * a.G) + hd) * ns_cap + x.i;
-            *reinterpret_cast<float2*>(o.part + rec * D + d) = sum;
+            *reinterpret_cast<float2*>(o.part + rec * D + d) = make_float2(sum[0], sum[1]);
             if (d == 0) o.part_ml[rec] = make_float2(M, L);
           }
         }
@@ -544,8 +524,9 @@ __global__ void __launch_bounds__(128)
   pdl_wait_and_trigger();
   pdl_trigger();
   const int lane = threadIdx.x & 31, H = a.Hk * a.G;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int hd = (int)(id % H), tk = (int)(id / H % tp), b = (int)(id / H / tp);
+  const uint32_t id = blockIdx.x * 4 + (threadIdx.x >> 5);   // (sequence, token, head)
+  const uint32_t rest = id / (uint32_t)H;
+  const int hd = (int)(id - rest * H), b = (int)(rest / (uint32_t)tp), tk = (int)(rest - b * tp);
   if (b >= a.n_seqs) return;
   const Seq s = seq_of(a, b);
   if (s.n > tp || tk >= s.n) return;
@@ -558,7 +539,7 @@ __global__ void __launch_bounds__(128)
 
 template <typename T, int D, int WR>
 cudaError_t run(const Args& a, const AttnPlan& p, const Maps& maps, const AttnOut& o,
-                cudaStream_t s) {
+                const void* v_pages, cudaStream_t s) {
   const size_t smem =
       Cfg<D, WR>::kCtlOff + sizeof(Ctl) + (size_t)(a.n_seqs + 1) * sizeof(int) + 1024;
   static_assert(Cfg<D, WR>::kCtlOff + sizeof(Ctl) + (kMaxSeqs + 1) * sizeof(int) + 1024 <=
@@ -571,7 +552,7 @@ cudaError_t run(const Args& a, const AttnPlan& p, const Maps& maps, const AttnOu
   const int64_t most = row_tiles * a.Hk * p.ns_cap;
   const int nsm = sm_count();
   err = launch(k_paged_attn<T, D, WR>, dim3((unsigned)(most < nsm ? most : nsm)), kThreads, smem, s,
-               a, p.tp, p.share, p.ns_cap, o, maps.k, maps.v, maps.q);
+               a, p.tp, p.share, p.ns_cap, o, maps.k, maps.v, maps.q, v_pages);
   if (err != cudaSuccess || p.ns_cap == 1) return err;
   const int64_t rows = (int64_t)a.n_seqs * p.tp * a.Hk * a.G;
   return launch(k_paged_join<T, D>, dim3((unsigned)((rows + 3) / 4)), 128, 0, s, a, p.tp, p.share,
@@ -580,8 +561,9 @@ cudaError_t run(const Args& a, const AttnPlan& p, const Maps& maps, const AttnOu
 
 template <typename T, int D>
 cudaError_t pick(const Args& a, const AttnPlan& p, const Maps& maps, const AttnOut& o,
-                 cudaStream_t s) {
-  return p.wr == 1 ? run<T, D, 1>(a, p, maps, o, s) : run<T, D, 2>(a, p, maps, o, s);
+                 const void* v_pages, cudaStream_t s) {
+  return p.wr == 1 ? run<T, D, 1>(a, p, maps, o, v_pages, s)
+                   : run<T, D, 2>(a, p, maps, o, v_pages, s);
 }
 
 }  // namespace
@@ -612,11 +594,12 @@ AttnPlan attn_plan(const Args& a, int max_q) {
 }
 
 cudaError_t launch_paged_attn(const Args& a, int type, const AttnPlan& plan, const Maps& maps,
-                              const AttnOut& o, cudaStream_t s) {
+                              const AttnOut& o, const void* v_pages, cudaStream_t s) {
   if (type == PP_BF16)
-    return a.D == 128 ? pick<__nv_bfloat16, 128>(a, plan, maps, o, s)
-                      : pick<__nv_bfloat16, 64>(a, plan, maps, o, s);
-  return a.D == 128 ? pick<__half, 128>(a, plan, maps, o, s) : pick<__half, 64>(a, plan, maps, o, s);
+    return a.D == 128 ? pick<__nv_bfloat16, 128>(a, plan, maps, o, v_pages, s)
+                      : pick<__nv_bfloat16, 64>(a, plan, maps, o, v_pages, s);
+  return a.D == 128 ? pick<__half, 128>(a, plan, maps, o, v_pages, s)
+                    : pick<__half, 64>(a, plan, maps, o, v_pages, s);
 }
 
 }  // namespace paged

@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ---- producer -----------------------------------------------------------------------
       uint32_t nq = 0, nl = 0, seen_bad = 0;
+#pragma unroll 1
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
         const Unit x = unit_of(a, pre, u, tp, ns_cap);
         if (x.tile0 == x.tile1) continue;
@@ -243,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           bx * 64, x.h * a.G, x.row0 + x.t0 + t * tp, 0, bar);
         }
         ++nq;
+#pragma unroll 1
         for (int i = 0; i < 2 * (x.tile1 - x.tile0); ++i) {
           const int slot = nl % kSlots;
           if (nl >= kSlots) wait(&ctl->empty[slot], (nl / kSlots - 1) & 1);
@@ -259,9 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
       // every copy lands before the CTA may exit (bounded waits)
       if (lane == 0) {
-        if (nq > 0) mbar_wait(smem_u32(&ctl->qfull), (nq - 1) & 1);
+        if (nq > 0) drain_phase(&ctl->qfull, (nq - 1) & 1);
+#pragma unroll 1
         for (uint32_t i = nl > kSlots ? nl - kSlots : 0; i < nl; ++i)
-          mbar_wait(smem_u32(&ctl->full[i % kSlots]), (i / kSlots) & 1);
+          drain_phase(&ctl->full[i % kSlots], (i / kSlots) & 1);
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -299,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     acc || kk > 0);
           }
         };
+#pragma unroll 1
         for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
           const Unit x = unit_of(a, pre, u, tp, ns_cap);
           const int nt = x.tile1 - x.tile0;
@@ -317,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (nt == 1) umma_commit(smem_u32(&ctl->qempty));
           ++nl;
           bool ready = false;                          // the next P has been seen
+#pragma unroll 1
           for (int j = 0; j < nt; ++j) {
             const uint32_t sv = nl % kSlots, sk = (nl + 1) % kSlots, kp = ((nl + 1) / kSlots) & 1;
             const bool more = j + 1 < nt;
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every MMA is done before tensor memory is given back (bounded wait)
         umma_commit(smem_u32(&ctl->done));
-        mbar_wait(smem_u32(&ctl->done), 0);
+        drain_phase(&ctl->done, 0);
       }
       __syncwarp();
     }
@@ -368,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = lane_base + t * kTile, o_at = lane_base + 2 * kTile + t * D;
     const uint64_t c2 = f32x2(a.c, a.c);
     uint32_t ns_ = 0, no = 0, nl = 0, ne = 0, nu = 0;
+#pragma unroll 1
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++nu) {
       const Unit x = unit_of(a, pre, u, tp, ns_cap);
       const int nt = x.tile1 - x.tile0;
@@ -382,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = first + t * tp + tk;
       const bool live = r < tokens * a.G;
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int j = 0; j < nt; ++j) {
         const int j0 = (x.tile0 + j) * kTile;
         // does some row of the pair not see some key?
@@ -395,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int share = kTile / tiles;
           uint8_t* vt = smem + vslot * C::kTileBytes;
           bool found = false;
+#pragma unroll 1
           for (int i = r; i < share * (D / 8); i += 128) {
             const int row = t * share + i / (D / 8), ch = i % (D / 8);
             uint4* at = reinterpret_cast<uint4*>(
@@ -451,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O = O 2^(old - new), row by row; the product that O holds is done, since S was
             // issued after it
             const float mn = want > m + kLag ? want : m;
-            const float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
+            const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
             l *= f;
             m = mn;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < D / 8; ++i) {
               uint32_t w[8];
               tmem_ld8(o_at + i * 8, w);
@@ -506,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                *reinterpret_cast<volatile int*>(&ctl->wild[1][nu & 3]) == u + 1;
       }
       const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < D / 32; ++i) {
         uint32_t w[32];
         if (nt > 0) {
@@ -519,25 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e) w[e] = 0;
         }
         if (wild && live) {
-          // rare: add the non-finite values that this row sees in the tiles that were cleaned
-          // (their weights are positive)
-          for (int j0 = x.tile0 * kTile; j0 < min(x.tile1 * kTile, x.end); j0 += kTile) {
-            const int j1 = min(j0 + kTile, x.end);
-            bool cleaned = j0 + kTile - 1 > first ||
-                           (a.window && j0 <= first + x.nt - 1 - a.window);
-            for (int j = j0; j < j1; j += 1 << a.lps) cleaned |= page_of(a, x.b, j) < 0;
-            if (!cleaned) continue;
-            for (int j = j0; j < j1; ++j) {
-              const int pg = page_of(a, x.b, j);
-              if (j > pos || (a.window && j <= pos - a.window) || pg < 0) continue;
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(v_pages) + pg * a.page_stride +
-                                  (((int64_t)x.h << a.lps) + (j & ((1 << a.lps) - 1))) * D + i * 32;
+          // rare (their weights are positive)
+          float add[32] = {};
+          add_lost<N, 32>(a, v_pages, x.b, x.h, x.tile0, x.tile1, x.end, first, first + x.nt - 1,
+                          pos, i * 32, add);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if ((v[e] & N::kExp) == N::kExp)
-                  w[e] = __float_as_uint(__uint_as_float(w[e]) + N::to_float(v[e]));
-            }
-          }
+          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) + add[e]);
         }
         if (live) {
           if (whole) {
@@ -584,8 +579,8 @@ __global__ void __launch_bounds__(128)
   pdl_wait_and_trigger();
   pdl_trigger();
   const int lane = threadIdx.x & 31, H = a.Hk * a.G;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int64_t row = id / H;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);   // below 2^31 + 3
+  const int row = (int)((uint32_t)id / (uint32_t)H);
   if (row >= a.T) return;
   int lo = 0, hi = a.n_seqs;           // the last sequence that starts at or before the row
   while (hi - lo > 1) {

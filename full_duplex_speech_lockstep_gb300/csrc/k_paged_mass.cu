@@ -125,6 +125,7 @@ template <typename M>
 __device__ __forceinline__ float weigh(uint32_t at, const float* ref, uint64_t c2, int cols, int lo,
                                        int hi, M) {
   uint64_t part[2] = {0, 0};   // two sums of two
+#pragma unroll 1
   for (int c0 = 0; c0 < cols; c0 += 16) {
     uint32_t s[16];
     tmem_ld16(at + c0, s);
@@ -214,10 +215,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A unit that no row sees has nothing to add; without decay it is left out.
   auto skip = [&](const Walk& x) { return x.t0 == x.t1 && decay == 1.f; };
 
+  Walk x(a, pre, tp);                   // every role walks by itself from the same start
+
   if (warp == 0) {
     // ---- producer -------------------------------------------------------------------------
     uint32_t nk = 0, nq = 0, seen_bad = 0;
-    for (Walk x(a, pre, tp); !x.done() && !*abort_flag; x.next()) {
+#pragma unroll 1
+    for (; !x.done() && !*abort_flag; x.next()) {
       if (x.t0 == x.t1) continue;
       const int ks = nk % KS;
       if (nk >= KS) wait(&ctl->kempty[ks], (nk / KS - 1) & 1);
@@ -225,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       seen_bad |= load_key_tile(a, &mapK, smem_u32(smem + ks * kTileBytes),
                                 smem_u32(&ctl->kfull[ks]), x.b, x.h, x.j0, x.s.len, lane, nullptr);
       ++nk;
+#pragma unroll 1
       for (int t = x.t0; t < x.t1; t += tp) {
         const int qs = nq % kQStages;
         if (nq >= kQStages) wait(&ctl->qempty[qs], (nq / kQStages - 1) & 1);
@@ -241,10 +246,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
     if (lane == 0) {   // every copy lands before the CTA may exit (bounded waits)
+#pragma unroll 1
       for (uint32_t i = nk > KS ? nk - KS : 0; i < nk; ++i)
-        mbar_wait(smem_u32(&ctl->kfull[i % KS]), (i / KS) & 1);
+        drain_phase(&ctl->kfull[i % KS], (i / KS) & 1);
+#pragma unroll 1
       for (uint32_t i = nq > kQStages ? nq - kQStages : 0; i < nq; ++i)
-        mbar_wait(smem_u32(&ctl->qfull[i % kQStages]), (i / kQStages) & 1);
+        drain_phase(&ctl->qfull[i % kQStages], (i / kQStages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -253,12 +260,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id = (1u << 4) | Num<T>::kMmaTypes | ((uint32_t)(kTile >> 4) << 24) |
                           ((uint32_t)(N_ >> 3) << 17);
       uint32_t nk = 0, nq = 0;
-      for (Walk x(a, pre, tp); !x.done() && !*abort_flag; x.next()) {
+#pragma unroll 1
+      for (; !x.done() && !*abort_flag; x.next()) {
         if (x.t0 == x.t1) continue;
         const int ks = nk % KS;
         wait(&ctl->kfull[ks], (nk / KS) & 1);
         ++nk;
         const uint32_t kb = smem_u32(smem + ks * kTileBytes);
+#pragma unroll 1
         for (int t = x.t0; t < x.t1; t += tp) {
           const int qs = nq % kQStages, bb = nq % kBufs;
           wait(&ctl->qfull[qs], (nq / kQStages) & 1);
@@ -279,13 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every MMA is done before tensor memory is given back (bounded wait)
       umma_commit(smem_u32(&ctl->done));
-      mbar_wait(smem_u32(&ctl->done), 0);
+      drain_phase(&ctl->done, 0);
     }
     __syncwarp();
   } else if (warp == 2) {
     // ---- old mass and pages: four keys to a lane, four units at a time
     uint32_t nu = 0;
-    for (Walk x(a, pre, tp); !x.done() && !*abort_flag;) {
+#pragma unroll 1
+    while (!x.done() && !*abort_flag) {
       float old[4][4];
       int page[4], n = 0;
 #pragma unroll
@@ -328,7 +338,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       gh[k] = lane + k * 32 - tk[k] * a.G;
     }
     uint32_t nl = 0;
-    Walk x(a, pre, tp);
     int t = x.done() ? 0 : x.t0;
     while (!x.done() && !*abort_flag) {
       float z[4][4];
@@ -371,12 +380,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint64_t c2 = f32x2(a.c, a.c);
     uint32_t nl = 0, nu = 0, nm = 0;
-    for (Walk x(a, pre, tp); !x.done(); x.next()) {
+#pragma unroll 1
+    for (; !x.done(); x.next()) {
       if (skip(x)) continue;
       const int first = x.s.len - x.s.n, j = x.j0 + key;
       const int steps = (x.t1 - x.t0 + tp - 1) / tp;
       float sum = 0.f;
       int t = x.t0;
+#pragma unroll 1
       for (int i = 0; i < steps; ++i, ++nl, t += tp) {
         if ((nl & 1) != g) continue;
         const int bb = nl % kBufs, ls = nl % kAux;

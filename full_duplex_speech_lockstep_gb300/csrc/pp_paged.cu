@@ -201,7 +201,7 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
   const AttnPlan p = attn_plan(a, max_q);
   if (!query_map(&maps.q, a, kv->type, q, q_stride, p.tp)) return PP_EINVAL;
   o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) + p.rec_bytes);
-  return rc(launch_paged_attn(a, kv->type, p, maps, o, (cudaStream_t)stream));
+  return rc(launch_paged_attn(a, kv->type, p, maps, o, kv->v, (cudaStream_t)stream));
 }
 
 int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const float* lse,

@@ -67,6 +67,7 @@ __device__ __forceinline__ void wait_phase(const Args& a, uint64_t* bar, uint32_
                                            volatile int* abort_flag) {
   const uint32_t at = smem_u32(bar);
   if (mbar_try_wait(at, parity)) return;
+#pragma unroll 1     // (unrolled, the many waits of a kernel outgrow the instruction cache)
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (*abort_flag) return;
     if (mbar_try_wait(at, parity)) return;
@@ -75,15 +76,25 @@ __device__ __forceinline__ void wait_phase(const Args& a, uint64_t* bar, uint32_
   raise(a, PP_S_TIMEOUT);
 }
 
+// The same for a thread that has nothing to report: copies in flight, the last MMAs.
+__device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i)
+    if (mbar_try_wait(at, parity)) return;
+}
+
 // Prefix sums of count(b) over the sequences into pre[0..n], by one CTA; ends with a
 // barrier.
 template <typename I, typename F>
 __device__ __forceinline__ void prefix_units(I* pre, int n, F count) {
+#pragma unroll 1
   for (int b = threadIdx.x; b < n; b += blockDim.x) pre[b + 1] = count(b);
   if (threadIdx.x == 0) pre[0] = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
     I base = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < n; b0 += 32) {
       const int b = b0 + threadIdx.x;
       I x = b < n ? pre[b + 1] : 0;
@@ -103,6 +114,7 @@ __device__ __forceinline__ void prefix_units(I* pre, int n, F count) {
 template <typename I>
 __device__ __forceinline__ int find_seq(const I* pre, int n, I u) {
   int lo = 0, hi = n;
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (pre[mid] <= u) lo = mid; else hi = mid;
@@ -140,6 +152,7 @@ __device__ __forceinline__ uint32_t load_key_tile(const Args& a, const CUtensorM
   uint32_t mask = __ballot_sync(0xffffffffu, bad && bx == 0);
   if (mask) {                                      // rare: from pages to groups
     uint32_t groups = 0;
+#pragma unroll 1
     for (int g = 0; g < 8; ++g) groups |= ((mask >> (g * 16 / per)) & 1u) << g;
     mask = groups;
   }
@@ -152,6 +165,33 @@ __device__ __forceinline__ uint32_t load_key_tile(const Args& a, const CUtensorM
     tma_load_4d(dst + bx * (kTile * 128) + pg * per * 128, map, bx * 64, j & ((1 << a.lps) - 1), h,
                 page, bar);
   return mask;
+}
+
+// The non-finite values of V that a row at entry `pos` sees in the tiles where they were taken
+// out of the product (those with a key that some row from `first` to `last` does not see):
+// their sum for dims [d, d + W) is added to acc.  Rare, so slow but small.
+template <typename N, int W>
+__device__ __forceinline__ void add_lost(const Args& a, const void* v_pages, int b, int h,
+                                         int tile0, int tile1, int end, int first, int last,
+                                         int pos, int d, float* acc) {
+#pragma unroll 1
+  for (int t = tile0; t < tile1; ++t) {
+    const int j0 = t * kTile, j1 = min(j0 + kTile, end);
+    bool edge = j0 + kTile - 1 > first || (a.window && j0 <= last - a.window);
+#pragma unroll 1
+    for (int j = j0; j < j1; j += 1 << a.lps) edge |= page_of(a, b, j) < 0;
+    if (!edge) continue;
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+      const int p = page_of(a, b, j);
+      if (j > pos || (a.window && j <= pos - a.window) || p < 0) continue;
+      const uint16_t* v = reinterpret_cast<const uint16_t*>(v_pages) + p * a.page_stride +
+                          (((int64_t)h << a.lps) + (j & ((1 << a.lps) - 1))) * a.D + d;
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        if ((v[e] & N::kExp) == N::kExp) acc[e] += N::to_float(v[e]);
+    }
+  }
 }
 
 // ---- matrix fragments ----------------------------------------------------------------------
@@ -176,7 +216,7 @@ struct Num;
 template <>
 struct Num<__nv_bfloat16> {
   static constexpr float kShift = 0.f;
-  static constexpr uint32_t kExp = 0x7f80u, kOne = 0x3f80u;
+  static constexpr uint32_t kExp = 0x7f80u;
   static constexpr uint32_t kMmaTypes = (1u << 7) | (1u << 10);   // A and B in an MMA descriptor
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
@@ -196,7 +236,7 @@ struct Num<__nv_bfloat16> {
 template <>
 struct Num<__half> {
   static constexpr float kShift = 7.f;
-  static constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;
+  static constexpr uint32_t kExp = 0x7c00u;
   static constexpr uint32_t kMmaTypes = 0u;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
@@ -258,7 +298,7 @@ __device__ __forceinline__ void join_row(const float* part, const float2* part_m
   float f[4], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[i] = exp2f(ml[i].x - ref);
+    f[i] = exp2_approx(ml[i].x - ref);
     sum += f[i] * ml[i].y;
   }
 #pragma unroll
@@ -268,6 +308,7 @@ __device__ __forceinline__ void join_row(const float* part, const float2* part_m
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int cnt = min(32, ns - i * 32);
+#pragma unroll 4
     for (int k = 0; k < cnt; ++k) {
       const float w = __shfl_sync(0xffffffffu, f[i], k);
       const float* src = part + (rec + i * 32 + k) * D + lane * DL;
@@ -346,7 +387,7 @@ struct AttnOut {
 };
 
 cudaError_t launch_paged_attn(const Args& a, int type, const AttnPlan& plan, const Maps& maps,
-                              const AttnOut& o, cudaStream_t s);
+                              const AttnOut& o, const void* v_pages, cudaStream_t s);
 cudaError_t launch_paged_attn_tc(const Args& a, int type, const LongPlan& plan, const Maps& maps,
                                  const AttnOut& o, const void* v_pages, cudaStream_t s);
 // Tokens of one step of rows (k_paged_mass.cu).
