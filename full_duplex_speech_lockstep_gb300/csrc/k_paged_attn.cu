@@ -58,7 +58,9 @@ struct Cfg {
 };
 
 struct Ctl {
+  UnitRing ring;
   uint64_t kfull[6], kempty[6], vfull[6], vempty[6], qfull[kQBufs], qempty[kQBufs];
+  uint64_t meet;         // of the eight warps
   uint32_t bad[6];
   int wild;              // 1 + place of the unit in which a non-finite V was taken out
   int abort;
@@ -194,6 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->qfull[i]), 1);
       mbar_init(smem_u32(&ctl->qempty[i]), kWarps);
     }
+    ring_init(ctl->ring, kWarps);
+    mbar_init(smem_u32(&ctl->meet), kWarps);
     ctl->wild = 0;
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -208,16 +212,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   });
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
 
-  Walk x(a, pre, tp, share);            // every role walks by itself from the same start
-
   if (threadIdx.x < 128) {
     // ---- producer -------------------------------------------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (threadIdx.x >= 32) return;
     uint32_t nq = 0, nk = 0, nv = 0;
-    uint32_t seen_bad = 0;
+    uint32_t seen_bad = 0, nu = 0;
+    Walk x(a, pre, tp, share);
 #pragma unroll 1
     for (; !x.done() && !*abort_flag; x.next()) {
+      put_unit(a, ctl->ring, nu++,
+               Unit{x.b, x.h, x.s.row0 + x.t0, x.nt, x.first, x.tile0, x.tile1,
+                    a.window ? max(x.first - a.window + 1, 0) : 0, x.stop, x.i, x.ns, x.at + 1},
+               lane, abort_flag);
       if (x.tile0 == x.tile1) continue;
       const int qb = nq % kQBufs;
       if (nq >= kQBufs) wait(&ctl->qempty[qb], (nq / kQBufs - 1) & 1);
@@ -247,6 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nv;
       }
     }
+    Unit last{};
+    last.b = -1;
+    put_unit(a, ctl->ring, nu, last, lane, abort_flag);
     if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
     // every copy lands before the CTA may exit (bounded waits)
     if (lane == 0) {
@@ -276,9 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tok[i] = (i * 8 + fr) / a.G;
     grp[i] = i * 8 + fr - tok[i] * a.G;
   }
-  uint32_t nq = 0, nk = 0, nv = 0;
+  uint32_t nq = 0, nk = 0, nv = 0, meets = 0;
+  Unit x;
 #pragma unroll 1
-  for (; !x.done(); x.next()) {
+  for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
     const int rows = x.nt * a.G;
     float m[2 * WR], l[2 * WR], acc[WR][D / 8][4];
 #pragma unroll
@@ -364,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return j <= p && (!a.window || j > p - a.window) && !((bad >> ((j - j0) >> 4)) & 1u);
       };
       const int j1 = j0 + warp * 16;
-      const int low = a.window ? max(x.first - a.window + 1, 0) : 0;
       uint32_t ap[WR][4];                       // P as the second product's operand
       float grow[2 * WR];
       bool grown = false;
@@ -421,14 +431,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t& w = bv[y][e];
               if ((w & N::kExp) == N::kExp) {
                 w &= 0xffff0000u;
-                seen = seen || (j >= low && j < x.stop);
+                seen = seen || (j >= x.low && j < x.stop);
               }
               if (((w >> 16) & N::kExp) == N::kExp) {
                 w &= 0xffffu;
-                seen = seen || (j + 1 >= low && j + 1 < x.stop);
+                seen = seen || (j + 1 >= x.low && j + 1 < x.stop);
               }
             }
-          if (seen) ctl->wild = x.at + 1;
+          if (seen) ctl->wild = x.tag;
         }
 #pragma unroll
         for (int y = 0; y < D / 32; ++y)
@@ -455,64 +465,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if ((lane & 3) == 0) ml[warp * R + i * 8 + fr] = make_float2(m[i], l[i]);
     }
-    named_sync(1, kWarps * 32);
-    const bool wild = *reinterpret_cast<volatile int*>(&ctl->wild) == x.at + 1;
+    sync_warps(a, &ctl->meet, meets, lane, abort_flag);
+    const bool wild = *reinterpret_cast<volatile int*>(&ctl->wild) == x.tag;
 #pragma unroll
     for (int i = 0; i < 2 * WR; ++i) {
-      if (i * 8 >= rows) break;
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * R + i * 8 + fr].x);
       // (a warp without a reference has nothing, or NaN: either passes unscaled)
       scale_rows<WR, D>(acc, i, m[i] == -INFINITY ? 1.f : exp2_approx(m[i] - top));
+    }
+    auto join_rows = [&](int i, int half) {
+      const int r0 = i * 8 + half * kJoinRows;
+      if (fr / kJoinRows == half) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r0 = i * 8 + half * kJoinRows;
-        if (r0 >= rows) break;
-        if ((fr >> 2) == half) {
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<float2*>(join + (warp * kJoinRows + (fr & 3)) * D +
-                                       ((n * 8 + fc) ^ ((fr & 3) << 3))) =
-                make_float2(acc[i >> 1][n][(i & 1) * 2], acc[i >> 1][n][(i & 1) * 2 + 1]);
-        }
-        named_sync(1, kWarps * 32);
-        const int jr = tid / (D / 2), d = tid % (D / 2) * 2, r = r0 + jr;
-        if (jr < kJoinRows && r < rows) {
-          float2 ol[kWarps];
-          float M = -INFINITY, L = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            ol[w] = ml[w * R + r];
-            M = fmaxf(M, ol[w].x);
-          }
-          float sum[2] = {0.f, 0.f};
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            L += (ol[w].x == -INFINITY ? 1.f : exp2_approx(ol[w].x - M)) * ol[w].y;
-            const float2 y =
-                *reinterpret_cast<const float2*>(join + (w * kJoinRows + jr) * D + (d ^ (jr << 3)));
-            sum[0] += y.x;
-            sum[1] += y.y;
-          }
-          const int tk = r / a.G, hd = x.h * a.G + r - tk * a.G;
-          if (wild)
-            add_lost<N, 2>(a, v_pages, x.b, x.h, x.tile0, x.tile1, x.stop, x.first,
-                           x.first + x.nt - 1, x.first + tk, d, sum);
-          if (x.ns == 1) {
-            const int64_t row = (int64_t)(x.s.row0 + x.t0 + tk) * (a.Hk * a.G) + hd;
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            *reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(o.out) + row * D + d) =
-                N::pack(sum[0] * inv, sum[1] * inv);
-            if (o.lse && d == 0) o.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-          } else {
-            const int64_t rec = (((int64_t)x.b * tp + tk) * (a.Hk * a.G) + hd) * ns_cap + x.i;
-            *reinterpret_cast<float2*>(o.part + rec * D + d) = make_float2(sum[0], sum[1]);
-            if (d == 0) o.part_ml[rec] = make_float2(M, L);
-          }
-        }
-        named_sync(1, kWarps * 32);   // the buffer, and after the last rows (m, l), may change
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(join + (warp * kJoinRows + (fr & 3)) * D +
+                                     ((n * 8 + fc) ^ ((fr & 3) << 3))) =
+              make_float2(acc[i >> 1][n][(i & 1) * 2], acc[i >> 1][n][(i & 1) * 2 + 1]);
       }
+      sync_warps(a, &ctl->meet, meets, lane, abort_flag);
+      const int jr = tid / (D / 2), d = tid % (D / 2) * 2, r = r0 + jr;
+      if (jr < kJoinRows && r < rows) {
+        float M = -INFINITY, L = 0.f, sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * R + r].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 y = ml[w * R + r];
+          L += (y.x == -INFINITY ? 1.f : exp2_approx(y.x - M)) * y.y;
+          const float2 z =
+              *reinterpret_cast<const float2*>(join + (w * kJoinRows + jr) * D + (d ^ (jr << 3)));
+          sum[0] += z.x;
+          sum[1] += z.y;
+        }
+        const int tk = r / a.G, hd = x.h * a.G + r - tk * a.G;
+        if (wild)
+          add_lost<N, 2>(a, v_pages, x.b, x.h, x.tile0, x.tile1, x.stop, x.first, x.first + x.nt - 1,
+                         x.first + tk, d, sum);
+        if (x.ns == 1) {
+          const int64_t row = (int64_t)(x.row + tk) * (a.Hk * a.G) + hd;
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          *reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(o.out) + row * D + d) =
+              N::pack(sum[0] * inv, sum[1] * inv);
+          if (o.lse && d == 0) o.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+        } else {
+          const int64_t rec = (((int64_t)x.b * tp + tk) * (a.Hk * a.G) + hd) * ns_cap + x.split;
+          *reinterpret_cast<float2*>(o.part + rec * D + d) = make_float2(sum[0], sum[1]);
+          if (d == 0) o.part_ml[rec] = make_float2(M, L);
+        }
+      }
+      // the buffer, and after the last rows (m, l), may change
+      sync_warps(a, &ctl->meet, meets, lane, abort_flag);
+    };
+#pragma unroll
+    for (int i = 0; i < 2 * WR; ++i) {
+#pragma unroll 1
+      for (int half = 0; half < 2 && i * 8 + half * kJoinRows < rows; ++half) join_rows(i, half);
     }
   }
 }

@@ -50,23 +50,16 @@ struct Cfg {
 };
 
 struct Ctl {
+  UnitRing ring;
   uint64_t full[8], empty[8];
   uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], done;
   uint64_t clean[2][2];   // [group][edge tile & 1]: the group's half of V is clean
   uint32_t bad[8];
   uint32_t tmem;
-  // 1 + the unit in which a softmax group took a non-finite value out of V.  The single query
+  // tag of the unit in which a softmax group took a non-finite value out of V.  The single query
   // buffer keeps a group at most two units ahead of the other: four entries are enough.
   int wild[2][4];
   int abort;
-};
-
-struct Unit {
-  int b, h, split, ns;
-  int row0, n, len;
-  int t0, nt;            // first token of the pair, its tokens (up to 2 tp)
-  int tile0, tile1;      // key tiles
-  int end, low;          // entries that some row of the pair sees: [low, end)
 };
 
 __device__ __forceinline__ int seq_splits(const Args& a, const Seq& s, int tp, int ns) {
@@ -83,6 +76,7 @@ __device__ __forceinline__ int seq_units(const Args& a, int b, int tp, int ns) {
 
 __device__ __forceinline__ Unit unit_of(const Args& a, const int* pre, int u, int tp, int ns) {
   Unit x;
+  x.tag = u + 1;
   x.b = find_seq(pre, a.n_seqs, u);
   const Seq s = seq_of(a, x.b);
   u -= pre[x.b];
@@ -94,15 +88,13 @@ __device__ __forceinline__ Unit unit_of(const Args& a, const int* pre, int u, in
   u %= per;
   x.h = u / x.ns;
   x.split = u - x.h * x.ns;
-  x.t0 = p * 2 * tp;
-  x.nt = min(2 * tp, s.n - x.t0);
-  x.row0 = s.row0;
-  x.n = s.n;
-  x.len = s.len;
-  const int first = s.len - s.n + x.t0;
-  x.end = max(first + x.nt, 0);
-  x.low = a.window ? min(max(first - a.window + 1, 0), x.end) : 0;
-  const int ta = x.low / kTile, tb = (x.end + kTile - 1) / kTile;
+  const int t0 = p * 2 * tp;
+  x.row = s.row0 + t0;
+  x.nt = min(2 * tp, s.n - t0);
+  x.first = s.len - s.n + t0;
+  x.stop = max(x.first + x.nt, 0);
+  x.low = a.window ? min(max(x.first - a.window + 1, 0), x.stop) : 0;
+  const int ta = x.low / kTile, tb = (x.stop + kTile - 1) / kTile;
   const int st = (tb - ta + x.ns - 1) / x.ns;
   x.tile0 = min(ta + x.split * st, tb);
   x.tile1 = min(x.tile0 + st, tb);
@@ -205,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl->clean[t][i]), 4);
       for (int i = 0; i < 4; ++i) ctl->wild[t][i] = 0;
     }
+    ring_init(ctl->ring, 9);            // the MMA issuer, eight softmax warps
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -227,10 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0) {
       // ---- producer -----------------------------------------------------------------------
-      uint32_t nq = 0, nl = 0, seen_bad = 0;
+      uint32_t nq = 0, nl = 0, nu = 0, seen_bad = 0;
 #pragma unroll 1
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
         const Unit x = unit_of(a, pre, u, tp, ns_cap);
+        put_unit(a, ctl->ring, nu++, x, lane, abort_flag);
         if (x.tile0 == x.tile1) continue;
         const int tiles = x.nt > tp ? 2 : 1;
         if (nq > 0) wait(&ctl->qempty, (nq - 1) & 1);
@@ -241,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < tiles; ++t)
             for (int bx = 0; bx < D / 64; ++bx)
               tma_load_4d(smem_u32(smem + C::kQOff + t * C::kQBytes + bx * kRowsT * 128), &mapQ,
-                          bx * 64, x.h * a.G, x.row0 + x.t0 + t * tp, 0, bar);
+                          bx * 64, x.h * a.G, x.row + t * tp, 0, bar);
         }
         ++nq;
 #pragma unroll 1
@@ -252,12 +246,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = x.tile0 + (i >> 1);
           const uint32_t bad =
               load_key_tile(a, (i & 1) ? &mapV : &mapK, smem_u32(smem + slot * C::kTileBytes),
-                            smem_u32(&ctl->full[slot]), x.b, x.h, t * kTile, x.end, lane,
+                            smem_u32(&ctl->full[slot]), x.b, x.h, t * kTile, x.stop, lane,
                             &ctl->bad[slot]);
           seen_bad |= bad;
           ++nl;
         }
       }
+      Unit none{};
+      none.b = -1;
+      put_unit(a, ctl->ring, nu, none, lane, abort_flag);
       if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
       // every copy lands before the CTA may exit (bounded waits)
       if (lane == 0) {
@@ -302,9 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     acc || kk > 0);
           }
         };
+        Unit x;
 #pragma unroll 1
-        for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
-          const Unit x = unit_of(a, pre, u, tp, ns_cap);
+        for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, true, abort_flag); ++nu) {
           const int nt = x.tile1 - x.tile0;
           if (nt == 0) continue;
           const int tiles = x.nt > tp ? 2 : 1;
@@ -373,16 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = lane_base + t * kTile, o_at = lane_base + 2 * kTile + t * D;
     const uint64_t c2 = f32x2(a.c, a.c);
     uint32_t ns_ = 0, no = 0, nl = 0, ne = 0, nu = 0;
+    Unit x;
 #pragma unroll 1
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++nu) {
-      const Unit x = unit_of(a, pre, u, tp, ns_cap);
+    for (; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
       const int nt = x.tile1 - x.tile0;
       const int tiles = x.nt > tp ? 2 : 1;
       if (t >= tiles) {        // a pair of one tile: nothing to do here but count
         nl += 2 * nt;
         continue;
       }
-      const int first = x.len - x.n + x.t0;
+      const int first = x.first;
       const int tokens = min(tp, x.nt - t * tp);
       const int tk = min(r / a.G, tokens - 1);
       const int pos = first + t * tp + tk;
@@ -412,10 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                              finite_only<N>(w.w);
             if (hit) {
               *at = w;
-              found = found || (j0 + row >= x.low && j0 + row < x.end);
+              found = found || (j0 + row >= x.low && j0 + row < x.stop);
             }
           }
-          if (found) ctl->wild[t][nu & 3] = u + 1;
+          if (found) ctl->wild[t][nu & 3] = x.tag;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (tiles == 2) {    // both halves, before either product
             __syncwarp();
@@ -501,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the rows' results, or the split's partials --------------------------------------
       const int H = a.Hk * a.G;
-      const int token = x.t0 + t * tp + tk, hd = x.h * a.G + r - tk * a.G;
-      const int64_t row = (int64_t)(x.row0 + token) * H + hd;
+      const int token = x.row + t * tp + tk, hd = x.h * a.G + r - tk * a.G;
+      const int64_t row = (int64_t)token * H + hd;
       const int64_t rec = row * ns_cap + x.split;
       const bool whole = x.ns == 1;
       bool wild = false;
@@ -510,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&ctl->ofull[t], no & 1);
         ++no;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        wild = *reinterpret_cast<volatile int*>(&ctl->wild[0][nu & 3]) == u + 1 ||
-               *reinterpret_cast<volatile int*>(&ctl->wild[1][nu & 3]) == u + 1;
+        wild = *reinterpret_cast<volatile int*>(&ctl->wild[0][nu & 3]) == x.tag ||
+               *reinterpret_cast<volatile int*>(&ctl->wild[1][nu & 3]) == x.tag;
       }
       const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll 1
@@ -529,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (wild && live) {
           // rare (their weights are positive)
           float add[32] = {};
-          add_lost<N, 32>(a, v_pages, x.b, x.h, x.tile0, x.tile1, x.end, first, first + x.nt - 1,
+          add_lost<N, 32>(a, v_pages, x.b, x.h, x.tile0, x.tile1, x.stop, first, first + x.nt - 1,
                           pos, i * 32, add);
 #pragma unroll
           for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) + add[e]);

@@ -9,12 +9,11 @@
 // no sum crosses threads but one (two groups take alternate steps), nothing is added
 // atomically, and the bits are the same in every run.
 //
-// A CTA takes a run of consecutive units of about the same number of steps as the others,
-// and each of its roles walks the run by itself:
+// A CTA takes a run of consecutive units of about the same number of steps as the others:
 //   warp 0        producer: the key tile, then the steps' rows, by TMA
 //   warp 1        one thread issues the MMAs, up to four steps ahead of the sums
-//   warp 2        each key's old mass and page, four units at a time (their loads overlap)
-//   warp 3        each row's lse, four steps at a time; rows that do not count: infinity
+//   warp 2        each key's old mass and page, a unit ahead
+//   warp 3        each row's lse, a step ahead; rows that do not count: infinity
 //   warps 4-7, 8-11   the sums, the two groups in turn to a step
 #include <type_traits>
 
@@ -32,10 +31,11 @@ constexpr int kMaxStages = 8;
 constexpr int kQStages = 3;
 
 struct Ctl {
+  UnitRing ring;
   uint64_t kfull[kMaxStages], kempty[kMaxStages], qfull[kQStages], qempty[kQStages];
   uint64_t sfull[kBufs], sfree[kBufs];
   uint64_t lfull[kAux], lempty[kAux], ufull[kAux], uempty[kAux];
-  uint64_t done;
+  uint64_t done, meet;
   uint32_t tmem;
   int abort;
   alignas(16) float ref[kAux][kTile];   // lse * log2(e) of a step's rows
@@ -191,6 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->uempty[i]), 4);
     }
     mbar_init(smem_u32(&ctl->done), 1);
+    ring_init(ctl->ring, 11);            // MMA issuer, two memory warps, eight of sums
+    mbar_init(smem_u32(&ctl->meet), 8);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -212,16 +214,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = ctl->tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
-  // A unit that no row sees has nothing to add; without decay it is left out.
-  auto skip = [&](const Walk& x) { return x.t0 == x.t1 && decay == 1.f; };
-
-  Walk x(a, pre, tp);                   // every role walks by itself from the same start
-
   if (warp == 0) {
     // ---- producer -------------------------------------------------------------------------
-    uint32_t nk = 0, nq = 0, seen_bad = 0;
+    uint32_t nk = 0, nq = 0, nu = 0, seen_bad = 0;
+    Walk x(a, pre, tp);
 #pragma unroll 1
     for (; !x.done() && !*abort_flag; x.next()) {
+      // a unit that no row sees has nothing to add; without decay it is left out
+      if (x.t0 == x.t1 && decay == 1.f) continue;
+      put_unit(a, ctl->ring, nu++,
+               Unit{x.b, x.h, x.s.row0 + x.t0, x.t1 - x.t0, x.s.len - x.s.n + x.t0, x.tile,
+                    x.tile + 1, 0, x.s.len, 0, 1, 0},
+               lane, abort_flag);
       if (x.t0 == x.t1) continue;
       const int ks = nk % KS;
       if (nk >= KS) wait(&ctl->kempty[ks], (nk / KS - 1) & 1);
@@ -244,6 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nq;
       }
     }
+    Unit last{};
+    last.b = -1;
+    put_unit(a, ctl->ring, nu, last, lane, abort_flag);
     if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
     if (lane == 0) {   // every copy lands before the CTA may exit (bounded waits)
 #pragma unroll 1
@@ -260,15 +267,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id = (1u << 4) | Num<T>::kMmaTypes | ((uint32_t)(kTile >> 4) << 24) |
                           ((uint32_t)(N_ >> 3) << 17);
       uint32_t nk = 0, nq = 0;
+      Unit x;
 #pragma unroll 1
-      for (; !x.done() && !*abort_flag; x.next()) {
-        if (x.t0 == x.t1) continue;
+      for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, true, abort_flag); ++nu) {
+        if (x.nt == 0) continue;
         const int ks = nk % KS;
         wait(&ctl->kfull[ks], (nk / KS) & 1);
         ++nk;
         const uint32_t kb = smem_u32(smem + ks * kTileBytes);
 #pragma unroll 1
-        for (int t = x.t0; t < x.t1; t += tp) {
+        for (int t = 0; t < x.nt; t += tp) {
           const int qs = nq % kQStages, bb = nq % kBufs;
           wait(&ctl->qfull[qs], (nq / kQStages) & 1);
           if (nq >= kBufs) wait(&ctl->sfree[bb], (nq / kBufs - 1) & 1);
@@ -292,44 +300,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    // ---- old mass and pages: four keys to a lane, four units at a time
-    uint32_t nu = 0;
+    // ---- old mass and pages: four keys to a lane; a unit's loads are issued before the last
+    // unit's values are handed on
+    Unit x;
+    float old[4] = {};
+    int page = -1;
+    bool have = false;
 #pragma unroll 1
-    while (!x.done() && !*abort_flag) {
-      float old[4][4];
-      int page[4], n = 0;
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        while (!x.done() && skip(x)) x.next();
-        if (!x.done()) {
-          const int j = x.j0 + lane * 4;               // one page: 4 divides the page size
-          const int p = j < x.s.len ? page_of(a, x.b, j) : -1;
-          page[y] = p;
+    for (uint32_t nu = 0;; ++nu) {
+      float next[4] = {};
+      int next_page = -1;
+      const bool more = get_unit(a, ctl->ring, nu, x, lane, false, abort_flag);
+      if (more) {
+        const int j = x.tile0 * kTile + lane * 4;        // one page: 4 divides the page size
+        next_page = j < x.stop ? page_of(a, x.b, j) : -1;
+        if (next_page >= 0 && decay != 0.f) {
           const float* src =
-              mass + ((((int64_t)p * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1)));
+              mass + ((((int64_t)next_page * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1)));
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            old[y][k] = p >= 0 && j + k < x.s.len && decay != 0.f ? src[k] * decay : 0.f;
-          n = y + 1;
-          x.next();
+            if (j + k < x.stop) next[k] = src[k];
         }
       }
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        if (y >= n) break;
-        const int us = nu % kAux;
-        if (nu >= kAux) wait(&ctl->uempty[us], (nu / kAux - 1) & 1);
-        if (*abort_flag) break;
+      if (have) {
+        const uint32_t n = nu - 1, us = n % kAux;
+        if (n >= kAux) wait(&ctl->uempty[us], (n / kAux - 1) & 1);
         *reinterpret_cast<float4*>(&ctl->old[us][lane * 4]) =
-            make_float4(old[y][0], old[y][1], old[y][2], old[y][3]);
-        if ((lane & 3) == 0) ctl->page[us][lane >> 2] = page[y];
+            make_float4(old[0] * decay, old[1] * decay, old[2] * decay, old[3] * decay);
+        if ((lane & 3) == 0) ctl->page[us][lane >> 2] = page;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->ufull[us]));
-        ++nu;
       }
+      if (!more) break;
+      have = true;
+      page = next_page;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) old[k] = next[k];
     }
   } else if (warp == 3) {
-    // ---- lse: four rows to a lane, four steps at a time
+    // ---- lse: four rows to a lane; a step's loads are issued before the last step's are handed on
     const int H = a.Hk * a.G;
     int tk[4], gh[4];                                   // a lane's rows: token and head of a step
 #pragma unroll
@@ -337,68 +346,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       tk[k] = (lane + k * 32) / a.G;
       gh[k] = lane + k * 32 - tk[k] * a.G;
     }
+    Unit x;
+    float z[4] = {};
     uint32_t nl = 0;
-    int t = x.done() ? 0 : x.t0;
-    while (!x.done() && !*abort_flag) {
-      float z[4][4];
-      int n = 0;
+    bool have = false;
+    auto hand_on = [&](uint32_t n) {
+      const int ls = n % kAux;
+      if (n >= kAux) wait(&ctl->lempty[ls], (n / kAux - 1) & 1);
+      // rows that are not there, or that saw nothing, give nothing
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        while (!x.done() && t >= x.t1) {
-          x.next();
-          if (!x.done()) t = x.t0;
-        }
-        if (!x.done()) {
-          const int nt = min(tp, x.t1 - t);
+      for (int k = 0; k < 4; ++k)
+        ctl->ref[ls][lane + k * 32] = z[k] == -INFINITY ? INFINITY : z[k] * kLog2e;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->lfull[ls]));
+    };
+#pragma unroll 1
+    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+#pragma unroll 1
+      for (int t = 0; t < x.nt && !*abort_flag; t += tp, ++nl) {
+        const int nt = min(tp, x.nt - t);
+        float next[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // rows that are not there, or that saw nothing, give nothing
-            float v = -INFINITY;
-            if (tk[k] < nt) v = lse[(int64_t)(x.s.row0 + t + tk[k]) * H + x.h * a.G + gh[k]];
-            z[y][k] = v == -INFINITY ? INFINITY : v * kLog2e;
-          }
-          n = y + 1;
-          t += tp;
-        }
+        for (int k = 0; k < 4; ++k)
+          next[k] = tk[k] < nt ? lse[(int64_t)(x.row + t + tk[k]) * H + x.h * a.G + gh[k]]
+                               : -INFINITY;
+        if (have) hand_on(nl - 1);
+        have = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = next[k];
       }
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        if (y >= n) break;
-        const int ls = nl % kAux;
-        if (nl >= kAux) wait(&ctl->lempty[ls], (nl / kAux - 1) & 1);
-        if (*abort_flag) break;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ctl->ref[ls][lane + k * 32] = z[y][k];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->lfull[ls]));
-        ++nl;
-      }
+      // the last step of a unit is handed on at once: the next unit may be far off
+      if (have) hand_on(nl - 1);
+      have = false;
     }
   } else {
     // ---- sums: a thread to a key, the two groups in turn to a step --------------------------
     const int g = (warp - 4) >> 2, key = threadIdx.x - 128 - g * 128;
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint64_t c2 = f32x2(a.c, a.c);
-    uint32_t nl = 0, nu = 0, nm = 0;
+    uint32_t nl = 0, nu = 0, nm = 0, meets = 0;
+    Unit x;
 #pragma unroll 1
-    for (; !x.done(); x.next()) {
-      if (skip(x)) continue;
-      const int first = x.s.len - x.s.n, j = x.j0 + key;
-      const int steps = (x.t1 - x.t0 + tp - 1) / tp;
+    for (; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+      const int j0 = x.tile0 * kTile, j = j0 + key;
+      const int steps = (x.nt + tp - 1) / tp;
       float sum = 0.f;
-      int t = x.t0;
+      int t = 0;
 #pragma unroll 1
       for (int i = 0; i < steps; ++i, ++nl, t += tp) {
         if ((nl & 1) != g) continue;
         const int bb = nl % kBufs, ls = nl % kAux;
-        const int nt = min(tp, x.t1 - t), cols = nt * a.G;
+        const int nt = min(tp, x.nt - t), cols = nt * a.G, first = x.first + t;
         // the rows of the step that see this key: columns [lo, hi)
         int lo = 0, hi = cols;
-        const bool edge = (cols & 15) || x.j0 + kTile - 1 > first + t ||
-                          (a.window && x.j0 <= first + t + nt - 1 - a.window);
+        const bool edge = (cols & 15) || j0 + kTile - 1 > first ||
+                          (a.window && j0 <= first + nt - 1 - a.window);
         if (edge) {
-          lo = max(0, j - first - t) * a.G;
-          if (a.window) hi = (int)min((int64_t)hi, ((int64_t)j + a.window - first - t) * a.G);
+          lo = max(0, j - first) * a.G;
+          if (a.window) hi = (int)min((int64_t)hi, ((int64_t)j + a.window - first) * a.G);
         }
         wait(&ctl->lfull[ls], (nl / kAux) & 1);
         wait(&ctl->sfull[bb], (nl / kBufs) & 1);
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int writer = steps > 0 ? (nl - 1) & 1 : nu & 1;
       if (steps > 1) {
         if (g != writer) ctl->half[nm & 1][key] = sum;
-        named_sync(1, 256);
+        sync_warps(a, &ctl->meet, meets, lane, abort_flag);
         if (g == writer) sum += ctl->half[nm & 1][key];
         ++nm;
       }
@@ -428,12 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&ctl->ufull[us], (nu / kAux) & 1);
         const int p = ctl->page[us][key >> 4];
         sum += ctl->old[us][key];
-        if (p >= 0 && j < x.s.len)
+        if (p >= 0 && j < x.stop)
           mass[(((int64_t)p * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1))] = sum;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
       }
-      ++nu;
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

@@ -122,6 +122,62 @@ __device__ __forceinline__ int find_seq(const I* pre, int n, I u) {
   return lo;
 }
 
+// ---- units ----------------------------------------------------------------------------------
+// The producer warp works out a CTA's units and tells the other roles through a ring in shared
+// memory: the others spend no instructions (and no instruction cache) on it.
+struct alignas(16) Unit {
+  int b, h;              // sequence (-1: no more units), key head
+  int row, nt;           // first row of the unit's tokens, how many
+  int first;             // entry index of that token (of the sequence's first one: k_paged_mass)
+  int tile0, tile1;      // key tiles
+  int low, stop;         // entries that some row sees lie in [low, stop)
+  int split, ns;         // split of the keys, of how many
+  int tag;               // 1 + the unit's place in this CTA's run
+};
+static_assert(sizeof(Unit) == 48, "three 16-byte words");
+constexpr int kUnits = 8;
+struct UnitRing {
+  Unit unit[kUnits];
+  uint64_t full[kUnits], empty[kUnits];
+};
+
+__device__ __forceinline__ void ring_init(UnitRing& r, int readers) {
+  for (int i = 0; i < kUnits; ++i) {
+    mbar_init(smem_u32(&r.full[i]), 1);
+    mbar_init(smem_u32(&r.empty[i]), readers);
+  }
+}
+// By the producer warp: the k-th unit.
+__device__ __forceinline__ void put_unit(const Args& a, UnitRing& r, uint32_t k, const Unit& x,
+                                         int lane, volatile int* abort_flag) {
+  const int i = k % kUnits;
+  if (k >= kUnits) wait_phase(a, &r.empty[i], (k / kUnits - 1) & 1, abort_flag);
+  if (lane == 0) {
+    r.unit[i] = x;
+    mbar_arrive(smem_u32(&r.full[i]));
+  }
+}
+// By each reader (a warp, or one thread of it with `alone`): the k-th unit, false after the
+// last one or when the CTA gives up.
+__device__ __forceinline__ bool get_unit(const Args& a, UnitRing& r, uint32_t k, Unit& x, int lane,
+                                         bool alone, volatile int* abort_flag) {
+  const int i = k % kUnits;
+  wait_phase(a, &r.full[i], (k / kUnits) & 1, abort_flag);
+  x = r.unit[i];
+  if (!alone) __syncwarp();
+  if (alone || lane == 0) mbar_arrive(smem_u32(&r.empty[i]));
+  return x.b >= 0 && !*abort_flag;
+}
+
+// Bounded barrier of `count` warps on an mbarrier initialised with that count.
+__device__ __forceinline__ void sync_warps(const Args& a, uint64_t* bar, uint32_t& phase, int lane,
+                                           volatile int* abort_flag) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(bar));
+  wait_phase(a, bar, phase & 1, abort_flag);
+  ++phase;
+}
+
 // ---- shared-memory tiles -----------------------------------------------------------------
 // A tile of R rows of D 16-bit values is D/64 boxes of R rows x 128 bytes, each in the
 // 128-byte swizzle: 16-byte chunk c of row r sits at chunk c ^ (r & 7).
@@ -171,7 +227,7 @@ __device__ __forceinline__ uint32_t load_key_tile(const Args& a, const CUtensorM
 // out of the product (those with a key that some row from `first` to `last` does not see):
 // their sum for dims [d, d + W) is added to acc.  Rare, so slow but small.
 template <typename N, int W>
-__device__ __forceinline__ void add_lost(const Args& a, const void* v_pages, int b, int h,
+__device__ __noinline__ void add_lost(const Args& a, const void* v_pages, int b, int h,
                                          int tile0, int tile1, int end, int first, int last,
                                          int pos, int d, float* acc) {
 #pragma unroll 1
