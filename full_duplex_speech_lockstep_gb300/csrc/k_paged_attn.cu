@@ -14,9 +14,9 @@
 // head counts only, so its bits do not depend on the rest of the batch.
 //
 //   warp 0      producer: query rows, K and V tiles by TMA, one box to a lane;
-//   warps 4-11  warp 4 + w takes keys 16w .. 16w+15 of every tile, all rows: S and P V as 16 x 8 x 16
-//               matrix products, P handed from one to the other in registers, with the
-//               warp's own m, l and O (16 * WR rows x D in fp32 registers).
+//   warps 4-11  in two teams of four, a team to every second tile, a warp to 32 keys of it, all
+//               rows: S and P V as 16 x 8 x 16 matrix products, P handed from one to the other in
+//               registers, with the warp's own m, l and O (16 * WR rows x D in fp32 registers).
 //
 // The warps meet only at a unit's end, where the eight (m, l, O) are joined through shared
 // memory.  (A tile shared by all warps, with the maxima and P exchanged under two barriers a
@@ -286,7 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tok[i] = (i * 8 + fr) / a.G;
     grp[i] = i * 8 + fr - tok[i] * a.G;
   }
-  uint32_t nq = 0, nk = 0, nv = 0, meets = 0;
+  const int team = warp >> 2, part = warp & 3;   // whose tiles, which of their keys
+  constexpr int kAhead = WR == 1 ? 4 : 2;
+  uint32_t nq = 0, n = 0, meets = 0;            // n: tiles of this CTA
   Unit x;
 #pragma unroll 1
   for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
@@ -314,82 +316,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         ldsm4(tile_addr(qbuf, R * 128, (lm & 1) * 8 + lr, kk * 2 + (lm >> 1)), aq[kk]);
     }
 #pragma unroll 1
-    for (int t = x.tile0; t < x.tile1; ++t) {
-      const int j0 = t * kTile;
-      // ---- S = Q K^T: this warp's 16 keys, every row
-      const int ks = nk % C::KS;
+    for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+      const int ks = n % C::KS, vs = n % C::VS;
+      wait(&ctl->kfull[ks], (n / C::KS) & 1);
+      if ((n & 1) != team) {
+        // the other team's tile: every warp sees every phase of every stage all the same (a
+        // phase that passed unseen could not be told from the one before it)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->kempty[ks]));
+        wait(&ctl->vfull[vs], (n / C::VS) & 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->vempty[vs]));
+        continue;
+      }
+      const int j1 = t * kTile + part * 32;     // this warp's first key
+      // ---- S = Q K^T: this warp's 32 keys, every row
       const uint32_t kbuf = smem_u32(smem + ks * C::kTileBytes);
-      wait(&ctl->kfull[ks], (nk / C::KS) & 1);
-      float s[WR][2][4];
+      float s[WR][4][4];
 #pragma unroll
       for (int i = 0; i < WR; ++i)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
-      auto load_k = [&](int kk, uint32_t r[4]) {
-        ldsm4(tile_addr(kbuf, kTile * 128, warp * 16 + (lm >> 1) * 8 + lr, kk * 2 + (lm & 1)), r);
-      };
-      if constexpr (WR == 1) {
-        uint32_t bk[D / 16][4];
+          for (int e = 0; e < 4; ++e) s[i][y][e] = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) load_k(kk, bk[kk]);
+      for (int k0 = 0; k0 < D / 16; k0 += kAhead) {   // kAhead steps' loads go out together
+        uint32_t bk[kAhead][2][4], q[WR == 1 ? 1 : kAhead][WR][4];
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          N::mma(s[0][0], aq[kk], bk[kk][0], bk[kk][1]);
-          N::mma(s[0][1], aq[kk], bk[kk][2], bk[kk][3]);
-        }
-      } else {                                  // one step's fragments ahead
-        uint32_t bk[2][4], q[2][WR][4];
-        auto load = [&](int kk) {
-          load_k(kk, bk[kk & 1]);
+        for (int k = 0; k < kAhead; ++k) {
 #pragma unroll
-          for (int i = 0; i < WR; ++i)
-            ldsm4(tile_addr(qbuf, R * 128, i * 16 + (lm & 1) * 8 + lr, kk * 2 + (lm >> 1)),
-                  q[kk & 1][i]);
-        };
-        load(0);
+          for (int y = 0; y < 2; ++y)
+            ldsm4(tile_addr(kbuf, kTile * 128, part * 32 + y * 16 + (lm >> 1) * 8 + lr,
+                            (k0 + k) * 2 + (lm & 1)), bk[k][y]);
+          if constexpr (WR > 1) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          if (kk + 1 < D / 16) load(kk + 1);
-#pragma unroll
-          for (int i = 0; i < WR; ++i) {
-            N::mma(s[i][0], q[kk & 1][i], bk[kk & 1][0], bk[kk & 1][1]);
-            N::mma(s[i][1], q[kk & 1][i], bk[kk & 1][2], bk[kk & 1][3]);
+            for (int i = 0; i < WR; ++i)
+              ldsm4(tile_addr(qbuf, R * 128, i * 16 + (lm & 1) * 8 + lr, (k0 + k) * 2 + (lm >> 1)),
+                    q[k][i]);
           }
         }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+          for (int i = 0; i < WR; ++i)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              N::mma(s[i][y], WR == 1 ? aq[k0 + k] : q[k][i], bk[k][y >> 1][(y & 1) * 2],
+                     bk[k][y >> 1][(y & 1) * 2 + 1]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->kempty[ks]));
-      ++nk;
       // which parts of the tile have no page comes with its V tile
-      const int vs = nv % C::VS;
       const uint32_t vbuf = smem_u32(smem + C::kVOff + vs * C::kTileBytes);
-      wait(&ctl->vfull[vs], (nv / C::VS) & 1);
+      wait(&ctl->vfull[vs], (n / C::VS) & 1);
       const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&ctl->bad[vs]);
       // does every row see every key of the tile?
-      const bool edge = bad != 0 || j0 + kTile - 1 > x.first ||
-                        (a.window && j0 <= x.first + x.nt - 1 - a.window);
-      auto sees = [&](int i, int j) {
-        const int p = x.first + min(tok[i], x.nt - 1);
-        return j <= p && (!a.window || j > p - a.window) && !((bad >> ((j - j0) >> 4)) & 1u);
-      };
-      const int j1 = j0 + warp * 16;
-      uint32_t ap[WR][4];                       // P as the second product's operand
+      const bool edge = bad != 0 || (t + 1) * kTile - 1 > x.first ||
+                        (a.window && t * kTile <= x.first + x.nt - 1 - a.window);
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 2 * WR; ++i) {
+          // the row sees keys (lo, hi], counted from this thread's first
+          const int hi = x.first + min(tok[i], x.nt - 1) - j1 - fc;
+          const int lo = a.window ? hi - a.window : -1;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const bool none = (bad >> (part * 2 + (y >> 1))) & 1u;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (none || y * 8 + e > hi || y * 8 + e <= lo)
+                s[i >> 1][y][(i & 1) * 2 + e] = -INFINITY;
+          }
+        }
+      }
+      uint32_t ap[WR][2][4];                    // P as the second product's operand
       float grow[2 * WR];
       bool grown = false;
 #pragma unroll
       for (int i = 0; i < 2 * WR; ++i) {
-        float* v0 = &s[i >> 1][0][(i & 1) * 2];
-        float* v1 = &s[i >> 1][1][(i & 1) * 2];
-        if (edge) {
+        float p[4][2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (!sees(i, j1 + fc + e)) v0[e] = -INFINITY;
-            if (!sees(i, j1 + 8 + fc + e)) v1[e] = -INFINITY;
-          }
-        }
-        float top = fmaxf(fmaxf(v0[0], v0[1]), fmaxf(v1[0], v1[1]));
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) p[y][e] = s[i >> 1][y][(i & 1) * 2 + e];
+        float top = fmaxf(fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[1][0], p[1][1])),
+                          fmaxf(fmaxf(p[2][0], p[2][1]), fmaxf(p[3][0], p[3][1])));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = fmaf(top, a.c, -N::kShift);
@@ -399,58 +410,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         grown = grown || mn != m[i];
         m[i] = mn;
         const float ref = mn == -INFINITY ? 0.f : -mn;
-        const float p0 = exp2_approx(fmaf(v0[0], a.c, ref)), p1 = exp2_approx(fmaf(v0[1], a.c, ref));
-        const float p2 = exp2_approx(fmaf(v1[0], a.c, ref)), p3 = exp2_approx(fmaf(v1[1], a.c, ref));
-        l[i] = fmaf(l[i], grow[i], (p0 + p1) + (p2 + p3));
-        ap[i >> 1][i & 1] = N::pack(p0, p1);
-        ap[i >> 1][2 + (i & 1)] = N::pack(p2, p3);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) p[y][e] = exp2_approx(fmaf(p[y][e], a.c, ref));
+        l[i] = fmaf(l[i], grow[i], ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1])) +
+                                       ((p[2][0] + p[2][1]) + (p[3][0] + p[3][1])));
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          ap[i >> 1][y >> 1][(y & 1) * 2 + (i & 1)] = N::pack(p[y][0], p[y][1]);
       }
       // ---- O = diag(grow) O + P V
       if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-        for (int i = 0; i < WR; ++i)
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][n][e] *= grow[i * 2 + (e >> 1)];
+        for (int i = 0; i < 2 * WR; ++i) scale_rows<WR, D>(acc, i, grow[i]);
       }
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {     // loads of half the dims go out together
-        uint32_t bv[D / 32][4];
+      for (int y = 0; y < 2; ++y) {             // 16 keys
+        constexpr int B = WR == 1 ? D / 16 : 4;   // 16-dim blocks whose loads go out together
 #pragma unroll
-        for (int y = 0; y < D / 32; ++y)
-          ldsm4_t(tile_addr(vbuf, kTile * 128, warp * 16 + (lm & 1) * 8 + lr,
-                            half * (D / 16) + y * 2 + (lm >> 1)), bv[y]);
-        if (edge) {
-          bool seen = false;     // of an entry that some row sees
+        for (int b0 = 0; b0 < D / 16; b0 += B) {
+          uint32_t bv[B][4];
 #pragma unroll
-          for (int y = 0; y < D / 32; ++y)
+          for (int k = 0; k < B; ++k)
+            ldsm4_t(tile_addr(vbuf, kTile * 128, part * 32 + y * 16 + (lm & 1) * 8 + lr,
+                              (b0 + k) * 2 + (lm >> 1)), bv[k]);
+          if (edge) {
+            uint32_t z = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = j1 + (e & 1) * 8 + fc;
-              uint32_t& w = bv[y][e];
-              if ((w & N::kExp) == N::kExp) {
-                w &= 0xffff0000u;
-                seen = seen || (j >= x.low && j < x.stop);
-              }
-              if (((w >> 16) & N::kExp) == N::kExp) {
-                w &= 0xffffu;
-                seen = seen || (j + 1 >= x.low && j + 1 < x.stop);
-              }
+            for (int k = 0; k < B; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) N::probe(z, bv[k][e]);
+            if (z & 0x7fff7fffu) {              // rare: a non-finite value
+#pragma unroll
+              for (int k = 0; k < B; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int j = j1 + y * 16 + (e & 1) * 8 + fc;
+                  uint32_t& w = bv[k][e];
+                  if ((w & N::kExp) == N::kExp) {
+                    w &= 0xffff0000u;
+                    if (j >= x.low && j < x.stop) ctl->wild = x.tag;
+                  }
+                  if (((w >> 16) & N::kExp) == N::kExp) {
+                    w &= 0xffffu;
+                    if (j + 1 >= x.low && j + 1 < x.stop) ctl->wild = x.tag;
+                  }
+                }
             }
-          if (seen) ctl->wild = x.tag;
-        }
-#pragma unroll
-        for (int y = 0; y < D / 32; ++y)
-#pragma unroll
-          for (int i = 0; i < WR; ++i) {
-            N::mma(acc[i][half * (D / 16) + y * 2], ap[i], bv[y][0], bv[y][1]);
-            N::mma(acc[i][half * (D / 16) + y * 2 + 1], ap[i], bv[y][2], bv[y][3]);
+            __syncwarp();
           }
+#pragma unroll
+          for (int k = 0; k < B; ++k)
+#pragma unroll
+            for (int i = 0; i < WR; ++i) {
+              N::mma(acc[i][(b0 + k) * 2], ap[i][y], bv[k][0], bv[k][1]);
+              N::mma(acc[i][(b0 + k) * 2 + 1], ap[i][y], bv[k][2], bv[k][3]);
+            }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->vempty[vs]));
-      ++nv;
     }
     if (x.tile0 < x.tile1) {
       __syncwarp();
@@ -470,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 2 * WR; ++i) {
       float top = -INFINITY;
-#pragma unroll
+#pragma unroll 4
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * R + i * 8 + fr].x);
       // (a warp without a reference has nothing, or NaN: either passes unscaled)
       scale_rows<WR, D>(acc, i, m[i] == -INFINITY ? 1.f : exp2_approx(m[i] - top));
@@ -488,9 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int jr = tid / (D / 2), d = tid % (D / 2) * 2, r = r0 + jr;
       if (jr < kJoinRows && r < rows) {
         float M = -INFINITY, L = 0.f, sum[2] = {0.f, 0.f};
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * R + r].x);
-#pragma unroll
+#pragma unroll 2
         for (int w = 0; w < kWarps; ++w) {
           const float2 y = ml[w * R + r];
           L += (y.x == -INFINITY ? 1.f : exp2_approx(y.x - M)) * y.y;

@@ -391,6 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // does some row of the pair not see some key?
         const int last = first + x.nt - 1;
         const uint32_t vslot = (nl + 2 * j + 1) % kSlots;
+        // S first: it comes after everything that earlier units loaded, so the phase of V's slot
+        // can then be no earlier one, although this group may have passed over whole units
+        wait(&ctl->sfull[t], ns_ & 1);
+        ++ns_;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         wait(&ctl->full[vslot], ((nl + 2 * j + 1) / kSlots) & 1);
         const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&ctl->bad[vslot]);
         const bool edge = bad || j0 + kTile - 1 > first || (a.window && j0 <= last - a.window);
@@ -421,9 +426,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++ne;
           }
         }
-        wait(&ctl->sfull[t], ns_ & 1);
-        ++ns_;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         auto weights = [&](auto masked) {
           uint32_t s[kTile];
 #pragma unroll

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->lfull[i]), 1);
       mbar_init(smem_u32(&ctl->lempty[i]), 4);
       mbar_init(smem_u32(&ctl->ufull[i]), 1);
-      mbar_init(smem_u32(&ctl->uempty[i]), 4);
+      mbar_init(smem_u32(&ctl->uempty[i]), 8);
     }
     mbar_init(smem_u32(&ctl->done), 1);
     ring_init(ctl->ring, 11);            // MMA issuer, two memory warps, eight of sums
@@ -428,16 +428,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (g == writer) sum += ctl->half[nm & 1][key];
         ++nm;
       }
+      // (both groups see every phase of the old values' stages)
+      const int us = nu % kAux;
+      wait(&ctl->ufull[us], (nu / kAux) & 1);
       if (g == writer) {
-        const int us = nu % kAux;
-        wait(&ctl->ufull[us], (nu / kAux) & 1);
         const int p = ctl->page[us][key >> 4];
         sum += ctl->old[us][key];
         if (p >= 0 && j < x.stop)
           mass[(((int64_t)p * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1))] = sum;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

@@ -280,6 +280,10 @@ struct Num<__nv_bfloat16> {
     return r;
   }
   static __device__ __forceinline__ float to_float(uint32_t h) { return __uint_as_float(h << 16); }
+  // z += 0 * w: stays zero while every w is finite
+  static __device__ __forceinline__ void probe(uint32_t& z, uint32_t w) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(w), "r"(0));
+  }
   static __device__ __forceinline__ void mma(float d[4], const uint32_t a[4], uint32_t b0,
                                              uint32_t b1) {
     asm volatile(
@@ -298,6 +302,9 @@ struct Num<__half> {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+  }
+  static __device__ __forceinline__ void probe(uint32_t& z, uint32_t w) {
+    asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(w), "r"(0));
   }
   static __device__ __forceinline__ float to_float(uint32_t h) {
     return __half2float(__ushort_as_half((unsigned short)h));
