@@ -94,7 +94,8 @@ struct Walk {
   int at, end;           // tiles before this unit, tiles where the run ends
   int b, h, i;           // sequence, key head, unit of the head
   Seq s;
-  int rt, st, ns, per, cost;   // row tiles, tiles of a split, splits, units of a head, their cost
+  int rt, st, ns, per;   // row tiles, tiles of a split, splits, units of a head
+  int cost, head;        // tiles of a unit but the last, of a head
   int t0, nt;            // first token of the row tile, its tokens
   int first;             // entry index of that token
   int tile0, tile1;      // key tiles of the split
@@ -108,27 +109,32 @@ struct Walk {
     if (at >= end) return;
     b = find_seq(pre, a.n_seqs, at);
     sequence();
-    const int k = (at - pre[b] + cost - 1) / cost;   // the first unit that starts in the run
-    h = k / per;
-    i = k - h * per;
-    at = pre[b] + k * cost;
+    // the first unit that starts in the run
+    h = (at - pre[b]) / head;
+    i = (at - pre[b] - h * head + cost - 1) / cost;
+    if (i == per) {
+      i = 0;
+      ++h;
+    }
+    at = pre[b] + h * head + i * cost;
     if (h == a.Hk) next_sequence();
     unit();
   }
   __device__ __forceinline__ bool done() const { return at >= end; }
-  // Units of a sequence: rt row tiles (each a unit), or the splits of its only one.
-  static __device__ __forceinline__ int units(const Args& a, const Seq& s, int tp, int share,
-                                              int& rt, int& st, int& ns, int& cost) {
-    rt = (s.n + tp - 1) / tp;
-    const int mt = max_tiles(a, s.len, tp);
-    st = split_tiles(mt, share);
-    ns = rt > 1 ? 1 : n_splits(mt, share);
-    cost = rt > 1 ? 1 : st;
-    return rt > 1 ? rt : ns;
+  // Tiles of one head: those of its keys, or (several row tiles, each a unit) one for each.
+  static __device__ __forceinline__ int head_tiles(const Args& a, const Seq& s, int tp) {
+    if (s.n == 0) return 0;
+    const int rt = (s.n + tp - 1) / tp;
+    return rt > 1 ? rt : max(1, max_tiles(a, s.len, tp));
   }
   __device__ __forceinline__ void sequence() {
     s = seq_of(a, b);
-    per = units(a, s, tp, share, rt, st, ns, cost);
+    rt = (s.n + tp - 1) / tp;
+    head = head_tiles(a, s, tp);
+    st = split_tiles(head, share);
+    ns = rt > 1 ? 1 : n_splits(head, share);
+    per = rt > 1 ? rt : ns;
+    cost = rt > 1 ? 1 : st;
   }
   __device__ __forceinline__ void next_sequence() {
     h = i = 0;
@@ -141,7 +147,9 @@ struct Walk {
     at += cost;
     if (++i == per) {
       i = 0;
-      if (++h == a.Hk) next_sequence();
+      ++h;
+      at = pre[b] + h * head;
+      if (h == a.Hk) next_sequence();
     }
     unit();
   }
@@ -170,15 +178,15 @@ __device__ __forceinline__ void scale_rows(float (&acc)[WR][D / 8][4], int i, fl
 
 template <typename T, int D, int WR>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_paged_attn(const Args a, const int tp, const int share, const int ns_cap, const AttnOut o,
+    k_paged_attn(const __grid_constant__ Args a, const int tp, const int share, const int ns_cap, const __grid_constant__ AttnOut o,
                  const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                  const __grid_constant__ CUtensorMap mapQ, const void* v_pages) {
   using C = Cfg<D, WR>;
   using N = Num<T>;
   constexpr int R = C::R;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // (an offset, not a rounded pointer: the compiler then knows that it is shared memory)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::kCtlOff);
   int* pre = reinterpret_cast<int*>(ctl + 1);
   volatile int* abort_flag = &ctl->abort;
@@ -205,10 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_and_trigger();
   pdl_trigger();
   prefix_units(pre, a.n_seqs, [&](int b) {
-    const Seq s = seq_of(a, b);
-    if (s.n == 0) return 0;
-    int rt, st, ns, cost;
-    return a.Hk * Walk::units(a, s, tp, share, rt, st, ns, cost) * cost;
+    return a.Hk * Walk::head_tiles(a, seq_of(a, b), tp);
   });
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
 
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Join the splits of each row, in split order: one warp to a (token, head).
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
-    k_paged_join(const Args a, const int tp, const int share, const int ns_cap, const AttnOut o) {
+    k_paged_join(const __grid_constant__ Args a, const int tp, const int share, const int ns_cap, const __grid_constant__ AttnOut o) {
   pdl_wait_and_trigger();
   pdl_trigger();
   const int lane = threadIdx.x & 31, H = a.Hk * a.G;

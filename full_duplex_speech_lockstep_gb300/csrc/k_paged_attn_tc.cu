@@ -168,7 +168,7 @@ __device__ __forceinline__ bool finite_only(uint32_t& w) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_paged_attn_tc(const Args a, const int tp, const int ns_cap, const AttnOut o,
+    k_paged_attn_tc(const __grid_constant__ Args a, const int tp, const int ns_cap, const __grid_constant__ AttnOut o,
                     const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapV,
                     const __grid_constant__ CUtensorMap mapQ, const void* v_pages) {
@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using N = Num<T>;
   constexpr int kSlots = C::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // (an offset, not a rounded pointer: the compiler then knows that it is shared memory)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::kCtlOff);
   int* pre = reinterpret_cast<int*>(ctl + 1);
   volatile int* abort_flag = &ctl->abort;
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Join the splits of each row: one warp to a (row, head).
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
-    k_paged_join_rows(const Args a, const int tp, const int ns_cap, const AttnOut o) {
+    k_paged_join_rows(const __grid_constant__ Args a, const int tp, const int ns_cap, const __grid_constant__ AttnOut o) {
   pdl_wait_and_trigger();
   pdl_trigger();
   const int lane = threadIdx.x & 31, H = a.Hk * a.G;

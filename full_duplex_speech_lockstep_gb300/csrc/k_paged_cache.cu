@@ -48,7 +48,7 @@ __device__ __forceinline__ void store8(T* p, const float x[8]) {
 // One CTA to a token; D/8 lanes to a head.
 template <typename I, typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads)
-    k_paged_append(const Args a, const AppendArgs x, const __grid_constant__ Turns turns) {
+    k_paged_append(const __grid_constant__ Args a, const __grid_constant__ AppendArgs x, const __grid_constant__ Turns turns) {
   constexpr int L = D / 8;                       // lanes of one head
   __shared__ float2 cs[D / 2];
   __shared__ float row[kAppendThreads / L][D + 4];
@@ -154,7 +154,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) k_paged_select(const Args a, const EvictArgs x) {
+__global__ void __launch_bounds__(kSelThreads) k_paged_select(const __grid_constant__ Args a, const __grid_constant__ EvictArgs x) {
   extern __shared__ uint32_t keys[];
   __shared__ uint32_t hist[256];
   __shared__ uint32_t pick[3];          // prefix, still wanted, spare
@@ -250,7 +250,7 @@ constexpr int kMoveRows = 64;        // destination entries of one CTA
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads)
-    k_paged_move(const Args a, const EvictArgs x, const int blocks) {
+    k_paged_move(const __grid_constant__ Args a, const __grid_constant__ EvictArgs x, const int blocks) {
   constexpr int L = D / 8;
   pdl_wait_and_trigger();
   pdl_trigger();

@@ -158,13 +158,13 @@ __device__ __forceinline__ float weigh(uint32_t at, const float* ref, uint64_t c
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_paged_mass(const Args a, const int tp, const int N_, const int KS, const float* lse,
+    k_paged_mass(const __grid_constant__ Args a, const int tp, const int N_, const int KS, const float* lse,
                  float* mass, const float decay, const __grid_constant__ CUtensorMap mapK,
                  const __grid_constant__ CUtensorMap mapQ) {
   constexpr int kTileBytes = kTile * D * 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // (an offset, not a rounded pointer: the compiler then knows that it is shared memory)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int q_bytes = N_ * D * 2;                       // a stage of rows
   uint8_t* q_smem = smem + KS * kTileBytes;
   Ctl* ctl = reinterpret_cast<Ctl*>(q_smem + kQStages * q_bytes);
