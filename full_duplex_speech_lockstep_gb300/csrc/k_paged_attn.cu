@@ -73,11 +73,13 @@ __device__ __forceinline__ int max_tiles(const Args& a, int len, int tp) {
 }
 // Tiles of one split.  Only chunks of a single row tile are split (the host's plan expects no
 // others).  `share` splits of each key head fill the SMs when a sequence is alone (its bits do
-// not depend on whether it is); a split has at least two tiles, at most eight (so that runs of
-// units come out even), and a sequence at most 128 splits.
+// not depend on whether it is).  A split has at least four tiles: its end costs 4500 clocks,
+// which four tiles' loads (2900 clocks each at an SM's share of the bandwidth) hide and two do
+// not.  It has at most eight, so that runs of units come out even, and a sequence at most 128
+// splits.
 __host__ __device__ __forceinline__ int split_tiles(int tiles, int share) {
   int st = (tiles + share - 1) / share;
-  st = st < 2 ? 2 : st > 8 ? 8 : st;
+  st = st < 4 ? 4 : st > 8 ? 8 : st;
   const int even = (tiles + 127) / 128;
   return st > even ? st : even;
 }
@@ -91,11 +93,11 @@ struct Walk {
   const Args& a;
   const int* pre;
   const int tp, share;
-  int at, end;           // tiles before this unit, tiles where the run ends
+  int at, end;           // cost before this unit, cost where the run ends (half tiles)
   int b, h, i;           // sequence, key head, unit of the head
   Seq s;
   int rt, st, ns, per;   // row tiles, tiles of a split, splits, units of a head
-  int cost, head;        // tiles of a unit but the last, of a head
+  int cost;              // of a unit
   int t0, nt;            // first token of the row tile, its tokens
   int first;             // entry index of that token
   int tile0, tile1;      // key tiles of the split
@@ -109,32 +111,28 @@ struct Walk {
     if (at >= end) return;
     b = find_seq(pre, a.n_seqs, at);
     sequence();
-    // the first unit that starts in the run
-    h = (at - pre[b]) / head;
-    i = (at - pre[b] - h * head + cost - 1) / cost;
-    if (i == per) {
-      i = 0;
-      ++h;
-    }
-    at = pre[b] + h * head + i * cost;
+    const int k = (at - pre[b] + cost - 1) / cost;   // the first unit that starts in the run
+    h = k / per;
+    i = k - h * per;
+    at = pre[b] + k * cost;
     if (h == a.Hk) next_sequence();
     unit();
   }
   __device__ __forceinline__ bool done() const { return at >= end; }
-  // Tiles of one head: those of its keys, or (several row tiles, each a unit) one for each.
-  static __device__ __forceinline__ int head_tiles(const Args& a, const Seq& s, int tp) {
-    if (s.n == 0) return 0;
-    const int rt = (s.n + tp - 1) / tp;
-    return rt > 1 ? rt : max(1, max_tiles(a, s.len, tp));
+  // Units of one head: its splits, or (several row tiles) one for each.  A unit costs its
+  // tiles' loads or, if they are few, their products and its end.
+  static __device__ __forceinline__ int head_units(const Args& a, const Seq& s, int tp, int share,
+                                                   int& rt, int& st, int& ns, int& cost) {
+    rt = (s.n + tp - 1) / tp;
+    const int mt = max_tiles(a, s.len, tp), few = min(split_tiles(mt, share), max(mt, 1));
+    st = split_tiles(mt, share);
+    ns = rt > 1 ? 1 : n_splits(mt, share);
+    cost = rt > 1 ? 1 : max(2 * few, few + 3);
+    return rt > 1 ? rt : ns;
   }
   __device__ __forceinline__ void sequence() {
     s = seq_of(a, b);
-    rt = (s.n + tp - 1) / tp;
-    head = head_tiles(a, s, tp);
-    st = split_tiles(head, share);
-    ns = rt > 1 ? 1 : n_splits(head, share);
-    per = rt > 1 ? rt : ns;
-    cost = rt > 1 ? 1 : st;
+    per = head_units(a, s, tp, share, rt, st, ns, cost);
   }
   __device__ __forceinline__ void next_sequence() {
     h = i = 0;
@@ -147,9 +145,7 @@ struct Walk {
     at += cost;
     if (++i == per) {
       i = 0;
-      ++h;
-      at = pre[b] + h * head;
-      if (h == a.Hk) next_sequence();
+      if (++h == a.Hk) next_sequence();
     }
     unit();
   }
@@ -213,7 +209,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_and_trigger();
   pdl_trigger();
   prefix_units(pre, a.n_seqs, [&](int b) {
-    return a.Hk * Walk::head_tiles(a, seq_of(a, b), tp);
+    const Seq s = seq_of(a, b);
+    if (s.n == 0) return 0;
+    int rt, st, ns, cost;
+    return a.Hk * Walk::head_units(a, s, tp, share, rt, st, ns, cost) * cost;
   });
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
 
@@ -615,9 +614,8 @@ AttnPlan attn_plan(const Args& a, int max_q) {
     const int64_t seen = ((int64_t)a.window + p.tp - 2) / kTile + 2;
     if (seen < tiles) tiles = seen;
   }
-  // splits of a shorter sequence are no more, but for rounding: at two tiles each, at most
-  // `share`; else at most one for every eight tiles or 128 in all
-  int64_t most = (tiles + 1) / 2;
+  // at four tiles each or more, at most `share` splits or one for every eight tiles, 128 in all
+  int64_t most = (tiles + 3) / 4;
   const int64_t by_share = p.share > (tiles + 7) / 8 ? p.share : (tiles + 7) / 8;
   if (by_share < most) most = by_share;
   p.ns_cap = (int)(most < 1 ? 1 : most < 128 ? most : 128);
