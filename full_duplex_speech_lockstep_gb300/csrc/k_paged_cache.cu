@@ -9,32 +9,38 @@
 //
 // k_paged_select / k_paged_move: the entries that stay - the newest `recent` and of the
 // others the heaviest, lower index first among equals - in their old order into the
-// destination's pages.  The threshold weight is found byte by byte (radix selection over
-// order-preserving integers), so no sort is needed.
+// destination's pages.  The threshold weight is found a few bits at a time (radix selection
+// over order-preserving integers), so no sort is needed.
+#include <cooperative_groups.h>
+
 #include "pp_paged.cuh"
 
 namespace pp {
 namespace paged {
 namespace {
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256;
+constexpr int kAppendRows = 4;        // heads of a token whose loads a thread has in flight
 
-// 8 consecutive values as floats (16-byte loads)
-__device__ __forceinline__ void load8(const float* p, float x[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float x[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// 8 consecutive values (16-byte loads), and as floats
+template <typename I>
+struct Raw {
+  uint4 w[sizeof(I) / 2];
+  __device__ __forceinline__ void load(const I* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = Num<T>::to_float(w[i] & 0xffffu);
-    x[2 * i + 1] = Num<T>::to_float(w[i] >> 16);
+    for (int i = 0; i < (int)sizeof(I) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-}
+  __device__ __forceinline__ void values(float x[8]) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(I) == 4)
+        x[i] = __uint_as_float(u[i]);
+      else
+        x[i] = Num<I>::to_float(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xffffu);
+    }
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float x[8]) {
   uint4 a;
@@ -45,30 +51,54 @@ __device__ __forceinline__ void store8(T* p, const float x[8]) {
   *reinterpret_cast<uint4*>(p) = a;
 }
 
-// One CTA to a token; D/8 lanes to a head.
+// One CTA to a token, D/8 lanes to a head.  Bound by reading and writing the rows once: the
+// first heads' loads go out before the token's place in the cache is known, whose chain of
+// lookups (row offsets, length, page) they hide.
 template <typename I, typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads)
-    k_paged_append(const __grid_constant__ Args a, const __grid_constant__ AppendArgs x, const __grid_constant__ Turns turns) {
+    k_paged_append(const __grid_constant__ Args a, const __grid_constant__ AppendArgs x,
+                   const __grid_constant__ Turns turns) {
   constexpr int L = D / 8;                       // lanes of one head
+  constexpr int kHeads = kAppendThreads / L;     // heads side by side
   __shared__ float2 cs[D / 2];
-  __shared__ float row[kAppendThreads / L][D + 4];
+  __shared__ float row[kHeads][D + 4];
+  __shared__ int found, entry;          // the token's sequence and cache entry
   pdl_wait_and_trigger();
   pdl_trigger();
-  const int t = blockIdx.x;
-  // the token's sequence: how many end at or before it
-  int before = 0;
-  for (int b0 = 0; b0 < a.n_seqs; b0 += kAppendThreads) {
-    const int b = b0 + threadIdx.x;
-    before += __syncthreads_count(b < a.n_seqs && a.cu[b + 1] <= t);
+  const int t = blockIdx.x, H = a.Hk * a.G, rows = H + 2 * a.Hk;
+  const int group = threadIdx.x / L, l = threadIdx.x % L;
+  Raw<I> raw[kAppendRows];
+  auto load = [&](int r0) {                      // queries, then keys, then values
+#pragma unroll
+    for (int i = 0; i < kAppendRows; ++i) {
+      const int r = r0 + i * kHeads + group;
+      if (r >= rows) break;
+      const I* src = r < H ? reinterpret_cast<const I*>(x.q) + t * x.q_stride + r * D
+                     : r < H + a.Hk
+                         ? reinterpret_cast<const I*>(x.k) + t * x.k_stride + (r - H) * D
+                         : reinterpret_cast<const I*>(x.v) + t * x.v_stride + (r - H - a.Hk) * D;
+      raw[i].load(src + l * 8);
+    }
+  };
+  load(0);
+  // the token's sequence: a thread to each
+  const int given = x.positions ? x.positions[t] : 0;
+  if (threadIdx.x == 0) found = -1;
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.n_seqs; b += kAppendThreads) {
+    const Seq s = seq_of(a, b);
+    if (t >= s.row0 && t < s.row0 + s.n) {
+      found = b;
+      entry = s.len - s.n + (t - s.row0);
+    }
   }
-  if (before >= a.n_seqs || t < a.cu[before]) return;   // a row of no sequence
-  const Seq s = seq_of(a, before);
-  if (t < s.row0 || t >= s.row0 + s.n) return;
-  const int j = s.len - s.n + (t - s.row0);             // the token's cache entry
-  const int page = j >= 0 ? page_of(a, before, j) : -1;
+  __syncthreads();
+  const int b = found, j = entry;
+  if (b < 0) return;                             // a row of no sequence
+  const int page = j >= 0 ? page_of(a, b, j) : -1;
   const int in_page = j & ((1 << a.lps) - 1);
   if (j >= 0 && page < 0 && threadIdx.x == 0) raise(a, PP_S_INDEX);
-  const int pos = x.positions ? x.positions[t] : j;
+  const int pos = x.positions ? given : j;
   for (int i = threadIdx.x; i < x.rot / 2; i += kAppendThreads) {
     const uint64_t turn = (uint64_t)(int64_t)pos * turns.f[i];
     float sn, cn;
@@ -76,76 +106,81 @@ __global__ void __launch_bounds__(kAppendThreads)
     cs[i] = make_float2(cn, sn);
   }
   __syncthreads();
-  const int H = a.Hk * a.G, group = threadIdx.x / L, l = threadIdx.x % L;
   const int half = x.rot / 2;
-  for (int r0 = 0; r0 < H + 2 * a.Hk; r0 += kAppendThreads / L) {
-    const int r = r0 + group;
-    const bool live = r < H + 2 * a.Hk;
-    const int kind = r < H ? 0 : r < H + a.Hk ? 1 : 2;   // query, key, value
-    const int h = kind == 0 ? r : kind == 1 ? r - H : r - H - a.Hk;
-    float y[8] = {};
-    if (live) {
-      const I* src = kind == 0 ? reinterpret_cast<const I*>(x.q) + t * x.q_stride
-                   : kind == 1 ? reinterpret_cast<const I*>(x.k) + t * x.k_stride
-                               : reinterpret_cast<const I*>(x.v) + t * x.v_stride;
-      load8(src + h * D + l * 8, y);
-    }
-    const float* alpha = kind == 0 ? x.q_alpha : kind == 1 ? x.k_alpha : nullptr;
-    float ss = 0.f;
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += kAppendRows * kHeads) {
+    if (r0 > 0) load(r0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+    for (int i = 0; i < kAppendRows; ++i) {
+      // (a warp's heads are consecutive: past the last row together, but for the lanes that
+      // share its shuffles)
+      const int r = r0 + i * kHeads + group;
+      if (r - (int)(threadIdx.x % 32) / L >= rows) break;
+      const bool live = r < rows;
+      const int kind = r < H ? 0 : r < H + a.Hk ? 1 : 2;   // query, key, value
+      const int h = kind == 0 ? r : kind == 1 ? r - H : r - H - a.Hk;
+      float y[8] = {};
+      if (live) raw[i].values(y);
+      const float* alpha = kind == 0 ? x.q_alpha : kind == 1 ? x.k_alpha : nullptr;
+      float ss = 0.f;
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (live && alpha) {
-      const float inv = 1.f / sqrtf(ss * (1.f / D) + x.eps);
-      float al[8];
-      load8(alpha + l * 8, al);
+      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * al[e];
-    }
-    if (x.halves) {
-      // partners lie half a rotation apart, in another lane
-      __syncwarp();
+      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (live && alpha) {
+        const float inv = 1.f / sqrtf(ss * (1.f / D) + x.eps);
+        const float4 a0 = reinterpret_cast<const float4*>(alpha + l * 8)[0];
+        const float4 a1 = reinterpret_cast<const float4*>(alpha + l * 8)[1];
+        const float al[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) row[group][l * 8 + e] = y[e];
-      __syncwarp();
-      if (kind != 2) {
+        for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * al[e];
+      }
+      if (x.halves) {
+        // partners lie half a rotation apart, in another lane
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 8; ++e) row[group][l * 8 + e] = y[e];
+        __syncwarp();
+        if (kind != 2) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int d = l * 8 + e;
+            if (d >= x.rot) continue;
+            const bool lo = d < half;
+            const float2 w = cs[lo ? d : d - half];
+            const float o = row[group][lo ? d + half : d - half];
+            y[e] = lo ? y[e] * w.x - o * w.y : o * w.y + y[e] * w.x;
+          }
+        }
+      } else if (kind != 2) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
           const int d = l * 8 + e;
           if (d >= x.rot) continue;
-          const bool lo = d < half;
-          const float2 w = cs[lo ? d : d - half];
-          const float o = row[group][lo ? d + half : d - half];
-          y[e] = lo ? y[e] * w.x - o * w.y : o * w.y + y[e] * w.x;
+          const float2 w = cs[d / 2];
+          const float p = y[e], o = y[e + 1];
+          y[e] = p * w.x - o * w.y;
+          y[e + 1] = p * w.y + o * w.x;
         }
       }
-    } else if (kind != 2) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const int d = l * 8 + e;
-        if (d >= x.rot) continue;
-        const float2 w = cs[d / 2];
-        const float p = y[e], o = y[e + 1];
-        y[e] = p * w.x - o * w.y;
-        y[e + 1] = p * w.y + o * w.x;
+      if (!live) continue;
+      if (kind == 0) {
+        store8(reinterpret_cast<T*>(x.q_out) + ((int64_t)t * H + h) * D + l * 8, y);
+      } else if (page >= 0) {
+        T* pool = reinterpret_cast<T*>(kind == 1 ? x.k_pages : x.v_pages);
+        store8(pool + page * a.page_stride + (((int64_t)h << a.lps) + in_page) * D + l * 8, y);
+        if (kind == 1 && x.mass && l == 0)
+          x.mass[(((int64_t)page * a.Hk + h) << a.lps) + in_page] = 0.f;
       }
-    }
-    if (!live) continue;
-    if (kind == 0) {
-      store8(reinterpret_cast<T*>(x.q_out) + ((int64_t)t * H + h) * D + l * 8, y);
-    } else if (page >= 0) {
-      T* pool = reinterpret_cast<T*>(kind == 1 ? x.k_pages : x.v_pages);
-      store8(pool + page * a.page_stride + (((int64_t)h << a.lps) + in_page) * D + l * 8, y);
-      if (kind == 1 && x.mass && l == 0)
-        x.mass[(((int64_t)page * a.Hk + h) << a.lps) + in_page] = 0.f;
     }
   }
 }
 
 // ---- eviction --------------------------------------------------------------------------------
-constexpr int kSelThreads = 1024;
-constexpr int kSelKeys = 48 * 1024;   // weights held on chip; longer rows are read again
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelKeys = 44 * 1024;   // weights that a CTA holds on chip; longer slices are read again
+constexpr int kBins = 4096;           // of the first 12 bits; then twice 1024 of 10 bits
 
 // Order-preserving integer of a weight: larger weight, larger integer; NaN lowest, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -154,94 +189,179 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) k_paged_select(const __grid_constant__ Args a, const __grid_constant__ EvictArgs x) {
+// One cluster of CTAs to a (sequence, key head), a slice of the older entries to a CTA.  Each
+// round counts the next bits of the keys that still match, adds the CTAs' counts up through
+// distributed shared memory and finds, in every CTA alike, the digit of the last key to stay.
+__global__ void __launch_bounds__(kSelThreads)
+    k_paged_select(const __grid_constant__ Args a, const __grid_constant__ EvictArgs x,
+                   const int cluster_size) {
+  namespace cg = cooperative_groups;
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t pick[3];          // prefix, still wanted, spare
-  __shared__ int warp_sum[33];
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t sums[kBins], share_sum;
+  __shared__ uint32_t scan[kSelWarps], pick[2];       // digit, wanted among its keys
+  __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps], total[2];   // larger keys, equal ones
+  const cg::cluster_group cluster = cg::this_cluster();
   pdl_wait_and_trigger();
   pdl_trigger();
-  const int b = blockIdx.x / a.Hk, h = blockIdx.x % a.Hk, tid = threadIdx.x;
+  const int pair = blockIdx.x / cluster_size, rank = blockIdx.x % cluster_size;
+  const int b = pair / a.Hk, h = pair - b * a.Hk;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = seq_len(a, b);
   const int m = min(len, x.budget);
   const int safe = min(x.recent, len);
   const int old = len - safe;                       // entries that compete
   const uint32_t want = (uint32_t)(m - safe);       // of which this many stay
-  int32_t* kept = x.kept + (int64_t)blockIdx.x * x.budget;
-  if (h == 0 && tid == 0) x.to_len[b] = m;
-  for (int i = m + tid; i < x.budget; i += kSelThreads) kept[i] = -1;
+  int32_t* kept = x.kept + (int64_t)pair * x.budget;
+  const int step = cluster_size * kSelThreads, first = rank * kSelThreads + tid;
+  if (h == 0 && first == 0) x.to_len[b] = m;
+  for (int i = m + first; i < x.budget; i += step) kept[i] = -1;
   if (m == len) {
-    for (int i = tid; i < m; i += kSelThreads) kept[i] = i;
+    for (int i = first; i < m; i += step) kept[i] = i;
     return;
   }
-  // weights of pages outside the pool count as the lowest
-  auto weight = [&](int j) {
-    const int p = page_of(a, b, j);
+  for (int i = first; i < safe; i += step) kept[m - safe + i] = old + i;
+  if (want == 0) return;
+  // this CTA's slice; entries of pages outside the pool count as the lowest
+  const int j0 = (int)((int64_t)old * rank / cluster_size);
+  const int n = (int)((int64_t)old * (rank + 1) / cluster_size) - j0;
+  auto weight = [&](int i) {
+    const int j = j0 + i, p = page_of(a, b, j);
     return p < 0 ? 0u
                  : weight_key(x.mass[(((int64_t)p * a.Hk + h) << a.lps) + (j & ((1 << a.lps) - 1))]);
   };
-  const bool on_chip = old <= kSelKeys;
-  if (on_chip)
-    for (int j = tid; j < old; j += kSelThreads) keys[j] = weight(j);
-  auto key = [&](int j) { return on_chip ? keys[j] : weight(j); };
-  // the want-th largest key, a byte at a time from the top
+  const bool on_chip = n <= kSelKeys;
+  if (on_chip) {
+#pragma unroll 4
+    for (int i = tid; i < n; i += kSelThreads) keys[i] = weight(i);
+  }
+  auto key = [&](int i) { return on_chip ? keys[i] : weight(i); };
+
+  // ---- the want-th largest key
   uint32_t prefix = 0, left = want;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+#pragma unroll 1
+  for (int round = 0; round < 3; ++round) {
+    const int shift = 20 - 10 * round, bits = round == 0 ? 12 : 10, bins = 1 << bits;
+    for (int i = tid; i < bins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-    for (int j = tid; j < old; j += kSelThreads) {
-      const uint32_t k = key(j);
-      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+#pragma unroll 4
+    for (int i = tid; i < n; i += kSelThreads) {
+      const uint32_t k = key(i);
+      if (round == 0 || (k >> (shift + bits)) == prefix)
+        atomicAdd(&hist[(k >> shift) & (uint32_t)(bins - 1)], 1u);
     }
+    cluster.sync();
+    // a CTA adds up its share of the bins over all CTAs (each thread neighbouring words, as
+    // distributed shared memory likes them) ...
+    const int share = bins / cluster_size;
+    uint32_t sum = 0;
+    for (int i = tid; i < share; i += kSelThreads) {
+      uint32_t c = 0;
+      for (int r = 0; r < cluster_size; ++r) c += cluster.map_shared_rank(hist, r)[rank * share + i];
+      sums[i] = c;
+      sum += c;
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) scan[warp] = sum;
     __syncthreads();
     if (tid == 0) {
-      uint32_t sum = 0;
-      int d = 255;
-      while (d > 0 && sum + hist[d] < left) sum += hist[d--];
-      pick[0] = (prefix << 8) | (uint32_t)d;
-      pick[1] = left - sum;
+      uint32_t c = 0;
+      for (int w = 0; w < kSelWarps; ++w) c += scan[w];
+      share_sum = c;
     }
+    cluster.sync();
+    // ... then all of them find the share, and in it the bin, of the left-th key from the top
+    uint32_t above = 0;
+    int at = cluster_size - 1;
+    for (;; --at) {
+      const uint32_t c = *cluster.map_shared_rank(&share_sum, at);
+      if (at == 0 || above + c >= left) break;
+      above += c;
+    }
+    const uint32_t* counts = cluster.map_shared_rank(sums, at);
+    const int run = (share + kSelThreads - 1) / kSelThreads;   // 8, 4, 2 or 1 bins to a thread
+    const int top = share - 1 - tid * run;            // this thread's highest bin
+    uint32_t c[kBins / kSelThreads];
+    sum = 0;
+#pragma unroll
+    for (int e = 0; e < kBins / kSelThreads; ++e) {
+      c[e] = e < run && top - e >= 0 ? counts[top - e] : 0u;
+      sum += c[e];
+    }
+    uint32_t over = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, over, o);
+      if (lane >= o) over += y;
+    }
+    if (lane == 31) scan[warp] = over;
     __syncthreads();
-    prefix = pick[0];
+    above += over - sum;
+    for (int w = 0; w < warp; ++w) above += scan[w];
+    if (above < left && left <= above + sum) {
+#pragma unroll
+      for (int e = 0; e < kBins / kSelThreads; ++e) {
+        if (above < left && left <= above + c[e]) {
+          pick[0] = (uint32_t)(at * share + top - e);
+          pick[1] = left - above;
+        }
+        above += c[e];
+      }
+    }
+    cluster.sync();                                   // also: every CTA has read every count
+    prefix = (prefix << bits) | pick[0];
     left = pick[1];
   }
-  // larger keys stay, and of the equal ones the first `left` (none when want is 0)
-  if (want == 0) left = 0;
-  int done = 0, ties = 0;
-  for (int j0 = 0; j0 < len; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t k = j < old ? key(j) : 0u;
-    const bool tie = j < old && k == prefix;
-    bool stay = j < len && (j >= old || k > prefix);
-    // ranks of the ties, then of those that stay, in index order
-    for (int pass = 0; pass < 2; ++pass) {
-      const bool f = pass == 0 ? tie : stay;
-      const unsigned bal = __ballot_sync(0xffffffffu, f);
-      if ((tid & 31) == 0) warp_sum[tid >> 5] = __popc(bal);
-      __syncthreads();
-      if (tid < 32) {
-        int v = warp_sum[tid], s = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, s, o);
-          if (tid >= o) s += y;
-        }
-        warp_sum[tid] = s - v;
-        if (tid == 31) warp_sum[32] = s;
-      }
-      __syncthreads();
-      const int rank = warp_sum[tid >> 5] + __popc(bal & ((1u << (tid & 31)) - 1u));
-      const int total = warp_sum[32];
-      if (pass == 0) {
-        if (tie && ties + rank < (int)left) stay = true;
-        ties += total;
-      } else {
-        if (stay) kept[done + rank] = j;
-        done += total;
-      }
-      __syncthreads();
+
+  // ---- larger keys stay, and of the equal ones the first `left`, in index order
+  const int part = (n + kSelWarps - 1) / kSelWarps;   // a run of the slice to each warp
+  const int i0 = min(warp * part, n), i1 = min(i0 + part, n);
+  int gt = 0, eq = 0;
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint32_t k = key(i);
+    gt += k > prefix;
+    eq += k == prefix;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    warp_gt[warp] = gt;
+    warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int g = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? warp_gt[lane] : 0);
+    const int e = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? warp_eq[lane] : 0);
+    if (lane == 0) {
+      total[0] = g;
+      total[1] = e;
     }
   }
+  cluster.sync();
+  // equal keys, and entries that stay, before this warp's run
+  int ties = 0, at = 0;
+  auto pass = [&](int g, int e) {
+    at += g + min(max((int)left - ties, 0), e);
+    ties += e;
+  };
+  for (int r = 0; r < rank; ++r) {
+    const int* remote = cluster.map_shared_rank(total, r);
+    pass(remote[0], remote[1]);
+  }
+  for (int w = 0; w < warp; ++w) pass(warp_gt[w], warp_eq[w]);
+  const unsigned below = (1u << lane) - 1u;
+  for (int i = i0; i < i1; i += 32) {
+    const uint32_t k = i + lane < i1 ? key(i + lane) : 0u;
+    const bool tie = i + lane < i1 && k == prefix;
+    const unsigned eqs = __ballot_sync(0xffffffffu, tie);
+    const bool stay = i + lane < i1 &&
+                      (k > prefix || (tie && ties + __popc(eqs & below) < (int)left));
+    const unsigned stays = __ballot_sync(0xffffffffu, stay);
+    if (stay) kept[at + __popc(stays & below)] = j0 + i + lane;
+    ties += __popc(eqs);
+    at += __popc(stays);
+  }
+  cluster.sync();                                     // no CTA leaves while its totals are read
 }
 
 // Copy the entries that stay: a group of D/8 lanes to an entry and 16 bytes to a lane.
@@ -302,11 +422,18 @@ cudaError_t launch_paged_append(const Args& a, const AppendArgs& x, const Turns&
 cudaError_t launch_paged_evict(const Args& a, const EvictArgs& x, cudaStream_t s) {
   const int pairs = a.n_seqs * a.Hk;
   const int64_t entries = (int64_t)a.table_ld << a.lps;
-  const size_t smem = (size_t)(entries < kSelKeys ? entries : kSelKeys) * sizeof(uint32_t);
+  // CTAs to a pair: enough for two on every SM, while a slice keeps two entries to a thread
+  int cluster = 1;
+  while (cluster < 8 && pairs * cluster * 2 <= 2 * 152 &&
+         entries >= (int64_t)cluster * 2 * 2 * kSelThreads)
+    cluster *= 2;
+  const int64_t slice = (entries + cluster - 1) / cluster;
+  const size_t smem = (size_t)(slice < kSelKeys ? slice : kSelKeys) * sizeof(uint32_t);
   cudaError_t err = cudaFuncSetAttribute(k_paged_select,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  err = launch(k_paged_select, dim3((unsigned)pairs), kSelThreads, smem, s, a, x);
+  err = launch_cluster(cluster, k_paged_select, dim3((unsigned)(pairs * cluster)), kSelThreads, smem,
+                       s, a, x, cluster);
   const int64_t most = entries < x.budget ? entries : x.budget;
   if (err != cudaSuccess || most == 0) return err;
   const int blocks = (int)((most + kMoveRows - 1) / kMoveRows);

@@ -403,19 +403,28 @@ inline int sm_count() {
 // Programmatic dependent launch: every kernel of this family waits for its predecessor
 // (griddepcontrol.wait) before it reads anything, so it may be scheduled early.
 template <typename... KArgs, typename... Args_>
-cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                   Args_... args) {
+cudaError_t launch_cluster(int cluster, void (*kern)(KArgs...), dim3 grid, int threads, size_t smem,
+                           cudaStream_t s, Args_... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+template <typename... KArgs, typename... Args_>
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                   Args_... args) {
+  return launch_cluster(1, kern, grid, threads, smem, s, args...);
 }
 
 struct Maps {
