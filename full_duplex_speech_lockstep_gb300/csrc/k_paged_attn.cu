@@ -242,19 +242,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(dst + bx * (R * 128), &mapQ, bx * 64, x.h * a.G, x.s.row0 + x.t0, 0, bar);
       }
       ++nq;
+      TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, lane);
 #pragma unroll 1
       for (int t = x.tile0; t < x.tile1; ++t) {
         const int ks = nk % C::KS, vs = nv % C::VS;
+        const TilePages now = next;
+        if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, lane);
         if (nk >= C::KS) wait(&ctl->kempty[ks], (nk / C::KS - 1) & 1);
         if (*abort_flag) break;
-        seen_bad |= load_key_tile(a, &mapK, smem_u32(smem + ks * C::kTileBytes),
-                                  smem_u32(&ctl->kfull[ks]), x.b, x.h, t * kTile, x.stop, lane,
-                                  nullptr);
+        load_key_tile(a, &mapK, smem_u32(smem + ks * C::kTileBytes), smem_u32(&ctl->kfull[ks]), now,
+                      x.h, t * kTile, lane, nullptr);
+        seen_bad |= now.bad;
         ++nk;
         if (nv >= C::VS) wait(&ctl->vempty[vs], (nv / C::VS - 1) & 1);
         if (*abort_flag) break;
         load_key_tile(a, &mapV, smem_u32(smem + C::kVOff + vs * C::kTileBytes),
-                      smem_u32(&ctl->vfull[vs]), x.b, x.h, t * kTile, x.stop, lane, &ctl->bad[vs]);
+                      smem_u32(&ctl->vfull[vs]), now, x.h, t * kTile, lane, &ctl->bad[vs]);
         ++nv;
       }
     }

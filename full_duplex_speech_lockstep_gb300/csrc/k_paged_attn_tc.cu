@@ -238,17 +238,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                           bx * 64, x.h * a.G, x.row + t * tp, 0, bar);
         }
         ++nq;
+        TilePages now{}, next = find_pages(a, x.b, x.tile0 * kTile, x.stop, lane);
 #pragma unroll 1
         for (int i = 0; i < 2 * (x.tile1 - x.tile0); ++i) {
-          const int slot = nl % kSlots;
+          const int slot = nl % kSlots, t = x.tile0 + (i >> 1);
+          if ((i & 1) == 0) {
+            now = next;
+            if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, lane);
+            seen_bad |= now.bad;
+          }
           if (nl >= kSlots) wait(&ctl->empty[slot], (nl / kSlots - 1) & 1);
           if (*abort_flag) break;
-          const int t = x.tile0 + (i >> 1);
-          const uint32_t bad =
-              load_key_tile(a, (i & 1) ? &mapV : &mapK, smem_u32(smem + slot * C::kTileBytes),
-                            smem_u32(&ctl->full[slot]), x.b, x.h, t * kTile, x.stop, lane,
-                            &ctl->bad[slot]);
-          seen_bad |= bad;
+          load_key_tile(a, (i & 1) ? &mapV : &mapK, smem_u32(smem + slot * C::kTileBytes),
+                        smem_u32(&ctl->full[slot]), now, x.h, t * kTile, lane, &ctl->bad[slot]);
           ++nl;
         }
       }

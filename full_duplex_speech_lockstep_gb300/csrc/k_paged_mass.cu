@@ -10,10 +10,11 @@
 // atomically, and the bits are the same in every run.
 //
 // A CTA takes a run of consecutive units of about the same number of steps as the others:
-//   warp 0        producer: the key tile, then the steps' rows, by TMA
+//   warp 0        producer: the units and their key tiles, by TMA
 //   warp 1        one thread issues the MMAs, up to four steps ahead of the sums
 //   warp 2        each key's old mass and page, a unit ahead
-//   warp 3        each row's lse, a step ahead; rows that do not count: infinity
+//   warp 3        the steps' rows by TMA; each row's lse, a step ahead; rows that do not count:
+//                 infinity
 //   warps 4-7, 8-11   the sums, the two groups in turn to a step
 #include <type_traits>
 
@@ -120,27 +121,25 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t r[16]) {
 }
 
 // Sum of 2^(s c - ref) over the columns [0, cols) of a lane, those outside [lo, hi) left out
-// (`masked`).  Columns from cols to the next multiple of 16 have an infinite ref.
-template <typename M>
+// (`masked`); cols is a multiple of W otherwise.  The next W columns are on their way from tensor
+// memory while these are summed.
+template <int W, typename M>
 __device__ __forceinline__ float weigh(uint32_t at, const float* ref, uint64_t c2, int cols, int lo,
                                        int hi, M) {
   uint64_t part[2] = {0, 0};   // two sums of two
-#pragma unroll 1
-  for (int c0 = 0; c0 < cols; c0 += 16) {
-    uint32_t s[16];
-    tmem_ld16(at + c0, s);
-    float4 z[4];
+  uint32_t s[2][W];
+  auto load = [&](uint32_t (&r)[W], int c0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] = reinterpret_cast<const float4*>(ref + c0)[i];
-    tmem_wait_ld();
+    for (int i = 0; i < W / 16; ++i) tmem_ld16(at + c0 + 16 * i, r + 16 * i);
+  };
+  auto sum = [&](uint32_t (&r)[W], int c0) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(after_wait(s[i]));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t e0 = fma2((uint64_t)s[4 * i] | ((uint64_t)s[4 * i + 1] << 32), c2,
-                               f32x2(-z[i].x, -z[i].y));
-      const uint64_t e1 = fma2((uint64_t)s[4 * i + 2] | ((uint64_t)s[4 * i + 3] << 32), c2,
-                               f32x2(-z[i].z, -z[i].w));
+    for (int i = 0; i < W / 4; ++i) {
+      const float4 z = reinterpret_cast<const float4*>(ref + c0)[i];
+      const uint64_t e0 = fma2((uint64_t)r[4 * i] | ((uint64_t)r[4 * i + 1] << 32), c2,
+                               f32x2(-z.x, -z.y));
+      const uint64_t e1 = fma2((uint64_t)r[4 * i + 2] | ((uint64_t)r[4 * i + 3] << 32), c2,
+                               f32x2(-z.z, -z.w));
       float p[4] = {exp2_approx(lo_of(e0)), exp2_approx(hi_of(e0)), exp2_approx(lo_of(e1)),
                     exp2_approx(hi_of(e1))};
       if constexpr (M::value) {
@@ -151,12 +150,29 @@ __device__ __forceinline__ float weigh(uint32_t at, const float* ref, uint64_t c
       part[0] = add2(part[0], f32x2(p[0], p[1]));
       part[1] = add2(part[1], f32x2(p[2], p[3]));
     }
+  };
+  auto landed = [&](uint32_t (&r)[W]) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < W; ++i) asm volatile("" : "+r"(r[i]));
+  };
+  load(s[0], 0);
+  landed(s[0]);
+#pragma unroll 1
+  for (int c0 = 0; c0 < cols; c0 += 2 * W) {
+    if (c0 + W < cols) load(s[1], c0 + W);
+    sum(s[0], c0);
+    if (c0 + W >= cols) break;
+    landed(s[1]);
+    if (c0 + 2 * W < cols) load(s[0], c0 + 2 * W);
+    sum(s[1], c0 + W);
+    if (c0 + 2 * W < cols) landed(s[0]);
   }
   const uint64_t both = add2(part[0], part[1]);
   return lo_of(both) + hi_of(both);
 }
 
-template <typename T, int D>
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_mass(const __grid_constant__ Args a, const int tp, const int N_, const int KS, const float* lse,
                  float* mass, const float decay, const __grid_constant__ CUtensorMap mapK,
@@ -216,37 +232,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
   if (warp == 0) {
     // ---- producer -------------------------------------------------------------------------
-    uint32_t nk = 0, nq = 0, nu = 0, seen_bad = 0;
+    uint32_t nk = 0, nu = 0, seen_bad = 0;
     Walk x(a, pre, tp);
+    TilePages next{};
+    if (!x.done()) next = find_pages(a, x.b, x.j0, x.s.len, lane);
 #pragma unroll 1
-    for (; !x.done() && !*abort_flag; x.next()) {
+    while (!x.done() && !*abort_flag) {
+      // this unit, and the next one's pages on their way
+      const Unit u{x.b, x.h, x.s.row0 + x.t0, x.t1 - x.t0, x.s.len - x.s.n + x.t0, x.tile,
+                   x.tile + 1, 0, x.s.len, 0, 1, 0};
+      const TilePages now = next;
+      const int j0 = x.j0;
+      x.next();
+      if (!x.done()) next = find_pages(a, x.b, x.j0, x.s.len, lane);
       // a unit that no row sees has nothing to add; without decay it is left out
-      if (x.t0 == x.t1 && decay == 1.f) continue;
-      put_unit(a, ctl->ring, nu++,
-               Unit{x.b, x.h, x.s.row0 + x.t0, x.t1 - x.t0, x.s.len - x.s.n + x.t0, x.tile,
-                    x.tile + 1, 0, x.s.len, 0, 1, 0},
-               lane, abort_flag);
-      if (x.t0 == x.t1) continue;
+      if (u.nt == 0 && decay == 1.f) continue;
+      put_unit(a, ctl->ring, nu++, u, lane, abort_flag);
+      if (u.nt == 0) continue;
       const int ks = nk % KS;
       if (nk >= KS) wait(&ctl->kempty[ks], (nk / KS - 1) & 1);
       if (*abort_flag) break;
-      seen_bad |= load_key_tile(a, &mapK, smem_u32(smem + ks * kTileBytes),
-                                smem_u32(&ctl->kfull[ks]), x.b, x.h, x.j0, x.s.len, lane, nullptr);
+      load_key_tile(a, &mapK, smem_u32(smem + ks * kTileBytes), smem_u32(&ctl->kfull[ks]), now, u.h,
+                    j0, lane, nullptr);
+      seen_bad |= now.bad;
       ++nk;
-#pragma unroll 1
-      for (int t = x.t0; t < x.t1; t += tp) {
-        const int qs = nq % kQStages;
-        if (nq >= kQStages) wait(&ctl->qempty[qs], (nq / kQStages - 1) & 1);
-        if (*abort_flag) break;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&ctl->qfull[qs]);
-          mbar_expect_tx(bar, (uint32_t)(tp * a.G * D * 2));
-          for (int bx = 0; bx < D / 64; ++bx)
-            tma_load_4d(smem_u32(q_smem + qs * q_bytes + bx * N_ * 128), &mapQ, bx * 64, x.h * a.G,
-                        x.s.row0 + t, 0, bar);
-        }
-        ++nq;
-      }
     }
     Unit last{};
     last.b = -1;
@@ -256,9 +265,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (uint32_t i = nk > KS ? nk - KS : 0; i < nk; ++i)
         drain_phase(&ctl->kfull[i % KS], (i / KS) & 1);
-#pragma unroll 1
-      for (uint32_t i = nq > kQStages ? nq - kQStages : 0; i < nq; ++i)
-        drain_phase(&ctl->qfull[i % kQStages], (i / kQStages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -338,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 4; ++k) old[k] = next[k];
     }
   } else if (warp == 3) {
-    // ---- lse: four rows to a lane; a step's loads are issued before the last step's are handed on
+    // ---- the steps' rows by TMA, and lse: four rows to a lane; a step's loads are issued before
+    // the last step's values are handed on
     const int H = a.Hk * a.G;
     int tk[4], gh[4];                                   // a lane's rows: token and head of a step
 #pragma unroll
@@ -364,7 +371,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
 #pragma unroll 1
       for (int t = 0; t < x.nt && !*abort_flag; t += tp, ++nl) {
-        const int nt = min(tp, x.nt - t);
+        const int nt = min(tp, x.nt - t), qs = nl % kQStages;
+        if (nl >= kQStages) wait(&ctl->qempty[qs], (nl / kQStages - 1) & 1);
+        if (*abort_flag) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&ctl->qfull[qs]);
+          mbar_expect_tx(bar, (uint32_t)(tp * a.G * D * 2));
+          for (int bx = 0; bx < D / 64; ++bx)
+            tma_load_4d(smem_u32(q_smem + qs * q_bytes + bx * N_ * 128), &mapQ, bx * 64, x.h * a.G,
+                        x.row + t, 0, bar);
+        }
         float next[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -379,6 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (have) hand_on(nl - 1);
       have = false;
     }
+    if (lane == 0) {   // every copy lands before the CTA may exit (bounded waits)
+#pragma unroll 1
+      for (uint32_t i = nl > kQStages ? nl - kQStages : 0; i < nl; ++i)
+        drain_phase(&ctl->qfull[i % kQStages], (i / kQStages) & 1);
+    }
+    __syncwarp();
   } else {
     // ---- sums: a thread to a key, the two groups in turn to a step --------------------------
     const int g = (warp - 4) >> 2, key = threadIdx.x - 128 - g * 128;
@@ -399,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt = min(tp, x.nt - t), cols = nt * a.G, first = x.first + t;
         // the rows of the step that see this key: columns [lo, hi)
         int lo = 0, hi = cols;
-        const bool edge = (cols & 15) || j0 + kTile - 1 > first ||
+        const bool edge = (cols % W) || j0 + kTile - 1 > first ||
                           (a.window && j0 <= first + nt - 1 - a.window);
         if (edge) {
           lo = max(0, j - first) * a.G;
@@ -409,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&ctl->sfull[bb], (nl / kBufs) & 1);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if (edge)
-          sum += weigh(at + bb * kTile, ctl->ref[ls], c2, cols, lo, hi, std::true_type());
+          sum += weigh<W>(at + bb * kTile, ctl->ref[ls], c2, cols, lo, hi, std::true_type());
         else
-          sum += weigh(at + bb * kTile, ctl->ref[ls], c2, cols, lo, hi, std::false_type());
+          sum += weigh<W>(at + bb * kTile, ctl->ref[ls], c2, cols, lo, hi, std::false_type());
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -459,14 +481,16 @@ cudaError_t run(const Args& a, const Maps& maps, int tp, const float* lse, float
   int ks = (227 * 1024 - fixed) / tile;
   if (ks > kMaxStages) ks = kMaxStages;
   const size_t smem = (size_t)fixed + (size_t)ks * tile;
-  cudaError_t err = cudaFuncSetAttribute(k_paged_mass<T, D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // a few rows go 16 columns at a time (the others may not be there at all), many 32
+  const auto kernel = n <= 16 ? k_paged_mass<T, D, 16> : k_paged_mass<T, D, 32>;
+  cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   const int nsm = sm_count();
   const int64_t tiles = (((int64_t)a.table_ld << a.lps) + kTile - 1) / kTile;
   const int64_t most = (int64_t)a.n_seqs * a.Hk * tiles;
-  return launch(k_paged_mass<T, D>, dim3((unsigned)(most < nsm ? most : nsm)), kThreads, smem, s, a,
-                tp, n, ks, lse, mass, decay, maps.k, maps.q);
+  return launch(kernel, dim3((unsigned)(most < nsm ? most : nsm)), kThreads, smem, s, a, tp, n, ks,
+                lse, mass, decay, maps.k, maps.q);
 }
 
 }  // namespace

@@ -186,41 +186,46 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int box_bytes, int 
   return base + (chunk >> 3) * box_bytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-// Load one key tile (entries [j0, j0 + 128) of head h) by one warp: a lane for each
-// (page, 64-dim box).  Entries at or past `end` and pages outside the pool arrive as zeros.
-// A mask of the tile's 16-key groups in pages outside the pool is returned in every lane and,
-// with `bad_out`, stored before the copy's barrier is armed: whoever has waited for the tile may
-// read it.
-__device__ __forceinline__ uint32_t load_key_tile(const Args& a, const CUtensorMap* map,
-                                                  uint32_t dst, uint32_t bar, int b, int h, int j0,
-                                                  int end, int lane, uint32_t* bad_out) {
+// Loading a key tile (entries [j0, j0 + 128) of head h) by one warp, a lane for each (page, 64-dim
+// box).  Its lane's page comes first, so that the lookup can be on its way ahead of time.  Entries
+// at or past `end` and pages outside the pool arrive as zeros.
+struct TilePages {
+  int page;              // of this lane's box; past the last page: zeros
+  uint32_t bad;          // in every lane: the tile's 16-key groups in pages outside the pool
+};
+__device__ __forceinline__ TilePages find_pages(const Args& a, int b, int j0, int end, int lane) {
   const int per = min(1 << a.lps, kTile);          // rows of one box
-  const int pages = kTile / per, boxes = a.D >> 6;
-  const int pg = lane % pages, bx = lane / pages;  // lane < pages * boxes <= 16 loads
-  const int j = j0 + pg * per;
-  int page = a.n_pages;                            // past the last page: zeros
+  const int pages = kTile / per;
+  const int j = j0 + (lane % pages) * per;
+  TilePages x{a.n_pages, 0u};
   bool bad = false;
-  if (bx < boxes && j < end) {
+  if (lane < pages * (a.D >> 6) && j < end) {      // at most 16 loads
     const int p = page_of(a, b, j);
     bad = p < 0;
-    if (!bad) page = p;
+    if (!bad) x.page = p;
   }
-  uint32_t mask = __ballot_sync(0xffffffffu, bad && bx == 0);
+  const uint32_t mask = __ballot_sync(0xffffffffu, bad && lane < pages);
   if (mask) {                                      // rare: from pages to groups
-    uint32_t groups = 0;
 #pragma unroll 1
-    for (int g = 0; g < 8; ++g) groups |= ((mask >> (g * 16 / per)) & 1u) << g;
-    mask = groups;
+    for (int g = 0; g < 8; ++g) x.bad |= ((mask >> (g * 16 / per)) & 1u) << g;
   }
+  return x;
+}
+// With `bad_out` the mask is stored before the copy's barrier is armed: whoever has waited for
+// the tile may read it.
+__device__ __forceinline__ void load_key_tile(const Args& a, const CUtensorMap* map, uint32_t dst,
+                                              uint32_t bar, const TilePages& x, int h, int j0,
+                                              int lane, uint32_t* bad_out) {
+  const int per = min(1 << a.lps, kTile), pages = kTile / per;
+  const int pg = lane % pages, bx = lane / pages;
   if (lane == 0) {
-    if (bad_out) *reinterpret_cast<volatile uint32_t*>(bad_out) = mask;
+    if (bad_out) *reinterpret_cast<volatile uint32_t*>(bad_out) = x.bad;
     mbar_expect_tx(bar, (uint32_t)(kTile * a.D * 2));
   }
   __syncwarp();
-  if (bx < boxes)
-    tma_load_4d(dst + bx * (kTile * 128) + pg * per * 128, map, bx * 64, j & ((1 << a.lps) - 1), h,
-                page, bar);
-  return mask;
+  if (bx < (a.D >> 6))
+    tma_load_4d(dst + bx * (kTile * 128) + pg * per * 128, map, bx * 64,
+                (j0 + pg * per) & ((1 << a.lps) - 1), h, x.page, bar);
 }
 
 // The non-finite values of V that a row at entry `pos` sees in the tiles where they were taken
