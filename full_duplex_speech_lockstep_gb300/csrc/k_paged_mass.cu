@@ -2,12 +2,13 @@
 //
 //   mass_j = decay mass_j + sum over rows (t, g) of the chunk that see j of exp(s_j - lse)
 // with the rows and scores of k_paged_attn.cu and the row sums that it returned.  A unit is
-// (sequence, key head, 128-key tile); the rows that see the tile go past it in steps of up to
-// 128 rows:
+// (sequence, key head, pair of 128-key tiles); the rows that see the pair go past it in steps of
+// up to 128 rows:
 //   S' = K Q^T   M = 128 keys, N = the step's rows, on the 5th-generation tensor cores
 // so that a thread owns a key (a tensor-memory lane) and adds up its weights in row order:
-// no sum crosses threads but one (two groups take alternate steps), nothing is added
-// atomically, and the bits are the same in every run.
+// no sum crosses threads, nothing is added atomically, and the bits are the same in every run.
+// (With one tile to a unit each step's 32 KB of rows served 128 keys only, and reading them
+// from L2 bounded the kernel: 114 us for 4 x 300 rows over up to 16000 entries.)
 //
 // A CTA takes a run of consecutive units of about the same number of steps as the others:
 //   warp 0        producer: the units and their key tiles, by TMA
@@ -15,7 +16,7 @@
 //   warp 2        each key's old mass and page, a unit ahead
 //   warp 3        the steps' rows by TMA; each row's lse, a step ahead; rows that do not count:
 //                 infinity
-//   warps 4-7, 8-11   the sums, the two groups in turn to a step
+//   warps 4-7, 8-11   the sums of the pair's first and second tile
 #include <type_traits>
 
 #include "pp_paged.cuh"
@@ -29,20 +30,19 @@ constexpr int kThreads = 384;
 constexpr int kBufs = 4;             // S buffers of 128 columns: all of tensor memory
 constexpr int kAux = 8;              // steps and units that the memory warps may be ahead
 constexpr int kMaxStages = 8;
-constexpr int kQStages = 3;
+constexpr int kQStages = 2;
 
 struct Ctl {
   UnitRing ring;
   uint64_t kfull[kMaxStages], kempty[kMaxStages], qfull[kQStages], qempty[kQStages];
   uint64_t sfull[kBufs], sfree[kBufs];
   uint64_t lfull[kAux], lempty[kAux], ufull[kAux], uempty[kAux];
-  uint64_t done, meet;
+  uint64_t done;
   uint32_t tmem;
   int abort;
   alignas(16) float ref[kAux][kTile];   // lse * log2(e) of a step's rows
-  alignas(16) float old[kAux][kTile];   // decayed mass of a unit's keys
-  int page[kAux][8];                 // pages of its 16-key groups, -1 for none
-  float half[2][kTile];              // sums from one group to the other
+  alignas(16) float old[kAux][2 * kTile];   // decayed mass of a unit's keys
+  int page[kAux][16];                // pages of its 16-key groups, -1 for none
 };
 
 // Steps of rows of a unit, at most: what it costs.
@@ -56,8 +56,8 @@ struct Walk {
   const int64_t* pre;
   const int tp;
   int64_t at, end;      // cost before this unit, cost where the run ends
-  int b, h, tile;
-  int tiles, cost;      // of the sequence
+  int b, h, pair;
+  int pairs, cost;      // of the sequence
   Seq s;
   int j0, t0, t1;       // the unit's first key; the tokens that see some key of it
 
@@ -70,8 +70,8 @@ struct Walk {
     b = find_seq(pre, a.n_seqs, at);
     sequence();
     const int64_t i = (at - pre[b] + cost - 1) / cost;   // the first unit that starts in the run
-    h = (int)(i / tiles);
-    tile = (int)(i - (int64_t)h * tiles);
+    h = (int)(i / pairs);
+    pair = (int)(i - (int64_t)h * pairs);
     at = pre[b] + i * cost;
     if (h == a.Hk) next_sequence();
     unit();
@@ -79,11 +79,11 @@ struct Walk {
   __device__ __forceinline__ bool done() const { return at >= end; }
   __device__ __forceinline__ void sequence() {
     s = seq_of(a, b);
-    tiles = (s.len + kTile - 1) / kTile;
+    pairs = (s.len + 2 * kTile - 1) / (2 * kTile);
     cost = unit_cost(s, tp);
   }
   __device__ __forceinline__ void next_sequence() {
-    h = tile = 0;
+    h = pair = 0;
     do {
       ++b;
     } while (b < a.n_seqs && pre[b + 1] == pre[b]);
@@ -91,20 +91,20 @@ struct Walk {
   }
   __device__ __forceinline__ void next() {
     at += cost;
-    if (++tile == tiles) {
-      tile = 0;
+    if (++pair == pairs) {
+      pair = 0;
       if (++h == a.Hk) next_sequence();
     }
     unit();
   }
   __device__ __forceinline__ void unit() {
     if (done()) return;
-    j0 = tile * kTile;
+    j0 = pair * 2 * kTile;
     const int first = s.len - s.n;
     t0 = max(0, j0 - first);
     t1 = s.n;
     if (a.window)
-      t1 = (int)min((int64_t)s.n, (int64_t)min(j0 + kTile, s.len) - 1 + a.window - first);
+      t1 = (int)min((int64_t)s.n, (int64_t)min(j0 + 2 * kTile, s.len) - 1 + a.window - first);
     if (t1 < t0) t1 = t0;
   }
 };
@@ -202,13 +202,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kAux; ++i) {
       mbar_init(smem_u32(&ctl->lfull[i]), 1);
-      mbar_init(smem_u32(&ctl->lempty[i]), 4);
+      mbar_init(smem_u32(&ctl->lempty[i]), 8);
       mbar_init(smem_u32(&ctl->ufull[i]), 1);
       mbar_init(smem_u32(&ctl->uempty[i]), 8);
     }
     mbar_init(smem_u32(&ctl->done), 1);
     ring_init(ctl->ring, 11);            // MMA issuer, two memory warps, eight of sums
-    mbar_init(smem_u32(&ctl->meet), 8);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -225,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   prefix_units(pre, a.n_seqs, [&](int b) -> int64_t {
     const Seq s = seq_of(a, b);
     if (s.n == 0 && decay == 1.f) return 0;
-    return (int64_t)a.Hk * ((s.len + kTile - 1) / kTile) * unit_cost(s, tp);
+    return (int64_t)a.Hk * ((s.len + 2 * kTile - 1) / (2 * kTile)) * unit_cost(s, tp);
   });
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = ctl->tmem;
@@ -234,28 +233,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- producer -------------------------------------------------------------------------
     uint32_t nk = 0, nu = 0, seen_bad = 0;
     Walk x(a, pre, tp);
-    TilePages next{};
-    if (!x.done()) next = find_pages(a, x.b, x.j0, x.s.len, lane);
+    TilePages next[2];
+    auto find = [&] {
+      if (x.done()) return;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        next[i] = find_pages(a, x.b, x.j0 + i * kTile, x.s.len, lane);
+    };
+    find();
 #pragma unroll 1
     while (!x.done() && !*abort_flag) {
       // this unit, and the next one's pages on their way
-      const Unit u{x.b, x.h, x.s.row0 + x.t0, x.t1 - x.t0, x.s.len - x.s.n + x.t0, x.tile,
-                   x.tile + 1, 0, x.s.len, 0, 1, 0};
-      const TilePages now = next;
-      const int j0 = x.j0;
+      const Unit u{x.b, x.h, x.s.row0 + x.t0, x.t1 - x.t0, x.s.len - x.s.n + x.t0, 2 * x.pair,
+                   min(2 * x.pair + 2, (x.s.len + kTile - 1) / kTile), 0, x.s.len, 0, 1, 0};
+      const TilePages now[2] = {next[0], next[1]};
       x.next();
-      if (!x.done()) next = find_pages(a, x.b, x.j0, x.s.len, lane);
+      find();
       // a unit that no row sees has nothing to add; without decay it is left out
       if (u.nt == 0 && decay == 1.f) continue;
       put_unit(a, ctl->ring, nu++, u, lane, abort_flag);
       if (u.nt == 0) continue;
-      const int ks = nk % KS;
-      if (nk >= KS) wait(&ctl->kempty[ks], (nk / KS - 1) & 1);
-      if (*abort_flag) break;
-      load_key_tile(a, &mapK, smem_u32(smem + ks * kTileBytes), smem_u32(&ctl->kfull[ks]), now, u.h,
-                    j0, lane, nullptr);
-      seen_bad |= now.bad;
-      ++nk;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (u.tile0 + i >= u.tile1) break;
+        const int ks = nk % KS;
+        if (nk >= KS) wait(&ctl->kempty[ks], (nk / KS - 1) & 1);
+        if (*abort_flag) break;
+        load_key_tile(a, &mapK, smem_u32(smem + ks * kTileBytes), smem_u32(&ctl->kfull[ks]), now[i],
+                      u.h, (u.tile0 + i) * kTile, lane, nullptr);
+        seen_bad |= now[i].bad;
+        ++nk;
+      }
     }
     Unit last{};
     last.b = -1;
@@ -272,33 +280,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const uint32_t id = (1u << 4) | Num<T>::kMmaTypes | ((uint32_t)(kTile >> 4) << 24) |
                           ((uint32_t)(N_ >> 3) << 17);
-      uint32_t nk = 0, nq = 0;
+      uint32_t nk = 0, nq = 0, n2 = 0;   // n2: steps of units with two tiles
       Unit x;
+      auto scores = [&](uint32_t buf, int ks, uint32_t qb) {
+        const uint32_t kb = smem_u32(smem + ks * kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16(tmem + buf * kTile, smem_desc(kb + (kk >> 2) * (kTile * 128) + (kk & 3) * 32),
+                    smem_desc(qb + (kk >> 2) * (N_ * 128) + (kk & 3) * 32), id, kk > 0);
+        umma_commit(smem_u32(&ctl->sfull[buf]));
+      };
 #pragma unroll 1
       for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, true, abort_flag); ++nu) {
         if (x.nt == 0) continue;
-        const int ks = nk % KS;
-        wait(&ctl->kfull[ks], (nk / KS) & 1);
-        ++nk;
-        const uint32_t kb = smem_u32(smem + ks * kTileBytes);
+        const bool two = x.tile1 - x.tile0 == 2;
+        const int k0 = nk % KS, k1 = (nk + 1) % KS;
+        wait(&ctl->kfull[k0], (nk / KS) & 1);
+        if (two) wait(&ctl->kfull[k1], ((nk + 1) / KS) & 1);
+        nk += two ? 2 : 1;
 #pragma unroll 1
         for (int t = 0; t < x.nt; t += tp) {
-          const int qs = nq % kQStages, bb = nq % kBufs;
+          const int qs = nq % kQStages;
+          const uint32_t b0 = (nq & 1) * 2, b1 = (n2 & 1) * 2 + 1;
           wait(&ctl->qfull[qs], (nq / kQStages) & 1);
-          if (nq >= kBufs) wait(&ctl->sfree[bb], (nq / kBufs - 1) & 1);
+          if (nq >= 2) wait(&ctl->sfree[b0], ((nq >> 1) - 1) & 1);
           if (*abort_flag) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t qb = smem_u32(q_smem + qs * q_bytes);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16(tmem + bb * kTile,
-                      smem_desc(kb + (kk >> 2) * (kTile * 128) + (kk & 3) * 32),
-                      smem_desc(qb + (kk >> 2) * (N_ * 128) + (kk & 3) * 32), id, kk > 0);
-          umma_commit(smem_u32(&ctl->sfull[bb]));
+          scores(b0, k0, qb);
+          if (two) {
+            if (n2 >= 2) wait(&ctl->sfree[b1], ((n2 >> 1) - 1) & 1);
+            if (*abort_flag) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            scores(b1, k1, qb);
+            ++n2;
+          }
           umma_commit(smem_u32(&ctl->qempty[qs]));
           ++nq;
         }
-        umma_commit(smem_u32(&ctl->kempty[ks]));
+        umma_commit(smem_u32(&ctl->kempty[k0]));
+        if (two) umma_commit(smem_u32(&ctl->kempty[k1]));
       }
       // every MMA is done before tensor memory is given back (bounded wait)
       umma_commit(smem_u32(&ctl->done));
@@ -306,34 +327,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    // ---- old mass and pages: four keys to a lane; a unit's loads are issued before the last
+    // ---- old mass and pages: eight keys to a lane; a unit's loads are issued before the last
     // unit's values are handed on
     Unit x;
-    float old[4] = {};
+    float old[8] = {};
     int page = -1;
     bool have = false;
 #pragma unroll 1
     for (uint32_t nu = 0;; ++nu) {
-      float next[4] = {};
+      float next[8] = {};
       int next_page = -1;
       const bool more = get_unit(a, ctl->ring, nu, x, lane, false, abort_flag);
       if (more) {
-        const int j = x.tile0 * kTile + lane * 4;        // one page: 4 divides the page size
+        const int j = x.tile0 * kTile + lane * 8;        // one page: 8 divides the page size
         next_page = j < x.stop ? page_of(a, x.b, j) : -1;
         if (next_page >= 0 && decay != 0.f) {
           const float* src =
               mass + ((((int64_t)next_page * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1)));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 8; ++k)
             if (j + k < x.stop) next[k] = src[k];
         }
       }
       if (have) {
         const uint32_t n = nu - 1, us = n % kAux;
         if (n >= kAux) wait(&ctl->uempty[us], (n / kAux - 1) & 1);
-        *reinterpret_cast<float4*>(&ctl->old[us][lane * 4]) =
-            make_float4(old[0] * decay, old[1] * decay, old[2] * decay, old[3] * decay);
-        if ((lane & 3) == 0) ctl->page[us][lane >> 2] = page;
+        float4* to = reinterpret_cast<float4*>(&ctl->old[us][lane * 8]);
+        to[0] = make_float4(old[0] * decay, old[1] * decay, old[2] * decay, old[3] * decay);
+        to[1] = make_float4(old[4] * decay, old[5] * decay, old[6] * decay, old[7] * decay);
+        if ((lane & 1) == 0) ctl->page[us][lane >> 1] = page;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->ufull[us]));
       }
@@ -341,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       have = true;
       page = next_page;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) old[k] = next[k];
+      for (int k = 0; k < 8; ++k) old[k] = next[k];
     }
   } else if (warp == 3) {
     // ---- the steps' rows by TMA, and lse: four rows to a lane; a step's loads are issued before
@@ -402,63 +424,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ---- sums: a thread to a key, the two groups in turn to a step --------------------------
-    const int g = (warp - 4) >> 2, key = threadIdx.x - 128 - g * 128;
+    // ---- sums: a thread to a key, a group to a tile -----------------------------------------
+    const int g = (warp - 4) >> 2, key = threadIdx.x - 128;
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint64_t c2 = f32x2(a.c, a.c);
-    uint32_t nl = 0, nu = 0, nm = 0, meets = 0;
+    uint32_t nl = 0, ns = 0;           // steps; this group's
     Unit x;
 #pragma unroll 1
-    for (; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
-      const int j0 = x.tile0 * kTile, j = j0 + key;
-      const int steps = (x.nt + tp - 1) / tp;
+    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+      const int j0 = (x.tile0 + g) * kTile, j = x.tile0 * kTile + key;
+      const bool mine = x.tile0 + g < x.tile1;
       float sum = 0.f;
-      int t = 0;
 #pragma unroll 1
-      for (int i = 0; i < steps; ++i, ++nl, t += tp) {
-        if ((nl & 1) != g) continue;
-        const int bb = nl % kBufs, ls = nl % kAux;
-        const int nt = min(tp, x.nt - t), cols = nt * a.G, first = x.first + t;
-        // the rows of the step that see this key: columns [lo, hi)
-        int lo = 0, hi = cols;
-        const bool edge = (cols % W) || j0 + kTile - 1 > first ||
-                          (a.window && j0 <= first + nt - 1 - a.window);
-        if (edge) {
-          lo = max(0, j - first) * a.G;
-          if (a.window) hi = (int)min((int64_t)hi, ((int64_t)j + a.window - first) * a.G);
-        }
+      for (int t = 0; t < x.nt; t += tp, ++nl) {
+        const int ls = nl % kAux;
         wait(&ctl->lfull[ls], (nl / kAux) & 1);
-        wait(&ctl->sfull[bb], (nl / kBufs) & 1);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (edge)
-          sum += weigh<W>(at + bb * kTile, ctl->ref[ls], c2, cols, lo, hi, std::true_type());
-        else
-          sum += weigh<W>(at + bb * kTile, ctl->ref[ls], c2, cols, lo, hi, std::false_type());
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&ctl->sfree[bb]));
-          mbar_arrive(smem_u32(&ctl->lempty[ls]));
+        if (mine) {
+          const uint32_t buf = (ns & 1) * 2 + g;
+          const int nt = min(tp, x.nt - t), cols = nt * a.G, first = x.first + t;
+          // the rows of the step that see this key: columns [lo, hi)
+          int lo = 0, hi = cols;
+          const bool edge = (cols % W) || j0 + kTile - 1 > first ||
+                            (a.window && j0 <= first + nt - 1 - a.window);
+          if (edge) {
+            lo = (int)min((int64_t)cols, (int64_t)max(0, j - first) * a.G);
+            if (a.window) {
+              const int64_t end = ((int64_t)j + a.window - first) * a.G;
+              hi = (int)max((int64_t)0, min((int64_t)hi, end));
+            }
+          }
+          wait(&ctl->sfull[buf], (ns >> 1) & 1);
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (edge)
+            sum += weigh<W>(at + buf * kTile, ctl->ref[ls], c2, cols, lo, hi, std::true_type());
+          else
+            sum += weigh<W>(at + buf * kTile, ctl->ref[ls], c2, cols, lo, hi, std::false_type());
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->sfree[buf]));
+          ++ns;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->lempty[ls]));
       }
-      // the group of the unit's last step writes; the other one's sum comes through shared
-      // memory, two units deep
-      const int writer = steps > 0 ? (nl - 1) & 1 : nu & 1;
-      if (steps > 1) {
-        if (g != writer) ctl->half[nm & 1][key] = sum;
-        sync_warps(a, &ctl->meet, meets, lane, abort_flag);
-        if (g == writer) sum += ctl->half[nm & 1][key];
-        ++nm;
-      }
-      // (both groups see every phase of the old values' stages)
       const int us = nu % kAux;
       wait(&ctl->ufull[us], (nu / kAux) & 1);
-      if (g == writer) {
-        const int p = ctl->page[us][key >> 4];
-        sum += ctl->old[us][key];
-        if (p >= 0 && j < x.stop)
-          mass[(((int64_t)p * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1))] = sum;
-      }
+      const int p = ctl->page[us][key >> 4];
+      sum += ctl->old[us][key];
+      if (p >= 0 && j < x.stop)
+        mass[(((int64_t)p * a.Hk + x.h) << a.lps) + (j & ((1 << a.lps) - 1))] = sum;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->uempty[us]));
     }
