@@ -35,6 +35,9 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kRowsT = 128;          // rows of a row tile
+constexpr int kMaxParts = 304;       // split units of a call, at most: two to an SM
+constexpr int kMostParts = 16;       // parts of one unit
+constexpr int kUnitRows = 2 * kRowsT;
 constexpr float kLag = 8.f;          // a row's maximum may exceed its reference by this (log2)
 // registers a thread: launched with 168; the softmax warps take what the others give up
 // (80 + 2 x 208 = 496 <= 3 x 168 for each three threads)
@@ -62,32 +65,57 @@ struct Ctl {
   int abort;
 };
 
-__device__ __forceinline__ int seq_splits(const Args& a, const Seq& s, int tp, int ns) {
-  const int all = (s.len + kTile - 1) / kTile;
-  const int most = a.window ? min(all, (int)(((int64_t)a.window + 2 * tp - 2) / kTile) + 2) : all;
-  return max(1, min(ns, most / 8));    // a split has at least eight tiles of keys
-}
-
-__device__ __forceinline__ int seq_units(const Args& a, int b, int tp, int ns) {
+// Units before any split: (pair of row tiles, key head).
+__device__ __forceinline__ int seq_units(const Args& a, int b, int tp) {
   const Seq s = seq_of(a, b);
-  if (s.n == 0) return 0;
-  return a.Hk * ((s.n + 2 * tp - 1) / (2 * tp)) * seq_splits(a, s, tp, ns);
+  return a.Hk * ((s.n + 2 * tp - 1) / (2 * tp));
 }
 
-__device__ __forceinline__ Unit unit_of(const Args& a, const int* pre, int u, int tp, int ns) {
+// The units run in waves of one to an SM.  Those of the last wave, if it is not full, are split
+// over their keys, each in `parts`, so that its end comes sooner: of `units`, the first `whole`
+// stay in one piece.
+struct Waves {
+  int units, whole, parts;
+};
+__device__ __forceinline__ Waves waves_of(int units, int most_parts) {
+  Waves w;
+  w.units = units;
+  const int rest = units % (int)gridDim.x;
+  w.whole = units - rest;
+  w.parts = 1;
+  // time of the last wave in 1/64 of a unit's; 2 for each part's start and join
+  int best = 64;
+  for (int p = 2; p <= most_parts && rest * p <= kMaxParts; ++p) {
+    const int time = (rest * p + (int)gridDim.x - 1) / (int)gridDim.x * (64 / p + 4);
+    if (rest > 0 && time < best) {
+      best = time;
+      w.parts = p;
+    }
+  }
+  if (w.parts == 1) w.whole = units;
+  return w;
+}
+
+// A split has at least four tiles of keys: the last ones of a short sequence may have none.
+__device__ __forceinline__ Unit unit_of(const Args& a, const int* pre, const Waves& w, int u,
+                                        int tp) {
   Unit x;
   x.tag = u + 1;
+  int slot = 0, part = 0;
+  x.ns = 1;
+  if (u >= w.whole) {
+    slot = (u - w.whole) / w.parts;
+    part = u - w.whole - slot * w.parts;
+    x.ns = w.parts;
+    u = w.whole + slot;
+  }
+  x.split = slot * kMostParts + part;
   x.b = find_seq(pre, a.n_seqs, u);
   const Seq s = seq_of(a, x.b);
   u -= pre[x.b];
-  const int pairs = (s.n + 2 * tp - 1) / (2 * tp);
-  x.ns = seq_splits(a, s, tp, ns);
   // the last pairs, whose rows see most, come first; heads vary fastest
-  const int per = a.Hk * x.ns;
-  const int p = pairs - 1 - u / per;
-  u %= per;
-  x.h = u / x.ns;
-  x.split = u - x.h * x.ns;
+  const int p = (s.n + 2 * tp - 1) / (2 * tp) - 1 - u / a.Hk;
+  x.h = u % a.Hk;
   const int t0 = p * 2 * tp;
   x.row = s.row0 + t0;
   x.nt = min(2 * tp, s.n - t0);
@@ -95,8 +123,8 @@ __device__ __forceinline__ Unit unit_of(const Args& a, const int* pre, int u, in
   x.stop = max(x.first + x.nt, 0);
   x.low = a.window ? min(max(x.first - a.window + 1, 0), x.stop) : 0;
   const int ta = x.low / kTile, tb = (x.stop + kTile - 1) / kTile;
-  const int st = (tb - ta + x.ns - 1) / x.ns;
-  x.tile0 = min(ta + x.split * st, tb);
+  const int st = max((tb - ta + x.ns - 1) / x.ns, x.ns > 1 ? 4 : 0);
+  x.tile0 = min(ta + part * st, tb);
   x.tile1 = min(x.tile0 + st, tb);
   return x;
 }
@@ -168,7 +196,8 @@ __device__ __forceinline__ bool finite_only(uint32_t& w) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_paged_attn_tc(const __grid_constant__ Args a, const int tp, const int ns_cap, const __grid_constant__ AttnOut o,
+    k_paged_attn_tc(const __grid_constant__ Args a, const int tp, const int most_parts,
+                    const __grid_constant__ AttnOut o,
                     const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapV,
                     const __grid_constant__ CUtensorMap mapQ, const void* v_pages) {
@@ -210,10 +239,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   pdl_wait_and_trigger();
   pdl_trigger();
-  prefix_units(pre, a.n_seqs, [&](int b) { return seq_units(a, b, tp, ns_cap); });
+  prefix_units(pre, a.n_seqs, [&](int b) { return seq_units(a, b, tp); });
+  const Waves waves = waves_of(pre[a.n_seqs], most_parts);
+  // what the join needs to find its rows: the waves and the sequences' units
+  if (blockIdx.x == 0 && most_parts > 1) {
+    if (threadIdx.x == 0) {
+      o.plan[0] = waves.units;
+      o.plan[1] = waves.whole;
+      o.plan[2] = waves.parts;
+    }
+    for (int b = threadIdx.x; b <= a.n_seqs; b += kThreads) o.plan[4 + b] = pre[b];
+  }
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = ctl->tmem;
-  const int units = pre[a.n_seqs];
+  const int units = waves.whole + (waves.units - waves.whole) * waves.parts;
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
 
   if (warp < 4) {
@@ -223,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t nq = 0, nl = 0, nu = 0, seen_bad = 0;
 #pragma unroll 1
       for (int u = blockIdx.x; u < units && !*abort_flag; u += gridDim.x) {
-        const Unit x = unit_of(a, pre, u, tp, ns_cap);
+        const Unit x = unit_of(a, pre, waves, u, tp);
         put_unit(a, ctl->ring, nu++, x, lane, abort_flag);
         if (x.tile0 == x.tile1) continue;
         const int tiles = x.nt > tp ? 2 : 1;
@@ -504,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int H = a.Hk * a.G;
       const int token = x.row + t * tp + tk, hd = x.h * a.G + r - tk * a.G;
       const int64_t row = (int64_t)token * H + hd;
-      const int64_t rec = row * ns_cap + x.split;
+      const int slot = x.split / kMostParts, part = x.split % kMostParts;
+      const int64_t rec = ((int64_t)slot * kUnitRows + t * kRowsT + r) * x.ns + part;
       const bool whole = x.ns == 1;
       bool wild = false;
       if (nt > 0) {
@@ -573,64 +613,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Join the splits of each row: one warp to a (row, head).
+// Join the parts of each split unit's rows: one warp to a row.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
-    k_paged_join_rows(const __grid_constant__ Args a, const int tp, const int ns_cap, const __grid_constant__ AttnOut o) {
+    k_paged_join_units(const __grid_constant__ Args a, const int tp,
+                       const __grid_constant__ AttnOut o) {
   pdl_wait_and_trigger();
   pdl_trigger();
   const int lane = threadIdx.x & 31, H = a.Hk * a.G;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);   // below 2^31 + 3
-  const int row = (int)((uint32_t)id / (uint32_t)H);
-  if (row >= a.T) return;
-  int lo = 0, hi = a.n_seqs;           // the last sequence that starts at or before the row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid] <= row) lo = mid; else hi = mid;
-  }
-  const Seq s = seq_of(a, lo);
-  if (row < s.row0 || row >= s.row0 + s.n) return;
-  const int ns = seq_splits(a, s, tp, ns_cap);
-  if (ns == 1) return;
-  join_row<T, D>(o.part, o.part_ml, id * ns_cap, ns, reinterpret_cast<T*>(o.out) + id * D,
-                 o.lse ? o.lse + id : nullptr, lane);
+  const int id = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int slot = id / kUnitRows, at = id - slot * kUnitRows;   // unit, row of its two tiles
+  const int t = at / kRowsT, r = at - t * kRowsT;
+  const int whole = o.plan[1], u = whole + slot, ns = o.plan[2];
+  if (u >= o.plan[0] || r >= tp * a.G) return;
+  const int* pre = o.plan + 4;
+  const int b = find_seq(pre, a.n_seqs, u);
+  const Seq s = seq_of(a, b);
+  const int k = u - pre[b];
+  const int p = (s.n + 2 * tp - 1) / (2 * tp) - 1 - k / a.Hk;
+  const int tk = r / a.G, token = p * 2 * tp + t * tp + tk;
+  if (token >= s.n) return;
+  const int64_t row = (int64_t)(s.row0 + token) * H + k % a.Hk * a.G + r - tk * a.G;
+  join_row<T, D>(o.part, o.part_ml, (int64_t)id * ns, ns, reinterpret_cast<T*>(o.out) + row * D,
+                 o.lse ? o.lse + row : nullptr, lane);
 }
 
 template <typename T, int D>
 cudaError_t run(const Args& a, const LongPlan& p, const Maps& maps, const AttnOut& o,
                 const void* v_pages, cudaStream_t s) {
   const size_t smem = Cfg<D>::kCtlOff + sizeof(Ctl) + (size_t)(a.n_seqs + 1) * sizeof(int) + 1024;
+  static_assert(Cfg<D>::kCtlOff + sizeof(Ctl) + (kMaxSeqs + 1) * sizeof(int) + 1024 <= 227 * 1024,
+                "long-chunk attention shared memory");
   cudaError_t err = cudaFuncSetAttribute(k_paged_attn_tc<T, D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  const int64_t most = ((int64_t)a.T / (2 * p.tp) + a.n_seqs) * a.Hk * p.ns;
+  const int64_t most = p.units * p.parts;
   const int nsm = sm_count();
   err = launch(k_paged_attn_tc<T, D>, dim3((unsigned)(most < nsm ? most : nsm)), kThreads, smem, s,
-               a, p.tp, p.ns, o, maps.k, maps.v, maps.q, v_pages);
-  if (err != cudaSuccess || p.ns == 1) return err;
-  const int64_t rows = (int64_t)a.T * a.Hk * a.G;
-  return launch(k_paged_join_rows<T, D>, dim3((unsigned)((rows + 3) / 4)), 128, 0, s, a, p.tp, p.ns,
-                o);
+               a, p.tp, p.parts, o, maps.k, maps.v, maps.q, v_pages);
+  if (err != cudaSuccess || p.parts == 1) return err;
+  const int64_t split = p.units < nsm ? p.units : nsm;   // units of the last wave, at most
+  return launch(k_paged_join_units<T, D>, dim3((unsigned)(split * kUnitRows / 4)), 128, 0, s, a,
+                p.tp, o);
 }
 
 }  // namespace
 
-LongPlan long_plan(const Args& a, int T, int max_q) {
+LongPlan long_plan(const Args& a, int T) {
   LongPlan p{};
   p.tp = kRowsT / a.G;
-  // sequences as long as max_q, and the units they make without a split; fewer than two for
-  // each of the 152 SMs: split the keys
-  const int64_t q = max_q < T ? max_q : (T < 1 ? 1 : T);
-  int64_t seqs = (T + q - 1) / q;
-  if (seqs > a.n_seqs) seqs = a.n_seqs;
-  const int64_t units = seqs * a.Hk * ((q + 2 * p.tp - 1) / (2 * p.tp));
-  int64_t ns = units < 1 ? 1 : (2 * 152 + units - 1) / units;
-  const int64_t tiles = (((int64_t)a.table_ld << a.lps) + kTile - 1) / kTile;
-  if (ns > tiles / 8) ns = tiles / 8;
-  p.ns = (int)(ns < 1 ? 1 : ns > 16 ? 16 : ns);
-  const size_t recs = (size_t)T * a.Hk * a.G * p.ns;
-  p.rec_bytes = p.ns == 1 ? 0 : (recs * a.D * sizeof(float) + 255) & ~(size_t)255;
-  p.ml_bytes = p.ns == 1 ? 0 : (recs * sizeof(float2) + 255) & ~(size_t)255;
+  p.units = ((int64_t)T / (2 * p.tp) + a.n_seqs) * a.Hk;
+  const int64_t parts = (((int64_t)a.table_ld << a.lps) + 4 * kTile - 1) / (4 * kTile);
+  p.parts = parts < 1 ? 1 : parts > kMostParts ? kMostParts : (int)parts;
+  const int64_t units = p.units * p.parts < kMaxParts ? p.units * p.parts : kMaxParts;
+  const size_t recs = p.parts == 1 ? 0 : (size_t)units * kUnitRows;
+  p.rec_bytes = recs * a.D * sizeof(float);
+  p.ml_bytes = recs * sizeof(float2);
+  p.plan_bytes = (size_t)(a.n_seqs + 5) * sizeof(int);
   return p;
 }
 

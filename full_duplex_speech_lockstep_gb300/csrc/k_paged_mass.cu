@@ -15,7 +15,7 @@
 //   warp 1        one thread issues the MMAs, up to four steps ahead of the sums
 //   warp 2        each key's old mass and page, a unit ahead
 //   warp 3        the steps' rows by TMA; each row's lse, a step ahead; rows that do not count:
-//                 infinity
+//                 minus infinity
 //   warps 4-7, 8-11   the sums of the pair's first and second tile
 #include <type_traits>
 
@@ -40,7 +40,7 @@ struct Ctl {
   uint64_t done;
   uint32_t tmem;
   int abort;
-  alignas(16) float ref[kAux][kTile];   // lse * log2(e) of a step's rows
+  alignas(16) float ref[kAux][kTile];   // -lse * log2(e) of a step's rows
   alignas(16) float old[kAux][2 * kTile];   // decayed mass of a unit's keys
   int page[kAux][16];                // pages of its 16-key groups, -1 for none
 };
@@ -120,7 +120,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t r[16]) {
       : "r"(t));
 }
 
-// Sum of 2^(s c - ref) over the columns [0, cols) of a lane, those outside [lo, hi) left out
+// Sum of 2^(s c + ref) over the columns [0, cols) of a lane, those outside [lo, hi) left out
 // (`masked`); cols is a multiple of W otherwise.  The next W columns are on their way from tensor
 // memory while these are summed.
 template <int W, typename M>
@@ -137,9 +137,9 @@ __device__ __forceinline__ float weigh(uint32_t at, const float* ref, uint64_t c
     for (int i = 0; i < W / 4; ++i) {
       const float4 z = reinterpret_cast<const float4*>(ref + c0)[i];
       const uint64_t e0 = fma2((uint64_t)r[4 * i] | ((uint64_t)r[4 * i + 1] << 32), c2,
-                               f32x2(-z.x, -z.y));
+                               f32x2(z.x, z.y));
       const uint64_t e1 = fma2((uint64_t)r[4 * i + 2] | ((uint64_t)r[4 * i + 3] << 32), c2,
-                               f32x2(-z.z, -z.w));
+                               f32x2(z.z, z.w));
       float p[4] = {exp2_approx(lo_of(e0)), exp2_approx(hi_of(e0)), exp2_approx(lo_of(e1)),
                     exp2_approx(hi_of(e1))};
       if constexpr (M::value) {
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows that are not there, or that saw nothing, give nothing
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        ctl->ref[ls][lane + k * 32] = z[k] == -INFINITY ? INFINITY : z[k] * kLog2e;
+        ctl->ref[ls][lane + k * 32] = z[k] == -INFINITY ? -INFINITY : z[k] * -kLog2e;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->lfull[ls]));
     };

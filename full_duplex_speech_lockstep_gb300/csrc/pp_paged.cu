@@ -158,8 +158,8 @@ size_t pp_paged_attention_scratch_bytes(const pp_paged_kv* kv, int n_heads, int 
   a.G = n_heads / kv->n_kv_heads;
   a.window = effective_window(kv, window);
   if (is_long(a, max_q)) {
-    const LongPlan p = long_plan(a, T, max_q);
-    return p.rec_bytes + p.ml_bytes + 256;
+    const LongPlan p = long_plan(a, T);
+    return p.rec_bytes + p.ml_bytes + p.plan_bytes + 256;
   }
   const AttnPlan p = attn_plan(a, max_q);
   return p.rec_bytes + p.ml_bytes + 256;
@@ -193,9 +193,10 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
   Maps maps;
   if (!page_map(&maps.k, kv, kv->k) || !page_map(&maps.v, kv, kv->v)) return PP_EINVAL;
   if (is_long(a, max_q)) {
-    const LongPlan p = long_plan(a, T, max_q);
+    const LongPlan p = long_plan(a, T);
     if (!query_map(&maps.q, a, kv->type, q, q_stride, p.tp)) return PP_EINVAL;
     o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) + p.rec_bytes);
+    o.plan = reinterpret_cast<int*>(reinterpret_cast<char*>(scratch) + p.rec_bytes + p.ml_bytes);
     return rc(launch_paged_attn_tc(a, kv->type, p, maps, o, kv->v, (cudaStream_t)stream));
   }
   const AttnPlan p = attn_plan(a, max_q);

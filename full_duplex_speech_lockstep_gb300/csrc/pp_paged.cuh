@@ -451,16 +451,18 @@ AttnPlan attn_plan(const Args& a, int max_q);
 constexpr int kShortRows = 32;
 struct LongPlan {
   int tp;          // tokens of a row tile
-  int ns;          // splits of a sequence's keys, at most
-  size_t rec_bytes, ml_bytes;
+  int64_t units;   // pairs of row tiles x key heads, at most
+  int parts;       // splits of a unit's keys, at most
+  size_t rec_bytes, ml_bytes, plan_bytes;
 };
-LongPlan long_plan(const Args& a, int T, int max_q);
+LongPlan long_plan(const Args& a, int T);
 
 struct AttnOut {
   void* out;
   float* lse;      // may be null
   float* part;     // split partials: [row][split][D] and [row][split] (reference, sum)
   float2* part_ml;
+  int* plan;       // long chunks: units, whole units, parts, -, units before each sequence
 };
 
 cudaError_t launch_paged_attn(const Args& a, int type, const AttnPlan& plan, const Maps& maps,

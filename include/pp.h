@@ -524,10 +524,13 @@ int pp_rvq_dequantize(const int32_t* codes, int code_stride, int n_frames, int n
  * Every call is asynchronous on `stream`, belongs to the current device, allocates nothing
  * and may be captured into a graph; lengths, tables and row offsets are read when the
  * graph runs.  status (a device word) may be NULL; PP_S_TIMEOUT is OR-ed into it when a
- * bounded wait inside a kernel gave up (the results are then incomplete).  A sequence's results depend,
- * bit for bit, on its own rows, entries and lengths and on the call's head counts and max_q,
- * not on the rest of the batch; with max_q rows of more than 32 query heads x tokens to a
- * key head, n_seqs and T (never what the other sequences hold) may set how its keys are split. */
+ * bounded wait inside a kernel gave up (the results are then incomplete).
+ *
+ * A sequence's results depend, bit for bit, on its own rows, entries and lengths and on the
+ * call's head counts and max_q, not on the rest of the batch.  One exception: where a chunk of
+ * max_q tokens has more than 32 rows to a key head (max_q * n_heads / n_kv_heads > 32), the
+ * number of new rows of the other sequences (never what they hold) may set how the attention
+ * splits a sequence's keys. */
 #define PP_F32 0
 #define PP_BF16 1
 #define PP_F16 2
