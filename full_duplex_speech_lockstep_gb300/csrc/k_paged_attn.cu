@@ -14,9 +14,12 @@
 // head counts only, so its bits do not depend on the rest of the batch.
 //
 //   warp 0      producer: query rows, K and V tiles by TMA, one box to a lane;
-//   warps 4-11  in two teams of four, a team to every second tile, a warp to 32 keys of it, all
-//               rows: S and P V as 16 x 8 x 16 matrix products, P handed from one to the other in
-//               registers, with the warp's own m, l and O (16 * WR rows x D in fp32 registers).
+//   warps 4-11  in two teams of four.  Up to 16 rows: a team to every second tile; up to 32: a
+//               team to 16 rows, both to every tile.  A warp takes 32 keys of a tile: S and P V
+//               as 16 x 8 x 16 matrix products, P handed from one to the other in registers,
+//               with the warp's own m, l and O (16 rows x D in fp32 registers).
+//               (All 32 rows in one warp, a team to every second tile, measured 295 us on 8
+//               sequences of up to 5 tokens x 4 heads over up to 65000 entries.)
 //
 // The warps meet only at a unit's end, where the eight (m, l, O) are joined through shared
 // memory.  (A tile shared by all warps, with the maxima and P exchanged under two barriers a
@@ -53,8 +56,8 @@ struct Cfg {
   static constexpr int kVOff = KS * kTileBytes;
   static constexpr int kQOff = kVOff + VS * kTileBytes;
   static constexpr int kJoinOff = kQOff + kQBufs * kQBytes;       // [8 warps][4 rows][D] floats
-  static constexpr int kMlOff = kJoinOff + kWarps * kJoinRows * D * 4;   // [8 warps][R] (m, l)
-  static constexpr int kCtlOff = kMlOff + kWarps * R * 8;
+  static constexpr int kMlOff = kJoinOff + kWarps * kJoinRows * D * 4;   // [8 warps][16] (m, l)
+  static constexpr int kCtlOff = kMlOff + kWarps * 16 * 8;
 };
 
 struct Ctl {
@@ -163,12 +166,12 @@ struct Walk {
 };
 
 // Row half i of the accumulators (rows 8i .. 8i + 7) times f.
-template <int WR, int D>
-__device__ __forceinline__ void scale_rows(float (&acc)[WR][D / 8][4], int i, float f) {
+template <int D>
+__device__ __forceinline__ void scale_rows(float (&acc)[D / 8][4], int i, float f) {
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) {
-    acc[i >> 1][n][(i & 1) * 2] *= f;
-    acc[i >> 1][n][(i & 1) * 2 + 1] *= f;
+    acc[n][i * 2] *= f;
+    acc[n][i * 2 + 1] *= f;
   }
 }
 
@@ -287,46 +290,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int fr = lane >> 2, fc = (lane & 3) * 2;   // fragment row and column pair
   float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff);
   float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
-  int tok[2 * WR], grp[2 * WR];                 // this thread's rows: token of the tile, head
+  const int team = warp >> 2, part = warp & 3;   // which of a tile's keys
+  constexpr bool kRowTeams = WR == 2;
+  const int row0 = kRowTeams ? team * 16 : 0;    // this warp's first row
+  int tok[2];                                    // this thread's rows: their token of the row tile
 #pragma unroll
-  for (int i = 0; i < 2 * WR; ++i) {
-    tok[i] = (i * 8 + fr) / a.G;
-    grp[i] = i * 8 + fr - tok[i] * a.G;
-  }
-  const int team = warp >> 2, part = warp & 3;   // whose tiles, which of their keys
-  constexpr int kAhead = WR == 1 ? 4 : 2;
+  for (int i = 0; i < 2; ++i) tok[i] = (row0 + i * 8 + fr) / a.G;
   uint32_t nq = 0, n = 0, meets = 0;            // n: tiles of this CTA
   Unit x;
 #pragma unroll 1
   for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
     const int rows = x.nt * a.G;
-    float m[2 * WR], l[2 * WR], acc[WR][D / 8][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[D / 8][4];
 #pragma unroll
-    for (int i = 0; i < 2 * WR; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-    }
+    for (int y = 0; y < D / 8; ++y)
 #pragma unroll
-    for (int i = 0; i < WR; ++i)
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) acc[y][e] = 0.f;
 
     const int qb = nq % kQBufs;
     const uint32_t qbuf = smem_u32(smem + C::kQOff + qb * C::kQBytes);
     if (x.tile0 < x.tile1) wait(&ctl->qfull[qb], (nq / kQBufs) & 1);
-    uint32_t aq[WR == 1 ? D / 16 : 1][4];       // the queries, where registers allow
-    if constexpr (WR == 1) {
+    uint32_t aq[D / 16][4];
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        ldsm4(tile_addr(qbuf, R * 128, (lm & 1) * 8 + lr, kk * 2 + (lm >> 1)), aq[kk]);
-    }
+    for (int kk = 0; kk < D / 16; ++kk)
+      ldsm4(tile_addr(qbuf, R * 128, row0 + (lm & 1) * 8 + lr, kk * 2 + (lm >> 1)), aq[kk]);
 #pragma unroll 1
     for (int t = x.tile0; t < x.tile1; ++t, ++n) {
       const int ks = n % C::KS, vs = n % C::VS;
       wait(&ctl->kfull[ks], (n / C::KS) & 1);
-      if ((n & 1) != team) {
+      if (!kRowTeams && (n & 1) != team) {
         // the other team's tile: every warp sees every phase of every stage all the same (a
         // phase that passed unseen could not be told from the one before it)
         __syncwarp();
@@ -339,37 +331,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j1 = t * kTile + part * 32;     // this warp's first key
       // ---- S = Q K^T: this warp's 32 keys, every row
       const uint32_t kbuf = smem_u32(smem + ks * C::kTileBytes);
-      float s[WR][4][4];
+      float s[4][4];
 #pragma unroll
-      for (int i = 0; i < WR; ++i)
+      for (int y = 0; y < 4; ++y)
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
+        for (int e = 0; e < 4; ++e) s[y][e] = 0.f;
+      constexpr int kAhead = 4;                 // steps whose loads go out together
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][y][e] = 0.f;
+      for (int k0 = 0; k0 < D / 16; k0 += kAhead) {
+        uint32_t bk[kAhead][2][4];
 #pragma unroll
-      for (int k0 = 0; k0 < D / 16; k0 += kAhead) {   // kAhead steps' loads go out together
-        uint32_t bk[kAhead][2][4], q[WR == 1 ? 1 : kAhead][WR][4];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
+        for (int k = 0; k < kAhead; ++k)
 #pragma unroll
           for (int y = 0; y < 2; ++y)
             ldsm4(tile_addr(kbuf, kTile * 128, part * 32 + y * 16 + (lm >> 1) * 8 + lr,
                             (k0 + k) * 2 + (lm & 1)), bk[k][y]);
-          if constexpr (WR > 1) {
-#pragma unroll
-            for (int i = 0; i < WR; ++i)
-              ldsm4(tile_addr(qbuf, R * 128, i * 16 + (lm & 1) * 8 + lr, (k0 + k) * 2 + (lm >> 1)),
-                    q[k][i]);
-          }
-        }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-          for (int i = 0; i < WR; ++i)
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              N::mma(s[i][y], WR == 1 ? aq[k0 + k] : q[k][i], bk[k][y >> 1][(y & 1) * 2],
-                     bk[k][y >> 1][(y & 1) * 2 + 1]);
+          for (int y = 0; y < 4; ++y)
+            N::mma(s[y], aq[k0 + k], bk[k][y >> 1][(y & 1) * 2], bk[k][y >> 1][(y & 1) * 2 + 1]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->kempty[ks]));
@@ -382,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (a.window && t * kTile <= x.first + x.nt - 1 - a.window);
       if (edge) {
 #pragma unroll
-        for (int i = 0; i < 2 * WR; ++i) {
+        for (int i = 0; i < 2; ++i) {
           // the row sees keys (lo, hi], counted from this thread's first
           const int hi = x.first + min(tok[i], x.nt - 1) - j1 - fc;
           const int lo = a.window ? hi - a.window : -1;
@@ -392,20 +373,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
               if (none || y * 8 + e > hi || y * 8 + e <= lo)
-                s[i >> 1][y][(i & 1) * 2 + e] = -INFINITY;
+                s[y][i * 2 + e] = -INFINITY;
           }
         }
       }
-      uint32_t ap[WR][2][4];                    // P as the second product's operand
-      float grow[2 * WR];
+      uint32_t ap[2][4];                        // P as the second product's operand
+      float grow[2];
       bool grown = false;
 #pragma unroll
-      for (int i = 0; i < 2 * WR; ++i) {
+      for (int i = 0; i < 2; ++i) {
         float p[4][2];
 #pragma unroll
         for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) p[y][e] = s[i >> 1][y][(i & 1) * 2 + e];
+          for (int e = 0; e < 2; ++e) p[y][e] = s[y][i * 2 + e];
         float top = fmaxf(fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[1][0], p[1][1])),
                           fmaxf(fmaxf(p[2][0], p[2][1]), fmaxf(p[3][0], p[3][1])));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -425,55 +406,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        ((p[2][0] + p[2][1]) + (p[3][0] + p[3][1])));
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          ap[i >> 1][y >> 1][(y & 1) * 2 + (i & 1)] = N::pack(p[y][0], p[y][1]);
+          ap[y >> 1][(y & 1) * 2 + i] = N::pack(p[y][0], p[y][1]);
       }
       // ---- O = diag(grow) O + P V
       if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-        for (int i = 0; i < 2 * WR; ++i) scale_rows<WR, D>(acc, i, grow[i]);
+        for (int i = 0; i < 2; ++i) scale_rows<D>(acc, i, grow[i]);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {             // 16 keys
-        constexpr int B = WR == 1 ? D / 16 : 4;   // 16-dim blocks whose loads go out together
+        constexpr int B = D / 16;               // 16-dim blocks: their loads go out together
+        uint32_t bv[B][4];
 #pragma unroll
-        for (int b0 = 0; b0 < D / 16; b0 += B) {
-          uint32_t bv[B][4];
+        for (int k = 0; k < B; ++k)
+          ldsm4_t(tile_addr(vbuf, kTile * 128, part * 32 + y * 16 + (lm & 1) * 8 + lr,
+                            k * 2 + (lm >> 1)), bv[k]);
+        if (edge) {
+          uint32_t z = 0;
 #pragma unroll
           for (int k = 0; k < B; ++k)
-            ldsm4_t(tile_addr(vbuf, kTile * 128, part * 32 + y * 16 + (lm & 1) * 8 + lr,
-                              (b0 + k) * 2 + (lm >> 1)), bv[k]);
-          if (edge) {
-            uint32_t z = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) N::probe(z, bv[k][e]);
+          if (z & 0x7fff7fffu) {              // rare: a non-finite value
 #pragma unroll
             for (int k = 0; k < B; ++k)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) N::probe(z, bv[k][e]);
-            if (z & 0x7fff7fffu) {              // rare: a non-finite value
-#pragma unroll
-              for (int k = 0; k < B; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int j = j1 + y * 16 + (e & 1) * 8 + fc;
-                  uint32_t& w = bv[k][e];
-                  if ((w & N::kExp) == N::kExp) {
-                    w &= 0xffff0000u;
-                    if (j >= x.low && j < x.stop) ctl->wild = x.tag;
-                  }
-                  if (((w >> 16) & N::kExp) == N::kExp) {
-                    w &= 0xffffu;
-                    if (j + 1 >= x.low && j + 1 < x.stop) ctl->wild = x.tag;
-                  }
+              for (int e = 0; e < 4; ++e) {
+                const int j = j1 + y * 16 + (e & 1) * 8 + fc;
+                uint32_t& w = bv[k][e];
+                if ((w & N::kExp) == N::kExp) {
+                  w &= 0xffff0000u;
+                  if (j >= x.low && j < x.stop) ctl->wild = x.tag;
                 }
-            }
-            __syncwarp();
+                if (((w >> 16) & N::kExp) == N::kExp) {
+                  w &= 0xffffu;
+                  if (j + 1 >= x.low && j + 1 < x.stop) ctl->wild = x.tag;
+                }
+              }
           }
+          __syncwarp();
+        }
 #pragma unroll
-          for (int k = 0; k < B; ++k)
-#pragma unroll
-            for (int i = 0; i < WR; ++i) {
-              N::mma(acc[i][(b0 + k) * 2], ap[i][y], bv[k][0], bv[k][1]);
-              N::mma(acc[i][(b0 + k) * 2 + 1], ap[i][y], bv[k][2], bv[k][3]);
-            }
+        for (int k = 0; k < B; ++k) {
+          N::mma(acc[k * 2], ap[y], bv[k][0], bv[k][1]);
+          N::mma(acc[k * 2 + 1], ap[y], bv[k][2], bv[k][3]);
         }
       }
       __syncwarp();
@@ -485,41 +461,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++nq;
     }
 
-    // ---- join the warps: everyone's (m, l) first, then O, four rows at a time
+    // ---- join the warps that share rows: everyone's (m, l) first, then O, four rows at a time
 #pragma unroll
-    for (int i = 0; i < 2 * WR; ++i) {
+    for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if ((lane & 3) == 0) ml[warp * R + i * 8 + fr] = make_float2(m[i], l[i]);
+      if ((lane & 3) == 0) ml[warp * 16 + i * 8 + fr] = make_float2(m[i], l[i]);
     }
     sync_warps(a, &ctl->meet, meets, lane, abort_flag);
     const bool wild = *reinterpret_cast<volatile int*>(&ctl->wild) == x.tag;
+    constexpr int kShare = kRowTeams ? kWarps / 2 : kWarps;   // warps that share rows
+    const int w0 = kRowTeams ? team * kShare : 0;
 #pragma unroll
-    for (int i = 0; i < 2 * WR; ++i) {
+    for (int i = 0; i < 2; ++i) {
       float top = -INFINITY;
 #pragma unroll 4
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * R + i * 8 + fr].x);
+      for (int w = w0; w < w0 + kShare; ++w) top = fmaxf(top, ml[w * 16 + i * 8 + fr].x);
       // (a warp without a reference has nothing, or NaN: either passes unscaled)
-      scale_rows<WR, D>(acc, i, m[i] == -INFINITY ? 1.f : exp2_approx(m[i] - top));
+      scale_rows<D>(acc, i, m[i] == -INFINITY ? 1.f : exp2_approx(m[i] - top));
     }
     auto join_rows = [&](int i, int half) {
-      const int r0 = i * 8 + half * kJoinRows;
       if (fr / kJoinRows == half) {
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
+        for (int y = 0; y < D / 8; ++y)
           *reinterpret_cast<float2*>(join + (warp * kJoinRows + (fr & 3)) * D +
-                                     ((n * 8 + fc) ^ ((fr & 3) << 3))) =
-              make_float2(acc[i >> 1][n][(i & 1) * 2], acc[i >> 1][n][(i & 1) * 2 + 1]);
+                                     ((y * 8 + fc) ^ ((fr & 3) << 3))) =
+              make_float2(acc[y][i * 2], acc[y][i * 2 + 1]);
       }
       sync_warps(a, &ctl->meet, meets, lane, abort_flag);
-      const int jr = tid / (D / 2), d = tid % (D / 2) * 2, r = r0 + jr;
-      if (jr < kJoinRows && r < rows) {
+      const int id = tid - w0 * 32, d = id % (D / 2) * 2;
+#pragma unroll 1
+      for (int jr = id / (D / 2); jr < kJoinRows; jr += kShare * 32 / (D / 2)) {
+        const int rl = i * 8 + half * kJoinRows + jr, r = row0 + rl;
+        if (r >= rows) break;
         float M = -INFINITY, L = 0.f, sum[2] = {0.f, 0.f};
 #pragma unroll 4
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * R + r].x);
+        for (int w = w0; w < w0 + kShare; ++w) M = fmaxf(M, ml[w * 16 + rl].x);
 #pragma unroll 2
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 y = ml[w * R + r];
+        for (int w = w0; w < w0 + kShare; ++w) {
+          const float2 y = ml[w * 16 + rl];
           L += (y.x == -INFINITY ? 1.f : exp2_approx(y.x - M)) * y.y;
           const float2 z =
               *reinterpret_cast<const float2*>(join + (w * kJoinRows + jr) * D + (d ^ (jr << 3)));
@@ -546,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sync_warps(a, &ctl->meet, meets, lane, abort_flag);
     };
 #pragma unroll
-    for (int i = 0; i < 2 * WR; ++i) {
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll 1
       for (int half = 0; half < 2 && i * 8 + half * kJoinRows < rows; ++half) join_rows(i, half);
     }
