@@ -13,7 +13,9 @@
 // the same number of tiles as the others; a sequence's splits depend on its own lengths and the
 // head counts only, so its bits do not depend on the rest of the batch.
 //
-//   warp 0      producer: query rows, K and V tiles by TMA, one box to a lane;
+//   warp 0      the units, their query rows and K tiles by TMA, one box to a lane;
+//   warp 1      the V tiles (with pages of 16 a tile is 16 boxes: one warp for both was 328 us on
+//               the 64-session tick);
 //   warps 4-11  in two teams of four.  Up to 16 rows: a team to every second tile; up to 32: a
 //               team to 16 rows, both to every tile.  A warp takes 32 keys of a tile: S and P V
 //               as 16 x 8 x 16 matrix products, P handed from one to the other in registers,
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->qfull[i]), 1);
       mbar_init(smem_u32(&ctl->qempty[i]), kWarps);
     }
-    ring_init(ctl->ring, kWarps);
+    ring_init(ctl->ring, kWarps + 1);   // the V producer too
     mbar_init(smem_u32(&ctl->meet), kWarps);
     ctl->wild = 0;
     ctl->abort = 0;
@@ -222,63 +224,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x < 128) {
     // ---- producer -------------------------------------------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
-    if (threadIdx.x >= 32) return;
-    uint32_t nq = 0, nk = 0, nv = 0;
-    uint32_t seen_bad = 0, nu = 0;
-    Walk x(a, pre, tp, share);
+    if (threadIdx.x < 32) {
+      uint32_t nq = 0, nk = 0, nu = 0, seen_bad = 0;
+      Walk x(a, pre, tp, share);
 #pragma unroll 1
-    for (; !x.done() && !*abort_flag; x.next()) {
-      put_unit(a, ctl->ring, nu++,
-               Unit{x.b, x.h, x.s.row0 + x.t0, x.nt, x.first, x.tile0, x.tile1,
-                    a.window ? max(x.first - a.window + 1, 0) : 0, x.stop, x.i, x.ns, x.at + 1},
-               lane, abort_flag);
-      if (x.tile0 == x.tile1) continue;
-      const int qb = nq % kQBufs;
-      if (nq >= kQBufs) wait(&ctl->qempty[qb], (nq / kQBufs - 1) & 1);
-      if (*abort_flag) break;
+      for (; !x.done() && !*abort_flag; x.next()) {
+        put_unit(a, ctl->ring, nu++,
+                 Unit{x.b, x.h, x.s.row0 + x.t0, x.nt, x.first, x.tile0, x.tile1,
+                      a.window ? max(x.first - a.window + 1, 0) : 0, x.stop, x.i, x.ns, x.at + 1},
+                 lane, abort_flag);
+        if (x.tile0 == x.tile1) continue;
+        TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, lane);
+        const int qb = nq % kQBufs;
+        if (nq >= kQBufs) wait(&ctl->qempty[qb], (nq / kQBufs - 1) & 1);
+        if (*abort_flag) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&ctl->qfull[qb]);
+          const uint32_t dst = smem_u32(smem + C::kQOff + qb * C::kQBytes);
+          // rows past the row tile's tokens may be another sequence's: their results go nowhere
+          mbar_expect_tx(bar, (uint32_t)(tp * a.G * D * 2));
+          for (int bx = 0; bx < D / 64; ++bx)
+            tma_load_4d(dst + bx * (R * 128), &mapQ, bx * 64, x.h * a.G, x.s.row0 + x.t0, 0, bar);
+        }
+        ++nq;
+#pragma unroll 1
+        for (int t = x.tile0; t < x.tile1; ++t, ++nk) {
+          const int ks = nk % C::KS;
+          const TilePages now = next;
+          if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, lane);
+          if (nk >= C::KS) wait(&ctl->kempty[ks], (nk / C::KS - 1) & 1);
+          if (*abort_flag) break;
+          load_key_tile(a, &mapK, smem_u32(smem + ks * C::kTileBytes), smem_u32(&ctl->kfull[ks]),
+                        now, x.h, t * kTile, lane, nullptr);
+          seen_bad |= now.bad;
+        }
+      }
+      Unit last{};
+      last.b = -1;
+      put_unit(a, ctl->ring, nu, last, lane, abort_flag);
+      if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
+      // every copy lands before the CTA may exit (bounded waits)
       if (lane == 0) {
-        const uint32_t bar = smem_u32(&ctl->qfull[qb]);
-        const uint32_t dst = smem_u32(smem + C::kQOff + qb * C::kQBytes);
-        // rows past the row tile's tokens may be another sequence's: their results go nowhere
-        mbar_expect_tx(bar, (uint32_t)(tp * a.G * D * 2));
-        for (int bx = 0; bx < D / 64; ++bx)
-          tma_load_4d(dst + bx * (R * 128), &mapQ, bx * 64, x.h * a.G, x.s.row0 + x.t0, 0, bar);
+#pragma unroll 1
+        for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; i < nq; ++i)
+          drain_phase(&ctl->qfull[i % kQBufs], (i / kQBufs) & 1);
+#pragma unroll 1
+        for (uint32_t i = nk > C::KS ? nk - C::KS : 0; i < nk; ++i)
+          drain_phase(&ctl->kfull[i % C::KS], (i / C::KS) & 1);
       }
-      ++nq;
-      TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, lane);
+    } else if (threadIdx.x < 64) {
+      uint32_t nv = 0;
+      Unit x;
 #pragma unroll 1
-      for (int t = x.tile0; t < x.tile1; ++t) {
-        const int ks = nk % C::KS, vs = nv % C::VS;
-        const TilePages now = next;
-        if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, lane);
-        if (nk >= C::KS) wait(&ctl->kempty[ks], (nk / C::KS - 1) & 1);
-        if (*abort_flag) break;
-        load_key_tile(a, &mapK, smem_u32(smem + ks * C::kTileBytes), smem_u32(&ctl->kfull[ks]), now,
-                      x.h, t * kTile, lane, nullptr);
-        seen_bad |= now.bad;
-        ++nk;
-        if (nv >= C::VS) wait(&ctl->vempty[vs], (nv / C::VS - 1) & 1);
-        if (*abort_flag) break;
-        load_key_tile(a, &mapV, smem_u32(smem + C::kVOff + vs * C::kTileBytes),
-                      smem_u32(&ctl->vfull[vs]), now, x.h, t * kTile, lane, &ctl->bad[vs]);
-        ++nv;
+      for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+        if (x.tile0 == x.tile1) continue;
+        TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, lane);
+#pragma unroll 1
+        for (int t = x.tile0; t < x.tile1; ++t, ++nv) {
+          const int vs = nv % C::VS;
+          const TilePages now = next;
+          if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, lane);
+          if (nv >= C::VS) wait(&ctl->vempty[vs], (nv / C::VS - 1) & 1);
+          if (*abort_flag) break;
+          load_key_tile(a, &mapV, smem_u32(smem + C::kVOff + vs * C::kTileBytes),
+                        smem_u32(&ctl->vfull[vs]), now, x.h, t * kTile, lane, &ctl->bad[vs]);
+        }
       }
-    }
-    Unit last{};
-    last.b = -1;
-    put_unit(a, ctl->ring, nu, last, lane, abort_flag);
-    if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
-    // every copy lands before the CTA may exit (bounded waits)
-    if (lane == 0) {
+      if (lane == 0) {
 #pragma unroll 1
-      for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; i < nq; ++i)
-        drain_phase(&ctl->qfull[i % kQBufs], (i / kQBufs) & 1);
-#pragma unroll 1
-      for (uint32_t i = nk > C::KS ? nk - C::KS : 0; i < nk; ++i)
-        drain_phase(&ctl->kfull[i % C::KS], (i / C::KS) & 1);
-#pragma unroll 1
-      for (uint32_t i = nv > C::VS ? nv - C::VS : 0; i < nv; ++i)
-        drain_phase(&ctl->vfull[i % C::VS], (i / C::VS) & 1);
+        for (uint32_t i = nv > C::VS ? nv - C::VS : 0; i < nv; ++i)
+          drain_phase(&ctl->vfull[i % C::VS], (i / C::VS) & 1);
+      }
     }
     return;
   }
