@@ -615,6 +615,7 @@ class PagedKV:
         self.c = pp_paged_kv(k.data_ptr(), v.data_ptr(), self._ptr(mass), table.data_ptr(),
                              stride, n_pages, rows, heads, dim, self.types[k.dtype],
                              table.shape[0], table.shape[1])
+        self.ref, self.lib, self.sizes = ctypes.byref(self.c), lib(), {}
         # the current stream's handle without building a stream object, where torch offers it
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -647,13 +648,25 @@ class PagedKV:
         self._fits("cu", cu, self.torch.int32, (self.n + 1,))
         self._fits("kv_len", kv_len, self.torch.int32, (self.n,))
 
-    def _call(self, fn, *args):
+    def _call(self, name, *args):
         """One library call on the cache's device and that device's current stream."""
-        torch = self.torch
-        if torch.cuda.current_device() == self.index:
-            return fn(*args, self.raw_stream(self.index))
-        with torch.cuda.device(self.index):
-            return fn(*args, self.raw_stream(self.index))
+        cuda, fn = self.torch.cuda, getattr(self.lib, name)
+        if cuda.current_device() == self.index:
+            rc = fn(*args, self.raw_stream(self.index))
+        else:
+            with cuda.device(self.index):
+                rc = fn(*args, self.raw_stream(self.index))
+        if rc != PP_OK:
+            raise PPError(name, rc)
+
+    def _scratch_bytes(self, *shape):
+        """Scratch of an attention call, by its shape (heads, rows, max_q, window)."""
+        n = self.sizes.get(shape)
+        if n is None:
+            if len(self.sizes) >= 1024:
+                self.sizes.clear()
+            n = self.sizes[shape] = pp_paged_attention_scratch_bytes(self.c, *shape)
+        return n
 
     @staticmethod
     def _longest(max_q, T):
@@ -689,7 +702,7 @@ class PagedKV:
             out = torch.empty((T, H, self.dim), dtype=self.dtype, device=self.device)
         else:
             self._fits("out", out, self.dtype, (T, H, self.dim))
-        self._call(pp_paged_append, self.c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        self._call("pp_paged_append", self.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
                    self.types[dtype], self._ptr(q_alpha), self._ptr(k_alpha), eps, rope_base,
                    self.dim if rot_dim is None else rot_dim, int(halves), self._ptr(positions),
                    cu.data_ptr(), kv_len.data_ptr(), T, H, out.data_ptr(), self.status.data_ptr())
@@ -708,10 +721,10 @@ class PagedKV:
             self._fits("out", out, self.dtype, (T, H, self.dim))
         lse = torch.empty((T, H), dtype=torch.float32, device=self.device) if with_lse else None
         max_q = self._longest(max_q, T)
-        nbytes = pp_paged_attention_scratch_bytes(self.c, H, T, max_q, window)
+        nbytes = self._scratch_bytes(H, T, max_q, window)
         scratch = self.unused if nbytes <= 256 else \
             torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        self._call(pp_paged_attention, self.c, q.data_ptr(), qs, cu.data_ptr(), kv_len.data_ptr(),
+        self._call("pp_paged_attention", self.ref, q.data_ptr(), qs, cu.data_ptr(), kv_len.data_ptr(),
                    T, max_q, H, self.dim ** -0.5 if scale is None else scale, window,
                    out.data_ptr(), self._ptr(lse), self.status.data_ptr(), scratch.data_ptr(),
                    nbytes)
@@ -724,14 +737,15 @@ class PagedKV:
         T, H, qs = self._rows("q", q, self.dtype)
         self._fits("lse", lse, self.torch.float32, (T, H))
         self._batch(cu, kv_len)
-        c = self.c
+        c = self.ref
         if mass is not None:
             self._fits("mass", mass, self.torch.float32, self.mass_shape)
-            c = pp_paged_kv.from_buffer_copy(c)
-            c.mass = mass.data_ptr()
+            other = pp_paged_kv.from_buffer_copy(self.c)
+            other.mass = mass.data_ptr()
+            c = ctypes.byref(other)
         elif self.mass is None:
             raise ValueError("this cache keeps no mass")
-        self._call(pp_paged_mass, c, q.data_ptr(), qs, lse.data_ptr(), cu.data_ptr(),
+        self._call("pp_paged_mass", c, q.data_ptr(), qs, lse.data_ptr(), cu.data_ptr(),
                    kv_len.data_ptr(), T, self._longest(max_q, T), H,
                    self.dim ** -0.5 if scale is None else scale, window, decay,
                    self.status.data_ptr())
@@ -748,6 +762,6 @@ class PagedKV:
         to_len = torch.empty(self.n, dtype=torch.int32, device=self.device)
         kept = torch.empty((self.n, self.heads, max(budget, 0)), dtype=torch.int32,
                            device=self.device)
-        self._call(pp_paged_evict, self.c, kv_len.data_ptr(), budget, recent, to.c,
+        self._call("pp_paged_evict", self.ref, kv_len.data_ptr(), budget, recent, to.ref,
                    to_len.data_ptr(), kept.data_ptr(), self.status.data_ptr())
         return to_len, kept

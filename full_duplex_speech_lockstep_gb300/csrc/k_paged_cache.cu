@@ -264,10 +264,9 @@ __global__ void __launch_bounds__(kSelThreads)
     sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == 0) scan[warp] = sum;
     __syncthreads();
-    if (tid == 0) {
-      uint32_t c = 0;
-      for (int w = 0; w < kSelWarps; ++w) c += scan[w];
-      share_sum = c;
+    if (warp == 0) {
+      const uint32_t c = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? scan[lane] : 0u);
+      if (lane == 0) share_sum = c;
     }
     cluster.sync();
     // ... then all of them find the share, and in it the bin, of the left-th key from the top
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(kSelThreads)
     if (lane == 31) scan[warp] = over;
     __syncthreads();
     above += over - sum;
-    for (int w = 0; w < warp; ++w) above += scan[w];
+    above += __reduce_add_sync(0xffffffffu, lane < warp ? scan[lane] : 0u);
     if (above < left && left <= above + sum) {
 #pragma unroll
       for (int e = 0; e < kBins / kSelThreads; ++e) {
