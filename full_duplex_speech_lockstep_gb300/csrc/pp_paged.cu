@@ -25,7 +25,7 @@ bool cache_ok(const pp_paged_kv* kv) {
   if ((int64_t)kv->table_ld * kv->page_size > (int64_t)1 << 28) return false;
   // units, tiles and blocks of a call are counted in 32 bits
   if ((int64_t)kv->n_seqs * kv->n_kv_heads *
-          (((int64_t)kv->table_ld * kv->page_size + kTile - 1) / kTile) >= (int64_t)1 << 30)
+          (((int64_t)kv->table_ld * kv->page_size + kTile - 1) / kTile) >= (int64_t)1 << 28)
     return false;
   const int64_t page = (int64_t)kv->n_kv_heads * kv->page_size * kv->head_dim;
   if (kv->page_stride < page || (kv->page_stride & 7) || kv->page_stride >= (int64_t)1 << 38)

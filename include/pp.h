@@ -509,7 +509,8 @@ int pp_rvq_dequantize(const int32_t* codes, int code_stride, int n_frames, int n
  *   pp_paged_evict       (now and then) the lightest entries leave
  *
  * Entry j of sequence b is row j % page_size of page table[b][j / page_size]; kv_len[b]
- * entries exist.  All device arrays are the caller's.  A page number outside [0, n_pages)
+ * entries exist.  Sequences may share pages that no call writes (a common prompt); calls that
+ * write entries or weights need each written row to belong to one place of one sequence.  All device arrays are the caller's.  A page number outside [0, n_pages)
  * that a call needs is never followed: nothing is stored there, its entries take no part,
  * and PP_S_INDEX is OR-ed into the status word.  Table entries past a sequence's last page
  * are not looked at.  kv_len is clamped to [0, table_ld * page_size].
@@ -549,7 +550,8 @@ typedef struct {
   int32_t head_dim;        /* 64 or 128 */
   int32_t type;            /* PP_BF16 or PP_F16 */
   int32_t n_seqs;          /* 1..2048 */
-  int32_t table_ld;        /* table_ld * page_size <= 2^28 */
+  int32_t table_ld;        /* table_ld * page_size <= 2^28, and n_seqs * n_kv_heads * (128-entry
+                              tiles of a table row) < 2^28 */
 } pp_paged_kv;
 
 /* Norm and rotation of the new queries and keys for each head, and the new cache entries:
@@ -587,7 +589,7 @@ int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, cons
  *            (a multiple of 8), 16-byte aligned
  *   max_q    the largest number of new rows of any sequence, as far as the host knows; sets
  *            tile sizes and scratch only: longer chunks are computed all the same
- *   out      [T][n_heads][head_dim] in the cache's type, 16-byte aligned
+ *   out      [T][n_heads][head_dim] in the cache's type, 16-byte aligned, not overlapping q
  *   lse      f32 [T][n_heads], or NULL
  *   scratch  at least pp_paged_attention_scratch_bytes(...) bytes, 256-byte aligned; its
  *            contents need no set-up; calls that may overlap need their own
