@@ -65,9 +65,9 @@ struct Ctl {
   uint64_t clean[2][2];   // [group][edge tile & 1]: the group's half of V is clean
   uint32_t bad[8];
   uint32_t tmem;
-  // tag of the unit in which a softmax group took a non-finite value out of V.  The single query
-  // buffer keeps a group at most two units ahead of the other: four entries are enough.
-  int wild[2][4];
+  // tag of the unit in which a softmax group took a non-finite value out of V.  The ring keeps a
+  // group at most kUnits units ahead of the other.
+  int wild[2][2 * kUnits];
   int abort;
 };
 
@@ -79,11 +79,12 @@ __device__ __forceinline__ int seq_units(const Args& a, int b, int tp) {
 
 // The units run in waves of one to an SM.  Those of the last wave, if it is not full, are split
 // over their keys, each in `parts`, so that its end comes sooner: of `units`, the first `whole`
-// stay in one piece.
+// stay in one piece.  `room` parts have a place in scratch: never too few, unless row offsets
+// that fall make more units than T rows can have.
 struct Waves {
   int units, whole, parts;
 };
-__device__ __forceinline__ Waves waves_of(int units, int most_parts) {
+__device__ __forceinline__ Waves waves_of(int units, int most_parts, int room) {
   Waves w;
   w.units = units;
   const int rest = units % (int)gridDim.x;
@@ -91,7 +92,7 @@ __device__ __forceinline__ Waves waves_of(int units, int most_parts) {
   w.parts = 1;
   // time of the last wave in 1/64 of a unit's; 2 for each part's start and join
   int best = 64;
-  for (int p = 2; p <= most_parts && rest * p <= kMaxParts; ++p) {
+  for (int p = 2; p <= most_parts && rest * p <= room; ++p) {
     const int time = (rest * p + (int)gridDim.x - 1) / (int)gridDim.x * (64 / p + 4);
     if (rest > 0 && time < best) {
       best = time;
@@ -203,6 +204,7 @@ __device__ __forceinline__ bool finite_only(uint32_t& w) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_attn_tc(const __grid_constant__ Args a, const int tp, const int most_parts,
+                    const int room,
                     const __grid_constant__ AttnOut o,
                     const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapV,
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->pfull[t]), 4);
       mbar_init(smem_u32(&ctl->ofull[t]), 1);
       for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl->clean[t][i]), 4);
-      for (int i = 0; i < 4; ++i) ctl->wild[t][i] = 0;
+      for (int i = 0; i < 2 * kUnits; ++i) ctl->wild[t][i] = 0;
     }
     ring_init(ctl->ring, 9);            // the MMA issuer, eight softmax warps
     ctl->abort = 0;
@@ -245,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   pdl_wait_and_trigger();
   pdl_trigger();
-  prefix_units(pre, a.n_seqs, [&](int b) { return seq_units(a, b, tp); });
-  const Waves waves = waves_of(pre[a.n_seqs], most_parts);
+  prefix_units(a, pre, [&](int b) { return seq_units(a, b, tp); });
+  const Waves waves = waves_of(pre[a.n_seqs], most_parts, room);
   // what the join needs to find its rows: the waves and the sequences' units
   if (blockIdx.x == 0 && most_parts > 1) {
     if (threadIdx.x == 0) {
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               found = found || (j0 + row >= x.low && j0 + row < x.stop);
             }
           }
-          if (found) ctl->wild[t][nu & 3] = x.tag;
+          if (found) ctl->wild[t][nu % (2 * kUnits)] = x.tag;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (tiles == 2) {    // both halves, before either product
             __syncwarp();
@@ -557,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&ctl->ofull[t], no & 1);
         ++no;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        wild = *reinterpret_cast<volatile int*>(&ctl->wild[0][nu & 3]) == x.tag ||
-               *reinterpret_cast<volatile int*>(&ctl->wild[1][nu & 3]) == x.tag;
+        wild = *reinterpret_cast<volatile int*>(&ctl->wild[0][nu % (2 * kUnits)]) == x.tag ||
+               *reinterpret_cast<volatile int*>(&ctl->wild[1][nu % (2 * kUnits)]) == x.tag;
       }
       const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll 1
@@ -656,7 +658,7 @@ cudaError_t run(const Args& a, const LongPlan& p, const Maps& maps, const AttnOu
   const int64_t most = p.units * p.parts;
   const int nsm = sm_count();
   err = launch(k_paged_attn_tc<T, D>, dim3((unsigned)(most < nsm ? most : nsm)), kThreads, smem, s,
-               a, p.tp, p.parts, o, maps.k, maps.v, maps.q, v_pages);
+               a, p.tp, p.parts, p.room, o, maps.k, maps.v, maps.q, v_pages);
   if (err != cudaSuccess || p.parts == 1) return err;
   const int64_t split = p.units < nsm ? p.units : nsm;   // units of the last wave, at most
   return launch(k_paged_join_units<T, D>, dim3((unsigned)(split * kUnitRows / 4)), 128, 0, s, a,
@@ -671,8 +673,8 @@ LongPlan long_plan(const Args& a, int T) {
   p.units = ((int64_t)T / (2 * p.tp) + a.n_seqs) * a.Hk;
   const int64_t parts = (((int64_t)a.table_ld << a.lps) + 4 * kTile - 1) / (4 * kTile);
   p.parts = parts < 1 ? 1 : parts > kMostParts ? kMostParts : (int)parts;
-  const int64_t units = p.units * p.parts < kMaxParts ? p.units * p.parts : kMaxParts;
-  const size_t recs = p.parts == 1 ? 0 : (size_t)units * kUnitRows;
+  p.room = p.units * p.parts < kMaxParts ? (int)(p.units * p.parts) : kMaxParts;
+  const size_t recs = p.parts == 1 ? 0 : (size_t)p.room * kUnitRows;
   p.rec_bytes = recs * a.D * sizeof(float);
   p.ml_bytes = recs * sizeof(float2);
   p.plan_bytes = (size_t)(a.n_seqs + 5) * sizeof(int);

@@ -10,6 +10,11 @@
 // (With one tile to a unit each step's 32 KB of rows served 128 keys only, and reading them
 // from L2 bounded the kernel: 114 us for 4 x 300 rows over up to 16000 entries.)
 //
+// Measured (bf16, 128 dims): 64 sequences of 1 token and up to 24576 entries, 4 heads on each of 8
+// key heads: 164 us, 4.8 TB/s, bound by reading K once and by the units' start, two tiles each.
+// 4 x 300 rows: 94 us, 815 TFLOP/s, bound by the exponentials and sums: 2200 clocks a step of two
+// tiles, whose products take half of that.
+//
 // A CTA takes a run of consecutive units of about the same number of steps as the others:
 //   warp 0        producer: the units and their key tiles, by TMA
 //   warp 1        one thread issues the MMAs, up to four steps ahead of the sums
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_and_trigger();
   pdl_trigger();
   // (a sequence without new rows only decays, and not even that at 1)
-  prefix_units(pre, a.n_seqs, [&](int b) -> int64_t {
+  prefix_units(a, pre, [&](int b) -> int64_t {
     const Seq s = seq_of(a, b);
     if (s.n == 0 && decay == 1.f) return 0;
     return (int64_t)a.Hk * ((s.len + 2 * kTile - 1) / (2 * kTile)) * unit_cost(s, tp);

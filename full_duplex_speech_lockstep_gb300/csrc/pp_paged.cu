@@ -238,7 +238,7 @@ int pp_paged_evict(const pp_paged_kv* kv, const int32_t* kv_len, int budget, int
                    void* stream) {
   if (!cache_ok(kv) || !cache_ok(to) || !kv->mass || !kv_len || !to_len || !kept) return PP_EINVAL;
   if (!aligned(kv_len, 4) || !aligned(to_len, 4) || !aligned(kept, 4)) return PP_EINVAL;
-  if (budget < 1 || recent < 0 || recent > budget) return PP_EINVAL;
+  if (budget < 1 || budget > 1 << 28 || recent < 0 || recent > budget) return PP_EINVAL;
   if (to->type != kv->type || to->head_dim != kv->head_dim || to->n_kv_heads != kv->n_kv_heads ||
       to->n_seqs != kv->n_seqs)
     return PP_EINVAL;

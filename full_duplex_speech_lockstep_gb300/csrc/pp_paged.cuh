@@ -85,19 +85,23 @@ __device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity) {
 }
 
 // Prefix sums of count(b) over the sequences into pre[0..n], by one CTA; ends with a
-// barrier.
+// barrier.  Only row offsets that fall, so that sequences share rows, can make more units than a
+// 32-bit sum holds: then there are none, and PP_S_INDEX tells.
 template <typename I, typename F>
-__device__ __forceinline__ void prefix_units(I* pre, int n, F count) {
+__device__ __forceinline__ void prefix_units(const Args& a, I* pre, F count) {
+  const int n = a.n_seqs;
 #pragma unroll 1
   for (int b = threadIdx.x; b < n; b += blockDim.x) pre[b + 1] = count(b);
   if (threadIdx.x == 0) pre[0] = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
     I base = 0;
+    float all = 0.f;
 #pragma unroll 1
     for (int b0 = 0; b0 < n; b0 += 32) {
       const int b = b0 + threadIdx.x;
       I x = b < n ? pre[b + 1] : 0;
+      all += (float)x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const I y = __shfl_up_sync(0xffffffffu, x, o);
@@ -105,6 +109,15 @@ __device__ __forceinline__ void prefix_units(I* pre, int n, F count) {
       }
       if (b < n) pre[b + 1] = base + x;
       base += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if constexpr (sizeof(I) == 4) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      if (all > 2.1e9f) {
+#pragma unroll 1
+        for (int b = threadIdx.x; b < n; b += 32) pre[b + 1] = 0;
+        if (threadIdx.x == 0) raise(a, PP_S_INDEX);
+      }
     }
   }
   __syncthreads();
@@ -453,6 +466,7 @@ struct LongPlan {
   int tp;          // tokens of a row tile
   int64_t units;   // pairs of row tiles x key heads, at most
   int parts;       // splits of a unit's keys, at most
+  int room;        // split units that scratch holds
   size_t rec_bytes, ml_bytes, plan_bytes;
 };
 LongPlan long_plan(const Args& a, int T);

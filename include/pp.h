@@ -510,14 +510,16 @@ int pp_rvq_dequantize(const int32_t* codes, int code_stride, int n_frames, int n
  *
  * Entry j of sequence b is row j % page_size of page table[b][j / page_size]; kv_len[b]
  * entries exist.  Sequences may share pages that no call writes (a common prompt); calls that
- * write entries or weights need each written row to belong to one place of one sequence.  All device arrays are the caller's.  A page number outside [0, n_pages)
- * that a call needs is never followed: nothing is stored there, its entries take no part,
- * and PP_S_INDEX is OR-ed into the status word.  Table entries past a sequence's last page
- * are not looked at.  kv_len is clamped to [0, table_ld * page_size].
+ * write entries or weights need each written row to belong to one place of one sequence.  All
+ * device arrays are the caller's.  A page number outside [0, n_pages) that a call needs is
+ * never followed: nothing is stored there, its entries take no part, and PP_S_INDEX is OR-ed
+ * into the status word.  Table entries past a sequence's last page are not looked at.  kv_len is clamped to [0, table_ld * page_size].
  *
  * New rows are packed: sequence b has rows cu[b] .. cu[b+1] - 1 of the T rows, its newest
- * tokens, in order; a sequence may have none.  Values of cu are clamped to [0, T]; rows of
- * no sequence (before cu[0], from cu[n_seqs] on) are neither read as queries nor written.
+ * tokens, in order; a sequence may have none.  cu ascends.  Its values are clamped to [0, T];
+ * rows of no sequence (before cu[0], from cu[n_seqs] on) are neither read as queries nor
+ * written.  (Offsets that fall all the same, so that sequences share rows, leave undefined
+ * results in those rows and entries, and touch nothing else.)
  * Row i of a sequence of n new rows sits at entry p = kv_len - n + i: kv_len counts the
  * new entries.  It sees the entries j <= p, with window > 0 only those with j > p - window
  * (entries are counted by index, so after an eviction a window counts what is left).
@@ -622,7 +624,8 @@ int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const 
  * pp_paged_append.
  *   to_len  int32 [n_seqs]: min(kv_len, budget)
  *   kept    int32 [n_seqs][n_kv_heads][budget]: the entries that stayed, ascending, then -1
- * kv->mass is required, to->mass is written if given.  0 <= recent <= budget, budget >= 1.
+ * kv->mass is required, to->mass is written if given.  0 <= recent <= budget,
+ * 1 <= budget <= 2^28.
  * Errors: PP_EINVAL (`to` of other sequences, heads, head dim or type), PP_E_RANGE (to's table
  * is too narrow for the budget), PP_E_CUDA. */
 int pp_paged_evict(const pp_paged_kv* kv, const int32_t* kv_len, int budget, int recent,

@@ -336,6 +336,62 @@ def test_graphs_replay_with_new_lengths_and_share_nothing(chunk):
             b.check(o, l)
 
 
+@pytest.mark.parametrize("G,n", [(1, 1), (2, 40)])
+def test_sequences_share_the_pages_of_a_common_prompt(G, n):
+    b = Batch(BF16, 128, 2, G, 64, [n, n, n], [700, 900, 600])
+    b.table[1:, :8] = b.table[0, :8]
+    out, lse = b.kv().attention(b.q, b.cu, b.len, with_lse=True)
+    b.check(out, lse)
+
+
+def guarded(shape, type, fill):
+    """A tensor with a guard behind it, and a check that the guard is untouched."""
+    n = math.prod(shape)
+    whole = torch.full((n + (1 << 20),), fill, dtype=type, device="cuda")
+
+    def intact():
+        return bool((whole[n:] == fill).all())
+    return whole[:n].view(shape), intact
+
+
+@pytest.mark.parametrize("T,page,n", [(6, 16, 1500), (2560, 64, 1500)])
+def test_row_offsets_that_fall_touch_nothing_else(T, page, n):
+    """Sequences 0, 2 and 4 are all given every row, so the call holds more units than T rows
+    make: outputs and scratch keep to their bounds, and what has no part in it stays."""
+    pp = pp_()
+    b = Batch(BF16, 128, 1, 1, page, [T], [n] * 6, pad=2)
+    cu = torch.tensor([0, T, 0, T, 0, T, 0], dtype=torch.int32, device="cuda")
+    kv = b.kv()
+    rows = b.T
+    stream = torch.cuda.current_stream().cuda_stream
+    size = pp.pp_paged_attention_scratch_bytes(kv.c, 1, rows, T, 0)
+    scratch, scratch_ok = guarded((size,), torch.uint8, 77)
+    out, out_ok = guarded((rows, 1, 128), BF16, 3.0)
+    lse, lse_ok = guarded((rows, 1), F32, 3.0)
+    k0, v0, mass0 = b.k.clone(), b.v.clone(), b.mass.clone()
+    pp.pp_paged_attention(kv.c, b.q.data_ptr(), 128, cu.data_ptr(), b.len.data_ptr(), rows, T,
+                          1, b.scale, 0, out.data_ptr(), lse.data_ptr(), 0, scratch.data_ptr(), size,
+                          stream)
+    torch.cuda.synchronize()
+    assert scratch_ok() and out_ok() and lse_ok()
+    assert (out[T:] == 3).all() and (lse[T:] == 3).all()
+    assert torch.equal(b.k, k0) and torch.equal(b.v, v0) and torch.equal(b.mass, mass0)
+
+    pp.pp_paged_mass(kv.c, b.q.data_ptr(), 128, lse.data_ptr(), cu.data_ptr(),
+                     b.len.data_ptr(), rows, T, 1, b.scale, 0, 1.0, 0, stream)
+    x, x_ok = guarded((rows, 1, 128), BF16, 3.0)
+    pp.pp_paged_append(kv.c, b.q.data_ptr(), 128, b.q.data_ptr(), 128, b.q.data_ptr(), 128,
+                       pp.PP_BF16, 0, 0, 1e-5, 1e4, 128, 0, 0, cu.data_ptr(), b.len.data_ptr(),
+                       rows, 1, x.data_ptr(), 0, stream)
+    torch.cuda.synchronize()
+    assert x_ok() and (x[T:] == 3).all()
+    for s in (1, 3, 5):                      # no rows: nothing of theirs has changed
+        p, r = b.where(s)
+        for new, old in ((b.k, k0), (b.v, v0)):
+            assert torch.equal(new[p, :, r], old[p, :, r])
+        assert torch.equal(b.mass[p, :, r], mass0[p, :, r])
+
+
 def test_calls_on_two_streams_at_once():
     x = Batch(BF16, 128, 4, 1, 64, [1] * 8, [3000] * 8, seed=3)
     y = Batch(F16, 64, 2, 4, 32, [100, 7], [4000, 6000], seed=4)

@@ -140,6 +140,11 @@ def test_evict_refuses_a_destination_that_is_too_narrow():
     assert evict(cache(), cache(table_ld=3), budget=10000, recent=0) == pp.PP_E_RANGE
 
 
+@pytest.mark.parametrize("budget", [(1 << 28) + 1, 2**31 - 1])
+def test_evict_refuses_a_budget_beyond_any_table(budget):
+    assert evict(cache(), cache(), budget=budget, recent=0) == pp.PP_EINVAL
+
+
 def test_no_rows_is_no_work():
     assert append(cache(), T=0, q=0, k=0, v=0, out=0) == pp.PP_OK
     assert attention(cache(), T=0, q=0, out=0, scratch=0) == pp.PP_OK
