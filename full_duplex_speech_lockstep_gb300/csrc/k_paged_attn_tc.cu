@@ -7,8 +7,8 @@
 // partial wave are split over their keys and joined by k_paged_join_units (628 -> 580 us on the
 // case below, whose 512 units are 3.4 waves).
 //
-// Measured: 4096 tokens, 32 query heads on 8 of 128 dims, over 12000 entries, bf16: 580 us, 1150
-// TFLOP/s, 0.61 of the measured cuBLAS rate.  Bound by the two tiles' alternation: for each 128
+// Measured: 4096 tokens, 32 query heads on 8 of 128 dims, over 12000 entries, bf16: 565 us, 1180
+// TFLOP/s, 0.62 of the measured cuBLAS rate.  Bound by the two tiles' alternation: for each 128
 // keys of both tiles the products take 2048 clocks, a softmax about 1500 from its S to its P.
 //
 //   S_t = Q_t K^T   M = 128 rows, N = 128 keys, operands in shared memory, S in tensor memory
@@ -89,16 +89,12 @@ __device__ __forceinline__ Waves waves_of(int units, int most_parts, int room) {
   w.units = units;
   const int rest = units % (int)gridDim.x;
   w.whole = units - rest;
-  w.parts = 1;
-  // time of the last wave in 1/64 of a unit's; 2 for each part's start and join
-  int best = 64;
-  for (int p = 2; p <= most_parts && rest * p <= room; ++p) {
-    const int time = (rest * p + (int)gridDim.x - 1) / (int)gridDim.x * (64 / p + 4);
-    if (rest > 0 && time < best) {
-      best = time;
-      w.parts = p;
-    }
-  }
+  // time of the last wave in 1/64 of a unit's, 4 of them for each part's start and join: a lane to
+  // each number of parts (a loop over them took 1.8 us), the fewest of the fastest win
+  const int p = (int)(threadIdx.x & 31) + 1, grid = (int)gridDim.x;
+  const bool may = p > 1 && p <= most_parts && rest > 0 && rest * p <= room;
+  const int time = may ? (rest * p + grid - 1) / grid * (64 / p + 4) : p == 1 ? 64 : 1 << 20;
+  w.parts = (int)(__reduce_min_sync(0xffffffffu, (unsigned)(time * 64 + p)) & 63u);
   if (w.parts == 1) w.whole = units;
   return w;
 }
@@ -452,22 +448,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           // take non-finite values out of V (this group's rows of the tile)
           const int share = kTile / tiles;
           uint8_t* vt = smem + vslot * C::kTileBytes;
-          bool found = false;
-#pragma unroll 1
-          for (int i = r; i < share * (D / 8); i += 128) {
+          bool found = false, any = false;
+          auto chunk = [&](int i) {       // 16 bytes of the tile
             const int row = t * share + i / (D / 8), ch = i % (D / 8);
-            uint4* at = reinterpret_cast<uint4*>(
-                vt + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-            uint4 w = *at;
-            const bool hit = finite_only<N>(w.x) | finite_only<N>(w.y) | finite_only<N>(w.z) |
-                             finite_only<N>(w.w);
-            if (hit) {
-              *at = w;
-              found = found || (j0 + row >= x.low && j0 + row < x.stop);
+            return reinterpret_cast<uint4*>(vt + (ch >> 3) * (kTile * 128) + row * 128 +
+                                            (((ch & 7) ^ (row & 7)) << 4));
+          };
+          // four at a time, as the share is a multiple of them; looked at closer only if need be
+#pragma unroll 1
+          for (int i0 = r; i0 < share * (D / 8); i0 += 4 * 128) {
+            uint4 w[4];
+            uint32_t z = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = *chunk(i0 + k * 128);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              N::probe(z, w[k].x);
+              N::probe(z, w[k].y);
+              N::probe(z, w[k].z);
+              N::probe(z, w[k].w);
+            }
+            if ((z & 0x7fff7fffu) == 0) continue;
+            any = true;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              const int i = i0 + k * 128, row = t * share + i / (D / 8);
+              uint4 y = *chunk(i);
+              const bool hit = finite_only<N>(y.x) | finite_only<N>(y.y) | finite_only<N>(y.z) |
+                               finite_only<N>(y.w);
+              if (hit) {
+                *chunk(i) = y;
+                found = found || (j0 + row >= x.low && j0 + row < x.stop);
+              }
             }
           }
           if (found) ctl->wild[t][nu % (2 * kUnits)] = x.tag;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (any) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (tiles == 2) {    // both halves, before either product
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl->clean[t][ne & 1]));
@@ -483,15 +499,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kTile; ++i) asm volatile("" : "+r"(s[i]));
           if constexpr (decltype(masked)::value) {
-            // keys (pos - window, pos], as places in this tile
+            // keys (pos - window, pos], as places in this tile; 32 at a time, for few of which
+            // some row of the warp does not see all
             const int hi = pos - j0, lo = a.window ? hi - a.window : -1;
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-              if (i > hi || i <= lo) s[i] = 0xff800000u;
-            if (bad) {
-  #pragma unroll
-              for (int i = 0; i < kTile; ++i)
-                if ((bad >> (i >> 4)) & 1u) s[i] = 0xff800000u;
+            for (int c = 0; c < kTile / 32; ++c) {
+              const int h = hi - c * 32, b = lo - c * 32;
+              uint32_t see = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
+              if (b >= 0) see &= b >= 31 ? 0u : ~((2u << b) - 1u);
+              if ((bad >> (2 * c)) & 1u) see &= 0xffff0000u;
+              if ((bad >> (2 * c + 1)) & 1u) see &= 0xffffu;
+              if (__any_sync(0xffffffffu, see != ~0u)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!((see >> i) & 1u)) s[c * 32 + i] = 0xff800000u;
+              }
             }
           }
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
