@@ -34,12 +34,12 @@
 // value of V is taken out of the product and, at the unit's end, added to the rows that see
 // the key.
 //
-// Measured (bf16, 128 dims, in a graph): 64 sequences of 1 token and up to 24576 entries, 4 heads
-// on each of 8 key heads, pages of 64: 271 us, 5.7 TB/s (0.84 of the measured copy rate; 1.01 with
-// equal lengths: what is left are the ends of short sequences' units, about 4500 clocks each).  8
-// sequences of 1 to 5 tokens, up to 65000 entries, pages of 16: 212 us, 4.4 TB/s, bound by the
-// products of 20 rows by mma.sync.  One sequence of 12000 entries: 14 us, of which the launches,
-// the first tiles' way and the join are 7.
+// Measured (128 dims, in a graph): 64 sequences of 1 token and up to 3000 entries, 32 heads on 32
+// key heads, pages of 64, bf16: 273 us, 5.6 TB/s (0.83 of the measured copy rate; 1.01 with equal
+// lengths: what is left are the ends of the many short units, about 4500 clocks each).  8
+// sequences of up to 5 tokens and 65000 entries, 32 heads on 8, pages of 16, fp16: 212 us, 4.4
+// TB/s, bound by the products of up to 20 rows with mma.sync.  One token over 3000 entries, 32
+// heads: 14 us, half of it launches, the first tiles' way and the join.
 #include "pp_paged.cuh"
 
 namespace pp {

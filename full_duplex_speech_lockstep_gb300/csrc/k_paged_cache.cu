@@ -54,10 +54,10 @@ __device__ __forceinline__ void store8(T* p, const float x[8]) {
 // One CTA to a token, D/8 lanes to a head.  Bound by reading and writing the rows once: the
 // first heads' loads go out before the token's place in the cache is known, whose chain of
 // lookups (row offsets, length, page) they hide.
-// Measured (bf16): 6021 tokens of 32 + 2 x 8 heads of 128: 49 us, 3.0 TB/s (37 without the norm);
-// 64 tokens: 6.2 us; 3 tokens: 3.6 us, the launch.  Bound by the latency of a CTA's one pass, at
-// 64 registers.  (Ten tokens to a CTA with the next one's loads ahead: 46 to 60 us, and slower
-// for few tokens.)
+// Measured (in a graph): 4 sequences of up to 6000 tokens, 6021 in all, 32 + 2 x 8 heads of 128
+// dims, bf16: 49 us, 3.0 TB/s (37 without the norm); 64 tokens of 32 + 2 x 32 heads, fp32 in: 6.2
+// us.  Bound by the latency of a CTA's one pass.  (Ten tokens to a CTA with the next one's loads
+// ahead: 46 to 60 us, and slower for few tokens.)
 template <typename I, typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads)
     k_paged_append(const __grid_constant__ Args a, const __grid_constant__ AppendArgs x,
@@ -196,9 +196,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // One cluster of CTAs to a (sequence, key head), a slice of the older entries to a CTA.  Each
 // round counts the next bits of the keys that still match, adds the CTAs' counts up through
 // distributed shared memory and finds, in every CTA alike, the digit of the last key to stay.
-// With the copy below: 64 sequences x 8 heads of up to 24576 entries down to 4096: 109 us, 5.3
-// TB/s; 4 x 8 of up to 32768: 36 us.  Few pairs are bound by the rounds' latency (three, each with
-// three cluster barriers), many by the copy.  One CTA to a pair took 100 us for the latter.
+// With the copy below: 16 sequences x 32 heads of 128 dims, up to 3000 entries down to 1500: 109
+// us, 5.3 TB/s; 2 x 8, 40000 entries down to 5001, pages of 16: 36 us (one CTA to a pair: 100).
+// Few pairs are bound by the rounds' latency (three, each with three cluster barriers), many by
+// the copy.
 __global__ void __launch_bounds__(kSelThreads)
     k_paged_select(const __grid_constant__ Args a, const __grid_constant__ EvictArgs x,
                    const int cluster_size) {

@@ -8,12 +8,13 @@
 // so that a thread owns a key (a tensor-memory lane) and adds up its weights in row order:
 // no sum crosses threads, nothing is added atomically, and the bits are the same in every run.
 // (With one tile to a unit each step's 32 KB of rows served 128 keys only, and reading them
-// from L2 bounded the kernel: 114 us for 4 x 300 rows over up to 16000 entries.)
+// from L2 bounded the kernel: 114 us for the 4 x 300 tokens below.)
 //
-// Measured (bf16, 128 dims): 64 sequences of 1 token and up to 24576 entries, 4 heads on each of 8
-// key heads: 164 us, 4.8 TB/s, bound by reading K once and by the units' start, two tiles each.
-// 4 x 300 rows: 94 us, 815 TFLOP/s, bound by the exponentials and sums: 2200 clocks a step of two
-// tiles, whose products take half of that.
+// Measured (bf16, 128 dims, in a graph): 64 sequences of 1 token and up to 3000 entries, 32 heads on
+// 32 key heads: 164 us, 4.8 TB/s, bound by reading K once and by the units' starts, two tiles to
+// a unit.  4 sequences of up to 300 tokens and 16000 entries, 32 heads on 8: 94 us, 815 TFLOP/s,
+// bound by the exponentials and sums: 2200 clocks a step of two tiles, whose products take half
+// of that.
 //
 // A CTA takes a run of consecutive units of about the same number of steps as the others:
 //   warp 0        producer: the units and their key tiles, by TMA
