@@ -13,8 +13,8 @@
 // Measured (bf16, 128 dims, in a graph): 64 sequences of 1 token and up to 3000 entries, 32 heads on
 // 32 key heads: 164 us, 4.8 TB/s, bound by reading K once and by the units' starts, two tiles to
 // a unit.  4 sequences of up to 300 tokens and 16000 entries, 32 heads on 8: 94 us, 815 TFLOP/s,
-// bound by the exponentials and sums: 2200 clocks a step of two tiles, whose products take half
-// of that.
+// bound by the way from S to the sums: 2500 clocks a step of two tiles, whose products take
+// 1024 and whose exponentials as many.  (16 warps of sums instead of 8: the same.)
 //
 // A CTA takes a run of consecutive units of about the same number of steps as the others:
 //   warp 0        producer: the units and their key tiles, by TMA
