@@ -59,7 +59,7 @@ __device__ __forceinline__ void store8(T* p, const float x[8]) {
 // us.  Bound by the latency of a CTA's one pass.  (Ten tokens to a CTA with the next one's loads
 // ahead: 46 to 60 us, and slower for few tokens.)
 template <typename I, typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, sizeof(I) == 2 ? 4 : 3)
     k_paged_append(const __grid_constant__ Args a, const __grid_constant__ AppendArgs x,
                    const __grid_constant__ Turns turns) {
   constexpr int L = D / 8;                       // lanes of one head
@@ -103,14 +103,20 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int in_page = j & ((1 << a.lps) - 1);
   if (j >= 0 && page < 0 && threadIdx.x == 0) raise(a, PP_S_INDEX);
   const int pos = x.positions ? given : j;
-  for (int i = threadIdx.x; i < x.rot / 2; i += kAppendThreads) {
-    const uint64_t turn = (uint64_t)(int64_t)pos * turns.f[i];
+  // partners half a rotation apart: in one lane's same place if that is a multiple of 8 dims (then
+  // cs lies by places, for lanes to read neighbouring words)
+  const int half = x.rot / 2;
+  const bool by_lane = x.halves && (half & 7) == 0;
+  for (int i = threadIdx.x; i < half; i += kAppendThreads) {
+    const uint64_t angle = (uint64_t)(int64_t)pos * turns.f[i];
     float sn, cn;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cn);
-    cs[i] = make_float2(cn, sn);
+    sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &sn, &cn);
+    cs[by_lane ? (i & 7) * (D / 16) + (i >> 3) : i] = make_float2(cn, sn);
   }
   __syncthreads();
-  const int half = x.rot / 2;
+  float2 turn[4];                                // of this thread's neighbouring pairs
+#pragma unroll
+  for (int e = 0; e < 4; ++e) turn[e] = !x.halves && l * 8 + 2 * e < x.rot ? cs[l * 4 + e] : float2{};
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += kAppendRows * kHeads) {
     if (r0 > 0) load(r0);
@@ -132,15 +138,26 @@ __global__ void __launch_bounds__(kAppendThreads)
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (live && alpha) {
-        const float inv = 1.f / sqrtf(ss * (1.f / D) + x.eps);
+        const float inv = rsqrtf(ss * (1.f / D) + x.eps);   // off by 2^-22 at most
         const float4 a0 = reinterpret_cast<const float4*>(alpha + l * 8)[0];
         const float4 a1 = reinterpret_cast<const float4*>(alpha + l * 8)[1];
         const float al[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * al[e];
       }
-      if (x.halves) {
-        // partners lie half a rotation apart, in another lane
+      if (by_lane) {
+        const int hl = half / 8, lane = threadIdx.x & 31;
+        const bool lo = l < hl, in = l < 2 * hl;
+        const int from = !in ? lane : lo ? lane + hl : lane - hl, place = lo ? l : l - hl;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float o = __shfl_sync(0xffffffffu, y[e], from);
+          if (!in || kind == 2) continue;
+          const float2 w = cs[e * (D / 16) + place];
+          y[e] = lo ? y[e] * w.x - o * w.y : o * w.y + y[e] * w.x;
+        }
+      } else if (x.halves) {
+        // any distance: through shared memory
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 8; ++e) row[group][l * 8 + e] = y[e];
@@ -161,7 +178,7 @@ __global__ void __launch_bounds__(kAppendThreads)
         for (int e = 0; e < 8; e += 2) {
           const int d = l * 8 + e;
           if (d >= x.rot) continue;
-          const float2 w = cs[d / 2];
+          const float2 w = turn[e / 2];
           const float p = y[e], o = y[e + 1];
           y[e] = p * w.x - o * w.y;
           y[e + 1] = p * w.y + o * w.x;
