@@ -55,9 +55,11 @@ __device__ __forceinline__ void store8(T* p, const float x[8]) {
 // first heads' loads go out before the token's place in the cache is known, whose chain of
 // lookups (row offsets, length, page) they hide.
 // Measured (in a graph): 4 sequences of up to 6000 tokens, 6021 in all, 32 + 2 x 8 heads of 128
-// dims, bf16: 49 us, 3.0 TB/s (37 without the norm); 64 tokens of 32 + 2 x 32 heads, fp32 in: 6.2
-// us.  Bound by the latency of a CTA's one pass.  (Ten tokens to a CTA with the next one's loads
-// ahead: 46 to 60 us, and slower for few tokens.)
+// dims, bf16: 43 us, 3.5 TB/s (39 without the norm, 50 with halves); fp32 in: 53 us, 4.2 TB/s; 64
+// tokens of 32 + 2 x 32 heads, fp32 in: 6 us.  Bound by what four CTAs on an SM keep in flight: 64
+// registers a thread (at 114, two CTAs, 65 us; at 48, five, they spill).  Halves through shared
+// memory took 75 us.  (Ten tokens to a CTA with the next one's loads ahead: no faster, and slower
+// for few tokens.)
 template <typename I, typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(I) == 2 ? 4 : 3)
     k_paged_append(const __grid_constant__ Args a, const __grid_constant__ AppendArgs x,
