@@ -3,7 +3,7 @@
 //
 // For row (t, g) of a sequence (new token t of n, query head g of a key head's G), with L
 // cache entries, the new ones included and last:
-//   p(t) = L - n + t;  keys j in (p - window, p] (or [0, p]);
+//   p(t) = L - n + t;  keys j in (p - window, p] (or [0, p]) that the table's row has room for;
 //   out = sum_j exp(s_j - lse) V_j,  s_j = scale q . K_j,  lse = log sum_j exp(s_j).
 // One pass over the keys with a running reference m and sum l, in powers of two.
 //
@@ -113,7 +113,7 @@ struct Walk {
   int t0, nt;            // first token of the row tile, its tokens
   int first;             // entry index of that token
   int tile0, tile1;      // key tiles of the split
-  int stop;              // entries that the last row sees end here
+  int stop;              // entries that the last row sees end here (or the table's row does)
 
   __device__ __forceinline__ Walk(const Args& a_, const int* pre_, int tp_, int share_)
       : a(a_), pre(pre_), tp(tp_), share(share_) {
@@ -165,8 +165,8 @@ struct Walk {
     if (done()) return;
     t0 = rt > 1 ? i * tp : 0;
     nt = min(tp, s.n - t0);
-    first = s.len - s.n + t0;
-    stop = max(first + nt, 0);
+    first = s.total - s.n + t0;
+    stop = min(max(first + nt, 0), s.len);
     const int lo = a.window ? max(first - a.window + 1, 0) : 0;
     const int ta = min(lo, stop) / kTile, tb = (stop + kTile - 1) / kTile;
     tile0 = rt > 1 ? ta : min(ta + i * st, tb);
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   prefix_units(a, pre, [&](int b) {
     const Seq s = seq_of(a, b);
     if (s.n == 0) return 0;
+    check_len(a, s);
     int rt, st, ns, cost;
     return a.Hk * Walk::head_units(a, s, tp, share, rt, st, ns, cost) * cost;
   });
@@ -241,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       a.window ? max(x.first - a.window + 1, 0) : 0, x.stop, x.i, x.ns, x.at + 1},
                  lane, abort_flag);
         if (x.tile0 == x.tile1) continue;
-        TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, lane);
+        const bool past = x.first + x.nt > x.stop;
+        TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, past, lane);
         const int qb = nq % kQBufs;
         if (nq >= kQBufs) wait(&ctl->qempty[qb], (nq / kQBufs - 1) & 1);
         if (*abort_flag) break;
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = x.tile0; t < x.tile1; ++t, ++nk) {
           const int ks = nk % C::KS;
           const TilePages now = next;
-          if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, lane);
+          if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, past, lane);
           if (nk >= C::KS) wait(&ctl->kempty[ks], (nk / C::KS - 1) & 1);
           if (*abort_flag) break;
           load_key_tile(a, &mapK, smem_u32(smem + ks * C::kTileBytes), smem_u32(&ctl->kfull[ks]),
@@ -285,12 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
         if (x.tile0 == x.tile1) continue;
-        TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, lane);
+        const bool past = x.first + x.nt > x.stop;
+        TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, past, lane);
 #pragma unroll 1
         for (int t = x.tile0; t < x.tile1; ++t, ++nv) {
           const int vs = nv % C::VS;
           const TilePages now = next;
-          if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, lane);
+          if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, past, lane);
           if (nv >= C::VS) wait(&ctl->vempty[vs], (nv / C::VS - 1) & 1);
           if (*abort_flag) break;
           load_key_tile(a, &mapV, smem_u32(smem + C::kVOff + vs * C::kTileBytes),

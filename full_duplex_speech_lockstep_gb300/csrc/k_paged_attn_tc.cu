@@ -74,6 +74,7 @@ struct Ctl {
 // Units before any split: (pair of row tiles, key head).
 __device__ __forceinline__ int seq_units(const Args& a, int b, int tp) {
   const Seq s = seq_of(a, b);
+  if (s.n > 0) check_len(a, s);
   return a.Hk * ((s.n + 2 * tp - 1) / (2 * tp));
 }
 
@@ -122,8 +123,8 @@ __device__ __forceinline__ Unit unit_of(const Args& a, const int* pre, const Wav
   const int t0 = p * 2 * tp;
   x.row = s.row0 + t0;
   x.nt = min(2 * tp, s.n - t0);
-  x.first = s.len - s.n + t0;
-  x.stop = max(x.first + x.nt, 0);
+  x.first = s.total - s.n + t0;
+  x.stop = min(max(x.first + x.nt, 0), s.len);
   x.low = a.window ? min(max(x.first - a.window + 1, 0), x.stop) : 0;
   const int ta = x.low / kTile, tb = (x.stop + kTile - 1) / kTile;
   const int st = max((tb - ta + x.ns - 1) / x.ns, x.ns > 1 ? 4 : 0);
@@ -281,13 +282,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                           bx * 64, x.h * a.G, x.row + t * tp, 0, bar);
         }
         ++nq;
-        TilePages now{}, next = find_pages(a, x.b, x.tile0 * kTile, x.stop, lane);
+        const bool past = x.first + x.nt > x.stop;
+        TilePages now{}, next = find_pages(a, x.b, x.tile0 * kTile, x.stop, past, lane);
 #pragma unroll 1
         for (int i = 0; i < 2 * (x.tile1 - x.tile0); ++i) {
           const int slot = nl % kSlots, t = x.tile0 + (i >> 1);
           if ((i & 1) == 0) {
             now = next;
-            if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, lane);
+            if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, past, lane);
             seen_bad |= now.bad;
           }
           if (nl >= kSlots) wait(&ctl->empty[slot], (nl / kSlots - 1) & 1);

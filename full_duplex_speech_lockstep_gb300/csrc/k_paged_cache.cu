@@ -95,13 +95,13 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(I) == 2 ? 4 : 3)
     const Seq s = seq_of(a, b);
     if (t >= s.row0 && t < s.row0 + s.n) {
       found = b;
-      entry = s.len - s.n + (t - s.row0);
+      entry = s.total - s.n + (t - s.row0);
     }
   }
   __syncthreads();
   const int b = found, j = entry;
   if (b < 0) return;                             // a row of no sequence
-  const int page = j >= 0 ? page_of(a, b, j) : -1;
+  const int page = j >= 0 && j < table_entries(a) ? page_of(a, b, j) : -1;
   const int in_page = j & ((1 << a.lps) - 1);
   if (j >= 0 && page < 0 && threadIdx.x == 0) raise(a, PP_S_INDEX);
   const int pos = x.positions ? given : j;
@@ -241,7 +241,10 @@ __global__ void __launch_bounds__(kSelThreads)
   const uint32_t want = (uint32_t)(m - safe);       // of which this many stay
   int32_t* kept = x.kept + (int64_t)pair * x.budget;
   const int step = cluster_size * kSelThreads, first = rank * kSelThreads + tid;
-  if (h == 0 && first == 0) x.to_len[b] = m;
+  if (h == 0 && first == 0) {
+    x.to_len[b] = m;
+    if (a.len[b] > len) raise(a, PP_S_INDEX);
+  }
   for (int i = m + first; i < x.budget; i += step) kept[i] = -1;
   if (m == len) {
     for (int i = first; i < m; i += step) kept[i] = i;

@@ -106,7 +106,7 @@ struct Walk {
   __device__ __forceinline__ void unit() {
     if (done()) return;
     j0 = pair * 2 * kTile;
-    const int first = s.len - s.n;
+    const int first = s.total - s.n;
     t0 = max(0, j0 - first);
     t1 = s.n;
     if (a.window)
@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   prefix_units(a, pre, [&](int b) -> int64_t {
     const Seq s = seq_of(a, b);
     if (s.n == 0 && decay == 1.f) return 0;
+    check_len(a, s);
     return (int64_t)a.Hk * ((s.len + 2 * kTile - 1) / (2 * kTile)) * unit_cost(s, tp);
   });
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -244,13 +245,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x.done()) return;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        next[i] = find_pages(a, x.b, x.j0 + i * kTile, x.s.len, lane);
+        next[i] = find_pages(a, x.b, x.j0 + i * kTile, x.s.len, false, lane);
     };
     find();
 #pragma unroll 1
     while (!x.done() && !*abort_flag) {
       // this unit, and the next one's pages on their way
-      const Unit u{x.b, x.h, x.s.row0 + x.t0, x.t1 - x.t0, x.s.len - x.s.n + x.t0, 2 * x.pair,
+      const Unit u{x.b, x.h, x.s.row0 + x.t0, x.t1 - x.t0, x.s.total - x.s.n + x.t0, 2 * x.pair,
                    min(2 * x.pair + 2, (x.s.len + kTile - 1) / kTile), 0, x.s.len, 0, 1, 0};
       const TilePages now[2] = {next[0], next[1]};
       x.next();

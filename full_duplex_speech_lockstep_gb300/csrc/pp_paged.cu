@@ -57,10 +57,8 @@ bool rows_ok(const pp_paged_kv* kv, const int32_t* cu, const int32_t* kv_len, in
   return G <= kMaxGroup && T <= 1 << 28 && (int64_t)T * n_heads < (int64_t)1 << 31;
 }
 
-// A window that no sequence outgrows is none.
-int effective_window(const pp_paged_kv* kv, int window) {
-  return window >= (int64_t)kv->table_ld * kv->page_size ? 0 : window;
-}
+// A window that no row outgrows is none.
+int effective_window(int window) { return window >= kMaxLen ? 0 : window; }
 
 bool scores_ok(float scale, int window, int max_q) {
   return scale > 0.f && scale <= 1e30f && window >= 0 && max_q >= 1;
@@ -156,7 +154,7 @@ size_t pp_paged_attention_scratch_bytes(const pp_paged_kv* kv, int n_heads, int 
     return 0;
   Args a = base_args(kv, nullptr, nullptr);
   a.G = n_heads / kv->n_kv_heads;
-  a.window = effective_window(kv, window);
+  a.window = effective_window(window);
   if (is_long(a, max_q)) {
     const LongPlan p = long_plan(a, T);
     return p.rec_bytes + p.ml_bytes + p.plan_bytes + 256;
@@ -184,7 +182,7 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
   a.cu = cu;
   a.T = T;
   a.G = n_heads / kv->n_kv_heads;
-  a.window = effective_window(kv, window);
+  a.window = effective_window(window);
   a.c = scale * kLog2e;
   AttnOut o{};
   o.out = out;
@@ -217,7 +215,7 @@ int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const 
   a.cu = cu;
   a.T = T;
   a.G = n_heads / kv->n_kv_heads;
-  a.window = effective_window(kv, window);
+  a.window = effective_window(window);
   a.c = scale * kLog2e;
   if (T > 0 && (!q || !lse || q_stride < n_heads * D || (q_stride & 7) ||
                 q_stride >= (int64_t)1 << 38 || !aligned(q, 16) || !aligned(lse, 4)))

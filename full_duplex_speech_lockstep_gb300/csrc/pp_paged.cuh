@@ -14,6 +14,8 @@ namespace paged {
 constexpr int kTile = 128;       // cache entries of one key tile
 constexpr int kMaxSeqs = 2048;   // sequences of one call (their prefix sums sit in shared memory)
 constexpr int kMaxGroup = 64;    // query heads to a key head
+constexpr int kMaxLen = 1 << 30; // larger kv_len count as this: four times the longest table row, and
+                                 // differences of places and windows stay within 32 bits
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -33,21 +35,24 @@ struct Args {
 };
 
 struct Seq {
-  int row0, n, len;        // first row, new tokens, cache entries (new ones included)
+  int row0, n;             // first row, new tokens
+  int total, len;          // kv_len (new tokens included), and the entries that have a place
 };
 
 // Lengths and tables are read with plain loads: an earlier kernel of the same stream may
 // have written them while this one was already on its SM (programmatic launch), which the
 // non-coherent path does not allow.
+__device__ __forceinline__ int table_entries(const Args& a) { return a.table_ld << a.lps; }
 __device__ __forceinline__ int seq_len(const Args& a, int b) {
-  return min(max(a.len[b], 0), a.table_ld << a.lps);
+  return min(max(a.len[b], 0), table_entries(a));
 }
 
 __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   Seq s;
   s.row0 = min(max(a.cu[b], 0), a.T);
   s.n = min(max(a.cu[b + 1], s.row0), a.T) - s.row0;
-  s.len = seq_len(a, b);
+  s.total = min(max(a.len[b], 0), kMaxLen);
+  s.len = min(s.total, table_entries(a));
   return s;
 }
 
@@ -59,6 +64,12 @@ __device__ __forceinline__ int page_of(const Args& a, int b, int j) {
 
 __device__ __forceinline__ void raise(const Args& a, uint32_t bits) {
   if (a.status) atomicOr(a.status, bits);
+}
+
+// New tokens sit where kv_len says, so rows and entries are counted from it; entries past the
+// table's row have no place and take no part.  One CTA of a call reports a length that has such.
+__device__ __forceinline__ void check_len(const Args& a, const Seq& s) {
+  if (s.total > s.len && blockIdx.x == 0) raise(a, PP_S_INDEX);
 }
 
 // Bounded wait for a barrier's phase.  A phase that has completed costs one test; only a wait
@@ -143,7 +154,8 @@ struct alignas(16) Unit {
   int row, nt;           // first row of the unit's tokens, how many
   int first;             // entry index of that token (of the sequence's first one: k_paged_mass)
   int tile0, tile1;      // key tiles
-  int low, stop;         // entries that some row sees lie in [low, stop)
+  int low, stop;         // entries that some row sees lie in [low, stop); stop < first + nt where
+                         // the table's row ends before the last token
   int split, ns;         // split of the keys, of how many
   int tag;               // 1 + the unit's place in this CTA's run
 };
@@ -200,18 +212,20 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int box_bytes, int 
 }
 
 // Loading a key tile (entries [j0, j0 + 128) of head h) by one warp, a lane for each (page, 64-dim
-// box).  Its lane's page comes first, so that the lookup can be on its way ahead of time.  Entries
-// at or past `end` and pages outside the pool arrive as zeros.
+// box).  Its lane's page comes first, so that the lookup can be on its way ahead of time.  Pages at
+// or past `end` and pages outside the pool arrive as zeros.  `past`: the table's row ends at `end`,
+// and rows beyond it would see zeros there as keys, so these groups are marked too.
 struct TilePages {
   int page;              // of this lane's box; past the last page: zeros
-  uint32_t bad;          // in every lane: the tile's 16-key groups in pages outside the pool
+  uint32_t bad;          // in every lane: the tile's 16-key groups without a page of the pool
 };
-__device__ __forceinline__ TilePages find_pages(const Args& a, int b, int j0, int end, int lane) {
+__device__ __forceinline__ TilePages find_pages(const Args& a, int b, int j0, int end, bool past,
+                                                int lane) {
   const int per = min(1 << a.lps, kTile);          // rows of one box
   const int pages = kTile / per;
   const int j = j0 + (lane % pages) * per;
   TilePages x{a.n_pages, 0u};
-  bool bad = false;
+  bool bad = past && j >= end;
   if (lane < pages * (a.D >> 6) && j < end) {      // at most 16 loads
     const int p = page_of(a, b, j);
     bad = p < 0;
@@ -251,7 +265,7 @@ __device__ __noinline__ void add_lost(const Args& a, const void* v_pages, int b,
 #pragma unroll 1
   for (int t = tile0; t < tile1; ++t) {
     const int j0 = t * kTile, j1 = min(j0 + kTile, end);
-    bool edge = j0 + kTile - 1 > first || (a.window && j0 <= last - a.window);
+    bool edge = j0 + kTile - 1 > min(first, end - 1) || (a.window && j0 <= last - a.window);
 #pragma unroll 1
     for (int j = j0; j < j1; j += 1 << a.lps) edge |= page_of(a, b, j) < 0;
     if (!edge) continue;

@@ -513,7 +513,10 @@ int pp_rvq_dequantize(const int32_t* codes, int code_stride, int n_frames, int n
  * write entries or weights need each written row to belong to one place of one sequence.  All
  * device arrays are the caller's.  A page number outside [0, n_pages) that a call needs is
  * never followed: nothing is stored there, its entries take no part, and PP_S_INDEX is OR-ed
- * into the status word.  Table entries past a sequence's last page are not looked at.  kv_len is clamped to [0, table_ld * page_size].
+ * into the status word.  The same holds for entries that kv_len counts past the table's row
+ * (from table_ld * page_size on): new rows keep the places that kv_len gives them, what has no
+ * place is not stored, and nothing else changes.  Table entries past a sequence's last page are
+ * not looked at.  A kv_len below 0 counts as 0, one above 2^30 as 2^30.
  *
  * New rows are packed: sequence b has rows cu[b] .. cu[b+1] - 1 of the T rows, its newest
  * tokens, in order; a sequence may have none.  cu ascends.  Its values are clamped to [0, T];
@@ -521,8 +524,9 @@ int pp_rvq_dequantize(const int32_t* codes, int code_stride, int n_frames, int n
  * written.  (Offsets that fall all the same, so that sequences share rows, leave undefined
  * results in those rows and entries, and touch nothing else.)
  * Row i of a sequence of n new rows sits at entry p = kv_len - n + i: kv_len counts the
- * new entries.  It sees the entries j <= p, with window > 0 only those with j > p - window
- * (entries are counted by index, so after an eviction a window counts what is left).
+ * new entries.  It sees the entries j <= p that have a place, with window > 0 only those with
+ * j > p - window (entries are counted by index, so after an eviction a window counts what is
+ * left).
  *
  * Every call is asynchronous on `stream`, belongs to the current device, allocates nothing
  * and may be captured into a graph; lengths, tables and row offsets are read when the
@@ -622,7 +626,7 @@ int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const 
  * sequence of `to`: other pages, of the same pool or another, of any page size.  No page may
  * be both read and written.  Keys stay rotated as they are: give later positions to
  * pp_paged_append.
- *   to_len  int32 [n_seqs]: min(kv_len, budget)
+ *   to_len  int32 [n_seqs]: min(kv_len, budget), of what kv_len counts only entries with a place
  *   kept    int32 [n_seqs][n_kv_heads][budget]: the entries that stayed, ascending, then -1
  * kv->mass is required, to->mass is written if given.  0 <= recent <= budget,
  * 1 <= budget <= 2^28.

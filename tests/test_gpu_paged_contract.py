@@ -1,0 +1,141 @@
+"""What the paged-cache calls promise beside their formulas: lengths past the table, a sequence's
+bits, rows that are to give nothing, calls from several host threads (GPU).  Tolerances are those
+of test_gpu_paged.py."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_paged import BF16, F16, Batch, check_mass, pp_, turned  # noqa: E402
+
+
+# ---- lengths past the table ---------------------------------------------------------------------
+
+def full(type, D, chunks, over, window=0, page=16, width=20, seed=1):
+    """Sequences that fill their table row (width * page entries), and one that does not; kv_len
+    says `over` entries more for the first ones.  `lens` are the entries that there are."""
+    cap = width * page
+    lens = [cap] * (len(chunks) - 1) + [cap // 2 + 3]
+    b = Batch(type, D, 2, 2, page, chunks, lens, window=window, seed=seed)
+    b.told = [cap + over] * (len(chunks) - 1) + lens[-1:]
+    b.len = torch.tensor(b.told, dtype=torch.int32, device="cuda")
+
+    def sees(s):
+        p = torch.arange(b.told[s] - b.chunks[s], b.told[s], device="cuda")[:, None]
+        j = torch.arange(b.lens[s], device="cuda")[None]
+        m = j <= p
+        return m & (j > p - b.window) if b.window else m
+    b.sees = sees
+    return b
+
+
+OVER = [(over, window) for over in (1, 3, 70) for window in (0, 50)] + [(70, 325)]
+
+
+@pytest.mark.parametrize("type,D", [(BF16, 128), (F16, 64)])
+@pytest.mark.parametrize("over,window", OVER)
+@pytest.mark.parametrize("chunks", [[1, 1], [5, 2], [200, 9]])
+def test_rows_keep_their_places_when_the_table_is_full(chunks, over, window, type, D):
+    """Row i sits at entry kv_len - n + i whether or not that entry has a place; the entries that
+    have none take no part, and the status says so."""
+    b = full(type, D, chunks, over, window)
+    kv = b.kv()
+    out, lse = kv.attention(b.q, b.cu, b.len, max_q=max(chunks), window=window, with_lse=True)
+    assert kv.read_status() == pp_().PP_S_INDEX
+    b.check(out, lse)
+    before = b.mass.clone()
+    kv.attention_mass(b.q, lse, b.cu, b.len, max_q=max(chunks), window=window, decay=0.5)
+    assert kv.read_status() == pp_().PP_S_INDEX
+    for s in range(len(chunks)):
+        check_mass(b, s, before, b.mass, lse, 0.5)
+    # a stored infinity in the last tile reaches the rows that see it and no other
+    p, r = b.where(0)
+    j = b.lens[0] - 2
+    v = b.v.clone()
+    v[p[j], :, r[j], 3] = math.inf
+    got, gl = pp_().PagedKV(b.k, v, b.table).attention(b.q, b.cu, b.len, max_q=max(chunks),
+                                                       window=window, with_lse=True)
+    see = torch.zeros(b.T, dtype=torch.bool, device="cuda")
+    see[b.at[0]:b.at[1]] = b.sees(0)[:, j]
+    ok = torch.ones_like(got, dtype=torch.bool)
+    ok[see, :, 3] = False
+    assert torch.equal(got[ok], out[ok]) and torch.equal(gl, lse)
+    assert (got[see][:, :, 3] == math.inf).all()
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("chunk,over", [(1, 1), (5, 2), (5, 40), (40, 1)])
+def test_append_past_the_table_leaves_the_entries_that_are_there(chunk, over, far):
+    b = full(BF16, 128, [chunk, 3], over)
+    x = torch.randn((b.T, 4 + 2 + 2, 128), generator=b.g, device="cuda").to(BF16)
+    K, V, M = b.k.clone(), b.v.clone(), b.mass.clone()
+    kv = pp_().PagedKV(K, V, b.table, mass=M)
+    entry = torch.cat([torch.arange(b.told[s] - b.chunks[s], b.told[s]) for s in range(2)]).int().cuda()
+    pos = entry + 1000 if far else entry
+    out = kv.append(x[:, :4], x[:, 4:6], x[:, 6:], b.cu, b.len, positions=pos if far else None)
+    assert kv.read_status() == pp_().PP_S_INDEX
+    want, tol = turned(x[:, :4], None, pos, 128, False)
+    half = torch.finfo(BF16).eps / 2
+    assert ((out.double() - want).abs() <= tol + half * want.abs()).all()
+    kw, ktol = turned(x[:, 4:6], None, pos, 128, False)
+    touched = torch.zeros(b.n_pages, b.page, dtype=torch.bool, device="cuda")
+    for s in range(2):
+        p, r = b.where(s)
+        for i in range(b.chunks[s]):
+            j, t = b.told[s] - b.chunks[s] + i, b.at[s] + i
+            if j >= b.lens[s]:
+                continue
+            touched[p[j], r[j]] = True
+            assert torch.equal(V[p[j], :, r[j]], x[t, 6:])
+            assert ((K[p[j], :, r[j]].double() - kw[t]).abs() <= ktol[t] + half * kw[t].abs()).all()
+            assert (M[p[j], :, r[j]] == 0).all()
+    for new, old in ((K, b.k), (V, b.v), (M, b.mass)):
+        assert torch.equal(new.transpose(1, 2)[~touched], old.transpose(1, 2)[~touched])
+
+
+def test_lengths_of_any_size_are_taken():
+    """The largest int32 (taken as 2^30) and the lowest: the first sees its whole row, the other
+    nothing."""
+    b = full(BF16, 64, [2, 2], 2 ** 31 - 1 - 320)
+    b.told[0], b.told[1], b.lens[1] = 2 ** 30, 0, 0
+    b.len[1] = -(2 ** 31)
+    for max_q in (2, 300):
+        kv = b.kv()
+        out, lse = kv.attention(b.q, b.cu, b.len, max_q=max_q, with_lse=True)
+        b.check(out, lse)
+        assert kv.read_status() == pp_().PP_S_INDEX
+        assert (out[2:] == 0).all() and (lse[2:] == -math.inf).all()
+        got, gl = kv.attention(b.q, b.cu, b.len, max_q=max_q, window=100, with_lse=True)
+        assert (got == 0).all() and (gl == -math.inf).all()
+        kv.read_status()
+        before = b.mass.clone()
+        kv.attention_mass(b.q, lse, b.cu, b.len, max_q=max_q)
+        check_mass(b, 0, before, b.mass, lse, 1.0)
+        assert kv.read_status() == pp_().PP_S_INDEX
+        K, V, M = b.k.clone(), b.v.clone(), b.mass.clone()
+        kv2 = pp_().PagedKV(K, V, b.table, mass=M)
+        kv2.append(b.q, b.q[:, :2], b.q[:, :2], b.cu, b.len)
+        assert kv2.read_status() == pp_().PP_S_INDEX
+        assert torch.equal(K, b.k) and torch.equal(V, b.v) and torch.equal(M, b.mass)
+
+
+def test_evict_reports_a_length_past_the_table():
+    b = Batch(BF16, 64, 2, 1, 16, [0, 0], [320, 100])
+    want = b.kv().evict(b.len, 50, 7, other(b, 50))
+    b.len[0] = 333
+    kv = b.kv()
+    got = kv.evict(b.len, 50, 7, other(b, 50))
+    assert kv.read_status() == pp_().PP_S_INDEX
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def other(b, budget):
+    need = -(-budget // b.page)
+    n = need * len(b.lens)
+    K = torch.zeros((n, b.Hk, b.page, b.D), dtype=b.type, device="cuda")
+    table = torch.arange(n, dtype=torch.int32, device="cuda").view(len(b.lens), need)
+    return pp_().PagedKV(K, K.clone(), table, mass=torch.zeros(K.shape[:3], device="cuda"))
+
