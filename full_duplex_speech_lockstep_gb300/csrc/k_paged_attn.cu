@@ -16,8 +16,8 @@
 //   warp 0      the units, their query rows and K tiles by TMA, one box to a lane;
 //   warp 1      the V tiles (with pages of 16 a tile is 16 boxes: one warp for both was 328 us on
 //               the 64-session tick);
-//   warps 4-11  in two teams of four.  Up to 16 rows: a team to every second tile; up to 32: a
-//               team to 16 rows, both to every tile.  A warp takes 32 keys of a tile: S and P V
+//   warps 4-11  in two teams of four.  Up to 16 rows: a team to every second tile of a unit; up to 32:
+//               a team to 16 rows, both to every tile.  A warp takes 32 keys of a tile: S and P V
 //               as 16 x 8 x 16 matrix products, P handed from one to the other in registers,
 //               with the warp's own m, l and O (16 rows x D in fp32 registers).
 //               (All 32 rows in one warp, a team to every second tile, measured 295 us on 8
@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = x.tile0; t < x.tile1; ++t, ++n) {
       const int ks = n % C::KS, vs = n % C::VS;
       wait(&ctl->kfull[ks], (n / C::KS) & 1);
-      if (!kRowTeams && (n & 1) != team) {
+      // (counted within the unit: which warp sums a tile must not depend on this CTA's past units)
+      if (!kRowTeams && ((t - x.tile0) & 1) != team) {
         // the other team's tile: every warp sees every phase of every stage all the same (a
         // phase that passed unseen could not be told from the one before it)
         __syncwarp();

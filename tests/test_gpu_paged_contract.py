@@ -139,3 +139,45 @@ def other(b, budget):
     table = torch.arange(n, dtype=torch.int32, device="cuda").view(len(b.lens), need)
     return pp_().PagedKV(K, K.clone(), table, mass=torch.zeros(K.shape[:3], device="cuda"))
 
+
+# ---- a sequence's bits ---------------------------------------------------------------------------
+
+def alone(b, s, max_q, window=0):
+    a, e = b.at[s], b.at[s + 1]
+    kv = pp_().PagedKV(b.k, b.v, b.table[s:s + 1].contiguous())
+    return kv.attention(b.q[a:e], b.cu[s:s + 2] - a, b.len[s:s + 1], max_q=max_q, window=window,
+                        with_lse=True)
+
+
+@pytest.mark.parametrize("type,D,Hk,G,window", [(BF16, 128, 8, 1, 0), (F16, 64, 16, 2, 0),
+                                                (BF16, 64, 8, 4, 700)])
+def test_bits_do_not_depend_on_what_an_sm_has_done_before(type, D, Hk, G, window):
+    """Many short units to a CTA, most with an odd number of tiles."""
+    n = 64
+    lens = [1 + (s * 389) % 1900 for s in range(n)]
+    b = Batch(type, D, Hk, G, 64, [1] * n, lens, window=window)
+    out, lse = b.kv().attention(b.q, b.cu, b.len, max_q=1, window=window, with_lse=True)
+    b.check(out, lse)
+    for s in range(n):
+        one, l = alone(b, s, 1, window)
+        assert torch.equal(one, out[s:s + 1]) and torch.equal(l, lse[s:s + 1]), s
+
+
+def test_the_same_call_gives_the_same_bits():
+    x = Batch(BF16, 128, 8, 1, 64, [1] * 40, [3000 - 61 * i for i in range(40)])
+    y = Batch(F16, 128, 2, 4, 16, [5, 1, 8, 3], [9000, 20000, 700, 5000])
+    z = Batch(BF16, 64, 2, 3, 32, [700, 1, 90, 300], [5000, 3000, 90, 2000], window=1000)
+    noise = torch.randn((4096, 4096), device="cuda")
+    for b in (x, y, z):
+        kv, n = b.kv(), max(b.chunks)
+        got = []
+        for i in range(6):
+            if i & 1:
+                noise = noise @ noise / 64
+            o, l = kv.attention(b.q, b.cu, b.len, max_q=n, window=b.window, with_lse=True)
+            m = torch.ones_like(b.mass)
+            kv.attention_mass(b.q, l, b.cu, b.len, max_q=n, window=b.window, mass=m)
+            got.append((o, l, m))
+        for g in got[1:]:
+            assert all(torch.equal(p, q) for p, q in zip(g, got[0]))
+
