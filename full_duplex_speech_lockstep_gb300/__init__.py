@@ -670,8 +670,10 @@ class PagedKV:
 
     @staticmethod
     def _longest(max_q, T):
-        # the library's hint is at least 1; more than all rows no chunk can be
-        return max(1, T if max_q is None else min(max_q, T))
+        # The library's hint is an int32 of at least 1.  A caller's is handed on whatever T is: it
+        # picks the kernel and its tiles, and with them a sequence's bits, which must not depend on
+        # how many rows the rest of the batch has.
+        return max(1, min(T if max_q is None else max_q, 2 ** 31 - 1))
 
     def read_status(self):
         """Wait for the current stream, then read and clear the status word."""
@@ -711,7 +713,9 @@ class PagedKV:
     def attention(self, q, cu, kv_len, max_q=None, scale=None, window=0, with_lse=False,
                   out=None):
         """Attention of the new rows over the cache: out, or (out, lse) on request.  max_q is
-        the longest chunk as far as the host knows (default: all rows)."""
+        the longest chunk as far as the host knows.  It picks the kernel: give it where chunks are
+        short.  Without it all rows count as one chunk, so the kernel, and with it a sequence's
+        bits, goes by the batch's row count."""
         torch = self.torch
         T, H, qs = self._rows("q", q, self.dtype)
         self._batch(cu, kv_len)

@@ -181,3 +181,36 @@ def test_the_same_call_gives_the_same_bits():
         for g in got[1:]:
             assert all(torch.equal(p, q) for p, q in zip(g, got[0]))
 
+
+# ---- the caller's max_q ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("G,max_q,chunks,window", [
+    (4, 8, [4, 1, 8, 2, 1], 0), (4, 8, [4, 1, 8, 2, 1], 300), (8, 5, [1, 5, 1, 3, 1], 0),
+    (1, 40, [1, 3, 40, 16, 33], 0), (2, 7, [7, 1, 1, 1, 5], 129)])
+def test_bits_follow_the_callers_max_q(G, max_q, chunks, window):
+    """The wrapper hands on the max_q that it is given, however few rows the call has.  (Chunks of
+    more than 32 rows to a key head: compared one sequence to a call, in which nothing else sets
+    the splits.)"""
+    lens = [900, 77, 3000, 300, 1500]
+    b = Batch(BF16, 128, 2, G, 64, chunks, lens, window=window)
+    out, lse = b.kv().attention(b.q, b.cu, b.len, max_q=max_q, window=window, with_lse=True)
+    b.check(out, lse)
+    for s in range(len(chunks)):
+        one, l = alone(b, s, max_q, window)
+        if max_q * G <= 32:
+            assert torch.equal(one, out[b.at[s]:b.at[s + 1]]), s
+            assert torch.equal(l, lse[b.at[s]:b.at[s + 1]]), s
+        # the same through the C call, which knows nothing of the wrapper
+        a, e = b.at[s], b.at[s + 1]
+        pp, T = pp_(), e - a
+        kv = pp.PagedKV(b.k, b.v, b.table[s:s + 1].contiguous())
+        size = pp.pp_paged_attention_scratch_bytes(kv.c, b.H, T, max_q, window)
+        scratch = torch.empty(size, dtype=torch.uint8, device="cuda")
+        o2, l2 = torch.empty_like(one), torch.empty_like(l)
+        cu = (b.cu[s:s + 2] - a).contiguous()
+        pp.pp_paged_attention(kv.c, b.q[a:e].data_ptr(), b.H * b.D, cu.data_ptr(),
+                              b.len[s:s + 1].data_ptr(), T, max_q, b.H, b.scale, window,
+                              o2.data_ptr(), l2.data_ptr(), kv.status.data_ptr(), scratch.data_ptr(),
+                              size, torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(one, o2) and torch.equal(l, l2), s
+
