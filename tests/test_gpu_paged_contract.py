@@ -214,3 +214,49 @@ def test_bits_follow_the_callers_max_q(G, max_q, chunks, window):
                               size, torch.cuda.current_stream().cuda_stream)
         assert torch.equal(one, o2) and torch.equal(l, l2), s
 
+
+# ---- rows that give nothing ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("type,D,G,chunks,lens", [
+    (BF16, 128, 1, [1, 1], [700, 130]), (F16, 64, 4, [32, 5], [900, 300]),
+    (BF16, 128, 2, [64, 200], [1500, 700]), (BF16, 64, 3, [300, 40], [400, 2000])])
+@pytest.mark.parametrize("window", [0, 200])
+def test_a_row_without_a_sum_gives_nothing_whatever_it_holds(type, D, G, chunks, lens, window):
+    """Rows with an lse of -infinity, as a caller marks rows of padding, whose queries may be
+    anything."""
+    b = Batch(type, D, 2, G, 32, chunks, lens, window=window)
+    kv = b.kv()
+    _, lse = kv.attention(b.q, b.cu, b.len, window=window, with_lse=True)
+    dead = torch.rand(b.T, generator=b.g, device="cuda") < 0.4
+    dead[0] = True
+    lse[dead] = -math.inf
+    want = torch.zeros_like(b.mass)
+    kv.attention_mass(b.q, lse, b.cu, b.len, window=window, mass=want)
+    for s in range(2):
+        check_mass(b, s, torch.zeros_like(want), want, lse, 1.0)
+    for bad in (math.nan, math.inf, -math.inf, torch.finfo(type).max):
+        q = b.q.clone()
+        q[dead] = bad
+        got = torch.zeros_like(b.mass)
+        kv.attention_mass(q, lse, b.cu, b.len, window=window, mass=got)
+        assert torch.equal(got, want), bad
+
+
+@pytest.mark.parametrize("G,max_q", [(1, 8), (4, 40)])
+def test_the_entries_of_padding_rows_stay_empty(G, max_q):
+    """The last rows of a chunk are padding: neither their queries nor their keys are finite, and
+    they alone see these keys."""
+    b = Batch(BF16, 128, 2, G, 32, [40, 5], [500, 300])
+    kv, live = b.kv(), 30
+    _, lse = kv.attention(b.q, b.cu, b.len, max_q=40, with_lse=True)
+    lse[live:40] = -math.inf
+    want = torch.zeros_like(b.mass)
+    kv.attention_mass(b.q, lse, b.cu, b.len, max_q=max_q, mass=want)
+    p, r = (t[-10:] for t in b.where(0))
+    assert (want[p, :, r] == 0).all()
+    b.q[live:40] = math.nan
+    b.k[p, :, r] = math.nan
+    got = torch.zeros_like(b.mass)
+    kv.attention_mass(b.q, lse, b.cu, b.len, max_q=max_q, mass=got)
+    assert torch.equal(got, want)
+
