@@ -585,10 +585,11 @@ cudaError_t run(const Args& a, const AttnPlan& p, const Maps& maps, const AttnOu
                 const void* v_pages, cudaStream_t s) {
   const size_t smem =
       Cfg<D, WR>::kCtlOff + sizeof(Ctl) + (size_t)(a.n_seqs + 1) * sizeof(int) + 1024;
-  static_assert(Cfg<D, WR>::kCtlOff + sizeof(Ctl) + (kMaxSeqs + 1) * sizeof(int) + 1024 <=
-                    227 * 1024, "attention shared memory");
-  cudaError_t err = cudaFuncSetAttribute(k_paged_attn<T, D, WR>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr size_t most_smem =
+      Cfg<D, WR>::kCtlOff + sizeof(Ctl) + (kMaxSeqs + 1) * sizeof(int) + 1024;
+  static_assert(most_smem <= 227 * 1024, "attention shared memory");
+  static std::atomic<uint64_t> done{0};
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(k_paged_attn<T, D, WR>), most_smem, done);
   if (err != cudaSuccess) return err;
   // no more CTAs than units there can be
   const int64_t row_tiles = (int64_t)a.T / p.tp + a.n_seqs;

@@ -674,10 +674,10 @@ template <typename T, int D>
 cudaError_t run(const Args& a, const LongPlan& p, const Maps& maps, const AttnOut& o,
                 const void* v_pages, cudaStream_t s) {
   const size_t smem = Cfg<D>::kCtlOff + sizeof(Ctl) + (size_t)(a.n_seqs + 1) * sizeof(int) + 1024;
-  static_assert(Cfg<D>::kCtlOff + sizeof(Ctl) + (kMaxSeqs + 1) * sizeof(int) + 1024 <= 227 * 1024,
-                "long-chunk attention shared memory");
-  cudaError_t err = cudaFuncSetAttribute(k_paged_attn_tc<T, D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr size_t most_smem = Cfg<D>::kCtlOff + sizeof(Ctl) + (kMaxSeqs + 1) * sizeof(int) + 1024;
+  static_assert(most_smem <= 227 * 1024, "long-chunk attention shared memory");
+  static std::atomic<uint64_t> done{0};
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(k_paged_attn_tc<T, D>), most_smem, done);
   if (err != cudaSuccess) return err;
   const int64_t most = p.units * p.parts;
   const int nsm = sm_count();

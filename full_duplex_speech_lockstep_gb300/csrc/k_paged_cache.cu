@@ -458,8 +458,9 @@ cudaError_t launch_paged_evict(const Args& a, const EvictArgs& x, cudaStream_t s
     cluster *= 2;
   const int64_t slice = (entries + cluster - 1) / cluster;
   const size_t smem = (size_t)(slice < kSelKeys ? slice : kSelKeys) * sizeof(uint32_t);
-  cudaError_t err = cudaFuncSetAttribute(k_paged_select,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(k_paged_select),
+                               kSelKeys * (int)sizeof(uint32_t), done);
   if (err != cudaSuccess) return err;
   err = launch_cluster(cluster, k_paged_select, dim3((unsigned)(pairs * cluster)), kSelThreads, smem,
                        s, a, x, cluster);

@@ -543,13 +543,14 @@ cudaError_t run(const Args& a, const Maps& maps, int tp, const float* lse, float
   const int q_bytes = n * D * 2, tile = kTile * D * 2;
   // key tiles fill what the rows and the control block leave of 227 KB
   const int fixed = (int)(sizeof(Ctl) + (a.n_seqs + 1) * sizeof(int64_t)) + 1024 + kQStages * q_bytes;
-  int ks = (227 * 1024 - fixed) / tile;
+  constexpr int most_smem = 227 * 1024;
+  int ks = (most_smem - fixed) / tile;
   if (ks > kMaxStages) ks = kMaxStages;
   const size_t smem = (size_t)fixed + (size_t)ks * tile;
   // a few rows go 16 columns at a time (the others may not be there at all), many 32
   const auto kernel = n <= 16 ? k_paged_mass<T, D, 16> : k_paged_mass<T, D, 32>;
-  cudaError_t err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done[2] = {};
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), most_smem, done[n <= 16]);
   if (err != cudaSuccess) return err;
   const int nsm = sm_count();
   const int64_t tiles = (((int64_t)a.table_ld << a.lps) + kTile - 1) / kTile;

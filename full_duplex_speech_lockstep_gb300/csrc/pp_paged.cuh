@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "pp_async.cuh"
 #include "pp_internal.cuh"
 
@@ -432,6 +434,22 @@ inline int sm_count() {
 }
 
 // ---- launches ------------------------------------------------------------------------------
+// A kernel's limit on dynamic shared memory belongs to the process and the device, and calls from
+// several threads share it: it is set once to the most that any call asks for, never to one call's
+// own size, which another call might lower between this one's setting and its launch.  `done` (one
+// for each kernel) has a bit for each device.
+inline cudaError_t allow_smem(const void* kern, int most, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;   // from 64 on it is set at every call
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t set =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (set == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return set;
+}
+
 // Programmatic dependent launch: every kernel of this family waits for its predecessor
 // (griddepcontrol.wait) before it reads anything, so it may be scheduled early.
 template <typename... KArgs, typename... Args_>

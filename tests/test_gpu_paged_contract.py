@@ -1,7 +1,9 @@
 """What the paged-cache calls promise beside their formulas: lengths past the table, a sequence's
 bits, rows that are to give nothing, calls from several host threads (GPU).  Tolerances are those
 of test_gpu_paged.py."""
+import ctypes
 import math
+import threading
 
 import pytest
 
@@ -259,4 +261,64 @@ def test_the_entries_of_padding_rows_stay_empty(G, max_q):
     got = torch.zeros_like(b.mass)
     kv.attention_mass(b.q, lse, b.cu, b.len, max_q=max_q, mass=got)
     assert torch.equal(got, want)
+
+
+# ---- several host threads --------------------------------------------------------------------------
+
+def test_host_threads_do_not_disturb_each_other():
+    """Two threads, each with its own stream and caches; the shared memory that their launches ask
+    for differs with the number of sequences, the rows of a step and the width of the table."""
+    pp = pp_()
+    L, rounds = pp.lib(), 3000
+
+    def calls(n, entries, heads, max_q):
+        k = torch.randn((n + 1, 1, 64, 128), device="cuda").to(BF16)
+        width = entries // 64
+        table = torch.zeros((n, width), dtype=torch.int32, device="cuda")
+        table[:, 0] = torch.arange(n, device="cuda")
+        kv = pp.PagedKV(k, k.clone(), table, mass=torch.zeros((n + 1, 1, 64), device="cuda"))
+        to = pp.PagedKV(k.clone(), k.clone(), table, mass=torch.zeros((n + 1, 1, 64), device="cuda"))
+        cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+        length = torch.full((n,), 9, dtype=torch.int32, device="cuda")
+        q = torch.randn((n, heads, 128), device="cuda").to(BF16)
+        out, lse = torch.empty_like(q), torch.zeros((n, heads), device="cuda")
+        size = pp.pp_paged_attention_scratch_bytes(kv.c, heads, n, max_q, 0)
+        scratch = torch.empty(size, dtype=torch.uint8, device="cuda")
+        to_len = torch.empty(n, dtype=torch.int32, device="cuda")
+        kept = torch.empty((n, 1, 8), dtype=torch.int32, device="cuda")
+        stream = torch.cuda.Stream()
+        ref, tref, s = ctypes.byref(kv.c), ctypes.byref(to.c), stream.cuda_stream
+        keep = (kv, to, cu, length, q, out, lse, scratch, to_len, kept, stream)
+
+        def go():
+            st = kv.status.data_ptr()
+            return (L.pp_paged_attention(ref, q.data_ptr(), heads * 128, cu.data_ptr(),
+                                         length.data_ptr(), n, max_q, heads, 0.1, 0, out.data_ptr(),
+                                         lse.data_ptr(), st, scratch.data_ptr(), size, s),
+                    L.pp_paged_mass(ref, q.data_ptr(), heads * 128, lse.data_ptr(), cu.data_ptr(),
+                                    length.data_ptr(), n, max_q, heads, 0.1, 0, 0.5, st, s),
+                    L.pp_paged_evict(ref, length.data_ptr(), 8, 2, tref, to_len.data_ptr(),
+                                     kept.data_ptr(), st, s))
+        return go, keep
+
+    # (the tables' unused entries are never looked at: nine entries to a sequence)
+    sides = [calls(1, 64, 1, 1), calls(48, 1 << 19, 2, 1)]
+    torch.cuda.synchronize()
+    wrong = [[], []]
+
+    def work(i):
+        torch.cuda.set_device(0)
+        for _ in range(rounds):
+            rc = sides[i][0]()
+            if any(rc):
+                wrong[i].append(rc)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong[0] and not wrong[1], (len(wrong[0]), wrong[0][:3], len(wrong[1]), wrong[1][:3])
+    for _, keep in sides:
+        assert keep[0].read_status() == 0
 
