@@ -8,6 +8,7 @@
 #include <new>
 #include <vector>
 
+#include "pp_found.cuh"
 #include "pp_internal.cuh"
 #include "pp_sample.cuh"
 
@@ -18,15 +19,15 @@ bool g_use_pdl = false;
 int g_launch_priority = 0;
 
 EncodeTiledFn encode_fn() {
-  static const EncodeTiledFn fn = [] {
+  static Found<EncodeTiledFn> fn;
+  return fn.get([] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     const cudaError_t err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
                                                              cudaEnableDefault, &q);
     const bool ok = err == cudaSuccess && q == cudaDriverEntryPointSuccess;
     return ok ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
-  }();
-  return fn;
+  });
 }
 }
 
