@@ -65,25 +65,28 @@ bool scores_ok(float scale, int window, int max_q) {
 }
 
 // Pages as [page][head][row][dim], box 64 dims x one page or one key tile, and queries as
-// [token][head][dim], box 64 dims x the G heads of a key head x the tokens of a row tile.
-bool encode(CUtensorMap* m, int type, const void* base, const cuuint64_t dim[4],
-            const cuuint64_t stride[3], const cuuint32_t box[4]) {
+// [token][head][dim], box 64 dims x the G heads of a key head x the tokens of a row tile.  PP_E_CUDA
+// where there is no driver to encode them.
+int encode(CUtensorMap* m, int type, const void* base, const cuuint64_t dim[4],
+           const cuuint64_t stride[3], const cuuint32_t box[4]) {
   const EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
+  if (!fn) return PP_E_CUDA;
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn(m, type == PP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-            4, const_cast<void*>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const CUresult r = fn(
+      m, type == PP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+      const_cast<void*>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PP_OK : PP_EINVAL;
 }
-bool page_map(CUtensorMap* m, const pp_paged_kv* kv, const void* base) {
+int page_map(CUtensorMap* m, const pp_paged_kv* kv, const void* base) {
   const cuuint64_t D = kv->head_dim, P = kv->page_size;
   const cuuint64_t dim[4] = {D, P, (cuuint64_t)kv->n_kv_heads, (cuuint64_t)kv->n_pages};
   const cuuint64_t stride[3] = {D * 2, P * D * 2, (cuuint64_t)kv->page_stride * 2};
   const cuuint32_t box[4] = {64, (cuuint32_t)(P < kTile ? P : kTile), 1, 1};
   return encode(m, kv->type, base, dim, stride, box);
 }
-bool query_map(CUtensorMap* m, const Args& a, int type, const void* q, int64_t stride_q, int tp) {
+int query_map(CUtensorMap* m, const Args& a, int type, const void* q, int64_t stride_q, int tp) {
   const cuuint64_t D = a.D, H = (cuuint64_t)a.Hk * a.G;
   const cuuint64_t dim[4] = {D, H, (cuuint64_t)a.T, 1};
   const cuuint64_t stride[3] = {D * 2, (cuuint64_t)stride_q * 2, (cuuint64_t)stride_q * 2};
@@ -189,16 +192,17 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
   o.lse = lse;
   o.part = reinterpret_cast<float*>(scratch);
   Maps maps;
-  if (!page_map(&maps.k, kv, kv->k) || !page_map(&maps.v, kv, kv->v)) return PP_EINVAL;
+  int bad = page_map(&maps.k, kv, kv->k);
+  if (bad || (bad = page_map(&maps.v, kv, kv->v))) return bad;
   if (is_long(a, max_q)) {
     const LongPlan p = long_plan(a, T);
-    if (!query_map(&maps.q, a, kv->type, q, q_stride, p.tp)) return PP_EINVAL;
+    if ((bad = query_map(&maps.q, a, kv->type, q, q_stride, p.tp))) return bad;
     o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) + p.rec_bytes);
     o.plan = reinterpret_cast<int*>(reinterpret_cast<char*>(scratch) + p.rec_bytes + p.ml_bytes);
     return rc(launch_paged_attn_tc(a, kv->type, p, maps, o, kv->v, (cudaStream_t)stream));
   }
   const AttnPlan p = attn_plan(a, max_q);
-  if (!query_map(&maps.q, a, kv->type, q, q_stride, p.tp)) return PP_EINVAL;
+  if ((bad = query_map(&maps.q, a, kv->type, q, q_stride, p.tp))) return bad;
   o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) + p.rec_bytes);
   return rc(launch_paged_attn(a, kv->type, p, maps, o, kv->v, (cudaStream_t)stream));
 }
@@ -225,9 +229,9 @@ int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const 
   // without a row the query map is never used: any valid one will do
   Args qa = a;
   if (T == 0) qa.T = 1;
-  if (!page_map(&maps.k, kv, kv->k) ||
-      !query_map(&maps.q, qa, kv->type, T ? q : kv->k, T ? q_stride : n_heads * D, tp))
-    return PP_EINVAL;
+  int bad = page_map(&maps.k, kv, kv->k);
+  if (bad || (bad = query_map(&maps.q, qa, kv->type, T ? q : kv->k, T ? q_stride : n_heads * D, tp)))
+    return bad;
   return rc(launch_paged_mass(a, kv->type, maps, lse, kv->mass, decay, tp, (cudaStream_t)stream));
 }
 
