@@ -392,11 +392,13 @@ __device__ __forceinline__ void join_row(const float* part, const float2* part_m
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
   const float ref = top == -INFINITY ? 0.f : top;
+  // (a split without a reference has no keys that this row sees: -1, nothing to add; or scores of NaN
+  // alone, which its sum tells)
   float f[4], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[i] = exp2_approx(ml[i].x - ref);
-    sum += f[i] * ml[i].y;
+    f[i] = ml[i].x == -INFINITY ? -1.f : exp2_approx(ml[i].x - ref);
+    sum += ml[i].x == -INFINITY ? ml[i].y : f[i] * ml[i].y;
   }
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
@@ -409,7 +411,7 @@ __device__ __forceinline__ void join_row(const float* part, const float2* part_m
     for (int k = 0; k < cnt; ++k) {
       const float w = __shfl_sync(0xffffffffu, f[i], k);
       const float* src = part + (rec + i * 32 + k) * D + lane * DL;
-      if (w == 0.f) continue;          // a split without keys that this row sees
+      if (w < 0.f) continue;           // (a weight of 0 counts: 0 times a NaN is one)
 #pragma unroll
       for (int e = 0; e < DL; e += 2) {
         const float2 y = __ldcg(reinterpret_cast<const float2*>(src + e));

@@ -142,6 +142,31 @@ def other(b, budget):
     return pp_().PagedKV(K, K.clone(), table, mass=torch.zeros(K.shape[:3], device="cuda"))
 
 
+# ---- values that are not finite -----------------------------------------------------------------
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("n,max_q", [(1, 1), (3, 3), (40, 40), (200, 200)])
+@pytest.mark.parametrize("entry", [5, 2000])
+def test_a_value_that_a_row_sees_is_not_lost_by_its_small_weight(entry, n, max_q, bad):
+    """A key whose score lies 2^-1000 below the others', in another split of the keys than theirs or
+    in the same one: its weight is 0 in fp32, its value all the same not finite."""
+    b = Batch(BF16, 128, 2, 1, 64, [n], [3000])
+    b.k.mul_(0.01)
+    b.q.fill_(1.0)
+    p, r = b.where(0)
+    near = slice(max(0, entry - 600), entry + 600)     # its split: as unlikely all of it
+    b.k[p[near], :, r[near]] = -64.0                   # a score of -64 sqrt(128)
+    want, _ = b.kv().attention(b.q, b.cu, b.len, max_q=max_q, with_lse=True)
+    assert torch.isfinite(want).all()
+    v = b.v.clone()
+    v[p[entry], :, r[entry], 3] = bad
+    got, _ = pp_().PagedKV(b.k, v, b.table).attention(b.q, b.cu, b.len, max_q=max_q, with_lse=True)
+    assert not torch.isfinite(got[..., 3]).any()
+    ok = torch.ones_like(got, dtype=torch.bool)
+    ok[..., 3] = False
+    assert torch.equal(got[ok], want[ok])
+
+
 # ---- a sequence's bits ---------------------------------------------------------------------------
 
 def alone(b, s, max_q, window=0):
