@@ -16,7 +16,9 @@
 // bound by the way from S to the sums: 2500 clocks a step of two tiles, whose products take
 // 1024 and whose exponentials as many.  (16 warps of sums instead of 8: the same.)
 //
-// A CTA takes a run of consecutive units of about the same number of steps as the others:
+// A CTA takes a run of consecutive units of about the same number of steps as the others (pairs of
+// tiles that no row sees, below a window, only decay and count as little; without a decay they are no
+// units: 4096 tokens under a window of 1000 over 65000 entries, 32 heads on 8: 613 -> 62 us):
 //   warp 0        producer: the units and their key tiles, by TMA
 //   warp 1        one thread issues the MMAs, up to four steps ahead of the sums
 //   warp 2        each key's old mass and page, a unit ahead
@@ -51,56 +53,72 @@ struct Ctl {
   int page[kAux][16];                // pages of its 16-key groups, -1 for none
 };
 
-// Steps of rows of a unit, at most: what it costs.
-__device__ __forceinline__ int unit_cost(const Seq& s, int tp) {
-  return max(1, (s.n + tp - 1) / tp);
-}
+// A head's units: pairs [from, seen) of tiles of which no row sees a key, which only decay and cost 1
+// (none without a decay), and pairs [seen, pairs), which cost the steps of all rows.
+struct Head {
+  int from, seen, pairs, steps;
+  __device__ __forceinline__ Head() {}
+  __device__ __forceinline__ Head(const Args& a, const Seq& s, int tp, bool decays) {
+    const int first = s.total - s.n;                 // the first row's entry
+    const int low = s.n == 0 ? s.len : a.window ? min(max(first - a.window + 1, 0), s.len) : 0;
+    pairs = (s.len + 2 * kTile - 1) / (2 * kTile);
+    seen = low < s.len ? low / (2 * kTile) : pairs;
+    from = decays ? 0 : seen;
+    steps = (s.n + tp - 1) / tp;
+  }
+  __device__ __forceinline__ int64_t cost() const {
+    return seen - from + (int64_t)(pairs - seen) * steps;
+  }
+};
 
 // A walk over this CTA's units, in order.
 struct Walk {
   const Args& a;
   const int64_t* pre;
   const int tp;
+  const bool decays;
   int64_t at, end;      // cost before this unit, cost where the run ends
   int b, h, pair;
-  int pairs, cost;      // of the sequence
+  Head head;            // of the sequence
   Seq s;
   int j0, t0, t1;       // the unit's first key; the tokens that see some key of it
 
-  __device__ __forceinline__ Walk(const Args& a_, const int64_t* pre_, int tp_)
-      : a(a_), pre(pre_), tp(tp_) {
+  __device__ __forceinline__ Walk(const Args& a_, const int64_t* pre_, int tp_, bool decays_)
+      : a(a_), pre(pre_), tp(tp_), decays(decays_) {
     const int64_t total = pre[a.n_seqs];
     at = total * blockIdx.x / gridDim.x;
     end = total * (blockIdx.x + 1) / gridDim.x;
     if (at >= end) return;
     b = find_seq(pre, a.n_seqs, at);
     sequence();
-    const int64_t i = (at - pre[b] + cost - 1) / cost;   // the first unit that starts in the run
-    h = (int)(i / pairs);
-    pair = (int)(i - (int64_t)h * pairs);
-    at = pre[b] + i * cost;
-    if (h == a.Hk) next_sequence();
+    // the first unit that starts in the run
+    const int64_t cost = head.cost(), dim = head.seen - head.from;
+    h = (int)((at - pre[b]) / cost);
+    const int64_t in = at - pre[b] - h * cost;
+    const int64_t i = in <= dim ? in : dim + (in - dim + head.steps - 1) / head.steps;
+    pair = head.from + (int)i;
+    at = pre[b] + h * cost + (i <= dim ? i : dim + (i - dim) * head.steps);
+    if (pair == head.pairs) next_head();
     unit();
   }
   __device__ __forceinline__ bool done() const { return at >= end; }
   __device__ __forceinline__ void sequence() {
     s = seq_of(a, b);
-    pairs = (s.len + 2 * kTile - 1) / (2 * kTile);
-    cost = unit_cost(s, tp);
+    head = Head(a, s, tp, decays);
   }
-  __device__ __forceinline__ void next_sequence() {
-    h = pair = 0;
-    do {
-      ++b;
-    } while (b < a.n_seqs && pre[b + 1] == pre[b]);
-    if (b < a.n_seqs) sequence();
+  __device__ __forceinline__ void next_head() {
+    if (++h == a.Hk) {
+      h = 0;
+      do {
+        ++b;
+      } while (b < a.n_seqs && pre[b + 1] == pre[b]);
+      if (b < a.n_seqs) sequence();
+    }
+    pair = head.from;
   }
   __device__ __forceinline__ void next() {
-    at += cost;
-    if (++pair == pairs) {
-      pair = 0;
-      if (++h == a.Hk) next_sequence();
-    }
+    at += pair < head.seen ? 1 : head.steps;
+    if (++pair == head.pairs) next_head();
     unit();
   }
   __device__ __forceinline__ void unit() {
@@ -261,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Seq s = seq_of(a, b);
     if (s.n == 0 && decay == 1.f) return 0;
     check_len(a, s);
-    return (int64_t)a.Hk * ((s.len + 2 * kTile - 1) / (2 * kTile)) * unit_cost(s, tp);
+    return a.Hk * Head(a, s, tp, decay != 1.f).cost();
   });
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = ctl->tmem;
@@ -269,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---- producer -------------------------------------------------------------------------
     uint32_t nk = 0, nu = 0, seen_bad = 0;
-    Walk x(a, pre, tp);
+    Walk x(a, pre, tp, decay != 1.f);
     TilePages next[2];
     auto find = [&] {
       if (x.done()) return;
@@ -286,8 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const TilePages now[2] = {next[0], next[1]};
       x.next();
       find();
-      // a unit that no row sees has nothing to add; without decay it is left out
-      if (u.nt == 0 && decay == 1.f) continue;
       put_unit(a, ctl->ring, nu++, u, lane, abort_flag);
       if (u.nt == 0) continue;
 #pragma unroll

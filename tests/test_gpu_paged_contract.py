@@ -288,6 +288,48 @@ def test_the_entries_of_padding_rows_stay_empty(G, max_q):
     assert torch.equal(got, want)
 
 
+# ---- weights under a window ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("decay", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("G,chunks,lens,window", [
+    (1, [1, 1, 0], [9000, 100, 600], 300), (4, [70, 5], [20000, 700], 500),
+    (2, [600, 0, 200], [5000, 300, 200], 257), (8, [33], [3000], 1)])
+def test_weights_under_a_window_over_a_long_cache(G, chunks, lens, window, decay):
+    """Most entries are seen by no row: they decay and nothing else."""
+    b = Batch(BF16, 64, 3, G, 64, chunks, lens, window=window)
+    kv = b.kv()
+    _, lse = kv.attention(b.q, b.cu, b.len, max_q=max(chunks), window=window, with_lse=True)
+    before = b.mass.clone()
+    kv.attention_mass(b.q, lse, b.cu, b.len, max_q=max(chunks), window=window, decay=decay)
+    for s, n in enumerate(lens):
+        check_mass(b, s, before, b.mass, lse, decay)
+        old = max(0, n - chunks[s] - window + 1) if chunks[s] else n
+        p, r = (t[:old] for t in b.where(s))
+        assert torch.equal(b.mass[p, :, r], before[p, :, r] * decay)
+
+
+def test_the_weights_cost_what_the_window_sees():
+    """The same rows and window over a short cache and over a long one: without a decay the older
+    entries are no work, and the rest spreads over the SMs alike (a ratio of 10 when the units that
+    no row sees counted as much as the others)."""
+    times = []
+    for n in (5120, 65000):
+        b = Batch(BF16, 128, 8, 4, 64, [4096], [n], window=1000)
+        kv = b.kv()
+        lse = torch.full((4096, 32), 8.0, device="cuda")
+        best = math.inf
+        for _ in range(5):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            for _ in range(20):
+                kv.attention_mass(b.q, lse, b.cu, b.len, max_q=4096, window=1000)
+            end.record()
+            torch.cuda.synchronize()
+            best = min(best, start.elapsed_time(end))
+        times.append(best)
+    assert times[1] < 3 * times[0], times
+
+
 # ---- several host threads --------------------------------------------------------------------------
 
 def test_host_threads_do_not_disturb_each_other():
