@@ -1,6 +1,7 @@
-"""What the paged-cache calls promise beside their formulas: lengths past the table, a sequence's
-bits, rows that are to give nothing, calls from several host threads (GPU).  Tolerances are those
-of test_gpu_paged.py."""
+"""What the paged-cache calls promise beside their formulas: lengths past the table, values that are
+not finite, a sequence's bits, rows that are to give nothing, weights under a window, calls from
+several host threads, and sizes past the tests of the formulas (GPU).  Tolerances are those of
+test_gpu_paged.py."""
 import ctypes
 import math
 import threading
@@ -11,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_paged import BF16, F16, Batch, check_mass, pp_, turned  # noqa: E402
+from test_gpu_paged import BF16, F16, Batch, check_mass, pp_, run_evict, turned  # noqa: E402
 
 
 # ---- lengths past the table ---------------------------------------------------------------------
@@ -389,3 +390,36 @@ def test_host_threads_do_not_disturb_each_other():
     for _, keep in sides:
         assert keep[0].read_status() == 0
 
+
+# ---- sizes that no other test reaches -----------------------------------------------------------------
+
+@pytest.mark.parametrize("lens,budget,recent", [([400000], 150000, 1000), ([400000, 5], 3, 0)])
+def test_evict_of_rows_too_long_for_shared_memory(lens, budget, recent):
+    """More than 8 x 45056 entries to a key head: each round reads the weights again."""
+    b = Batch(BF16, 64, 1, 1, 256, [0] * len(lens), lens)
+    b.mass.mul_(500).round_()                    # ties, at the threshold too
+    run_evict(b, budget, recent, 256)
+
+
+def test_long_chunks_of_very_different_lengths():
+    """More units than SMs: one of 20000 entries beside chunks of 33 to 64 tokens."""
+    chunks = [33 + (i * 7) % 32 for i in range(100)]
+    lens = [c + (i * 13) % 50 for i, c in enumerate(chunks)]
+    lens[40] = 20000
+    lens[99] = 9000
+    b = Batch(BF16, 64, 4, 1, 64, chunks, lens)
+    out, lse = b.kv().attention(b.q, b.cu, b.len, max_q=64, with_lse=True)
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("type,D,chunks,lens", [(BF16, 128, [1], [60000]), (F16, 64, [1, 2], [30000, 900]),
+                                                (BF16, 128, [3, 1], [500, 20000])])
+def test_many_query_heads_over_a_long_cache(type, D, chunks, lens):
+    b = Batch(type, D, 1, 64, 64, chunks, lens)
+    kv = b.kv()
+    out, lse = kv.attention(b.q, b.cu, b.len, max_q=max(chunks), with_lse=True)
+    b.check(out, lse)
+    before = b.mass.clone()
+    kv.attention_mass(b.q, lse, b.cu, b.len, max_q=max(chunks))
+    for s in range(len(lens)):
+        check_mass(b, s, before, b.mass, lse, 1.0)
