@@ -35,7 +35,7 @@
 // the key.
 //
 // Measured (128 dims, in a graph): 64 sequences of 1 token and up to 3000 entries, 32 heads on 32
-// key heads, pages of 64, bf16: 273 us, 5.6 TB/s (0.83 of the measured copy rate; 1.01 with equal
+// key heads, pages of 64, bf16: 269 us, 5.7 TB/s (0.84 of the measured copy rate; 1.01 with equal
 // lengths: what is left are the ends of the many short units, about 4500 clocks each).  8
 // sequences of up to 5 tokens and 65000 entries, 32 heads on 8, pages of 16, fp16: 212 us, 4.4
 // TB/s, bound by the products of up to 20 rows with mma.sync.  One token over 3000 entries, 32
@@ -618,7 +618,7 @@ AttnPlan attn_plan(const Args& a, int max_q) {
   p.wr = rows <= 16 ? 1 : 2;
   p.tp = 16 * p.wr / a.G;
   if (max_q < p.tp) p.tp = max_q;
-  p.share = 152 / a.Hk < 1 ? 1 : 152 / a.Hk;
+  p.share = kSms / a.Hk < 1 ? 1 : kSms / a.Hk;
   const int64_t entries = (int64_t)a.table_ld << a.lps;
   int64_t tiles = (entries + kTile - 1) / kTile;
   if (a.window) {

@@ -56,8 +56,9 @@ __device__ __forceinline__ void store8(T* p, const float x[8]) {
 // lookups (row offsets, length, page) they hide.
 // Measured (in a graph): 4 sequences of up to 6000 tokens, 6021 in all, 32 + 2 x 8 heads of 128
 // dims, bf16: 43 us, 3.5 TB/s (39 without the norm, 50 with halves); fp32 in: 53 us, 4.2 TB/s; 64
-// tokens of 32 + 2 x 32 heads, fp32 in: 6 us.  Bound by what four CTAs on an SM keep in flight: 64
-// registers a thread (at 114, two CTAs, 65 us; at 48, five, they spill).  Halves through shared
+// tokens of 32 + 2 x 32 heads, fp32 in: 6 us.  Bound by a CTA's chain (loads, lookups, angles, norm,
+// stores), of which four to an SM overlap: 64 registers a thread (at 114, two CTAs, 65 us; at 48,
+// five, they spill).  Halves through shared
 // memory took 75 us.  (Ten tokens to a CTA with the next one's loads ahead: no faster, and slower
 // for few tokens.)
 template <typename I, typename T, int D>
@@ -453,7 +454,7 @@ cudaError_t launch_paged_evict(const Args& a, const EvictArgs& x, cudaStream_t s
   const int64_t entries = (int64_t)a.table_ld << a.lps;
   // CTAs to a pair: enough for two on every SM, while a slice keeps two entries to a thread
   int cluster = 1;
-  while (cluster < 8 && pairs * cluster * 2 <= 2 * 152 &&
+  while (cluster < 8 && pairs * cluster * 2 <= 2 * kSms &&
          entries >= (int64_t)cluster * 2 * 2 * kSelThreads)
     cluster *= 2;
   const int64_t slice = (entries + cluster - 1) / cluster;

@@ -11,10 +11,10 @@
 // from L2 bounded the kernel: 114 us for the 4 x 300 tokens below.)
 //
 // Measured (bf16, 128 dims, in a graph): 64 sequences of 1 token and up to 3000 entries, 32 heads on
-// 32 key heads: 164 us, 4.8 TB/s, bound by reading K once and by the units' starts, two tiles to
-// a unit.  4 sequences of up to 300 tokens and 16000 entries, 32 heads on 8: 94 us, 815 TFLOP/s,
-// bound by the way from S to the sums: 2500 clocks a step of two tiles, whose products take
-// 1024 and whose exponentials as many.  (16 warps of sums instead of 8: the same.)
+// 32 key heads: 158 us, 5.0 TB/s, bound by reading K once and by the units' starts, two tiles to
+// a unit.  4 sequences of up to 300 tokens and 16000 entries, 32 heads on 8: 95 us, 805 TFLOP/s,
+// 2500 clocks a step of two tiles, whose products take 1024 and whose exponentials as many; what
+// takes the rest is not known (16 warps of sums instead of 8: the same).
 //
 // A CTA takes a run of consecutive units of about the same number of steps as the others (pairs of
 // tiles that no row sees, below a window, only decay and count as little; without a decay they are no

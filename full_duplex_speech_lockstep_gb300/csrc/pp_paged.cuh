@@ -14,6 +14,8 @@ namespace pp {
 namespace paged {
 
 constexpr int kTile = 128;       // cache entries of one key tile
+constexpr int kSms = 152;        // that a split is made for: a number of the GPU, not asked of the device,
+                                 // so that neither bits nor scratch sizes depend on which one is current
 constexpr int kMaxSeqs = 2048;   // sequences of one call (their prefix sums sit in shared memory)
 constexpr int kMaxGroup = 64;    // query heads to a key head
 constexpr int kMaxLen = 1 << 30; // larger kv_len count as this: four times the longest table row, and
@@ -300,7 +302,10 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t r[4]) {
 
 // The two 16-bit types: their product, their packed rounding, their non-finite values, and
 // the power of two that softmax weights carry so that small ones stay normal numbers
-// (fp16 has no exponents below 2^-14; bf16 has fp32's).
+// (fp16 has no exponents below 2^-14; bf16 has fp32's).  The weights are rounded before the second
+// product, by at most 2^-8 (bf16) or 2^-11 (fp16) of each, which its operands' common type asks for;
+// what that adds to the output's error (0.0015 in bf16) is less than the output's own rounding
+// (0.0017).  Weights as hi + lo would double that product.
 template <typename T>
 struct Num;
 template <>

@@ -536,8 +536,8 @@ int pp_rvq_dequantize(const int32_t* codes, int code_stride, int n_frames, int n
  * A sequence's results depend, bit for bit, on its own rows, entries and lengths and on the
  * call's head counts and max_q, not on the rest of the batch.  One exception: where a chunk of
  * max_q tokens has more than 32 rows to a key head (max_q * n_heads / n_kv_heads > 32), the
- * number of new rows of the other sequences (never what they hold) may set how the attention
- * splits a sequence's keys. */
+ * number of new rows of the other sequences (never what they hold), T, n_seqs and table_ld may
+ * set how the attention splits a sequence's keys. */
 #define PP_F32 0
 #define PP_BF16 1
 #define PP_F16 2
@@ -590,7 +590,8 @@ int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, cons
  * over the entries j that the row sees, of key head h / (n_heads / n_kv_heads).  A row that
  * sees none gives zeros and an lse of -infinity.  What a row does not see never reaches it,
  * whatever is stored there (NaN and infinities included).  Scores, sums and outputs are
- * accumulated in fp32; softmax weights enter the second product in the cache's type.
+ * accumulated in fp32; softmax weights enter the second product in the cache's type (rounded once:
+ * 8 significant bits in bf16, 11 in fp16, where the ring attention of the tick carries about 16).
  *   q        [T] rows of [n_heads][head_dim] in the cache's type, q_stride elements apart
  *            (a multiple of 8), 16-byte aligned
  *   max_q    the largest number of new rows of any sequence, as far as the host knows; sets
@@ -614,8 +615,8 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
  * for every entry j < kv_len, seen or not.  decay in [0, 1]: 1 accumulates, 0 starts afresh
  * (old contents are then not read).  q, lse, scale and window as in (and from)
  * pp_paged_attention; a caller may pass fewer rows than it attended with, the last ones of
- * each sequence.  Rows with an lse of -infinity give nothing.  The sum over rows runs in a
- * fixed order.  Errors: PP_EINVAL, PP_E_CUDA. */
+ * each sequence.  Rows with an lse of -infinity give nothing, whatever they hold.  The sum over
+ * rows runs in a fixed order.  Errors: PP_EINVAL, PP_E_CUDA. */
 int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const float* lse,
                   const int32_t* cu, const int32_t* kv_len, int T, int max_q, int n_heads,
                   float scale, int window, float decay, uint32_t* status, void* stream);
