@@ -715,7 +715,7 @@ class PagedKV:
         """Attention of the new rows over the cache: out, or (out, lse) on request.  max_q is
         the longest chunk as far as the host knows.  It picks the kernel: give it where chunks are
         short.  Without it all rows count as one chunk, so the kernel, and with it a sequence's
-        bits, goes by the batch's row count."""
+        bits, goes by the batch's row count.  out must not lie over q."""
         torch = self.torch
         T, H, qs = self._rows("q", q, self.dtype)
         self._batch(cu, kv_len)

@@ -94,6 +94,13 @@ int query_map(CUtensorMap* m, const Args& a, int type, const void* q, int64_t st
   return encode(m, type, q, dim, stride, box);
 }
 
+// Do T rows of `len` bytes, `stride` >= len bytes apart, meet the `n` bytes from `at`?
+bool rows_meet(const void* rows, int64_t stride, int64_t len, int T, const void* at, int64_t n) {
+  const int64_t d = reinterpret_cast<intptr_t>(at) - reinterpret_cast<intptr_t>(rows);
+  const int64_t t = d < len ? 0 : (d - len) / stride + 1;   // the first row that ends past `at`
+  return t < T && t * stride < d + n;
+}
+
 bool is_long(const Args& a, int max_q) { return (int64_t)max_q * a.G > kShortRows; }
 
 int rc(cudaError_t err) { return err == cudaSuccess ? PP_OK : PP_E_CUDA; }
@@ -181,6 +188,8 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
     return PP_EINVAL;
   if (scratch_bytes < pp_paged_attention_scratch_bytes(kv, n_heads, T, max_q, window))
     return PP_E_NOSPACE;
+  // a CTA's queries are read while others' outputs are written
+  if (rows_meet(q, q_stride * 2, n_heads * D * 2, T, out, T * n_heads * D * 2)) return PP_EINVAL;
   Args a = base_args(kv, kv_len, status);
   a.cu = cu;
   a.T = T;

@@ -9,8 +9,9 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CHILD = """
 import test_paged_abi as t
 import full_duplex_speech_lockstep_gb300 as pp
-for f in (t.append, t.attention, t.mass, lambda kv: t.evict(kv, t.cache(k=2 * t.A, v=2 * t.A)),
-          lambda kv: t.attention(kv, max_q=300)):
+for f in (t.append, lambda kv: t.attention(kv, out=2 * t.A), t.mass,
+          lambda kv: t.evict(kv, t.cache(k=2 * t.A, v=2 * t.A)),
+          lambda kv: t.attention(kv, out=2 * t.A, max_q=300)):
     print(f(t.cache()))
 """
 
