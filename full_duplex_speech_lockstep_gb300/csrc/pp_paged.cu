@@ -257,6 +257,8 @@ int pp_paged_evict(const pp_paged_kv* kv, const int32_t* kv_len, int budget, int
   const int64_t entries = (int64_t)kv->table_ld * kv->page_size;
   const int64_t most = entries < budget ? entries : budget;
   if ((int64_t)to->table_ld * to->page_size < most) return PP_E_RANGE;
+  // its own pages: entries would be written over before they are read
+  if (to->k == kv->k && to->table == kv->table) return PP_EINVAL;
   Args a = base_args(kv, kv_len, status);
   EvictArgs x{};
   x.k = kv->k;

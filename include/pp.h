@@ -631,8 +631,10 @@ int pp_paged_mass(const pp_paged_kv* kv, const void* q, int64_t q_stride, const 
  *   kept    int32 [n_seqs][n_kv_heads][budget]: the entries that stayed, ascending, then -1
  * kv->mass is required, to->mass is written if given.  0 <= recent <= budget,
  * 1 <= budget <= 2^28.
- * Errors: PP_EINVAL (`to` of other sequences, heads, head dim or type), PP_E_RANGE (to's table
- * is too narrow for the budget), PP_E_CUDA. */
+ * An entry of a page outside the pool counts as the lowest; where it stays all the same its place
+ * in `to` is left as it was.
+ * Errors: PP_EINVAL (`to` of other sequences, heads, head dim or type, or the cache itself),
+ * PP_E_RANGE (to's table is too narrow for the budget), PP_E_CUDA. */
 int pp_paged_evict(const pp_paged_kv* kv, const int32_t* kv_len, int budget, int recent,
                    const pp_paged_kv* to, int32_t* to_len, int32_t* kept, uint32_t* status,
                    void* stream);

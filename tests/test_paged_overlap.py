@@ -32,3 +32,9 @@ def call(what):
     ("A + 11264", 8192, False), ("A + 11280", 8192, True), ("A + 4 * 16384 + 1024", 8192, False)])
 def test_attention_refuses_an_output_over_its_queries(at, stride, meets):
     assert call("t.attention(t.cache(), qs=%d, out=%s)" % (stride, at)) == (-1 if meets else -5)
+
+
+def test_evict_refuses_the_cache_itself():
+    assert call("t.evict(t.cache(), t.cache())") == -1
+    assert call("t.evict(t.cache(), t.cache(table=2 * A))") == -5
+    assert call("t.evict(t.cache(), t.cache(k=2 * A, v=2 * A))") == -5
