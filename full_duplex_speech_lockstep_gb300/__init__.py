@@ -43,7 +43,7 @@ EXPORTS = ["pp_weight_shape", "pp_workspace_bytes", "pp_create", "pp_destroy",
            "pp_driver_prepare", "pp_driver_absorb", "pp_driver_tick", "pp_session_sampling",
            "pp_sample", "pp_test_faults", "pp_paged_append",
            "pp_paged_attention_scratch_bytes", "pp_paged_attention", "pp_paged_mass",
-           "pp_paged_evict"]
+           "pp_paged_evict", "pp_test_paged_faults"]
 
 # enum pp_kernel_kind
 KERNEL_KINDS = ["begin", "norm", "qkv", "rope_ring", "attn", "oproj", "gateup", "down",
@@ -183,6 +183,8 @@ def lib():
         L.pp_paged_mass.restype = I
         L.pp_paged_evict.argtypes = [KV, P, I, I, KV, P, P, P, P]
         L.pp_paged_evict.restype = I
+        L.pp_test_paged_faults.argtypes = [ctypes.c_int32, ctypes.c_int32]
+        L.pp_test_paged_faults.restype = I
         _lib = L
     return _lib
 
@@ -464,6 +466,11 @@ def pp_paged_mass(kv, q, q_stride, lse, cu, kv_len, T, max_q, n_heads, scale, wi
     return _check("pp_paged_mass", lib().pp_paged_mass(
         ctypes.byref(kv), q, q_stride, lse, cu, kv_len, T, max_q, n_heads, scale, window, decay,
         status, stream))
+
+
+def pp_test_paged_faults(wait_polls, withhold):
+    """Failure-detection tests of the paged calls of this thread; reset with (0, 0)."""
+    return _check("pp_test_paged_faults", lib().pp_test_paged_faults(wait_polls, withhold))
 
 
 def pp_paged_evict(kv, kv_len, budget, recent, to, to_len, kept, status, stream):

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->kempty[i]), kWarps);
     }
     for (int i = 0; i < C::VS; ++i) {
-      mbar_init(smem_u32(&ctl->vfull[i]), 1);
+      mbar_init(smem_u32(&ctl->vfull[i]), i == 0 ? 1 + a.withhold : 1);
       mbar_init(smem_u32(&ctl->vempty[i]), kWarps);
     }
     for (int i = 0; i < kQBufs; ++i) {
@@ -276,10 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
 #pragma unroll 1
         for (uint32_t i = nq > kQBufs ? nq - kQBufs : 0; i < nq; ++i)
-          drain_phase(&ctl->qfull[i % kQBufs], (i / kQBufs) & 1);
+          drain_phase(a, &ctl->qfull[i % kQBufs], (i / kQBufs) & 1);
 #pragma unroll 1
         for (uint32_t i = nk > C::KS ? nk - C::KS : 0; i < nk; ++i)
-          drain_phase(&ctl->kfull[i % C::KS], (i / C::KS) & 1);
+          drain_phase(a, &ctl->kfull[i % C::KS], (i / C::KS) & 1);
       }
     } else if (threadIdx.x < 64) {
       uint32_t nv = 0;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
 #pragma unroll 1
         for (uint32_t i = nv > C::VS ? nv - C::VS : 0; i < nv; ++i)
-          drain_phase(&ctl->vfull[i % C::VS], (i / C::VS) & 1);
+          drain_phase(a, &ctl->vfull[i % C::VS], (i / C::VS) & 1);
       }
     }
     return;

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(smem_u32(&ctl->full[i]), 1);
+      mbar_init(smem_u32(&ctl->full[i]), i == 1 ? 1 + a.withhold : 1);   // (1: the first V)
       mbar_init(smem_u32(&ctl->empty[i]), 1);
     }
     mbar_init(smem_u32(&ctl->qfull), 1);
@@ -305,10 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
       // every copy lands before the CTA may exit (bounded waits)
       if (lane == 0) {
-        if (nq > 0) drain_phase(&ctl->qfull, (nq - 1) & 1);
+        if (nq > 0) drain_phase(a, &ctl->qfull, (nq - 1) & 1);
 #pragma unroll 1
         for (uint32_t i = nl > kSlots ? nl - kSlots : 0; i < nl; ++i)
-          drain_phase(&ctl->full[i % kSlots], (i / kSlots) & 1);
+          drain_phase(a, &ctl->full[i % kSlots], (i / kSlots) & 1);
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every MMA is done before tensor memory is given back (bounded wait)
         umma_commit(smem_u32(&ctl->done));
-        drain_phase(&ctl->done, 0);
+        drain_phase(a, &ctl->done, 0);
       }
       __syncwarp();
     }

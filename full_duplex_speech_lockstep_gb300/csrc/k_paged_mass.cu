@@ -11,7 +11,7 @@
 // from L2 bounded the kernel: 114 us for the 4 x 300 tokens below.)
 //
 // Measured (bf16, 128 dims, in a graph): 64 sequences of 1 token and up to 3000 entries, 32 heads on
-// 32 key heads: 158 us, 5.0 TB/s, bound by reading K once and by the units' starts, two tiles to
+// 32 key heads: 130 us, 6.0 TB/s, bound by reading K once and by the units' starts, two tiles to
 // a unit.  4 sequences of up to 300 tokens and 16000 entries, 32 heads on 8: 95 us, 805 TFLOP/s,
 // 2500 clocks a step of two tiles, whose products take 1024 and whose exponentials as many; what
 // takes the rest is not known (16 warps of sums instead of 8: the same).
@@ -232,6 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                  float* mass, const float decay, const __grid_constant__ CUtensorMap mapK,
                  const __grid_constant__ CUtensorMap mapQ) {
   constexpr int kTileBytes = kTile * D * 2;
+  // Steps of few rows pass through many units, and with every wait's loop in place the roles' code is
+  // larger than the instruction cache: there the loop is a function (137 us instead of 180 for the
+  // tick).  Steps of many rows wait more than they fetch code (106 us instead of 104.5).
+  constexpr bool kCall = W == 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (an offset, not a rounded pointer: the compiler then knows that it is shared memory)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) {
-      mbar_init(smem_u32(&ctl->kfull[i]), 1);
+      mbar_init(smem_u32(&ctl->kfull[i]), i == 0 ? 1 + a.withhold : 1);
       mbar_init(smem_u32(&ctl->kempty[i]), 1);
     }
     for (int i = 0; i < kQStages; ++i) {
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   });
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = ctl->tmem;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase<kCall>(a, bar, parity, abort_flag); };
   if (warp == 0) {
     // ---- producer -------------------------------------------------------------------------
     uint32_t nk = 0, nu = 0, seen_bad = 0;
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const TilePages now[2] = {next[0], next[1]};
       x.next();
       find();
-      put_unit(a, ctl->ring, nu++, u, lane, abort_flag);
+      put_unit<kCall>(a, ctl->ring, nu++, u, lane, abort_flag);
       if (u.nt == 0) continue;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -320,12 +324,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     Unit last{};
     last.b = -1;
-    put_unit(a, ctl->ring, nu, last, lane, abort_flag);
+    put_unit<kCall>(a, ctl->ring, nu, last, lane, abort_flag);
     if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
     if (lane == 0) {   // every copy lands before the CTA may exit (bounded waits)
 #pragma unroll 1
       for (uint32_t i = nk > KS ? nk - KS : 0; i < nk; ++i)
-        drain_phase(&ctl->kfull[i % KS], (i / KS) & 1);
+        drain_phase(a, &ctl->kfull[i % KS], (i / KS) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(smem_u32(&ctl->sfull[buf]));
       };
 #pragma unroll 1
-      for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, true, abort_flag); ++nu) {
+      for (uint32_t nu = 0; get_unit<kCall>(a, ctl->ring, nu, x, lane, true, abort_flag); ++nu) {
         if (x.nt == 0) continue;
         const bool two = x.tile1 - x.tile0 == 2;
         const int k0 = nk % KS, k1 = (nk + 1) % KS;
@@ -376,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every MMA is done before tensor memory is given back (bounded wait)
       umma_commit(smem_u32(&ctl->done));
-      drain_phase(&ctl->done, 0);
+      drain_phase(a, &ctl->done, 0);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t nu = 0;; ++nu) {
       float next[8] = {};
       int next_page = -1;
-      const bool more = get_unit(a, ctl->ring, nu, x, lane, false, abort_flag);
+      const bool more = get_unit<kCall>(a, ctl->ring, nu, x, lane, false, abort_flag);
       if (more) {
         const int j = x.tile0 * kTile + lane * 8;        // one page: 8 divides the page size
         next_page = j < x.stop ? page_of(a, x.b, j) : -1;
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&ctl->lfull[ls]));
     };
 #pragma unroll 1
-    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+    for (uint32_t nu = 0; get_unit<kCall>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
 #pragma unroll 1
       for (int t = 0; t < x.nt && !*abort_flag; t += tp, ++nl) {
         const int nt = min(tp, x.nt - t), qs = nl % kQStages;
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {   // every copy lands before the CTA may exit (bounded waits)
 #pragma unroll 1
       for (uint32_t i = nl > kQStages ? nl - kQStages : 0; i < nl; ++i)
-        drain_phase(&ctl->qfull[i % kQStages], (i / kQStages) & 1);
+        drain_phase(a, &ctl->qfull[i % kQStages], (i / kQStages) & 1);
     }
     __syncwarp();
   } else {
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t nl = 0, ns = 0;           // steps; this group's
     Unit x;
 #pragma unroll 1
-    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+    for (uint32_t nu = 0; get_unit<kCall>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
       const int j0 = (x.tile0 + g) * kTile, j = x.tile0 * kTile + key;
       const bool mine = x.tile0 + g < x.tile1;
       float sum = 0.f;

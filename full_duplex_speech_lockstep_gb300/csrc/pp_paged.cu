@@ -9,6 +9,9 @@ using namespace pp::paged;
 
 namespace {
 
+// pp_test_paged_faults: of this host thread's calls
+thread_local int test_wait_polls = 0, test_withhold = 0;
+
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 // The cache's own description: sizes, alignments, and offsets that stay within 64 bits.
@@ -46,6 +49,8 @@ Args base_args(const pp_paged_kv* kv, const int32_t* kv_len, uint32_t* status) {
   a.n_seqs = kv->n_seqs;
   a.table_ld = kv->table_ld;
   a.status = status;
+  a.wait_limit = test_wait_polls ? (uint32_t)test_wait_polls : kWaitLimit;
+  a.withhold = test_withhold;
   return a;
 }
 
@@ -155,6 +160,13 @@ int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, cons
   double f = 18446744073709551616.0 / 6.283185307179586476925;
   for (int i = 0; i < rot_dim / 2; ++i, f *= step) turns.f[i] = (uint64_t)f;
   return rc(launch_paged_append(a, x, turns, in_type, kv->type, (cudaStream_t)stream));
+}
+
+int pp_test_paged_faults(int32_t wait_polls, int32_t withhold) {
+  if (wait_polls < 0 || (withhold != 0 && withhold != 1)) return PP_EINVAL;
+  test_wait_polls = wait_polls;
+  test_withhold = withhold;
+  return PP_OK;
 }
 
 size_t pp_paged_attention_scratch_bytes(const pp_paged_kv* kv, int n_heads, int T, int max_q,

@@ -36,6 +36,9 @@ struct Args {
   int window;              // 0: none
   float c;                 // scale * log2(e): scores in powers of two
   uint32_t* status;
+  uint32_t wait_limit;     // polls before a wait gives up
+  int withhold;            // 1 in a failure-detection test: the barrier of a CTA's first tile waits for
+                           // an arrival that never comes
 };
 
 struct Seq {
@@ -78,24 +81,40 @@ __device__ __forceinline__ void check_len(const Args& a, const Seq& s) {
 
 // Bounded wait for a barrier's phase.  A phase that has completed costs one test; only a wait
 // that goes on looks at the CTA's abort flag, and one that runs out sets it and reports.
-__device__ __forceinline__ void wait_phase(const Args& a, uint64_t* bar, uint32_t parity,
-                                           volatile int* abort_flag) {
-  const uint32_t at = smem_u32(bar);
-  if (mbar_try_wait(at, parity)) return;
+// (`kCall`: what goes on is a function call, so that the wait's code is short.  Not for kernels that
+// split registers between warps: a call's are those of the whole kernel.)
+__device__ __forceinline__ void poll_phase(uint32_t* status, uint32_t limit, uint32_t at,
+                                           uint32_t parity, volatile int* abort_flag) {
 #pragma unroll 1     // (unrolled, the many waits of a kernel outgrow the instruction cache)
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+  for (uint32_t i = 0; i < limit; ++i) {
     if (*abort_flag) return;
     if (mbar_try_wait(at, parity)) return;
   }
   *abort_flag = 1;
-  raise(a, PP_S_TIMEOUT);
+  if (status) atomicOr(status, PP_S_TIMEOUT);
+}
+[[maybe_unused]] static __device__ __noinline__ void poll_phase_call(uint32_t* status, uint32_t limit,
+                                                                     uint32_t at, uint32_t parity,
+                                                                     volatile int* abort_flag) {
+  poll_phase(status, limit, at, parity, abort_flag);
+}
+template <bool kCall = false>
+__device__ __forceinline__ void wait_phase(const Args& a, uint64_t* bar, uint32_t parity,
+                                           volatile int* abort_flag) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait(at, parity)) return;
+  if constexpr (kCall)
+    poll_phase_call(a.status, a.wait_limit, at, parity, abort_flag);
+  else
+    poll_phase(a.status, a.wait_limit, at, parity, abort_flag);
 }
 
-// The same for a thread that has nothing to report: copies in flight, the last MMAs.
-__device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity) {
+// The same for a thread that has nothing to report: copies in flight, the last MMAs.  Both come in
+// microseconds, so a test's short limit does not cut them off.
+__device__ __forceinline__ void drain_phase(const Args& a, uint64_t* bar, uint32_t parity) {
   const uint32_t at = smem_u32(bar);
 #pragma unroll 1
-  for (uint32_t i = 0; i < kWaitLimit; ++i)
+  for (uint32_t i = 0; i < max(a.wait_limit, 1u << 16); ++i)
     if (mbar_try_wait(at, parity)) return;
 }
 
@@ -177,10 +196,11 @@ __device__ __forceinline__ void ring_init(UnitRing& r, int readers) {
   }
 }
 // By the producer warp: the k-th unit.
+template <bool kCall = false>
 __device__ __forceinline__ void put_unit(const Args& a, UnitRing& r, uint32_t k, const Unit& x,
                                          int lane, volatile int* abort_flag) {
   const int i = k % kUnits;
-  if (k >= kUnits) wait_phase(a, &r.empty[i], (k / kUnits - 1) & 1, abort_flag);
+  if (k >= kUnits) wait_phase<kCall>(a, &r.empty[i], (k / kUnits - 1) & 1, abort_flag);
   if (lane == 0) {
     r.unit[i] = x;
     mbar_arrive(smem_u32(&r.full[i]));
@@ -188,10 +208,11 @@ __device__ __forceinline__ void put_unit(const Args& a, UnitRing& r, uint32_t k,
 }
 // By each reader (a warp, or one thread of it with `alone`): the k-th unit, false after the
 // last one or when the CTA gives up.
+template <bool kCall = false>
 __device__ __forceinline__ bool get_unit(const Args& a, UnitRing& r, uint32_t k, Unit& x, int lane,
                                          bool alone, volatile int* abort_flag) {
   const int i = k % kUnits;
-  wait_phase(a, &r.full[i], (k / kUnits) & 1, abort_flag);
+  wait_phase<kCall>(a, &r.full[i], (k / kUnits) & 1, abort_flag);
   x = r.unit[i];
   if (!alone) __syncwarp();
   if (alone || lane == 0) mbar_arrive(smem_u32(&r.empty[i]));

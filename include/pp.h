@@ -585,6 +585,14 @@ int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, cons
                     const int32_t* kv_len, int T, int n_heads, void* q_out, uint32_t* status,
                     void* stream);
 
+/* Failure-detection tests of the two calls below, as pp_test_faults for an engine: of what this host
+ * thread's calls launch from now on, each bounded wait of a kernel has `wait_polls` polls (0: the
+ * default, 2^24), and with withhold = 1 the first tile of values (keys) of each CTA of an attention
+ * (mass) kernel never counts as loaded.  A wait for it then runs out, the kernel raises PP_S_TIMEOUT,
+ * drains its copies, frees its tensor memory and returns, with incomplete results.  Reset with (0, 0).
+ * Errors: PP_EINVAL (a negative number, another withhold). */
+int pp_test_paged_faults(int32_t wait_polls, int32_t withhold);
+
 /* Attention of the new rows over the cache:
  *   out[t][h] = sum_j exp(s_j - lse) V_j,  s_j = scale q[t][h] . K_j,  lse = log sum_j exp(s_j)
  * over the entries j that the row sees, of key head h / (n_heads / n_kv_heads).  A row that
