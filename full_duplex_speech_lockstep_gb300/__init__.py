@@ -43,7 +43,9 @@ EXPORTS = ["pp_weight_shape", "pp_workspace_bytes", "pp_create", "pp_destroy",
            "pp_driver_prepare", "pp_driver_absorb", "pp_driver_tick", "pp_session_sampling",
            "pp_sample", "pp_test_faults", "pp_paged_append",
            "pp_paged_attention_scratch_bytes", "pp_paged_attention", "pp_paged_mass",
-           "pp_paged_evict", "pp_test_paged_faults"]
+           "pp_paged_evict", "pp_test_paged_faults", "pp_packed_append",
+           "pp_packed_attention_scratch_bytes", "pp_packed_attention", "pp_packed_read",
+           "pp_token_logprobs"]
 
 # enum pp_kernel_kind
 KERNEL_KINDS = ["begin", "norm", "qkv", "rope_ring", "attn", "oproj", "gateup", "down",
@@ -91,6 +93,14 @@ class pp_paged_kv(ctypes.Structure):
     """One cache of pages with its block table (device pointers)."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("mass", ctypes.c_void_p),
                 ("table", ctypes.c_void_p), ("page_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ["n_pages", "page_size", "n_kv_heads", "head_dim", "type",
+                                      "n_seqs", "table_ld"]]
+
+
+class pp_packed_kv(ctypes.Structure):
+    """One 8-bit cache of pages with its block table (device pointers)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ["k", "v", "k_scale", "v_scale", "table"]] + [
+        ("page_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64)] + [
         (n, ctypes.c_int32) for n in ["n_pages", "page_size", "n_kv_heads", "head_dim", "type",
                                       "n_seqs", "table_ld"]]
 
@@ -185,6 +195,17 @@ def lib():
         L.pp_paged_evict.restype = I
         L.pp_test_paged_faults.argtypes = [ctypes.c_int32, ctypes.c_int32]
         L.pp_test_paged_faults.restype = I
+        KV8 = ctypes.POINTER(pp_packed_kv)
+        L.pp_packed_append.argtypes = [KV8] + L.pp_paged_append.argtypes[1:]
+        L.pp_packed_append.restype = I
+        L.pp_packed_attention_scratch_bytes.argtypes = [KV8, I, I, I, I]
+        L.pp_packed_attention_scratch_bytes.restype = ctypes.c_size_t
+        L.pp_packed_attention.argtypes = [KV8] + L.pp_paged_attention.argtypes[1:]
+        L.pp_packed_attention.restype = I
+        L.pp_packed_read.argtypes = [KV8, P, KV, P, P]
+        L.pp_packed_read.restype = I
+        L.pp_token_logprobs.argtypes = [P, I, I64, I, I, I64, I, P, I64, I, P, P, P, P, P, P]
+        L.pp_token_logprobs.restype = I
         _lib = L
     return _lib
 
@@ -479,7 +500,117 @@ def pp_paged_evict(kv, kv_len, budget, recent, to, to_len, kept, status, stream)
         ctypes.byref(kv), kv_len, budget, recent, ctypes.byref(to), to_len, kept, status, stream))
 
 
+def pp_packed_append(kv, q, q_stride, k, k_stride, v, v_stride, in_type, q_alpha, k_alpha, eps,
+                     rope_base, rot_dim, halves, positions, cu, kv_len, T, n_heads, q_out, status,
+                     stream):
+    """pp_paged_append into an 8-bit cache."""
+    return _check("pp_packed_append", lib().pp_packed_append(
+        ctypes.byref(kv), q, q_stride, k, k_stride, v, v_stride, in_type, q_alpha, k_alpha, eps,
+        rope_base, rot_dim, halves, positions, cu, kv_len, T, n_heads, q_out, status, stream))
+
+
+def pp_packed_attention_scratch_bytes(kv, n_heads, T, max_q, window):
+    n = lib().pp_packed_attention_scratch_bytes(ctypes.byref(kv), n_heads, T, max_q, window)
+    if n == 0:
+        raise PPError("pp_packed_attention_scratch_bytes", PP_EINVAL)
+    return n
+
+
+def pp_packed_attention(kv, q, q_stride, cu, kv_len, T, max_q, n_heads, scale, window, out, lse,
+                        status, scratch, scratch_bytes, stream):
+    """Attention of new rows over an 8-bit cache."""
+    return _check("pp_packed_attention", lib().pp_packed_attention(
+        ctypes.byref(kv), q, q_stride, cu, kv_len, T, max_q, n_heads, scale, window, out, lse,
+        status, scratch, scratch_bytes, stream))
+
+
+def pp_packed_read(kv, kv_len, to, status, stream):
+    """The entries of an 8-bit cache into the pages of a 16-bit one."""
+    return _check("pp_packed_read", lib().pp_packed_read(
+        ctypes.byref(kv), kv_len, ctypes.byref(to), status, stream))
+
+
+def pp_token_logprobs(logits, type, ld, rows, inner, inner_ld, n, tokens, token_ld, top, logprob,
+                      entropy, top_tokens, top_logprobs, status, stream):
+    """Log probabilities of given tokens, entropy and the likeliest alternatives of each row."""
+    return _check("pp_token_logprobs", lib().pp_token_logprobs(
+        logits, type, ld, rows, inner, inner_ld, n, tokens, token_ld, top, logprob, entropy,
+        top_tokens, top_logprobs, status, stream))
+
+
 # ---- convenience wrapper over torch device memory ---------------------------------------
+
+def _types(torch):
+    return {torch.float32: PP_F32, torch.bfloat16: PP_BF16, torch.float16: PP_F16}
+
+
+def _raw_stream(torch):
+    """The current stream's handle by device index, without a stream object where torch offers it."""
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_device(torch, index, raw_stream, name, fn, *args):
+    """One library call on a device and that device's current stream."""
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw_stream(index))
+    if rc != PP_OK:
+        raise PPError(name, rc)
+
+
+def token_logprobs(logits, tokens=None, top=0, with_entropy=False, status=None):
+    """Log probabilities of given tokens: a dict of "logprob" (f32, like ``tokens``),
+    "entropy" (f32, on request) and, with ``top`` > 0, "top_tokens" (int32) and "top_logprobs"
+    (f32) of the likeliest alternatives in order ([..., top]).
+
+    ``logits`` is [rows, n] or [groups, rows, n] in f32, bf16 or fp16, ``tokens`` int32 of its
+    leading shape; the last dim of each must be contiguous, rows and groups may lie apart.  A negative
+    token is padding and gives 0.  ``status`` (int32, one word) collects PP_S_* bits.  Runs on the
+    logits' device, on its current stream."""
+    import torch
+    types, lead = _types(torch), tuple(logits.shape[:-1])
+    if not logits.is_cuda or logits.dtype not in types or logits.dim() not in (2, 3):
+        raise ValueError("logits: %s %s on %s, expected CUDA [rows, n] or [groups, rows, n] in f32, "
+                         "bf16 or fp16" % (logits.dtype, tuple(logits.shape), logits.device))
+    n = logits.shape[-1]
+    if n > 1 and logits.stride(-1) != 1:
+        raise ValueError("logits: the values of a row must be contiguous")
+    index = logits.get_device()
+    for name, t in (("tokens", tokens), ("status", status)):
+        if t is not None and (t.get_device() != index or t.dtype is not torch.int32):
+            raise ValueError("%s: %s on %s, expected int32 on %s" % (name, t.dtype, t.device,
+                                                                    logits.device))
+    if status is not None and tuple(status.shape) != (1,):
+        raise ValueError("status: %s, expected one word" % (tuple(status.shape),))
+    if tokens is not None:
+        if tuple(tokens.shape) != lead:
+            raise ValueError("tokens: %s, expected %s" % (tuple(tokens.shape), lead))
+        if len(lead) == 2 and lead[1] > 1 and tokens.stride(1) != 1:
+            raise ValueError("tokens: the tokens of a group must be contiguous")
+    rows, inner = lead if len(lead) == 2 else (lead[0], 1)
+    out = {}
+    new = lambda dtype, *shape: torch.empty(lead + shape, dtype=dtype, device=logits.device)
+    if tokens is not None:
+        out["logprob"] = new(torch.float32)
+    if with_entropy:
+        out["entropy"] = new(torch.float32)
+    if top:
+        out["top_tokens"] = new(torch.int32, max(top, 0))
+        out["top_logprobs"] = new(torch.float32, max(top, 0))
+    ptr = lambda t: None if t is None else t.data_ptr()
+    if rows * inner == 0:
+        inner, rows = max(inner, 1), 0
+    _on_device(torch, index, _raw_stream(torch), "pp_token_logprobs", lib().pp_token_logprobs,
+               logits.data_ptr(), types[logits.dtype], logits.stride(0), rows, inner,
+               logits.stride(1) if len(lead) == 2 else 0, n, ptr(tokens),
+               tokens.stride(0) if tokens is not None else 0, top, ptr(out.get("logprob")),
+               ptr(out.get("entropy")), ptr(out.get("top_tokens")), ptr(out.get("top_logprobs")),
+               ptr(status))
+    return out
+
 
 class Engine:
     """One engine over torch-owned device memory (weights dict + workspace)."""
@@ -562,6 +693,20 @@ class Engine:
                 None if logits is None else logits.data_ptr(), self._stream())
         return col
 
+    def score(self, logits, column, top=0, with_entropy=False, status=None):
+        """What the model made of a tick's tokens: token_logprobs of the text row ([B]) and of
+        the codebook rows ([B, n_q]), from the ``logits`` that ``step`` wrote and a column
+        (forced, generated or any other; a closed slot's -1 gives 0).  Initial tokens have no
+        logit: they give 0 and raise PP_S_INDEX in ``status``."""
+        text, shape = self.shape.text_vocab, self.shape
+        if tuple(logits.shape) != (self.B, self.logits_ld):
+            raise ValueError("logits: %s, expected %s" % (tuple(logits.shape),
+                                                          (self.B, self.logits_ld)))
+        return tuple(token_logprobs(x, t, top, with_entropy, status) for x, t in (
+            (logits[:, :text], column[:, 0]),
+            (logits[:, text:].unflatten(1, (shape.n_q, shape.audio_card)),
+             column[:, 1:1 + shape.n_q])))
+
     def profile_step(self, prev_column, user_codes, kind_ms, kind_launches, out=None):
         """One tick through the profiling graph; accumulates per-kind ms / launches."""
         col = self.column if out is None else out
@@ -580,52 +725,32 @@ class Engine:
         return column
 
 
-class PagedKV:
-    """One layer's paged cache over torch-owned device memory.
+class _Pages:
+    """What the caches of pages have in common: a block table, a status word, checks of tensors,
+    and the calls whose arguments are the same for 16-bit and 8-bit entries."""
 
-    ``k`` and ``v`` are [pages, kv_heads, page_size, head_dim] in bf16 or fp16, ``table``
-    [sequences, table width] int32 page numbers, ``mass`` (optional) f32 [pages, kv_heads,
-    page_size].  ``cu`` is int32 [sequences + 1] row offsets and ``kv_len`` int32 [sequences]
-    entry counts, the new entries included.  Every call runs on the cache's device, on its
-    current stream.  Tensors that do not fit raise ValueError; what the library refuses
-    raises PPError."""
+    family = scratch_bytes = None        # of the library's calls
 
-    def __init__(self, k, v, table, mass=None, status=None):
+    def _table(self, k, table, status):
+        """Device, sequences and status word of a cache whose keys are k."""
         import torch
-        self.torch = torch
-        self.types = {torch.float32: PP_F32, torch.bfloat16: PP_BF16, torch.float16: PP_F16}
-        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
-            raise ValueError("k and v must be [pages, heads, rows, dims] of one layout and type")
-        if k.dtype not in (torch.bfloat16, torch.float16):
-            raise ValueError("the cache holds bf16 or fp16, not %s" % k.dtype)
-        if not k.is_cuda or v.device != k.device:
-            raise ValueError("k and v must be on one CUDA device")
-        n_pages, heads, rows, dim = k.shape
-        if n_pages and not k[0].is_contiguous():
-            raise ValueError("each page of k and v must be contiguous")
+        self.torch, self.types = torch, _types(torch)
         if table.dim() != 2:
             raise ValueError("table must be [sequences, width]")
-        self.device, self.index, self.dtype = k.device, k.get_device(), k.dtype
-        self.k, self.v, self.table, self.mass = k, v, table, mass
-        self.heads, self.dim, self.n = heads, dim, table.shape[0]
+        self.device, self.index = k.device, k.get_device()
+        self.table, self.n = table, table.shape[0]
         self._fits("table", table, torch.int32, table.shape)
-        self.mass_shape = (n_pages, heads, rows)
-        if mass is not None:
-            self._fits("mass", mass, torch.float32, self.mass_shape)
         if status is None:
             status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._fits("status", status, torch.int32, (1,))
         self.status = status
         # stands in for a scratch that a call asks for but does not use (the smallest size)
         self.unused = torch.empty(256, dtype=torch.uint8, device=self.device)
-        stride = k.stride(0) if n_pages > 1 else heads * rows * dim
-        self.c = pp_paged_kv(k.data_ptr(), v.data_ptr(), self._ptr(mass), table.data_ptr(),
-                             stride, n_pages, rows, heads, dim, self.types[k.dtype],
-                             table.shape[0], table.shape[1])
-        self.ref, self.lib, self.sizes = ctypes.byref(self.c), lib(), {}
-        # the current stream's handle without building a stream object, where torch offers it
-        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self.raw_stream = _raw_stream(torch)
+
+    def _bind(self, c):
+        self.c = c
+        self.ref, self.lib, self.sizes = ctypes.byref(c), lib(), {}
 
     @staticmethod
     def _ptr(t):
@@ -657,14 +782,7 @@ class PagedKV:
 
     def _call(self, name, *args):
         """One library call on the cache's device and that device's current stream."""
-        cuda, fn = self.torch.cuda, getattr(self.lib, name)
-        if cuda.current_device() == self.index:
-            rc = fn(*args, self.raw_stream(self.index))
-        else:
-            with cuda.device(self.index):
-                rc = fn(*args, self.raw_stream(self.index))
-        if rc != PP_OK:
-            raise PPError(name, rc)
+        _on_device(self.torch, self.index, self.raw_stream, name, getattr(self.lib, name), *args)
 
     def _scratch_bytes(self, *shape):
         """Scratch of an attention call, by its shape (heads, rows, max_q, window)."""
@@ -672,7 +790,7 @@ class PagedKV:
         if n is None:
             if len(self.sizes) >= 1024:
                 self.sizes.clear()
-            n = self.sizes[shape] = pp_paged_attention_scratch_bytes(self.c, *shape)
+            n = self.sizes[shape] = self.scratch_bytes(self.c, *shape)
         return n
 
     @staticmethod
@@ -711,7 +829,7 @@ class PagedKV:
             out = torch.empty((T, H, self.dim), dtype=self.dtype, device=self.device)
         else:
             self._fits("out", out, self.dtype, (T, H, self.dim))
-        self._call("pp_paged_append", self.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        self._call(self.family + "_append", self.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
                    self.types[dtype], self._ptr(q_alpha), self._ptr(k_alpha), eps, rope_base,
                    self.dim if rot_dim is None else rot_dim, int(halves), self._ptr(positions),
                    cu.data_ptr(), kv_len.data_ptr(), T, H, out.data_ptr(), self.status.data_ptr())
@@ -735,11 +853,46 @@ class PagedKV:
         nbytes = self._scratch_bytes(H, T, max_q, window)
         scratch = self.unused if nbytes <= 256 else \
             torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        self._call("pp_paged_attention", self.ref, q.data_ptr(), qs, cu.data_ptr(), kv_len.data_ptr(),
+        self._call(self.family + "_attention", self.ref, q.data_ptr(), qs, cu.data_ptr(), kv_len.data_ptr(),
                    T, max_q, H, self.dim ** -0.5 if scale is None else scale, window,
                    out.data_ptr(), self._ptr(lse), self.status.data_ptr(), scratch.data_ptr(),
                    nbytes)
         return (out, lse) if with_lse else out
+
+
+class PagedKV(_Pages):
+    """One layer's paged cache over torch-owned device memory.
+
+    ``k`` and ``v`` are [pages, kv_heads, page_size, head_dim] in bf16 or fp16, ``table``
+    [sequences, table width] int32 page numbers, ``mass`` (optional) f32 [pages, kv_heads,
+    page_size].  ``cu`` is int32 [sequences + 1] row offsets and ``kv_len`` int32 [sequences]
+    entry counts, the new entries included.  Every call runs on the cache's device, on its
+    current stream.  Tensors that do not fit raise ValueError; what the library refuses
+    raises PPError."""
+
+    family, scratch_bytes = "pp_paged", staticmethod(pp_paged_attention_scratch_bytes)
+
+    def __init__(self, k, v, table, mass=None, status=None):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise ValueError("k and v must be [pages, heads, rows, dims] of one layout and type")
+        if k.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("the cache holds bf16 or fp16, not %s" % k.dtype)
+        if not k.is_cuda or v.device != k.device:
+            raise ValueError("k and v must be on one CUDA device")
+        n_pages, heads, rows, dim = k.shape
+        if n_pages and not k[0].is_contiguous():
+            raise ValueError("each page of k and v must be contiguous")
+        self.k, self.v, self.mass, self.dtype = k, v, mass, k.dtype
+        self.heads, self.dim = heads, dim
+        self._table(k, table, status)
+        self.mass_shape = (n_pages, heads, rows)
+        if mass is not None:
+            self._fits("mass", mass, torch.float32, self.mass_shape)
+        stride = k.stride(0) if n_pages > 1 else heads * rows * dim
+        self._bind(pp_paged_kv(k.data_ptr(), v.data_ptr(), self._ptr(mass), table.data_ptr(), stride,
+                               n_pages, rows, heads, dim, self.types[k.dtype], table.shape[0],
+                               table.shape[1]))
 
     def attention_mass(self, q, lse, cu, kv_len, max_q=None, scale=None, window=0, decay=1.0,
                        mass=None):
@@ -776,3 +929,52 @@ class PagedKV:
         self._call("pp_paged_evict", self.ref, kv_len.data_ptr(), budget, recent, to.ref,
                    to_len.data_ptr(), kept.data_ptr(), self.status.data_ptr())
         return to_len, kept
+
+
+class PagedKV8(_Pages):
+    """One layer's paged cache in 8 bits over torch-owned device memory.
+
+    ``k`` and ``v`` are [pages, kv_heads, page_size, head_dim] float8_e4m3fn codes, ``k_scale`` and
+    ``v_scale`` [pages, kv_heads, page_size] powers of two (float8_e8m0fnu, or their bytes as uint8),
+    ``dtype`` (bf16 or fp16) the type of queries and outputs.  Append and attention are those of
+    PagedKV; ``read`` gives 16-bit entries for what works on them (attention mass, eviction)."""
+
+    family, scratch_bytes = "pp_packed", staticmethod(pp_packed_attention_scratch_bytes)
+
+    def __init__(self, k, v, k_scale, v_scale, table, dtype=None, status=None):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must be [pages, heads, rows, dims] of one layout")
+        if k.dtype is not torch.float8_e4m3fn or v.dtype is not k.dtype:
+            raise ValueError("the cache holds float8_e4m3fn, not %s and %s" % (k.dtype, v.dtype))
+        if not k.is_cuda or any(t.device != k.device for t in (v, k_scale, v_scale)):
+            raise ValueError("k, v and their scales must be on one CUDA device")
+        n_pages, heads, rows, dim = k.shape
+        if (tuple(k_scale.shape) != (n_pages, heads, rows) or k_scale.shape != v_scale.shape
+                or k_scale.stride() != v_scale.stride()):
+            raise ValueError("k_scale and v_scale must be [%d, %d, %d] of one layout" % (
+                n_pages, heads, rows))
+        if any(t.dtype not in (torch.uint8, torch.float8_e8m0fnu) for t in (k_scale, v_scale)):
+            raise ValueError("scales are float8_e8m0fnu or uint8, not %s and %s" % (
+                k_scale.dtype, v_scale.dtype))
+        if n_pages and not (k[0].is_contiguous() and k_scale[0].is_contiguous()):
+            raise ValueError("each page of k, v and their scales must be contiguous")
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("queries and outputs are bf16 or fp16, not %s" % dtype)
+        self.k, self.v, self.k_scale, self.v_scale, self.dtype = k, v, k_scale, v_scale, dtype
+        self.heads, self.dim = heads, dim
+        self._table(k, table, status)
+        stride = k.stride(0) if n_pages > 1 else heads * rows * dim
+        scales = k_scale.stride(0) if n_pages > 1 else heads * rows
+        self._bind(pp_packed_kv(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                table.data_ptr(), stride, scales, n_pages, rows, heads, dim,
+                                self.types[dtype], table.shape[0], table.shape[1]))
+
+    def read(self, kv_len, to):
+        """What the first kv_len entries of each sequence hold, into the same entries of the
+        PagedKV `to` (of this cache's ``dtype``; of any page size)."""
+        if to.index != self.index:
+            raise ValueError("both caches must be on one device")
+        self._fits("kv_len", kv_len, self.torch.int32, (self.n,))
+        self._call("pp_packed_read", self.ref, kv_len.data_ptr(), to.ref, self.status.data_ptr())

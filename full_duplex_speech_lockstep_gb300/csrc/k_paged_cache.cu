@@ -51,6 +51,37 @@ __device__ __forceinline__ void store8(T* p, const float x[8]) {
   *reinterpret_cast<uint4*>(p) = a;
 }
 
+// Eight values of a head as e4m3 codes under the head's power of two (include/pp.h, "the paged cache in 8
+// bits").  The head's largest magnitude goes by bits: those of a NaN or an infinity are above all others.
+// `L` lanes hold the head; all of a warp's lanes take part.
+template <int L>
+__device__ __forceinline__ uint2 pack_codes(const float y[8], uint32_t& scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (top >= 0x7f800000u) {
+    scale = 255u;
+    return make_uint2(0u, 0u);
+  }
+  // a = m 2^(E - 127), m in [1, 2): a 2^-e <= 448 = 1.75 2^8 for e = E - 135, or one more if m > 1.75
+  const int byte = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+  scale = (uint32_t)max(byte, 0);
+  const float f = __uint_as_float((254u - scale) << 23);   // 2^(127 - byte), at most 2^127
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[4 * i + 1] * f), "f"(y[4 * i] * f));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(hi)
+        : "f"(y[4 * i + 3] * f), "f"(y[4 * i + 2] * f));
+    w[i] = lo | (uint32_t)hi << 16;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
 // One CTA to a token, D/8 lanes to a head.  Bound by reading and writing the rows once: the
 // first heads' loads go out before the token's place in the cache is known, whose chain of
 // lookups (row offsets, length, page) they hide.
@@ -61,7 +92,8 @@ __device__ __forceinline__ void store8(T* p, const float x[8]) {
 // five, they spill).  Halves through shared
 // memory took 75 us.  (Ten tokens to a CTA with the next one's loads ahead: no faster, and slower
 // for few tokens.)
-template <typename I, typename T, int D>
+// `kPack`: keys and values are held in 8 bits.
+template <typename I, typename T, int D, bool kPack>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(I) == 2 ? 4 : 3)
     k_paged_append(const __grid_constant__ Args a, const __grid_constant__ AppendArgs x,
                    const __grid_constant__ Turns turns) {
@@ -187,9 +219,17 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(I) == 2 ? 4 : 3)
           y[e + 1] = p * w.y + o * w.x;
         }
       }
+      uint32_t scale = 0;
+      uint2 codes{};
+      if constexpr (kPack) codes = pack_codes<L>(y, scale);
       if (!live) continue;
       if (kind == 0) {
         store8(reinterpret_cast<T*>(x.q_out) + ((int64_t)t * H + h) * D + l * 8, y);
+      } else if (kPack && page >= 0) {
+        uint8_t* pool = reinterpret_cast<uint8_t*>(kind == 1 ? x.k_pages : x.v_pages);
+        const int64_t at = ((int64_t)h << a.lps) + in_page;
+        *reinterpret_cast<uint2*>(pool + page * a.page_stride + at * D + l * 8) = codes;
+        if (l == 0) (kind == 1 ? x.k_scale : x.v_scale)[page * x.scale_stride + at] = (uint8_t)scale;
       } else if (page >= 0) {
         T* pool = reinterpret_cast<T*>(kind == 1 ? x.k_pages : x.v_pages);
         store8(pool + page * a.page_stride + (((int64_t)h << a.lps) + in_page) * D + l * 8, y);
@@ -431,22 +471,29 @@ __global__ void __launch_bounds__(kMoveThreads)
   }
 }
 
-template <typename I, typename T>
+template <typename I, typename T, bool kPack>
 cudaError_t append(const Args& a, const AppendArgs& x, const Turns& turns, cudaStream_t s) {
-  if (a.D == 128)
-    return launch(k_paged_append<I, T, 128>, dim3((unsigned)a.T), kAppendThreads, 0, s, a, x, turns);
-  return launch(k_paged_append<I, T, 64>, dim3((unsigned)a.T), kAppendThreads, 0, s, a, x, turns);
+  const dim3 grid((unsigned)a.T);
+  return a.D == 128
+             ? launch(k_paged_append<I, T, 128, kPack>, grid, kAppendThreads, 0, s, a, x, turns)
+             : launch(k_paged_append<I, T, 64, kPack>, grid, kAppendThreads, 0, s, a, x, turns);
+}
+template <typename T, bool kPack>
+cudaError_t append_type(const Args& a, const AppendArgs& x, const Turns& turns, int in_type,
+                        cudaStream_t s) {
+  return in_type == PP_F32 ? append<float, T, kPack>(a, x, turns, s)
+                           : append<T, T, kPack>(a, x, turns, s);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const Args& a, const AppendArgs& x, const Turns& turns, int in_type,
                                 int type, cudaStream_t s) {
-  if (type == PP_BF16)
-    return in_type == PP_F32 ? append<float, __nv_bfloat16>(a, x, turns, s)
-                             : append<__nv_bfloat16, __nv_bfloat16>(a, x, turns, s);
-  return in_type == PP_F32 ? append<float, __half>(a, x, turns, s)
-                           : append<__half, __half>(a, x, turns, s);
+  if (x.k_scale)
+    return type == PP_BF16 ? append_type<__nv_bfloat16, true>(a, x, turns, in_type, s)
+                           : append_type<__half, true>(a, x, turns, in_type, s);
+  return type == PP_BF16 ? append_type<__nv_bfloat16, false>(a, x, turns, in_type, s)
+                         : append_type<__half, false>(a, x, turns, in_type, s);
 }
 
 cudaError_t launch_paged_evict(const Args& a, const EvictArgs& x, cudaStream_t s) {

@@ -14,11 +14,9 @@ thread_local int test_wait_polls = 0, test_withhold = 0;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-// The cache's own description: sizes, alignments, and offsets that stay within 64 bits.
-bool cache_ok(const pp_paged_kv* kv) {
-  if (!kv || !kv->k || !kv->v || !kv->table) return false;
-  if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->mass, 4) || !aligned(kv->table, 4))
-    return false;
+// A cache's sizes (of either kind), and counts that stay within 32 bits.
+template <typename KV>
+bool sizes_ok(const KV* kv) {
   if (kv->type != PP_BF16 && kv->type != PP_F16) return false;
   if (kv->head_dim != 64 && kv->head_dim != 128) return false;
   if (kv->page_size < 16 || kv->page_size > 256 || (kv->page_size & (kv->page_size - 1)))
@@ -27,16 +25,34 @@ bool cache_ok(const pp_paged_kv* kv) {
   if (kv->n_seqs < 1 || kv->n_seqs > kMaxSeqs || kv->table_ld < 1) return false;
   if ((int64_t)kv->table_ld * kv->page_size > (int64_t)1 << 28) return false;
   // units, tiles and blocks of a call are counted in 32 bits
-  if ((int64_t)kv->n_seqs * kv->n_kv_heads *
-          (((int64_t)kv->table_ld * kv->page_size + kTile - 1) / kTile) >= (int64_t)1 << 28)
-    return false;
-  const int64_t page = (int64_t)kv->n_kv_heads * kv->page_size * kv->head_dim;
-  if (kv->page_stride < page || (kv->page_stride & 7) || kv->page_stride >= (int64_t)1 << 38)
-    return false;
-  return true;
+  return (int64_t)kv->n_seqs * kv->n_kv_heads *
+             (((int64_t)kv->table_ld * kv->page_size + kTile - 1) / kTile) <
+         (int64_t)1 << 28;
 }
 
-Args base_args(const pp_paged_kv* kv, const int32_t* kv_len, uint32_t* status) {
+// The cache's own description: sizes, alignments, and offsets that stay within 64 bits.
+bool cache_ok(const pp_paged_kv* kv) {
+  if (!kv || !kv->k || !kv->v || !kv->table) return false;
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->mass, 4) || !aligned(kv->table, 4))
+    return false;
+  if (!sizes_ok(kv)) return false;
+  const int64_t page = (int64_t)kv->n_kv_heads * kv->page_size * kv->head_dim;
+  return kv->page_stride >= page && !(kv->page_stride & 7) && kv->page_stride < (int64_t)1 << 38;
+}
+bool cache_ok(const pp_packed_kv* kv) {
+  if (!kv || !kv->k || !kv->v || !kv->k_scale || !kv->v_scale || !kv->table) return false;
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->k_scale, 16) ||
+      !aligned(kv->v_scale, 16) || !aligned(kv->table, 4))
+    return false;
+  if (!sizes_ok(kv)) return false;
+  const int64_t rows = (int64_t)kv->n_kv_heads * kv->page_size;
+  return kv->page_stride >= rows * kv->head_dim && !(kv->page_stride & 15) &&
+         kv->page_stride < (int64_t)1 << 38 && kv->scale_stride >= rows &&
+         !(kv->scale_stride & 15) && kv->scale_stride < (int64_t)1 << 38;
+}
+
+template <typename KV>
+Args base_args(const KV* kv, const int32_t* kv_len, uint32_t* status) {
   Args a{};
   a.table = kv->table;
   a.len = kv_len;
@@ -55,11 +71,20 @@ Args base_args(const pp_paged_kv* kv, const int32_t* kv_len, uint32_t* status) {
 }
 
 // The new rows of a call: cu, T and the query heads.
-bool rows_ok(const pp_paged_kv* kv, const int32_t* cu, const int32_t* kv_len, int T, int n_heads) {
+template <typename KV>
+bool rows_ok(const KV* kv, const int32_t* cu, const int32_t* kv_len, int T, int n_heads) {
   if (!cu || !kv_len || !aligned(cu, 4) || !aligned(kv_len, 4)) return false;
   if (T < 0 || n_heads < 1 || n_heads % kv->n_kv_heads != 0) return false;
   const int G = n_heads / kv->n_kv_heads;
   return G <= kMaxGroup && T <= 1 << 28 && (int64_t)T * n_heads < (int64_t)1 << 31;
+}
+
+// An attention's arrays, for rows of `row` values.
+bool attention_ok(const void* q, int64_t q_stride, const void* out, const float* lse,
+                  const void* scratch, int64_t row) {
+  return q && out && scratch && q_stride >= row && !(q_stride & 7) &&
+         q_stride < (int64_t)1 << 38 && aligned(q, 16) && aligned(out, 16) && aligned(lse, 4) &&
+         aligned(scratch, 256);
 }
 
 // A window that no row outgrows is none.
@@ -110,16 +135,63 @@ bool is_long(const Args& a, int max_q) { return (int64_t)max_q * a.G > kShortRow
 
 int rc(cudaError_t err) { return err == cudaSuccess ? PP_OK : PP_E_CUDA; }
 
-}  // namespace
+// Do `n` bytes from a and `m` bytes from b meet?
+bool meet(const void* a, int64_t n, const void* b, int64_t m) {
+  const intptr_t x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
+  return x < y + m && y < x + n;
+}
 
-extern "C" {
+// A 16-bit copy of an 8-bit cache in scratch: a page for each entry of its table, and their table.
+struct Mirror {
+  int64_t pages, page;       // pages; values of one
+  size_t pool, bytes;        // bytes of K (and of V); of all
+};
+Mirror mirror_of(const pp_packed_kv* kv) {
+  Mirror m;
+  m.pages = (int64_t)kv->n_seqs * kv->table_ld;
+  m.page = (int64_t)kv->n_kv_heads * kv->page_size * kv->head_dim;
+  m.pool = (size_t)(m.pages * m.page) * 2;      // (a page has 2 KB or more)
+  m.bytes = 2 * m.pool + (((size_t)m.pages * sizeof(int32_t) + 255) & ~(size_t)255);
+  return m;
+}
+pp_paged_kv mirror_cache(const pp_packed_kv* kv, const Mirror& m, char* scratch) {
+  pp_paged_kv to{};
+  to.k = scratch;
+  to.v = scratch + m.pool;
+  to.table = reinterpret_cast<const int32_t*>(scratch + 2 * m.pool);
+  to.page_stride = m.page;
+  to.n_pages = (int32_t)m.pages;                // at most eight to a key tile, of which 2^28
+  to.page_size = kv->page_size;
+  to.n_kv_heads = kv->n_kv_heads;
+  to.head_dim = kv->head_dim;
+  to.type = kv->type;
+  to.n_seqs = kv->n_seqs;
+  to.table_ld = kv->table_ld;
+  return to;
+}
+ReadArgs read_args(const pp_packed_kv* kv, const pp_paged_kv* to) {
+  ReadArgs x{};
+  x.from = Packed{reinterpret_cast<const uint8_t*>(kv->k), reinterpret_cast<const uint8_t*>(kv->v),
+                  reinterpret_cast<const uint8_t*>(kv->k_scale),
+                  reinterpret_cast<const uint8_t*>(kv->v_scale), kv->scale_stride};
+  x.to_k = to->k;
+  x.to_v = to->v;
+  x.to_mass = to->mass;
+  x.to_table = const_cast<int32_t*>(to->table);
+  x.to_page_stride = to->page_stride;
+  x.to_n_pages = to->n_pages;
+  while ((1 << x.to_lps) < to->page_size) ++x.to_lps;
+  x.to_table_ld = to->table_ld;
+  return x;
+}
 
-int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, const void* k,
-                    int64_t k_stride, const void* v, int64_t v_stride, int in_type,
-                    const float* q_alpha, const float* k_alpha, float eps, float rope_base,
-                    int rot_dim, int halves, const int32_t* positions, const int32_t* cu,
-                    const int32_t* kv_len, int T, int n_heads, void* q_out, uint32_t* status,
-                    void* stream) {
+// The arguments of an append beside the cache: checked, and as its kernel takes them.
+template <typename KV>
+int append(const KV* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+           const void* v, int64_t v_stride, int in_type, const float* q_alpha, const float* k_alpha,
+           float eps, float rope_base, int rot_dim, int halves, const int32_t* positions,
+           const int32_t* cu, const int32_t* kv_len, int T, int n_heads, void* q_out,
+           uint32_t* status, void* stream, AppendArgs x) {
   if (!cache_ok(kv) || !rows_ok(kv, cu, kv_len, T, n_heads)) return PP_EINVAL;
   if (in_type != PP_F32 && in_type != kv->type) return PP_EINVAL;
   if (rot_dim < 0 || rot_dim > kv->head_dim || (rot_dim & 1)) return PP_EINVAL;
@@ -137,7 +209,6 @@ int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, cons
   a.cu = cu;
   a.T = T;
   a.G = n_heads / kv->n_kv_heads;
-  AppendArgs x{};
   x.q = q;
   x.k = k;
   x.v = v;
@@ -153,13 +224,28 @@ int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, cons
   x.q_out = q_out;
   x.k_pages = kv->k;
   x.v_pages = kv->v;
-  x.mass = kv->mass;
   // turns of pair i per position: base^(-2i/rot) / 2 pi, below a sixth, in units of 2^-64
   Turns turns{};
   const double step = rot_dim ? pow((double)rope_base, -2.0 / rot_dim) : 1.0;
   double f = 18446744073709551616.0 / 6.283185307179586476925;
   for (int i = 0; i < rot_dim / 2; ++i, f *= step) turns.f[i] = (uint64_t)f;
   return rc(launch_paged_append(a, x, turns, in_type, kv->type, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int pp_paged_append(const pp_paged_kv* kv, const void* q, int64_t q_stride, const void* k,
+                    int64_t k_stride, const void* v, int64_t v_stride, int in_type,
+                    const float* q_alpha, const float* k_alpha, float eps, float rope_base,
+                    int rot_dim, int halves, const int32_t* positions, const int32_t* cu,
+                    const int32_t* kv_len, int T, int n_heads, void* q_out, uint32_t* status,
+                    void* stream) {
+  AppendArgs x{};
+  if (kv) x.mass = kv->mass;
+  return append(kv, q, q_stride, k, k_stride, v, v_stride, in_type, q_alpha, k_alpha, eps, rope_base,
+                rot_dim, halves, positions, cu, kv_len, T, n_heads, q_out, status, stream, x);
 }
 
 int pp_test_paged_faults(int32_t wait_polls, int32_t withhold) {
@@ -193,11 +279,7 @@ int pp_paged_attention(const pp_paged_kv* kv, const void* q, int64_t q_stride, c
     return PP_EINVAL;
   if (T == 0) return PP_OK;
   const int64_t D = kv->head_dim;
-  if (!q || !out || !scratch || q_stride < n_heads * D || (q_stride & 7) ||
-      q_stride >= (int64_t)1 << 38)
-    return PP_EINVAL;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(scratch, 256))
-    return PP_EINVAL;
+  if (!attention_ok(q, q_stride, out, lse, scratch, n_heads * D)) return PP_EINVAL;
   if (scratch_bytes < pp_paged_attention_scratch_bytes(kv, n_heads, T, max_q, window))
     return PP_E_NOSPACE;
   // a CTA's queries are read while others' outputs are written
@@ -289,6 +371,77 @@ int pp_paged_evict(const pp_paged_kv* kv, const int32_t* kv_len, int budget, int
   x.to_len = to_len;
   x.kept = kept;
   return rc(launch_paged_evict(a, x, (cudaStream_t)stream));
+}
+
+// ---- the cache in 8 bits
+
+int pp_packed_append(const pp_packed_kv* kv, const void* q, int64_t q_stride, const void* k,
+                     int64_t k_stride, const void* v, int64_t v_stride, int in_type,
+                     const float* q_alpha, const float* k_alpha, float eps, float rope_base,
+                     int rot_dim, int halves, const int32_t* positions, const int32_t* cu,
+                     const int32_t* kv_len, int T, int n_heads, void* q_out, uint32_t* status,
+                     void* stream) {
+  AppendArgs x{};
+  if (kv) {
+    x.k_scale = reinterpret_cast<uint8_t*>(kv->k_scale);
+    x.v_scale = reinterpret_cast<uint8_t*>(kv->v_scale);
+    x.scale_stride = kv->scale_stride;
+  }
+  return append(kv, q, q_stride, k, k_stride, v, v_stride, in_type, q_alpha, k_alpha, eps, rope_base,
+                rot_dim, halves, positions, cu, kv_len, T, n_heads, q_out, status, stream, x);
+}
+
+size_t pp_packed_attention_scratch_bytes(const pp_packed_kv* kv, int n_heads, int T, int max_q,
+                                         int window) {
+  const int32_t any = 0;
+  if (!cache_ok(kv) || !rows_ok(kv, &any, &any, T, n_heads) || !scores_ok(1.f, window, max_q))
+    return 0;
+  const Mirror m = mirror_of(kv);
+  const pp_paged_kv copy = mirror_cache(kv, m, reinterpret_cast<char*>(kv->k));
+  return m.bytes + pp_paged_attention_scratch_bytes(&copy, n_heads, T, max_q, window);
+}
+
+int pp_packed_attention(const pp_packed_kv* kv, const void* q, int64_t q_stride, const int32_t* cu,
+                        const int32_t* kv_len, int T, int max_q, int n_heads, float scale, int window,
+                        void* out, float* lse, uint32_t* status, void* scratch, size_t scratch_bytes,
+                        void* stream) {
+  if (!cache_ok(kv) || !rows_ok(kv, cu, kv_len, T, n_heads) || !scores_ok(scale, window, max_q))
+    return PP_EINVAL;
+  if (T == 0) return PP_OK;
+  const int64_t D = kv->head_dim;
+  if (!attention_ok(q, q_stride, out, lse, scratch, n_heads * D)) return PP_EINVAL;
+  if (scratch_bytes < pp_packed_attention_scratch_bytes(kv, n_heads, T, max_q, window))
+    return PP_E_NOSPACE;
+  if (rows_meet(q, q_stride * 2, n_heads * D * 2, T, out, T * n_heads * D * 2)) return PP_EINVAL;
+  const Mirror m = mirror_of(kv);
+  const pp_paged_kv copy = mirror_cache(kv, m, reinterpret_cast<char*>(scratch));
+  Args a = base_args(kv, kv_len, status);
+  a.cu = cu;
+  a.T = T;
+  a.window = effective_window(window);
+  ReadArgs x = read_args(kv, &copy);
+  x.mirror = 1;
+  const cudaError_t err = launch_packed_read(a, kv->type, x, (cudaStream_t)stream);
+  if (err != cudaSuccess) return PP_E_CUDA;
+  return pp_paged_attention(&copy, q, q_stride, cu, kv_len, T, max_q, n_heads, scale, window, out, lse,
+                            status, reinterpret_cast<char*>(scratch) + m.bytes,
+                            scratch_bytes - m.bytes, stream);
+}
+
+int pp_packed_read(const pp_packed_kv* kv, const int32_t* kv_len, const pp_paged_kv* to,
+                   uint32_t* status, void* stream) {
+  if (!cache_ok(kv) || !cache_ok(to) || !kv_len || !aligned(kv_len, 4)) return PP_EINVAL;
+  if (to->type != kv->type || to->head_dim != kv->head_dim || to->n_kv_heads != kv->n_kv_heads ||
+      to->n_seqs != kv->n_seqs)
+    return PP_EINVAL;
+  const int64_t codes = kv->n_pages * kv->page_stride, scales = kv->n_pages * kv->scale_stride;
+  const int64_t values = to->n_pages * to->page_stride * 2;
+  for (const void* t : {to->k, to->v})
+    if (meet(kv->k, codes, t, values) || meet(kv->v, codes, t, values) ||
+        meet(kv->k_scale, scales, t, values) || meet(kv->v_scale, scales, t, values))
+      return PP_EINVAL;
+  return rc(launch_packed_read(base_args(kv, kv_len, status), kv->type, read_args(kv, to),
+                               (cudaStream_t)stream));
 }
 
 }  // extern "C"

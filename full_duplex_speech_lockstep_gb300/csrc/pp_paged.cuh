@@ -557,6 +557,8 @@ struct AppendArgs {
   const int32_t* positions;
   void *q_out, *k_pages, *v_pages;
   float* mass;
+  uint8_t *k_scale, *v_scale;   // of a cache in 8 bits, else null
+  int64_t scale_stride;
 };
 struct Turns {
   uint64_t f[64];   // turns of each pair per position, as a fraction of 2^64
@@ -576,6 +578,26 @@ struct EvictArgs {
   int32_t *to_len, *kept;
 };
 cudaError_t launch_paged_evict(const Args& a, const EvictArgs& x, cudaStream_t s);
+
+// ---- the cache in 8 bits ---------------------------------------------------------------------
+// (Args::page_stride counts its bytes)
+struct Packed {
+  const uint8_t *k, *v, *k_scale, *v_scale;
+  int64_t scale_stride;
+};
+
+// Entries as 16-bit values into another cache's pages (k_packed_read.cu).
+struct ReadArgs {
+  Packed from;
+  void *to_k, *to_v;
+  float* to_mass;            // may be null
+  int32_t* to_table;
+  int64_t to_page_stride;    // elements
+  int to_n_pages, to_lps, to_table_ld;
+  int mirror;                // 1: `to` is a copy for an attention call: entries that its rows see, at
+                             // page b * table_ld + i for page i of sequence b, which to_table is told
+};
+cudaError_t launch_packed_read(const Args& a, int type, const ReadArgs& x, cudaStream_t s);
 
 }  // namespace paged
 }  // namespace pp

@@ -647,6 +647,89 @@ int pp_paged_evict(const pp_paged_kv* kv, const int32_t* kv_len, int budget, int
                    const pp_paged_kv* to, int32_t* to_len, int32_t* kept, uint32_t* status,
                    void* stream);
 
+/* ---- the paged cache in 8 bits ----------------------------------------------------------
+ * The same pages, sequences, rows and status bits as above, with entries of half the size: reading
+ * the cache is what a tick over long caches costs.  An entry of a key head (its key and its value
+ * alike) is head_dim e4m3 codes (4 exponent bits with a bias of 7, 3 mantissa bits) and one power of
+ * two for all of them:
+ *   a = max |y_d|;  e = the least whole number such that a 2^-e <= 448, at least -127;
+ *   code_d = y_d 2^-e rounded to e4m3 (nearest, ties to even);  scale byte = e + 127;
+ *   the entry reads as code_d 2^e, which bf16 holds exactly.
+ * With a = 0 the byte is 0.  An entry that holds a NaN or an infinity has codes 0 and the byte 255: it
+ * reads as NaN in every dim.  (A caller's own e4m3 NaN codes, 0x7f and 0xff, read as NaN too, in their
+ * dim or in the whole entry.)
+ * Weights by attention received and eviction work on 16-bit entries: pp_packed_read gives them. */
+typedef struct {
+  void* k;                 /* e4m3 codes: [n_pages] pages of [n_kv_heads][page_size][head_dim] bytes,
+                              16-byte aligned, page_stride bytes apart */
+  void* v;                 /* the same layout and stride */
+  void* k_scale;           /* scale bytes: [n_pages] pages of [n_kv_heads][page_size], 16-byte
+                              aligned, scale_stride bytes apart */
+  void* v_scale;           /* the same layout and stride */
+  const int32_t* table;    /* [n_seqs][table_ld], as in pp_paged_kv */
+  int64_t page_stride;     /* bytes, >= n_kv_heads * page_size * head_dim, multiple of 16 */
+  int64_t scale_stride;    /* bytes, >= n_kv_heads * page_size, multiple of 16 */
+  int32_t n_pages;
+  int32_t page_size, n_kv_heads, head_dim;   /* as in pp_paged_kv */
+  int32_t type;            /* PP_BF16 or PP_F16: queries and outputs */
+  int32_t n_seqs, table_ld;
+} pp_packed_kv;
+
+/* pp_paged_append into 8 bits: the same arguments, norm and rotation; keys after it, and values as they
+ * come, are held as above, of their fp32 results.  q_out stays in 16 bits.  Errors: PP_EINVAL, PP_E_CUDA. */
+int pp_packed_append(const pp_packed_kv* kv, const void* q, int64_t q_stride, const void* k,
+                     int64_t k_stride, const void* v, int64_t v_stride, int in_type,
+                     const float* q_alpha, const float* k_alpha, float eps, float rope_base,
+                     int rot_dim, int halves, const int32_t* positions, const int32_t* cu,
+                     const int32_t* kv_len, int T, int n_heads, void* q_out, uint32_t* status,
+                     void* stream);
+
+/* pp_paged_attention over 8-bit entries: the same arguments, masks and results, of what the entries read
+ * as.  Scratch: pp_packed_attention_scratch_bytes(...) bytes.
+ * Errors: PP_EINVAL, PP_E_NOSPACE, PP_E_CUDA. */
+size_t pp_packed_attention_scratch_bytes(const pp_packed_kv* kv, int n_heads, int T, int max_q,
+                                         int window);
+int pp_packed_attention(const pp_packed_kv* kv, const void* q, int64_t q_stride, const int32_t* cu,
+                        const int32_t* kv_len, int T, int max_q, int n_heads, float scale, int window,
+                        void* out, float* lse, uint32_t* status, void* scratch, size_t scratch_bytes,
+                        void* stream);
+
+/* What entries 0 .. kv_len - 1 of each sequence read as, into the same entries of `to`: a 16-bit cache
+ * of the same sequences, heads, head dim and type, of any page size.  Their mass (where to->mass is
+ * given) becomes 0.  An entry of a page outside either pool, or without a place in either table, is left
+ * as it was and raises PP_S_INDEX.  fp16 rounds what it cannot hold (values below 2^-14 to multiples of
+ * 2^-24, those from 65520 on to infinity).  `to` must not share memory with kv.
+ * Errors: PP_EINVAL, PP_E_CUDA. */
+int pp_packed_read(const pp_packed_kv* kv, const int32_t* kv_len, const pp_paged_kv* to,
+                   uint32_t* status, void* stream);
+
+/* ---- log probabilities of given tokens --------------------------------------------------------
+ * What a model made of tokens that it was given: personas and voice prompts are forced (mhpq, "Persona
+ * Voice 注入"), and their logits come out of pp_step like any other.  For each row of n logits x
+ *   lse = log sum_i exp(x_i);  logprob = x_token - lse;  entropy = -sum_i p_i log p_i, p = exp(x - lse);
+ *   the `top` largest logits: their tokens, the lower index first among equals, and x - lse.
+ * Logits that are not finite take no part: they have no probability, are no alternative and, as the
+ * token, give -infinity; NaN and +infinity raise PP_S_NAN.  A row without a finite logit gives -infinity
+ * and an entropy of 0.  Where a row has fewer than `top` finite logits the rest is -1 and -infinity.
+ *   logits     PP_F32, PP_BF16 or PP_F16 (type), device, aligned to one value: `rows` groups, ld values
+ *              apart, of `inner` rows, inner_ld values apart.  pp_step's codebook logits are such
+ *              groups: logits + text_vocab, ld = text_vocab + n_q * audio_card, inner = n_q,
+ *              inner_ld = n = audio_card
+ *   tokens     int32: of row i of group r at tokens[r * token_ld + i] (for pp_step's column: column + 1,
+ *              token_ld = 17); NULL with logprob NULL.  A negative token (padding, a closed slot) gives
+ *              0; so does one >= n, which raises PP_S_INDEX
+ *   logprob    f32 [rows][inner], or NULL
+ *   entropy    f32 [rows][inner], or NULL
+ *   top_tokens, top_logprobs   int32 and f32 [rows][inner][top]; either may be NULL
+ *   status     optional device word
+ * 0 <= top <= 64, inner >= 1, ld and inner_ld >= 0, 1 <= n <= 2^24, rows * inner < 2^28.  Sums are taken
+ * in fp32, in an order that n, `type` and the row's alignment set.  rows == 0 does nothing.  Asynchronous
+ * on `stream`; allocates nothing; may be captured.  Errors: PP_EINVAL, PP_E_CUDA. */
+int pp_token_logprobs(const void* logits, int type, int64_t ld, int rows, int inner, int64_t inner_ld,
+                      int n, const int32_t* tokens, int64_t token_ld, int top, float* logprob,
+                      float* entropy, int32_t* top_tokens, float* top_logprobs, uint32_t* status,
+                      void* stream);
+
 #ifdef __cplusplus
 }
 #endif
