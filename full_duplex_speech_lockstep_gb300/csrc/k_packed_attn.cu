@@ -1,0 +1,856 @@
+// k_packed_attn.cu - attention of single tokens and chunks of up to kPackedRows rows over the 8-bit paged
+// cache.  Rows, masks and results as in k_paged_attn.cu; K_j = 2^ek_j k_j and V_j = 2^ev_j v_j with e4m3
+// codes k_j, v_j.
+//
+// Codes go to the 5th-generation tensor cores as they lie: no value of the cache is converted.  The
+// other operands are sums of e4m3 numbers, which have 4 significant bits each, as more columns of the
+// product:
+//   q = 2^eq (q1 + q2/16 [+ q3/256])     two are exact for bf16's 8 bits, three for fp16's 11
+//   w = w1 + w2/16 + w3/256              12 bits; w is at most 256, so 2^-26 of that is its floor
+// Keys are the rows of both products, a thread of the softmax owns one key:
+//   S[j][r]  = k_j . q_r                 M = 128 keys, N = parts x R rows, K = D
+//   w[j][r]  = 2^(s_jr - m_r + 8) 2^(ev_j - E_r),   s_jr = S c 2^(ek_j + eq_r)
+//   O[d][r]  = sum_j v_jd w_jr           M = D dims, N = 3 x R rows, K = 128 keys
+// m_r is the tile's own maximum and E_r the largest ev that the row sees, so a tile depends on nothing before it; the
+// epilogue adds the tiles up in fp32, in order: acc = acc 2^(M - M') + O 2^(m + E_r - M').
+//
+// A work unit is (sequence, key head, split of its keys, row tile of up to R rows).  Each CTA takes a run
+// of consecutive units with about as many tiles as the others'; a sequence's splits depend on its own
+// lengths, the head counts and max_q only.  A unit that is not its rows' only one leaves (m, l, O) in
+// scratch and k_packed_join adds the splits up in split order.
+//
+//   warp 0       the units; K tiles and their scales
+//   warp 1       one thread issues every MMA: O of tile n - 2, then S of tile n
+//   warp 2       V tiles and their scales
+//   warp 3       the units' queries, as parts
+//   warps 4-7, 8-11   softmax of every second tile
+//   warps 12-15  epilogue: a thread owns one dim
+//
+// What no row of a unit sees must not reach the second product, where a weight of zero times a NaN
+// would be one: those rows of V are zeroed in shared memory.  An entry that only some rows see and
+// that holds a NaN code is zeroed too, and its scale taken for NaN, which only its seers' weights get.
+#include "pp_paged.cuh"
+#include "pp_tcgen05.cuh"
+
+namespace pp {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kReaders = 15;         // of the units: MMA issuer, V, queries, eight of softmax, epilogue
+constexpr int kParts = 3;            // of a weight
+constexpr float kTop = 8.f;          // a tile's largest weight is 2^8 (e4m3 holds up to 448)
+
+template <typename T, int D, int R>
+struct Cfg {
+  static constexpr int QP = sizeof(T) == 2 && Num<T>::kShift == 0.f ? 2 : 3;   // parts of a query
+  static constexpr int NQ = (QP * R + 15) / 16 * 16;                 // columns of S
+  static constexpr int NP = (kParts * R + 15) / 16 * 16;             // columns of O
+  static constexpr int kTileBytes = kTile * D;
+  static constexpr int S = D == 128 ? (R == 32 && QP == 3 ? 4 : 5) : 8;   // stages of K, and of V
+  static constexpr int kQBytes = NQ * 128;
+  static constexpr int kPBytes = NP / 16 * 2048;
+  static constexpr int kVOff = S * kTileBytes;
+  static constexpr int kQOff = 2 * S * kTileBytes;
+  static constexpr int kPOff = kQOff + 2 * kQBytes;
+  static constexpr int kScaleOff = kPOff + 2 * kPBytes;              // K's, then V's: 128 bytes a stage
+  static constexpr int kCtlOff = kScaleOff + 2 * S * kTile;
+};
+
+struct Ctl {
+  UnitRing ring;
+  uint64_t kfull[8], kempty[8], vfull[8], vempty[8], qfull[2], qempty[2];
+  uint64_t sfull[2], pfull[2], ofull[2], oempty[2], meet[2], done;
+  uint32_t bad[8];
+  uint32_t tmem;
+  int abort;
+  // of the two units in flight: each row's factor of its scores (to powers of two) and its entry
+  alignas(16) float row_c[2][32];
+  alignas(16) int row_at[2][32];
+  // of the two tiles in flight: maxima and sums of rows, and the largest V exponents that they see
+  alignas(16) float warp_max[2][4][32];
+  uint32_t warp_e[2][4][32];
+  alignas(16) float ref[2][4][32];     // each warp's copy of the references
+  int ref_e[2][4][32];
+  alignas(16) float m[2][32], l[2][4][32];
+  uint32_t e[2][32];
+  alignas(16) float keep[4][32], add[4][32];   // epilogue warps: factors of acc and of O
+};
+
+// ---- units -----------------------------------------------------------------------------------
+// Tokens that R consecutive rows (heads within tokens) touch, at most.
+__host__ __device__ __forceinline__ int row_span(int R, int G) { return (R - 1) / G + 2; }
+// Key tiles that a row tile can touch, at most.
+__host__ __device__ __forceinline__ int64_t most_tiles(int64_t entries, int window, int span) {
+  const int64_t all = (entries + kTile - 1) / kTile;
+  const int64_t seen = ((int64_t)window + span - 2) / kTile + 2;
+  return window && seen < all ? seen : all;
+}
+// Tiles of one split: `share` splits of each key head fill the SMs when a sequence is alone.  From four
+// (shorter units leave the pipeline between them idle) to eight (runs of units come out even), and at
+// most 128 splits.
+__host__ __device__ __forceinline__ int64_t split_tiles(int64_t tiles, int share) {
+  int64_t st = (tiles + share - 1) / share;
+  st = st < 4 ? 4 : st > 8 ? 8 : st;
+  const int64_t even = (tiles + 127) / 128;
+  return st > even ? st : even;
+}
+__host__ __device__ __forceinline__ int n_splits(int64_t tiles, int share) {
+  const int64_t st = split_tiles(tiles, share);
+  return tiles <= st ? 1 : (int)((tiles + st - 1) / st);
+}
+
+struct Shape {       // of a sequence's units
+  int rt, ns, st, cost;
+  // A chunk longer than the caller said is not split: scratch has no room for its parts.
+  __device__ __forceinline__ Shape(const Args& a, const Seq& s, int R, int max_q, int share) {
+    const int mt = (int)most_tiles(s.len, a.window, row_span(R, a.G));
+    rt = (int)(((int64_t)s.n * a.G + R - 1) / R);
+    ns = s.n > max_q ? 1 : n_splits(mt, share);
+    st = ns == 1 ? mt : (int)split_tiles(mt, share);
+    cost = st + 2;                     // a unit's ends cost as much as two tiles
+  }
+};
+
+struct Walk {
+  const Args& a;
+  const int64_t* pre;
+  const int R, max_q, share;
+  int64_t at, end;
+  int b, h, i;
+  Seq s;
+  int rt, ns, st, cost;
+
+  __device__ __forceinline__ Walk(const Args& a_, const int64_t* pre_, int R_, int max_q_, int share_)
+      : a(a_), pre(pre_), R(R_), max_q(max_q_), share(share_) {
+    const int64_t total = pre[a.n_seqs];
+    at = total * blockIdx.x / gridDim.x;
+    end = total * (blockIdx.x + 1) / gridDim.x;
+    if (at >= end) return;
+    b = find_seq(pre, a.n_seqs, at);
+    sequence();
+    const int64_t k = (at - pre[b] + cost - 1) / cost;   // the first unit that starts in the run
+    h = (int)(k / (rt * ns));
+    i = (int)(k - (int64_t)h * (rt * ns));
+    at = pre[b] + k * cost;
+    if (h == a.Hk) next_sequence();
+  }
+  __device__ __forceinline__ bool done() const { return at >= end; }
+  __device__ __forceinline__ void sequence() {
+    s = seq_of(a, b);
+    const Shape x(a, s, R, max_q, share);
+    rt = x.rt;
+    ns = x.ns;
+    st = x.st;
+    cost = x.cost;
+  }
+  __device__ __forceinline__ void next_sequence() {
+    h = i = 0;
+    do {
+      ++b;
+    } while (b < a.n_seqs && pre[b + 1] == pre[b]);
+    if (b < a.n_seqs) sequence();
+  }
+  __device__ __forceinline__ void next() {
+    at += cost;
+    if (++i == rt * ns) {
+      i = 0;
+      if (++h == a.Hk) next_sequence();
+    }
+  }
+  // Row tiles of a split follow each other: its keys are in L2 for the second.
+  __device__ __forceinline__ Unit unit() const {
+    Unit x;
+    const int split = i / rt, r0 = (i - split * rt) * R;
+    x.b = b;
+    x.h = h;
+    x.row = s.row0;
+    x.nt = min(R, s.n * a.G - r0);               // rows
+    x.first = s.total - s.n;                     // entry of the sequence's first new token
+    const int p0 = x.first + r0 / a.G, p1 = x.first + (r0 + x.nt - 1) / a.G;
+    x.stop = min(max(p1 + 1, 0), s.len);
+    x.low = a.window ? min(max(p0 - a.window + 1, 0), x.stop) : 0;
+    const int ta = x.low / kTile, tb = (x.stop + kTile - 1) / kTile;
+    x.tile0 = min(ta + split * st, tb);
+    x.tile1 = min(x.tile0 + st, tb);
+    x.split = split;
+    x.ns = ns;
+    x.tag = r0;
+    return x;
+  }
+};
+
+// ---- loads -----------------------------------------------------------------------------------
+// A tile of codes and its scales, by one warp, a lane to a page.  Pages without a place arrive as zeros,
+// their scales not at all: nobody looks at those.
+__device__ __forceinline__ void load_codes(const Args& a, const CUtensorMap* map, const uint8_t* scales,
+                                           int64_t scale_stride, uint32_t dst, uint32_t scale_dst,
+                                           uint32_t bar, const TilePages& x, int h, int j0, int lane,
+                                           volatile uint32_t* bad_out) {
+  const int per = min(1 << a.lps, kTile), pages = kTile / per;
+  const bool have = lane < pages && x.page < a.n_pages;
+  const int n = __popc(__ballot_sync(0xffffffffu, have));
+  if (lane == 0) {
+    if (bad_out) *bad_out = x.bad;
+    mbar_expect_tx(bar, (uint32_t)(kTile * a.D + n * per));
+  }
+  __syncwarp();
+  if (lane < pages) {
+    const int row = (j0 + lane * per) & ((1 << a.lps) - 1);
+    tma_load_4d(dst + lane * per * a.D, map, 0, row, h, x.page, bar);
+    if (have)
+      bulk_load(scale_dst + lane * per, scales + x.page * scale_stride + ((int64_t)h << a.lps) + row,
+                (uint32_t)per, bar);
+  }
+}
+
+// ---- products --------------------------------------------------------------------------------
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+}
+// Matrix descriptor: leading and stride offsets in bytes; layout 2: 128-byte swizzle, 4: 64-byte, 0: none
+__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t layout) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)(lead >> 4) << 16 |
+         (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)layout << 61;
+}
+
+// ---- numbers ---------------------------------------------------------------------------------
+// Two values as e4m3 (nearest; the first one in the lower byte), and what they stand for
+__device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Four values as `P` words of four codes: each part is what the ones before left, sixteen times
+template <int P>
+__device__ __forceinline__ void split4(float (&x)[4], uint32_t (&w)[P]) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const uint32_t a = to_e4m3(x[0], x[1]), b = to_e4m3(x[2], x[3]);
+    w[p] = a | b << 16;
+    if (p + 1 == P) break;
+    const float2 ya = from_e4m3(a), yb = from_e4m3(b);
+    x[0] = (x[0] - ya.x) * 16.f;
+    x[1] = (x[1] - ya.y) * 16.f;
+    x[2] = (x[2] - yb.x) * 16.f;
+    x[3] = (x[3] - yb.y) * 16.f;
+  }
+}
+// 2^(byte - 127), NaN for 255
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7fc00000u : byte == 0u ? 0x00400000u : byte << 23);
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_packed_attn(const __grid_constant__ Args a, const int max_q, const int share, const int ns_cap,
+                  const __grid_constant__ AttnOut o, const __grid_constant__ Packed kv,
+                  const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                  const T* q, const int64_t q_stride) {
+  using C = Cfg<T, D, R>;
+  constexpr int S = C::S;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // (an offset, not a rounded pointer: the compiler then knows that it is shared memory)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::kCtlOff);
+  int64_t* pre = reinterpret_cast<int64_t*>(ctl + 1);
+  volatile int* abort_flag = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&ctl->kfull[i]), 1);
+      mbar_init(smem_u32(&ctl->kempty[i]), 5);          // the first product, four warps of softmax
+      mbar_init(smem_u32(&ctl->vfull[i]), i == 0 ? 1 + a.withhold : 1);
+      mbar_init(smem_u32(&ctl->vempty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl->qfull[i]), 1);
+      mbar_init(smem_u32(&ctl->qempty[i]), 9);          // the first product, eight warps of softmax
+      mbar_init(smem_u32(&ctl->sfull[i]), 1);
+      mbar_init(smem_u32(&ctl->pfull[i]), 4);
+      mbar_init(smem_u32(&ctl->ofull[i]), 1);
+      mbar_init(smem_u32(&ctl->oempty[i]), 4);
+      mbar_init(smem_u32(&ctl->meet[i]), 4);
+    }
+    mbar_init(smem_u32(&ctl->done), 1);
+    ring_init(ctl->ring, kReaders);
+    ctl->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&ctl->tmem)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  pdl_wait_and_trigger();
+  pdl_trigger();
+  prefix_units(a, pre, [&](int b) -> int64_t {
+    const Seq s = seq_of(a, b);
+    if (s.n == 0) return 0;
+    check_len(a, s);
+    const Shape x(a, s, R, max_q, share);
+    return (int64_t)a.Hk * x.rt * x.ns * x.cost;
+  });
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  // S of the even and odd tiles, then O
+  const uint32_t tmem = ctl->tmem;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
+
+  if (warp == 0) {
+    // ---- units, K tiles -------------------------------------------------------------------
+    uint32_t n = 0, nu = 0, seen_bad = 0;
+    Walk walk(a, pre, R, max_q, share);
+#pragma unroll 1
+    for (; !walk.done() && !*abort_flag; walk.next()) {
+      const Unit x = walk.unit();
+      put_unit(a, ctl->ring, nu++, x, lane, abort_flag);
+      if (x.tile0 == x.tile1) continue;
+      const bool past = x.first + (x.tag + x.nt - 1) / a.G >= x.stop;
+      TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, past, lane);
+#pragma unroll 1
+      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+        const int i = n % S;
+        const TilePages now = next;
+        if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, past, lane);
+        if (n >= S) wait(&ctl->kempty[i], (n / S - 1) & 1);
+        if (*abort_flag) break;
+        load_codes(a, &mapK, kv.k_scale, kv.scale_stride, smem_u32(smem + i * C::kTileBytes),
+                   smem_u32(smem + C::kScaleOff + i * kTile), smem_u32(&ctl->kfull[i]), now, x.h,
+                   t * kTile, lane, &ctl->bad[i]);
+        seen_bad |= now.bad;
+      }
+    }
+    Unit last{};
+    last.b = -1;
+    put_unit(a, ctl->ring, nu, last, lane, abort_flag);
+    if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
+    // every copy lands before the CTA may exit (bounded waits)
+    if (lane == 0) {
+#pragma unroll 1
+      for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &ctl->kfull[i % S], (i / S) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- MMA issuer -----------------------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t id = (1u << 4) | ((uint32_t)(kTile >> 4) << 24);   // fp32 of e4m3, M = 128
+      constexpr uint32_t id_s = id | ((uint32_t)(C::NQ >> 3) << 17);
+      constexpr uint32_t id_o = id | ((uint32_t)(C::NP >> 3) << 17) | (1u << 15) | (1u << 16);
+      constexpr uint32_t kRow = D == 128 ? 2 : 4;       // the tiles' layout: rows of D bytes, swizzled
+      uint32_t n = 0, nq = 0;
+      auto values = [&](uint32_t m) {
+        const uint32_t g = m & 1, i = m % S;
+        wait(&ctl->pfull[g], (m >> 1) & 1);
+        wait(&ctl->vfull[i], (m / S) & 1);
+        if (*abort_flag) return;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t vb = smem_u32(smem + C::kVOff + i * C::kTileBytes);
+        const uint32_t pb = smem_u32(smem + C::kPOff + g * C::kPBytes);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 32; ++kk)
+          // V: dims contiguous, 8 keys to an atom of 8 D bytes (with 64 dims rows 64-127 of the product
+          // are the keys 8 further on, and nobody reads them).  Weights: 16 columns of 8 keys to 128
+          // bytes, keys following each other, the next columns 2048 bytes on.
+          umma_e4m3(tmem + 256 + g * 128, desc(vb + kk * 32 * D, 512, 8 * D, kRow),
+                    desc(pb + kk * 512, 128, 2048, 0), id_o, kk > 0);
+        umma_commit(smem_u32(&ctl->ofull[g]));
+        umma_commit(smem_u32(&ctl->vempty[i]));
+      };
+      Unit x;
+#pragma unroll 1
+      for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, true, abort_flag); ++nu) {
+        if (x.tile0 == x.tile1) continue;
+        const uint32_t qb = nq & 1;
+#pragma unroll 1
+        for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+          const uint32_t g = n & 1, i = n % S;
+          if (n >= 2) values(n - 2);                    // (also: S of n - 2 has been read)
+          if (t == x.tile0) wait(&ctl->qfull[qb], (nq >> 1) & 1);
+          wait(&ctl->kfull[i], (n / S) & 1);
+          if (*abort_flag) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t kb = smem_u32(smem + i * C::kTileBytes);
+          const uint32_t qo = smem_u32(smem + C::kQOff + qb * C::kQBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            umma_e4m3(tmem + g * 128, desc(kb + kk * 32, 0, 8 * D, kRow),
+                      desc(qo + kk * 32, 0, 1024, 2), id_s, kk > 0);
+          umma_commit(smem_u32(&ctl->sfull[g]));
+          umma_commit(smem_u32(&ctl->kempty[i]));
+        }
+        if (*abort_flag) break;
+        umma_commit(smem_u32(&ctl->qempty[qb]));
+        ++nq;
+      }
+      if (n >= 2 && !*abort_flag) values(n - 2);
+      if (n >= 1 && !*abort_flag) values(n - 1);
+      // every MMA is done before tensor memory is given back (bounded wait)
+      umma_commit(smem_u32(&ctl->done));
+      drain_phase(a, &ctl->done, 0);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---- V tiles --------------------------------------------------------------------------
+    uint32_t n = 0;
+    Unit x;
+#pragma unroll 1
+    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+      if (x.tile0 == x.tile1) continue;
+      const bool past = x.first + (x.tag + x.nt - 1) / a.G >= x.stop;
+      TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, past, lane);
+#pragma unroll 1
+      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+        const int i = n % S;
+        const TilePages now = next;
+        if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, past, lane);
+        if (n >= S) wait(&ctl->vempty[i], (n / S - 1) & 1);
+        if (*abort_flag) break;
+        load_codes(a, &mapV, kv.v_scale, kv.scale_stride, smem_u32(smem + C::kVOff + i * C::kTileBytes),
+                   smem_u32(smem + C::kScaleOff + (S + i) * kTile), smem_u32(&ctl->vfull[i]), now, x.h,
+                   t * kTile, lane, nullptr);
+      }
+    }
+    if (lane == 0) {
+#pragma unroll 1
+      for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &ctl->vfull[i % S], (i / S) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ---- queries: L lanes to a row, four dims to a lane -----------------------------------
+    constexpr int L = D / 4, kSide = 32 / L, kAhead = 4;   // rows side by side; passes loaded at once
+    const int l = lane % L, side = lane / L;
+    uint32_t nq = 0;
+    Unit x;
+#pragma unroll 1
+    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+      if (x.tile0 == x.tile1) continue;
+      const uint32_t qb = nq & 1;
+      if (nq >= 2) wait(&ctl->qempty[qb], ((nq >> 1) - 1) & 1);
+      if (*abort_flag) break;
+      uint8_t* to = smem + C::kQOff + qb * C::kQBytes;
+#pragma unroll 1
+      for (int r0 = 0; r0 < R; r0 += kSide * kAhead) {
+        uint2 raw[kAhead];
+        int at[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int r = r0 + k * kSide + side, f = x.tag + r, t = f / a.G;
+          at[k] = x.first + t;
+          raw[k] = make_uint2(0u, 0u);
+          if (r < x.nt)
+            raw[k] = *reinterpret_cast<const uint2*>(q + (int64_t)(x.row + t) * q_stride +
+                                                     (int64_t)(x.h * a.G + f - t * a.G) * D + l * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int r = r0 + k * kSide + side;
+          float y[4] = {Num<T>::to_float(raw[k].x & 0xffffu), Num<T>::to_float(raw[k].x >> 16),
+                        Num<T>::to_float(raw[k].y & 0xffffu), Num<T>::to_float(raw[k].y >> 16)};
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+#pragma unroll
+          for (int w = L / 2; w > 0; w >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, w));
+          // the row's power of two, as a cache entry's; a row that is not finite has NaN scores
+          const bool wild = top >= 0x7f800000u;
+          const int byte =
+              max((int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
+          const float f = wild ? 0.f : __uint_as_float((254u - (uint32_t)byte) << 23);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = wild ? 0.f : y[e] * f;
+          uint32_t w[C::QP];
+          split4<C::QP>(y, w);
+#pragma unroll
+          for (int p = 0; p < C::QP; ++p) {
+            const int n = p * R + r;
+            *reinterpret_cast<uint32_t*>(to + n * 128 + (((l >> 2) ^ (n & 7)) << 4) + (l & 3) * 4) =
+                w[p];
+          }
+          if (l == 0) {
+            ctl->row_c[qb][r] = wild ? __uint_as_float(0x7fc00000u) : a.c * scale_of((uint32_t)byte);
+            ctl->row_at[qb][r] = at[k];
+          }
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->qfull[qb]));
+      ++nq;
+    }
+  } else if (warp < 12) {
+    // ---- softmax: thread k of a group owns key k of the group's tiles ---------------------
+    const uint32_t g = warp >= 8;
+    const int wq = warp & 3, key = wq * 32 + lane;
+    const uint32_t lane_at = tmem + ((uint32_t)(wq * 32) << 16);
+    uint32_t n = 0, nq = 0, meets = 0;
+    Unit x;
+#pragma unroll 1
+    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+      if (x.tile0 == x.tile1) continue;
+      const uint32_t qb = nq & 1;
+      wait(&ctl->qfull[qb], (nq >> 1) & 1);
+      const int p0 = x.first + x.tag / a.G, p1 = x.first + (x.tag + x.nt - 1) / a.G;
+#pragma unroll 1
+      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+        if ((n & 1) != g) continue;
+        if (*abort_flag) break;
+        const int i = n % S, j = t * kTile + key;
+        const uint32_t ph = (n >> 1) & 1;
+        wait(&ctl->sfull[g], ph);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        // (the first product has seen this phase of K, and the next one waits for this warp)
+        wait(&ctl->kfull[i], (n / S) & 1);
+        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&ctl->bad[i]);
+        const float kf = scale_of(smem[C::kScaleOff + i * kTile + key]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->kempty[i]));
+        // does every row see every key of the tile?
+        const bool edge = bad != 0 || t * kTile + kTile - 1 > min(p0, x.stop - 1) ||
+                          (a.window && t * kTile <= p1 - a.window);
+        const bool live = !edge || (j < x.stop && j >= x.low && !((bad >> (key >> 4)) & 1u));
+        // ---- scores and the tile's maxima
+        float v[R];
+        float mine = 0.f;                                // lane r: row r's
+#pragma unroll
+        for (int c = 0; c < R; c += 8) {
+          uint32_t s[C::QP][8];
+#pragma unroll
+          for (int p = 0; p < C::QP; ++p) tmem_ld8(lane_at + g * 128 + p * R + c, s[p]);
+          tmem_wait_ld();
+          float f[8];
+          *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&ctl->row_c[qb][c]);
+          *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&ctl->row_c[qb][c + 4]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float y = after_wait(s[C::QP - 1][e]);
+#pragma unroll
+            for (int p = C::QP - 2; p >= 0; --p) y = fmaf(y, 0.0625f, after_wait(s[p][e]));
+            v[c + e] = y * kf * f[e];
+          }
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int at = ctl->row_at[qb][c + e];
+              if (!live || j > at || (a.window && j <= at - a.window)) v[c + e] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float top = warp_max(v[c + e]);
+            if (lane == c + e) mine = top;
+          }
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        // ---- what V brings: its scale, and rows that must not be multiplied
+        const int vi = n % S;
+        wait(&ctl->vfull[vi], (n / S) & 1);
+        uint32_t ev = smem[C::kScaleOff + (S + vi) * kTile + key];
+        bool nan_value = ev == 255u;
+        if (edge && !(live && j <= p0 && (!a.window || j > p1 - a.window))) {
+          uint4* row = reinterpret_cast<uint4*>(smem + C::kVOff + vi * C::kTileBytes + key * D);
+          bool clear = !live;
+          if (live) {
+            uint32_t z = 0;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint4 w = row[k];
+              z |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
+                   ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+            }
+            clear = (z & 0x80808080u) != 0;
+            nan_value |= clear;
+          }
+          if (clear) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) row[k] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        // (each row goes by the exponents that it sees: another's could take its weights below e4m3)
+        const uint32_t own_e = ev == 255u ? 0u : ev;
+        uint32_t top_e;
+        if (edge) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const uint32_t y = __reduce_max_sync(0xffffffffu, v[r] == -INFINITY ? 0u : own_e);
+            if (lane == r) top_e = y;
+          }
+        } else {
+          top_e = __reduce_max_sync(0xffffffffu, own_e);
+        }
+        if (lane < R) {
+          ctl->warp_max[g][wq][lane] = mine;
+          ctl->warp_e[g][wq][lane] = top_e;
+        }
+        sync_warps(a, &ctl->meet[g], meets, lane, abort_flag);
+        // lane r works row r's reference out for its warp
+        float top = -INFINITY;
+        uint32_t E = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (lane >= R) break;
+          top = fmaxf(top, ctl->warp_max[g][w][lane]);
+          E = max(E, ctl->warp_e[g][w][lane]);
+        }
+        const float ref = top == -INFINITY ? 0.f : top - kTop;
+        if (lane < R) {
+          ctl->ref[g][wq][lane] = ref;
+          ctl->ref_e[g][wq][lane] = (int)E;
+        }
+        // the last tile's weights and sums of this buffer have been used
+        if (n >= 2) wait(&ctl->oempty[g], ((n >> 1) - 1) & 1);
+        if (wq == 0) {
+          if (lane < R) {
+            ctl->m[g][lane] = top == -INFINITY ? -INFINITY : ref;
+            ctl->e[g][lane] = E;
+          }
+        }
+        __syncwarp();
+        // 2^(ev - E), for every row alike where all see all
+        auto value_factor = [&](int E_) {
+          const int de = (int)ev - E_;
+          return nan_value ? __uint_as_float(0x7fc00000u)
+                           : de <= -127 ? 0.f : __uint_as_float((uint32_t)(127 + de) << 23);
+        };
+        const float vf = value_factor((int)__shfl_sync(0xffffffffu, E, 0));
+        // ---- weights, eight rows at a time
+        uint8_t* pt = smem + C::kPOff + g * C::kPBytes + key * 16;
+#pragma unroll
+        for (int c = 0; c < R; c += 8) {
+          float f[8], p[8];
+          *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&ctl->ref[g][wq][c]);
+          *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&ctl->ref[g][wq][c + 4]);
+          uint32_t w[2][kParts];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float s = v[c + half * 4 + e];
+              p[half * 4 + e] = exp2_approx(s - f[half * 4 + e]);
+              if (!edge)
+                y[e] = p[half * 4 + e] * vf;
+              else if (s == -INFINITY)
+                y[e] = 0.f;                              // (not a NaN of a value that it does not see)
+              else
+                y[e] = p[half * 4 + e] * value_factor(ctl->ref_e[g][wq][c + half * 4 + e]);
+            }
+            split4<kParts>(y, w[half]);
+          }
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) {
+            const int col = k * R + c;
+            *reinterpret_cast<uint2*>(pt + (col >> 4) * 2048 + (col & 15)) = make_uint2(w[0][k], w[1][k]);
+          }
+          // sums of the eight rows over the warp's keys: lanes halve the rows, then the keys
+#pragma unroll
+          for (int k = 4, d = 16; k > 0; k >>= 1, d >>= 1) {
+#pragma unroll
+            for (int e = 0; e < k; ++e) {
+              const bool up = lane & d;
+              const float give = up ? p[e] : p[e + k];
+              p[e] = (up ? p[e + k] : p[e]) + __shfl_xor_sync(0xffffffffu, give, d);
+            }
+          }
+          p[0] += __shfl_xor_sync(0xffffffffu, p[0], 2);
+          p[0] += __shfl_xor_sync(0xffffffffu, p[0], 1);
+          if ((lane & 3) == 0) ctl->l[g][wq][c + (lane >> 2 & 1) + (lane >> 3 & 1) * 2 + (lane >> 4) * 4] = p[0];
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->pfull[g]));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->qempty[qb]));
+      ++nq;
+    }
+  } else {
+    // ---- epilogue: thread d owns dim d; lane r of each warp keeps row r's maximum and sum ---
+    const int wq = warp & 3, d = wq * 32 + lane, H = a.Hk * a.G;
+    const uint32_t lane_at = tmem + ((uint32_t)(wq * 32) << 16) + 256;
+    uint32_t n = 0;
+    Unit x;
+#pragma unroll 1
+    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+      float acc[R], M = -INFINITY, Lsum = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r] = 0.f;
+#pragma unroll 1
+      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+        const uint32_t g = n & 1, ph = (n >> 1) & 1;
+        wait(&ctl->pfull[g], ph);                        // sums and maxima
+        if (lane < R) {
+          const float m = ctl->m[g][lane];
+          const float l = (ctl->l[g][0][lane] + ctl->l[g][1][lane]) +
+                          (ctl->l[g][2][lane] + ctl->l[g][3][lane]);
+          const float top = fmaxf(M, m);
+          // (a side without a reference has nothing, or NaN, which passes)
+          const float keep = M == -INFINITY ? 0.f : exp2_approx(M - top);
+          const float add = m == -INFINITY ? 0.f : exp2_approx(m - top);
+          Lsum = Lsum * keep + l * add;
+          M = top;
+          ctl->keep[wq][lane] = keep;
+          ctl->add[wq][lane] = add * scale_of(ctl->e[g][lane]);
+        }
+        __syncwarp();
+        wait(&ctl->ofull[g], ph);
+        if (*abort_flag) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < R; c += 8) {
+          uint32_t y[kParts][8];
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) tmem_ld8(lane_at + g * 128 + p * R + c, y[p]);
+          tmem_wait_ld();
+          float keep[8], add[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            *reinterpret_cast<float4*>(keep + e) = *reinterpret_cast<const float4*>(&ctl->keep[wq][c + e]);
+            *reinterpret_cast<float4*>(add + e) = *reinterpret_cast<const float4*>(&ctl->add[wq][c + e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float z = fmaf(fmaf(after_wait(y[2][e]), 0.0625f, after_wait(y[1][e])), 0.0625f,
+                                 after_wait(y[0][e]));
+            acc[c + e] = fmaf(acc[c + e], keep[e], z * add[e]);
+          }
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->oempty[g]));
+      }
+      if (*abort_flag) break;
+      // lane r: where row r goes
+      const int f = x.tag + min(lane, x.nt - 1), tk = f / a.G, hd = x.h * a.G + f - tk * a.G;
+      const int64_t row = (int64_t)(x.row + tk) * H + hd;
+      const int64_t rec = (((int64_t)x.b * max_q + tk) * H + hd) * ns_cap + x.split;
+      const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+      if (wq == 0 && lane < x.nt) {
+        if (x.ns > 1)
+          o.part_ml[rec] = make_float2(M, Lsum);
+        else if (o.lse)
+          o.lse[row] = Lsum == 0.f ? -INFINITY : (M + log2f(Lsum)) * kLn2;
+      }
+      const int64_t place = x.ns > 1 ? rec : row;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= x.nt) break;
+        const int64_t to = __shfl_sync(0xffffffffu, place, r) * D + d;
+        const float scale = __shfl_sync(0xffffffffu, inv, r);
+        if (d >= D) continue;
+        if (x.ns > 1)
+          o.part[to] = acc[r];
+        else
+          reinterpret_cast<uint16_t*>(o.out)[to] = (uint16_t)Num<T>::pack(acc[r] * scale, 0.f);
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+// Join the splits of each row, in split order: one warp to a (token, head).
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+    k_packed_join(const __grid_constant__ Args a, const int R, const int max_q, const int share,
+                  const int ns_cap, const __grid_constant__ AttnOut o) {
+  pdl_wait_and_trigger();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, H = a.Hk * a.G;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);   // (sequence, token, head)
+  const int64_t rest = id / H;
+  const int hd = (int)(id - rest * H), b = (int)(rest / max_q), tk = (int)(rest - (int64_t)b * max_q);
+  if (b >= a.n_seqs) return;
+  const Seq s = seq_of(a, b);
+  if (s.n > max_q || tk >= s.n) return;
+  const int ns = n_splits(most_tiles(s.len, a.window, row_span(R, a.G)), share);
+  if (ns == 1) return;
+  const int64_t row = (int64_t)(s.row0 + tk) * H + hd;
+  join_row<T, D>(o.part, o.part_ml, id * ns_cap, ns, reinterpret_cast<T*>(o.out) + row * D,
+                 o.lse ? o.lse + row : nullptr, lane);
+}
+
+template <typename T, int D, int R>
+cudaError_t run(const Args& a, const PackedPlan& p, const Maps& maps, const AttnOut& o, const Packed& kv,
+                const void* q, int64_t q_stride, cudaStream_t s) {
+  using C = Cfg<T, D, R>;
+  static_assert(C::kQBytes % 1024 == 0 && C::kPBytes % 1024 == 0 && C::NQ <= 128 && C::NP <= 128,
+                "operands start on 1024 bytes, products fit their columns");
+  const size_t smem = C::kCtlOff + sizeof(Ctl) + (size_t)(a.n_seqs + 1) * sizeof(int64_t) + 1024;
+  constexpr size_t most_smem = C::kCtlOff + sizeof(Ctl) + (kMaxSeqs + 1) * sizeof(int64_t) + 1024;
+  static_assert(most_smem <= 227 * 1024, "attention shared memory");
+  static std::atomic<uint64_t> done{0};
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(k_packed_attn<T, D, R>), most_smem, done);
+  if (err != cudaSuccess) return err;
+  // no more CTAs than units there can be
+  const int64_t row_tiles = (int64_t)a.T * a.G / R + a.n_seqs;
+  const int64_t most = row_tiles * a.Hk * p.ns_cap;
+  const int nsm = sm_count();
+  err = launch(k_packed_attn<T, D, R>, dim3((unsigned)(most < nsm ? most : nsm)), kThreads, smem, s, a,
+               p.max_q, p.share, p.ns_cap, o, kv, maps.k, maps.v, reinterpret_cast<const T*>(q), q_stride);
+  if (err != cudaSuccess || p.ns_cap == 1) return err;
+  const int64_t rows = (int64_t)a.n_seqs * p.max_q * a.Hk * a.G;
+  return launch(k_packed_join<T, D>, dim3((unsigned)((rows + 3) / 4)), 128, 0, s, a, R, p.max_q, p.share,
+                p.ns_cap, o);
+}
+
+template <typename T, int D>
+cudaError_t pick(const Args& a, const PackedPlan& p, const Maps& maps, const AttnOut& o,
+                 const Packed& kv, const void* q, int64_t q_stride, cudaStream_t s) {
+  return p.R == 8    ? run<T, D, 8>(a, p, maps, o, kv, q, q_stride, s)
+         : p.R == 16 ? run<T, D, 16>(a, p, maps, o, kv, q, q_stride, s)
+                     : run<T, D, 32>(a, p, maps, o, kv, q, q_stride, s);
+}
+
+}  // namespace
+
+PackedPlan packed_plan(const Args& a, int max_q) {
+  PackedPlan p{};
+  const int rows = max_q * a.G;
+  p.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  p.max_q = max_q;
+  const int heads = a.Hk * ((rows + p.R - 1) / p.R);
+  p.share = kSms / heads < 1 ? 1 : kSms / heads;
+  const int64_t tiles = most_tiles((int64_t)a.table_ld << a.lps, a.window, row_span(p.R, a.G));
+  // shorter sequences have splits of four tiles or more each, `share` of them or one for every eight tiles
+  int64_t most = (tiles + 3) / 4;
+  const int64_t by_share = p.share > (tiles + 7) / 8 ? p.share : (tiles + 7) / 8;
+  if (by_share < most) most = by_share;
+  p.ns_cap = (int)(most < 1 ? 1 : most < 128 ? most : 128);
+  const size_t recs = (size_t)a.n_seqs * max_q * a.Hk * a.G * p.ns_cap;
+  p.rec_bytes = p.ns_cap == 1 ? 0 : (recs * a.D * sizeof(float) + 255) & ~(size_t)255;
+  p.ml_bytes = p.ns_cap == 1 ? 0 : (recs * sizeof(float2) + 255) & ~(size_t)255;
+  return p;
+}
+
+cudaError_t launch_packed_attn(const Args& a, int type, const PackedPlan& plan, const Maps& maps,
+                               const AttnOut& o, const Packed& kv, const void* q, int64_t q_stride,
+                               cudaStream_t s) {
+  if (type == PP_BF16)
+    return a.D == 128 ? pick<__nv_bfloat16, 128>(a, plan, maps, o, kv, q, q_stride, s)
+                      : pick<__nv_bfloat16, 64>(a, plan, maps, o, kv, q, q_stride, s);
+  return a.D == 128 ? pick<__half, 128>(a, plan, maps, o, kv, q, q_stride, s)
+                    : pick<__half, 64>(a, plan, maps, o, kv, q, q_stride, s);
+}
+
+}  // namespace paged
+}  // namespace pp

@@ -97,31 +97,42 @@ bool scores_ok(float scale, int window, int max_q) {
 // Pages as [page][head][row][dim], box 64 dims x one page or one key tile, and queries as
 // [token][head][dim], box 64 dims x the G heads of a key head x the tokens of a row tile.  PP_E_CUDA
 // where there is no driver to encode them.
-int encode(CUtensorMap* m, int type, const void* base, const cuuint64_t dim[4],
-           const cuuint64_t stride[3], const cuuint32_t box[4]) {
+int encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t dim[4],
+           const cuuint64_t stride[3], const cuuint32_t box[4],
+           CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return PP_E_CUDA;
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  const CUresult r = fn(
-      m, type == PP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-      const_cast<void*>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r =
+      fn(m, type, 4, const_cast<void*>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PP_OK : PP_EINVAL;
+}
+CUtensorMapDataType map_type(int type) {
+  return type == PP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 int page_map(CUtensorMap* m, const pp_paged_kv* kv, const void* base) {
   const cuuint64_t D = kv->head_dim, P = kv->page_size;
   const cuuint64_t dim[4] = {D, P, (cuuint64_t)kv->n_kv_heads, (cuuint64_t)kv->n_pages};
   const cuuint64_t stride[3] = {D * 2, P * D * 2, (cuuint64_t)kv->page_stride * 2};
   const cuuint32_t box[4] = {64, (cuuint32_t)(P < kTile ? P : kTile), 1, 1};
-  return encode(m, kv->type, base, dim, stride, box);
+  return encode(m, map_type(kv->type), base, dim, stride, box);
+}
+// Codes: box all dims x one page or one key tile.
+int page_map(CUtensorMap* m, const pp_packed_kv* kv, const void* base) {
+  const cuuint64_t D = kv->head_dim, P = kv->page_size;
+  const cuuint64_t dim[4] = {D, P, (cuuint64_t)kv->n_kv_heads, (cuuint64_t)kv->n_pages};
+  const cuuint64_t stride[3] = {D, P * D, (cuuint64_t)kv->page_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(P < kTile ? P : kTile), 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, dim, stride, box,
+                D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 int query_map(CUtensorMap* m, const Args& a, int type, const void* q, int64_t stride_q, int tp) {
   const cuuint64_t D = a.D, H = (cuuint64_t)a.Hk * a.G;
   const cuuint64_t dim[4] = {D, H, (cuuint64_t)a.T, 1};
   const cuuint64_t stride[3] = {D * 2, (cuuint64_t)stride_q * 2, (cuuint64_t)stride_q * 2};
   const cuuint32_t box[4] = {64, (cuuint32_t)a.G, (cuuint32_t)tp, 1};
-  return encode(m, type, q, dim, stride, box);
+  return encode(m, map_type(type), q, dim, stride, box);
 }
 
 // Do T rows of `len` bytes, `stride` >= len bytes apart, meet the `n` bytes from `at`?
@@ -169,11 +180,14 @@ pp_paged_kv mirror_cache(const pp_packed_kv* kv, const Mirror& m, char* scratch)
   to.table_ld = kv->table_ld;
   return to;
 }
+Packed packed_of(const pp_packed_kv* kv) {
+  return Packed{reinterpret_cast<const uint8_t*>(kv->k), reinterpret_cast<const uint8_t*>(kv->v),
+                reinterpret_cast<const uint8_t*>(kv->k_scale),
+                reinterpret_cast<const uint8_t*>(kv->v_scale), kv->scale_stride};
+}
 ReadArgs read_args(const pp_packed_kv* kv, const pp_paged_kv* to) {
   ReadArgs x{};
-  x.from = Packed{reinterpret_cast<const uint8_t*>(kv->k), reinterpret_cast<const uint8_t*>(kv->v),
-                  reinterpret_cast<const uint8_t*>(kv->k_scale),
-                  reinterpret_cast<const uint8_t*>(kv->v_scale), kv->scale_stride};
+  x.from = packed_of(kv);
   x.to_k = to->k;
   x.to_v = to->v;
   x.to_mass = to->mass;
@@ -396,6 +410,13 @@ size_t pp_packed_attention_scratch_bytes(const pp_packed_kv* kv, int n_heads, in
   const int32_t any = 0;
   if (!cache_ok(kv) || !rows_ok(kv, &any, &any, T, n_heads) || !scores_ok(1.f, window, max_q))
     return 0;
+  Args a = base_args(kv, nullptr, nullptr);
+  a.G = n_heads / kv->n_kv_heads;
+  a.window = effective_window(window);
+  if ((int64_t)max_q * a.G <= kPackedRows) {
+    const PackedPlan p = packed_plan(a, max_q);
+    return p.rec_bytes + p.ml_bytes + 256;
+  }
   const Mirror m = mirror_of(kv);
   const pp_paged_kv copy = mirror_cache(kv, m, reinterpret_cast<char*>(kv->k));
   return m.bytes + pp_paged_attention_scratch_bytes(&copy, n_heads, T, max_q, window);
@@ -413,12 +434,27 @@ int pp_packed_attention(const pp_packed_kv* kv, const void* q, int64_t q_stride,
   if (scratch_bytes < pp_packed_attention_scratch_bytes(kv, n_heads, T, max_q, window))
     return PP_E_NOSPACE;
   if (rows_meet(q, q_stride * 2, n_heads * D * 2, T, out, T * n_heads * D * 2)) return PP_EINVAL;
-  const Mirror m = mirror_of(kv);
-  const pp_paged_kv copy = mirror_cache(kv, m, reinterpret_cast<char*>(scratch));
   Args a = base_args(kv, kv_len, status);
   a.cu = cu;
   a.T = T;
+  a.G = n_heads / kv->n_kv_heads;
   a.window = effective_window(window);
+  a.c = scale * kLog2e;
+  if ((int64_t)max_q * a.G <= kPackedRows) {
+    const PackedPlan p = packed_plan(a, max_q);
+    Maps maps{};
+    int bad = page_map(&maps.k, kv, kv->k);
+    if (bad || (bad = page_map(&maps.v, kv, kv->v))) return bad;
+    AttnOut o{};
+    o.out = out;
+    o.lse = lse;
+    o.part = reinterpret_cast<float*>(scratch);
+    o.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(scratch) + p.rec_bytes);
+    return rc(launch_packed_attn(a, kv->type, p, maps, o, packed_of(kv), q, q_stride,
+                                 (cudaStream_t)stream));
+  }
+  const Mirror m = mirror_of(kv);
+  const pp_paged_kv copy = mirror_cache(kv, m, reinterpret_cast<char*>(scratch));
   ReadArgs x = read_args(kv, &copy);
   x.mirror = 1;
   const cudaError_t err = launch_packed_read(a, kv->type, x, (cudaStream_t)stream);

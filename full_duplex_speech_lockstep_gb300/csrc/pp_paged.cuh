@@ -599,5 +599,20 @@ struct ReadArgs {
 };
 cudaError_t launch_packed_read(const Args& a, int type, const ReadArgs& x, cudaStream_t s);
 
+// Chunks of up to kPackedRows rows (tokens x heads of a key head) run on the codes themselves
+// (k_packed_attn.cu); longer ones on a 16-bit copy of what they see.
+constexpr int kPackedRows = 128;
+struct PackedPlan {
+  int R;           // rows of a row tile: 8, 16 or 32
+  int max_q;
+  int share;       // SMs for each (sequence, key head, row tile), at least 1
+  int ns_cap;      // splits of the longest sequence that the table can hold
+  size_t rec_bytes, ml_bytes;
+};
+PackedPlan packed_plan(const Args& a, int max_q);
+cudaError_t launch_packed_attn(const Args& a, int type, const PackedPlan& plan, const Maps& maps,
+                               const AttnOut& o, const Packed& kv, const void* q, int64_t q_stride,
+                               cudaStream_t s);
+
 }  // namespace paged
 }  // namespace pp

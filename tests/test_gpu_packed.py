@@ -647,3 +647,17 @@ def test_a_captured_tick_is_the_eager_one():
         torch.cuda.synchronize()
         for y, z in zip(out + state, w):
             assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("type", [BF16, F16])
+def test_a_value_that_some_rows_do_not_see_costs_them_no_precision(type):
+    """Later entries of a chunk with values 2^60 (2^12) larger: the rows before them keep their bits."""
+    b = Packed(type, 128, 1, 2, 16, [6], [90], seed=4)
+    want, wl = b.kv().attention(b.q, b.cu, b.len, max_q=6, with_lse=True)
+    b.check(want, wl)
+    p, r = (t[87:] for t in b.where(0))
+    b.vs[p, :, r] += 60 if type == BF16 else 12
+    got, gl = b.kv().attention(b.q, b.cu, b.len, max_q=6, with_lse=True)
+    assert torch.equal(got[:3], want[:3]) and torch.equal(gl, wl)
+    b.v[p, :, r] *= 2.0 ** (60 if type == BF16 else 12)
+    b.check(got[:, :], gl) if type == BF16 else None
