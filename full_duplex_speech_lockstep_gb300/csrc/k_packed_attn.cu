@@ -66,16 +66,23 @@ struct Ctl {
   int abort;
   // of the two units in flight: each row's factor of its scores (to powers of two) and its entry
   alignas(16) float row_c[2][32];
-  alignas(16) int row_at[2][32];
-  // of the two tiles in flight: maxima and sums of rows, and the largest V exponents that they see
-  alignas(16) float warp_max[2][4][32];
+  int row_at[2][32];
+  // of the two tiles in flight: maxima of rows, and the largest V exponents that they see
+  float warp_max[2][4][32];
   uint32_t warp_e[2][4][32];
-  alignas(16) float ref[2][4][32];     // each warp's copy of the references
-  int ref_e[2][4][32];
-  alignas(16) float m[2][32], l[2][4][32];
+  // each warp's copy of the references, and of 2^(127 - E)
+  alignas(16) float ref[2][4][32];
+  alignas(16) float fit[2][4][32];
+  float m[2][32], l[2][4][32];
   uint32_t e[2][32];
-  alignas(16) float keep[4][32], add[4][32];   // epilogue warps: factors of acc and of O
+  alignas(16) float keep[4][32];       // epilogue warps: factors of acc and of O
+  alignas(16) float add[4][32];
 };
+
+// What a Unit of the ring holds here: `row` and `first` of its first row (token's row, its entry), nt =
+// the last row's entry, tag = rows | head of the first row << 8, ns = the first row's token within
+// its chunk, split = split | splits << 8.
+constexpr int kHeadShift = 8;
 
 // ---- units -----------------------------------------------------------------------------------
 // Tokens that R consecutive rows (heads within tokens) touch, at most.
@@ -161,21 +168,21 @@ struct Walk {
   // Row tiles of a split follow each other: its keys are in L2 for the second.
   __device__ __forceinline__ Unit unit() const {
     Unit x;
-    const int split = i / rt, r0 = (i - split * rt) * R;
+    const int split = i / rt, r0 = (i - split * rt) * R, rows = min(R, s.n * a.G - r0);
+    const int t0 = r0 / a.G, g0 = r0 - t0 * a.G;
     x.b = b;
     x.h = h;
-    x.row = s.row0;
-    x.nt = min(R, s.n * a.G - r0);               // rows
-    x.first = s.total - s.n;                     // entry of the sequence's first new token
-    const int p0 = x.first + r0 / a.G, p1 = x.first + (r0 + x.nt - 1) / a.G;
-    x.stop = min(max(p1 + 1, 0), s.len);
-    x.low = a.window ? min(max(p0 - a.window + 1, 0), x.stop) : 0;
+    x.row = s.row0 + t0;
+    x.first = s.total - s.n + t0;
+    x.nt = x.first + (g0 + rows - 1) / a.G;
+    x.tag = rows | g0 << kHeadShift;
+    x.ns = t0;
+    x.stop = min(max(x.nt + 1, 0), s.len);
+    x.low = a.window ? min(max(x.first - a.window + 1, 0), x.stop) : 0;
     const int ta = x.low / kTile, tb = (x.stop + kTile - 1) / kTile;
     x.tile0 = min(ta + split * st, tb);
     x.tile1 = min(x.tile0 + st, tb);
-    x.split = split;
-    x.ns = ns;
-    x.tag = r0;
+    x.split = split | ns << 8;
     return x;
   }
 };
@@ -310,7 +317,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   // S of the even and odd tiles, then O
   const uint32_t tmem = ctl->tmem;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(a, bar, parity, abort_flag); };
+  // (waits that go on are calls: with their loops in place the roles' code is larger than the
+  // instruction cache)
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase<true>(a, bar, parity, abort_flag); };
+  // a unit's tiles of K (of V) and their scales; `part`: their stages' place among the scales
+  auto load_tiles = [&](const Unit& x, uint32_t& n, const CUtensorMap& map, const uint8_t* scales,
+                        int part, uint64_t* full, uint64_t* empty, uint32_t* seen_bad) {
+    if (x.tile0 == x.tile1) return;
+    const bool past = x.nt >= x.stop;
+    TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, past, lane);
+#pragma unroll 1
+    for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+      const int i = n % S;
+      const TilePages now = next;
+      if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, past, lane);
+      if (n >= S) wait(&empty[i], (n / S - 1) & 1);
+      if (*abort_flag) break;
+      load_codes(a, &map, scales, kv.scale_stride, smem_u32(smem + (part + i) * C::kTileBytes),
+                 smem_u32(smem + C::kScaleOff + (part + i) * kTile), smem_u32(&full[i]), now, x.h,
+                 t * kTile, lane, seen_bad ? &ctl->bad[i] : nullptr);
+      if (seen_bad) *seen_bad |= now.bad;
+    }
+  };
+  // every copy lands before the CTA may exit (bounded waits)
+  auto drain = [&](uint32_t n, uint64_t* full) {
+    if (lane == 0) {
+#pragma unroll 1
+      for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &full[i % S], (i / S) & 1);
+    }
+    __syncwarp();
+  };
 
   if (warp == 0) {
     // ---- units, K tiles -------------------------------------------------------------------
@@ -319,33 +355,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (; !walk.done() && !*abort_flag; walk.next()) {
       const Unit x = walk.unit();
-      put_unit(a, ctl->ring, nu++, x, lane, abort_flag);
-      if (x.tile0 == x.tile1) continue;
-      const bool past = x.first + (x.tag + x.nt - 1) / a.G >= x.stop;
-      TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, past, lane);
-#pragma unroll 1
-      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
-        const int i = n % S;
-        const TilePages now = next;
-        if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, past, lane);
-        if (n >= S) wait(&ctl->kempty[i], (n / S - 1) & 1);
-        if (*abort_flag) break;
-        load_codes(a, &mapK, kv.k_scale, kv.scale_stride, smem_u32(smem + i * C::kTileBytes),
-                   smem_u32(smem + C::kScaleOff + i * kTile), smem_u32(&ctl->kfull[i]), now, x.h,
-                   t * kTile, lane, &ctl->bad[i]);
-        seen_bad |= now.bad;
-      }
+      put_unit<true>(a, ctl->ring, nu++, x, lane, abort_flag);
+      load_tiles(x, n, mapK, kv.k_scale, 0, ctl->kfull, ctl->kempty, &seen_bad);
     }
     Unit last{};
     last.b = -1;
-    put_unit(a, ctl->ring, nu, last, lane, abort_flag);
+    put_unit<true>(a, ctl->ring, nu, last, lane, abort_flag);
     if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
-    // every copy lands before the CTA may exit (bounded waits)
-    if (lane == 0) {
+    drain(n, ctl->kfull);
+  } else if (warp == 2) {
+    // ---- V tiles --------------------------------------------------------------------------
+    uint32_t n = 0;
+    Unit x;
 #pragma unroll 1
-      for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &ctl->kfull[i % S], (i / S) & 1);
-    }
-    __syncwarp();
+    for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu)
+      load_tiles(x, n, mapV, kv.v_scale, S, ctl->vfull, ctl->vempty, nullptr);
+    drain(n, ctl->vfull);
   } else if (warp == 1) {
     // ---- MMA issuer -----------------------------------------------------------------------
     if (lane == 0) {
@@ -353,109 +378,81 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_s = id | ((uint32_t)(C::NQ >> 3) << 17);
       constexpr uint32_t id_o = id | ((uint32_t)(C::NP >> 3) << 17) | (1u << 15) | (1u << 16);
       constexpr uint32_t kRow = D == 128 ? 2 : 4;       // the tiles' layout: rows of D bytes, swizzled
-      uint32_t n = 0, nq = 0;
-      auto values = [&](uint32_t m) {
-        const uint32_t g = m & 1, i = m % S;
-        wait(&ctl->pfull[g], (m >> 1) & 1);
-        wait(&ctl->vfull[i], (m / S) & 1);
-        if (*abort_flag) return;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t vb = smem_u32(smem + C::kVOff + i * C::kTileBytes);
-        const uint32_t pb = smem_u32(smem + C::kPOff + g * C::kPBytes);
-#pragma unroll
-        for (int kk = 0; kk < kTile / 32; ++kk)
+      uint32_t n = 0, nq = 0, nu = 0;
+      Unit x{};
+      bool more = true;                                 // there are tiles to come
+      // step n: O of tile n - 2, S of tile n; two more steps after the last tile
+#pragma unroll 1
+      for (uint32_t last = ~0u; n < last; ++n) {
+        const bool fresh = more && x.tile0 == x.tile1;
+        while (more && x.tile0 == x.tile1) more = get_unit<true>(a, ctl->ring, nu++, x, lane, true, abort_flag);
+        if (!more && last == ~0u) last = n + 2;
+        if (n >= 2) {
+          const uint32_t m = n - 2, g = m & 1, i = m % S;
+          wait(&ctl->pfull[g], (m >> 1) & 1);           // (also: S of tile n - 2 has been read)
+          wait(&ctl->vfull[i], (m / S) & 1);
+          if (*abort_flag) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           // V: dims contiguous, 8 keys to an atom of 8 D bytes (with 64 dims rows 64-127 of the product
           // are the keys 8 further on, and nobody reads them).  Weights: 16 columns of 8 keys to 128
           // bytes, keys following each other, the next columns 2048 bytes on.
-          umma_e4m3(tmem + 256 + g * 128, desc(vb + kk * 32 * D, 512, 8 * D, kRow),
-                    desc(pb + kk * 512, 128, 2048, 0), id_o, kk > 0);
-        umma_commit(smem_u32(&ctl->ofull[g]));
-        umma_commit(smem_u32(&ctl->vempty[i]));
-      };
-      Unit x;
-#pragma unroll 1
-      for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, true, abort_flag); ++nu) {
-        if (x.tile0 == x.tile1) continue;
-        const uint32_t qb = nq & 1;
-#pragma unroll 1
-        for (int t = x.tile0; t < x.tile1; ++t, ++n) {
-          const uint32_t g = n & 1, i = n % S;
-          if (n >= 2) values(n - 2);                    // (also: S of n - 2 has been read)
-          if (t == x.tile0) wait(&ctl->qfull[qb], (nq >> 1) & 1);
-          wait(&ctl->kfull[i], (n / S) & 1);
-          if (*abort_flag) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t kb = smem_u32(smem + i * C::kTileBytes);
-          const uint32_t qo = smem_u32(smem + C::kQOff + qb * C::kQBytes);
+          const uint64_t v = desc(smem_u32(smem + C::kVOff + i * C::kTileBytes), 512, 8 * D, kRow);
+          const uint64_t w = desc(smem_u32(smem + C::kPOff + g * C::kPBytes), 128, 2048, 0);
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            umma_e4m3(tmem + g * 128, desc(kb + kk * 32, 0, 8 * D, kRow),
-                      desc(qo + kk * 32, 0, 1024, 2), id_s, kk > 0);
-          umma_commit(smem_u32(&ctl->sfull[g]));
-          umma_commit(smem_u32(&ctl->kempty[i]));
+          for (int kk = 0; kk < kTile / 32; ++kk)
+            umma_e4m3(tmem + 256 + g * 128, v + (kk * 32 * D >> 4), w + (kk * 512 >> 4), id_o, kk > 0);
+          umma_commit(smem_u32(&ctl->ofull[g]));
+          umma_commit(smem_u32(&ctl->vempty[i]));
         }
+        if (!more) continue;
+        const uint32_t g = n & 1, i = n % S, qb = nq & 1;
+        if (fresh) wait(&ctl->qfull[qb], (nq >> 1) & 1);
+        wait(&ctl->kfull[i], (n / S) & 1);
         if (*abort_flag) break;
-        umma_commit(smem_u32(&ctl->qempty[qb]));
-        ++nq;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint64_t k = desc(smem_u32(smem + i * C::kTileBytes), 0, 8 * D, kRow);
+        const uint64_t r = desc(smem_u32(smem + C::kQOff + qb * C::kQBytes), 0, 1024, 2);
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+          umma_e4m3(tmem + g * 128, k + (kk * 32 >> 4), r + (kk * 32 >> 4), id_s, kk > 0);
+        umma_commit(smem_u32(&ctl->sfull[g]));
+        umma_commit(smem_u32(&ctl->kempty[i]));
+        if (++x.tile0 == x.tile1) {
+          umma_commit(smem_u32(&ctl->qempty[qb]));
+          ++nq;
+        }
       }
-      if (n >= 2 && !*abort_flag) values(n - 2);
-      if (n >= 1 && !*abort_flag) values(n - 1);
       // every MMA is done before tensor memory is given back (bounded wait)
       umma_commit(smem_u32(&ctl->done));
       drain_phase(a, &ctl->done, 0);
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ---- V tiles --------------------------------------------------------------------------
-    uint32_t n = 0;
-    Unit x;
-#pragma unroll 1
-    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
-      if (x.tile0 == x.tile1) continue;
-      const bool past = x.first + (x.tag + x.nt - 1) / a.G >= x.stop;
-      TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, past, lane);
-#pragma unroll 1
-      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
-        const int i = n % S;
-        const TilePages now = next;
-        if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, past, lane);
-        if (n >= S) wait(&ctl->vempty[i], (n / S - 1) & 1);
-        if (*abort_flag) break;
-        load_codes(a, &mapV, kv.v_scale, kv.scale_stride, smem_u32(smem + C::kVOff + i * C::kTileBytes),
-                   smem_u32(smem + C::kScaleOff + (S + i) * kTile), smem_u32(&ctl->vfull[i]), now, x.h,
-                   t * kTile, lane, nullptr);
-      }
-    }
-    if (lane == 0) {
-#pragma unroll 1
-      for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &ctl->vfull[i % S], (i / S) & 1);
     }
     __syncwarp();
   } else if (warp == 3) {
     // ---- queries: L lanes to a row, four dims to a lane -----------------------------------
     constexpr int L = D / 4, kSide = 32 / L, kAhead = 4;   // rows side by side; passes loaded at once
     const int l = lane % L, side = lane / L;
+    const uint32_t per_head = (65536u + a.G - 1) / a.G;    // f / G for f G < 2^16
     uint32_t nq = 0;
     Unit x;
 #pragma unroll 1
-    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+    for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
       if (x.tile0 == x.tile1) continue;
       const uint32_t qb = nq & 1;
       if (nq >= 2) wait(&ctl->qempty[qb], ((nq >> 1) - 1) & 1);
       if (*abort_flag) break;
+      const int rows = x.tag & 0xff, g0 = x.tag >> kHeadShift;
+      const T* base = q + (int64_t)x.row * q_stride + (int64_t)x.h * a.G * D + l * 4;
       uint8_t* to = smem + C::kQOff + qb * C::kQBytes;
 #pragma unroll 1
       for (int r0 = 0; r0 < R; r0 += kSide * kAhead) {
         uint2 raw[kAhead];
-        int at[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const int r = r0 + k * kSide + side, f = x.tag + r, t = f / a.G;
-          at[k] = x.first + t;
+          const int r = r0 + k * kSide + side;
+          const uint32_t f = g0 + r, t = f * per_head >> 16;
           raw[k] = make_uint2(0u, 0u);
-          if (r < x.nt)
-            raw[k] = *reinterpret_cast<const uint2*>(q + (int64_t)(x.row + t) * q_stride +
-                                                     (int64_t)(x.h * a.G + f - t * a.G) * D + l * 4);
+          if (r < rows)
+            raw[k] = *reinterpret_cast<const uint2*>(base + t * q_stride + (int)(f - t * a.G) * D);
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
@@ -469,8 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int w = L / 2; w > 0; w >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, w));
           // the row's power of two, as a cache entry's; a row that is not finite has NaN scores
           const bool wild = top >= 0x7f800000u;
-          const int byte =
-              max((int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
+          const int byte = max((int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
           const float f = wild ? 0.f : __uint_as_float((254u - (uint32_t)byte) << 23);
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = wild ? 0.f : y[e] * f;
@@ -484,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (l == 0) {
             ctl->row_c[qb][r] = wild ? __uint_as_float(0x7fc00000u) : a.c * scale_of((uint32_t)byte);
-            ctl->row_at[qb][r] = at[k];
+            ctl->row_at[qb][r] = x.first + (int)((g0 + r) * per_head >> 16);
           }
         }
       }
@@ -497,22 +493,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- softmax: thread k of a group owns key k of the group's tiles ---------------------
     const uint32_t g = warp >= 8;
     const int wq = warp & 3, key = wq * 32 + lane;
-    const uint32_t lane_at = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t scores = tmem + ((uint32_t)(wq * 32) << 16) + g * 128;
+    uint8_t* const weights = smem + C::kPOff + g * C::kPBytes + key * 16;
     uint32_t n = 0, nq = 0, meets = 0;
     Unit x;
 #pragma unroll 1
-    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+    for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
       if (x.tile0 == x.tile1) continue;
       const uint32_t qb = nq & 1;
       wait(&ctl->qfull[qb], (nq >> 1) & 1);
-      const int p0 = x.first + x.tag / a.G, p1 = x.first + (x.tag + x.nt - 1) / a.G;
 #pragma unroll 1
       for (int t = x.tile0; t < x.tile1; ++t, ++n) {
         if ((n & 1) != g) continue;
         if (*abort_flag) break;
         const int i = n % S, j = t * kTile + key;
-        const uint32_t ph = (n >> 1) & 1;
-        wait(&ctl->sfull[g], ph);
+        wait(&ctl->sfull[g], (n >> 1) & 1);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         // (the first product has seen this phase of K, and the next one waits for this warp)
         wait(&ctl->kfull[i], (n / S) & 1);
@@ -521,53 +516,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->kempty[i]));
         // does every row see every key of the tile?
-        const bool edge = bad != 0 || t * kTile + kTile - 1 > min(p0, x.stop - 1) ||
-                          (a.window && t * kTile <= p1 - a.window);
-        const bool live = !edge || (j < x.stop && j >= x.low && !((bad >> (key >> 4)) & 1u));
-        // ---- scores and the tile's maxima
-        float v[R];
-        float mine = 0.f;                                // lane r: row r's
-#pragma unroll
-        for (int c = 0; c < R; c += 8) {
+        const bool edge = bad != 0 || t * kTile + kTile - 1 > min(x.first, x.stop - 1) ||
+                          (a.window && t * kTile <= x.nt - a.window);
+        uint32_t see = ~0u;                              // a bit for each row that sees this key
+        bool live = true;                                // some row does
+        if (edge) {
+          live = j < x.stop && j >= x.low && !((bad >> (key >> 4)) & 1u);
+          see = 0u;
+          if (live) {
+#pragma unroll 1
+            for (int r = 0; r < (x.tag & 0xff); ++r) {
+              const int at = ctl->row_at[qb][r];
+              see |= (j <= at && !(a.window && j <= at - a.window) ? 1u : 0u) << r;
+            }
+          }
+        }
+        // the scores of rows c .. c + 7, as powers of two, -infinity where a row does not see the key
+        auto load_scores = [&](int c, float (&v)[8]) {
           uint32_t s[C::QP][8];
 #pragma unroll
-          for (int p = 0; p < C::QP; ++p) tmem_ld8(lane_at + g * 128 + p * R + c, s[p]);
-          tmem_wait_ld();
+          for (int p = 0; p < C::QP; ++p) tmem_ld8(scores + p * R + c, s[p]);
           float f[8];
           *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&ctl->row_c[qb][c]);
           *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&ctl->row_c[qb][c + 4]);
+          tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float y = after_wait(s[C::QP - 1][e]);
 #pragma unroll
             for (int p = C::QP - 2; p >= 0; --p) y = fmaf(y, 0.0625f, after_wait(s[p][e]));
-            v[c + e] = y * kf * f[e];
+            y = y * kf * f[e];
+            v[e] = (see >> c) & (1u << e) ? y : -INFINITY;
           }
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int at = ctl->row_at[qb][c + e];
-              if (!live || j > at || (a.window && j <= at - a.window)) v[c + e] = -INFINITY;
-            }
-          }
+        };
+        // ---- the tile's maxima; lane r has row r's
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < R; c += 8) {
+          float v[8];
+          load_scores(c, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float top = warp_max(v[c + e]);
-            if (lane == c + e) mine = top;
+            const float y = warp_max(v[e]);
+            if (lane - c == e) top = y;
           }
         }
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         // ---- what V brings: its scale, and rows that must not be multiplied
-        const int vi = n % S;
-        wait(&ctl->vfull[vi], (n / S) & 1);
-        uint32_t ev = smem[C::kScaleOff + (S + vi) * kTile + key];
+        wait(&ctl->vfull[i], (n / S) & 1);
+        const uint32_t ev = smem[C::kScaleOff + (S + i) * kTile + key];
         bool nan_value = ev == 255u;
-        if (edge && !(live && j <= p0 && (!a.window || j > p1 - a.window))) {
-          uint4* row = reinterpret_cast<uint4*>(smem + C::kVOff + vi * C::kTileBytes + key * D);
+        const uint32_t own_e = nan_value ? 0u : ev;
+        // each row goes by the exponents that it sees: another's could take its weights below e4m3
+        uint32_t E;
+        if (!edge) {
+          E = __reduce_max_sync(0xffffffffu, own_e);
+        } else {
+          E = 0;
+#pragma unroll 1
+          for (int r = 0; r < (x.tag & 0xff); ++r) {
+            const uint32_t y = __reduce_max_sync(0xffffffffu, see >> r & 1u ? own_e : 0u);
+            if (lane == r) E = y;
+          }
+          uint4* row = reinterpret_cast<uint4*>(smem + C::kVOff + i * C::kTileBytes + key * D);
           bool clear = !live;
-          if (live) {
+          if (live && !(j <= x.first && (!a.window || j > x.nt - a.window))) {
+            // some rows do not see it: its NaN codes must not meet their weights of zero
             uint32_t z = 0;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D / 16; ++k) {
               const uint4 w = row[k];
               z |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
@@ -577,100 +592,82 @@ __global__ void __launch_bounds__(kThreads, 1)
             nan_value |= clear;
           }
           if (clear) {
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D / 16; ++k) row[k] = make_uint4(0u, 0u, 0u, 0u);
           }
-        }
-        // (each row goes by the exponents that it sees: another's could take its weights below e4m3)
-        const uint32_t own_e = ev == 255u ? 0u : ev;
-        uint32_t top_e;
-        if (edge) {
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const uint32_t y = __reduce_max_sync(0xffffffffu, v[r] == -INFINITY ? 0u : own_e);
-            if (lane == r) top_e = y;
-          }
-        } else {
-          top_e = __reduce_max_sync(0xffffffffu, own_e);
+          __syncwarp();
         }
         if (lane < R) {
-          ctl->warp_max[g][wq][lane] = mine;
-          ctl->warp_e[g][wq][lane] = top_e;
+          ctl->warp_max[g][wq][lane] = top;
+          ctl->warp_e[g][wq][lane] = E;
         }
-        sync_warps(a, &ctl->meet[g], meets, lane, abort_flag);
+        sync_warps<true>(a, &ctl->meet[g], meets, lane, abort_flag);
         // lane r works row r's reference out for its warp
-        float top = -INFINITY;
-        uint32_t E = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if (lane >= R) break;
-          top = fmaxf(top, ctl->warp_max[g][w][lane]);
-          E = max(E, ctl->warp_e[g][w][lane]);
-        }
-        const float ref = top == -INFINITY ? 0.f : top - kTop;
         if (lane < R) {
-          ctl->ref[g][wq][lane] = ref;
-          ctl->ref_e[g][wq][lane] = (int)E;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            top = fmaxf(top, ctl->warp_max[g][w][lane]);
+            E = max(E, ctl->warp_e[g][w][lane]);
+          }
+          if (top != top) top = -INFINITY;               // (a row of NaN: its weights are NaN all the same)
+          ctl->ref[g][wq][lane] = top == -INFINITY ? 0.f : top - kTop;
+          ctl->fit[g][wq][lane] = __uint_as_float((254u - E) << 23);
         }
         // the last tile's weights and sums of this buffer have been used
         if (n >= 2) wait(&ctl->oempty[g], ((n >> 1) - 1) & 1);
-        if (wq == 0) {
-          if (lane < R) {
-            ctl->m[g][lane] = top == -INFINITY ? -INFINITY : ref;
-            ctl->e[g][lane] = E;
-          }
+        if (wq == 0 && lane < R) {
+          ctl->m[g][lane] = top - kTop;
+          ctl->e[g][lane] = E;
         }
         __syncwarp();
-        // 2^(ev - E), for every row alike where all see all
-        auto value_factor = [&](int E_) {
-          const int de = (int)ev - E_;
-          return nan_value ? __uint_as_float(0x7fc00000u)
-                           : de <= -127 ? 0.f : __uint_as_float((uint32_t)(127 + de) << 23);
-        };
-        const float vf = value_factor((int)__shfl_sync(0xffffffffu, E, 0));
-        // ---- weights, eight rows at a time
-        uint8_t* pt = smem + C::kPOff + g * C::kPBytes + key * 16;
-#pragma unroll
+        // ---- weights: w = p 2^(ev - 127) 2^(127 - E).  (What lies below fp32's normal range between
+        // the two factors is 2^-30 of the largest weight or less.)
+        const float vf = nan_value ? __uint_as_float(0x7fc00000u) : scale_of(ev);
+#pragma unroll 1
         for (int c = 0; c < R; c += 8) {
-          float f[8], p[8];
-          *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&ctl->ref[g][wq][c]);
-          *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&ctl->ref[g][wq][c + 4]);
+          float p[8];
+          load_scores(c, p);
+          float f[8], u[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            *reinterpret_cast<float4*>(f + e) = *reinterpret_cast<const float4*>(&ctl->ref[g][wq][c + e]);
+            *reinterpret_cast<float4*>(u + e) = *reinterpret_cast<const float4*>(&ctl->fit[g][wq][c + e]);
+          }
           uint32_t w[2][kParts];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             float y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float s = v[c + half * 4 + e];
-              p[half * 4 + e] = exp2_approx(s - f[half * 4 + e]);
-              if (!edge)
-                y[e] = p[half * 4 + e] * vf;
-              else if (s == -INFINITY)
-                y[e] = 0.f;                              // (not a NaN of a value that it does not see)
-              else
-                y[e] = p[half * 4 + e] * value_factor(ctl->ref_e[g][wq][c + half * 4 + e]);
+              const int r = half * 4 + e;
+              const bool hidden = p[r] == -INFINITY;
+              p[r] = exp2_approx(p[r] - f[r]);
+              y[e] = hidden ? 0.f : p[r] * vf * u[r];    // (not a NaN of a value that it does not see)
             }
             split4<kParts>(y, w[half]);
           }
 #pragma unroll
           for (int k = 0; k < kParts; ++k) {
             const int col = k * R + c;
-            *reinterpret_cast<uint2*>(pt + (col >> 4) * 2048 + (col & 15)) = make_uint2(w[0][k], w[1][k]);
+            *reinterpret_cast<uint2*>(weights + (col >> 4) * 2048 + (col & 15)) =
+                make_uint2(w[0][k], w[1][k]);
           }
           // sums of the eight rows over the warp's keys: lanes halve the rows, then the keys
 #pragma unroll
           for (int k = 4, d = 16; k > 0; k >>= 1, d >>= 1) {
+            const bool up = lane & d;
 #pragma unroll
             for (int e = 0; e < k; ++e) {
-              const bool up = lane & d;
               const float give = up ? p[e] : p[e + k];
               p[e] = (up ? p[e + k] : p[e]) + __shfl_xor_sync(0xffffffffu, give, d);
             }
           }
           p[0] += __shfl_xor_sync(0xffffffffu, p[0], 2);
           p[0] += __shfl_xor_sync(0xffffffffu, p[0], 1);
-          if ((lane & 3) == 0) ctl->l[g][wq][c + (lane >> 2 & 1) + (lane >> 3 & 1) * 2 + (lane >> 4) * 4] = p[0];
+          if ((lane & 3) == 0)
+            ctl->l[g][wq][c + (lane >> 2 & 1) + (lane >> 3 & 1) * 2 + (lane >> 4) * 4] = p[0];
         }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->pfull[g]));
@@ -686,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0;
     Unit x;
 #pragma unroll 1
-    for (uint32_t nu = 0; get_unit(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+    for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
       float acc[R], M = -INFINITY, Lsum = 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[r] = 0.f;
@@ -716,13 +713,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t y[kParts][8];
 #pragma unroll
           for (int p = 0; p < kParts; ++p) tmem_ld8(lane_at + g * 128 + p * R + c, y[p]);
-          tmem_wait_ld();
           float keep[8], add[8];
 #pragma unroll
           for (int e = 0; e < 8; e += 4) {
             *reinterpret_cast<float4*>(keep + e) = *reinterpret_cast<const float4*>(&ctl->keep[wq][c + e]);
             *reinterpret_cast<float4*>(add + e) = *reinterpret_cast<const float4*>(&ctl->add[wq][c + e]);
           }
+          tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float z = fmaf(fmaf(after_wait(y[2][e]), 0.0625f, after_wait(y[1][e])), 0.0625f,
@@ -736,24 +733,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (*abort_flag) break;
       // lane r: where row r goes
-      const int f = x.tag + min(lane, x.nt - 1), tk = f / a.G, hd = x.h * a.G + f - tk * a.G;
+      const int rows = x.tag & 0xff, f = (x.tag >> kHeadShift) + min(lane, rows - 1), tk = f / a.G;
+      const int hd = x.h * a.G + f - tk * a.G;
+      const bool whole = x.split >> 8 == 1;
       const int64_t row = (int64_t)(x.row + tk) * H + hd;
-      const int64_t rec = (((int64_t)x.b * max_q + tk) * H + hd) * ns_cap + x.split;
+      const int64_t rec =
+          (((int64_t)x.b * max_q + x.ns + tk) * H + hd) * ns_cap + (x.split & 0xff);
       const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-      if (wq == 0 && lane < x.nt) {
-        if (x.ns > 1)
+      if (wq == 0 && lane < rows) {
+        if (!whole)
           o.part_ml[rec] = make_float2(M, Lsum);
         else if (o.lse)
           o.lse[row] = Lsum == 0.f ? -INFINITY : (M + log2f(Lsum)) * kLn2;
       }
-      const int64_t place = x.ns > 1 ? rec : row;
+      const int64_t place = whole ? row : rec;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (r >= x.nt) break;
+        if (r >= rows) break;
         const int64_t to = __shfl_sync(0xffffffffu, place, r) * D + d;
         const float scale = __shfl_sync(0xffffffffu, inv, r);
         if (d >= D) continue;
-        if (x.ns > 1)
+        if (!whole)
           o.part[to] = acc[r];
         else
           reinterpret_cast<uint16_t*>(o.out)[to] = (uint16_t)Num<T>::pack(acc[r] * scale, 0.f);

@@ -220,11 +220,12 @@ __device__ __forceinline__ bool get_unit(const Args& a, UnitRing& r, uint32_t k,
 }
 
 // Bounded barrier of `count` warps on an mbarrier initialised with that count.
+template <bool kCall = false>
 __device__ __forceinline__ void sync_warps(const Args& a, uint64_t* bar, uint32_t& phase, int lane,
                                            volatile int* abort_flag) {
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(bar));
-  wait_phase(a, bar, phase & 1, abort_flag);
+  wait_phase<kCall>(a, bar, phase & 1, abort_flag);
   ++phase;
 }
 

@@ -36,23 +36,28 @@ def packed(seed, units, stages, late=False):
             yield pfull[m & 1], m >> 1
             yield vfull[m % stages], m // stages
             s.commits += [ofull[m & 1], vempty[m % stages]]
-        for k, count in enumerate(units):
-            yield from ring.get(k)
-            if not count:
-                continue
-            for t in range(count):
-                if n >= 2:
-                    yield from values(n - 2)
-                if t == 0:
-                    yield qfull[nq & 1], nq >> 1
-                yield kfull[n % stages], n // stages
-                s.commits += [sfull[n & 1], kempty[n % stages]]
-                n += 1
-            s.commits.append(qempty[nq & 1])
-            nq += 1
-        yield from ring.get(len(units))
-        for m in range(max(0, n - 2), n):
-            yield from values(m)
+        k = left = 0
+        fresh = True
+        while True:                             # step n: values of tile n - 2, scores of tile n
+            fresh = left == 0
+            while left == 0 and k <= len(units):
+                yield from ring.get(k)
+                left = units[k] if k < len(units) else 0
+                k += 1
+            if n >= 2:
+                yield from values(n - 2)
+            if left == 0:
+                break
+            if fresh:
+                yield qfull[nq & 1], nq >> 1
+            yield kfull[n % stages], n // stages
+            s.commits += [sfull[n & 1], kempty[n % stages]]
+            n, left = n + 1, left - 1
+            if left == 0:
+                s.commits.append(qempty[nq & 1])
+                nq += 1
+        if n >= 1:
+            yield from values(n - 1)
 
     def queries():
         nq = 0
