@@ -6,7 +6,7 @@
 // other operands are sums of e4m3 numbers, which have 4 significant bits each, as more columns of the
 // product:
 //   q = 2^eq (q1 + q2/16 [+ q3/256])     two are exact for bf16's 8 bits, three for fp16's 11
-//   w = w1 + w2/16 + w3/256              12 bits; w is at most 256, so 2^-26 of that is its floor
+//   w = w1 + w2/16 + w3/256              fp16's 11 bits; w is at most 256, so 2^-26 of that is its floor
 // Keys are the rows of both products, a thread of the softmax owns one key:
 //   S[j][r]  = k_j . q_r                 M = 128 keys, N = parts x R rows, K = D
 //   w[j][r]  = 2^(s_jr - m_r + 8) 2^(ev_j - E_r),   s_jr = S c 2^(ek_j + eq_r)
@@ -70,7 +70,7 @@ struct Ctl {
   // of the two tiles in flight: maxima of rows, and the largest V exponents that they see
   float warp_max[2][4][32];
   uint32_t warp_e[2][4][32];
-  // each warp's copy of the references, and of 2^(127 - E)
+  // each warp's copy of the references (negative), and of 2^(127 - E)
   alignas(16) float ref[2][4][32];
   alignas(16) float fit[2][4][32];
   float m[2][32], l[2][4][32];
@@ -226,30 +226,33 @@ __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead, uint32_t 
 }
 
 // ---- numbers ---------------------------------------------------------------------------------
-// Two values as e4m3 (nearest; the first one in the lower byte), and what they stand for
-__device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+// Two values as fp16 (nearest; the first one in the lower half)
+__device__ __forceinline__ uint32_t to_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float2 from_e4m3(uint32_t codes) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-// Four values as `P` words of four codes: each part is what the ones before left, sixteen times
+// Four fp16 numbers of at most 2^8 as `P` words of four codes: each part is what the ones before left,
+// sixteen times, which fp16 holds exactly.
 template <int P>
-__device__ __forceinline__ void split4(float (&x)[4], uint32_t (&w)[P]) {
+__device__ __forceinline__ void split4(uint32_t x, uint32_t y, uint32_t (&w)[P]) {
+  const __half2 up = __float2half2_rn(16.f), down = __float2half2_rn(-16.f);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const uint32_t a = to_e4m3(x[0], x[1]), b = to_e4m3(x[2], x[3]);
-    w[p] = a | b << 16;
+    uint16_t a, b;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(x));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(y));
+    w[p] = a | (uint32_t)b << 16;
     if (p + 1 == P) break;
-    const float2 ya = from_e4m3(a), yb = from_e4m3(b);
-    x[0] = (x[0] - ya.x) * 16.f;
-    x[1] = (x[1] - ya.y) * 16.f;
-    x[2] = (x[2] - yb.x) * 16.f;
-    x[3] = (x[3] - yb.y) * 16.f;
+    auto left = [&](uint32_t z, uint16_t code) {
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(code));
+      const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&h), down,
+                                __hmul2(*reinterpret_cast<const __half2*>(&z), up));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    };
+    x = left(x, a);
+    y = left(y, b);
   }
 }
 // 2^(byte - 127), NaN for 255
@@ -280,13 +283,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_u32(&ctl->kfull[i]), 1);
-      mbar_init(smem_u32(&ctl->kempty[i]), 5);          // the first product, four warps of softmax
+      mbar_init(smem_u32(&ctl->kempty[i]), 4);          // softmax, which has waited for the product
       mbar_init(smem_u32(&ctl->vfull[i]), i == 0 ? 1 + a.withhold : 1);
-      mbar_init(smem_u32(&ctl->vempty[i]), 1);
+      mbar_init(smem_u32(&ctl->vempty[i]), 4);          // epilogue
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl->qfull[i]), 1);
-      mbar_init(smem_u32(&ctl->qempty[i]), 9);          // the first product, eight warps of softmax
+      mbar_init(smem_u32(&ctl->qempty[i]), 8);          // softmax
       mbar_init(smem_u32(&ctl->sfull[i]), 1);
       mbar_init(smem_u32(&ctl->pfull[i]), 4);
       mbar_init(smem_u32(&ctl->ofull[i]), 1);
@@ -402,7 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < kTile / 32; ++kk)
             umma_e4m3(tmem + 256 + g * 128, v + (kk * 32 * D >> 4), w + (kk * 512 >> 4), id_o, kk > 0);
           umma_commit(smem_u32(&ctl->ofull[g]));
-          umma_commit(smem_u32(&ctl->vempty[i]));
         }
         if (!more) continue;
         const uint32_t g = n & 1, i = n % S, qb = nq & 1;
@@ -416,11 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < D / 32; ++kk)
           umma_e4m3(tmem + g * 128, k + (kk * 32 >> 4), r + (kk * 32 >> 4), id_s, kk > 0);
         umma_commit(smem_u32(&ctl->sfull[g]));
-        umma_commit(smem_u32(&ctl->kempty[i]));
-        if (++x.tile0 == x.tile1) {
-          umma_commit(smem_u32(&ctl->qempty[qb]));
-          ++nq;
-        }
+        if (++x.tile0 == x.tile1) ++nq;
       }
       // every MMA is done before tensor memory is given back (bounded wait)
       umma_commit(smem_u32(&ctl->done));
@@ -471,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = wild ? 0.f : y[e] * f;
           uint32_t w[C::QP];
-          split4<C::QP>(y, w);
+          split4<C::QP>(to_half(y[0], y[1]), to_half(y[2], y[3]), w);
 #pragma unroll
           for (int p = 0; p < C::QP; ++p) {
             const int n = p * R + r;
@@ -501,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
       if (x.tile0 == x.tile1) continue;
       const uint32_t qb = nq & 1;
+      const int rows = x.tag & 0xff;
       wait(&ctl->qfull[qb], (nq >> 1) & 1);
 #pragma unroll 1
       for (int t = x.tile0; t < x.tile1; ++t, ++n) {
@@ -525,14 +524,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           see = 0u;
           if (live) {
 #pragma unroll 1
-            for (int r = 0; r < (x.tag & 0xff); ++r) {
+            for (int r = 0; r < rows; ++r) {
               const int at = ctl->row_at[qb][r];
               see |= (j <= at && !(a.window && j <= at - a.window) ? 1u : 0u) << r;
             }
           }
         }
-        // the scores of rows c .. c + 7, as powers of two, -infinity where a row does not see the key
-        auto load_scores = [&](int c, float (&v)[8]) {
+        // ---- scores, as powers of two, -infinity where a row does not see the key, and the tile's
+        // maxima: lane r has row r's.  More than eight rows' scores wait in tensor memory, over S.
+        const uint64_t kf2 = f32x2(kf, kf);
+        float top = -INFINITY, v[8];
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 8) {
           uint32_t s[C::QP][8];
 #pragma unroll
           for (int p = 0; p < C::QP; ++p) tmem_ld8(scores + p * R + c, s[p]);
@@ -541,26 +544,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&ctl->row_c[qb][c + 4]);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float y = after_wait(s[C::QP - 1][e]);
+          for (int e = 0; e < 8; e += 2) {
+            uint64_t y = f32x2(after_wait(s[C::QP - 1][e]), after_wait(s[C::QP - 1][e + 1]));
 #pragma unroll
-            for (int p = C::QP - 2; p >= 0; --p) y = fmaf(y, 0.0625f, after_wait(s[p][e]));
-            y = y * kf * f[e];
-            v[e] = (see >> c) & (1u << e) ? y : -INFINITY;
+            for (int p = C::QP - 2; p >= 0; --p)
+              y = fma2(y, f32x2(0.0625f, 0.0625f), f32x2(after_wait(s[p][e]), after_wait(s[p][e + 1])));
+            y = mul2(mul2(y, kf2), f32x2(f[e], f[e + 1]));
+            v[e] = (see >> c) & (1u << e) ? lo_of(y) : -INFINITY;
+            v[e + 1] = (see >> c) & (2u << e) ? hi_of(y) : -INFINITY;
           }
-        };
-        // ---- the tile's maxima; lane r has row r's
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < R; c += 8) {
-          float v[8];
-          load_scores(c, v);
+          if constexpr (R > 8) tmem_st8(scores + c, reinterpret_cast<const uint32_t*>(v));
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float y = warp_max(v[e]);
             if (lane - c == e) top = y;
           }
         }
+        if constexpr (R > 8) tmem_wait_st();
         // ---- what V brings: its scale, and rows that must not be multiplied
         wait(&ctl->vfull[i], (n / S) & 1);
         const uint32_t ev = smem[C::kScaleOff + (S + i) * kTile + key];
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           E = 0;
 #pragma unroll 1
-          for (int r = 0; r < (x.tag & 0xff); ++r) {
+          for (int r = 0; r < rows; ++r) {
             const uint32_t y = __reduce_max_sync(0xffffffffu, see >> r & 1u ? own_e : 0u);
             if (lane == r) E = y;
           }
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             E = max(E, ctl->warp_e[g][w][lane]);
           }
           if (top != top) top = -INFINITY;               // (a row of NaN: its weights are NaN all the same)
-          ctl->ref[g][wq][lane] = top == -INFINITY ? 0.f : top - kTop;
+          ctl->ref[g][wq][lane] = top == -INFINITY ? 0.f : kTop - top;
           ctl->fit[g][wq][lane] = __uint_as_float((254u - E) << 23);
         }
         // the last tile's weights and sums of this buffer have been used
@@ -623,29 +623,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- weights: w = p 2^(ev - 127) 2^(127 - E).  (What lies below fp32's normal range between
         // the two factors is 2^-30 of the largest weight or less.)
         const float vf = nan_value ? __uint_as_float(0x7fc00000u) : scale_of(ev);
+        const uint64_t vf2 = f32x2(vf, vf);
 #pragma unroll 1
-        for (int c = 0; c < R; c += 8) {
-          float p[8];
-          load_scores(c, p);
-          float f[8], u[8];
+        for (int c = 0; c < rows; c += 8) {
+          if constexpr (R > 8) {
+            uint32_t s[8];
+            tmem_ld8(scores + c, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = after_wait(s[e]);
+          }
+          float f[8], u[8], p[8];
 #pragma unroll
           for (int e = 0; e < 8; e += 4) {
             *reinterpret_cast<float4*>(f + e) = *reinterpret_cast<const float4*>(&ctl->ref[g][wq][c + e]);
             *reinterpret_cast<float4*>(u + e) = *reinterpret_cast<const float4*>(&ctl->fit[g][wq][c + e]);
           }
-          uint32_t w[2][kParts];
+          uint32_t y[4];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = half * 4 + e;
-              const bool hidden = p[r] == -INFINITY;
-              p[r] = exp2_approx(p[r] - f[r]);
-              y[e] = hidden ? 0.f : p[r] * vf * u[r];    // (not a NaN of a value that it does not see)
-            }
-            split4<kParts>(y, w[half]);
+          for (int e = 0; e < 8; e += 2) {
+            const uint64_t x2 = add2(f32x2(v[e], v[e + 1]), f32x2(f[e], f[e + 1]));
+            p[e] = exp2_approx(lo_of(x2));
+            p[e + 1] = exp2_approx(hi_of(x2));
+            const uint64_t w2 = mul2(mul2(f32x2(p[e], p[e + 1]), vf2), f32x2(u[e], u[e + 1]));
+            // (not a NaN of a value that a row does not see)
+            y[e / 2] = to_half(v[e] == -INFINITY ? 0.f : lo_of(w2), v[e + 1] == -INFINITY ? 0.f : hi_of(w2));
           }
+          uint32_t w[2][kParts];
+          split4<kParts>(y[0], y[1], w[0]);
+          split4<kParts>(y[2], y[3], w[1]);
 #pragma unroll
           for (int k = 0; k < kParts; ++k) {
             const int col = k * R + c;
@@ -684,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit x;
 #pragma unroll 1
     for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
+      const int rows = x.tag & 0xff;
       float acc[R], M = -INFINITY, Lsum = 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[r] = 0.f;
@@ -710,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
         for (int c = 0; c < R; c += 8) {
+          if (c >= rows) break;
           uint32_t y[kParts][8];
 #pragma unroll
           for (int p = 0; p < kParts; ++p) tmem_ld8(lane_at + g * 128 + p * R + c, y[p]);
@@ -729,11 +737,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->oempty[g]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ctl->oempty[g]));
+          mbar_arrive(smem_u32(&ctl->vempty[n % S]));
+        }
       }
       if (*abort_flag) break;
       // lane r: where row r goes
-      const int rows = x.tag & 0xff, f = (x.tag >> kHeadShift) + min(lane, rows - 1), tk = f / a.G;
+      const int f = (x.tag >> kHeadShift) + min(lane, rows - 1), tk = f / a.G;
       const int hd = x.h * a.G + f - tk * a.G;
       const bool whole = x.split >> 8 == 1;
       const int64_t row = (int64_t)(x.row + tk) * H + hd;

@@ -57,6 +57,17 @@ __device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t r[2]) {
                : "r"(taddr));
 }
 
+// 8 consecutive columns of this thread's TMEM lane, written (no wait).
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // The constant upper words of the two kinds of descriptors here, for code that steps through a
 // tile by adding to the lower word (an address in units of 16 bytes).
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);

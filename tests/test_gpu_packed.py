@@ -4,9 +4,9 @@ arithmetic on the same inputs (GPU).
 Tolerances count roundings, as in test_gpu_paged.py, of what the codes stand for.  Beyond those, of the
 kernel for short chunks: queries enter the first product as sums of e4m3 numbers of 4 bits each, two for
 bf16 (which has 8 bits) and three for fp16 (11), down to a floor of 2^-14 (2^-18) where the row's largest
-value is 224 or more: 2^-21 of it.  Softmax weights enter the second product as three such numbers: off by
-2^-12 of themselves (less than eps_t / 2) or, below the floor of 2^-18 where a tile's largest is 256, by
-2^-26 of the row's largest weight.
+value is 224 or more: 2^-21 of it.  Softmax weights enter the second product rounded to fp16 (2^-11 of
+themselves: eps_t / 2 or less), as three such numbers: below their floor of 2^-18, where a tile's largest
+is 256, off by 2^-26 of the row's largest weight.
 """
 import math
 

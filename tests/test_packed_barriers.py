@@ -12,9 +12,9 @@ def packed(seed, units, stages, late=False):
     """Units of (key tiles, whether tiles are edges).  `late`: the softmax reuses the weights' buffer as
     soon as its product is done, before the epilogue has taken the tile's sums."""
     s, ring = Schedule(seed), Ring(15)
-    kfull, kempty = bars(stages, 1), bars(stages, 5)
-    vfull, vempty = bars(stages, 1), bars(stages, 1)
-    qfull, qempty = bars(2, 1), bars(2, 9)
+    kfull, kempty = bars(stages, 1), bars(stages, 4)
+    vfull, vempty = bars(stages, 1), bars(stages, 4)
+    qfull, qempty = bars(2, 1), bars(2, 8)
     sfull, pfull, ofull, oempty = bars(2, 1), bars(2, 4), bars(2, 1), bars(2, 4)
     meet = bars(2, 4)
 
@@ -35,7 +35,7 @@ def packed(seed, units, stages, late=False):
         def values(m):
             yield pfull[m & 1], m >> 1
             yield vfull[m % stages], m // stages
-            s.commits += [ofull[m & 1], vempty[m % stages]]
+            s.commits.append(ofull[m & 1])
         k = left = 0
         fresh = True
         while True:                             # step n: values of tile n - 2, scores of tile n
@@ -51,11 +51,9 @@ def packed(seed, units, stages, late=False):
             if fresh:
                 yield qfull[nq & 1], nq >> 1
             yield kfull[n % stages], n // stages
-            s.commits += [sfull[n & 1], kempty[n % stages]]
+            s.commits.append(sfull[n & 1])
             n, left = n + 1, left - 1
-            if left == 0:
-                s.commits.append(qempty[nq & 1])
-                nq += 1
+            nq += left == 0
         if n >= 1:
             yield from values(n - 1)
 
@@ -110,6 +108,7 @@ def packed(seed, units, stages, late=False):
                 yield ofull[n & 1], n >> 1
                 yield from s.work(8)
                 oempty[n & 1].arrive()
+                vempty[n % stages].arrive()
                 n += 1
             yield from s.work(10)
         yield from ring.get(len(units))
