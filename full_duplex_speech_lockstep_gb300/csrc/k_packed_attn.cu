@@ -7,12 +7,15 @@
 // product:
 //   q = 2^eq (q1 + q2/16 [+ q3/256])     two are exact for bf16's 8 bits, three for fp16's 11
 //   w = w1 + w2/16 + w3/256              fp16's 11 bits; w is at most 256, so 2^-26 of that is its floor
-// Keys are the rows of both products, a thread of the softmax owns one key:
+// Keys are the rows of both products, a thread of the softmax owns a key of each tile:
 //   S[j][r]  = k_j . q_r                 M = 128 keys, N = parts x R rows, K = D
 //   w[j][r]  = 2^(s_jr - m_r + 8) 2^(ev_j - E_r),   s_jr = S c 2^(ek_j + eq_r)
-//   O[d][r]  = sum_j v_jd w_jr           M = D dims, N = 3 x R rows, K = 128 keys
-// m_r is the tile's own maximum and E_r the largest ev that the row sees, so a tile depends on nothing before it; the
-// epilogue adds the tiles up in fp32, in order: acc = acc 2^(M - M') + O 2^(m + E_r - M').
+//   O[d][r]  = sum_j v_jd w_jr           M = D dims, N = 3 x R rows, K = 128 keys a tile
+// A step is 32 / R tiles, so that a thread has 32 scores whatever R is, and what a step costs beside
+// them (barriers, maxima, the epilogue) is the same.  (A tile at a time, 8 rows took as long as 32: 313 us
+// on the 64-session tick.)  m_r is the step's own maximum and E_r the largest ev that the row sees: a step
+// depends on nothing before it.  The epilogue adds the steps up in fp32, in order:
+// acc = acc 2^(M - M') + O 2^(m + E_r - M').
 //
 // A work unit is (sequence, key head, split of its keys, row tile of up to R rows).  Each CTA takes a run
 // of consecutive units with about as many tiles as the others'; a sequence's splits depend on its own
@@ -20,15 +23,18 @@
 // scratch and k_packed_join adds the splits up in split order.
 //
 //   warp 0       the units; K tiles and their scales
-//   warp 1       one thread issues every MMA: O of tile n - 2, then S of tile n
+//   warp 1       one thread issues the MMAs of S
 //   warp 2       V tiles and their scales
-//   warp 3       the units' queries, as parts
-//   warps 4-7, 8-11   softmax of every second tile
+//   warp 3       one thread issues the MMAs of O.  (One thread for both took 1900 clocks a tile.)
+//   warps 4-7, 8-11   softmax of every second step
 //   warps 12-15  epilogue: a thread owns one dim
+//   warps 16-19  the units' queries, as parts.  (One warp took 13000 clocks for 32 rows.)
 //
 // What no row of a unit sees must not reach the second product, where a weight of zero times a NaN
 // would be one: those rows of V are zeroed in shared memory.  An entry that only some rows see and
 // that holds a NaN code is zeroed too, and its scale taken for NaN, which only its seers' weights get.
+#include <type_traits>
+
 #include "pp_paged.cuh"
 #include "pp_tcgen05.cuh"
 
@@ -36,8 +42,9 @@ namespace pp {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kReaders = 15;         // of the units: MMA issuer, V, queries, eight of softmax, epilogue
+constexpr int kThreads = 640;
+constexpr int kReaders = 19;         // of the units: both issuers, V, eight of softmax, epilogue, queries
+constexpr int kSlots = 16;           // tiles whose scales are held
 constexpr int kParts = 3;            // of a weight
 constexpr float kTop = 8.f;          // a tile's largest weight is 2^8 (e4m3 holds up to 448)
 
@@ -46,28 +53,29 @@ struct Cfg {
   static constexpr int QP = sizeof(T) == 2 && Num<T>::kShift == 0.f ? 2 : 3;   // parts of a query
   static constexpr int NQ = (QP * R + 15) / 16 * 16;                 // columns of S
   static constexpr int NP = (kParts * R + 15) / 16 * 16;             // columns of O
+  static constexpr int KT = 32 / R;                                  // tiles of a step
   static constexpr int kTileBytes = kTile * D;
-  static constexpr int S = D == 128 ? (R == 32 && QP == 3 ? 4 : 5) : 8;   // stages of K, and of V
+  static constexpr int KS = D == 128 ? 4 : 8, VS = D == 128 ? 5 : 8;   // stages of K, of V
   static constexpr int kQBytes = NQ * 128;
   static constexpr int kPBytes = NP / 16 * 2048;
-  static constexpr int kVOff = S * kTileBytes;
-  static constexpr int kQOff = 2 * S * kTileBytes;
+  static constexpr int kVOff = KS * kTileBytes;
+  static constexpr int kQOff = (KS + VS) * kTileBytes;
   static constexpr int kPOff = kQOff + 2 * kQBytes;
-  static constexpr int kScaleOff = kPOff + 2 * kPBytes;              // K's, then V's: 128 bytes a stage
-  static constexpr int kCtlOff = kScaleOff + 2 * S * kTile;
+  static constexpr int kScaleOff = kPOff + 2 * KT * kPBytes;         // K's, then V's: 128 bytes a tile
+  static constexpr int kCtlOff = kScaleOff + 2 * kSlots * kTile;
 };
 
 struct Ctl {
   UnitRing ring;
-  uint64_t kfull[8], kempty[8], vfull[8], vempty[8], qfull[2], qempty[2];
+  uint64_t kfull[8], kempty[8], vfull[8], vempty[8], kscale[kSlots], qfull[2], qempty[2];
   uint64_t sfull[2], pfull[2], ofull[2], oempty[2], meet[2], done;
-  uint32_t bad[8];
+  uint32_t bad[kSlots];
   uint32_t tmem;
   int abort;
   // of the two units in flight: each row's factor of its scores (to powers of two) and its entry
   alignas(16) float row_c[2][32];
   int row_at[2][32];
-  // of the two tiles in flight: maxima of rows, and the largest V exponents that they see
+  // of the two steps in flight: maxima of rows, and the largest V exponents that they see
   float warp_max[2][4][32];
   uint32_t warp_e[2][4][32];
   // each warp's copy of the references (negative), and of 2^(127 - E)
@@ -188,27 +196,60 @@ struct Walk {
 };
 
 // ---- loads -----------------------------------------------------------------------------------
-// A tile of codes and its scales, by one warp, a lane to a page.  Pages without a place arrive as zeros,
-// their scales not at all: nobody looks at those.
-__device__ __forceinline__ void load_codes(const Args& a, const CUtensorMap* map, const uint8_t* scales,
-                                           int64_t scale_stride, uint32_t dst, uint32_t scale_dst,
-                                           uint32_t bar, const TilePages& x, int h, int j0, int lane,
-                                           volatile uint32_t* bad_out) {
+// A tile's pages and scales come to the producer's registers ahead of its turn: lane i < pages has page
+// i's number, lane k < 8 the scales of entries 16 k .. 16 k + 15.
+struct Ahead {
+  int j0, end;           // the tile's first entry; entries from here on have no place
+  int raw;               // this lane's table entry, as it lies
+  TilePages pages;
+  uint4 scales;
+};
+__device__ __forceinline__ void find(const Args& a, Ahead& x, int b, int j0, int end, int lane) {
+  const int per = min(1 << a.lps, kTile);
+  x.j0 = j0;
+  x.end = end;
+  const int j = j0 + lane * per;
+  x.raw = lane < kTile / per && j < end ? a.table[(int64_t)b * a.table_ld + (j >> a.lps)] : 0;
+}
+// When the table entries have come: which pages are there, and the scales on their way.  `past`: rows look
+// beyond `end`.
+__device__ __forceinline__ void look(const Args& a, Ahead& x, const uint8_t* scales, int64_t scale_stride,
+                                     int h, bool past, int lane) {
   const int per = min(1 << a.lps, kTile), pages = kTile / per;
-  const bool have = lane < pages && x.page < a.n_pages;
-  const int n = __popc(__ballot_sync(0xffffffffu, have));
+  const bool mine = lane < pages, in = x.j0 + lane * per < x.end;
+  const bool have = mine && in && (unsigned)x.raw < (unsigned)a.n_pages;
+  x.pages.page = have ? x.raw : a.n_pages;
+  x.pages.bad = 0;
+  const uint32_t mask = __ballot_sync(0xffffffffu, mine && !have && (in || past));
+  if (mask) {                                      // rare: from pages to groups of 16
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g) x.pages.bad |= ((mask >> (g * 16 / per)) & 1u) << g;
+  }
+  const int page = __shfl_sync(0xffffffffu, x.pages.page, (lane & 7) * 16 / per);
+  x.scales = make_uint4(0u, 0u, 0u, 0u);
+  if (lane < 8 && page < a.n_pages)
+    x.scales = *reinterpret_cast<const uint4*>(scales + page * scale_stride + ((int64_t)h << a.lps) +
+                                               ((x.j0 + lane * 16) & ((1 << a.lps) - 1)));
+}
+// Pages without a place arrive as zeros.
+// With `scale_bar` (K's) that barrier tells of the scales and of the pages that are missing.
+__device__ __forceinline__ void load_codes(const Args& a, const CUtensorMap* map, const Ahead& x,
+                                           uint32_t dst, uint8_t* scale_dst, uint32_t bar, int h,
+                                           int lane, uint32_t* bad_out, uint64_t* scale_bar) {
+  const int per = min(1 << a.lps, kTile);
+  if (lane < 8) reinterpret_cast<uint4*>(scale_dst)[lane] = x.scales;
+  __syncwarp();
   if (lane == 0) {
-    if (bad_out) *bad_out = x.bad;
-    mbar_expect_tx(bar, (uint32_t)(kTile * a.D + n * per));
+    if (scale_bar) {
+      *bad_out = x.pages.bad;
+      mbar_arrive(smem_u32(scale_bar));
+    }
+    mbar_expect_tx(bar, (uint32_t)(kTile * a.D));
   }
   __syncwarp();
-  if (lane < pages) {
-    const int row = (j0 + lane * per) & ((1 << a.lps) - 1);
-    tma_load_4d(dst + lane * per * a.D, map, 0, row, h, x.page, bar);
-    if (have)
-      bulk_load(scale_dst + lane * per, scales + x.page * scale_stride + ((int64_t)h << a.lps) + row,
-                (uint32_t)per, bar);
-  }
+  if (lane < kTile / per)
+    tma_load_4d(dst + lane * per * a.D, map, 0, (x.j0 + lane * per) & ((1 << a.lps) - 1), h,
+                x.pages.page, bar);
 }
 
 // ---- products --------------------------------------------------------------------------------
@@ -224,6 +265,8 @@ __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead, uint32_t 
   return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)(lead >> 4) << 16 |
          (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)layout << 61;
 }
+
+constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kTile >> 4) << 24);   // fp32 of e4m3, M = 128
 
 // ---- numbers ---------------------------------------------------------------------------------
 // Two values as fp16 (nearest; the first one in the lower half)
@@ -272,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                   const T* q, const int64_t q_stride) {
   using C = Cfg<T, D, R>;
-  constexpr int S = C::S;
+  constexpr int KS = C::KS, VS = C::VS;
+  constexpr uint32_t kRowLayout = D == 128 ? 2 : 4;   // of the tiles, rows of D bytes: swizzled by them
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (an offset, not a rounded pointer: the compiler then knows that it is shared memory)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -281,14 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < KS; ++i) {
       mbar_init(smem_u32(&ctl->kfull[i]), 1);
-      mbar_init(smem_u32(&ctl->kempty[i]), 4);          // softmax, which has waited for the product
-      mbar_init(smem_u32(&ctl->vfull[i]), i == 0 ? 1 + a.withhold : 1);
-      mbar_init(smem_u32(&ctl->vempty[i]), 4);          // epilogue
+      mbar_init(smem_u32(&ctl->kempty[i]), 1);
     }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(smem_u32(&ctl->vfull[i]), i == 0 ? 1 + a.withhold : 1);
+      mbar_init(smem_u32(&ctl->vempty[i]), 1);
+    }
+    for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(&ctl->kscale[i]), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ctl->qfull[i]), 1);
+      mbar_init(smem_u32(&ctl->qfull[i]), 4);
       mbar_init(smem_u32(&ctl->qempty[i]), 8);          // softmax
       mbar_init(smem_u32(&ctl->sfull[i]), 1);
       mbar_init(smem_u32(&ctl->pfull[i]), 4);
@@ -296,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->oempty[i]), 4);
       mbar_init(smem_u32(&ctl->meet[i]), 4);
     }
-    mbar_init(smem_u32(&ctl->done), 1);
+    mbar_init(smem_u32(&ctl->done), 2);
     ring_init(ctl->ring, kReaders);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -324,26 +371,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   // instruction cache)
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase<true>(a, bar, parity, abort_flag); };
   // a unit's tiles of K (of V) and their scales; `part`: their stages' place among the scales
-  auto load_tiles = [&](const Unit& x, uint32_t& n, const CUtensorMap& map, const uint8_t* scales,
-                        int part, uint64_t* full, uint64_t* empty, uint32_t* seen_bad) {
+  auto load_tiles = [&](auto stages, const Unit& x, uint32_t& n, const CUtensorMap& map,
+                        const uint8_t* scales, int part, uint64_t* full, uint64_t* empty,
+                        uint32_t* seen_bad) {
+    constexpr int S = decltype(stages)::value;
     if (x.tile0 == x.tile1) return;
     const bool past = x.nt >= x.stop;
-    TilePages next = find_pages(a, x.b, x.tile0 * kTile, x.stop, past, lane);
+    Ahead now, next;
+    find(a, next, x.b, x.tile0 * kTile, x.stop, lane);
+    look(a, next, scales, kv.scale_stride, x.h, past, lane);
+    now = next;
+    find(a, next, x.b, (x.tile0 + 1) * kTile, x.stop, lane);
 #pragma unroll 1
     for (int t = x.tile0; t < x.tile1; ++t, ++n) {
       const int i = n % S;
-      const TilePages now = next;
-      if (t + 1 < x.tile1) next = find_pages(a, x.b, (t + 1) * kTile, x.stop, past, lane);
+      const Ahead it = now;
+      if (t + 1 < x.tile1) {
+        look(a, next, scales, kv.scale_stride, x.h, past, lane);
+        now = next;
+        find(a, next, x.b, (t + 2) * kTile, x.stop, lane);
+      }
       if (n >= S) wait(&empty[i], (n / S - 1) & 1);
       if (*abort_flag) break;
-      load_codes(a, &map, scales, kv.scale_stride, smem_u32(smem + (part + i) * C::kTileBytes),
-                 smem_u32(smem + C::kScaleOff + (part + i) * kTile), smem_u32(&full[i]), now, x.h,
-                 t * kTile, lane, seen_bad ? &ctl->bad[i] : nullptr);
-      if (seen_bad) *seen_bad |= now.bad;
+      const int slot = n % kSlots;
+      load_codes(a, &map, it, smem_u32(smem + ((part ? KS : 0) + i) * C::kTileBytes),
+                 smem + C::kScaleOff + (part + slot) * kTile, smem_u32(&full[i]), x.h, lane,
+                 &ctl->bad[slot], part ? nullptr : &ctl->kscale[slot]);
+      if (seen_bad) *seen_bad |= it.pages.bad;
     }
   };
   // every copy lands before the CTA may exit (bounded waits)
-  auto drain = [&](uint32_t n, uint64_t* full) {
+  auto drain = [&](auto stages, uint32_t n, uint64_t* full) {
+    constexpr int S = decltype(stages)::value;
     if (lane == 0) {
 #pragma unroll 1
       for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &full[i % S], (i / S) & 1);
@@ -359,76 +418,101 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; !walk.done() && !*abort_flag; walk.next()) {
       const Unit x = walk.unit();
       put_unit<true>(a, ctl->ring, nu++, x, lane, abort_flag);
-      load_tiles(x, n, mapK, kv.k_scale, 0, ctl->kfull, ctl->kempty, &seen_bad);
+      load_tiles(std::integral_constant<int, KS>(), x, n, mapK, kv.k_scale, 0, ctl->kfull, ctl->kempty, &seen_bad);
     }
     Unit last{};
     last.b = -1;
     put_unit<true>(a, ctl->ring, nu, last, lane, abort_flag);
     if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
-    drain(n, ctl->kfull);
+    drain(std::integral_constant<int, KS>(), n, ctl->kfull);
   } else if (warp == 2) {
     // ---- V tiles --------------------------------------------------------------------------
     uint32_t n = 0;
     Unit x;
 #pragma unroll 1
     for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu)
-      load_tiles(x, n, mapV, kv.v_scale, S, ctl->vfull, ctl->vempty, nullptr);
-    drain(n, ctl->vfull);
+      load_tiles(std::integral_constant<int, VS>(), x, n, mapV, kv.v_scale, kSlots, ctl->vfull, ctl->vempty, nullptr);
+    drain(std::integral_constant<int, VS>(), n, ctl->vfull);
   } else if (warp == 1) {
-    // ---- MMA issuer -----------------------------------------------------------------------
+    // ---- MMA issuer of S ------------------------------------------------------------------
     if (lane == 0) {
-      constexpr uint32_t id = (1u << 4) | ((uint32_t)(kTile >> 4) << 24);   // fp32 of e4m3, M = 128
-      constexpr uint32_t id_s = id | ((uint32_t)(C::NQ >> 3) << 17);
-      constexpr uint32_t id_o = id | ((uint32_t)(C::NP >> 3) << 17) | (1u << 15) | (1u << 16);
-      constexpr uint32_t kRow = D == 128 ? 2 : 4;       // the tiles' layout: rows of D bytes, swizzled
-      uint32_t n = 0, nq = 0, nu = 0;
-      Unit x{};
-      bool more = true;                                 // there are tiles to come
-      // step n: O of tile n - 2, S of tile n; two more steps after the last tile
+      constexpr uint32_t id = kIdesc | ((uint32_t)(C::NQ >> 3) << 17);
+      const uint64_t k0 = desc(smem_u32(smem), 0, 8 * D, kRowLayout);
+      const uint64_t q0 = desc(smem_u32(smem + C::kQOff), 0, 1024, 2);
+      uint32_t n = 0, step = 0, nq = 0;
+      Unit x;
 #pragma unroll 1
-      for (uint32_t last = ~0u; n < last; ++n) {
-        const bool fresh = more && x.tile0 == x.tile1;
-        while (more && x.tile0 == x.tile1) more = get_unit<true>(a, ctl->ring, nu++, x, lane, true, abort_flag);
-        if (!more && last == ~0u) last = n + 2;
-        if (n >= 2) {
-          const uint32_t m = n - 2, g = m & 1, i = m % S;
-          wait(&ctl->pfull[g], (m >> 1) & 1);           // (also: S of tile n - 2 has been read)
-          wait(&ctl->vfull[i], (m / S) & 1);
+      for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, true, abort_flag); ++nu) {
+        if (x.tile0 == x.tile1) continue;
+        wait(&ctl->qfull[nq & 1], (nq >> 1) & 1);
+#pragma unroll 1
+        for (int t = x.tile0; t < x.tile1; t += C::KT, ++step) {
+          const uint32_t g = step & 1;
+          if (step >= 2) wait(&ctl->pfull[g], ((step >> 1) - 1) & 1);   // the last S has been read
+#pragma unroll 1
+          for (int k = 0; k < min(C::KT, x.tile1 - t); ++k, ++n) {
+            const uint32_t i = n % KS;
+            wait(&ctl->kfull[i], (n / KS) & 1);
+            if (*abort_flag) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_e4m3(tmem + g * 128 + k * C::NQ, k0 + ((i * C::kTileBytes + kk * 32) >> 4),
+                        q0 + (((nq & 1) * C::kQBytes + kk * 32) >> 4), id, kk > 0);
+            umma_commit(smem_u32(&ctl->kempty[i]));
+          }
           if (*abort_flag) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          // V: dims contiguous, 8 keys to an atom of 8 D bytes (with 64 dims rows 64-127 of the product
-          // are the keys 8 further on, and nobody reads them).  Weights: 16 columns of 8 keys to 128
-          // bytes, keys following each other, the next columns 2048 bytes on.
-          const uint64_t v = desc(smem_u32(smem + C::kVOff + i * C::kTileBytes), 512, 8 * D, kRow);
-          const uint64_t w = desc(smem_u32(smem + C::kPOff + g * C::kPBytes), 128, 2048, 0);
-#pragma unroll
-          for (int kk = 0; kk < kTile / 32; ++kk)
-            umma_e4m3(tmem + 256 + g * 128, v + (kk * 32 * D >> 4), w + (kk * 512 >> 4), id_o, kk > 0);
-          umma_commit(smem_u32(&ctl->ofull[g]));
+          umma_commit(smem_u32(&ctl->sfull[g]));
         }
-        if (!more) continue;
-        const uint32_t g = n & 1, i = n % S, qb = nq & 1;
-        if (fresh) wait(&ctl->qfull[qb], (nq >> 1) & 1);
-        wait(&ctl->kfull[i], (n / S) & 1);
-        if (*abort_flag) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t k = desc(smem_u32(smem + i * C::kTileBytes), 0, 8 * D, kRow);
-        const uint64_t r = desc(smem_u32(smem + C::kQOff + qb * C::kQBytes), 0, 1024, 2);
-#pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk)
-          umma_e4m3(tmem + g * 128, k + (kk * 32 >> 4), r + (kk * 32 >> 4), id_s, kk > 0);
-        umma_commit(smem_u32(&ctl->sfull[g]));
-        if (++x.tile0 == x.tile1) ++nq;
+        ++nq;
       }
-      // every MMA is done before tensor memory is given back (bounded wait)
+      // every MMA is done before tensor memory is given back (bounded waits)
       umma_commit(smem_u32(&ctl->done));
       drain_phase(a, &ctl->done, 0);
     }
     __syncwarp();
   } else if (warp == 3) {
+    // ---- MMA issuer of O ------------------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t id = kIdesc | ((uint32_t)(C::NP >> 3) << 17) | (1u << 15) | (1u << 16);
+      // V: dims contiguous, 8 keys to an atom of 8 D bytes (with 64 dims rows 64-127 of the product are
+      // the keys 8 further on, and nobody reads them).  Weights: 16 columns of 8 keys to 128 bytes, keys
+      // following each other, the next columns 2048 bytes on.
+      const uint64_t v0 = desc(smem_u32(smem + C::kVOff), 512, 8 * D, kRowLayout);
+      const uint64_t w0 = desc(smem_u32(smem + C::kPOff), 128, 2048, 0);
+      uint32_t n = 0, step = 0;
+      Unit x;
+#pragma unroll 1
+      for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, true, abort_flag); ++nu) {
+#pragma unroll 1
+        for (int t = x.tile0; t < x.tile1; t += C::KT, ++step) {
+          const uint32_t g = step & 1;
+          wait(&ctl->pfull[g], (step >> 1) & 1);        // (whose arrivals have waited for the last O)
+#pragma unroll 1
+          for (int k = 0; k < min(C::KT, x.tile1 - t); ++k, ++n) {
+            const uint32_t i = n % VS;
+            wait(&ctl->vfull[i], (n / VS) & 1);
+            if (*abort_flag) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+            for (int kk = 0; kk < kTile / 32; ++kk)
+              umma_e4m3(tmem + 256 + g * 128, v0 + ((i * C::kTileBytes + kk * 32 * D) >> 4),
+                        w0 + (((g * C::KT + k) * C::kPBytes + kk * 512) >> 4), id, k + kk > 0);
+            umma_commit(smem_u32(&ctl->vempty[i]));
+          }
+          if (*abort_flag) break;
+          umma_commit(smem_u32(&ctl->ofull[g]));
+        }
+      }
+      umma_commit(smem_u32(&ctl->done));
+      drain_phase(a, &ctl->done, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 16) {
     // ---- queries: L lanes to a row, four dims to a lane -----------------------------------
-    constexpr int L = D / 4, kSide = 32 / L, kAhead = 4;   // rows side by side; passes loaded at once
-    const int l = lane % L, side = lane / L;
+    constexpr int L = D / 4, kSide = 4 * 32 / L;           // rows side by side, of four warps
+    constexpr int kAhead = R / kSide < 4 ? R / kSide : 4;  // passes loaded at once
+    const int l = lane % L, side = (threadIdx.x - 512) / L;
     const uint32_t per_head = (65536u + a.G - 1) / a.G;    // f / G for f G < 2^16
     uint32_t nq = 0;
     Unit x;
@@ -442,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const T* base = q + (int64_t)x.row * q_stride + (int64_t)x.h * a.G * D + l * 4;
       uint8_t* to = smem + C::kQOff + qb * C::kQBytes;
 #pragma unroll 1
-      for (int r0 = 0; r0 < R; r0 += kSide * kAhead) {
+      for (int r0 = 0; r0 < rows; r0 += kSide * kAhead) {
         uint2 raw[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
@@ -492,110 +576,148 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t g = warp >= 8;
     const int wq = warp & 3, key = wq * 32 + lane;
     const uint32_t scores = tmem + ((uint32_t)(wq * 32) << 16) + g * 128;
-    uint8_t* const weights = smem + C::kPOff + g * C::kPBytes + key * 16;
-    uint32_t n = 0, nq = 0, meets = 0;
+    uint8_t* const weights = smem + C::kPOff + g * C::KT * C::kPBytes + key * 16;
+    uint32_t n = 0, step = 0, nq = 0, meets = 0;
     Unit x;
 #pragma unroll 1
     for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
       if (x.tile0 == x.tile1) continue;
       const uint32_t qb = nq & 1;
       const int rows = x.tag & 0xff;
+      const bool mixed = x.first != x.nt;                // rows of several tokens
       wait(&ctl->qfull[qb], (nq >> 1) & 1);
 #pragma unroll 1
-      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
-        if ((n & 1) != g) continue;
+      for (int t = x.tile0; t < x.tile1; t += C::KT, ++step) {
+        const int tiles = min(C::KT, x.tile1 - t);
+        n += tiles;
+        if ((step & 1) != g) continue;
         if (*abort_flag) break;
-        const int i = n % S, j = t * kTile + key;
-        wait(&ctl->sfull[g], (n >> 1) & 1);
+        const uint32_t n0 = n - tiles;                   // the step's first tile
+        auto k_scale = [&](int k) { return scale_of(smem[C::kScaleOff + (n0 + k) % kSlots * kTile + key]); };
+        auto v_scale = [&](int k) -> uint32_t {
+          return smem[C::kScaleOff + (kSlots + (n0 + k) % kSlots) * kTile + key];
+        };
+        wait(&ctl->sfull[g], (step >> 1) & 1);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        // (the first product has seen this phase of K, and the next one waits for this warp)
-        wait(&ctl->kfull[i], (n / S) & 1);
-        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&ctl->bad[i]);
-        const float kf = scale_of(smem[C::kScaleOff + i * kTile + key]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->kempty[i]));
-        // does every row see every key of the tile?
-        const bool edge = bad != 0 || t * kTile + kTile - 1 > min(x.first, x.stop - 1) ||
+        uint32_t bad = 0;
+#pragma unroll 1
+        for (int k = 0; k < tiles; ++k) {                // (they have come, with the tiles)
+          wait(&ctl->kscale[(n0 + k) % kSlots], ((n0 + k) / kSlots) & 1);
+          bad |= ctl->bad[(n0 + k) % kSlots];
+        }
+        // does every row see every key of the step?
+        const int j0 = t * kTile + key;
+        const bool edge = bad != 0 || (t + tiles) * kTile - 1 > min(x.first, x.stop - 1) ||
                           (a.window && t * kTile <= x.nt - a.window);
-        uint32_t see = ~0u;                              // a bit for each row that sees this key
-        bool live = true;                                // some row does
+        uint32_t see = ~0u;                              // bit k R + r: row r sees this thread's key of tile k
+        uint32_t live = ~0u;                             // bit k: some row does
         if (edge) {
-          live = j < x.stop && j >= x.low && !((bad >> (key >> 4)) & 1u);
-          see = 0u;
-          if (live) {
+          see = live = 0u;
+#pragma unroll 1
+          for (int k = 0; k < tiles; ++k) {
+            const int j = j0 + k * kTile;
+            if (j >= x.stop || j < x.low || (ctl->bad[(n0 + k) % kSlots] >> (key >> 4) & 1u)) continue;
+            live |= 1u << k;
+            if (!mixed) {
+              see |= (R == 32 ? ~0u : (1u << (R & 31)) - 1u) << (k * R);
+              continue;
+            }
 #pragma unroll 1
             for (int r = 0; r < rows; ++r) {
               const int at = ctl->row_at[qb][r];
-              see |= (j <= at && !(a.window && j <= at - a.window) ? 1u : 0u) << r;
+              see |= (j <= at && !(a.window && j <= at - a.window) ? 1u : 0u) << (k * R + r);
             }
           }
         }
-        // ---- scores, as powers of two, -infinity where a row does not see the key, and the tile's
-        // maxima: lane r has row r's.  More than eight rows' scores wait in tensor memory, over S.
-        const uint64_t kf2 = f32x2(kf, kf);
-        float top = -INFINITY, v[8];
+        // ---- scores, as powers of two, -infinity where a row does not see the key, and the step's
+        // maxima: lane r has row r's.  The scores wait in tensor memory, over S.
+        float top = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < rows; c += 8) {
-          uint32_t s[C::QP][8];
-#pragma unroll
-          for (int p = 0; p < C::QP; ++p) tmem_ld8(scores + p * R + c, s[p]);
-          float f[8];
+          float most[8], f[8];
           *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&ctl->row_c[qb][c]);
           *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&ctl->row_c[qb][c + 4]);
-          tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            uint64_t y = f32x2(after_wait(s[C::QP - 1][e]), after_wait(s[C::QP - 1][e + 1]));
+          for (int e = 0; e < 8; ++e) most[e] = -INFINITY;
+#pragma unroll 1
+          for (int k = 0; k < tiles; ++k) {
+            uint32_t s[C::QP][8];
 #pragma unroll
-            for (int p = C::QP - 2; p >= 0; --p)
-              y = fma2(y, f32x2(0.0625f, 0.0625f), f32x2(after_wait(s[p][e]), after_wait(s[p][e + 1])));
-            y = mul2(mul2(y, kf2), f32x2(f[e], f[e + 1]));
-            v[e] = (see >> c) & (1u << e) ? lo_of(y) : -INFINITY;
-            v[e + 1] = (see >> c) & (2u << e) ? hi_of(y) : -INFINITY;
+            for (int p = 0; p < C::QP; ++p) tmem_ld8(scores + k * C::NQ + p * R + c, s[p]);
+            const float kf = k_scale(k);
+            const uint64_t kf2 = f32x2(kf, kf);
+            const uint32_t seen = see >> (k * R + c);
+            float v[8];
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              uint64_t y = f32x2(after_wait(s[C::QP - 1][e]), after_wait(s[C::QP - 1][e + 1]));
+#pragma unroll
+              for (int p = C::QP - 2; p >= 0; --p)
+                y = fma2(y, f32x2(0.0625f, 0.0625f), f32x2(after_wait(s[p][e]), after_wait(s[p][e + 1])));
+              y = mul2(mul2(y, kf2), f32x2(f[e], f[e + 1]));
+              v[e] = seen & (1u << e) ? lo_of(y) : -INFINITY;
+              v[e + 1] = seen & (2u << e) ? hi_of(y) : -INFINITY;
+            }
+            tmem_st8(scores + k * C::NQ + c, reinterpret_cast<const uint32_t*>(v));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most[e] = fmaxf(most[e], v[e]);
           }
-          if constexpr (R > 8) tmem_st8(scores + c, reinterpret_cast<const uint32_t*>(v));
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float y = warp_max(v[e]);
+            const float y = warp_max(most[e]);
             if (lane - c == e) top = y;
           }
         }
-        if constexpr (R > 8) tmem_wait_st();
-        // ---- what V brings: its scale, and rows that must not be multiplied
-        wait(&ctl->vfull[i], (n / S) & 1);
-        const uint32_t ev = smem[C::kScaleOff + (S + i) * kTile + key];
-        bool nan_value = ev == 255u;
-        const uint32_t own_e = nan_value ? 0u : ev;
-        // each row goes by the exponents that it sees: another's could take its weights below e4m3
-        uint32_t E;
-        if (!edge) {
-          E = __reduce_max_sync(0xffffffffu, own_e);
-        } else {
-          E = 0;
+        tmem_wait_st();
+        // ---- what V brings: its scales, and rows that must not be multiplied
+        uint32_t nan_value = 0, E = 0;                   // bit k: the value of tile k reads as NaN
 #pragma unroll 1
-          for (int r = 0; r < rows; ++r) {
-            const uint32_t y = __reduce_max_sync(0xffffffffu, see >> r & 1u ? own_e : 0u);
-            if (lane == r) E = y;
-          }
+        for (int k = 0; k < tiles; ++k) {
+          const uint32_t i = (n0 + k) % VS;
+          wait(&ctl->vfull[i], ((n0 + k) / VS) & 1);
+          const uint32_t ev = v_scale(k);
+          if (ev == 255u) nan_value |= 1u << k;
+          if (live >> k & 1u) E = max(E, ev == 255u ? 0u : ev);
+          if (!edge) continue;
+          const int j = j0 + k * kTile;
           uint4* row = reinterpret_cast<uint4*>(smem + C::kVOff + i * C::kTileBytes + key * D);
-          bool clear = !live;
-          if (live && !(j <= x.first && (!a.window || j > x.nt - a.window))) {
+          bool clear = !(live >> k & 1u);
+          if (!clear && !(j <= x.first && (!a.window || j > x.nt - a.window))) {
             // some rows do not see it: its NaN codes must not meet their weights of zero
             uint32_t z = 0;
 #pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              const uint4 w = row[k];
+            for (int y = 0; y < D / 16; ++y) {
+              const uint4 w = row[y];
               z |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
                    ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
             }
             clear = (z & 0x80808080u) != 0;
-            nan_value |= clear;
+            if (clear) nan_value |= 1u << k;
           }
           if (clear) {
 #pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) row[k] = make_uint4(0u, 0u, 0u, 0u);
+            for (int y = 0; y < D / 16; ++y) row[y] = make_uint4(0u, 0u, 0u, 0u);
           }
-          __syncwarp();
+        }
+        __syncwarp();
+        if (!edge || !mixed) {
+          E = __reduce_max_sync(0xffffffffu, E);
+        } else {
+          // each row goes by the exponents that it sees: another's could take its weights below e4m3
+          uint32_t own = 0;
+#pragma unroll 1
+          for (int r = 0; r < rows; ++r) {
+            uint32_t y = 0;
+#pragma unroll 1
+            for (int k = 0; k < tiles; ++k) {
+              const uint32_t ev = v_scale(k);
+              if (see >> (k * R + r) & 1u) y = max(y, ev == 255u ? 0u : ev);
+            }
+            y = __reduce_max_sync(0xffffffffu, y);
+            if (lane == r) own = y;
+          }
+          E = own;
         }
         if (lane < R) {
           ctl->warp_max[g][wq][lane] = top;
@@ -613,8 +735,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ctl->ref[g][wq][lane] = top == -INFINITY ? 0.f : kTop - top;
           ctl->fit[g][wq][lane] = __uint_as_float((254u - E) << 23);
         }
-        // the last tile's weights and sums of this buffer have been used
-        if (n >= 2) wait(&ctl->oempty[g], ((n >> 1) - 1) & 1);
+        // the last step's weights and sums of this buffer have been used
+        if (step >= 2) wait(&ctl->oempty[g], ((step >> 1) - 1) & 1);
         if (wq == 0 && lane < R) {
           ctl->m[g][lane] = top - kTop;
           ctl->e[g][lane] = E;
@@ -622,41 +744,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         // ---- weights: w = p 2^(ev - 127) 2^(127 - E).  (What lies below fp32's normal range between
         // the two factors is 2^-30 of the largest weight or less.)
-        const float vf = nan_value ? __uint_as_float(0x7fc00000u) : scale_of(ev);
-        const uint64_t vf2 = f32x2(vf, vf);
 #pragma unroll 1
         for (int c = 0; c < rows; c += 8) {
-          if constexpr (R > 8) {
-            uint32_t s[8];
-            tmem_ld8(scores + c, s);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = after_wait(s[e]);
-          }
-          float f[8], u[8], p[8];
+          float f[8], u[8], sum[8];
 #pragma unroll
           for (int e = 0; e < 8; e += 4) {
             *reinterpret_cast<float4*>(f + e) = *reinterpret_cast<const float4*>(&ctl->ref[g][wq][c + e]);
             *reinterpret_cast<float4*>(u + e) = *reinterpret_cast<const float4*>(&ctl->fit[g][wq][c + e]);
           }
-          uint32_t y[4];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const uint64_t x2 = add2(f32x2(v[e], v[e + 1]), f32x2(f[e], f[e + 1]));
-            p[e] = exp2_approx(lo_of(x2));
-            p[e + 1] = exp2_approx(hi_of(x2));
-            const uint64_t w2 = mul2(mul2(f32x2(p[e], p[e + 1]), vf2), f32x2(u[e], u[e + 1]));
-            // (not a NaN of a value that a row does not see)
-            y[e / 2] = to_half(v[e] == -INFINITY ? 0.f : lo_of(w2), v[e + 1] == -INFINITY ? 0.f : hi_of(w2));
-          }
-          uint32_t w[2][kParts];
-          split4<kParts>(y[0], y[1], w[0]);
-          split4<kParts>(y[2], y[3], w[1]);
+          for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < tiles; ++k) {
+            uint32_t s[8];
+            tmem_ld8(scores + k * C::NQ + c, s);
+            const float vf = nan_value >> k & 1u ? __uint_as_float(0x7fc00000u) : scale_of(v_scale(k));
+            const uint64_t vf2 = f32x2(vf, vf);
+            tmem_wait_ld();
+            uint32_t y[4];
 #pragma unroll
-          for (int k = 0; k < kParts; ++k) {
-            const int col = k * R + c;
-            *reinterpret_cast<uint2*>(weights + (col >> 4) * 2048 + (col & 15)) =
-                make_uint2(w[0][k], w[1][k]);
+            for (int e = 0; e < 8; e += 2) {
+              const float v0 = after_wait(s[e]), v1 = after_wait(s[e + 1]);
+              const uint64_t x2 = add2(f32x2(v0, v1), f32x2(f[e], f[e + 1]));
+              const float p0 = exp2_approx(lo_of(x2)), p1 = exp2_approx(hi_of(x2));
+              const uint64_t w2 = mul2(mul2(f32x2(p0, p1), vf2), f32x2(u[e], u[e + 1]));
+              // (not a NaN of a value that a row does not see)
+              y[e / 2] = to_half(v0 == -INFINITY ? 0.f : lo_of(w2), v1 == -INFINITY ? 0.f : hi_of(w2));
+              sum[e] += p0;
+              sum[e + 1] += p1;
+            }
+            uint32_t w[2][kParts];
+            split4<kParts>(y[0], y[1], w[0]);
+            split4<kParts>(y[2], y[3], w[1]);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+              const int col = p * R + c;
+              *reinterpret_cast<uint2*>(weights + k * C::kPBytes + (col >> 4) * 2048 + (col & 15)) =
+                  make_uint2(w[0][p], w[1][p]);
+            }
           }
           // sums of the eight rows over the warp's keys: lanes halve the rows, then the keys
 #pragma unroll
@@ -664,14 +789,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool up = lane & d;
 #pragma unroll
             for (int e = 0; e < k; ++e) {
-              const float give = up ? p[e] : p[e + k];
-              p[e] = (up ? p[e + k] : p[e]) + __shfl_xor_sync(0xffffffffu, give, d);
+              const float give = up ? sum[e] : sum[e + k];
+              sum[e] = (up ? sum[e + k] : sum[e]) + __shfl_xor_sync(0xffffffffu, give, d);
             }
           }
-          p[0] += __shfl_xor_sync(0xffffffffu, p[0], 2);
-          p[0] += __shfl_xor_sync(0xffffffffu, p[0], 1);
+          sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
+          sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
           if ((lane & 3) == 0)
-            ctl->l[g][wq][c + (lane >> 2 & 1) + (lane >> 3 & 1) * 2 + (lane >> 4) * 4] = p[0];
+            ctl->l[g][wq][c + (lane >> 2 & 1) + (lane >> 3 & 1) * 2 + (lane >> 4) * 4] = sum[0];
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -686,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- epilogue: thread d owns dim d; lane r of each warp keeps row r's maximum and sum ---
     const int wq = warp & 3, d = wq * 32 + lane, H = a.Hk * a.G;
     const uint32_t lane_at = tmem + ((uint32_t)(wq * 32) << 16) + 256;
-    uint32_t n = 0;
+    uint32_t step = 0;
     Unit x;
 #pragma unroll 1
     for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
@@ -695,8 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[r] = 0.f;
 #pragma unroll 1
-      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
-        const uint32_t g = n & 1, ph = (n >> 1) & 1;
+      for (int t = x.tile0; t < x.tile1; t += C::KT, ++step) {
+        const uint32_t g = step & 1, ph = (step >> 1) & 1;
         wait(&ctl->pfull[g], ph);                        // sums and maxima
         if (lane < R) {
           const float m = ctl->m[g][lane];
@@ -737,10 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&ctl->oempty[g]));
-          mbar_arrive(smem_u32(&ctl->vempty[n % S]));
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->oempty[g]));
       }
       if (*abort_flag) break;
       // lane r: where row r goes
@@ -804,7 +926,8 @@ template <typename T, int D, int R>
 cudaError_t run(const Args& a, const PackedPlan& p, const Maps& maps, const AttnOut& o, const Packed& kv,
                 const void* q, int64_t q_stride, cudaStream_t s) {
   using C = Cfg<T, D, R>;
-  static_assert(C::kQBytes % 1024 == 0 && C::kPBytes % 1024 == 0 && C::NQ <= 128 && C::NP <= 128,
+  static_assert(C::KS + 2 * C::KT <= kSlots, "scales outlive the steps that are under way");
+  static_assert(C::kQBytes % 1024 == 0 && C::kPBytes % 1024 == 0 && C::KT * C::NQ <= 128 && C::NP <= 128,
                 "operands start on 1024 bytes, products fit their columns");
   const size_t smem = C::kCtlOff + sizeof(Ctl) + (size_t)(a.n_seqs + 1) * sizeof(int64_t) + 1024;
   constexpr size_t most_smem = C::kCtlOff + sizeof(Ctl) + (kMaxSeqs + 1) * sizeof(int64_t) + 1024;

@@ -8,54 +8,70 @@ import pytest
 from test_paged_barriers import SEEDS, Bar, Ring, Schedule, bars  # noqa: F401
 
 
-def packed(seed, units, stages, late=False):
-    """Units of (key tiles, whether tiles are edges).  `late`: the softmax reuses the weights' buffer as
-    soon as its product is done, before the epilogue has taken the tile's sums."""
-    s, ring = Schedule(seed), Ring(15)
-    kfull, kempty = bars(stages, 1), bars(stages, 4)
-    vfull, vempty = bars(stages, 1), bars(stages, 4)
-    qfull, qempty = bars(2, 1), bars(2, 8)
-    sfull, pfull, ofull, oempty = bars(2, 1), bars(2, 4), bars(2, 1), bars(2, 4)
-    meet = bars(2, 4)
+SLOTS = 16     # tiles whose scales are held
 
-    def tiles(full, empty, unit):
-        n = 0
+
+def packed(seed, units, stages, most, late=False):
+    """Units of so many key tiles, in steps of up to `most`.  `late`: the softmax reuses the weights' buffer as
+    soon as its product is done, before the epilogue has taken the step's sums."""
+    s, ring = Schedule(seed), Ring(19)
+    ks, vs = stages
+    kfull, kempty, vfull, vempty = bars(ks, 1), bars(ks, 1), bars(vs, 1), bars(vs, 1)
+    kscale, qfull, qempty = bars(SLOTS, 1), bars(2, 4), bars(2, 8)
+    sfull, pfull, ofull, oempty = bars(2, 1), bars(2, 4), bars(2, 1), bars(2, 4)
+    meet, held = bars(2, 4), {"k": {}, "v": {}}
+
+    def steps(count):
+        return [min(most, count - t) for t in range(0, count, most)]
+
+    def tiles(name, full, empty, unit):
+        n, size = 0, len(full)
         for k, count in enumerate(units):
             yield from unit(k)
             for _ in range(count):
-                if n >= stages:
-                    yield empty[n % stages], n // stages - 1
-                s.load(full[n % stages])
+                if n >= size:
+                    yield empty[n % size], n // size - 1
+                # the scales of the tile that had this place are no longer looked at
+                assert held[name].get(n % SLOTS, 0) == 0, "scales overwritten"
+                held[name][n % SLOTS] = 8 // 2
+                if name == "k":
+                    kscale[n % SLOTS].arrive()
+                s.load(full[n % size])
                 n += 1
         yield from unit(len(units))
 
-    def issuer():
-        n = nq = 0
+    def scores():
+        n = step = nq = 0
+        for k, count in enumerate(units):
+            yield from ring.get(k)
+            if not count:
+                continue
+            yield qfull[nq & 1], nq >> 1
+            for kt in steps(count):
+                if step >= 2:
+                    yield pfull[step & 1], (step >> 1) - 1
+                for _ in range(kt):
+                    yield kfull[n % ks], n // ks
+                    s.commits.append(kempty[n % ks])
+                    n += 1
+                s.commits.append(sfull[step & 1])
+                step += 1
+            nq += 1
+        yield from ring.get(len(units))
 
-        def values(m):
-            yield pfull[m & 1], m >> 1
-            yield vfull[m % stages], m // stages
-            s.commits.append(ofull[m & 1])
-        k = left = 0
-        fresh = True
-        while True:                             # step n: values of tile n - 2, scores of tile n
-            fresh = left == 0
-            while left == 0 and k <= len(units):
-                yield from ring.get(k)
-                left = units[k] if k < len(units) else 0
-                k += 1
-            if n >= 2:
-                yield from values(n - 2)
-            if left == 0:
-                break
-            if fresh:
-                yield qfull[nq & 1], nq >> 1
-            yield kfull[n % stages], n // stages
-            s.commits.append(sfull[n & 1])
-            n, left = n + 1, left - 1
-            nq += left == 0
-        if n >= 1:
-            yield from values(n - 1)
+    def values():
+        n = step = 0
+        for k, count in enumerate(units):
+            yield from ring.get(k)
+            for kt in steps(count):
+                yield pfull[step & 1], step >> 1
+                for _ in range(kt):
+                    yield vfull[n % vs], n // vs
+                    s.commits.append(vempty[n % vs])
+                    n += 1
+                s.commits.append(ofull[step & 1])
+                step += 1
+        yield from ring.get(len(units))
 
     def queries():
         nq = 0
@@ -71,62 +87,67 @@ def packed(seed, units, stages, late=False):
         yield from ring.get(len(units))
 
     def softmax(g):
-        n = nq = met = 0
+        n = step = nq = met = 0
         for k, count in enumerate(units):
             yield from ring.get(k)
             if not count:
                 continue
             yield qfull[nq & 1], nq >> 1
-            for _ in range(count):
-                if (n & 1) == g:
-                    yield sfull[g], n >> 1
-                    yield kfull[n % stages], n // stages
-                    kempty[n % stages].arrive()
+            for kt in steps(count):
+                n += kt
+                if (step & 1) == g:
+                    mine = range(n - kt, n)
+                    yield sfull[g], step >> 1
+                    for m in mine:
+                        yield kscale[m % SLOTS], m // SLOTS
                     yield from s.work(5)
-                    yield vfull[n % stages], n // stages
+                    for m in mine:
+                        held["k"][m % SLOTS] -= 1
+                        yield vfull[m % vs], m // vs
                     meet[g].arrive()
                     yield meet[g], met
                     met += 1
-                    if n >= 2:
-                        if late:
-                            yield ofull[g], (n >> 1) - 1
-                        else:
-                            yield oempty[g], (n >> 1) - 1
+                    if step >= 2:
+                        yield (ofull if late else oempty)[g], (step >> 1) - 1
                     yield from s.work(5)
+                    for m in mine:
+                        held["v"][m % SLOTS] -= 1
                     pfull[g].arrive()
-                n += 1
+                step += 1
             qempty[nq & 1].arrive()
             nq += 1
         yield from ring.get(len(units))
 
     def epilogue():
-        n = 0
+        step = 0
         for k, count in enumerate(units):
             yield from ring.get(k)
-            for _ in range(count):
-                yield pfull[n & 1], n >> 1
-                yield ofull[n & 1], n >> 1
+            for _ in steps(count):
+                yield pfull[step & 1], step >> 1
+                yield ofull[step & 1], step >> 1
                 yield from s.work(8)
-                oempty[n & 1].arrive()
-                vempty[n % stages].arrive()
-                n += 1
+                oempty[step & 1].arrive()
+                step += 1
             yield from s.work(10)
         yield from ring.get(len(units))
 
-    s.run([tiles(kfull, kempty, ring.put), tiles(vfull, vempty, ring.get), issuer(), queries()] +
-          [softmax(w // 4) for w in range(8)] + [epilogue() for _ in range(4)])
+    s.run([tiles("k", kfull, kempty, ring.put), tiles("v", vfull, vempty, ring.get), scores(), values()] +
+          [softmax(w // 4) for w in range(8)] + [epilogue() for _ in range(4)] +
+          [queries() for _ in range(4)])
 
 
-@pytest.mark.parametrize("stages", [4, 5, 8])
+@pytest.mark.parametrize("most", [1, 2, 4])
+@pytest.mark.parametrize("stages", [(4, 5), (8, 8)])
 @pytest.mark.parametrize("seed", SEEDS)
-def test_packed_attention(seed, stages):
+def test_packed_attention(seed, stages, most):
     r = random.Random(seed)
-    packed(seed, [r.choice([0, 1, 1, 2, 3, 4, 8]) for _ in range(30)], stages)
-    packed(seed, [r.choice([0, 1, 1, 2]) for _ in range(60)], stages)
-    packed(seed, [1] * 40, stages)
+    packed(seed, [r.choice([0, 1, 1, 2, 3, 4, 8]) for _ in range(30)], stages, most)
+    packed(seed, [r.choice([0, 1, 1, 2]) for _ in range(60)], stages, most)
+    packed(seed, [1] * 40, stages, most)
+    packed(seed, [37, 64], stages, most)
 
 
 def test_a_buffer_that_is_used_again_too_early_mistakes_a_phase():
     with pytest.raises(AssertionError, match="phase|deadlock"):
         for seed in range(200):
-            packed(seed, [9, 1, 1, 30, 2], 5, late=True)
+            packed(seed, [9, 1, 1, 30, 2], (4, 5), 1, late=True)
