@@ -67,9 +67,10 @@ struct Cfg {
 
 struct Ctl {
   UnitRing ring;
-  uint64_t kfull[8], kempty[8], vfull[8], vempty[8], kscale[kSlots], qfull[2], qempty[2];
+  uint64_t kfull[8], kempty[8], vfull[8], vempty[8], qfull[2], qempty[2];
   uint64_t sfull[2], pfull[2], ofull[2], oempty[2], meet[2], done;
   uint32_t bad[kSlots];
+  int any_bad;                         // a tile of this CTA had a page that is missing
   uint32_t tmem;
   int abort;
   // of the two units in flight: each row's factor of its scores (to powers of two) and its entry
@@ -196,60 +197,53 @@ struct Walk {
 };
 
 // ---- loads -----------------------------------------------------------------------------------
-// A tile's pages and scales come to the producer's registers ahead of its turn: lane i < pages has page
-// i's number, lane k < 8 the scales of entries 16 k .. 16 k + 15.
+// Scales go by asynchronous copies of 16 bytes, a lane to each: a bulk copy for every page was slower with
+// pages of 16, and through registers a tile waits for memory's latency.
+constexpr int kScaleLanes = kTile / 16;
+// A tile's table entries come to the producer's registers ahead of its turn, a lane to a page.
 struct Ahead {
   int j0, end;           // the tile's first entry; entries from here on have no place
   int raw;               // this lane's table entry, as it lies
-  TilePages pages;
-  uint4 scales;
 };
-__device__ __forceinline__ void find(const Args& a, Ahead& x, int b, int j0, int end, int lane) {
-  const int per = min(1 << a.lps, kTile);
-  x.j0 = j0;
-  x.end = end;
-  const int j = j0 + lane * per;
-  x.raw = lane < kTile / per && j < end ? a.table[(int64_t)b * a.table_ld + (j >> a.lps)] : 0;
+__device__ __forceinline__ Ahead find(const Args& a, int b, int j0, int end, int lane) {
+  const int per = min(1 << a.lps, kTile), j = j0 + lane * per;
+  return Ahead{j0, end, lane < kTile / per && j < end ? a.table[(int64_t)b * a.table_ld + (j >> a.lps)] : 0};
 }
-// When the table entries have come: which pages are there, and the scales on their way.  `past`: rows look
-// beyond `end`.
-__device__ __forceinline__ void look(const Args& a, Ahead& x, const uint8_t* scales, int64_t scale_stride,
-                                     int h, bool past, int lane) {
-  const int per = min(1 << a.lps, kTile), pages = kTile / per;
+// Codes and scales of a tile; pages without a place arrive as zeros.  `past`: rows look beyond the tile's
+// end.  Returns the 16-key groups without a page.
+__device__ __forceinline__ uint32_t load_codes(const Args& a, const CUtensorMap* map, const uint8_t* scales,
+                                               int64_t scale_stride, const Ahead& x, bool past, int h,
+                                               uint32_t dst, uint32_t scale_dst, uint32_t bar, int lane,
+                                               uint32_t* bad_out, int* any_bad) {
+  const int per = min(1 << a.lps, kTile), pages = kTile / per, in_page = (1 << a.lps) - 1;
   const bool mine = lane < pages, in = x.j0 + lane * per < x.end;
   const bool have = mine && in && (unsigned)x.raw < (unsigned)a.n_pages;
-  x.pages.page = have ? x.raw : a.n_pages;
-  x.pages.bad = 0;
+  const int page = have ? x.raw : a.n_pages;
   const uint32_t mask = __ballot_sync(0xffffffffu, mine && !have && (in || past));
+  uint32_t bad = 0;
   if (mask) {                                      // rare: from pages to groups of 16
 #pragma unroll 1
-    for (int g = 0; g < 8; ++g) x.pages.bad |= ((mask >> (g * 16 / per)) & 1u) << g;
+    for (int g = 0; g < 8; ++g) bad |= ((mask >> (g * 16 / per)) & 1u) << g;
   }
-  const int page = __shfl_sync(0xffffffffu, x.pages.page, (lane & 7) * 16 / per);
-  x.scales = make_uint4(0u, 0u, 0u, 0u);
-  if (lane < 8 && page < a.n_pages)
-    x.scales = *reinterpret_cast<const uint4*>(scales + page * scale_stride + ((int64_t)h << a.lps) +
-                                               ((x.j0 + lane * 16) & ((1 << a.lps) - 1)));
-}
-// Pages without a place arrive as zeros.
-// With `scale_bar` (K's) that barrier tells of the scales and of the pages that are missing.
-__device__ __forceinline__ void load_codes(const Args& a, const CUtensorMap* map, const Ahead& x,
-                                           uint32_t dst, uint8_t* scale_dst, uint32_t bar, int h,
-                                           int lane, uint32_t* bad_out, uint64_t* scale_bar) {
-  const int per = min(1 << a.lps, kTile);
-  if (lane < 8) reinterpret_cast<uint4*>(scale_dst)[lane] = x.scales;
-  __syncwarp();
   if (lane == 0) {
-    if (scale_bar) {
-      *bad_out = x.pages.bad;
-      mbar_arrive(smem_u32(scale_bar));
+    if (bad_out) {
+      *bad_out = bad;
+      if (bad) *any_bad = 1;
     }
     mbar_expect_tx(bar, (uint32_t)(kTile * a.D));
   }
-  __syncwarp();
-  if (lane < kTile / per)
-    tma_load_4d(dst + lane * per * a.D, map, 0, (x.j0 + lane * per) & ((1 << a.lps) - 1), h,
-                x.pages.page, bar);
+  const int from = __shfl_sync(0xffffffffu, page, (lane & 7) * 16 / per);
+  if (mine) tma_load_4d(dst + lane * per * a.D, map, 0, (x.j0 + lane * per) & in_page, h, page, bar);
+  if (lane < kScaleLanes) {
+    const uint8_t* src = scales;                   // (nothing is read of a page that is missing)
+    if (from < a.n_pages)
+      src += from * scale_stride + ((int64_t)h << a.lps) + ((x.j0 + lane * 16) & in_page);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(scale_dst + lane * 16), "l"(src),
+                 "r"(from < a.n_pages ? 16 : 0)
+                 : "memory");
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+  }
+  return bad;
 }
 
 // ---- products --------------------------------------------------------------------------------
@@ -326,18 +320,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) {
-      mbar_init(smem_u32(&ctl->kfull[i]), 1);
+      mbar_init(smem_u32(&ctl->kfull[i]), 1 + kScaleLanes);
       mbar_init(smem_u32(&ctl->kempty[i]), 1);
     }
     for (int i = 0; i < VS; ++i) {
-      mbar_init(smem_u32(&ctl->vfull[i]), i == 0 ? 1 + a.withhold : 1);
+      mbar_init(smem_u32(&ctl->vfull[i]), (i == 0 ? 1 + a.withhold : 1) + kScaleLanes);
       mbar_init(smem_u32(&ctl->vempty[i]), 1);
     }
-    for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(&ctl->kscale[i]), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl->qfull[i]), 4);
       mbar_init(smem_u32(&ctl->qempty[i]), 8);          // softmax
-      mbar_init(smem_u32(&ctl->sfull[i]), 1);
+      mbar_init(smem_u32(&ctl->sfull[i]), 2);           // the product, and its issuer, who has seen the scales
       mbar_init(smem_u32(&ctl->pfull[i]), 4);
       mbar_init(smem_u32(&ctl->ofull[i]), 1);
       mbar_init(smem_u32(&ctl->oempty[i]), 4);
@@ -345,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&ctl->done), 2);
     ring_init(ctl->ring, kReaders);
-    ctl->abort = 0;
+    ctl->abort = ctl->any_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -370,69 +363,82 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (waits that go on are calls: with their loops in place the roles' code is larger than the
   // instruction cache)
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase<true>(a, bar, parity, abort_flag); };
-  // a unit's tiles of K (of V) and their scales; `part`: their stages' place among the scales
-  auto load_tiles = [&](auto stages, const Unit& x, uint32_t& n, const CUtensorMap& map,
-                        const uint8_t* scales, int part, uint64_t* full, uint64_t* empty,
-                        uint32_t* seen_bad) {
+  // The tiles of K (of V) with their scales, unit by unit; the next tile's lookups are on their way, over
+  // the end of a unit too.  fetch(x): the next unit, false after the last one.
+  auto load_tiles = [&](auto stages, auto fetch, const CUtensorMap& map, const uint8_t* scales, int part,
+                        uint64_t* full, uint64_t* empty) -> uint32_t {
     constexpr int S = decltype(stages)::value;
-    if (x.tile0 == x.tile1) return;
-    const bool past = x.nt >= x.stop;
-    Ahead now, next;
-    find(a, next, x.b, x.tile0 * kTile, x.stop, lane);
-    look(a, next, scales, kv.scale_stride, x.h, past, lane);
-    now = next;
-    find(a, next, x.b, (x.tile0 + 1) * kTile, x.stop, lane);
+    uint32_t n = 0, bad = 0;
+    Unit x, y;
+    Ahead next{};
+    bool more = fetch(x);
+    if (more) next = find(a, x.b, x.tile0 * kTile, x.stop, lane);
 #pragma unroll 1
-    for (int t = x.tile0; t < x.tile1; ++t, ++n) {
-      const int i = n % S;
-      const Ahead it = now;
-      if (t + 1 < x.tile1) {
-        look(a, next, scales, kv.scale_stride, x.h, past, lane);
-        now = next;
-        find(a, next, x.b, (t + 2) * kTile, x.stop, lane);
+    while (more && !*abort_flag) {
+#pragma unroll 1
+      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+        const int i = n % S, slot = n % kSlots;
+        const Ahead now = next;
+        if (t + 1 < x.tile1) {
+          next = find(a, x.b, (t + 1) * kTile, x.stop, lane);
+        } else if ((more = fetch(y))) {
+          next = find(a, y.b, y.tile0 * kTile, y.stop, lane);
+        }
+        if (n >= S) wait(&empty[i], (n / S - 1) & 1);
+        if (*abort_flag) break;
+        bad |= load_codes(a, &map, scales, kv.scale_stride, now, x.nt >= x.stop, x.h,
+                          smem_u32(smem + ((part ? KS : 0) + i) * C::kTileBytes),
+                          smem_u32(smem + C::kScaleOff + (part + slot) * kTile), smem_u32(&full[i]), lane,
+                          part ? nullptr : &ctl->bad[slot], &ctl->any_bad);
       }
-      if (n >= S) wait(&empty[i], (n / S - 1) & 1);
-      if (*abort_flag) break;
-      const int slot = n % kSlots;
-      load_codes(a, &map, it, smem_u32(smem + ((part ? KS : 0) + i) * C::kTileBytes),
-                 smem + C::kScaleOff + (part + slot) * kTile, smem_u32(&full[i]), x.h, lane,
-                 &ctl->bad[slot], part ? nullptr : &ctl->kscale[slot]);
-      if (seen_bad) *seen_bad |= it.pages.bad;
+      x = y;
     }
-  };
-  // every copy lands before the CTA may exit (bounded waits)
-  auto drain = [&](auto stages, uint32_t n, uint64_t* full) {
-    constexpr int S = decltype(stages)::value;
+    // every copy lands before the CTA may exit (bounded waits)
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0) {
 #pragma unroll 1
       for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &full[i % S], (i / S) & 1);
     }
     __syncwarp();
+    return bad;
   };
 
   if (warp == 0) {
-    // ---- units, K tiles -------------------------------------------------------------------
-    uint32_t n = 0, nu = 0, seen_bad = 0;
+    // ---- units, K tiles.  A unit without tiles is passed on only. -------------------------
+    uint32_t nu = 0;
     Walk walk(a, pre, R, max_q, share);
+    bool begun = false;
+    auto fetch = [&](Unit& x) {
 #pragma unroll 1
-    for (; !walk.done() && !*abort_flag; walk.next()) {
-      const Unit x = walk.unit();
-      put_unit<true>(a, ctl->ring, nu++, x, lane, abort_flag);
-      load_tiles(std::integral_constant<int, KS>(), x, n, mapK, kv.k_scale, 0, ctl->kfull, ctl->kempty, &seen_bad);
-    }
-    Unit last{};
-    last.b = -1;
-    put_unit<true>(a, ctl->ring, nu, last, lane, abort_flag);
-    if (seen_bad && lane == 0) raise(a, PP_S_INDEX);
-    drain(std::integral_constant<int, KS>(), n, ctl->kfull);
+      while (!*abort_flag) {
+        if (begun) walk.next();
+        begun = true;
+        const bool done = walk.done();
+        x = Unit{};
+        x.b = -1;
+        if (!done) x = walk.unit();
+        put_unit<true>(a, ctl->ring, nu++, x, lane, abort_flag);
+        if (done) return false;
+        if (x.tile0 < x.tile1) return true;
+      }
+      return false;
+    };
+    const uint32_t bad = load_tiles(std::integral_constant<int, KS>(), fetch, mapK, kv.k_scale, 0,
+                                    ctl->kfull, ctl->kempty);
+    if (bad && lane == 0) raise(a, PP_S_INDEX);
   } else if (warp == 2) {
     // ---- V tiles --------------------------------------------------------------------------
-    uint32_t n = 0;
-    Unit x;
+    uint32_t nu = 0;
+    auto fetch = [&](Unit& x) {
+      bool more;
 #pragma unroll 1
-    for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu)
-      load_tiles(std::integral_constant<int, VS>(), x, n, mapV, kv.v_scale, kSlots, ctl->vfull, ctl->vempty, nullptr);
-    drain(std::integral_constant<int, VS>(), n, ctl->vfull);
+      do {
+        more = get_unit<true>(a, ctl->ring, nu++, x, lane, false, abort_flag);
+      } while (more && x.tile0 == x.tile1);
+      return more;
+    };
+    load_tiles(std::integral_constant<int, VS>(), fetch, mapV, kv.v_scale, kSlots, ctl->vfull,
+               ctl->vempty);
   } else if (warp == 1) {
     // ---- MMA issuer of S ------------------------------------------------------------------
     if (lane == 0) {
@@ -462,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(smem_u32(&ctl->kempty[i]));
           }
           if (*abort_flag) break;
+          mbar_arrive(smem_u32(&ctl->sfull[g]));
           umma_commit(smem_u32(&ctl->sfull[g]));
         }
         ++nq;
@@ -599,15 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         wait(&ctl->sfull[g], (step >> 1) & 1);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        uint32_t bad = 0;
-#pragma unroll 1
-        for (int k = 0; k < tiles; ++k) {                // (they have come, with the tiles)
-          wait(&ctl->kscale[(n0 + k) % kSlots], ((n0 + k) / kSlots) & 1);
-          bad |= ctl->bad[(n0 + k) % kSlots];
-        }
+        const bool bad = *reinterpret_cast<volatile int*>(&ctl->any_bad) != 0;
         // does every row see every key of the step?
         const int j0 = t * kTile + key;
-        const bool edge = bad != 0 || (t + tiles) * kTile - 1 > min(x.first, x.stop - 1) ||
+        const bool edge = bad || (t + tiles) * kTile - 1 > min(x.first, x.stop - 1) ||
                           (a.window && t * kTile <= x.nt - a.window);
         uint32_t see = ~0u;                              // bit k R + r: row r sees this thread's key of tile k
         uint32_t live = ~0u;                             // bit k: some row does

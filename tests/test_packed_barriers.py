@@ -8,6 +8,16 @@ import pytest
 from test_paged_barriers import SEEDS, Bar, Ring, Schedule, bars  # noqa: F401
 
 
+class Arrival:
+    """An asynchronous copy that arrives, when it lands, as a thread does."""
+
+    def __init__(self, bar):
+        self.bar = bar
+
+    def land(self):
+        self.bar.arrive()
+
+
 SLOTS = 16     # tiles whose scales are held
 
 
@@ -16,29 +26,39 @@ def packed(seed, units, stages, most, late=False):
     soon as its product is done, before the epilogue has taken the step's sums."""
     s, ring = Schedule(seed), Ring(19)
     ks, vs = stages
-    kfull, kempty, vfull, vempty = bars(ks, 1), bars(ks, 1), bars(vs, 1), bars(vs, 1)
-    kscale, qfull, qempty = bars(SLOTS, 1), bars(2, 4), bars(2, 8)
-    sfull, pfull, ofull, oempty = bars(2, 1), bars(2, 4), bars(2, 1), bars(2, 4)
+    kfull, kempty, vfull, vempty = bars(ks, 9), bars(ks, 1), bars(vs, 9), bars(vs, 1)
+    qfull, qempty = bars(2, 4), bars(2, 8)
+    sfull, pfull, ofull, oempty = bars(2, 2), bars(2, 4), bars(2, 1), bars(2, 4)
     meet, held = bars(2, 4), {"k": {}, "v": {}}
 
     def steps(count):
         return [min(most, count - t) for t in range(0, count, most)]
 
     def tiles(name, full, empty, unit):
-        n, size = 0, len(full)
-        for k, count in enumerate(units):
-            yield from unit(k)
-            for _ in range(count):
+        n, size, k = 0, len(full), 0
+
+        def fetch():                            # the next unit with tiles; the one after the last is the end
+            nonlocal k
+            while True:
+                yield from unit(k)
+                k += 1
+                if k > len(units) or units[k - 1]:
+                    return
+
+        yield from fetch()
+        while k <= len(units):
+            count = units[k - 1]
+            for t in range(count):
+                if t + 1 == count:
+                    yield from fetch()
                 if n >= size:
                     yield empty[n % size], n // size - 1
                 # the scales of the tile that had this place are no longer looked at
                 assert held[name].get(n % SLOTS, 0) == 0, "scales overwritten"
-                held[name][n % SLOTS] = 8 // 2
-                if name == "k":
-                    kscale[n % SLOTS].arrive()
+                held[name][n % SLOTS] = 4
                 s.load(full[n % size])
+                s.copies += [Arrival(full[n % size]) for _ in range(8)]
                 n += 1
-        yield from unit(len(units))
 
     def scores():
         n = step = nq = 0
@@ -54,6 +74,7 @@ def packed(seed, units, stages, most, late=False):
                     yield kfull[n % ks], n // ks
                     s.commits.append(kempty[n % ks])
                     n += 1
+                sfull[step & 1].arrive()
                 s.commits.append(sfull[step & 1])
                 step += 1
             nq += 1
@@ -98,8 +119,6 @@ def packed(seed, units, stages, most, late=False):
                 if (step & 1) == g:
                     mine = range(n - kt, n)
                     yield sfull[g], step >> 1
-                    for m in mine:
-                        yield kscale[m % SLOTS], m // SLOTS
                     yield from s.work(5)
                     for m in mine:
                         held["k"][m % SLOTS] -= 1
