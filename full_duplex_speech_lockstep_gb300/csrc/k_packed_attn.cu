@@ -22,13 +22,14 @@
 // lengths, the head counts and max_q only.  A unit that is not its rows' only one leaves (m, l, O) in
 // scratch and k_packed_join adds the splits up in split order.
 //
-//   warp 0       the units; K tiles and their scales
+//   warp 0       the units and their tiles' pages, up to 16 tiles ahead.  (With lookups in the warps that
+//                load, a tile took 1150 clocks and a unit's start 3600.)
 //   warp 1       one thread issues the MMAs of S
-//   warp 2       V tiles and their scales
+//   warps 2, 16  K tiles and V tiles with their scales
 //   warp 3       one thread issues the MMAs of O.  (One thread for both took 1900 clocks a tile.)
 //   warps 4-7, 8-11   softmax of every second step
 //   warps 12-15  epilogue: a thread owns one dim
-//   warps 16-19  the units' queries, as parts.  (One warp took 13000 clocks for 32 rows.)
+//   warps 17-18  the units' queries, as parts.  (One warp took 13000 clocks for 32 rows.)
 //
 // What no row of a unit sees must not reach the second product, where a weight of zero times a NaN
 // would be one: those rows of V are zeroed in shared memory.  An entry that only some rows see and
@@ -42,9 +43,9 @@ namespace pp {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kReaders = 19;         // of the units: both issuers, V, eight of softmax, epilogue, queries
-constexpr int kSlots = 16;           // tiles whose scales are held
+constexpr int kThreads = 608;
+constexpr int kReaders = 16;         // of the units: both issuers, eight of softmax, epilogue, queries
+constexpr int kSlots = 16;           // tiles that are planned, and those whose scales are held
 constexpr int kParts = 3;            // of a weight
 constexpr float kTop = 8.f;          // a tile's largest weight is 2^8 (e4m3 holds up to 448)
 
@@ -53,9 +54,12 @@ struct Cfg {
   static constexpr int QP = sizeof(T) == 2 && Num<T>::kShift == 0.f ? 2 : 3;   // parts of a query
   static constexpr int NQ = (QP * R + 15) / 16 * 16;                 // columns of S
   static constexpr int NP = (kParts * R + 15) / 16 * 16;             // columns of O
-  static constexpr int KT = 32 / R;                                  // tiles of a step
+  static constexpr int KT = R == 8 ? 2 : 1;                          // tiles of a step
+  static constexpr int SB = KT * NQ <= 64 ? 4 : 2;                   // buffers of S in tensor memory
   static constexpr int kTileBytes = kTile * D;
-  static constexpr int KS = D == 128 ? 4 : 8, VS = D == 128 ? 5 : 8;   // stages of K, of V
+  // Stages of K, which a product frees at once, and of V, which waits for the softmax.
+  static constexpr int KS = D == 128 ? 3 : 8;
+  static constexpr int VS = D == 128 ? (R == 32 ? 6 : 7) : 8;
   static constexpr int kQBytes = NQ * 128;
   static constexpr int kPBytes = NP / 16 * 2048;
   static constexpr int kVOff = KS * kTileBytes;
@@ -65,10 +69,19 @@ struct Cfg {
   static constexpr int kCtlOff = kScaleOff + 2 * kSlots * kTile;
 };
 
+// A tile as its loads need it: the pages of its groups of 16 entries (n_pages: none) and the groups that miss
+// one; key head (-1: no more tiles), first entry's row; tiles that its step lacks (-1: more of it follow).
+struct alignas(16) Tile {
+  int page[8];
+  int h, row, lack;
+  uint32_t bad;
+};
+
 struct Ctl {
   UnitRing ring;
-  uint64_t kfull[8], kempty[8], vfull[8], vempty[8], qfull[2], qempty[2];
-  uint64_t sfull[2], pfull[2], ofull[2], oempty[2], meet[2], done;
+  Tile tile[kSlots];
+  uint64_t tfull[kSlots], tempty[kSlots], kfull[8], kempty[8], vempty[8], qfull[2], qempty[2];
+  uint64_t sfull[4], sempty[4], vfull[8], pfull[2], ofull[2], oempty[2], meet[2], done;
   uint32_t bad[kSlots];
   int any_bad;                         // a tile of this CTA had a page that is missing
   uint32_t tmem;
@@ -117,14 +130,15 @@ __host__ __device__ __forceinline__ int n_splits(int64_t tiles, int share) {
 }
 
 struct Shape {       // of a sequence's units
-  int rt, ns, st, cost;
+  int rt, ns, cost;
   // A chunk longer than the caller said is not split: scratch has no room for its parts.
   __device__ __forceinline__ Shape(const Args& a, const Seq& s, int R, int max_q, int share) {
     const int mt = (int)most_tiles(s.len, a.window, row_span(R, a.G));
     rt = (int)(((int64_t)s.n * a.G + R - 1) / R);
     ns = s.n > max_q ? 1 : n_splits(mt, share);
-    st = ns == 1 ? mt : (int)split_tiles(mt, share);
-    cost = st + 2;                     // a unit's ends cost as much as two tiles
+    // a unit's ends and a step's cost as much as a tile each (steps of `per` tiles)
+    const int per = R == 8 ? 2 : 1, st = (mt + ns - 1) / ns;
+    cost = st + (st + per - 1) / per + 1;
   }
 };
 
@@ -135,7 +149,7 @@ struct Walk {
   int64_t at, end;
   int b, h, i;
   Seq s;
-  int rt, ns, st, cost;
+  int rt, ns, cost;
 
   __device__ __forceinline__ Walk(const Args& a_, const int64_t* pre_, int R_, int max_q_, int share_)
       : a(a_), pre(pre_), R(R_), max_q(max_q_), share(share_) {
@@ -157,7 +171,6 @@ struct Walk {
     const Shape x(a, s, R, max_q, share);
     rt = x.rt;
     ns = x.ns;
-    st = x.st;
     cost = x.cost;
   }
   __device__ __forceinline__ void next_sequence() {
@@ -189,75 +202,67 @@ struct Walk {
     x.stop = min(max(x.nt + 1, 0), s.len);
     x.low = a.window ? min(max(x.first - a.window + 1, 0), x.stop) : 0;
     const int ta = x.low / kTile, tb = (x.stop + kTile - 1) / kTile;
-    x.tile0 = min(ta + split * st, tb);
-    x.tile1 = min(x.tile0 + st, tb);
+    x.tile0 = ta + (int)((int64_t)(tb - ta) * split / ns);       // even splits
+    x.tile1 = ta + (int)((int64_t)(tb - ta) * (split + 1) / ns);
     x.split = split | ns << 8;
     return x;
   }
 };
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
 // ---- loads -----------------------------------------------------------------------------------
 // Scales go by asynchronous copies of 16 bytes, a lane to each: a bulk copy for every page was slower with
 // pages of 16, and through registers a tile waits for memory's latency.
 constexpr int kScaleLanes = kTile / 16;
-// A tile's table entries come to the producer's registers ahead of its turn, a lane to a page.
+// Table entries come to the planner's registers 32 at a time, a lane to each (those of 4 to 64 tiles), ahead
+// of their turn.
 struct Ahead {
-  int j0, end;           // the tile's first entry; entries from here on have no place
-  int raw;               // this lane's table entry, as it lies
+  int first, raw;        // the first entry; this lane's, as it lies
 };
-__device__ __forceinline__ Ahead find(const Args& a, int b, int j0, int end, int lane) {
-  const int per = min(1 << a.lps, kTile), j = j0 + lane * per;
-  return Ahead{j0, end, lane < kTile / per && j < end ? a.table[(int64_t)b * a.table_ld + (j >> a.lps)] : 0};
+__device__ __forceinline__ Ahead find(const Args& a, int b, int first, int end, int lane) {
+  const bool in = first + lane <= (end - 1) >> a.lps;
+  return Ahead{first, in ? a.table[(int64_t)b * a.table_ld + first + lane] : 0};
 }
-// Codes and scales of a tile; pages without a place arrive as zeros.  `past`: rows look beyond the tile's
-// end.  Returns the 16-key groups without a page.
-__device__ __forceinline__ uint32_t load_codes(const Args& a, const CUtensorMap* map, const uint8_t* scales,
-                                               int64_t scale_stride, const Ahead& x, bool past, int h,
-                                               uint32_t dst, uint32_t scale_dst, uint32_t bar, int lane,
-                                               uint32_t* bad_out, int* any_bad) {
-  const int per = min(1 << a.lps, kTile), pages = kTile / per, in_page = (1 << a.lps) - 1;
-  const bool mine = lane < pages, in = x.j0 + lane * per < x.end;
-  const bool have = mine && in && (unsigned)x.raw < (unsigned)a.n_pages;
-  const int page = have ? x.raw : a.n_pages;
-  const uint32_t mask = __ballot_sync(0xffffffffu, mine && !have && (in || past));
-  uint32_t bad = 0;
-  if (mask) {                                      // rare: from pages to groups of 16
-#pragma unroll 1
-    for (int g = 0; g < 8; ++g) bad |= ((mask >> (g * 16 / per)) & 1u) << g;
-  }
-  if (lane == 0) {
-    if (bad_out) {
-      *bad_out = bad;
-      if (bad) *any_bad = 1;
-    }
-    mbar_expect_tx(bar, (uint32_t)(kTile * a.D));
-  }
-  const int from = __shfl_sync(0xffffffffu, page, (lane & 7) * 16 / per);
-  if (mine) tma_load_4d(dst + lane * per * a.D, map, 0, (x.j0 + lane * per) & in_page, h, page, bar);
+// Codes and scales of a tile, by the lanes of its groups; groups without a page arrive as zeros.
+template <int D>
+__device__ __forceinline__ void load_codes(const Args& a, const CUtensorMap* map, const uint8_t* scales,
+                                           int64_t scale_stride, const Tile& x, uint32_t dst,
+                                           uint32_t scale_dst, uint32_t bar, int lane) {
+  if (lane == 0) mbar_expect_tx(bar, (uint32_t)(kTile * D));
+  __syncwarp();
   if (lane < kScaleLanes) {
-    const uint8_t* src = scales;                   // (nothing is read of a page that is missing)
-    if (from < a.n_pages)
-      src += from * scale_stride + ((int64_t)h << a.lps) + ((x.j0 + lane * 16) & in_page);
+    const int page = x.page[lane], row = (x.row + lane * 16) & ((1 << a.lps) - 1);
+    const bool have = page < a.n_pages;
+    // (nothing is read of a page that is missing)
+    const uint8_t* src = scales + (have ? page * scale_stride + ((int64_t)x.h << a.lps) + row : 0);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(scale_dst + lane * 16), "l"(src),
-                 "r"(from < a.n_pages ? 16 : 0)
+                 "r"(have ? 16 : 0)
                  : "memory");
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    const int groups = 1 << (min(a.lps, 7) - 4);           // of a page
+    if ((lane & (groups - 1)) == 0) tma_load_4d(dst + lane * 16 * D, map, 0, row, x.h, page, bar);
   }
-  return bad;
 }
 
 // ---- products --------------------------------------------------------------------------------
-__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          bool accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+// Matrix descriptors: the lower word has the address and the leading offset (bytes), the upper one the stride
+// and the layout (2: 128-byte swizzle, 4: 64-byte, 0: none) and does not change.
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t stride, uint32_t layout) {
+  return (stride >> 4) | 1u << 14 | layout << 29;
 }
-// Matrix descriptor: leading and stride offsets in bytes; layout 2: 128-byte swizzle, 4: 64-byte, 0: none
-__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t layout) {
-  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)(lead >> 4) << 16 |
-         (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)layout << 61;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return (addr >> 4 & 0x3fffu) | (lead >> 4) << 16;
+}
+// D = A B (`acc` false) or D += A B.  (The issuing thread is alone: every instruction between two counts.)
+template <uint32_t kAHi, uint32_t kBHi>
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %4};\n"
+      " mov.b64 b, {%2, %5};\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kAHi), "n"(kBHi), "r"((uint32_t)acc));
 }
 
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kTile >> 4) << 24);   // fp32 of e4m3, M = 128
@@ -323,14 +328,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->kfull[i]), 1 + kScaleLanes);
       mbar_init(smem_u32(&ctl->kempty[i]), 1);
     }
-    for (int i = 0; i < VS; ++i) {
-      mbar_init(smem_u32(&ctl->vfull[i]), (i == 0 ? 1 + a.withhold : 1) + kScaleLanes);
-      mbar_init(smem_u32(&ctl->vempty[i]), 1);
+    for (int i = 0; i < VS; ++i) mbar_init(smem_u32(&ctl->vempty[i]), 1);   // epilogue
+    // V by steps, as many of them as there are stages at most
+    for (int i = 0; i < 8; ++i)
+      mbar_init(smem_u32(&ctl->vfull[i]), C::KT * (1 + kScaleLanes) + (i == 0 ? a.withhold : 0));
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&ctl->tfull[i]), 1);
+      mbar_init(smem_u32(&ctl->tempty[i]), 2);          // K, V
+    }
+    for (int i = 0; i < C::SB; ++i) {
+      mbar_init(smem_u32(&ctl->sfull[i]), 2);           // the product, and its issuer, who has seen the scales
+      mbar_init(smem_u32(&ctl->sempty[i]), 4);          // softmax
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ctl->qfull[i]), 4);
+      mbar_init(smem_u32(&ctl->qfull[i]), 2);
       mbar_init(smem_u32(&ctl->qempty[i]), 8);          // softmax
-      mbar_init(smem_u32(&ctl->sfull[i]), 2);           // the product, and its issuer, who has seen the scales
       mbar_init(smem_u32(&ctl->pfull[i]), 4);
       mbar_init(smem_u32(&ctl->ofull[i]), 1);
       mbar_init(smem_u32(&ctl->oempty[i]), 4);
@@ -363,88 +375,121 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (waits that go on are calls: with their loops in place the roles' code is larger than the
   // instruction cache)
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase<true>(a, bar, parity, abort_flag); };
-  // The tiles of K (of V) with their scales, unit by unit; the next tile's lookups are on their way, over
-  // the end of a unit too.  fetch(x): the next unit, false after the last one.
-  auto load_tiles = [&](auto stages, auto fetch, const CUtensorMap& map, const uint8_t* scales, int part,
-                        uint64_t* full, uint64_t* empty) -> uint32_t {
-    constexpr int S = decltype(stages)::value;
-    uint32_t n = 0, bad = 0;
-    Unit x, y;
-    Ahead next{};
-    bool more = fetch(x);
-    if (more) next = find(a, x.b, x.tile0 * kTile, x.stop, lane);
+  // The tiles of K (of V) with their scales, as the planner has them.
+  auto load_tiles = [&](auto kind, const CUtensorMap& map, const uint8_t* scales, uint64_t* empty) {
+    constexpr bool kV = decltype(kind)::value;
+    constexpr int S = kV ? VS : KS;
+    uint32_t n = 0, step = 0;
 #pragma unroll 1
-    while (more && !*abort_flag) {
-#pragma unroll 1
-      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
-        const int i = n % S, slot = n % kSlots;
-        const Ahead now = next;
-        if (t + 1 < x.tile1) {
-          next = find(a, x.b, (t + 1) * kTile, x.stop, lane);
-        } else if ((more = fetch(y))) {
-          next = find(a, y.b, y.tile0 * kTile, y.stop, lane);
-        }
-        if (n >= S) wait(&empty[i], (n / S - 1) & 1);
-        if (*abort_flag) break;
-        bad |= load_codes(a, &map, scales, kv.scale_stride, now, x.nt >= x.stop, x.h,
-                          smem_u32(smem + ((part ? KS : 0) + i) * C::kTileBytes),
-                          smem_u32(smem + C::kScaleOff + (part + slot) * kTile), smem_u32(&full[i]), lane,
-                          part ? nullptr : &ctl->bad[slot], &ctl->any_bad);
+    for (; !*abort_flag; ++n) {
+      const uint32_t i = n % S, slot = n % kSlots;
+      wait(&ctl->tfull[slot], (n / kSlots) & 1);
+      const Tile& x = ctl->tile[slot];
+      if (x.h < 0) break;
+      if (n >= S) wait(&empty[i], (n / S - 1) & 1);
+      if (*abort_flag) break;
+      const uint32_t full = smem_u32(kV ? &ctl->vfull[step % 8] : &ctl->kfull[i]);
+      if (!kV && lane == 0) {
+        ctl->bad[slot] = x.bad;
+        if (x.bad) ctl->any_bad = 1;
       }
-      x = y;
+      load_codes<D>(a, &map, scales, kv.scale_stride, x, smem_u32(smem + (kV ? C::kVOff : 0) + i * C::kTileBytes),
+                    smem_u32(smem + C::kScaleOff + ((kV ? kSlots : 0) + slot) * kTile), full, lane);
+      // V is waited for by steps: the tiles that a step lacks count as there
+      const int lack = x.lack;
+      if (kV && lack > 0 && lane == 0) mbar_arrive_n(full, lack * (1 + kScaleLanes));
+      step += lack >= 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[slot]));
     }
     // every copy lands before the CTA may exit (bounded waits)
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0) {
+      if (kV) {
 #pragma unroll 1
-      for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &full[i % S], (i / S) & 1);
+        for (uint32_t i = step > 8 ? step - 8 : 0; i < step; ++i)
+          drain_phase(a, &ctl->vfull[i % 8], (i / 8) & 1);
+      } else {
+#pragma unroll 1
+        for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &ctl->kfull[i % S], (i / S) & 1);
+      }
     }
     __syncwarp();
-    return bad;
   };
 
   if (warp == 0) {
-    // ---- units, K tiles.  A unit without tiles is passed on only. -------------------------
-    uint32_t nu = 0;
+    // ---- planner: units, and their tiles' pages -------------------------------------------
+    uint32_t n = 0, bad = 0;
     Walk walk(a, pre, R, max_q, share);
-    bool begun = false;
-    auto fetch = [&](Unit& x) {
-#pragma unroll 1
-      while (!*abort_flag) {
-        if (begun) walk.next();
-        begun = true;
-        const bool done = walk.done();
-        x = Unit{};
-        x.b = -1;
-        if (!done) x = walk.unit();
-        put_unit<true>(a, ctl->ring, nu++, x, lane, abort_flag);
-        if (done) return false;
-        if (x.tile0 < x.tile1) return true;
-      }
-      return false;
-    };
-    const uint32_t bad = load_tiles(std::integral_constant<int, KS>(), fetch, mapK, kv.k_scale, 0,
-                                    ctl->kfull, ctl->kempty);
-    if (bad && lane == 0) raise(a, PP_S_INDEX);
-  } else if (warp == 2) {
-    // ---- V tiles --------------------------------------------------------------------------
+    bool more = !walk.done();
+    Unit x{}, y{};
+    Ahead now, next{};                                   // next: the next block of this unit, or the next unit's
+    if (more) {
+      x = walk.unit();
+      next = find(a, x.b, x.tile0 * kTile >> a.lps, x.stop, lane);
+    }
     uint32_t nu = 0;
-    auto fetch = [&](Unit& x) {
-      bool more;
 #pragma unroll 1
-      do {
-        more = get_unit<true>(a, ctl->ring, nu++, x, lane, false, abort_flag);
-      } while (more && x.tile0 == x.tile1);
-      return more;
-    };
-    load_tiles(std::integral_constant<int, VS>(), fetch, mapV, kv.v_scale, kSlots, ctl->vfull,
-               ctl->vempty);
+    for (; more && !*abort_flag; x = y) {
+      put_unit<true>(a, ctl->ring, nu++, x, lane, abort_flag);
+      // the next unit's first entries are on their way while this one's tiles are handed on
+      const int end = min(x.stop, x.tile1 * kTile);
+      now = next;
+      Ahead then = find(a, x.b, now.first + 32, end, lane);
+      walk.next();
+      more = !walk.done();
+      if (more) {
+        y = walk.unit();
+        next = find(a, y.b, y.tile0 * kTile >> a.lps, y.stop, lane);
+      }
+      const bool past = x.nt >= x.stop;
+#pragma unroll 1
+      for (int t = x.tile0; t < x.tile1; ++t, ++n) {
+        const int slot = n % kSlots, j0 = t * kTile, j = j0 + (lane & 7) * 16;
+        if ((j0 >> a.lps) - now.first >= 32) {
+          now = then;
+          then = find(a, x.b, now.first + 32, end, lane);
+        }
+        const int raw = __shfl_sync(0xffffffffu, now.raw, (j >> a.lps) - now.first);
+        const bool in = j < x.stop, have = in && (unsigned)raw < (unsigned)a.n_pages;
+        const uint32_t missing = __ballot_sync(0xffffffffu, lane < 8 && !have && (in || past));
+        if (n >= kSlots) wait(&ctl->tempty[slot], (n / kSlots - 1) & 1);
+        if (*abort_flag) break;
+        if (lane < 8) ctl->tile[slot].page[lane] = have ? raw : a.n_pages;
+        if (lane == 0) {
+          const int k = (t - x.tile0) % C::KT;
+          ctl->tile[slot].h = x.h;
+          ctl->tile[slot].row = j0 & ((1 << a.lps) - 1);
+          ctl->tile[slot].lack = k == C::KT - 1 || t + 1 == x.tile1 ? C::KT - 1 - k : -1;
+          ctl->tile[slot].bad = missing;
+        }
+        bad |= missing;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->tfull[slot]));
+      }
+    }
+    Unit last{};
+    last.b = -1;
+    put_unit<true>(a, ctl->ring, nu, last, lane, abort_flag);
+    const int slot = n % kSlots;
+    if (n >= kSlots) wait(&ctl->tempty[slot], (n / kSlots - 1) & 1);
+    if (lane == 0) {
+      if (!*abort_flag) {
+        ctl->tile[slot].h = -1;
+        mbar_arrive(smem_u32(&ctl->tfull[slot]));
+      }
+      if (bad) raise(a, PP_S_INDEX);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    load_tiles(std::false_type(), mapK, kv.k_scale, ctl->kempty);
+  } else if (warp == 16) {
+    load_tiles(std::true_type(), mapV, kv.v_scale, ctl->vempty);
   } else if (warp == 1) {
     // ---- MMA issuer of S ------------------------------------------------------------------
     if (lane == 0) {
       constexpr uint32_t id = kIdesc | ((uint32_t)(C::NQ >> 3) << 17);
-      const uint64_t k0 = desc(smem_u32(smem), 0, 8 * D, kRowLayout);
-      const uint64_t q0 = desc(smem_u32(smem + C::kQOff), 0, 1024, 2);
+      const uint32_t k0 = desc_lo(smem_u32(smem), 0), q0 = desc_lo(smem_u32(smem + C::kQOff), 0);
       uint32_t n = 0, step = 0, nq = 0;
       Unit x;
 #pragma unroll 1
@@ -453,23 +498,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&ctl->qfull[nq & 1], (nq >> 1) & 1);
 #pragma unroll 1
         for (int t = x.tile0; t < x.tile1; t += C::KT, ++step) {
-          const uint32_t g = step & 1;
-          if (step >= 2) wait(&ctl->pfull[g], ((step >> 1) - 1) & 1);   // the last S has been read
+          const uint32_t sb = step % C::SB;
+          if (step >= C::SB) wait(&ctl->sempty[sb], (step / C::SB - 1) & 1);
+          const int tiles = min(C::KT, x.tile1 - t);
 #pragma unroll 1
-          for (int k = 0; k < min(C::KT, x.tile1 - t); ++k, ++n) {
+          for (int k = 0; k < tiles; ++k, ++n) {
             const uint32_t i = n % KS;
             wait(&ctl->kfull[i], (n / KS) & 1);
             if (*abort_flag) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t kt = k0 + i * (C::kTileBytes >> 4), qt = q0 + (nq & 1) * (C::kQBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
-              umma_e4m3(tmem + g * 128 + k * C::NQ, k0 + ((i * C::kTileBytes + kk * 32) >> 4),
-                        q0 + (((nq & 1) * C::kQBytes + kk * 32) >> 4), id, kk > 0);
+              umma_e4m3<desc_hi(8 * D, kRowLayout), desc_hi(1024, 2)>(
+                  tmem + sb * (256 / C::SB) + k * C::NQ, kt + kk * 2, qt + kk * 2, id, kk > 0);
             umma_commit(smem_u32(&ctl->kempty[i]));
           }
           if (*abort_flag) break;
-          mbar_arrive(smem_u32(&ctl->sfull[g]));
-          umma_commit(smem_u32(&ctl->sfull[g]));
+          mbar_arrive(smem_u32(&ctl->sfull[sb]));
+          umma_commit(smem_u32(&ctl->sfull[sb]));
         }
         ++nq;
       }
@@ -485,8 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V: dims contiguous, 8 keys to an atom of 8 D bytes (with 64 dims rows 64-127 of the product are
       // the keys 8 further on, and nobody reads them).  Weights: 16 columns of 8 keys to 128 bytes, keys
       // following each other, the next columns 2048 bytes on.
-      const uint64_t v0 = desc(smem_u32(smem + C::kVOff), 512, 8 * D, kRowLayout);
-      const uint64_t w0 = desc(smem_u32(smem + C::kPOff), 128, 2048, 0);
+      const uint32_t v0 = desc_lo(smem_u32(smem + C::kVOff), 512), w0 = desc_lo(smem_u32(smem + C::kPOff), 128);
       uint32_t n = 0, step = 0;
       Unit x;
 #pragma unroll 1
@@ -494,20 +540,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int t = x.tile0; t < x.tile1; t += C::KT, ++step) {
           const uint32_t g = step & 1;
-          wait(&ctl->pfull[g], (step >> 1) & 1);        // (whose arrivals have waited for the last O)
+          // (whose arrivals have waited for the last O of this buffer, and for V)
+          wait(&ctl->pfull[g], (step >> 1) & 1);
+          if (*abort_flag) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const int tiles = min(C::KT, x.tile1 - t);
 #pragma unroll 1
-          for (int k = 0; k < min(C::KT, x.tile1 - t); ++k, ++n) {
-            const uint32_t i = n % VS;
-            wait(&ctl->vfull[i], (n / VS) & 1);
-            if (*abort_flag) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          for (int k = 0; k < tiles; ++k, ++n) {
+            const uint32_t vt = v0 + n % VS * (C::kTileBytes >> 4);
+            const uint32_t wt = w0 + (g * C::KT + k) * (C::kPBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < kTile / 32; ++kk)
-              umma_e4m3(tmem + 256 + g * 128, v0 + ((i * C::kTileBytes + kk * 32 * D) >> 4),
-                        w0 + (((g * C::KT + k) * C::kPBytes + kk * 512) >> 4), id, k + kk > 0);
-            umma_commit(smem_u32(&ctl->vempty[i]));
+              umma_e4m3<desc_hi(8 * D, kRowLayout), desc_hi(2048, 0)>(
+                  tmem + 256 + g * 128, vt + kk * (32 * D >> 4), wt + kk * (512 >> 4), id, k + kk > 0);
           }
-          if (*abort_flag) break;
           umma_commit(smem_u32(&ctl->ofull[g]));
         }
       }
@@ -515,11 +561,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_phase(a, &ctl->done, 0);
     }
     __syncwarp();
-  } else if (warp >= 16) {
+  } else if (warp >= 17) {
     // ---- queries: L lanes to a row, four dims to a lane -----------------------------------
-    constexpr int L = D / 4, kSide = 4 * 32 / L;           // rows side by side, of four warps
+    constexpr int L = D / 4, kSide = 2 * 32 / L;           // rows side by side, of two warps
     constexpr int kAhead = R / kSide < 4 ? R / kSide : 4;  // passes loaded at once
-    const int l = lane % L, side = (threadIdx.x - 512) / L;
+    const int l = lane % L, side = (threadIdx.x - 544) / L;
     const uint32_t per_head = (65536u + a.G - 1) / a.G;    // f / G for f G < 2^16
     uint32_t nq = 0;
     Unit x;
@@ -582,7 +628,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- softmax: thread k of a group owns key k of the group's tiles ---------------------
     const uint32_t g = warp >= 8;
     const int wq = warp & 3, key = wq * 32 + lane;
-    const uint32_t scores = tmem + ((uint32_t)(wq * 32) << 16) + g * 128;
     uint8_t* const weights = smem + C::kPOff + g * C::KT * C::kPBytes + key * 16;
     uint32_t n = 0, step = 0, nq = 0, meets = 0;
     Unit x;
@@ -604,7 +649,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto v_scale = [&](int k) -> uint32_t {
           return smem[C::kScaleOff + (kSlots + (n0 + k) % kSlots) * kTile + key];
         };
-        wait(&ctl->sfull[g], (step >> 1) & 1);
+        const uint32_t sb = step % C::SB;
+        const uint32_t scores = tmem + ((uint32_t)(wq * 32) << 16) + sb * (256 / C::SB);
+        wait(&ctl->sfull[sb], (step / C::SB) & 1);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const bool bad = *reinterpret_cast<volatile int*>(&ctl->any_bad) != 0;
         // does every row see every key of the step?
@@ -674,10 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         // ---- what V brings: its scales, and rows that must not be multiplied
         uint32_t nan_value = 0, E = 0;                   // bit k: the value of tile k reads as NaN
+        wait(&ctl->vfull[step % 8], (step / 8) & 1);
 #pragma unroll 1
         for (int k = 0; k < tiles; ++k) {
           const uint32_t i = (n0 + k) % VS;
-          wait(&ctl->vfull[i], ((n0 + k) / VS) & 1);
           const uint32_t ev = v_scale(k);
           if (ev == 255u) nan_value |= 1u << k;
           if (live >> k & 1u) E = max(E, ev == 255u ? 0u : ev);
@@ -803,7 +850,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->pfull[g]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ctl->pfull[g]));
+          mbar_arrive(smem_u32(&ctl->sempty[sb]));
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->qempty[qb]));
@@ -813,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- epilogue: thread d owns dim d; lane r of each warp keeps row r's maximum and sum ---
     const int wq = warp & 3, d = wq * 32 + lane, H = a.Hk * a.G;
     const uint32_t lane_at = tmem + ((uint32_t)(wq * 32) << 16) + 256;
-    uint32_t step = 0;
+    uint32_t n = 0, step = 0;
     Unit x;
 #pragma unroll 1
     for (uint32_t nu = 0; get_unit<true>(a, ctl->ring, nu, x, lane, false, abort_flag); ++nu) {
@@ -865,6 +915,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->oempty[g]));
+        const int tiles = min(C::KT, x.tile1 - t);
+        if (wq == 0 && lane < tiles) mbar_arrive(smem_u32(&ctl->vempty[(n + lane) % VS]));
+        n += tiles;
       }
       if (*abort_flag) break;
       // lane r: where row r goes
@@ -928,7 +981,7 @@ template <typename T, int D, int R>
 cudaError_t run(const Args& a, const PackedPlan& p, const Maps& maps, const AttnOut& o, const Packed& kv,
                 const void* q, int64_t q_stride, cudaStream_t s) {
   using C = Cfg<T, D, R>;
-  static_assert(C::KS + 2 * C::KT <= kSlots, "scales outlive the steps that are under way");
+  static_assert(C::KS + C::SB * C::KT <= kSlots && C::VS <= 8, "scales outlive the steps that are under way");
   static_assert(C::kQBytes % 1024 == 0 && C::kPBytes % 1024 == 0 && C::KT * C::NQ <= 128 && C::NP <= 128,
                 "operands start on 1024 bytes, products fit their columns");
   const size_t smem = C::kCtlOff + sizeof(Ctl) + (size_t)(a.n_seqs + 1) * sizeof(int64_t) + 1024;
