@@ -25,7 +25,8 @@
 //   warp 0       the units and their tiles' pages, up to 16 tiles ahead.  (With lookups in the warps that
 //                load, a tile took 1150 clocks and a unit's start 3600.)
 //   warp 1       one thread issues the MMAs of S
-//   warps 2, 16  K tiles and V tiles with their scales
+//   warps 2, 19, 16   K tiles with both scales, of even and odd stages (a tile takes a warp 1000 clocks);
+//                V tiles
 //   warp 3       one thread issues the MMAs of O.  (One thread for both took 1900 clocks a tile.)
 //   warps 4-7, 8-11   softmax of every second step
 //   warps 12-15  epilogue: a thread owns one dim
@@ -43,7 +44,7 @@ namespace pp {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 608;
+constexpr int kThreads = 640;
 constexpr int kReaders = 16;         // of the units: both issuers, eight of softmax, epilogue, queries
 constexpr int kSlots = 16;           // tiles that are planned, and those whose scales are held
 constexpr int kParts = 3;            // of a weight
@@ -59,7 +60,7 @@ struct Cfg {
   static constexpr int kTileBytes = kTile * D;
   // Stages of K, which a product frees at once, and of V, which waits for the softmax.
   static constexpr int KS = D == 128 ? 3 : 8;
-  static constexpr int VS = D == 128 ? (R == 32 ? 6 : 7) : 8;
+  static constexpr int VS = D == 128 ? (R == 32 ? 7 : 8) : 8;
   static constexpr int kQBytes = NQ * 128;
   static constexpr int kPBytes = NP / 16 * 2048;
   static constexpr int kVOff = KS * kTileBytes;
@@ -144,15 +145,15 @@ struct Shape {       // of a sequence's units
 
 struct Walk {
   const Args& a;
-  const int64_t* pre;
   const int R, max_q, share;
   int64_t at, end;
   int b, h, i;
   Seq s;
   int rt, ns, cost;
 
-  __device__ __forceinline__ Walk(const Args& a_, const int64_t* pre_, int R_, int max_q_, int share_)
-      : a(a_), pre(pre_), R(R_), max_q(max_q_), share(share_) {
+  // (the prefix sums are looked at here only)
+  __device__ __forceinline__ Walk(const Args& a_, const int64_t* pre, int R_, int max_q_, int share_)
+      : a(a_), R(R_), max_q(max_q_), share(share_) {
     const int64_t total = pre[a.n_seqs];
     at = total * blockIdx.x / gridDim.x;
     end = total * (blockIdx.x + 1) / gridDim.x;
@@ -177,7 +178,8 @@ struct Walk {
     h = i = 0;
     do {
       ++b;
-    } while (b < a.n_seqs && pre[b + 1] == pre[b]);
+      s = b < a.n_seqs ? seq_of(a, b) : Seq{};
+    } while (b < a.n_seqs && s.n == 0);
     if (b < a.n_seqs) sequence();
   }
   __device__ __forceinline__ void next() {
@@ -226,25 +228,29 @@ __device__ __forceinline__ Ahead find(const Args& a, int b, int first, int end, 
   const bool in = first + lane <= (end - 1) >> a.lps;
   return Ahead{first, in ? a.table[(int64_t)b * a.table_ld + first + lane] : 0};
 }
-// Codes and scales of a tile, by the lanes of its groups; groups without a page arrive as zeros.
+// Codes of a tile, by the lanes of its groups; pages that are missing arrive as zeros.
 template <int D>
-__device__ __forceinline__ void load_codes(const Args& a, const CUtensorMap* map, const uint8_t* scales,
-                                           int64_t scale_stride, const Tile& x, uint32_t dst,
-                                           uint32_t scale_dst, uint32_t bar, int lane) {
+__device__ __forceinline__ void load_codes(const Args& a, const CUtensorMap* map, const Tile& x, uint32_t dst,
+                                           uint32_t bar, int lane) {
+  // (copies may land before their bytes are expected: the phase waits for this arrival)
   if (lane == 0) mbar_expect_tx(bar, (uint32_t)(kTile * D));
-  __syncwarp();
-  if (lane < kScaleLanes) {
-    const int page = x.page[lane], row = (x.row + lane * 16) & ((1 << a.lps) - 1);
-    const bool have = page < a.n_pages;
-    // (nothing is read of a page that is missing)
-    const uint8_t* src = scales + (have ? page * scale_stride + ((int64_t)x.h << a.lps) + row : 0);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(scale_dst + lane * 16), "l"(src),
-                 "r"(have ? 16 : 0)
-                 : "memory");
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-    const int groups = 1 << (min(a.lps, 7) - 4);           // of a page
-    if ((lane & (groups - 1)) == 0) tma_load_4d(dst + lane * 16 * D, map, 0, row, x.h, page, bar);
-  }
+  const int groups = 1 << (min(a.lps, 7) - 4);             // of a page
+  if (lane < kTile / 16 && (lane & (groups - 1)) == 0)
+    tma_load_4d(dst + lane * 16 * D, map, 0, (x.row + lane * 16) & ((1 << a.lps) - 1), x.h, x.page[lane], bar);
+}
+// Its scales: K's by lanes 0 to 7, V's by lanes 8 to 15.  Nothing is read of a page that is missing.
+__device__ __forceinline__ void load_scales(const Args& a, const Packed& kv, const Tile& x, uint32_t k_dst,
+                                            uint32_t v_dst, uint32_t bar, int lane) {
+  if (lane >= 2 * kScaleLanes) return;
+  const int i = lane & (kScaleLanes - 1), page = x.page[i];
+  const bool have = page < a.n_pages;
+  const uint8_t* src = lane < kScaleLanes ? kv.k_scale : kv.v_scale;
+  if (have)
+    src += page * kv.scale_stride + ((int64_t)x.h << a.lps) + ((x.row + i * 16) & ((1 << a.lps) - 1));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((lane < kScaleLanes ? k_dst : v_dst) + i * 16),
+               "l"(src), "r"(have ? 16 : 0)
+               : "memory");
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // ---- products --------------------------------------------------------------------------------
@@ -320,21 +326,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (an offset, not a rounded pointer: the compiler then knows that it is shared memory)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::kCtlOff);
-  int64_t* pre = reinterpret_cast<int64_t*>(ctl + 1);
+  int64_t* pre = reinterpret_cast<int64_t*>(smem);       // until the first tile is planned
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) {
-      mbar_init(smem_u32(&ctl->kfull[i]), 1 + kScaleLanes);
+      mbar_init(smem_u32(&ctl->kfull[i]), 1 + 2 * kScaleLanes);
       mbar_init(smem_u32(&ctl->kempty[i]), 1);
     }
     for (int i = 0; i < VS; ++i) mbar_init(smem_u32(&ctl->vempty[i]), 1);   // epilogue
     // V by steps, as many of them as there are stages at most
     for (int i = 0; i < 8; ++i)
-      mbar_init(smem_u32(&ctl->vfull[i]), C::KT * (1 + kScaleLanes) + (i == 0 ? a.withhold : 0));
+      mbar_init(smem_u32(&ctl->vfull[i]), C::KT + (i == 0 ? a.withhold : 0));
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&ctl->tfull[i]), 1);
-      mbar_init(smem_u32(&ctl->tempty[i]), 2);          // K, V
+      mbar_init(smem_u32(&ctl->tempty[i]), 3);          // the loading warps
     }
     for (int i = 0; i < C::SB; ++i) {
       mbar_init(smem_u32(&ctl->sfull[i]), 2);           // the product, and its issuer, who has seen the scales
@@ -369,35 +375,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Shape x(a, s, R, max_q, share);
     return (int64_t)a.Hk * x.rt * x.ns * x.cost;
   });
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (tiles come to the same memory)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   // S of the even and odd tiles, then O
   const uint32_t tmem = ctl->tmem;
   // (waits that go on are calls: with their loops in place the roles' code is larger than the
   // instruction cache)
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase<true>(a, bar, parity, abort_flag); };
-  // The tiles of K (of V) with their scales, as the planner has them.
-  auto load_tiles = [&](auto kind, const CUtensorMap& map, const uint8_t* scales, uint64_t* empty) {
+  // The tiles of K, with both scales, or of V, as the planner has them, in stages `odd`, `odd` + `by`, ..
+  // (a stage has one producer, who sees every phase of its barriers).
+  auto load_tiles = [&](auto kind, uint32_t odd, uint32_t by, const CUtensorMap& map, uint64_t* empty) {
     constexpr bool kV = decltype(kind)::value;
-    constexpr int S = kV ? VS : KS;
+    constexpr uint32_t S = kV ? VS : KS;
     uint32_t n = 0, step = 0;
 #pragma unroll 1
     for (; !*abort_flag; ++n) {
       const uint32_t i = n % S, slot = n % kSlots;
       wait(&ctl->tfull[slot], (n / kSlots) & 1);
       const Tile& x = ctl->tile[slot];
-      if (x.h < 0) break;
-      if (n >= S) wait(&empty[i], (n / S - 1) & 1);
-      if (*abort_flag) break;
-      const uint32_t full = smem_u32(kV ? &ctl->vfull[step % 8] : &ctl->kfull[i]);
-      if (!kV && lane == 0) {
-        ctl->bad[slot] = x.bad;
-        if (x.bad) ctl->any_bad = 1;
+      const int h = x.h, lack = x.lack;
+      if (h < 0) break;
+      if (i % by == odd) {
+        if (n >= S) wait(&empty[i], (n / S - 1) & 1);
+        if (*abort_flag) break;
+        const uint32_t full = smem_u32(kV ? &ctl->vfull[step % 8] : &ctl->kfull[i]);
+        if (!kV) {
+          const uint32_t scale = smem_u32(smem + C::kScaleOff + slot * kTile);
+          load_scales(a, kv, x, scale, scale + kSlots * kTile, full, lane);
+          if (lane == 0) {
+            ctl->bad[slot] = x.bad;
+            if (x.bad) ctl->any_bad = 1;
+          }
+        }
+        load_codes<D>(a, &map, x, smem_u32(smem + (kV ? C::kVOff : 0) + i * C::kTileBytes), full, lane);
+        // V is waited for by steps: the tiles that a step lacks count as there
+        if (kV && lack > 0 && lane == 0) mbar_arrive_n(full, lack);
       }
-      load_codes<D>(a, &map, scales, kv.scale_stride, x, smem_u32(smem + (kV ? C::kVOff : 0) + i * C::kTileBytes),
-                    smem_u32(smem + C::kScaleOff + ((kV ? kSlots : 0) + slot) * kTile), full, lane);
-      // V is waited for by steps: the tiles that a step lacks count as there
-      const int lack = x.lack;
-      if (kV && lack > 0 && lane == 0) mbar_arrive_n(full, lack * (1 + kScaleLanes));
       step += lack >= 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[slot]));
@@ -411,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           drain_phase(a, &ctl->vfull[i % 8], (i / 8) & 1);
       } else {
 #pragma unroll 1
-        for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &ctl->kfull[i % S], (i / S) & 1);
+        for (uint32_t i = n > S ? n - S : 0; i < n; ++i)
+          if (i % S % by == odd) drain_phase(a, &ctl->kfull[i % S], (i / S) & 1);
       }
     }
     __syncwarp();
@@ -421,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- planner: units, and their tiles' pages -------------------------------------------
     uint32_t n = 0, bad = 0;
     Walk walk(a, pre, R, max_q, share);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     bool more = !walk.done();
     Unit x{}, y{};
     Ahead now, next{};                                   // next: the next block of this unit, or the next unit's
@@ -481,10 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bad) raise(a, PP_S_INDEX);
     }
     __syncwarp();
-  } else if (warp == 2) {
-    load_tiles(std::false_type(), mapK, kv.k_scale, ctl->kempty);
+  } else if (warp == 2 || warp == 19) {
+    load_tiles(std::false_type(), warp == 19, 2, mapK, ctl->kempty);
   } else if (warp == 16) {
-    load_tiles(std::true_type(), mapV, kv.v_scale, ctl->vempty);
+    load_tiles(std::true_type(), 0, 1, mapV, ctl->vempty);
   } else if (warp == 1) {
     // ---- MMA issuer of S ------------------------------------------------------------------
     if (lane == 0) {
@@ -540,8 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int t = x.tile0; t < x.tile1; t += C::KT, ++step) {
           const uint32_t g = step & 1;
-          // (whose arrivals have waited for the last O of this buffer, and for V)
-          wait(&ctl->pfull[g], (step >> 1) & 1);
+          wait(&ctl->vfull[step % 8], (step / 8) & 1);
+          wait(&ctl->pfull[g], (step >> 1) & 1);        // (whose arrivals have waited for the last O of this buffer)
           if (*abort_flag) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const int tiles = min(C::KT, x.tile1 - t);
@@ -719,37 +734,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tmem_wait_st();
-        // ---- what V brings: its scales, and rows that must not be multiplied
-        uint32_t nan_value = 0, E = 0;                   // bit k: the value of tile k reads as NaN
-        wait(&ctl->vfull[step % 8], (step / 8) & 1);
+        // ---- V's scales (they came with K's): bit k of nan_value: the value of tile k reads as NaN
+        uint32_t nan_value = 0, E = 0;
 #pragma unroll 1
         for (int k = 0; k < tiles; ++k) {
-          const uint32_t i = (n0 + k) % VS;
           const uint32_t ev = v_scale(k);
           if (ev == 255u) nan_value |= 1u << k;
           if (live >> k & 1u) E = max(E, ev == 255u ? 0u : ev);
-          if (!edge) continue;
-          const int j = j0 + k * kTile;
-          uint4* row = reinterpret_cast<uint4*>(smem + C::kVOff + i * C::kTileBytes + key * D);
-          bool clear = !(live >> k & 1u);
-          if (!clear && !(j <= x.first && (!a.window || j > x.nt - a.window))) {
-            // some rows do not see it: its NaN codes must not meet their weights of zero
-            uint32_t z = 0;
-#pragma unroll 1
-            for (int y = 0; y < D / 16; ++y) {
-              const uint4 w = row[y];
-              z |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
-                   ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
-            }
-            clear = (z & 0x80808080u) != 0;
-            if (clear) nan_value |= 1u << k;
-          }
-          if (clear) {
-#pragma unroll 1
-            for (int y = 0; y < D / 16; ++y) row[y] = make_uint4(0u, 0u, 0u, 0u);
-          }
         }
-        __syncwarp();
         if (!edge || !mixed) {
           E = __reduce_max_sync(0xffffffffu, E);
         } else {
@@ -786,6 +778,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the last step's weights and sums of this buffer have been used
         if (step >= 2) wait(&ctl->oempty[g], ((step >> 1) - 1) & 1);
+        // rows of V that must not be multiplied.  (Only such steps look at V here: its phases of eight steps
+        // ago have been waited for by the product that this wait tells of.)
+        if (edge) {
+          wait(&ctl->vfull[step % 8], (step / 8) & 1);
+#pragma unroll 1
+          for (int k = 0; k < tiles; ++k) {
+            const int j = j0 + k * kTile;
+            uint4* row = reinterpret_cast<uint4*>(smem + C::kVOff + (n0 + k) % VS * C::kTileBytes + key * D);
+            bool clear = !(live >> k & 1u);
+            if (!clear && !(j <= x.first && (!a.window || j > x.nt - a.window))) {
+              // some rows do not see it: its NaN codes must not meet their weights of zero
+              uint32_t z = 0;
+#pragma unroll 1
+              for (int y = 0; y < D / 16; ++y) {
+                const uint4 w = row[y];
+                z |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
+                     ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+              }
+              clear = (z & 0x80808080u) != 0;
+              if (clear) nan_value |= 1u << k;
+            }
+            if (clear) {
+#pragma unroll 1
+              for (int y = 0; y < D / 16; ++y) row[y] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
         if (wq == 0 && lane < R) {
           ctl->m[g][lane] = top - kTop;
           ctl->e[g][lane] = E;
@@ -984,8 +1003,8 @@ cudaError_t run(const Args& a, const PackedPlan& p, const Maps& maps, const Attn
   static_assert(C::KS + C::SB * C::KT <= kSlots && C::VS <= 8, "scales outlive the steps that are under way");
   static_assert(C::kQBytes % 1024 == 0 && C::kPBytes % 1024 == 0 && C::KT * C::NQ <= 128 && C::NP <= 128,
                 "operands start on 1024 bytes, products fit their columns");
-  const size_t smem = C::kCtlOff + sizeof(Ctl) + (size_t)(a.n_seqs + 1) * sizeof(int64_t) + 1024;
-  constexpr size_t most_smem = C::kCtlOff + sizeof(Ctl) + (kMaxSeqs + 1) * sizeof(int64_t) + 1024;
+  constexpr size_t smem = C::kCtlOff + sizeof(Ctl) + 1024, most_smem = smem;
+  static_assert((kMaxSeqs + 1) * sizeof(int64_t) <= C::kVOff, "prefix sums lie where the K tiles come to");
   static_assert(most_smem <= 227 * 1024, "attention shared memory");
   static std::atomic<uint64_t> done{0};
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(k_packed_attn<T, D, R>), most_smem, done);

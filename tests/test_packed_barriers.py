@@ -26,12 +26,14 @@ def packed(seed, units, stages, most, buffers=4, late=False):
     soon as its product is done, before the epilogue has taken the step's sums."""
     s, ring = Schedule(seed), Ring(16)
     ks, vs = stages
-    kfull, kempty, vfull, vempty = bars(ks, 9), bars(ks, 1), bars(8, 9 * most), bars(vs, 1)
+    kfull, kempty, vfull, vempty = bars(ks, 17), bars(ks, 1), bars(8, most), bars(vs, 1)
     sfull, sempty = bars(buffers, 2), bars(buffers, 4)
     qfull, qempty = bars(2, 2), bars(2, 8)
     pfull, ofull, oempty = bars(2, 4), bars(2, 1), bars(2, 4)
-    tfull, tempty, tile = bars(SLOTS, 1), bars(SLOTS, 2), {}
-    meet, held = bars(2, 4), {"k": {}, "v": {}}
+    tfull, tempty, tile = bars(SLOTS, 1), bars(SLOTS, 3), {}
+    meet, held = bars(2, 4), {}
+
+    edges = {}                                  # steps in which rows of V are cleared
 
     def steps(count):
         return [min(most, count - t) for t in range(0, count, most)]
@@ -53,23 +55,26 @@ def packed(seed, units, stages, most, buffers=4, late=False):
         tile[n % SLOTS] = None
         tfull[n % SLOTS].arrive()
 
-    def loads(name, empty):
+    def loads(kind, odd, by, empty):
         n, size, step = 0, len(empty), 0
         while True:
             yield tfull[n % SLOTS], n // SLOTS
             lack = tile[n % SLOTS]
             if lack is None:
                 return
-            if n >= size:
-                yield empty[n % size], n // size - 1
-            # the scales of the tile that had this place are no longer looked at
-            assert held[name].get(n % SLOTS, 0) == 0, "scales overwritten"
-            held[name][n % SLOTS] = 4
-            full = kfull[n % size] if name == "k" else vfull[step % 8]
-            s.load(full)
-            s.copies += [Arrival(full) for _ in range(8)]
-            for _ in range(9 * lack if name == "v" and lack > 0 else 0):
-                full.arrive()
+            if n % size % by == odd:
+                if n >= size:
+                    yield empty[n % size], n // size - 1
+                if kind == "k":
+                    # the scales of the tile that had this place are no longer looked at
+                    assert held.get(n % SLOTS, 0) == 0, "scales overwritten"
+                    held[n % SLOTS] = 4
+                    s.copies += [Arrival(kfull[n % size]) for _ in range(16)]
+                    s.load(kfull[n % size])
+                else:
+                    s.load(vfull[step % 8])
+                    for _ in range(lack):
+                        vfull[step % 8].arrive()
             step += lack >= 0
             tempty[n % SLOTS].arrive()
             n += 1
@@ -99,6 +104,7 @@ def packed(seed, units, stages, most, buffers=4, late=False):
         for k, count in enumerate(units):
             yield from ring.get(k)
             for kt in steps(count):
+                yield vfull[step % 8], step // 8
                 yield pfull[step & 1], step >> 1
                 s.commits.append(ofull[step & 1])
                 step += 1
@@ -130,17 +136,16 @@ def packed(seed, units, stages, most, buffers=4, late=False):
                     mine = range(n - kt, n)
                     yield sfull[step % buffers], step // buffers
                     yield from s.work(5)
-                    for m in mine:
-                        held["k"][m % SLOTS] -= 1
-                    yield vfull[step % 8], step // 8
                     meet[g].arrive()
                     yield meet[g], met
                     met += 1
                     if step >= 2:
                         yield (ofull if late else oempty)[g], (step >> 1) - 1
+                    if edges[step] if step in edges else edges.setdefault(step, s.rng.random() < 0.3):
+                        yield vfull[step % 8], step // 8
                     yield from s.work(5)
                     for m in mine:
-                        held["v"][m % SLOTS] -= 1
+                        held[m % SLOTS] -= 1
                     pfull[g].arrive()
                     sempty[step % buffers].arrive()
                 step += 1
@@ -164,13 +169,14 @@ def packed(seed, units, stages, most, buffers=4, late=False):
             yield from s.work(10)
         yield from ring.get(len(units))
 
-    s.run([planner(), loads("k", kempty), loads("v", vempty), scores(), values()] +
+    s.run([planner(), loads("k", 0, 2, kempty), loads("k", 1, 2, kempty),
+           loads("v", 0, 1, vempty), scores(), values()] +
           [softmax(w // 4) for w in range(8)] + [epilogue(w) for w in range(4)] +
           [queries() for _ in range(2)])
 
 
 @pytest.mark.parametrize("most,buffers", [(1, 2), (1, 4), (2, 4)])
-@pytest.mark.parametrize("stages", [(3, 6), (3, 7), (8, 8)])
+@pytest.mark.parametrize("stages", [(3, 7), (3, 8), (8, 8)])
 @pytest.mark.parametrize("seed", SEEDS)
 def test_packed_attention(seed, stages, most, buffers):
     r = random.Random(seed)
@@ -183,4 +189,4 @@ def test_packed_attention(seed, stages, most, buffers):
 def test_a_buffer_that_is_used_again_too_early_mistakes_a_phase():
     with pytest.raises(AssertionError, match="phase|deadlock"):
         for seed in range(200):
-            packed(seed, [9, 1, 1, 30, 2], (3, 7), 1, late=True)
+            packed(seed, [9, 1, 1, 30, 2], (3, 8), 1, late=True)
