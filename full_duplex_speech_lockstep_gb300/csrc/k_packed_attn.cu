@@ -46,21 +46,25 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kReaders = 16;         // of the units: both issuers, eight of softmax, epilogue, queries
-constexpr int kSlots = 16;           // tiles that are planned, and those whose scales are held
+constexpr int kSlots = 32;           // tiles that are planned, and those whose scales are held
 constexpr int kParts = 3;            // of a weight
 constexpr float kTop = 8.f;          // a tile's largest weight is 2^8 (e4m3 holds up to 448)
+
+// Few rows: a thread has 8 or 16 scores a step all the same.
+__host__ __device__ constexpr int step_tiles(int R) { return R < 8 ? 4 : R == 8 ? 2 : 1; }
 
 template <typename T, int D, int R>
 struct Cfg {
   static constexpr int QP = sizeof(T) == 2 && Num<T>::kShift == 0.f ? 2 : 3;   // parts of a query
   static constexpr int NQ = (QP * R + 15) / 16 * 16;                 // columns of S
   static constexpr int NP = (kParts * R + 15) / 16 * 16;             // columns of O
-  static constexpr int KT = R == 8 ? 2 : 1;                          // tiles of a step
+  static constexpr int KT = step_tiles(R);                           // tiles of a step
+  static constexpr int W = R < 8 ? R : 8;                            // rows at a time
   static constexpr int SB = KT * NQ <= 64 ? 4 : 2;                   // buffers of S in tensor memory
   static constexpr int kTileBytes = kTile * D;
   // Stages of K, which a product frees at once, and of V, which waits for the softmax.
   static constexpr int KS = D == 128 ? 3 : 8;
-  static constexpr int VS = D == 128 ? (R == 32 ? 7 : 8) : 8;
+  static constexpr int VS = D == 128 ? (R < 32 ? 8 : QP == 2 ? 7 : 6) : 8;
   static constexpr int kQBytes = NQ * 128;
   static constexpr int kPBytes = NP / 16 * 2048;
   static constexpr int kVOff = KS * kTileBytes;
@@ -138,7 +142,7 @@ struct Shape {       // of a sequence's units
     rt = (int)(((int64_t)s.n * a.G + R - 1) / R);
     ns = s.n > max_q ? 1 : n_splits(mt, share);
     // a unit's ends and a step's cost as much as a tile each (steps of `per` tiles)
-    const int per = R == 8 ? 2 : 1, st = (mt + ns - 1) / ns;
+    const int per = step_tiles(R), st = (mt + ns - 1) / ns;
     cost = st + (st + per - 1) / per + 1;
   }
 };
@@ -306,6 +310,30 @@ __device__ __forceinline__ void split4(uint32_t x, uint32_t y, uint32_t (&w)[P])
 // 2^(byte - 127), NaN for 255
 __device__ __forceinline__ float scale_of(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7fc00000u : byte == 0u ? 0x00400000u : byte << 23);
+}
+// W consecutive columns of this thread's tensor-memory lane (no wait)
+template <int W>
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t* r) {
+  if constexpr (W == 8)
+    tmem_ld8(t, r);
+  else if constexpr (W == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(t));
+  else
+    tmem_ld2(t, r);
+}
+template <int W>
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t* r) {
+  if constexpr (W == 8)
+    tmem_st8(t, r);
+  else if constexpr (W == 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(t), "r"(r[0]), "r"(r[1])
+                 : "memory");
 }
 __device__ __forceinline__ float warp_max(float x) {
   float y;
@@ -579,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 17) {
     // ---- queries: L lanes to a row, four dims to a lane -----------------------------------
     constexpr int L = D / 4, kSide = 2 * 32 / L;           // rows side by side, of two warps
-    constexpr int kAhead = R / kSide < 4 ? R / kSide : 4;  // passes loaded at once
+    constexpr int kAhead = R <= kSide ? 1 : R / kSide < 4 ? R / kSide : 4;   // passes loaded at once
     const int l = lane % L, side = (threadIdx.x - 544) / L;
     const uint32_t per_head = (65536u + a.G - 1) / a.G;    // f / G for f G < 2^16
     uint32_t nq = 0;
@@ -622,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e) y[e] = wild ? 0.f : y[e] * f;
           uint32_t w[C::QP];
           split4<C::QP>(to_half(y[0], y[1]), to_half(y[2], y[3]), w);
+          if (r >= R) continue;                          // (fewer rows than lie side by side)
 #pragma unroll
           for (int p = 0; p < C::QP; ++p) {
             const int n = p * R + r;
@@ -642,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 12) {
     // ---- softmax: thread k of a group owns key k of the group's tiles ---------------------
     const uint32_t g = warp >= 8;
+    constexpr int W = C::W;
     const int wq = warp & 3, key = wq * 32 + lane;
     uint8_t* const weights = smem + C::kPOff + g * C::KT * C::kPBytes + key * 16;
     uint32_t n = 0, step = 0, nq = 0, meets = 0;
@@ -697,38 +727,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         // maxima: lane r has row r's.  The scores wait in tensor memory, over S.
         float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < rows; c += 8) {
-          float most[8], f[8];
-          *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&ctl->row_c[qb][c]);
-          *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&ctl->row_c[qb][c + 4]);
+        for (int c = 0; c < rows; c += W) {
+          float most[W], f[W];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) most[e] = -INFINITY;
+          for (int e = 0; e < W; ++e) {
+            most[e] = -INFINITY;
+            f[e] = ctl->row_c[qb][c + e];
+          }
 #pragma unroll 1
           for (int k = 0; k < tiles; ++k) {
-            uint32_t s[C::QP][8];
+            const uint32_t at = scores + k * C::NQ + c;
+            uint32_t s[R < 8 ? 16 : C::QP * 8];          // parts side by side, R (8) columns apart
+            if constexpr (R < 8) {
+              tmem_ld16(at, s);
+            } else {
 #pragma unroll
-            for (int p = 0; p < C::QP; ++p) tmem_ld8(scores + k * C::NQ + p * R + c, s[p]);
+              for (int p = 0; p < C::QP; ++p) tmem_ld8(at + p * R, s + p * 8);
+            }
             const float kf = k_scale(k);
             const uint64_t kf2 = f32x2(kf, kf);
-            const uint32_t seen = see >> (k * R + c);
-            float v[8];
+            float v[W];
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              uint64_t y = f32x2(after_wait(s[C::QP - 1][e]), after_wait(s[C::QP - 1][e + 1]));
+            for (int e = 0; e < W; e += 2) {
+              uint64_t y = f32x2(after_wait(s[(C::QP - 1) * W + e]), after_wait(s[(C::QP - 1) * W + e + 1]));
 #pragma unroll
               for (int p = C::QP - 2; p >= 0; --p)
-                y = fma2(y, f32x2(0.0625f, 0.0625f), f32x2(after_wait(s[p][e]), after_wait(s[p][e + 1])));
+                y = fma2(y, f32x2(0.0625f, 0.0625f),
+                         f32x2(after_wait(s[p * W + e]), after_wait(s[p * W + e + 1])));
               y = mul2(mul2(y, kf2), f32x2(f[e], f[e + 1]));
-              v[e] = seen & (1u << e) ? lo_of(y) : -INFINITY;
-              v[e + 1] = seen & (2u << e) ? hi_of(y) : -INFINITY;
+              v[e] = lo_of(y);
+              v[e + 1] = hi_of(y);
             }
-            tmem_st8(scores + k * C::NQ + c, reinterpret_cast<const uint32_t*>(v));
+            if (edge) {
+              const uint32_t seen = see >> (k * R + c);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) most[e] = fmaxf(most[e], v[e]);
+              for (int e = 0; e < W; ++e) v[e] = seen & (1u << e) ? v[e] : -INFINITY;
+            }
+            tmem_st<W>(at, reinterpret_cast<const uint32_t*>(v));
+#pragma unroll
+            for (int e = 0; e < W; ++e) most[e] = fmaxf(most[e], v[e]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < W; ++e) {
             const float y = warp_max(most[e]);
             if (lane - c == e) top = y;
           }
@@ -813,58 +854,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- weights: w = p 2^(ev - 127) 2^(127 - E).  (What lies below fp32's normal range between
         // the two factors is 2^-30 of the largest weight or less.)
 #pragma unroll 1
-        for (int c = 0; c < rows; c += 8) {
-          float f[8], u[8], sum[8];
+        for (int c = 0; c < rows; c += W) {
+          float f[W], u[W], sum[W];
 #pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            *reinterpret_cast<float4*>(f + e) = *reinterpret_cast<const float4*>(&ctl->ref[g][wq][c + e]);
-            *reinterpret_cast<float4*>(u + e) = *reinterpret_cast<const float4*>(&ctl->fit[g][wq][c + e]);
+          for (int e = 0; e < W; ++e) {
+            f[e] = ctl->ref[g][wq][c + e];
+            u[e] = ctl->fit[g][wq][c + e];
+            sum[e] = 0.f;
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] = 0.f;
 #pragma unroll 1
           for (int k = 0; k < tiles; ++k) {
-            uint32_t s[8];
-            tmem_ld8(scores + k * C::NQ + c, s);
+            uint32_t s[W], y[W / 2];
+            tmem_ld<W>(scores + k * C::NQ + c, s);
             const float vf = nan_value >> k & 1u ? __uint_as_float(0x7fc00000u) : scale_of(v_scale(k));
             const uint64_t vf2 = f32x2(vf, vf);
             tmem_wait_ld();
-            uint32_t y[4];
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
+            for (int e = 0; e < W; e += 2) {
               const float v0 = after_wait(s[e]), v1 = after_wait(s[e + 1]);
               const uint64_t x2 = add2(f32x2(v0, v1), f32x2(f[e], f[e + 1]));
               const float p0 = exp2_approx(lo_of(x2)), p1 = exp2_approx(hi_of(x2));
               const uint64_t w2 = mul2(mul2(f32x2(p0, p1), vf2), f32x2(u[e], u[e + 1]));
-              // (not a NaN of a value that a row does not see)
-              y[e / 2] = to_half(v0 == -INFINITY ? 0.f : lo_of(w2), v1 == -INFINITY ? 0.f : hi_of(w2));
+              float w0 = lo_of(w2), w1 = hi_of(w2);
+              if (edge) {                                // (not a NaN of a value that a row does not see)
+                if (v0 == -INFINITY) w0 = 0.f;
+                if (v1 == -INFINITY) w1 = 0.f;
+              }
+              y[e / 2] = to_half(w0, w1);
               sum[e] += p0;
               sum[e + 1] += p1;
             }
+            uint8_t* to = weights + k * C::kPBytes;
             uint32_t w[2][kParts];
-            split4<kParts>(y[0], y[1], w[0]);
-            split4<kParts>(y[2], y[3], w[1]);
+            if constexpr (W == 2) {                      // columns: two rows' first parts, then their second, ..
+              split4<kParts>(y[0], y[0], w[0]);
+              *reinterpret_cast<uint2*>(to) =
+                  make_uint2(__byte_perm(w[0][0], w[0][1], 0x5410), w[0][2] & 0xffffu);
+            } else if constexpr (W == 4) {
+              split4<kParts>(y[0], y[1], w[0]);
+              *reinterpret_cast<uint2*>(to) = make_uint2(w[0][0], w[0][1]);
+              *reinterpret_cast<uint32_t*>(to + 8) = w[0][2];
+            } else {
+              split4<kParts>(y[0], y[1], w[0]);
+              split4<kParts>(y[2], y[3], w[1]);
 #pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-              const int col = p * R + c;
-              *reinterpret_cast<uint2*>(weights + k * C::kPBytes + (col >> 4) * 2048 + (col & 15)) =
-                  make_uint2(w[0][p], w[1][p]);
+              for (int p = 0; p < kParts; ++p) {
+                const int col = p * R + c;
+                *reinterpret_cast<uint2*>(to + (col >> 4) * 2048 + (col & 15)) = make_uint2(w[0][p], w[1][p]);
+              }
             }
           }
-          // sums of the eight rows over the warp's keys: lanes halve the rows, then the keys
+          // sums of the rows over the warp's keys: lanes halve the rows while there are several
+          int row = c;
 #pragma unroll
-          for (int k = 4, d = 16; k > 0; k >>= 1, d >>= 1) {
-            const bool up = lane & d;
+          for (int d = 16, k = W / 2; d > 0; d >>= 1, k >>= 1) {
+            if (k > 0) {
+              const bool up = lane & d;
+              row += up ? k : 0;
 #pragma unroll
-            for (int e = 0; e < k; ++e) {
-              const float give = up ? sum[e] : sum[e + k];
-              sum[e] = (up ? sum[e + k] : sum[e]) + __shfl_xor_sync(0xffffffffu, give, d);
+              for (int e = 0; e < k; ++e) {
+                const float give = up ? sum[e] : sum[e + k];
+                sum[e] = (up ? sum[e + k] : sum[e]) + __shfl_xor_sync(0xffffffffu, give, d);
+              }
+            } else {
+              sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
             }
           }
-          sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
-          sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
-          if ((lane & 3) == 0)
-            ctl->l[g][wq][c + (lane >> 2 & 1) + (lane >> 3 & 1) * 2 + (lane >> 4) * 4] = sum[0];
+          if ((lane & (32 / W - 1)) == 0) ctl->l[g][wq][row] = sum[0];
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -880,6 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---- epilogue: thread d owns dim d; lane r of each warp keeps row r's maximum and sum ---
+    constexpr int W = C::W;
     const int wq = warp & 3, d = wq * 32 + lane, H = a.Hk * a.G;
     const uint32_t lane_at = tmem + ((uint32_t)(wq * 32) << 16) + 256;
     uint32_t n = 0, step = 0;
@@ -912,22 +969,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (*abort_flag) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-        for (int c = 0; c < R; c += 8) {
+        for (int c = 0; c < R; c += W) {
           if (c >= rows) break;
-          uint32_t y[kParts][8];
+          uint32_t y[R < 8 ? 16 : kParts * 8];           // parts side by side, R (8) columns apart
+          if constexpr (R < 8) {
+            tmem_ld16(lane_at + g * 128, y);
+          } else {
 #pragma unroll
-          for (int p = 0; p < kParts; ++p) tmem_ld8(lane_at + g * 128 + p * R + c, y[p]);
-          float keep[8], add[8];
+            for (int p = 0; p < kParts; ++p) tmem_ld8(lane_at + g * 128 + p * R + c, y + p * 8);
+          }
+          float keep[W], add[W];
 #pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            *reinterpret_cast<float4*>(keep + e) = *reinterpret_cast<const float4*>(&ctl->keep[wq][c + e]);
-            *reinterpret_cast<float4*>(add + e) = *reinterpret_cast<const float4*>(&ctl->add[wq][c + e]);
+          for (int e = 0; e < W; ++e) {
+            keep[e] = ctl->keep[wq][c + e];
+            add[e] = ctl->add[wq][c + e];
           }
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float z = fmaf(fmaf(after_wait(y[2][e]), 0.0625f, after_wait(y[1][e])), 0.0625f,
-                                 after_wait(y[0][e]));
+          for (int e = 0; e < W; ++e) {
+            const float z = fmaf(fmaf(after_wait(y[2 * W + e]), 0.0625f, after_wait(y[W + e])), 0.0625f,
+                                 after_wait(y[e]));
             acc[c + e] = fmaf(acc[c + e], keep[e], z * add[e]);
           }
         }
@@ -1024,7 +1085,9 @@ cudaError_t run(const Args& a, const PackedPlan& p, const Maps& maps, const Attn
 template <typename T, int D>
 cudaError_t pick(const Args& a, const PackedPlan& p, const Maps& maps, const AttnOut& o,
                  const Packed& kv, const void* q, int64_t q_stride, cudaStream_t s) {
-  return p.R == 8    ? run<T, D, 8>(a, p, maps, o, kv, q, q_stride, s)
+  return p.R == 2    ? run<T, D, 2>(a, p, maps, o, kv, q, q_stride, s)
+         : p.R == 4  ? run<T, D, 4>(a, p, maps, o, kv, q, q_stride, s)
+         : p.R == 8  ? run<T, D, 8>(a, p, maps, o, kv, q, q_stride, s)
          : p.R == 16 ? run<T, D, 16>(a, p, maps, o, kv, q, q_stride, s)
                      : run<T, D, 32>(a, p, maps, o, kv, q, q_stride, s);
 }
@@ -1034,7 +1097,8 @@ cudaError_t pick(const Args& a, const PackedPlan& p, const Maps& maps, const Att
 PackedPlan packed_plan(const Args& a, int max_q) {
   PackedPlan p{};
   const int rows = max_q * a.G;
-  p.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  p.R = 2;
+  while (p.R < rows && p.R < 32) p.R *= 2;
   p.max_q = max_q;
   const int heads = a.Hk * ((rows + p.R - 1) / p.R);
   p.share = kSms / heads < 1 ? 1 : kSms / heads;

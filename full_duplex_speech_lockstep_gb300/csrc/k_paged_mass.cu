@@ -133,17 +133,6 @@ struct Walk {
   }
 };
 
-// 16 columns of this thread's tensor-memory lane
-__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t r[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(t));
-}
-
 // Sum of 2^(s c + ref) over the columns [0, cols) of a lane, those outside [lo, hi) left out
 // (`masked`); cols is a multiple of W otherwise.  Rows of no sum have a ref of -infinity and give 0
 // unless their s is a NaN or +infinity: then the sum is NaN, but for masked steps of few rows, which

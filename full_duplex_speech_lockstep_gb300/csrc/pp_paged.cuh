@@ -609,7 +609,7 @@ cudaError_t launch_packed_read(const Args& a, int type, const ReadArgs& x, cudaS
 // (k_packed_attn.cu); longer ones on a 16-bit copy of what they see.
 constexpr int kPackedRows = 128;
 struct PackedPlan {
-  int R;           // rows of a row tile: 8, 16 or 32
+  int R;           // rows of a row tile: 2, 4, 8, 16 or 32
   int max_q;
   int share;       // SMs for each (sequence, key head, row tile), at least 1
   int ns_cap;      // splits of the longest sequence that the table can hold

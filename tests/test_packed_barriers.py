@@ -18,7 +18,7 @@ class Arrival:
         self.bar.arrive()
 
 
-SLOTS = 16     # tiles that are planned, and those whose scales are held
+SLOTS = 32     # tiles that are planned, and those whose scales are held
 
 
 def packed(seed, units, stages, most, buffers=4, late=False):
@@ -175,7 +175,7 @@ def packed(seed, units, stages, most, buffers=4, late=False):
           [queries() for _ in range(2)])
 
 
-@pytest.mark.parametrize("most,buffers", [(1, 2), (1, 4), (2, 4)])
+@pytest.mark.parametrize("most,buffers", [(1, 2), (1, 4), (2, 4), (4, 4)])
 @pytest.mark.parametrize("stages", [(3, 7), (3, 8), (8, 8)])
 @pytest.mark.parametrize("seed", SEEDS)
 def test_packed_attention(seed, stages, most, buffers):
