@@ -25,8 +25,7 @@
 //   warp 0       the units and their tiles' pages, up to 16 tiles ahead.  (With lookups in the warps that
 //                load, a tile took 1150 clocks and a unit's start 3600.)
 //   warp 1       one thread issues the MMAs of S
-//   warps 2, 19, 16   K tiles with both scales, of even and odd stages (a tile takes a warp 1000 clocks);
-//                V tiles
+//   warps 2, 16  K tiles with both scales; V tiles
 //   warp 3       one thread issues the MMAs of O.  (One thread for both took 1900 clocks a tile.)
 //   warps 4-7, 8-11   softmax of every second step
 //   warps 12-15  epilogue: a thread owns one dim
@@ -44,7 +43,7 @@ namespace pp {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 608;
 constexpr int kReaders = 16;         // of the units: both issuers, eight of softmax, epilogue, queries
 constexpr int kSlots = 32;           // tiles that are planned, and those whose scales are held
 constexpr int kParts = 3;            // of a weight
@@ -63,8 +62,8 @@ struct Cfg {
   static constexpr int SB = KT * NQ <= 64 ? 4 : 2;                   // buffers of S in tensor memory
   static constexpr int kTileBytes = kTile * D;
   // Stages of K, which a product frees at once, and of V, which waits for the softmax.
-  static constexpr int KS = D == 128 ? 3 : 8;
-  static constexpr int VS = D == 128 ? (R < 32 ? 8 : QP == 2 ? 7 : 6) : 8;
+  static constexpr int KS = D == 128 ? 4 : 8;
+  static constexpr int VS = D == 128 ? (R < 32 ? 7 : QP == 2 ? 6 : 5) : 8;
   static constexpr int kQBytes = NQ * 128;
   static constexpr int kPBytes = NP / 16 * 2048;
   static constexpr int kVOff = KS * kTileBytes;
@@ -120,12 +119,13 @@ __host__ __device__ __forceinline__ int64_t most_tiles(int64_t entries, int wind
   const int64_t seen = ((int64_t)window + span - 2) / kTile + 2;
   return window && seen < all ? seen : all;
 }
-// Tiles of one split: `share` splits of each key head fill the SMs when a sequence is alone.  From four
-// (shorter units leave the pipeline between them idle) to eight (runs of units come out even), and at
-// most 128 splits.
+// Tiles of one split: `share` splits of each key head fill the SMs when a sequence is alone.  From twelve (a
+// unit's ends cost 4000 clocks, as much as six tiles: four to eight tiles took 201 us on the 64-session
+// tick) to 24 (runs of units come out even), and at most 128 splits.
+constexpr int kLeast = 12, kMost = 24;
 __host__ __device__ __forceinline__ int64_t split_tiles(int64_t tiles, int share) {
   int64_t st = (tiles + share - 1) / share;
-  st = st < 4 ? 4 : st > 8 ? 8 : st;
+  st = st < kLeast ? kLeast : st > kMost ? kMost : st;
   const int64_t even = (tiles + 127) / 128;
   return st > even ? st : even;
 }
@@ -141,9 +141,10 @@ struct Shape {       // of a sequence's units
     const int mt = (int)most_tiles(s.len, a.window, row_span(R, a.G));
     rt = (int)(((int64_t)s.n * a.G + R - 1) / R);
     ns = s.n > max_q ? 1 : n_splits(mt, share);
-    // a unit's ends and a step's cost as much as a tile each (steps of `per` tiles)
-    const int per = step_tiles(R), st = (mt + ns - 1) / ns;
-    cost = st + (st + per - 1) / per + 1;
+    // Of a unit, in about 250 clocks: its tiles (by rows), steps and ends.  (Counted by tiles and steps alone,
+    // the SMs' times went from 108 to 201 us on the 64-session tick.)
+    const int per = step_tiles(R), st = (mt + ns - 1) / ns, chunks = (min(s.n * a.G, R) + 7) / 8;
+    cost = R < 8 ? 2 * st + 4 * ((st + per - 1) / per) + 12 : st * (per == 2 ? 4 : 3 + 2 * chunks) + 12;
   }
 };
 
@@ -232,26 +233,25 @@ __device__ __forceinline__ Ahead find(const Args& a, int b, int first, int end, 
   const bool in = first + lane <= (end - 1) >> a.lps;
   return Ahead{first, in ? a.table[(int64_t)b * a.table_ld + first + lane] : 0};
 }
-// Codes of a tile, by the lanes of its groups; pages that are missing arrive as zeros.
+// Codes of a tile by its groups' lanes (0 to 7); pages that are missing arrive as zeros.
 template <int D>
 __device__ __forceinline__ void load_codes(const Args& a, const CUtensorMap* map, const Tile& x, uint32_t dst,
-                                           uint32_t bar, int lane) {
+                                           uint32_t bar, int l) {
   // (copies may land before their bytes are expected: the phase waits for this arrival)
-  if (lane == 0) mbar_expect_tx(bar, (uint32_t)(kTile * D));
+  if (l == 0) mbar_expect_tx(bar, (uint32_t)(kTile * D));
   const int groups = 1 << (min(a.lps, 7) - 4);             // of a page
-  if (lane < kTile / 16 && (lane & (groups - 1)) == 0)
-    tma_load_4d(dst + lane * 16 * D, map, 0, (x.row + lane * 16) & ((1 << a.lps) - 1), x.h, x.page[lane], bar);
+  if (l < kTile / 16 && (l & (groups - 1)) == 0)
+    tma_load_4d(dst + l * 16 * D, map, 0, (x.row + l * 16) & ((1 << a.lps) - 1), x.h, x.page[l], bar);
 }
 // Its scales: K's by lanes 0 to 7, V's by lanes 8 to 15.  Nothing is read of a page that is missing.
 __device__ __forceinline__ void load_scales(const Args& a, const Packed& kv, const Tile& x, uint32_t k_dst,
-                                            uint32_t v_dst, uint32_t bar, int lane) {
-  if (lane >= 2 * kScaleLanes) return;
-  const int i = lane & (kScaleLanes - 1), page = x.page[i];
+                                            uint32_t v_dst, uint32_t bar, int l) {
+  const int i = l & (kScaleLanes - 1), page = x.page[i];
   const bool have = page < a.n_pages;
-  const uint8_t* src = lane < kScaleLanes ? kv.k_scale : kv.v_scale;
+  const uint8_t* src = l < kScaleLanes ? kv.k_scale : kv.v_scale;
   if (have)
     src += page * kv.scale_stride + ((int64_t)x.h << a.lps) + ((x.row + i * 16) & ((1 << a.lps) - 1));
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((lane < kScaleLanes ? k_dst : v_dst) + i * 16),
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((l < kScaleLanes ? k_dst : v_dst) + i * 16),
                "l"(src), "r"(have ? 16 : 0)
                : "memory");
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->vfull[i]), C::KT + (i == 0 ? a.withhold : 0));
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&ctl->tfull[i]), 1);
-      mbar_init(smem_u32(&ctl->tempty[i]), 3);          // the loading warps
+      mbar_init(smem_u32(&ctl->tempty[i]), 2);          // K, V
     }
     for (int i = 0; i < C::SB; ++i) {
       mbar_init(smem_u32(&ctl->sfull[i]), 2);           // the product, and its issuer, who has seen the scales
@@ -410,38 +410,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (waits that go on are calls: with their loops in place the roles' code is larger than the
   // instruction cache)
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase<true>(a, bar, parity, abort_flag); };
-  // The tiles of K, with both scales, or of V, as the planner has them, in stages `odd`, `odd` + `by`, ..
-  // (a stage has one producer, who sees every phase of its barriers).
-  auto load_tiles = [&](auto kind, uint32_t odd, uint32_t by, const CUtensorMap& map, uint64_t* empty) {
+  // The tiles of K, with both scales, or of V, as the planner has them: two at a time, half a warp to each.
+  // (One at a time took 1000 clocks a tile, nearly all of it latencies.)
+  auto load_tiles = [&](auto kind, const CUtensorMap& map, uint64_t* empty) {
     constexpr bool kV = decltype(kind)::value;
     constexpr uint32_t S = kV ? VS : KS;
-    uint32_t n = 0, step = 0;
+    const int half = lane >> 4, l = lane & 15;
+    uint32_t n = 0, step = 0;                            // of tiles and steps before this round
+    bool live = true;
 #pragma unroll 1
-    for (; !*abort_flag; ++n) {
-      const uint32_t i = n % S, slot = n % kSlots;
-      wait(&ctl->tfull[slot], (n / kSlots) & 1);
+    while (live) {
+      const uint32_t m = n + half, i = m % S, slot = m % kSlots;
+      wait(&ctl->tfull[slot], (m / kSlots) & 1);
       const Tile& x = ctl->tile[slot];
-      const int h = x.h, lack = x.lack;
-      if (h < 0) break;
-      if (i % by == odd) {
-        if (n >= S) wait(&empty[i], (n / S - 1) & 1);
-        if (*abort_flag) break;
-        const uint32_t full = smem_u32(kV ? &ctl->vfull[step % 8] : &ctl->kfull[i]);
+      const int lack = x.lack;
+      live = x.h >= 0;
+      if (live && m >= S) wait(&empty[i], (m / S - 1) & 1);
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      const int ends = __shfl_sync(0xffffffffu, lack >= 0, 0);   // the first tile ends a step
+      if (live) {
+        const uint32_t full = smem_u32(kV ? &ctl->vfull[(step + (half ? ends : 0)) % 8] : &ctl->kfull[i]);
         if (!kV) {
           const uint32_t scale = smem_u32(smem + C::kScaleOff + slot * kTile);
-          load_scales(a, kv, x, scale, scale + kSlots * kTile, full, lane);
-          if (lane == 0) {
+          load_scales(a, kv, x, scale, scale + kSlots * kTile, full, l);
+          if (l == 0) {
             ctl->bad[slot] = x.bad;
             if (x.bad) ctl->any_bad = 1;
           }
         }
-        load_codes<D>(a, &map, x, smem_u32(smem + (kV ? C::kVOff : 0) + i * C::kTileBytes), full, lane);
+        load_codes<D>(a, &map, x, smem_u32(smem + (kV ? C::kVOff : 0) + i * C::kTileBytes), full, l);
         // V is waited for by steps: the tiles that a step lacks count as there
-        if (kV && lack > 0 && lane == 0) mbar_arrive_n(full, lack);
+        if (kV && lack > 0 && l == 0) mbar_arrive_n(full, lack);
+        if (l == 0) mbar_arrive(smem_u32(&ctl->tempty[slot]));
       }
-      step += lack >= 0;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[slot]));
+      const uint32_t both = __ballot_sync(0xffffffffu, live);
+      n += (both & 1u) + (both >> 16 & 1u);
+      step += (both & 1u ? ends : 0) + __shfl_sync(0xffffffffu, live && lack >= 0 ? 1 : 0, 16);
+      live = both == 0xffffffffu;
     }
     // every copy lands before the CTA may exit (bounded waits)
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -452,8 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           drain_phase(a, &ctl->vfull[i % 8], (i / 8) & 1);
       } else {
 #pragma unroll 1
-        for (uint32_t i = n > S ? n - S : 0; i < n; ++i)
-          if (i % S % by == odd) drain_phase(a, &ctl->kfull[i % S], (i / S) & 1);
+        for (uint32_t i = n > S ? n - S : 0; i < n; ++i) drain_phase(a, &ctl->kfull[i % S], (i / S) & 1);
       }
     }
     __syncwarp();
@@ -514,20 +518,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit last{};
     last.b = -1;
     put_unit<true>(a, ctl->ring, nu, last, lane, abort_flag);
-    const int slot = n % kSlots;
-    if (n >= kSlots) wait(&ctl->tempty[slot], (n / kSlots - 1) & 1);
-    if (lane == 0) {
-      if (!*abort_flag) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i, ++n) {                   // (two: tiles are loaded in pairs)
+      const int slot = n % kSlots;
+      if (n >= kSlots) wait(&ctl->tempty[slot], (n / kSlots - 1) & 1);
+      if (lane == 0 && !*abort_flag) {
         ctl->tile[slot].h = -1;
         mbar_arrive(smem_u32(&ctl->tfull[slot]));
       }
-      if (bad) raise(a, PP_S_INDEX);
     }
+    if (bad && lane == 0) raise(a, PP_S_INDEX);
     __syncwarp();
-  } else if (warp == 2 || warp == 19) {
-    load_tiles(std::false_type(), warp == 19, 2, mapK, ctl->kempty);
+  } else if (warp == 2) {
+    load_tiles(std::false_type(), mapK, ctl->kempty);
   } else if (warp == 16) {
-    load_tiles(std::true_type(), 0, 1, mapV, ctl->vempty);
+    load_tiles(std::true_type(), mapV, ctl->vempty);
   } else if (warp == 1) {
     // ---- MMA issuer of S ------------------------------------------------------------------
     if (lane == 0) {
@@ -1103,9 +1108,9 @@ PackedPlan packed_plan(const Args& a, int max_q) {
   const int heads = a.Hk * ((rows + p.R - 1) / p.R);
   p.share = kSms / heads < 1 ? 1 : kSms / heads;
   const int64_t tiles = most_tiles((int64_t)a.table_ld << a.lps, a.window, row_span(p.R, a.G));
-  // shorter sequences have splits of four tiles or more each, `share` of them or one for every eight tiles
-  int64_t most = (tiles + 3) / 4;
-  const int64_t by_share = p.share > (tiles + 7) / 8 ? p.share : (tiles + 7) / 8;
+  // shorter sequences have `share` splits at most or one for every kMost tiles, of kLeast or more each
+  int64_t most = (tiles + kLeast - 1) / kLeast;
+  const int64_t by_share = p.share > (tiles + kMost - 1) / kMost ? p.share : (tiles + kMost - 1) / kMost;
   if (by_share < most) most = by_share;
   p.ns_cap = (int)(most < 1 ? 1 : most < 128 ? most : 128);
   const size_t recs = (size_t)a.n_seqs * max_q * a.Hk * a.G * p.ns_cap;
