@@ -357,34 +357,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* pre = reinterpret_cast<int64_t*>(smem);       // until the first tile is planned
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < KS; ++i) {
-      mbar_init(smem_u32(&ctl->kfull[i]), 1 + 2 * kScaleLanes);
-      mbar_init(smem_u32(&ctl->kempty[i]), 1);
-    }
-    for (int i = 0; i < VS; ++i) mbar_init(smem_u32(&ctl->vempty[i]), 1);   // epilogue
+  // (by lanes: one thread for all of them took 4 us)
+  if (warp == 0) {
+    auto init = [&](uint64_t* bars, int n, uint32_t count) {
+      if (lane < n) mbar_init(smem_u32(bars + lane), count);
+    };
+    init(ctl->kfull, KS, 1 + 2 * kScaleLanes);
+    init(ctl->kempty, KS, 1);
+    init(ctl->vempty, VS, 1);                            // epilogue
     // V by steps, as many of them as there are stages at most
-    for (int i = 0; i < 8; ++i)
-      mbar_init(smem_u32(&ctl->vfull[i]), C::KT + (i == 0 ? a.withhold : 0));
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(smem_u32(&ctl->tfull[i]), 1);
-      mbar_init(smem_u32(&ctl->tempty[i]), 2);          // K, V
-    }
-    for (int i = 0; i < C::SB; ++i) {
-      mbar_init(smem_u32(&ctl->sfull[i]), 2);           // the product, and its issuer, who has seen the scales
-      mbar_init(smem_u32(&ctl->sempty[i]), 4);          // softmax
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ctl->qfull[i]), 2);
-      mbar_init(smem_u32(&ctl->qempty[i]), 8);          // softmax
-      mbar_init(smem_u32(&ctl->pfull[i]), 4);
-      mbar_init(smem_u32(&ctl->ofull[i]), 1);
-      mbar_init(smem_u32(&ctl->oempty[i]), 4);
-      mbar_init(smem_u32(&ctl->meet[i]), 4);
-    }
-    mbar_init(smem_u32(&ctl->done), 2);
-    ring_init(ctl->ring, kReaders);
-    ctl->abort = ctl->any_bad = 0;
+    init(ctl->vfull, 8, C::KT + (lane == 0 ? a.withhold : 0));
+    init(ctl->tfull, kSlots, 1);
+    init(ctl->tempty, kSlots, 2);                        // K, V
+    init(ctl->sfull, C::SB, 2);                          // the product, and its issuer, who has seen the scales
+    init(ctl->sempty, C::SB, 4);                         // softmax
+    init(ctl->qfull, 2, 2);
+    init(ctl->qempty, 2, 8);                             // softmax
+    init(ctl->pfull, 2, 4);
+    init(ctl->ofull, 2, 1);
+    init(ctl->oempty, 2, 4);
+    init(ctl->meet, 2, 4);
+    init(&ctl->done, 1, 2);
+    init(ctl->ring.full, kUnits, 1);
+    init(ctl->ring.empty, kUnits, kReaders);
+    if (lane == 0) ctl->abort = ctl->any_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
