@@ -3,18 +3,21 @@
 // For a row of logits x (those that are finite), with m = max x, l = sum exp(x_i - m) and
 // t = sum exp(x_i - m) (x_i - m):
 //   log p_i = x_i - m - log l,   entropy = -sum p_i log p_i = log l - t / l.
-// One pass: a thread keeps its own (m, l, t) and rescales them when its maximum grows.
+// A thread's values lie in registers: their maximum first, then the sums; a longer row's threads take
+// several blocks of them and rescale (m, l, t) when the maximum grows.
 //
-// The `top` largest: every thread's maximum is one of the row's values, so the top-th largest of the
-// maxima bounds the row's top-th largest value from below.  What reaches the bound (a few more than
-// `top`) is listed and put in order by counting.  Values and places make one 64-bit key, so that
-// equal values go by their place and no two keys are equal.  Where too many reach the bound (long runs
-// of equal values) the exact top-th key is found bit by bit.
+// The `top` largest: the maximum of each of 64 groups of threads is one of the row's values, so the
+// top-th largest of the maxima bounds the row's top-th largest value from below.  What reaches the bound
+// (a few more than `top`) is listed and put in order by counting.  Values and places make one 64-bit key,
+// so that equal values go by their place and no two keys are equal.  Where too many reach the bound (long
+// runs of equal values) the exact top-th key is found bit by bit.
 //
-// Bound by reading the logits once: a row is cut into slices, one to a CTA of a cluster, of 8192
-// values, or of an eighth of the row where that is more; a slice of 8192 stays in registers for its
-// second look.
+// Bound by reading the logits once; an exponential a value costs nearly as much.  A row that a CTA's
+// registers hold (512 threads of eight 16-byte vectors; 128 threads of four for short rows) is one CTA's;
+// longer rows are cut into slices, one to a CTA of a cluster of up to eight.
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "pp_paged.cuh"
 
@@ -27,17 +30,16 @@ using paged::Num;
 using paged::exp2_approx;
 using paged::kLog2e;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBlock = 8192;          // values that a CTA's registers hold
+constexpr int kGroups = 64;           // of threads, for the bound
 constexpr int kMost = 64;             // alternatives at most
+static_assert(kMost <= kGroups, "the bound is one of the groups' maxima");
 constexpr int kList = 1024;           // keys that may reach the bound before it is made exact
 constexpr int kCluster = 8;
 constexpr float kFar = -1e4f;         // a distance below the maximum that weighs nothing
 
 struct Call {
   const void* x;
-  int64_t ld, inner_ld, token_ld;
+  int64_t ld, inner_ld, token_ld, rows;
   int inner, n, top, slice;
   const int32_t* tokens;
   float *logprob, *entropy;
@@ -57,29 +59,26 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   return Stat{m, a.l * fa + b.l * fb, fa * fmaf(a.l, da, a.t) + fb * fmaf(b.l, db, b.t)};
 }
 
-// N more values
-template <int N>
-__device__ __forceinline__ void take(const float (&y)[N], Stat& s, bool& bad) {
-  float v[N], top = s.m;
+// Of all lanes, the same bits in each of them; `most`: the maximum of groups of kGroup lanes
+template <int kGroup, bool kEntropy>
+__device__ __forceinline__ Stat warp_join(Stat s, float& most) {
+  float m = s.m;
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    bad |= !(y[e] < INFINITY);
-    v[e] = fabsf(y[e]) < INFINITY ? y[e] : -INFINITY;
-    top = fmaxf(top, v[e]);
+  for (int o = 1; o < 32; o <<= 1) {
+    if (o == kGroup) most = m;
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  if (top > s.m) {
-    const float d = fmaxf(s.m - top, kFar), f = exp2_approx(d * kLog2e);
-    s.t = f * fmaf(s.l, d, s.t);
-    s.l *= f;
-    s.m = top;
-  }
+  if (kGroup == 32) most = m;
+  const float d = fmaxf(s.m - m, kFar), f = exp2_approx(d * kLog2e);
+  s.t = f * fmaf(s.l, d, s.t);
+  s.l *= f;
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const float d = fmaxf(v[e] - s.m, kFar);        // (a NaN, minus infinity less itself, goes too)
-    const float p = exp2_approx(d * kLog2e);
-    s.l += p;
-    s.t = fmaf(p, d, s.t);
+  for (int o = 1; o < 32; o <<= 1) {
+    s.l += __shfl_xor_sync(0xffffffffu, s.l, o);
+    if (kEntropy) s.t += __shfl_xor_sync(0xffffffffu, s.t, o);
   }
+  s.m = m;
+  return s;
 }
 
 // Order of values as unsigned integers (0: below all); -0 counts as 0.
@@ -102,23 +101,64 @@ __device__ __forceinline__ float load_value(const T* p) {
   else
     return Num<T>::to_float(*reinterpret_cast<const uint16_t*>(p));
 }
-// Value e of a 16-byte vector
+// Two values of a word (16 bits each), or the word itself
 template <typename T>
-__device__ __forceinline__ float value_at(const uint4& w, int e) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ float value_at(uint32_t w, int e) {
   if constexpr (sizeof(T) == 4)
-    return __uint_as_float(u[e]);
+    return __uint_as_float(w);
   else
-    return Num<T>::to_float(e & 1 ? u[e >> 1] >> 16 : u[e >> 1] & 0xffffu);
+    return Num<T>::to_float(e ? w >> 16 : w & 0xffffu);
+}
+// The larger of two words' values, half by half (a NaN loses)
+template <typename T>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 4) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  } else {
+    uint32_t r;
+    if constexpr (Num<T>::kShift == 0.f)
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+      asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+}
+// z += 0 w: stays zero while every value is finite
+template <typename T>
+__device__ __forceinline__ void probe(uint32_t& z, uint32_t w) {
+  if constexpr (sizeof(T) == 4)
+    z = __float_as_uint(fmaf(__uint_as_float(w), 0.f, __uint_as_float(z)));
+  else
+    Num<T>::probe(z, w);
+}
+// The word with -infinity for each value that is not finite; `bad` if one is a NaN or +infinity
+template <typename T>
+__device__ __forceinline__ uint32_t finite_word(uint32_t w, bool& bad) {
+  if constexpr (sizeof(T) == 4) {
+    const float v = __uint_as_float(w);
+    bad |= !(v < INFINITY);
+    return fabsf(v) < INFINITY ? w : 0xff800000u;
+  } else {
+    constexpr uint32_t none = 0x8000u | Num<T>::kExp;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t h = w >> (16 * e) & 0xffffu;
+      if ((h & Num<T>::kExp) != Num<T>::kExp) continue;
+      bad |= h != none;
+      w = (w & ~(0xffffu << (16 * e))) | none << (16 * e);
+    }
+    return w;
+  }
 }
 
-// A thread's part of its CTA's slice [s0, s1) of a row: whole vectors in [p0, ..), and up to V - 1 values
-// on either side of them, one to a thread.
-template <typename T>
+// A thread's part of its CTA's slice [s0, s1) of a row: whole vectors from p0 on, and up to V - 1 values on
+// either side of them, one to a thread.
+template <typename T, int kThreads, int kVectors>
 struct Slice {
-  static constexpr int V = 16 / sizeof(T);               // values of a vector
-  static constexpr int U = kBlock / (kThreads * V);      // vectors of a thread, held in registers
-  uint4 w[U];
+  static constexpr int N = 4 / sizeof(T);                // values of a word
+  static constexpr int V = 4 * N;                        // values of a vector
+  static constexpr int kWords = kVectors * 4;
+  uint32_t w[kWords];
   const uint4* body;
   int p0, nv;                                            // first place, vectors
   int tid, side;                                         // place of this thread's single value, or -1
@@ -132,32 +172,90 @@ struct Slice {
     side = tid < p0 - s0 ? s0 + tid : tid >= V && tid - V < s1 - p1 ? p1 + tid - V : -1;
     body = reinterpret_cast<const uint4*>(x + p0);
   }
+  __device__ __forceinline__ bool whole() const { return nv <= kVectors * kThreads; }
+  // A block of vectors; -infinity where there are none
   __device__ __forceinline__ void load(int v0) {
+    constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : (0x8000u | Num16::kExp) * 0x10001u;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kVectors; ++u) {
       const int v = v0 + u * kThreads + tid;
-      if (v < nv) w[u] = body[v];
+      const uint4 x = v < nv ? body[v] : make_uint4(none, none, none, none);
+      w[4 * u] = x.x;
+      w[4 * u + 1] = x.y;
+      w[4 * u + 2] = x.z;
+      w[4 * u + 3] = x.w;
     }
   }
-  // f(key) for each finite value: its order above the complement of its place
+  // The block's values that are not finite become -infinity.
+  __device__ __forceinline__ void clean(int v0, bool& bad) {
+    uint32_t z = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      if (v0 + i / 4 * kThreads + tid < nv) probe<T>(z, w[i]);
+    if ((z & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) == 0) return;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = finite_word<T>(w[i], bad);
+  }
+  __device__ __forceinline__ float largest() const {
+    uint32_t m = w[0];
+#pragma unroll
+    for (int i = 1; i < kWords; ++i) m = max_word<T>(m, w[i]);
+    return N == 1 ? value_at<T>(m, 0) : fmaxf(value_at<T>(m, 0), value_at<T>(m, 1));
+  }
+  // The block's share of (l, t) for the maximum m
+  template <bool kEntropy>
+  __device__ __forceinline__ void sums(Stat& s) const {
+    const float ref = s.m == -INFINITY ? 0.f : -s.m;
+    const uint64_t ref2 = paged::f32x2(ref, ref), log2e = paged::f32x2(kLog2e, kLog2e);
+    uint64_t l2 = 0, t2 = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; i += 2 / N) {
+      uint64_t d = paged::add2(paged::f32x2(value_at<T>(w[i], 0), value_at<T>(w[N == 1 ? i + 1 : i], 1)), ref2);
+      if constexpr (kEntropy)                            // (0 times minus infinity would be a NaN)
+        d = paged::f32x2(fmaxf(paged::lo_of(d), kFar), fmaxf(paged::hi_of(d), kFar));
+      const uint64_t e = paged::mul2(d, log2e);
+      const uint64_t p = paged::f32x2(exp2_approx(paged::lo_of(e)), exp2_approx(paged::hi_of(e)));
+      l2 = paged::add2(l2, p);
+      if constexpr (kEntropy) t2 = paged::fma2(p, d, t2);
+    }
+    s.l += paged::lo_of(l2) + paged::hi_of(l2);
+    if constexpr (kEntropy) s.t += paged::lo_of(t2) + paged::hi_of(t2);
+  }
+  // f(key) for each finite value from `least` on: its order above the complement of its place
   template <typename F>
-  __device__ __forceinline__ void each(F f) {
-    if (side >= 0 && fabsf(single) < INFINITY) f(key_of(single, side));
+  __device__ __forceinline__ void each(float least, F f) {
+    if (side >= 0 && fabsf(single) < INFINITY && single >= least) f(key_of(single, side));
 #pragma unroll 1
-    for (int v0 = 0; v0 < nv; v0 += U * kThreads) {
-      if (nv > U * kThreads) load(v0);
+    for (int v0 = 0; v0 < nv; v0 += kVectors * kThreads) {
+      if (!whole()) load(v0);
+      uint32_t hits = 0;                                 // vectors that reach it: hardly any
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = v0 + u * kThreads + tid;
-        if (v >= nv) break;
+      for (int u = 0; u < kVectors; ++u) {
+        const uint32_t m =
+            max_word<T>(max_word<T>(w[4 * u], w[4 * u + 1]), max_word<T>(w[4 * u + 2], w[4 * u + 3]));
+        const float most = N == 1 ? value_at<T>(m, 0) : fmaxf(value_at<T>(m, 0), value_at<T>(m, 1));
+        if (most >= least && most > -INFINITY) hits |= 1u << u;
+      }
+#pragma unroll 1
+      for (; hits; hits &= hits - 1) {
+        const int u = __ffs(hits) - 1, place = p0 + (v0 + u * kThreads + tid) * V;
+        uint32_t own[4];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float y = value_at<T>(w[u], e);
-          if (fabsf(y) < INFINITY) f(key_of(y, p0 + v * V + e));
+        for (int i = 0; i < kVectors; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (i == 0 || u == i) own[j] = w[4 * i + j];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float v = value_at<T>(own[i / N], i % N);
+          if (fabsf(v) < INFINITY && v >= least) f(key_of(v, place + i));
         }
       }
     }
   }
+
+ private:
+  using Num16 = Num<typename std::conditional<sizeof(T) == 4, __half, T>::type>;
 };
 struct ListFrom {                     // keys from `least` on into a list
   uint64_t least;
@@ -175,108 +273,122 @@ struct CountFrom {
   __device__ __forceinline__ void operator()(uint64_t key) const { *count += key >= least; }
 };
 
+template <int kThreads>
 struct Shared {
-  Stat stat[kWarps];                  // of the warps, then [0]: of the CTA
+  Stat stat[kThreads / 32];           // of the warps, then [0]: of the CTA
+  __align__(16) float most[kGroups];  // the groups' maxima
+  float bound;
+  float chosen;                       // rank 0: the given token's value
+  int token;
+  int count, found;
   uint64_t list[kList];
   uint64_t best[kMost];               // this CTA's largest, in order; 0: none
   uint64_t all[kCluster * kMost];     // rank 0: everyone's
-  int count, found;
 };
 
-// Ranks the `c` keys of `list` and writes the first `top` in order (0: none).  By the whole CTA.
+// The `top` largest of the `c` keys of `list`, in order (0: none).  By the whole CTA.
+template <int kThreads>
 __device__ __forceinline__ void put_in_order(const uint64_t* list, int c, uint64_t* out, int top) {
-  for (int i = threadIdx.x; i < top; i += kThreads) out[i] = 0;
-  __syncthreads();
   for (int i = threadIdx.x; i < c; i += kThreads) {
     const uint64_t key = list[i];
     int above = 0;
-    for (int k = 0; k < c; ++k) above += list[k] > key;
-    if (key != 0 && above < top) out[above] = key;
+#pragma unroll 4
+    for (int k = 0; k < c; ++k) {
+      const uint64_t other = list[k];
+      above += other > key || (other == key && k < i);  // (only keys of 0 are equal)
+    }
+    if (above < top) out[above] = key;
   }
+  for (int i = c + threadIdx.x; i < top; i += kThreads) out[i] = 0;
   __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int kThreads, int kVectors, bool kEntropy>
+__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8)
     k_logprobs(const __grid_constant__ Call a) {
-  constexpr int V = Slice<T>::V, U = Slice<T>::U;
-  __shared__ Shared sh;
+  using S = Slice<T, kThreads, kVectors>;
+  __shared__ Shared<kThreads> sh;
   const cg::cluster_group cluster = cg::this_cluster();
   const int size = cluster.num_blocks(), rank = cluster.block_rank();
-  const int64_t r = blockIdx.x / size;              // the row
-  const int64_t group = r / a.inner, in = r - group * a.inner;
-  const T* x = reinterpret_cast<const T*>(a.x) + group * a.ld + in * a.inner_ld;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int s0 = min(rank * a.slice, a.n), s1 = min(s0 + a.slice, a.n);
+  const int64_t r = blockIdx.x / size, group = r / a.inner, in = r - group * a.inner;    // the row
+  const T* x = reinterpret_cast<const T*>(a.x) + group * a.ld + in * a.inner_ld;
   pdl_wait_and_trigger();
   pdl_trigger();
-  Slice<T> in_slice(x, min(rank * a.slice, a.n), min(rank * a.slice + a.slice, a.n), tid);
-  uint4 (&w)[U] = in_slice.w;
-  const int nv = in_slice.nv, side = in_slice.side;
-  in_slice.load(0);
-  const float single = in_slice.single = side >= 0 ? load_value(x + side) : -INFINITY;
-
-  Stat s{-INFINITY, 0.f, 0.f};
-  bool bad = false;
-  if (side >= 0) {
-    const float y[1] = {single};
-    take<1>(y, s, bad);
-  }
-  for (int v0 = 0; v0 < nv; v0 += U * kThreads) {
-    if (v0 > 0) in_slice.load(v0);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (v0 + u * kThreads + tid >= nv) break;
-      float y[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = value_at<T>(w[u], e);
-      take<V>(y, s, bad);
-    }
-  }
-  const float mine = s.m;                           // this thread's largest value
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Stat y{__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.l, o),
-                 __shfl_xor_sync(0xffffffffu, s.t, o)};
-    // the lower lane's side first, in both lanes
-    s = (lane & o) ? join(y, s) : join(s, y);
-  }
-  if (lane == 0) sh.stat[warp] = s;
+  S part(x, s0, s1, tid);
+  part.load(0);
+  part.single = part.side >= 0 ? load_value(x + part.side) : -INFINITY;
   if (tid == 0) sh.count = 0;
-  __syncthreads();
-  if (tid == 0) {
-    Stat y = sh.stat[0];
-    for (int i = 1; i < kWarps; ++i) y = join(y, sh.stat[i]);
-    sh.stat[0] = y;
+
+  bool bad = !(part.single < INFINITY);
+  if (!(fabsf(part.single) < INFINITY)) part.single = -INFINITY;
+  Stat s{part.single, part.single == -INFINITY ? 0.f : 1.f, 0.f};
+#pragma unroll 1
+  for (int v0 = 0; v0 < part.nv; v0 += kVectors * kThreads) {
+    if (v0 > 0) part.load(v0);
+    part.clean(v0, bad);
+    const float m = part.largest();
+    if (m > s.m) {
+      const float d = fmaxf(s.m - m, kFar), f = exp2_approx(d * kLog2e);
+      s.t = f * fmaf(s.l, d, s.t);
+      s.l *= f;
+      s.m = m;
+    }
+    part.template sums<kEntropy>(s);
   }
   if (bad && a.status) atomicOr(a.status, PP_S_NAN);
-
+  float most;                                       // of this thread's group of kThreads / kGroups lanes
+  s = warp_join<kThreads / kGroups, kEntropy>(s, most);
+  if (lane == 0) sh.stat[warp] = s;
+  if (a.top > 0 && tid % (kThreads / kGroups) == 0) sh.most[tid / (kThreads / kGroups)] = most;
+  __syncthreads();
+  if (warp == kThreads / 32 - 1) {                  // (the last warp: the first ones rank the maxima)
+    float unused;
+    const Stat y = warp_join<32, kEntropy>(
+        lane < kThreads / 32 ? sh.stat[lane] : Stat{-INFINITY, 0.f, 0.f}, unused);
+    __syncwarp();
+    if (lane == 0) sh.stat[0] = y;
+  }
+  if (tid == kThreads - 64 && rank == 0 && a.logprob) {
+    const int32_t token = a.tokens[group * a.token_ld + in];
+    sh.token = token;
+    if (token >= 0 && token < a.n) sh.chosen = load_value(x + token);
+  }
   if (a.top > 0) {
-    const uint32_t most = mine == -INFINITY ? 0u : order(mine);
-    // the top-th largest of the threads' maxima, by bits from the highest; 16 of them are enough for
-    // a bound
-    uint32_t bound = 0;
-#pragma unroll 1
-    for (int b = 31; b >= 16; --b) {
-      const uint32_t at = bound | 1u << b;
-      if (__syncthreads_count(most >= at) >= a.top) bound = at;
+    if (tid < kGroups) {
+      const float mine = sh.most[tid];
+      int above = 0;
+#pragma unroll 4
+      for (int i = 0; i < kGroups; i += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(&sh.most[i]);
+        above += y.x > mine || (y.x == mine && i < tid);
+        above += y.y > mine || (y.y == mine && i + 1 < tid);
+        above += y.z > mine || (y.z == mine && i + 2 < tid);
+        above += y.w > mine || (y.w == mine && i + 3 < tid);
+      }
+      if (above == a.top - 1) sh.bound = mine;
     }
-    if (most >= bound) in_slice.each(ListFrom{(uint64_t)bound << 32, &sh.count, sh.list});
+    __syncthreads();
+    const float bound = sh.bound;
+    part.each(bound, ListFrom{0, &sh.count, sh.list});
     __syncthreads();
     int c = sh.count;
     if (c > kList) {
       // the top-th largest key itself, bit by bit: at least `top` keys reach the bound
+      const uint64_t known = (uint64_t)order(bound) << 32;
       uint64_t least = 0;
 #pragma unroll 1
       for (int b = 63; b >= 0; --b) {
         const uint64_t at = least | (uint64_t)1 << b;
-        if (at <= (uint64_t)bound << 32) {
+        if (at <= known) {
           least = at;
           continue;
         }
         if (tid == 0) sh.found = 0;
         __syncthreads();
         int k = 0;
-        in_slice.each(CountFrom{at, &k});
+        part.each(bound, CountFrom{at, &k});
         if (k) atomicAdd(&sh.found, k);
         __syncthreads();
         if (sh.found >= a.top) least = at;
@@ -284,11 +396,11 @@ __global__ void __launch_bounds__(kThreads)
       }
       if (tid == 0) sh.count = 0;
       __syncthreads();
-      in_slice.each(ListFrom{least, &sh.count, sh.list});
+      part.each(bound, ListFrom{least, &sh.count, sh.list});
       __syncthreads();
       c = sh.count;
     }
-    put_in_order(sh.list, c, sh.best, a.top);
+    put_in_order<kThreads>(sh.list, c, sh.best, a.top);
   } else {
     __syncthreads();
   }
@@ -305,24 +417,23 @@ __global__ void __launch_bounds__(kThreads)
     }
     cluster.sync();                                 // the others' memory has been read
     if (rank > 0) return;
-    if (a.top > 0) put_in_order(sh.all, size * a.top, sh.best, a.top);
+    if (a.top > 0) put_in_order<kThreads>(sh.all, size * a.top, sh.best, a.top);
   }
-  __syncthreads();
   const Stat y = sh.stat[0];
   const float log_l = logf(y.l);
   if (tid == 0) {
     if (a.logprob) {
-      const int32_t token = a.tokens[group * a.token_ld + in];
+      const int32_t token = sh.token;
       float lp = 0.f;
       if (token >= a.n) {
         if (a.status) atomicOr(a.status, PP_S_INDEX);
       } else if (token >= 0) {
-        const float v = load_value(x + token);
+        const float v = sh.chosen;
         lp = fabsf(v) < INFINITY ? (v - y.m) - log_l : -INFINITY;
       }
       a.logprob[r] = lp;
     }
-    if (a.entropy) a.entropy[r] = y.l > 0.f ? fmaxf(log_l - y.t / y.l, 0.f) : 0.f;
+    if (kEntropy) a.entropy[r] = y.l > 0.f ? fmaxf(log_l - y.t / y.l, 0.f) : 0.f;
   }
   for (int i = tid; i < a.top; i += kThreads) {
     const uint64_t key = sh.best[i];
@@ -333,9 +444,19 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+template <typename T, int kThreads, int kVectors>
+cudaError_t run(Call a, cudaStream_t s) {
+  constexpr int kBlock = kThreads * kVectors * 16 / (int)sizeof(T);
+  int size = 1;
+  while (size < kCluster && (int64_t)size * kBlock < a.n) size *= 2;
+  a.slice = ((a.n + size - 1) / size + 7) / 8 * 8;  // (whole vectors, where the row is aligned)
+  auto kern = a.entropy ? k_logprobs<T, kThreads, kVectors, true> : k_logprobs<T, kThreads, kVectors, false>;
+  return paged::launch_cluster(size, kern, dim3((unsigned)(a.rows * size)), kThreads, 0, s, a);
+}
+// Short rows in small CTAs, more of them side by side.
 template <typename T>
-cudaError_t run(const Call& a, int64_t rows, int size, cudaStream_t s) {
-  return paged::launch_cluster(size, k_logprobs<T>, dim3((unsigned)(rows * size)), kThreads, 0, s, a);
+cudaError_t pick(const Call& a, cudaStream_t s) {
+  return a.n <= 128 * 4 * 16 / (int)sizeof(T) ? run<T, 128, 4>(a, s) : run<T, 512, 8>(a, s);
 }
 
 }  // namespace
@@ -361,15 +482,11 @@ extern "C" int pp_token_logprobs(const void* logits, int type, int64_t ld, int r
       off(top_tokens, 4) || off(top_logprobs, 4) || (logprob && !tokens))
     return PP_EINVAL;
   // (without a place for them no alternative is looked for)
-  Call a{logits, ld, inner_ld, token_ld, inner, n, top_tokens || top_logprobs ? top : 0, 0, tokens,
-         logprob, entropy, top_tokens, top_logprobs, status};
-  int size = 1;
-  while (size < kCluster && (int64_t)size * kBlock < n) size *= 2;
-  a.slice = ((n + size - 1) / size + 7) / 8 * 8;    // (whole vectors, where the row is aligned)
-  const int64_t all = (int64_t)rows * inner;
+  Call a{logits, ld, inner_ld, token_ld, (int64_t)rows * inner, inner, n,
+         top_tokens || top_logprobs ? top : 0, 0, tokens, logprob, entropy, top_tokens, top_logprobs, status};
   const cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t err = type == PP_F32    ? run<float>(a, all, size, s)
-                          : type == PP_BF16 ? run<__nv_bfloat16>(a, all, size, s)
-                                            : run<__half>(a, all, size, s);
+  const cudaError_t err = type == PP_F32    ? pick<float>(a, s)
+                          : type == PP_BF16 ? pick<__nv_bfloat16>(a, s)
+                                            : pick<__half>(a, s);
   return err == cudaSuccess ? PP_OK : PP_E_CUDA;
 }
