@@ -139,14 +139,11 @@ __device__ __forceinline__ uint32_t finite_word(uint32_t w, bool& bad) {
     bad |= !(v < INFINITY);
     return fabsf(v) < INFINITY ? w : 0xff800000u;
   } else {
-    constexpr uint32_t none = 0x8000u | Num<T>::kExp;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t h = w >> (16 * e) & 0xffffu;
-      if ((h & Num<T>::kExp) != Num<T>::kExp) continue;
-      bad |= h != none;
-      w = (w & ~(0xffffu << (16 * e))) | none << (16 * e);
-    }
+    constexpr uint32_t exp = Num<T>::kExp, last = exp & (~exp + 1), none = (0x8000u | exp) * 0x10001u;
+    // (one more on an exponent of ones carries into the sign's place)
+    const uint32_t ones = ((w & exp * 0x10001u) + last * 0x10001u) >> 15 & 0x10001u, all = ones * 0xffffu;
+    bad |= ((w ^ none) & all) != 0;
+    w = (w & ~all) | (none & all);
     return w;
   }
 }
@@ -223,7 +220,7 @@ struct Slice {
   }
   // f(key) for each finite value from `least` on: its order above the complement of its place
   template <typename F>
-  __device__ __forceinline__ void each(float least, F f) {
+  __device__ __forceinline__ void each(float least, F& f) {
     if (side >= 0 && fabsf(single) < INFINITY && single >= least) f(key_of(single, side));
 #pragma unroll 1
     for (int v0 = 0; v0 < nv; v0 += kVectors * kThreads) {
@@ -257,20 +254,20 @@ struct Slice {
  private:
   using Num16 = Num<typename std::conditional<sizeof(T) == 4, __half, T>::type>;
 };
-struct ListFrom {                     // keys from `least` on into a list
+struct Keys {                         // from `least` on: counted, and listed if there is a list
   uint64_t least;
-  int* count;
   uint64_t* list;
-  __device__ __forceinline__ void operator()(uint64_t key) const {
+  int* count;
+  int mine;
+  __device__ __forceinline__ void operator()(uint64_t key) {
     if (key < least) return;
+    if (!list) {
+      ++mine;
+      return;
+    }
     const int at = atomicAdd(count, 1);
     if (at < kList) list[at] = key;
   }
-};
-struct CountFrom {
-  uint64_t least;
-  int* count;
-  __device__ __forceinline__ void operator()(uint64_t key) const { *count += key >= least; }
 };
 
 template <int kThreads>
@@ -280,7 +277,7 @@ struct Shared {
   float bound;
   float chosen;                       // rank 0: the given token's value
   int token;
-  int count, found;
+  int count;
   uint64_t list[kList];
   uint64_t best[kMost];               // this CTA's largest, in order; 0: none
   uint64_t all[kCluster * kMost];     // rank 0: everyone's
@@ -289,6 +286,7 @@ struct Shared {
 // The `top` largest of the `c` keys of `list`, in order (0: none).  By the whole CTA.
 template <int kThreads>
 __device__ __forceinline__ void put_in_order(const uint64_t* list, int c, uint64_t* out, int top) {
+#pragma unroll 1
   for (int i = threadIdx.x; i < c; i += kThreads) {
     const uint64_t key = list[i];
     int above = 0;
@@ -299,6 +297,7 @@ __device__ __forceinline__ void put_in_order(const uint64_t* list, int c, uint64
     }
     if (above < top) out[above] = key;
   }
+#pragma unroll 1
   for (int i = c + threadIdx.x; i < top; i += kThreads) out[i] = 0;
   __syncthreads();
 }
@@ -312,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8)
   const int size = cluster.num_blocks(), rank = cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s0 = min(rank * a.slice, a.n), s1 = min(s0 + a.slice, a.n);
-  const int64_t r = blockIdx.x / size, group = r / a.inner, in = r - group * a.inner;    // the row
+  const uint32_t row = blockIdx.x / (uint32_t)size, group_of = row / (uint32_t)a.inner;
+  const int64_t r = row, group = group_of, in = row - group_of * (uint32_t)a.inner;
   const T* x = reinterpret_cast<const T*>(a.x) + group * a.ld + in * a.inner_ld;
   pdl_wait_and_trigger();
   pdl_trigger();
@@ -371,34 +371,31 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8)
     }
     __syncthreads();
     const float bound = sh.bound;
-    part.each(bound, ListFrom{0, &sh.count, sh.list});
-    __syncthreads();
-    int c = sh.count;
-    if (c > kList) {
-      // the top-th largest key itself, bit by bit: at least `top` keys reach the bound
-      const uint64_t known = (uint64_t)order(bound) << 32;
-      uint64_t least = 0;
+    // Listed at once; or, where too many reach the bound, counted from keys that are made bit by bit, up
+    // to the top-th largest, and listed from there.
+    const uint64_t known = (uint64_t)order(bound) << 32;
+    uint64_t least = 0;
+    int c, bit = 64;
+    Keys keys{0, sh.list, &sh.count, 0};
 #pragma unroll 1
-      for (int b = 63; b >= 0; --b) {
-        const uint64_t at = least | (uint64_t)1 << b;
-        if (at <= known) {
-          least = at;
-          continue;
-        }
-        if (tid == 0) sh.found = 0;
-        __syncthreads();
-        int k = 0;
-        part.each(bound, CountFrom{at, &k});
-        if (k) atomicAdd(&sh.found, k);
-        __syncthreads();
-        if (sh.found >= a.top) least = at;
-        __syncthreads();
-      }
-      if (tid == 0) sh.count = 0;
-      __syncthreads();
-      part.each(bound, ListFrom{least, &sh.count, sh.list});
+    for (;;) {
+      part.each(bound, keys);
+      if (keys.mine) atomicAdd(&sh.count, keys.mine);
       __syncthreads();
       c = sh.count;
+      if (keys.list && c <= kList) break;
+      if (!keys.list && c >= a.top) least = keys.least;
+      __syncthreads();
+      if (tid == 0) sh.count = 0;
+      uint64_t at = least;
+#pragma unroll 1
+      while (--bit >= 0) {
+        at = least | (uint64_t)1 << bit;
+        if (at > known) break;                      // (at least `top` keys reach the bound)
+        least = at;
+      }
+      keys = Keys{at, bit < 0 ? sh.list : nullptr, &sh.count, 0};
+      __syncthreads();
     }
     put_in_order<kThreads>(sh.list, c, sh.best, a.top);
   } else {
@@ -409,9 +406,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8)
     if (rank == 0) {
       if (tid == 0) {
         Stat y = sh.stat[0];
+#pragma unroll 1
         for (int i = 1; i < size; ++i) y = join(y, cluster.map_shared_rank(&sh, i)->stat[0]);
         sh.stat[0] = y;
       }
+#pragma unroll 1
       for (int i = tid; i < size * a.top; i += kThreads)
         sh.all[i] = cluster.map_shared_rank(&sh, i / a.top)->best[i % a.top];
     }
@@ -435,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8)
     }
     if (kEntropy) a.entropy[r] = y.l > 0.f ? fmaxf(log_l - y.t / y.l, 0.f) : 0.f;
   }
+#pragma unroll 1
   for (int i = tid; i < a.top; i += kThreads) {
     const uint64_t key = sh.best[i];
     if (a.top_tokens) a.top_tokens[r * a.top + i] = key ? (int32_t)~(uint32_t)key : -1;
