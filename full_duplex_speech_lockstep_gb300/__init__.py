@@ -752,6 +752,13 @@ class _Pages:
         self.c = c
         self.ref, self.lib, self.sizes = ctypes.byref(c), lib(), {}
 
+    def _other(self, name, to):
+        """Refuse what is not a 16-bit cache on this cache's device."""
+        if not isinstance(to, PagedKV):
+            raise ValueError("%s: %s, expected a PagedKV" % (name, type(to).__name__))
+        if to.index != self.index:
+            raise ValueError("both caches must be on one device")
+
     @staticmethod
     def _ptr(t):
         return None if t is None else t.data_ptr()
@@ -829,8 +836,8 @@ class _Pages:
             out = torch.empty((T, H, self.dim), dtype=self.dtype, device=self.device)
         else:
             self._fits("out", out, self.dtype, (T, H, self.dim))
-        self._call(self.family + "_append", self.ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                   self.types[dtype], self._ptr(q_alpha), self._ptr(k_alpha), eps, rope_base,
+        self._call(self.family + "_append", self.ref, q.data_ptr(), qs, k.data_ptr(), ks,
+                   v.data_ptr(), vs, self.types[dtype], self._ptr(q_alpha), self._ptr(k_alpha), eps, rope_base,
                    self.dim if rot_dim is None else rot_dim, int(halves), self._ptr(positions),
                    cu.data_ptr(), kv_len.data_ptr(), T, H, out.data_ptr(), self.status.data_ptr())
         return out
@@ -853,8 +860,8 @@ class _Pages:
         nbytes = self._scratch_bytes(H, T, max_q, window)
         scratch = self.unused if nbytes <= 256 else \
             torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        self._call(self.family + "_attention", self.ref, q.data_ptr(), qs, cu.data_ptr(), kv_len.data_ptr(),
-                   T, max_q, H, self.dim ** -0.5 if scale is None else scale, window,
+        self._call(self.family + "_attention", self.ref, q.data_ptr(), qs, cu.data_ptr(),
+                   kv_len.data_ptr(), T, max_q, H, self.dim ** -0.5 if scale is None else scale, window,
                    out.data_ptr(), self._ptr(lse), self.status.data_ptr(), scratch.data_ptr(),
                    nbytes)
         return (out, lse) if with_lse else out
@@ -920,8 +927,7 @@ class PagedKV(_Pages):
         torch = self.torch
         if self.mass is None:
             raise ValueError("this cache keeps no mass")
-        if to.index != self.index:
-            raise ValueError("both caches must be on one device")
+        self._other("to", to)
         self._fits("kv_len", kv_len, torch.int32, (self.n,))
         to_len = torch.empty(self.n, dtype=torch.int32, device=self.device)
         kept = torch.empty((self.n, self.heads, max(budget, 0)), dtype=torch.int32,
@@ -974,7 +980,6 @@ class PagedKV8(_Pages):
     def read(self, kv_len, to):
         """What the first kv_len entries of each sequence hold, into the same entries of the
         PagedKV `to` (of this cache's ``dtype``; of any page size)."""
-        if to.index != self.index:
-            raise ValueError("both caches must be on one device")
+        self._other("to", to)
         self._fits("kv_len", kv_len, self.torch.int32, (self.n,))
         self._call("pp_packed_read", self.ref, kv_len.data_ptr(), to.ref, self.status.data_ptr())

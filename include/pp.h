@@ -654,7 +654,7 @@ int pp_paged_evict(const pp_paged_kv* kv, const int32_t* kv_len, int budget, int
  * two for all of them:
  *   a = max |y_d|;  e = the least whole number such that a 2^-e <= 448, at least -127;
  *   code_d = y_d 2^-e rounded to e4m3 (nearest, ties to even);  scale byte = e + 127;
- *   the entry reads as code_d 2^e, which bf16 holds exactly.
+ *   the entry reads as code_d 2^e, which bf16 holds exactly (multiples of 2^-133, below 2^-126).
  * With a = 0 the byte is 0.  An entry that holds a NaN or an infinity has codes 0 and the byte 255: it
  * reads as NaN in every dim.  (A caller's own e4m3 NaN codes, 0x7f and 0xff, read as NaN too, in their
  * dim or in the whole entry.)
@@ -685,7 +685,9 @@ int pp_packed_append(const pp_packed_kv* kv, const void* q, int64_t q_stride, co
                      void* stream);
 
 /* pp_paged_attention over 8-bit entries: the same arguments, masks and results, of what the entries read
- * as.  Scratch: pp_packed_attention_scratch_bytes(...) bytes.
+ * as (fp16: as pp_packed_read rounds them, in chunks of more than 64 rows).  Scratch:
+ * pp_packed_attention_scratch_bytes(...) bytes; by max_q, chunks of more than 64 rows to a key head take a
+ * 16-bit copy of all that the table has room for.
  * Errors: PP_EINVAL, PP_E_NOSPACE, PP_E_CUDA. */
 size_t pp_packed_attention_scratch_bytes(const pp_packed_kv* kv, int n_heads, int T, int max_q,
                                          int window);

@@ -188,3 +188,13 @@ def test_logprobs_of_host_tensors_is_refused():
     torch = pytest.importorskip("torch")
     with pytest.raises(ValueError):
         pp.token_logprobs(torch.zeros(3, 5))
+
+
+def test_caches_of_one_kind_do_not_pass_for_the_other():
+    wide_kv, packed = (c.__new__(c) for c in (pp.PagedKV, pp.PagedKV8))
+    wide_kv.index = packed.index = 0
+    wide_kv.mass, wide_kv.torch = object(), None
+    for call in (lambda: wide_kv.evict(None, 4, 2, packed), lambda: packed.read(None, packed),
+                 lambda: packed.read(None, None)):
+        with pytest.raises(ValueError, match="expected a PagedKV"):
+            call()
