@@ -11,9 +11,9 @@
 //   S[j][r]  = k_j . q_r                 M = 128 keys, N = parts x R rows, K = D
 //   w[j][r]  = 2^(s_jr - m_r + 8) 2^(ev_j - E_r),   s_jr = S c 2^(ek_j + eq_r)
 //   O[d][r]  = sum_j v_jd w_jr           M = D dims, N = 3 x R rows, K = 128 keys a tile
-// A step is 32 / R tiles, so that a thread has 32 scores whatever R is, and what a step costs beside
-// them (barriers, maxima, the epilogue) is the same.  (A tile at a time, 8 rows took as long as 32: 313 us
-// on the 64-session tick.)  m_r is the step's own maximum and E_r the largest ev that the row sees: a step
+// A step is four tiles of 2 or 4 rows, two of 8, one of more: a thread has 8 to 32 scores a step, and what a
+// step costs beside them (barriers, maxima, the epilogue) is paid for several tiles.  (A tile at a time, few
+// rows took as long as 32: 313 us on the 64-session tick; tiles of 8 rows for one: 261 us.)  m_r is the step's own maximum and E_r the largest ev that the row sees: a step
 // depends on nothing before it.  The epilogue adds the steps up in fp32, in order:
 // acc = acc 2^(M - M') + O 2^(m + E_r - M').
 //
@@ -22,10 +22,10 @@
 // lengths, the head counts and max_q only.  A unit that is not its rows' only one leaves (m, l, O) in
 // scratch and k_packed_join adds the splits up in split order.
 //
-//   warp 0       the units and their tiles' pages, up to 16 tiles ahead.  (With lookups in the warps that
+//   warp 0       the units and their tiles' pages, up to 32 tiles ahead.  (With lookups in the warps that
 //                load, a tile took 1150 clocks and a unit's start 3600.)
 //   warp 1       one thread issues the MMAs of S
-//   warps 2, 16  K tiles with both scales; V tiles
+//   warps 2, 16  K tiles with both scales, two at a time; V tiles
 //   warp 3       one thread issues the MMAs of O.  (One thread for both took 1900 clocks a tile.)
 //   warps 4-7, 8-11   softmax of every second step
 //   warps 12-15  epilogue: a thread owns one dim
