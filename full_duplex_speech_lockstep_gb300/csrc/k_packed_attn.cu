@@ -15,7 +15,7 @@
 // step costs beside them (barriers, maxima, the epilogue) is paid for several tiles.  (A tile at a time, few
 // rows took as long as 32: 313 us on the 64-session tick; tiles of 8 rows for one: 261 us.)  m_r is the step's own maximum and E_r the largest ev that the row sees: a step
 // depends on nothing before it.  The epilogue adds the steps up in fp32, in order:
-// acc = acc 2^(M - M') + O 2^(m + E_r - M').
+// acc = acc 2^(M - M') + O 2^(m - 8 + E_r - M').
 //
 // A work unit is (sequence, key head, split of its keys, row tile of up to R rows).  Each CTA takes a run
 // of consecutive units with about as many tiles as the others'; a sequence's splits depend on its own
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int p = C::QP - 2; p >= 0; --p)
                 y = fma2(y, f32x2(0.0625f, 0.0625f),
                          f32x2(after_wait(s[p * W + e]), after_wait(s[p * W + e + 1])));
-              y = mul2(mul2(y, kf2), f32x2(f[e], f[e + 1]));
+              y = mul2(y, mul2(kf2, f32x2(f[e], f[e + 1])));
               v[e] = lo_of(y);
               v[e + 1] = hi_of(y);
             }
@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (top != top) top = -INFINITY;               // (a row of NaN: its weights are NaN all the same)
           ctl->ref[g][wq][lane] = top == -INFINITY ? 0.f : kTop - top;
-          ctl->fit[g][wq][lane] = __uint_as_float((254u - E) << 23);
+          ctl->fit[g][wq][lane] = __uint_as_float(E == 254u ? 0x00400000u : (254u - E) << 23);
         }
         // the last step's weights and sums of this buffer have been used
         if (step >= 2) wait(&ctl->oempty[g], ((step >> 1) - 1) & 1);
@@ -848,12 +848,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (wq == 0 && lane < R) {
-          ctl->m[g][lane] = top - kTop;
+          ctl->m[g][lane] = top;
           ctl->e[g][lane] = E;
         }
         __syncwarp();
-        // ---- weights: w = p 2^(ev - 127) 2^(127 - E).  (What lies below fp32's normal range between
-        // the two factors is 2^-30 of the largest weight or less.)
+        // ---- weights: w = p 2^(ev - E), that power as 2^(ev - 127) 2^(127 - E): neither it nor the product
+        // leaves fp32's range where the values are near its end.
 #pragma unroll 1
         for (int c = 0; c < rows; c += W) {
           float f[W], u[W], sum[W];
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float v0 = after_wait(s[e]), v1 = after_wait(s[e + 1]);
               const uint64_t x2 = add2(f32x2(v0, v1), f32x2(f[e], f[e + 1]));
               const float p0 = exp2_approx(lo_of(x2)), p1 = exp2_approx(hi_of(x2));
-              const uint64_t w2 = mul2(mul2(f32x2(p0, p1), vf2), f32x2(u[e], u[e + 1]));
+              const uint64_t w2 = mul2(f32x2(p0, p1), mul2(vf2, f32x2(u[e], u[e + 1])));
               float w0 = lo_of(w2), w1 = hi_of(w2);
               if (edge) {                                // (not a NaN of a value that a row does not see)
                 if (v0 == -INFINITY) w0 = 0.f;
@@ -959,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float top = fmaxf(M, m);
           // (a side without a reference has nothing, or NaN, which passes)
           const float keep = M == -INFINITY ? 0.f : exp2_approx(M - top);
-          const float add = m == -INFINITY ? 0.f : exp2_approx(m - top);
+          const float add = m == -INFINITY ? 0.f : exp2_approx(m - top - kTop);
           Lsum = Lsum * keep + l * add;
           M = top;
           ctl->keep[wq][lane] = keep;

@@ -661,3 +661,37 @@ def test_a_value_that_some_rows_do_not_see_costs_them_no_precision(type):
     assert torch.equal(got[:3], want[:3]) and torch.equal(gl, wl)
     b.v[p, :, r] *= 2.0 ** (60 if type == BF16 else 12)
     b.check(got[:, :], gl) if type == BF16 else None
+
+
+@pytest.mark.parametrize("type", [BF16, F16])
+@pytest.mark.parametrize("G", [1, 4, 20])
+def test_values_at_the_end_of_the_range(type, G):
+    """Powers of two of V reach the output as they are, up to where bf16 ends (fp16: infinity), the
+    sums over the entries on their way to it included."""
+    b = Packed(type, 128, 2, G, 64, [1, 1], [300, 3000], seed=31)
+    low = b.vs.clone()
+    for up in (0, int(245 - int(low.max()))):
+        b.vs = low + up
+        out = b.kv().attention(b.q, b.cu, b.len, max_q=1)
+        if up == 0:
+            # (weights of 1 in all at most: a value of the output is the largest of V at most)
+            want = out.double()
+            tiny = want.abs() < 2.0 ** -100 if type == BF16 else want.abs() < 2.0 ** -14
+        else:
+            got, scaled = out.double(), want * 2.0 ** up
+            if type == F16:
+                scaled = torch.where(scaled.abs() >= 65520, scaled.sign() * math.inf, scaled)
+            assert (tiny | (got == scaled)).all()
+
+
+@pytest.mark.parametrize("type", [BF16, F16])
+def test_the_largest_power_of_two(type):
+    b = Packed(type, 128, 2, 2, 64, [1], [1], seed=32)
+    b.v8.view(torch.uint8).bitwise_and_(0x87)            # codes below 2^-6: 2^121 with the largest scale
+    b.vs.fill_(254)
+    out = b.kv().attention(b.q, b.cu, b.len, max_q=1)
+    p, r = b.where(0)
+    want = value(b.v8[p[0], :, r[0]].double(), b.vs[p[0], :, r[0]]).repeat_interleave(2, 0)[None]
+    if type == F16:
+        want = torch.where(want == 0, want, want.sign() * math.inf)
+    assert want.abs().max() > 2.0 ** 118 and (out.double() == want).all()
