@@ -444,6 +444,91 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 8)
   }
 }
 
+// Rows of up to 32 V values: a warp to a row, lane l has places l, l + 32, ..; the alternatives one by one.
+constexpr int kWarps = 8;
+template <typename T, int V>
+__global__ void __launch_bounds__(32 * kWarps) k_logprobs_few(const __grid_constant__ Call a) {
+  pdl_wait_and_trigger();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const uint32_t row = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
+  const uint32_t group = row / (uint32_t)a.inner, in = row - group * (uint32_t)a.inner;
+  const T* x = reinterpret_cast<const T*>(a.x) + group * a.ld + in * a.inner_ld;
+  const int32_t token = a.logprob ? a.tokens[group * a.token_ld + in] : -1;
+  float v[V], m = -INFINITY;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = i * 32 + lane < a.n ? load_value(x + i * 32 + lane) : -INFINITY;
+  const float chosen = token >= 0 && token < a.n ? load_value(x + token) : 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    bad |= !(v[i] < INFINITY);
+    if (!(fabsf(v[i]) < INFINITY)) v[i] = -INFINITY;
+    m = fmaxf(m, v[i]);
+  }
+  if (bad && a.status) atomicOr(a.status, PP_S_NAN);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f, t = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float d = fmaxf(v[i] - m, kFar), p = exp2_approx(d * kLog2e);   // (without a finite value: 0)
+    l += p;
+    t = fmaf(p, d, t);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, o);
+    t += __shfl_xor_sync(0xffffffffu, t, o);
+  }
+  const float log_l = logf(l);
+  if (lane == 0) {
+    if (a.logprob) {
+      float lp = 0.f;
+      if (token >= a.n) {
+        if (a.status) atomicOr(a.status, PP_S_INDEX);
+      } else if (token >= 0) {
+        lp = fabsf(chosen) < INFINITY ? (chosen - m) - log_l : -INFINITY;
+      }
+      a.logprob[row] = lp;
+    }
+    if (a.entropy) a.entropy[row] = l > 0.f ? fmaxf(log_l - t / l, 0.f) : 0.f;
+  }
+  if (a.top == 0) return;
+  uint32_t o[V], best[2] = {0, 0}, place[2] = {0, 0};   // the lane's values; alternatives lane and 32 + lane
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = v[i] == -INFINITY ? 0u : order(v[i]);
+#pragma unroll 1
+  for (int k = 0; k < a.top; ++k) {
+    uint32_t most = 0, at = ~0u;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (o[i] >= most) {
+        most = o[i];
+        at = i * 32 + lane;
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, most);
+    if (top == 0) break;
+    at = __reduce_min_sync(0xffffffffu, most == top ? at : ~0u);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (at == i * 32 + lane) o[i] = 0;
+    if (lane == (k & 31)) {
+      best[k >> 5 & 1] = top;
+      place[k >> 5 & 1] = at;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int k = 32 * j + lane;
+    if (k >= a.top) continue;
+    if (a.top_tokens) a.top_tokens[(int64_t)row * a.top + k] = best[j] ? (int32_t)place[j] : -1;
+    if (a.top_logprobs)
+      a.top_logprobs[(int64_t)row * a.top + k] = best[j] ? (value_of(best[j]) - m) - log_l : -INFINITY;
+  }
+}
+
 template <typename T, int kThreads, int kVectors>
 cudaError_t run(Call a, cudaStream_t s) {
   constexpr int kBlock = kThreads * kVectors * 16 / (int)sizeof(T);
@@ -453,9 +538,16 @@ cudaError_t run(Call a, cudaStream_t s) {
   auto kern = a.entropy ? k_logprobs<T, kThreads, kVectors, true> : k_logprobs<T, kThreads, kVectors, false>;
   return paged::launch_cluster(size, kern, dim3((unsigned)(a.rows * size)), kThreads, 0, s, a);
 }
-// Short rows in small CTAs, more of them side by side.
+template <typename T, int V>
+cudaError_t run_few(const Call& a, cudaStream_t s) {
+  return paged::launch(k_logprobs_few<T, V>, dim3((unsigned)((a.rows + kWarps - 1) / kWarps)), 32 * kWarps, 0,
+                       s, a);
+}
+// Short rows in small CTAs, more of them side by side; the shortest by warps.
 template <typename T>
 cudaError_t pick(const Call& a, cudaStream_t s) {
+  if (a.n <= 64) return run_few<T, 2>(a, s);
+  if (a.n <= 256) return run_few<T, 8>(a, s);
   return a.n <= 128 * 4 * 16 / (int)sizeof(T) ? run<T, 128, 4>(a, s) : run<T, 512, 8>(a, s);
 }
 
