@@ -260,3 +260,25 @@ def test_the_columns_of_a_tick():
     assert (text["logprob"] == 0).all() and (audio["logprob"] == 0).all()
     assert status.item() == pp.PP_S_INDEX
     eng.close_engine()
+
+
+@pytest.mark.parametrize("type", [F32, BF16, F16])
+@pytest.mark.parametrize("n", [31, 33, 64, 65, 256, 257, 512, 513, 1024, 1025, 2049, 4096, 4097, 8200, 16385])
+def test_where_one_form_ends(type, n):
+    """Lengths on both sides of a change of kernels, with equal values and some that are not finite."""
+    x, t = make(type, (9, n), seed=n)
+    x[1] = x[1].round()
+    x[2] = 2.5
+    x[3] = -math.inf
+    x[4, ::3] = math.nan
+    x[5, n // 2:] = -math.inf
+    x[6, -1] = torch.finfo(type).max
+    x[7, 0] = torch.finfo(type).min
+    t[8] = n - 1
+    for top in (0, 3, 64):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = pp_().token_logprobs(x, t, top=top, with_entropy=True, status=status)
+        check(x, t, got, top)
+        alone = pp_().token_logprobs(x[5:6], t[5:6], top=top, with_entropy=True)
+        assert all(torch.equal(alone[k][0], got[k][5]) for k in alone)
+        assert status.item() == pp_().PP_S_NAN
