@@ -221,7 +221,9 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(I) == 2 ? 4 : 3)
       }
       uint32_t scale = 0;
       uint2 codes{};
-      if constexpr (kPack) codes = pack_codes<L>(y, scale);
+      if constexpr (kPack) {                       // (where the warp's last head is no query)
+        if (r - (int)(threadIdx.x % 32) / L + 32 / L > H) codes = pack_codes<L>(y, scale);
+      }
       if (!live) continue;
       if (kind == 0) {
         store8(reinterpret_cast<T*>(x.q_out) + ((int64_t)t * H + h) * D + l * 8, y);
