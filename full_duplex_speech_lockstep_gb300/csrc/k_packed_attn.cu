@@ -31,6 +31,12 @@
 //   warps 12-15  epilogue: a thread owns one dim
 //   warps 17-18  the units' queries, as parts.  (One warp took 13000 clocks for 32 rows.)
 //
+// Measured (in a graph, with the join): 64 sequences, one token, up to 3000 entries, 32 heads of 128 dims, bf16:
+// 156 us, 5.0 TB/s; 8 sequences of up to 5 tokens over up to 65000 entries, 32 heads on 8, pages of 16, fp16:
+// 155 us, 3.0 TB/s; one token over 3000 entries, 32 heads: 18 us.  Bound, with a row to a key head, by units'
+// ends and the SMs' unequal runs; with 20 rows by the softmax's instructions (4700 of a warp a tile, at half
+// the issue rate); alone by latencies.
+//
 // What no row of a unit sees must not reach the second product, where a weight of zero times a NaN
 // would be one: those rows of V are zeroed in shared memory.  An entry that only some rows see and
 // that holds a NaN code is zeroed too, and its scale taken for NaN, which only its seers' weights get.

@@ -92,7 +92,8 @@ __device__ __forceinline__ uint2 pack_codes(const float y[8], uint32_t& scale) {
 // five, they spill).  Halves through shared
 // memory took 75 us.  (Ten tokens to a CTA with the next one's loads ahead: no faster, and slower
 // for few tokens.)
-// `kPack`: keys and values are held in 8 bits.
+// `kPack`: keys and values are held in 8 bits: the 6021 tokens take 46 us (50 with queries packed as well).
+// 35 instructions a value then, at 0.69 of the issue rate: bound by them.
 template <typename I, typename T, int D, bool kPack>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(I) == 2 ? 4 : 3)
     k_paged_append(const __grid_constant__ Args a, const __grid_constant__ AppendArgs x,
