@@ -571,44 +571,47 @@ def token_logprobs(logits, tokens=None, top=0, with_entropy=False, status=None):
     token is padding and gives 0.  ``status`` (int32, one word) collects PP_S_* bits.  Runs on the
     logits' device, on its current stream."""
     import torch
-    types, lead = _types(torch), tuple(logits.shape[:-1])
-    if not logits.is_cuda or logits.dtype not in types or logits.dim() not in (2, 3):
+    type, shape = _types(torch).get(logits.dtype), logits.shape
+    if type is None or not logits.is_cuda or len(shape) not in (2, 3):
         raise ValueError("logits: %s %s on %s, expected CUDA [rows, n] or [groups, rows, n] in f32, "
-                         "bf16 or fp16" % (logits.dtype, tuple(logits.shape), logits.device))
-    n = logits.shape[-1]
-    if n > 1 and logits.stride(-1) != 1:
+                         "bf16 or fp16" % (logits.dtype, tuple(shape), logits.device))
+    stride, lead, n, index = logits.stride(), shape[:-1], shape[-1], logits.get_device()
+    if n > 1 and stride[-1] != 1:
         raise ValueError("logits: the values of a row must be contiguous")
-    index = logits.get_device()
     for name, t in (("tokens", tokens), ("status", status)):
         if t is not None and (t.get_device() != index or t.dtype is not torch.int32):
             raise ValueError("%s: %s on %s, expected int32 on %s" % (name, t.dtype, t.device,
                                                                     logits.device))
     if status is not None and tuple(status.shape) != (1,):
         raise ValueError("status: %s, expected one word" % (tuple(status.shape),))
+    out, empty, device = {}, torch.empty, logits.device
+    token_at = logprob = entropy = top_tokens = top_logprobs = None
+    token_ld = 0
     if tokens is not None:
-        if tuple(tokens.shape) != lead:
-            raise ValueError("tokens: %s, expected %s" % (tuple(tokens.shape), lead))
-        if len(lead) == 2 and lead[1] > 1 and tokens.stride(1) != 1:
+        if tokens.shape != lead:
+            raise ValueError("tokens: %s, expected %s" % (tuple(tokens.shape), tuple(lead)))
+        token_stride = tokens.stride()
+        if len(lead) == 2 and lead[1] > 1 and token_stride[1] != 1:
             raise ValueError("tokens: the tokens of a group must be contiguous")
-    rows, inner = lead if len(lead) == 2 else (lead[0], 1)
-    out = {}
-    new = lambda dtype, *shape: torch.empty(lead + shape, dtype=dtype, device=logits.device)
-    if tokens is not None:
-        out["logprob"] = new(torch.float32)
+        token_at, token_ld = tokens.data_ptr(), token_stride[0]
+        out["logprob"] = t = empty(lead, dtype=torch.float32, device=device)
+        logprob = t.data_ptr()
     if with_entropy:
-        out["entropy"] = new(torch.float32)
+        out["entropy"] = t = empty(lead, dtype=torch.float32, device=device)
+        entropy = t.data_ptr()
     if top:
-        out["top_tokens"] = new(torch.int32, max(top, 0))
-        out["top_logprobs"] = new(torch.float32, max(top, 0))
-    ptr = lambda t: None if t is None else t.data_ptr()
+        most = tuple(lead) + (max(top, 0),)
+        out["top_tokens"] = t = empty(most, dtype=torch.int32, device=device)
+        top_tokens = t.data_ptr()
+        out["top_logprobs"] = t = empty(most, dtype=torch.float32, device=device)
+        top_logprobs = t.data_ptr()
+    rows, inner, inner_ld = (lead[0], 1, 0) if len(lead) == 1 else (lead[0], lead[1], stride[1])
     if rows * inner == 0:
         inner, rows = max(inner, 1), 0
     _on_device(torch, index, _raw_stream(torch), "pp_token_logprobs", lib().pp_token_logprobs,
-               logits.data_ptr(), types[logits.dtype], logits.stride(0), rows, inner,
-               logits.stride(1) if len(lead) == 2 else 0, n, ptr(tokens),
-               tokens.stride(0) if tokens is not None else 0, top, ptr(out.get("logprob")),
-               ptr(out.get("entropy")), ptr(out.get("top_tokens")), ptr(out.get("top_logprobs")),
-               ptr(status))
+               logits.data_ptr(), type, stride[0], rows, inner, inner_ld, n, token_at, token_ld, top,
+               logprob, entropy, top_tokens, top_logprobs,
+               None if status is None else status.data_ptr())
     return out
 
 

@@ -13,9 +13,9 @@
 //   O[d][r]  = sum_j v_jd w_jr           M = D dims, N = 3 x R rows, K = 128 keys a tile
 // A step is four tiles of 2 or 4 rows, two of 8, one of more: a thread has 8 to 32 scores a step, and what a
 // step costs beside them (barriers, maxima, the epilogue) is paid for several tiles.  (A tile at a time, few
-// rows took as long as 32: 313 us on the 64-session tick; tiles of 8 rows for one: 261 us.)  m_r is the step's own maximum and E_r the largest ev that the row sees: a step
-// depends on nothing before it.  The epilogue adds the steps up in fp32, in order:
-// acc = acc 2^(M - M') + O 2^(m - 8 + E_r - M').
+// rows took as long as 32: 313 us on the 64-session tick; tiles of 8 rows for one: 261 us.)
+// m_r is the step's own maximum and E_r the largest ev that the row sees: a step depends on nothing before
+// it.  The epilogue adds the steps up in fp32, in order: acc = acc 2^(M - M') + O 2^(m - 8 + E_r - M').
 //
 // A work unit is (sequence, key head, split of its keys, row tile of up to R rows).  Each CTA takes a run
 // of consecutive units with about as many tiles as the others'; a sequence's splits depend on its own
