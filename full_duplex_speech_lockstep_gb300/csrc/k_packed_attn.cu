@@ -54,6 +54,9 @@ constexpr int kReaders = 16;         // of the units: both issuers, eight of sof
 constexpr int kSlots = 32;           // tiles that are planned, and those whose scales are held
 constexpr int kParts = 3;            // of a weight
 constexpr float kTop = 8.f;          // a tile's largest weight is 2^8 (e4m3 holds up to 448)
+// Buffers of a softmax group's maxima.  A warp writes a step's while another of its group may still read those
+// of the group's step before; past its own meeting it comes only when that one has read them and arrived there too.
+constexpr int kMaxima = 2;
 
 // Few rows: a thread has 8 or 16 scores a step all the same.
 __host__ __device__ constexpr int step_tiles(int R) { return R < 8 ? 4 : R == 8 ? 2 : 1; }
@@ -99,9 +102,9 @@ struct Ctl {
   // of the two units in flight: each row's factor of its scores (to powers of two) and its entry
   alignas(16) float row_c[2][32];
   int row_at[2][32];
-  // of the two steps in flight: maxima of rows, and the largest V exponents that they see
-  float warp_max[2][4][32];
-  uint32_t warp_e[2][4][32];
+  // of the groups' steps, by warps: maxima of rows, and the largest V exponents that they see
+  float warp_max[2][kMaxima][4][32];
+  uint32_t warp_e[2][kMaxima][4][32];
   // each warp's copy of the references (negative), and of 2^(127 - E)
   alignas(16) float ref[2][4][32];
   alignas(16) float fit[2][4][32];
@@ -808,17 +811,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           E = own;
         }
+        const uint32_t mb = (step >> 1) % kMaxima;
         if (lane < R) {
-          ctl->warp_max[g][wq][lane] = top;
-          ctl->warp_e[g][wq][lane] = E;
+          ctl->warp_max[g][mb][wq][lane] = top;
+          ctl->warp_e[g][mb][wq][lane] = E;
         }
         sync_warps<true>(a, &ctl->meet[g], meets, lane, abort_flag);
         // lane r works row r's reference out for its warp
         if (lane < R) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            top = fmaxf(top, ctl->warp_max[g][w][lane]);
-            E = max(E, ctl->warp_e[g][w][lane]);
+            top = fmaxf(top, ctl->warp_max[g][mb][w][lane]);
+            E = max(E, ctl->warp_e[g][mb][w][lane]);
           }
           if (top != top) top = -INFINITY;               // (a row of NaN: its weights are NaN all the same)
           ctl->ref[g][wq][lane] = top == -INFINITY ? 0.f : kTop - top;
