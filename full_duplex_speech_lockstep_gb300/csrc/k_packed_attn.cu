@@ -446,8 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_codes<D>(a, &map, x, smem_u32(smem + (kV ? C::kVOff : 0) + i * C::kTileBytes), full, l);
         // V is waited for by steps: the tiles that a step lacks count as there
         if (kV && lack > 0 && l == 0) mbar_arrive_n(full, lack);
-        if (l == 0) mbar_arrive(smem_u32(&ctl->tempty[slot]));
       }
+      __syncwarp();                                      // (the half warp has read the tile before it is given back)
+      if (live && l == 0) mbar_arrive(smem_u32(&ctl->tempty[slot]));
       const uint32_t both = __ballot_sync(0xffffffffu, live);
       n += (both & 1u) + (both >> 16 & 1u);
       step += (both & 1u ? ends : 0) + __shfl_sync(0xffffffffu, live && lack >= 0 ? 1 : 0, 16);

@@ -329,3 +329,21 @@ def test_one_buffer_of_maxima_is_written_while_it_is_read(most, buffers):
     with pytest.raises(AssertionError, match="maxima"):
         for seed in range(200):
             packed(seed, [200], (4, 7), most, buffers, maxima=1)
+
+
+def half_warps_read_together():
+    """Whether the loaders' lanes meet between the last read of a planned tile and its return."""
+    loader = kernel_source().split("auto load_tiles", 1)[1]
+    before = loader.split("mbar_arrive(smem_u32(&ctl->tempty[slot]))", 1)[0]
+    return "__syncwarp();" in before.rsplit("load_codes<D>", 1)[1]
+
+
+@pytest.mark.parametrize("seed", SEEDS)
+def test_a_tile_is_given_back_when_all_lanes_have_read_it(seed):
+    packed(seed, [100, 1, 3, 90], (4, 7), 4, together=half_warps_read_together())
+
+
+def test_a_tile_given_back_by_one_lane_alone_is_overwritten():
+    with pytest.raises(AssertionError, match="tile"):
+        for seed in range(200):
+            packed(seed, [200], (4, 7), 4, together=False)
