@@ -9,13 +9,14 @@
 //   w = w1 + w2/16 + w3/256              fp16's 11 bits; w is at most 256, so 2^-26 of that is its floor
 // Keys are the rows of both products, a thread of the softmax owns a key of each tile:
 //   S[j][r]  = k_j . q_r                 M = 128 keys, N = parts x R rows, K = D
-//   w[j][r]  = 2^(s_jr - m_r + 8) 2^(ev_j - E_r),   s_jr = S c 2^(ek_j + eq_r)
+//   w[j][r]  = 2^(s_jr - m_r + 8 + ev_j - E_r),   s_jr = S c 2^(ek_j + eq_r)
 //   O[d][r]  = sum_j v_jd w_jr           M = D dims, N = 3 x R rows, K = 128 keys a tile
 // A step is four tiles of 2 or 4 rows, two of 8, one of more: a thread has 8 to 32 scores a step, and what a
 // step costs beside them (barriers, maxima, the epilogue) is paid for several tiles.  (A tile at a time, few
 // rows took as long as 32: 313 us on the 64-session tick; tiles of 8 rows for one: 261 us.)
-// m_r is the step's own maximum and E_r the largest ev that the row sees: a step depends on nothing before
-// it.  The epilogue adds the steps up in fp32, in order: acc = acc 2^(M - M') + O 2^(m - 8 + E_r - M').
+// m_r is the step's own maximum and E_r the whole number from max_j (s_jr - m_r + ev_j) on, or up to kSlack
+// above it: a row keeps the precision of what weighs in it, whatever else it sees.  A step depends on nothing
+// before it.  The epilogue adds the steps up in fp32, in order: acc = acc 2^(M - M') + O 2^(m - 8 + E_r - M').
 //
 // A work unit is (sequence, key head, split of its keys, row tile of up to R rows).  Each CTA takes a run
 // of consecutive units with about as many tiles as the others'; a sequence's splits depend on its own
@@ -54,6 +55,10 @@ constexpr int kReaders = 16;         // of the units: both issuers, eight of sof
 constexpr int kSlots = 32;           // tiles that are planned, and those whose scales are held
 constexpr int kParts = 3;            // of a weight
 constexpr float kTop = 8.f;          // a tile's largest weight is 2^8 (e4m3 holds up to 448)
+// Where the V exponents of a warp's keys are no further apart than this, its largest one stands for the largest
+// weighted one and nothing has to be looked for: weights are held to 2^-20 of the step's largest then, to 2^-25
+// otherwise.  (Looked for in every step, 8 long caches took 173 us in place of 161.)
+constexpr int kSlack = 6;
 // Buffers of a softmax group's maxima.  A warp writes a step's while another of its group may still read those
 // of the group's step before; past its own meeting it comes only when that one has read them and arrived there too.
 constexpr int kMaxima = 2;
@@ -102,10 +107,10 @@ struct Ctl {
   // of the two units in flight: each row's factor of its scores (to powers of two) and its entry
   alignas(16) float row_c[2][32];
   int row_at[2][32];
-  // of the groups' steps, by warps: maxima of rows, and the largest V exponents that they see
+  // of the groups' steps, by warps: maxima of rows, and E for that maximum
   float warp_max[2][kMaxima][4][32];
-  uint32_t warp_e[2][kMaxima][4][32];
-  // each warp's copy of the references (negative), and of 2^(127 - E)
+  float warp_e[2][kMaxima][4][32];
+  // each warp's copy of the references (negative), and of -E
   alignas(16) float ref[2][4][32];
   alignas(16) float fit[2][4][32];
   float m[2][32], l[2][4][32];
@@ -712,8 +717,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool bad = *reinterpret_cast<volatile int*>(&ctl->any_bad) != 0;
         // does every row see every key of the step?
         const int j0 = t * kTile + key;
-        const bool edge = bad || (t + tiles) * kTile - 1 > min(x.first, x.stop - 1) ||
-                          (a.window && t * kTile <= x.nt - a.window);
+        const bool partly = (t + tiles) * kTile - 1 > min(x.first, x.stop - 1) ||
+                            (a.window && t * kTile <= x.nt - a.window);
+        const bool edge = bad || partly;
         uint32_t see = ~0u;                              // bit k R + r: row r sees this thread's key of tile k
         uint32_t live = ~0u;                             // bit k: some row does
         if (edge) {
@@ -787,30 +793,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         // ---- V's scales (they came with K's): bit k of nan_value: the value of tile k reads as NaN
-        uint32_t nan_value = 0, E = 0;
+        uint32_t nan_value = 0, high = 0, low = 255;
 #pragma unroll 1
         for (int k = 0; k < tiles; ++k) {
           const uint32_t ev = v_scale(k);
-          if (ev == 255u) nan_value |= 1u << k;
-          if (live >> k & 1u) E = max(E, ev == 255u ? 0u : ev);
+          if (ev == 255u) {
+            nan_value |= 1u << k;
+          } else if (live >> k & 1u) {
+            high = max(high, ev);
+            low = min(low, ev);
+          }
         }
-        if (!edge || !mixed) {
-          E = __reduce_max_sync(0xffffffffu, E);
-        } else {
-          // each row goes by the exponents that it sees: another's could take its weights below e4m3
-          uint32_t own = 0;
+        high = __reduce_max_sync(0xffffffffu, high);
+        low = __reduce_min_sync(0xffffffffu, low);
+        float E = (float)high;
+        if ((int)(high - low) > kSlack || (mixed && partly)) {
+          // by the scores, and by what each row sees itself: lane r has row r's
+          E = -INFINITY;
 #pragma unroll 1
-          for (int r = 0; r < rows; ++r) {
-            uint32_t y = 0;
+          for (int c = 0; c < rows; c += W) {
+            float most[W], f[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              most[e] = -INFINITY;
+              f[e] = -__shfl_sync(0xffffffffu, top, c + e);
+            }
 #pragma unroll 1
             for (int k = 0; k < tiles; ++k) {
+              uint32_t s[W];
+              tmem_ld<W>(scores + k * C::NQ + c, s);
               const uint32_t ev = v_scale(k);
-              if (see >> (k * R + r) & 1u) y = max(y, ev == 255u ? 0u : ev);
+              const float vf = ev == 255u ? 0.f : (float)ev;
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < W; ++e)                // (where there is no maximum: a NaN, which passes by)
+                most[e] = fmaxf(most[e], after_wait(s[e]) + f[e] + vf);
             }
-            y = __reduce_max_sync(0xffffffffu, y);
-            if (lane == r) own = y;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              const float y = warp_max(most[e]);
+              if (lane - c == e) E = y;
+            }
           }
-          E = own;
         }
         const uint32_t mb = (step >> 1) % kMaxima;
         if (lane < R) {
@@ -821,13 +845,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // lane r works row r's reference out for its warp
         if (lane < R) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            top = fmaxf(top, ctl->warp_max[g][mb][w][lane]);
-            E = max(E, ctl->warp_e[g][mb][w][lane]);
-          }
+          for (int w = 0; w < 4; ++w) top = fmaxf(top, ctl->warp_max[g][mb][w][lane]);
+          E = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            E = fmaxf(E, ctl->warp_e[g][mb][w][lane] + (ctl->warp_max[g][mb][w][lane] - top));
+          E = ceilf(E);
           if (top != top) top = -INFINITY;               // (a row of NaN: its weights are NaN all the same)
           ctl->ref[g][wq][lane] = top == -INFINITY ? 0.f : kTop - top;
-          ctl->fit[g][wq][lane] = __uint_as_float(E == 254u ? 0x00400000u : (254u - E) << 23);
+          ctl->fit[g][wq][lane] = -E;
         }
         // the last step's weights and sums of this buffer have been used
         if (step >= 2) wait(&ctl->oempty[g], ((step >> 1) - 1) & 1);
@@ -860,11 +886,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (wq == 0 && lane < R) {
           ctl->m[g][lane] = top;
-          ctl->e[g][lane] = E;
+          ctl->e[g][lane] = (uint32_t)E;
         }
         __syncwarp();
-        // ---- weights: w = p 2^(ev - E), that power as 2^(ev - 127) 2^(127 - E): neither it nor the product
-        // leaves fp32's range where the values are near its end.
+        // ---- weights, with an exponential of their own: p 2^(ev - E) would be 0 or not finite where p is below
+        // fp32's range, or that power above it
 #pragma unroll 1
         for (int c = 0; c < rows; c += W) {
           float f[W], u[W], sum[W];
@@ -878,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < tiles; ++k) {
             uint32_t s[W], y[W / 2];
             tmem_ld<W>(scores + k * C::NQ + c, s);
-            const float vf = nan_value >> k & 1u ? __uint_as_float(0x7fc00000u) : scale_of(v_scale(k));
+            const float vf = nan_value >> k & 1u ? __uint_as_float(0x7fc00000u) : (float)v_scale(k);
             const uint64_t vf2 = f32x2(vf, vf);
             tmem_wait_ld();
 #pragma unroll
@@ -886,8 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float v0 = after_wait(s[e]), v1 = after_wait(s[e + 1]);
               const uint64_t x2 = add2(f32x2(v0, v1), f32x2(f[e], f[e + 1]));
               const float p0 = exp2_approx(lo_of(x2)), p1 = exp2_approx(hi_of(x2));
-              const uint64_t w2 = mul2(f32x2(p0, p1), mul2(vf2, f32x2(u[e], u[e + 1])));
-              float w0 = lo_of(w2), w1 = hi_of(w2);
+              const uint64_t w2 = add2(x2, add2(vf2, f32x2(u[e], u[e + 1])));
+              float w0 = exp2_approx(lo_of(w2)), w1 = exp2_approx(hi_of(w2));
               if (edge) {                                // (not a NaN of a value that a row does not see)
                 if (v0 == -INFINITY) w0 = 0.f;
                 if (v1 == -INFINITY) w1 = 0.f;
@@ -970,11 +996,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float top = fmaxf(M, m);
           // (a side without a reference has nothing, or NaN, which passes)
           const float keep = M == -INFINITY ? 0.f : exp2_approx(M - top);
-          const float add = m == -INFINITY ? 0.f : exp2_approx(m - top - kTop);
-          Lsum = Lsum * keep + l * add;
+          const float add = m == -INFINITY ? 0.f : exp2_approx(m - top);
+          constexpr float down = 1.f / 256.f;            // 2^-kTop
+          Lsum = Lsum * keep + l * (add * down);
           M = top;
           ctl->keep[wq][lane] = keep;
-          ctl->add[wq][lane] = add * scale_of(ctl->e[g][lane]);
+          ctl->add[wq][lane] = add * scale_of(ctl->e[g][lane]) * down;
         }
         __syncwarp();
         wait(&ctl->ofull[g], ph);
