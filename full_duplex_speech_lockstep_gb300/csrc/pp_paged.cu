@@ -152,6 +152,13 @@ bool meet(const void* a, int64_t n, const void* b, int64_t m) {
   return x < y + m && y < x + n;
 }
 
+// Bytes from a pool's first page to the end of its last one, `page` bytes of every `stride` (what lies between
+// pages may be another's).  At most 2^62: no address is that far from another.
+int64_t pool_bytes(int64_t n, int64_t stride, int64_t page) {
+  const int64_t most = (int64_t)1 << 62;
+  return n - 1 > (most - page) / stride ? most : (n - 1) * stride + page;
+}
+
 // A 16-bit copy of an 8-bit cache in scratch: a page for each entry of its table, and their table.
 struct Mirror {
   int64_t pages, page;       // pages; values of one
@@ -470,11 +477,17 @@ int pp_packed_read(const pp_packed_kv* kv, const int32_t* kv_len, const pp_paged
   if (to->type != kv->type || to->head_dim != kv->head_dim || to->n_kv_heads != kv->n_kv_heads ||
       to->n_seqs != kv->n_seqs)
     return PP_EINVAL;
-  const int64_t codes = kv->n_pages * kv->page_stride, scales = kv->n_pages * kv->scale_stride;
-  const int64_t values = to->n_pages * to->page_stride * 2;
+  const int64_t rows = (int64_t)kv->n_kv_heads * kv->page_size, to_rows = (int64_t)to->n_kv_heads * to->page_size;
+  const int64_t codes = pool_bytes(kv->n_pages, kv->page_stride, rows * kv->head_dim);
+  const int64_t scales = pool_bytes(kv->n_pages, kv->scale_stride, rows);
+  const int64_t values = pool_bytes(to->n_pages, to->page_stride * 2, to_rows * to->head_dim * 2);
+  const int64_t entry = sizeof(int32_t), table = (int64_t)kv->n_seqs * kv->table_ld * entry;
+  const int64_t to_table = (int64_t)to->n_seqs * to->table_ld * entry;
   for (const void* t : {to->k, to->v})
     if (meet(kv->k, codes, t, values) || meet(kv->v, codes, t, values) ||
-        meet(kv->k_scale, scales, t, values) || meet(kv->v_scale, scales, t, values))
+        meet(kv->k_scale, scales, t, values) || meet(kv->v_scale, scales, t, values) ||
+        meet(kv->table, table, t, values) || meet(to->table, to_table, t, values) ||
+        meet(kv_len, kv->n_seqs * entry, t, values))
       return PP_EINVAL;
   return rc(launch_packed_read(base_args(kv, kv_len, status), kv->type, read_args(kv, to),
                                (cudaStream_t)stream));

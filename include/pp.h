@@ -700,7 +700,8 @@ int pp_packed_attention(const pp_packed_kv* kv, const void* q, int64_t q_stride,
  * of the same sequences, heads, head dim and type, of any page size.  Their mass (where to->mass is
  * given) becomes 0.  An entry of a page outside either pool, or without a place in either table, is left
  * as it was and raises PP_S_INDEX.  fp16 rounds what it cannot hold (values below 2^-14 to multiples of
- * 2^-24, those from 65520 on to infinity).  `to` must not share memory with kv.
+ * 2^-24, those from 65520 on to infinity).  `to` must not share memory with kv: PP_EINVAL where its pools'
+ * first to last page meet kv's, a table or kv_len.  (Its mass is the caller's to keep apart.)
  * Errors: PP_EINVAL, PP_E_CUDA. */
 int pp_packed_read(const pp_packed_kv* kv, const int32_t* kv_len, const pp_paged_kv* to,
                    uint32_t* status, void* stream);
