@@ -756,8 +756,9 @@ class _Pages:
         self.ref, self.lib, self.sizes = ctypes.byref(c), lib(), {}
 
     def _other(self, name, to):
-        """Refuse what is not a 16-bit cache on this cache's device."""
-        if not isinstance(to, PagedKV):
+        """Refuse what is not a 16-bit cache on this cache's device: a PagedKV, or a caller's own
+        object with its ``ref`` (the library's structure) and ``index``."""
+        if not hasattr(to, "ref") or getattr(to, "family", PagedKV.family) != PagedKV.family:
             raise ValueError("%s: %s, expected a PagedKV" % (name, type(to).__name__))
         if to.index != self.index:
             raise ValueError("both caches must be on one device")
