@@ -159,26 +159,44 @@ int64_t pool_bytes(int64_t n, int64_t stride, int64_t page) {
   return n - 1 > (most - page) / stride ? most : (n - 1) * stride + page;
 }
 
-// A 16-bit copy of an 8-bit cache in scratch: a page for each entry of its table, and their table.
+// A 16-bit copy of some of an 8-bit cache's sequences in scratch: a page for each entry of their tables, and
+// their table.  A call takes as many sequences at a time as kCopyBytes have room for (one at least), as even in
+// number as they come: the host knows the table's size and not what is in use, and the copy of a whole wide
+// table can be larger than all else.  64 sequences of 3000 entries, 32 heads of 128 dims, 100 new tokens each:
+// 1417 us with a copy of 3.1 GB, 1474 in two turns, 1563 in four of 0.8 GB; one of them alone with new tokens: 49, 64
+// and 90.
+constexpr int64_t kCopyBytes = (int64_t)2 << 30;
 struct Mirror {
-  int64_t pages, page;       // pages; values of one
+  int seqs;                  // sequences at a time
+  int64_t page;              // values of one page
   size_t pool, bytes;        // bytes of K (and of V); of all
 };
 Mirror mirror_of(const pp_packed_kv* kv) {
   Mirror m;
-  m.pages = (int64_t)kv->n_seqs * kv->table_ld;
   m.page = (int64_t)kv->n_kv_heads * kv->page_size * kv->head_dim;
-  m.pool = (size_t)(m.pages * m.page) * 2;      // (a page has 2 KB or more)
-  m.bytes = 2 * m.pool + (((size_t)m.pages * sizeof(int32_t) + 255) & ~(size_t)255);
+  const int64_t room = kCopyBytes / (kv->table_ld * m.page * 4), n = room < 1 ? 1 : room;
+  const int64_t turns = (kv->n_seqs + n - 1) / n;
+  m.seqs = (int)((kv->n_seqs + turns - 1) / turns);
+  const int64_t pages = (int64_t)m.seqs * kv->table_ld;
+  m.pool = (size_t)(pages * m.page) * 2;        // (a page has 2 KB or more)
+  m.bytes = 2 * m.pool + (((size_t)pages * sizeof(int32_t) + 255) & ~(size_t)255);
   return m;
 }
+// Sequences [b, b + n) of a cache.
+pp_packed_kv sequences(const pp_packed_kv* kv, int b, int n) {
+  pp_packed_kv some = *kv;
+  some.table += (int64_t)b * kv->table_ld;
+  some.n_seqs = n;
+  return some;
+}
+// The copy of the sequences of `kv` (m.seqs at most).
 pp_paged_kv mirror_cache(const pp_packed_kv* kv, const Mirror& m, char* scratch) {
   pp_paged_kv to{};
   to.k = scratch;
   to.v = scratch + m.pool;
   to.table = reinterpret_cast<const int32_t*>(scratch + 2 * m.pool);
   to.page_stride = m.page;
-  to.n_pages = (int32_t)m.pages;                // at most eight to a key tile, of which 2^28
+  to.n_pages = kv->n_seqs * kv->table_ld;       // at most eight to a key tile, of which 2^28
   to.page_size = kv->page_size;
   to.n_kv_heads = kv->n_kv_heads;
   to.head_dim = kv->head_dim;
@@ -425,7 +443,8 @@ size_t pp_packed_attention_scratch_bytes(const pp_packed_kv* kv, int n_heads, in
     return p.rec_bytes + p.ml_bytes + 256;
   }
   const Mirror m = mirror_of(kv);
-  const pp_paged_kv copy = mirror_cache(kv, m, reinterpret_cast<char*>(kv->k));
+  const pp_packed_kv some = sequences(kv, 0, m.seqs);
+  const pp_paged_kv copy = mirror_cache(&some, m, reinterpret_cast<char*>(kv->k));
   return m.bytes + pp_paged_attention_scratch_bytes(&copy, n_heads, T, max_q, window);
 }
 
@@ -461,14 +480,24 @@ int pp_packed_attention(const pp_packed_kv* kv, const void* q, int64_t q_stride,
                                  (cudaStream_t)stream));
   }
   const Mirror m = mirror_of(kv);
-  const pp_paged_kv copy = mirror_cache(kv, m, reinterpret_cast<char*>(scratch));
-  ReadArgs x = read_args(kv, &copy);
-  x.mirror = 1;
-  const cudaError_t err = launch_packed_read(a, kv->type, x, (cudaStream_t)stream);
-  if (err != cudaSuccess) return PP_E_CUDA;
-  return pp_paged_attention(&copy, q, q_stride, cu, kv_len, T, max_q, n_heads, scale, window, out, lse,
-                            status, reinterpret_cast<char*>(scratch) + m.bytes,
-                            scratch_bytes - m.bytes, stream);
+  for (int b = 0; b < kv->n_seqs; b += m.seqs) {
+    const pp_packed_kv some = sequences(kv, b, kv->n_seqs - b < m.seqs ? kv->n_seqs - b : m.seqs);
+    const pp_paged_kv copy = mirror_cache(&some, m, reinterpret_cast<char*>(scratch));
+    Args part = a;
+    part.table = some.table;
+    part.len = kv_len + b;
+    part.cu = cu + b;
+    part.n_seqs = some.n_seqs;
+    ReadArgs x = read_args(&some, &copy);
+    x.mirror = 1;
+    if (launch_packed_read(part, kv->type, x, (cudaStream_t)stream) != cudaSuccess) return PP_E_CUDA;
+    // (rows of other sequences are outside its row offsets)
+    const int bad = pp_paged_attention(&copy, q, q_stride, cu + b, kv_len + b, T, max_q, n_heads, scale, window,
+                                       out, lse, status, reinterpret_cast<char*>(scratch) + m.bytes,
+                                       scratch_bytes - m.bytes, stream);
+    if (bad) return bad;
+  }
+  return PP_OK;
 }
 
 int pp_packed_read(const pp_packed_kv* kv, const int32_t* kv_len, const pp_paged_kv* to,

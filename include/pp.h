@@ -687,7 +687,7 @@ int pp_packed_append(const pp_packed_kv* kv, const void* q, int64_t q_stride, co
 /* pp_paged_attention over 8-bit entries: the same arguments, masks and results, of what the entries read
  * as (fp16: as pp_packed_read rounds them, in chunks of more than 64 rows).  Scratch:
  * pp_packed_attention_scratch_bytes(...) bytes; by max_q, chunks of more than 64 rows to a key head take a
- * 16-bit copy of all that the table has room for.
+ * 16-bit copy of what their tables have room for, of some sequences at a time: up to 2 GB, or one sequence's.
  * Errors: PP_EINVAL, PP_E_NOSPACE, PP_E_CUDA. */
 size_t pp_packed_attention_scratch_bytes(const pp_packed_kv* kv, int n_heads, int T, int max_q,
                                          int window);
