@@ -584,6 +584,8 @@ def token_logprobs(logits, tokens=None, top=0, with_entropy=False, status=None):
                                                                     logits.device))
     if status is not None and tuple(status.shape) != (1,):
         raise ValueError("status: %s, expected one word" % (tuple(status.shape),))
+    if lead.numel() >= 1 << 28 or n > 1 << 24:   # (a larger count would wrap on its way to the library)
+        raise PPError("pp_token_logprobs", PP_EINVAL)
     out, empty, device = {}, torch.empty, logits.device
     token_at = logprob = entropy = top_tokens = top_logprobs = None
     token_ld = 0
