@@ -569,7 +569,8 @@ def token_logprobs(logits, tokens=None, top=0, with_entropy=False, status=None):
     ``logits`` is [rows, n] or [groups, rows, n] in f32, bf16 or fp16, ``tokens`` int32 of its
     leading shape; the last dim of each must be contiguous, rows and groups may lie apart.  A negative
     token is padding and gives 0.  ``status`` (int32, one word) collects PP_S_* bits.  Runs on the
-    logits' device, on its current stream."""
+    logits' device, on its current stream.  What it returns has no gradient, whether or not the
+    logits ask for one."""
     import torch
     type, shape = _types(torch).get(logits.dtype), logits.shape
     if type is None or not logits.is_cuda or len(shape) not in (2, 3):
@@ -949,7 +950,11 @@ class PagedKV8(_Pages):
     ``k`` and ``v`` are [pages, kv_heads, page_size, head_dim] float8_e4m3fn codes, ``k_scale`` and
     ``v_scale`` [pages, kv_heads, page_size] powers of two (float8_e8m0fnu, or their bytes as uint8),
     ``dtype`` (bf16 or fp16) the type of queries and outputs.  Append and attention are those of
-    PagedKV; ``read`` gives 16-bit entries for what works on them (attention mass, eviction)."""
+    PagedKV; ``read`` gives 16-bit entries for what works on them (attention mass, eviction).
+
+    Say ``max_q`` (the longest chunk): without it all rows count as one chunk, and chunks of more
+    than 64 rows to a key head go through a 16-bit copy of what they see, in scratch of up to 2 GB
+    (or one sequence's part of the table)."""
 
     family, scratch_bytes = "pp_packed", staticmethod(pp_packed_attention_scratch_bytes)
 

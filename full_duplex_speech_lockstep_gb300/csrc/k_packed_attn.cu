@@ -33,9 +33,9 @@
 //   warps 17-18  the units' queries, as parts.  (One warp took 13000 clocks for 32 rows.)
 //
 // Measured (in a graph, with the join): 64 sequences, one token, up to 3000 entries, 32 heads of 128 dims, bf16:
-// 156 us, 5.0 TB/s; 8 sequences of up to 5 tokens over up to 65000 entries, 32 heads on 8, pages of 16, fp16:
-// 155 us, 3.0 TB/s; one token over 3000 entries, 32 heads: 18 us.  Bound, with a row to a key head, by units'
-// ends and the SMs' unequal runs; with 20 rows by the softmax's instructions (4700 of a warp a tile, at half
+// 157 us, 4.9 TB/s; 8 sequences of up to 5 tokens over up to 65000 entries, 32 heads on 8, pages of 16, fp16:
+// 161 us, 2.9 TB/s; one token over 3000 entries, 32 heads: 18 us.  Bound, with a row to a key head, by units'
+// ends and the SMs' unequal runs; with 20 rows by the softmax's instructions (4850 of a warp a tile, at half
 // the issue rate); alone by latencies.
 //
 // What no row of a unit sees must not reach the second product, where a weight of zero times a NaN
@@ -54,7 +54,7 @@ constexpr int kThreads = 608;
 constexpr int kReaders = 16;         // of the units: both issuers, eight of softmax, epilogue, queries
 constexpr int kSlots = 32;           // tiles that are planned, and those whose scales are held
 constexpr int kParts = 3;            // of a weight
-constexpr float kTop = 8.f;          // a tile's largest weight is 2^8 (e4m3 holds up to 448)
+constexpr float kTop = 8.f;          // a step's largest weight is 2^8 (e4m3 holds up to 448)
 // Where the V exponents of a warp's keys are no further apart than this, its largest one stands for the largest
 // weighted one and nothing has to be looked for: weights are held to 2^-20 of the step's largest then, to 2^-25
 // otherwise.  (Looked for in every step, 8 long caches took 173 us in place of 161.)
@@ -133,9 +133,10 @@ __host__ __device__ __forceinline__ int64_t most_tiles(int64_t entries, int wind
   const int64_t seen = ((int64_t)window + span - 2) / kTile + 2;
   return window && seen < all ? seen : all;
 }
-// Tiles of one split: `share` splits of each key head fill the SMs when a sequence is alone.  From twelve (a
-// unit's ends cost 4000 clocks, as much as six tiles: four to eight tiles took 201 us on the 64-session
-// tick) to 24 (runs of units come out even), and at most 128 splits.
+// Tiles of one split, at most: `share` splits of each key head fill the SMs when a sequence is alone.  Twelve (a
+// unit's ends cost 4000 clocks, as much as six tiles: with four to eight, the 64-session tick took 201 us) to 24
+// (runs of units come out even), and at most 128 splits.  Splits are counted upwards and made even, so that
+// units can have little more than half of it: 13 tiles are two of 6 and 7.
 constexpr int kLeast = 12, kMost = 24;
 __host__ __device__ __forceinline__ int64_t split_tiles(int64_t tiles, int share) {
   int64_t st = (tiles + share - 1) / share;
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   });
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (tiles come to the same memory)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  // S of the even and odd tiles, then O
+  // S in SB buffers of a step each, then O in two
   const uint32_t tmem = ctl->tmem;
   // (waits that go on are calls: with their loops in place the roles' code is larger than the
   // instruction cache)
@@ -1142,7 +1143,7 @@ PackedPlan packed_plan(const Args& a, int max_q) {
   const int heads = a.Hk * ((rows + p.R - 1) / p.R);
   p.share = kSms / heads < 1 ? 1 : kSms / heads;
   const int64_t tiles = most_tiles((int64_t)a.table_ld << a.lps, a.window, row_span(p.R, a.G));
-  // shorter sequences have `share` splits at most or one for every kMost tiles, of kLeast or more each
+  // shorter sequences have `share` splits at most or one for every kMost tiles, and one for every kLeast at most
   int64_t most = (tiles + kLeast - 1) / kLeast;
   const int64_t by_share = p.share > (tiles + kMost - 1) / kMost ? p.share : (tiles + kMost - 1) / kMost;
   if (by_share < most) most = by_share;

@@ -607,7 +607,7 @@ cudaError_t launch_packed_read(const Args& a, int type, const ReadArgs& x, cudaS
 
 // Chunks of up to kPackedRows rows (tokens x heads of a key head) run on the codes themselves
 // (k_packed_attn.cu); longer ones on a 16-bit copy of what they see.  8 sequences of 20000 entries, 8 key
-// heads: 64 rows 261 us on the codes, 332 on a copy; 128 rows 482 and 334.
+// heads: 64 rows 262 us on the codes, 321 on a copy; 128 rows 488 and 322.
 constexpr int kPackedRows = 64;
 struct PackedPlan {
   int R;           // rows of a row tile: 2, 4, 8, 16 or 32
